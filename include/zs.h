@@ -98,6 +98,8 @@ typedef int32_t zs_status;
  * (round to nearest even; an fp16 overflow becomes inf). */
 #define ZS_DTYPE_BF16 0
 #define ZS_DTYPE_FP16 1
+/* float32: gradients of a tensor list and matrices of the 4-bit calls only. */
+#define ZS_DTYPE_FP32 2
 
 /* Bits of the device flag word written by zs_grad_norm / zs_shard_step. */
 #define ZS_SKIP_NONFINITE 1   /* gradient norm not finite: update skipped */
@@ -615,6 +617,143 @@ zs_status zs_sched_stats(const zs_sched *sched, zs_sched_stats_t *out);
 /* Copy up to cap of the kept log records (oldest first); *n receives how
  * many are kept (at most log_limit). */
 zs_status zs_sched_log(const zs_sched *sched, zs_sched_event *out, int64_t cap, int64_t *n);
+
+/* ------------------------------------------------------------------------
+ * Training with little memory.  The pages count 2 + 2 + 12 bytes an element
+ * ([Core flow] §1: 16-bit parameters and gradients, fp32 master and
+ * moments); the calls below hold the moments in 2 bytes instead of 8 and the
+ * parameters that the products read in 0.53 instead of 2.  They have no
+ * counterpart on the pages and need no plan: they work on any device
+ * memory, a plan's buffers among it (a rank's shard row, a gathered
+ * parameter, a reduce bucket entry).
+ *
+ * Adam(W) over a list of tensors. */
+typedef struct zs_tensors zs_tensors;   /* opaque, host memory */
+
+#define ZS_ROUND_NEAREST    0
+#define ZS_ROUND_STOCHASTIC 1
+
+typedef struct {
+    int32_t state_bits;       /* 32, or 8                                      */
+    int32_t grad_dtype;       /* ZS_DTYPE_BF16, FP16 or FP32                   */
+    int32_t param_dtype;      /* of the 16-bit copies: ZS_DTYPE_BF16 or FP16   */
+    int32_t reserved;         /* must be 0                                     */
+} zs_tensors_config;
+
+/* One tensor: device pointers, each aligned to its element type at least
+ * (16 bytes on all of them, 8 on 8-bit moments, takes the vector path).
+ * With state_bits 8 the moments are blocks of 256 consecutive elements (the
+ * last block may be short): codes of one byte each in IEEE-like e4m3 and one
+ * float32 scale a block, so that
+ *   exp_avg[i]          = e4m3(exp_avg code i)    * exp_avg_scale[i / 256]
+ *   sqrt(exp_avg_sq[i]) = e4m3(exp_avg_sq code i) * exp_avg_sq_scale[i / 256]
+ * (the second moment is held as its root).  All bytes zero is the state of a
+ * run that has not begun. */
+typedef struct {
+    int64_t     numel;             /* >= 0                                     */
+    const void *grad;              /* grad_dtype [numel]                       */
+    void       *param;             /* param_dtype [numel], or NULL: no copy    */
+    float      *master;            /* fp32 [numel]                             */
+    void       *exp_avg;           /* fp32 [numel], or e4m3 codes [numel]      */
+    void       *exp_avg_sq;        /* fp32 [numel], or e4m3 codes [numel]      */
+    float      *exp_avg_scale;     /* [ceil(numel / 256)] with state_bits 8    */
+    float      *exp_avg_sq_scale;  /* the same                                 */
+} zs_tensor;
+
+typedef struct {
+    int32_t n_tensors, state_bits;
+    int64_t numel;                 /* of all tensors                           */
+    int64_t n_chunks;              /* CTAs of a step                           */
+    int64_t n_blocks;              /* 256-element blocks                       */
+    int64_t device_table_bytes;    /* device memory zs_tensors_upload needs    */
+} zs_tensors_info_t;
+
+/* Build a list (host only: no device call).  The list keeps the pointers,
+ * not what they point to; it is the caller's until zs_free_tensors.  Errors:
+ * ZS_EINVAL (config, numel, a NULL or misaligned pointer of a tensor with
+ * elements), ZS_ENOMEM. */
+zs_status zs_build_tensors(const zs_tensors_config *cfg, int32_t n, const zs_tensor *tensors,
+                           zs_tensors **out);
+void zs_free_tensors(zs_tensors *list);
+zs_status zs_tensors_info(const zs_tensors *list, zs_tensors_info_t *out);
+
+/* Copy the list's work table to device memory of the caller (16-byte
+ * aligned, >= device_table_bytes), enqueued on stream; the list uses it in
+ * every later step, as zs_plan_upload's table. */
+zs_status zs_tensors_upload(zs_tensors *list, void *d_table, int64_t bytes, void *stream);
+
+/* One Adam(W) step of every tensor in one launch.  d_clip_coef multiplies
+ * the gradients (NULL: 1); when d_flags (NULL: never) has ZS_SKIP_NONFINITE
+ * set nothing is written.
+ * state_bits 32: zs_adam_step's operations in its order, with its bits;
+ *   rounding must be ZS_ROUND_NEAREST.
+ * state_bits 8, in fp32, per element, in this order (m, r: the values held):
+ *   g = float(grad) * coef
+ *   AdamW: p = p - (lr*wd)*p        |  Adam-L2: g = g + wd*p
+ *   m = b1*m + (1-b1)*g;  r = sqrt(b2*(r*r) + (1-b2)*(g*g))
+ *   p = p - (lr/bc1) * (m / (r*(1/sqrt(bc2)) + eps));  param = rne16(p)
+ *   with lr/bc1 and 1/sqrt(bc2) computed in double and rounded to fp32; then
+ *   a block's scale is 2^(floor(log2 max) - 7) of its new |m| (of its r), at
+ *   least 2^-126, and the codes are m/scale and r/scale in e4m3.
+ *   ZS_ROUND_NEAREST: to nearest even.  ZS_ROUND_STOCHASTIC: to one of the
+ *   two neighbours, the upper one (in magnitude) with the probability of the
+ *   value's place between them, from 16 random bits: word j of Philox4x32
+ *   with 7 rounds, key seed, counter (q low, q high, index of the tensor,
+ *   step mod 2^32) belongs to element 4q + j of the tensor, its low half to
+ *   m, its high half to r.  With beta2 near 1 a step moves r by far less
+ *   than half the distance of two codes, and rounding to nearest would leave
+ *   it where it is: long runs want the stochastic rounding.
+ *   A positive r never gets code 0, which would divide an update by eps.
+ *   An element whose m or r is not finite gets a NaN code and does not count
+ *   for the scale.
+ * step >= 1.  Errors: ZS_EINVAL, ZS_ESTATE (not uploaded), ZS_ECUDA. */
+zs_status zs_adam_tensors(const zs_tensors *list, const zs_adam_hparams *hp, int64_t step,
+                          int32_t rounding, uint64_t seed, const float *d_clip_coef,
+                          const int32_t *d_flags, void *stream);
+
+/* Microscaled 4-bit matrices.  A matrix [rows][cols] is held as e2m1 codes
+ * (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives), two a byte, the element
+ * of even column in the low half, rows of 16 * ceil(cols / 32) bytes; and
+ * one scale byte s (2^(s-127); 255: NaN) for each 32 consecutive elements of
+ * a row, in tiles of 128 rows by 4 groups of 512 bytes each: row r, group g
+ * in tile (r / 128, g / 4), at byte (r % 32) * 16 + (r % 128 / 32) * 4 + g % 4
+ * of it, tiles row-major, their number along a row rounded up to even.
+ * Columns past cols hold code 0, rows and groups past the matrix scale 0. */
+typedef struct {
+    void *codes;              /* rows * row_bytes bytes, 16-byte aligned */
+    void *scales;             /* scale_bytes bytes, 16-byte aligned      */
+} zs_mx4;
+
+/* Bytes of a matrix: of a row of codes, of all codes, of all scales. */
+zs_status zs_mx4_sizes(int64_t rows, int64_t cols, int64_t *row_bytes, int64_t *code_bytes,
+                       int64_t *scale_bytes);
+
+/* Quantise x [rows][cols] (dtype, row stride ld >= cols elements; 16-byte
+ * vectors when x and its rows are 16-byte aligned).  along_rows: x itself,
+ * groups of 32 along its rows.  along_cols: the transposed matrix
+ * [cols][rows], groups along x's columns (what the gradients' products read).
+ * Either may be NULL; both come from one read.  A group with largest
+ * magnitude max has s = floor(log2 max) - 2 + 127, at least 0 (s = 0 also
+ * for a group of zeros or of fp32 subnormals), and the codes of
+ * x * 2^(127-s) to nearest, ties to even, at most 6 in magnitude.  A group
+ * with an infinity or NaN has s = 255 and codes 0: it is NaN in every
+ * product.  Errors: ZS_EINVAL, ZS_ECUDA. */
+zs_status zs_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
+                          const zs_mx4 *along_rows, const zs_mx4 *along_cols, void *stream);
+
+/* The values of a matrix: out [rows][cols] (dtype, row stride ldo). */
+zs_status zs_mx4_dequantize(const zs_mx4 *held, int64_t rows, int64_t cols, void *out, int64_t ldo,
+                            int32_t dtype, void *stream);
+
+/* out[m][n] = sum over k of a[m][k] * b[n][k] (dtype, row stride ldo),
+ * products and sums in fp32, rounded once.  For a linear layer y = x w^T:
+ *   y  = matmul(x along rows,  w along rows)     k = inputs
+ *   dx = matmul(dy along rows, w along cols)     k = outputs
+ *   dw = matmul(dy along cols, x along cols)     k = tokens
+ * k = 0 gives zeros.  Errors: ZS_EINVAL, ZS_ECUDA; a device wait that gave
+ * up is counted by zs_device_wait_timeouts. */
+zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const zs_mx4 *a, const zs_mx4 *b, void *out,
+                        int64_t ldo, int32_t dtype, void *stream);
 
 #ifdef __cplusplus
 }

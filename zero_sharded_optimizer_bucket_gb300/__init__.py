@@ -8,7 +8,10 @@ fails loudly when libzs.so is missing: there is no fallback.
 
 Functions keep the C names: zs_build_partition, zs_plan_upload,
 zs_partition, zs_reduce_scatter, zs_grad_norm, zs_adam_step,
-zs_all_gather_coalesced, zs_shard_step, plus the plan queries.
+zs_all_gather_coalesced, zs_shard_step, plus the plan queries; and, for
+training with little memory, zs_build_tensors / zs_adam_tensors and
+zs_mx4_quantize, zs_mx4_dequantize, zs_mx4_matmul, which take torch tensors
+and read sizes, strides and types from them.
 """
 from __future__ import annotations
 
@@ -27,7 +30,9 @@ _lib = C.CDLL(LIB_PATH)
 ZS_OK, ZS_EINVAL, ZS_ENOMEM, ZS_ECUDA, ZS_ESTATE, ZS_ETIMEOUT = 0, -1, -2, -3, -4, -5
 ZS_MAX_RANKS = 256
 ZS_SKIP_NONFINITE = 1
-ZS_DTYPE_BF16, ZS_DTYPE_FP16 = 0, 1
+ZS_DTYPE_BF16, ZS_DTYPE_FP16, ZS_DTYPE_FP32 = 0, 1, 2
+ZS_ROUND_NEAREST, ZS_ROUND_STOCHASTIC = 0, 1
+ZS_STATE_BLOCK = 256     # elements that share the scales of 8-bit moments
 ZS_NOALLOC_NORM_MAX_SCRATCH = 1 << 20
 TILE_DTYPE = [("dst", "<i8"), ("src", "<i8"), ("flat", "<i8"), ("win", "<i8"),
               ("len", "<i4"), ("valid", "<i4"), ("flat_len", "<i4"), ("bucket", "<i4")]
@@ -114,6 +119,27 @@ class zs_sched_event(C.Structure):
                 ("param", C.c_int32), ("offset", C.c_int64), ("aux", C.c_int64)]
 
 
+class zs_tensors_config(C.Structure):
+    _fields_ = [("state_bits", C.c_int32), ("grad_dtype", C.c_int32), ("param_dtype", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
+class zs_tensor(C.Structure):
+    _fields_ = [("numel", C.c_int64)] + \
+               [(n, C.c_void_p) for n in ("grad", "param", "master", "exp_avg", "exp_avg_sq",
+                                          "exp_avg_scale", "exp_avg_sq_scale")]
+
+
+class zs_tensors_info_t(C.Structure):
+    _fields_ = [("n_tensors", C.c_int32), ("state_bits", C.c_int32), ("numel", C.c_int64),
+                ("n_chunks", C.c_int64), ("n_blocks", C.c_int64),
+                ("device_table_bytes", C.c_int64)]
+
+
+class zs_mx4(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p)]
+
+
 _P = C.c_void_p
 _i32, _i64, _f32 = C.c_int32, C.c_int64, C.c_float
 
@@ -171,6 +197,17 @@ _sig("zs_sched_stats", _i32, [_P, C.POINTER(zs_sched_stats_t)])
 _sig("zs_sched_log", _i32, [_P, C.POINTER(zs_sched_event), _i64, C.POINTER(_i64)])
 _sig("zs_shard_step", _i32, [_P, _P, C.POINTER(zs_shard_state), _P, C.POINTER(zs_adam_hparams),
                              _i64, _f32, _P, _P, _P, _P, _P])
+_sig("zs_build_tensors", _i32, [C.POINTER(zs_tensors_config), _i32, C.POINTER(zs_tensor),
+                                C.POINTER(_P)])
+_sig("zs_free_tensors", None, [_P])
+_sig("zs_tensors_info", _i32, [_P, C.POINTER(zs_tensors_info_t)])
+_sig("zs_tensors_upload", _i32, [_P, _P, _i64, _P])
+_sig("zs_adam_tensors", _i32, [_P, C.POINTER(zs_adam_hparams), _i64, _i32, C.c_uint64, _P, _P, _P])
+_sig("zs_mx4_sizes", _i32, [_i64, _i64, C.POINTER(_i64), C.POINTER(_i64), C.POINTER(_i64)])
+_sig("zs_mx4_quantize", _i32, [_P, _i64, _i64, _i64, _i32, C.POINTER(zs_mx4), C.POINTER(zs_mx4), _P])
+_sig("zs_mx4_dequantize", _i32, [C.POINTER(zs_mx4), _i64, _i64, _P, _i64, _i32, _P])
+_sig("zs_mx4_matmul", _i32, [_i64, _i64, _i64, C.POINTER(zs_mx4), C.POINTER(zs_mx4), _P, _i64,
+                             _i32, _P])
 
 
 def _check(status: int, fn: str) -> None:
@@ -551,3 +588,160 @@ def zs_sched_log(sched) -> list:
     buf = (zs_sched_event * max(n.value, 1))()
     _check(_lib.zs_sched_log(sched.handle, buf, n.value, C.byref(n)), "zs_sched_log")
     return [(e.kind, e.module_pos, e.op, e.param, e.offset, e.aux) for e in buf[:n.value]]
+
+
+# ---------------------------------------------- training with little memory --
+
+def _dtype(t) -> int:
+    """ZS_DTYPE_* of a torch tensor."""
+    name = str(t.dtype)
+    got = {"torch.bfloat16": ZS_DTYPE_BF16, "torch.float16": ZS_DTYPE_FP16,
+           "torch.float32": ZS_DTYPE_FP32}.get(name)
+    if got is None:
+        raise TypeError(f"bfloat16, float16 or float32 expected, got {name}")
+    return got
+
+
+class Tensors:
+    """Owner of a zs_tensors* (freed with the object); keeps the tensors alive."""
+
+    def __init__(self, handle: int, keep):
+        self._h, self._keep, self._table = handle, keep, None
+
+    @property
+    def handle(self):
+        return self._h
+
+    def __del__(self):
+        if getattr(self, "_h", None):
+            _lib.zs_free_tensors(self._h)
+            self._h = None
+
+
+_TENSOR_ITEMS = ("grad", "param", "master", "exp_avg", "exp_avg_sq", "exp_avg_scale",
+                 "exp_avg_sq_scale")
+
+
+def zs_build_tensors(tensors, state_bits: int = 32, grad_dtype=None, param_dtype=None) -> Tensors:
+    """tensors: a list of dicts by the names of zs_tensor, of contiguous torch
+    tensors (param, and with state_bits 32 the scales, may be left out), or of
+    addresses with "numel" and both dtypes given.  Torch tensors give the
+    dtypes themselves; all gradients have one, all parameters one."""
+    size = {"master": 4, "exp_avg": state_bits // 8, "exp_avg_sq": state_bits // 8,
+            "exp_avg_scale": 4, "exp_avg_sq_scale": 4}
+    n = len(tensors)
+    arr = (zs_tensor * max(n, 1))()
+    for i, t in enumerate(tensors):
+        unknown = set(t) - set(_TENSOR_ITEMS) - {"numel"}
+        if unknown:
+            raise TypeError(f"tensor {i}: unknown {sorted(unknown)}")
+        numel = int(t["numel"]) if "numel" in t else t["master"].numel()
+        arr[i].numel = numel
+        for name in _TENSOR_ITEMS:
+            x = t.get(name)
+            if x is None:
+                continue
+            if hasattr(x, "data_ptr"):
+                need = -(-numel // ZS_STATE_BLOCK) if name.endswith("_scale") else numel
+                if x.numel() < need or not x.is_contiguous():
+                    raise ValueError(f"tensor {i}: {name} is not {need} contiguous elements")
+                if name in ("grad", "param"):
+                    d = _dtype(x)
+                    if name == "grad":
+                        grad_dtype = d if grad_dtype is None else grad_dtype
+                    else:
+                        param_dtype = d if param_dtype is None else param_dtype
+                    if d != (grad_dtype if name == "grad" else param_dtype):
+                        raise TypeError(f"tensor {i}: {name} is {x.dtype}, another type than before it")
+                elif x.element_size() != size[name]:
+                    raise TypeError(f"tensor {i}: {name} is {x.dtype}, {size[name]} bytes an element expected")
+            setattr(arr[i], name, _ptr(x))
+    cfg = zs_tensors_config(int(state_bits), ZS_DTYPE_BF16 if grad_dtype is None else int(grad_dtype),
+                            ZS_DTYPE_BF16 if param_dtype is None else int(param_dtype), 0)
+    out = _P()
+    _check(_lib.zs_build_tensors(C.byref(cfg), n, arr, C.byref(out)), "zs_build_tensors")
+    return Tensors(out.value, list(tensors))
+
+
+def zs_free_tensors(tensors: Tensors) -> None:
+    if tensors._h:
+        _lib.zs_free_tensors(tensors._h)
+        tensors._h = None
+
+
+def zs_tensors_info(tensors) -> dict:
+    o = zs_tensors_info_t()
+    _check(_lib.zs_tensors_info(tensors.handle, C.byref(o)), "zs_tensors_info")
+    return _to_dict(o)
+
+
+def zs_tensors_upload(tensors, d_table, nbytes: int, stream=None) -> None:
+    _check(_lib.zs_tensors_upload(tensors.handle, _ptr(d_table), int(nbytes), _stream(stream)),
+           "zs_tensors_upload")
+    tensors._table = d_table
+
+
+_ROUNDING = {"nearest": ZS_ROUND_NEAREST, "stochastic": ZS_ROUND_STOCHASTIC}
+
+
+def zs_adam_tensors(tensors, hp, step: int, d_clip_coef=None, d_flags=None, rounding="nearest",
+                    seed: int = 0, stream=None) -> None:
+    h = _hp(hp)
+    _check(_lib.zs_adam_tensors(tensors.handle, C.byref(h), int(step),
+                                _ROUNDING[rounding] if isinstance(rounding, str) else int(rounding),
+                                int(seed) & 0xFFFFFFFFFFFFFFFF, _ptr(d_clip_coef), _ptr(d_flags),
+                                _stream(stream)), "zs_adam_tensors")
+
+
+def zs_mx4_sizes(rows: int, cols: int) -> dict:
+    r, c, s = _i64(), _i64(), _i64()
+    _check(_lib.zs_mx4_sizes(int(rows), int(cols), C.byref(r), C.byref(c), C.byref(s)), "zs_mx4_sizes")
+    return dict(row_bytes=r.value, code_bytes=c.value, scale_bytes=s.value)
+
+
+def _mx4(held, rows: int, cols: int):
+    """zs_mx4 of a dict with "codes" [rows, row_bytes] and "scales" (uint8
+    tensors, or addresses), whose tensors are large enough for rows x cols."""
+    if held is None:
+        return None
+    if hasattr(held["codes"], "numel"):
+        size = zs_mx4_sizes(rows, cols)
+        for name, need in (("codes", size["code_bytes"]), ("scales", size["scale_bytes"])):
+            x = held[name]
+            if x.element_size() != 1 or x.numel() < need or not x.is_contiguous():
+                raise ValueError(f"{name}: {need} contiguous bytes expected for {rows} x {cols}")
+    return zs_mx4(_ptr(held["codes"]), _ptr(held["scales"]))
+
+
+def _matrix(x, what: str):
+    """(rows, cols, row stride) of a 2-D torch tensor whose rows are contiguous."""
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{what}: a matrix with contiguous rows expected")
+    return x.shape[0], x.shape[1], max(x.stride(0), x.shape[1]) if x.shape[0] > 1 else x.shape[1]
+
+
+def zs_mx4_quantize(x, rows=None, cols=None, stream=None) -> None:
+    """x: [r, c] torch matrix.  rows: the dict of x held along its rows
+    ([r, c]); cols: of the transposed matrix ([c, r]); either may be None."""
+    r, c, ld = _matrix(x, "x")
+    a, b = _mx4(rows, r, c), _mx4(cols, c, r)
+    _check(_lib.zs_mx4_quantize(_ptr(x), r, c, ld, _dtype(x), C.byref(a) if a else None,
+                                C.byref(b) if b else None, _stream(stream)), "zs_mx4_quantize")
+
+
+def zs_mx4_dequantize(held, out, stream=None):
+    """out: [r, c] torch matrix that receives the values; returned."""
+    r, c, ld = _matrix(out, "out")
+    h = _mx4(held, r, c)
+    _check(_lib.zs_mx4_dequantize(C.byref(h), r, c, _ptr(out), ld, _dtype(out), _stream(stream)),
+           "zs_mx4_dequantize")
+    return out
+
+
+def zs_mx4_matmul(a, b, k: int, out, stream=None):
+    """out [m, n] = a [m, k] b [n, k]^T of two held matrices; out is returned."""
+    m, n, ld = _matrix(out, "out")
+    ha, hb = _mx4(a, m, k), _mx4(b, n, k)
+    _check(_lib.zs_mx4_matmul(m, n, int(k), C.byref(ha), C.byref(hb), _ptr(out), ld, _dtype(out),
+                              _stream(stream)), "zs_mx4_matmul")
+    return out

@@ -50,7 +50,21 @@ zs_status check_state(const zs_plan *P, const zs_shard_state *st, bool grads, bo
     return ZS_OK;
 }
 
-zs_status adam_scalars(const zs_adam_hparams *hp, int64_t step, ZsAdamScalars *c, const char *fn) {
+zs_status check_scalars(const float *a, const float *b, const int32_t *f, const char *fn) {
+    if (!al(a, 4) || !al(b, 4) || !al(f, 4))
+        return zs_fail(ZS_EINVAL, "%s: device scalar pointers must be non-NULL and 4-byte aligned", fn);
+    return ZS_OK;
+}
+
+zs_status check_scratch(const zs_plan *P, const double *s, const char *fn) {
+    if (!al(s, 8)) return zs_fail(ZS_EINVAL, "%s: norm_scratch NULL or not 8-byte aligned", fn);
+    (void)P;
+    return ZS_OK;
+}
+
+}  // namespace
+
+zs_status zs_adam_scalars(const zs_adam_hparams *hp, int64_t step, ZsAdamScalars *c, const char *fn) {
     if (!hp) return zs_fail(ZS_EINVAL, "%s: NULL hyper-parameters", fn);
     if (step < 1) return zs_fail(ZS_EINVAL, "%s: step %lld < 1", fn, (long long)step);
     if (!(hp->lr >= 0.0f) || !(hp->eps >= 0.0f) || !(hp->weight_decay >= 0.0f) ||
@@ -65,29 +79,16 @@ zs_status adam_scalars(const zs_adam_hparams *hp, int64_t step, ZsAdamScalars *c
     c->omb1 = (float)(1.0 - (double)hp->beta1);
     c->omb2 = (float)(1.0 - (double)hp->beta2);
     c->lr_wd = (float)((double)hp->lr * (double)hp->weight_decay);
-    if (hp->bias_correction) {
-        c->bc1 = (float)(1.0 - std::pow((double)hp->beta1, (double)step));
-        c->bc2 = (float)(1.0 - std::pow((double)hp->beta2, (double)step));
-    } else {
-        c->bc1 = c->bc2 = 1.0f;
-    }
     c->adamw = hp->adamw ? 1 : 0;
+    const double bc1 = hp->bias_correction ? 1.0 - std::pow((double)hp->beta1, (double)step) : 1.0;
+    const double bc2 = hp->bias_correction ? 1.0 - std::pow((double)hp->beta2, (double)step) : 1.0;
+    c->bc1 = (float)bc1;
+    c->bc2 = (float)bc2;
+    // for the one division of the update with 8-bit moments
+    c->step_size = (float)((double)hp->lr / bc1);
+    c->root = (float)(1.0 / std::sqrt(bc2));
     return ZS_OK;
 }
-
-zs_status check_scalars(const float *a, const float *b, const int32_t *f, const char *fn) {
-    if (!al(a, 4) || !al(b, 4) || !al(f, 4))
-        return zs_fail(ZS_EINVAL, "%s: device scalar pointers must be non-NULL and 4-byte aligned", fn);
-    return ZS_OK;
-}
-
-zs_status check_scratch(const zs_plan *P, const double *s, const char *fn) {
-    if (!al(s, 8)) return zs_fail(ZS_EINVAL, "%s: norm_scratch NULL or not 8-byte aligned", fn);
-    (void)P;
-    return ZS_OK;
-}
-
-}  // namespace
 
 extern "C" {
 
@@ -186,7 +187,7 @@ zs_status zs_adam_step(const zs_plan *P, int32_t sub_group, const zs_adam_hparam
     if (sub_group < -1 || sub_group >= (int32_t)P->sub_groups.size())
         return zs_fail(ZS_EINVAL, "%s: sub_group %d out of range", fn, sub_group);
     ZsAdamScalars c;
-    zs_status r = adam_scalars(hp, step, &c, fn);
+    zs_status r = zs_adam_scalars(hp, step, &c, fn);
     if (r) return r;
     if (!al(d_clip_coef, 4) || !al(d_flags, 4))
         return zs_fail(ZS_EINVAL, "%s: d_clip_coef / d_flags NULL or misaligned", fn);
@@ -275,8 +276,10 @@ extern "C" {
 
 zs_status zs_device_wait_timeouts(int32_t *count, int32_t reset) {
     if (!count) return zs_fail(ZS_EINVAL, "zs_device_wait_timeouts: NULL count");
-    int c = 0;
-    const cudaError_t e = zsl_bulk_wait_timeouts(&c, reset != 0);
+    int c = 0, mx4 = 0;
+    cudaError_t e = zsl_bulk_wait_timeouts(&c, reset != 0);
+    if (e == cudaSuccess) e = zsl_mx4_wait_timeouts(&mx4, reset != 0);
+    c += mx4;
     if (e != cudaSuccess) return cuda_status(e, "zs_device_wait_timeouts");
     *count = c;
     if (c != 0)
@@ -394,7 +397,7 @@ zs_status zs_adam_gather(const zs_plan *P, const zs_adam_hparams *hp, int64_t st
     zs_status r = need_table(P, fn);
     if (r) return r;
     ZsAdamScalars c;
-    if ((r = adam_scalars(hp, step, &c, fn))) return r;
+    if ((r = zs_adam_scalars(hp, step, &c, fn))) return r;
     if ((r = check_state(P, st, true, true, fn, true))) return r;
     if (!al(d_clip_coef, 4) || !al(d_flags, 4))
         return zs_fail(ZS_EINVAL, "%s: d_clip_coef / d_flags NULL or misaligned", fn);
@@ -412,7 +415,7 @@ zs_status zs_shard_step(const zs_plan *P, const void *const *d_rank_grads,
     zs_status r = need_table(P, fn);
     if (r) return r;
     ZsAdamScalars c;
-    if ((r = adam_scalars(hp, step, &c, fn))) return r;
+    if ((r = zs_adam_scalars(hp, step, &c, fn))) return r;
     if ((r = check_state(P, st, true, true, fn, true))) return r;
     if ((r = check_scratch(P, norm_scratch, fn))) return r;
     if ((r = check_scalars(d_norm, d_clip_coef, d_flags, fn))) return r;
@@ -436,7 +439,7 @@ zs_status zs_shard_step_scaled(const zs_plan *P, const void *const *d_rank_grads
     zs_status r = need_table(P, fn);
     if (r) return r;
     ZsAdamScalars c;
-    if ((r = adam_scalars(hp, step, &c, fn))) return r;
+    if ((r = zs_adam_scalars(hp, step, &c, fn))) return r;
     if ((r = check_state(P, st, true, true, fn, true))) return r;
     if ((r = check_scratch(P, norm_scratch, fn))) return r;
     if ((r = check_scalars(d_norm, d_clip_coef, d_flags, fn))) return r;

@@ -10,7 +10,11 @@
 struct ZsAdamScalars {
     float lr, b1, b2, omb1, omb2, eps, wd, lr_wd, bc1, bc2;
     int adamw;
+    float step_size, root;   // lr / bc1, 1 / sqrt(bc2) (8-bit moments)
 };
+
+// The scalars of one update, checked (ZS_EINVAL in the name of fn).
+zs_status zs_adam_scalars(const zs_adam_hparams *hp, int64_t step, ZsAdamScalars *c, const char *fn);
 
 // Loss scale of the norm finish (see zs_loss_scaler); d_scale NULL: S = 1.
 struct ZsScaleArgs {
@@ -76,3 +80,5 @@ cudaError_t zsl_gather(const ZsGatherArgs &a, const uint16_t *shards, uint16_t *
 cudaError_t zsl_bulk_wait_timeouts(int *count, bool reset);
 // One bounded wait on an mbarrier nothing arrives on (gives up after limit_ns).
 cudaError_t zsl_wait_timeout_test(int64_t limit_ns, cudaStream_t s);
+// The same of the 4-bit product.
+cudaError_t zsl_mx4_wait_timeouts(int *count, bool reset);

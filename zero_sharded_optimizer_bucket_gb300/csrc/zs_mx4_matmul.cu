@@ -1,0 +1,443 @@
+// The product of two microscaled 4-bit matrices on the 5th-generation tensor
+// cores (zs_mx4_matmul): out[m][n] = sum over k of A[m][k] * B[n][k].
+//
+// tcgen05.mma kind::mxf4 multiplies e2m1 codes, applies both scales and adds
+// in float32 in tensor memory, 64 elements of k an instruction.  A stage is
+// 256 elements of k: 128 bytes a row, one 128-byte swizzled TMA box an
+// operand, and two scale atoms a 128 rows, which tcgen05.cp moves to tensor
+// memory.  A warp loads, one thread issues the products, four warps store.
+#include <cuda.h>
+
+#include <atomic>
+
+#include "zs_launch.h"
+#include "zs_mx4.cuh"
+
+namespace zsk {
+
+constexpr int MM_P = 128;                 // rows of P a tile: lanes of tensor memory
+constexpr int MM_KB = 128;                // bytes of a row a stage: 256 elements
+constexpr int MM_THREADS = 192;           // 4 warps store, 1 loads, 1 multiplies
+constexpr uint64_t MM_WAIT_NS = 1000000000ull;   // one wait gives up after 1 s
+
+__device__ int g_mx4_wait_timeouts;       // waits that gave up
+
+// P holds the tile's 128 rows, Q its BN; D[p][q].
+template <int BN>
+struct MmShape {
+    static constexpr int QA = (BN + 127) / 128;                 // scale atoms of Q per 4 groups
+    static constexpr int P_BYTES = MM_P * MM_KB, Q_BYTES = BN * MM_KB;
+    static constexpr int SP_BYTES = 2 * MX4_ATOM, SQ_BYTES = 2 * QA * MX4_ATOM;
+    static constexpr int STAGE = P_BYTES + Q_BYTES + SP_BYTES + SQ_BYTES;    // a multiple of 1024
+    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 3 : 4;
+    // tensor memory: accumulator, then two sets of scales
+    static constexpr int SP_COL = BN < 32 ? 32 : BN, SQ_COL = SP_COL + 16;
+    static constexpr int USED = SQ_COL + 16 * QA;
+    static constexpr int COLS = USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
+    static constexpr int RED = BN * MM_P * 4;                  // partial sums of a split
+    static constexpr int BODY = STAGES * STAGE > RED ? STAGES * STAGE : RED;
+    static constexpr int SMEM = BODY + 1024;                   // and room to align
+};
+
+struct MmArgs {
+    const uint8_t *p_scales, *q_scales;
+    void *out;
+    int64_t ldo;
+    int32_t np, nq;           // rows of P and Q
+    int32_t k_tiles, atoms;   // stages along k, scale atoms a row tile
+    int32_t p_tiles, q_tiles;
+    int32_t split;            // CTAs of the cluster that share the tile's k
+    int32_t dtype;
+    int32_t vec;              // 16-byte stores of whole runs
+};
+
+__device__ __forceinline__ uint64_t mm_desc(uint32_t addr, uint32_t sbo, uint64_t layout) {
+    // shared-memory operand: start address, leading and stride byte offsets
+    // (16-byte units), version 1, swizzle
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(sbo >> 4) << 32) |
+           ((uint64_t)1 << 46) | (layout << 61);
+}
+
+__device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        :
+        : "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void bulk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :
+                 : "r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" : : "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : : : "memory");
+}
+
+__device__ __forceinline__ uint32_t mm_cast(float x, int dtype) {
+    return dtype == ZS_DTYPE_FP16 ? FP16T::from_f32(x) : BF16T::from_f32(x);
+}
+
+// 32 neighbouring results of one row of out, the first n of them inside
+__device__ __forceinline__ void store_run(const MmArgs &a, int64_t at, const float (&f)[32], int n) {
+    if (a.dtype == ZS_DTYPE_FP32) {
+        float *o = static_cast<float *>(a.out) + at;
+        if (a.vec && n >= 32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                reinterpret_cast<float4 *>(o)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) if (i < n) o[i] = f[i];
+        }
+        return;
+    }
+    uint16_t *o = static_cast<uint16_t *>(a.out) + at;
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = mm_cast(f[i], a.dtype);
+    if (a.vec && n >= 32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) reinterpret_cast<uint4 *>(o)[i] = pack8(r + 8 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) if (i < n) o[i] = (uint16_t)r[i];
+    }
+}
+
+__device__ __forceinline__ void store_one(const MmArgs &a, int64_t at, float f) {
+    if (a.dtype == ZS_DTYPE_FP32) static_cast<float *>(a.out)[at] = f;
+    else static_cast<uint16_t *>(a.out)[at] = (uint16_t)mm_cast(f, a.dtype);
+}
+
+// FLIP: P are the rows of B (features) and Q those of A (tokens), for few
+// tokens: out[q][p].  Otherwise out[p][q].
+template <int BN, bool FLIP>
+__global__ void __launch_bounds__(MM_THREADS)
+mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, MmArgs a) {
+    using S = MmShape<BN>;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[2 * S::STAGES + 1];
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile int failed;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t bar0 = smem_u32(bars), done = bar0 + 16 * S::STAGES;
+    auto full = [&](int s) { return bar0 + 8 * s; };
+    auto empty = [&](int s) { return bar0 + 8 * (S::STAGES + s); };
+    const int part = a.split > 1 ? (int)(blockIdx.x % a.split) : 0;
+    const int tile = (int)(blockIdx.x / a.split);
+    const int pt = tile % a.p_tiles, qt = tile / a.p_tiles;
+    const int k0 = (int)((int64_t)a.k_tiles * part / a.split), k1 = (int)((int64_t)a.k_tiles * (part + 1) / a.split);
+    if (threadIdx.x == 0) {
+        failed = 0;
+        for (int i = 0; i < 2 * S::STAGES + 1; ++i)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" : : "r"(bar0 + 8 * i) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" : : : "memory");
+        asm volatile("fence.proxy.async.shared::cta;" : : : "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     :
+                     : "r"(smem_u32(&tmem_base)), "n"(S::COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" : : : "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
+    const uint32_t tmem = tmem_base;
+
+    int issued = 0;                        // stages that the loads of warp 4 were issued for
+    if (warp == 4 && lane == 0) {
+        const uint8_t *sp = a.p_scales + ((int64_t)pt * a.atoms) * MX4_ATOM;
+        for (int k = k0; k < k1; ++k) {
+            const int i = k - k0, s = i % S::STAGES;
+            if (i >= S::STAGES && !mbar_wait(empty(s), (uint32_t)((i / S::STAGES - 1) & 1), MM_WAIT_NS)) {
+                failed = 1;
+                break;
+            }
+            const uint32_t p = base + s * S::STAGE, q = p + S::P_BYTES, scp = q + S::Q_BYTES, scq = scp + S::SP_BYTES;
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(S::STAGE) : "memory");
+            tma2d(p, &map_p, k * MM_KB, pt * MM_P, full(s));
+            tma2d(q, &map_q, k * MM_KB, qt * BN, full(s));
+            bulk(scp, sp + (int64_t)k * S::SP_BYTES, S::SP_BYTES, full(s));
+#pragma unroll
+            for (int j = 0; j < S::QA; ++j) {
+                // a row tile past the matrix's last scales no stored column
+                const int rt = min((int)((int64_t)qt * BN / 128) + j, (a.nq - 1) / 128);
+                bulk(scq + j * S::SP_BYTES, a.q_scales + ((int64_t)rt * a.atoms + 2 * k) * MX4_ATOM, S::SP_BYTES, full(s));
+            }
+            issued = i + 1;
+        }
+    } else if (warp == 5 && lane == 0) {
+        // kind::mxf4: e2m1 x e2m1, ue8m0 scales, M = 128, N = BN
+        const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(BN / 8) << 17) | (1u << 23) | (8u << 24);
+        for (int k = k0; k < k1; ++k) {
+            const int i = k - k0, s = i % S::STAGES;
+            if (!mbar_wait(full(s), (uint32_t)((i / S::STAGES) & 1), MM_WAIT_NS)) {
+                failed = 1;
+                break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
+            const uint32_t p = base + s * S::STAGE, q = p + S::P_BYTES, scp = q + S::Q_BYTES, scq = scp + S::SP_BYTES;
+            const uint32_t tp = tmem + S::SP_COL + 8 * (i & 1), tq = tmem + S::SQ_COL + 8 * S::QA * (i & 1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
+                             :
+                             : "r"(tp + 4 * j), "l"(mm_desc(scp + j * MX4_ATOM, 128, 0))
+                             : "memory");
+#pragma unroll
+                for (int h = 0; h < S::QA; ++h)
+                    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
+                                 :
+                                 : "r"(tq + 4 * (S::QA * j + h)), "l"(mm_desc(scq + h * S::SP_BYTES + j * MX4_ATOM, 128, 0))
+                                 : "memory");
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t id = (uint32_t)(2 * (j & 1));        // scale bytes 0-1 or 2-3 of an atom
+                const uint32_t d = idesc | (id << 4) | (id << 29);
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+                    "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                    :
+                    : "r"(tmem), "l"(mm_desc(p + 32 * j, 1024, 2)), "l"(mm_desc(q + 32 * j, 1024, 2)), "r"(d),
+                      "r"(tp + 4 * (j >> 1)), "r"(tq + 4 * S::QA * (j >> 1)), "r"((uint32_t)(i > 0 || j > 0))
+                    : "memory");
+            }
+            tc_commit(empty(s));
+        }
+        tc_commit(done);
+    }
+    // everyone waits until the products of this CTA are in tensor memory
+    // (the idle lanes of the two issuing warps only once their lane is through)
+    __syncwarp();
+    if (!mbar_wait(done, 0, 4 * MM_WAIT_NS)) failed = 1;
+    __syncwarp();
+    asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
+    const int p0 = pt * MM_P, q0 = qt * BN;
+    if (a.split > 1) {
+        // partial sums to shared memory as [q][p] (the loads and products
+        // that used it are done), then each CTA of the cluster adds its share of the columns, over
+        // the parts in order
+        if (warp < 4) {
+#pragma unroll 1
+            for (int c = 0; c < BN; c += 32) {
+                uint32_t v[32];
+                tc_ld32(tmem + ((uint32_t)warp << 21) + c, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (BN >= 32 || i < BN)
+                        asm volatile("st.shared.b32 [%0], %1;" : : "r"(base + 4 * ((c + i) * MM_P + 32 * warp + lane)), "r"(v[i]) : "memory");
+            }
+        }
+        asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" : : : "memory");
+        const int c0 = BN * part / a.split, c1 = BN * (part + 1) / a.split;
+        if (!failed) {
+            for (int u = threadIdx.x; u < (c1 - c0) * MM_P; u += MM_THREADS) {
+                // neighbouring threads take neighbouring elements of out
+                const int w = c1 - c0;
+                const int q = FLIP ? c0 + u / MM_P : c0 + u % w, p = FLIP ? u % MM_P : u / w;
+                float sum = 0.0f;
+                for (int r = 0; r < a.split; ++r) {
+                    uint32_t remote;
+                    float x;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(base + 4 * (q * MM_P + p)), "r"(r));
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(remote) : "memory");
+                    sum = __fadd_rn(sum, x);
+                }
+                if (p0 + p < a.np && q0 + q < a.nq)
+                    store_one(a, FLIP ? (int64_t)(q0 + q) * a.ldo + p0 + p : (int64_t)(p0 + p) * a.ldo + q0 + q, sum);
+            }
+        }
+        asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" : : : "memory");
+    } else if (warp < 4 && !failed) {
+        const int p = p0 + 32 * warp + lane;
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 32) {
+            if (q0 + c >= a.nq) break;
+            uint32_t v[32];
+            tc_ld32(tmem + ((uint32_t)warp << 21) + c, v);
+            if (p < a.np) {
+                float f[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+                if (FLIP) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < BN && q0 + c + i < a.nq) store_one(a, (int64_t)(q0 + c + i) * a.ldo + p, f[i]);
+                } else {
+                    store_run(a, (int64_t)p * a.ldo + q0 + c, f, a.nq - q0 - c);
+                }
+            }
+        }
+    }
+    if (warp == 4 && lane == 0 && failed) {
+        // let the loads already issued land before the shared memory goes away
+        for (int i = issued > S::STAGES ? issued - S::STAGES : 0; i < issued; ++i)
+            mbar_wait(full(i % S::STAGES), (uint32_t)((i / S::STAGES) & 1), MM_WAIT_NS);
+        atomicAdd(&g_mx4_wait_timeouts, 1);
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
+    __syncthreads();
+    if (warp == 0) {
+        asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" : : "r"(tmem), "n"(S::COLS));
+    }
+}
+
+// out = 0, for a product over no elements
+__global__ void mx4_zero_kernel(void *out, int64_t m, int64_t n, int64_t ldo, int fp32) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < m * n; i += (int64_t)gridDim.x * 256) {
+        const int64_t at = i / n * ldo + i % n;
+        if (fp32) static_cast<float *>(out)[at] = 0.0f;
+        else static_cast<uint16_t *>(out)[at] = 0;
+    }
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiled encode_tiled() {
+    static std::atomic<void *> fn{nullptr};
+    void *p = fn.load(std::memory_order_relaxed);
+    if (!p) {
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn.store(p, std::memory_order_relaxed);
+    }
+    return reinterpret_cast<EncodeTiled>(p);
+}
+
+// Codes as bytes [rows][row_bytes]: boxes of 128 bytes (256 elements) by
+// `box` rows; zero (value 0) outside.
+static bool code_map(CUtensorMap *m, const void *codes, int64_t rows, int64_t row_bytes, int box) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)row_bytes};
+    const cuuint32_t boxes[2] = {MM_KB, (cuuint32_t)box}, ones[2] = {1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, boxes, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, bool FLIP>
+static cudaError_t mm_launch(const CUtensorMap &p, const CUtensorMap &q, const MmArgs &a, cudaStream_t s) {
+    using S = MmShape<BN>;
+    cudaError_t e = cudaFuncSetAttribute(mx4_matmul_kernel<BN, FLIP>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)a.p_tiles * a.q_tiles * a.split));
+    cfg.blockDim = dim3(MM_THREADS);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)a.split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, mx4_matmul_kernel<BN, FLIP>, p, q, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace zsk
+
+cudaError_t zsl_mx4_wait_timeouts(int *count, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(count, zsk::g_mx4_wait_timeouts, sizeof(int));
+    if (e == cudaSuccess && reset) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(zsk::g_mx4_wait_timeouts, &zero, sizeof(int));
+    }
+    return e;
+}
+
+extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const zs_mx4 *A, const zs_mx4 *B, void *out,
+                                   int64_t ldo, int32_t dtype, void *stream) {
+    const char *fn = "zs_mx4_matmul";
+    constexpr int64_t MOST = (int64_t)1 << 31;
+    if (m < 0 || n < 0 || k < 0 || m >= MOST || n >= MOST || k >= MOST)
+        return zs_fail(ZS_EINVAL, "%s: m %lld, n %lld, k %lld out of range", fn, (long long)m, (long long)n, (long long)k);
+    if (dtype < ZS_DTYPE_BF16 || dtype > ZS_DTYPE_FP32) return zs_fail(ZS_EINVAL, "%s: dtype %d", fn, dtype);
+    if (ldo < n) return zs_fail(ZS_EINVAL, "%s: row stride %lld < n = %lld", fn, (long long)ldo, (long long)n);
+    if (!A || !B) return zs_fail(ZS_EINVAL, "%s: NULL matrix", fn);
+    if (m == 0 || n == 0) {
+        zs_clear_error();
+        return ZS_OK;
+    }
+    const int size = dtype == ZS_DTYPE_FP32 ? 4 : 2;
+    if (!out || reinterpret_cast<uintptr_t>(out) % size)
+        return zs_fail(ZS_EINVAL, "%s: out NULL or not aligned to its elements", fn);
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (k == 0) {
+        const int64_t grid = (m * n + 255) / 256;
+        zsk::mx4_zero_kernel<<<(unsigned)(grid < 4096 ? grid : 4096), 256, 0, s>>>(out, m, n, ldo, dtype == ZS_DTYPE_FP32);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return zs_fail(ZS_ECUDA, "%s: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
+        zs_clear_error();
+        return ZS_OK;
+    }
+    const void *four[4] = {A->codes, A->scales, B->codes, B->scales};
+    for (const void *p : four)
+        if (!p || (reinterpret_cast<uintptr_t>(p) & 15))
+            return zs_fail(ZS_EINVAL, "%s: codes or scales NULL or not 16-byte aligned", fn);
+    const bool flip = m <= 128;
+    const int64_t np = flip ? n : m, nq = flip ? m : n;
+    const zs_mx4 *P = flip ? B : A, *Q = flip ? A : B;
+    int bn = 128;
+    if (flip) bn = nq <= 16 ? 16 : nq <= 32 ? 32 : nq <= 64 ? 64 : 128;
+    else if (((np + 127) / 128) * ((nq + 255) / 256) >= 152) bn = 256;
+    zsk::MmArgs a;
+    a.p_scales = static_cast<const uint8_t *>(P->scales);
+    a.q_scales = static_cast<const uint8_t *>(Q->scales);
+    a.out = out;
+    a.ldo = ldo;
+    a.np = (int32_t)np;
+    a.nq = (int32_t)nq;
+    a.k_tiles = (int32_t)((k + 255) / 256);
+    a.atoms = (int32_t)mx4_atoms(k);
+    const int64_t pt = (np + 127) / 128, qt = (nq + bn - 1) / bn;
+    a.p_tiles = (int32_t)pt;
+    a.q_tiles = (int32_t)qt;
+    int split = 1;
+    while (split < 8 && pt * qt * split * 2 <= 304 && a.k_tiles >= 4 * split) split *= 2;
+    if (pt * qt * split > 0x7FFFFFFF) return zs_fail(ZS_EINVAL, "%s: too many tiles", fn);
+    a.split = split;
+    a.dtype = dtype;
+    a.vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ldo * size % 16 == 0;
+    CUtensorMap mp, mq;
+    if (!zsk::code_map(&mp, P->codes, np, mx4_row_bytes(k), zsk::MM_P) ||
+        !zsk::code_map(&mq, Q->codes, nq, mx4_row_bytes(k), bn))
+        return zs_fail(ZS_ECUDA, "%s: cuTensorMapEncodeTiled failed", fn);
+    using namespace zsk;
+    cudaError_t e;
+    if (flip)
+        e = bn == 16 ? mm_launch<16, true>(mp, mq, a, s) : bn == 32 ? mm_launch<32, true>(mp, mq, a, s)
+          : bn == 64 ? mm_launch<64, true>(mp, mq, a, s) : mm_launch<128, true>(mp, mq, a, s);
+    else
+        e = bn == 256 ? mm_launch<256, false>(mp, mq, a, s) : mm_launch<128, false>(mp, mq, a, s);
+    if (e != cudaSuccess) return zs_fail(ZS_ECUDA, "%s: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
+    zs_clear_error();
+    return ZS_OK;
+}
