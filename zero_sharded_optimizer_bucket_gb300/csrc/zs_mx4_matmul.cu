@@ -230,7 +230,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     // everyone waits until the products of this CTA are in tensor memory
     // (the idle lanes of the two issuing warps only once their lane is through)
     __syncwarp();
-    if (!mbar_wait(done, 0, 4 * MM_WAIT_NS)) failed = 1;
+    if (!mbar_wait(done, 0, 4 * MM_WAIT_NS + 4000ull * (uint64_t)(k1 - k0))) failed = 1;
     __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
     const int p0 = pt * MM_P, q0 = qt * BN;
@@ -304,6 +304,258 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     }
 }
 
+// ------------------------------------------------------ two-SM products --
+// For products with enough work: a cluster of two CTAs (two SMs) works on a
+// 256 x 256 tile of out, each holding half of the rows of A and half of
+// those of B in its shared memory, so that a byte of B is read once for
+// 256 rows.  Persistent: a pair walks tiles, the loads running ahead over
+// the tile boundary, while 8 warps of each CTA empty the accumulator of the
+// previous tile into registers, release it, and store.
+constexpr int PAIR_ROWS = 256, PAIR_COLS = 256;
+constexpr int PAIR_STAGES = 5;
+constexpr int PAIR_THREADS = 320;         // 8 warps store, 1 loads, 1 multiplies (leader only)
+constexpr int PAIR_P = 128 * MM_KB, PAIR_Q = 128 * MM_KB;
+constexpr int PAIR_SP = 2 * MX4_ATOM, PAIR_SQ = 4 * MX4_ATOM;
+constexpr int PAIR_STAGE = PAIR_P + PAIR_Q + PAIR_SP + PAIR_SQ;
+constexpr int PAIR_SLAB = 32 * 33 * 4;    // a storing warp's transposition buffer
+constexpr int PAIR_SMEM = PAIR_STAGES * PAIR_STAGE + 8 * PAIR_SLAB + 1024;
+constexpr int PAIR_SP_COL = 256, PAIR_SQ_COL = PAIR_SP_COL + 16;   // scales, two sets of each
+
+__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void tma2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];"
+        :
+        : "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        :
+        : "r"(bar), "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_ld32_nowait(uint32_t addr, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+}
+
+// 32 bytes to a 32-byte boundary: whole sectors from one lane
+__device__ __forceinline__ void st32(void *p, const uint32_t r[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :
+                 : "l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+struct PairArgs {
+    void *out;
+    int64_t ldo;
+    int32_t m, n;
+    int32_t k_tiles, p_tiles, tiles;
+    int32_t dtype;
+    int32_t vec32;            // rows of out are 32-byte aligned
+};
+
+__global__ void __launch_bounds__(PAIR_THREADS)
+mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+                       const __grid_constant__ CUtensorMap map_sp, const __grid_constant__ CUtensorMap map_sq, PairArgs a) {
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[2 * PAIR_STAGES + 2];
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile int failed;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8 * s; };
+    auto empty = [&](int s) { return bar0 + 8 * (PAIR_STAGES + s); };
+    const uint32_t acc_full = bar0 + 16 * PAIR_STAGES, acc_empty = acc_full + 8;
+    const int rank = (int)(blockIdx.x & 1);
+    const int first = (int)(blockIdx.x >> 1), stride = (int)(gridDim.x >> 1);
+    if (threadIdx.x == 0) {
+        failed = 0;
+        for (int i = 0; i < 2 * PAIR_STAGES + 1; ++i)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" : : "r"(bar0 + 8 * i) : "memory");
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 16;" : : "r"(acc_empty) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" : : : "memory");
+        asm volatile("fence.proxy.async.shared::cta;" : : : "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" : : "r"(smem_u32(&tmem_base)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" : : : "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" : : : "memory");
+    asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
+    const uint32_t tmem = tmem_base;
+
+    int issued = 0;
+    if (warp == 8 && lane == 0) {
+        // loads of this CTA: its half of the rows of A and of B, the scales
+        // of its rows of A, and all the tile's scales of B
+        bool ok = true;
+        for (int t = first; t < a.tiles && ok; t += stride) {
+            const int pt = t % a.p_tiles, qt = t / a.p_tiles;
+            for (int k = 0; k < a.k_tiles; ++k, ++issued) {
+                const int s = issued % PAIR_STAGES;
+                if (issued >= PAIR_STAGES && !mbar_wait(empty(s), (uint32_t)((issued / PAIR_STAGES - 1) & 1), MM_WAIT_NS)) {
+                    failed = 1;
+                    ok = false;
+                    break;
+                }
+                const uint32_t p = base + s * PAIR_STAGE, q = p + PAIR_P, sp = q + PAIR_Q, sq = sp + PAIR_SP;
+                const uint32_t bar = map_to(full(s), 0);       // the leader multiplies for both
+                if (rank == 0)
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(2 * PAIR_STAGE) : "memory");
+                tma2d_pair(p, &map_p, k * MM_KB, pt * PAIR_ROWS + rank * 128, bar);
+                tma2d_pair(q, &map_q, k * MM_KB, qt * PAIR_COLS + rank * 128, bar);
+                tma2d_pair(sp, &map_sp, k * (PAIR_SP / 4), pt * 2 + rank, bar);
+                tma2d_pair(sq, &map_sq, k * (PAIR_SP / 4), qt * 2, bar);
+            }
+        }
+    } else if (warp == 9 && lane == 0 && rank == 0) {
+        const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(PAIR_COLS / 8) << 17) | (1u << 23) | (16u << 24);
+        int i = 0, n = 0;
+        bool ok = true;
+        for (int t = first; t < a.tiles && ok; t += stride, ++n) {
+            if (n > 0 && !mbar_wait(acc_empty, (uint32_t)((n - 1) & 1), MM_WAIT_NS)) {
+                failed = 1;
+                break;
+            }
+            asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
+            for (int k = 0; k < a.k_tiles; ++k, ++i) {
+                const int s = i % PAIR_STAGES;
+                if (!mbar_wait(full(s), (uint32_t)((i / PAIR_STAGES) & 1), MM_WAIT_NS)) {
+                    failed = 1;
+                    ok = false;
+                    break;
+                }
+                asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
+                const uint32_t p = base + s * PAIR_STAGE, q = p + PAIR_P, sp = q + PAIR_Q, sq = sp + PAIR_SP;
+                const uint32_t tp = tmem + PAIR_SP_COL + 8 * (i & 1), tq = tmem + PAIR_SQ_COL + 16 * (i & 1);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;"
+                                 : : "r"(tp + 4 * j), "l"(mm_desc(sp + j * MX4_ATOM, 128, 0)) : "memory");
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;"
+                                     : : "r"(tq + 4 * (2 * j + h)), "l"(mm_desc(sq + h * PAIR_SP + j * MX4_ATOM, 128, 0)) : "memory");
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t id = (uint32_t)(2 * (j & 1));
+                    const uint32_t d = idesc | (id << 4) | (id << 29);
+                    asm volatile(
+                        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+                        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                        :
+                        : "r"(tmem), "l"(mm_desc(p + 32 * j, 1024, 2)), "l"(mm_desc(q + 32 * j, 1024, 2)), "r"(d),
+                          "r"(tp + 4 * (j >> 1)), "r"(tq + 8 * (j >> 1)), "r"((uint32_t)(k > 0 || j > 0))
+                        : "memory");
+                }
+                tc_commit_pair(empty(s));
+            }
+            tc_commit_pair(acc_full);
+        }
+    } else if (warp < 8) {
+        const uint32_t slab = base + PAIR_STAGES * PAIR_STAGE + warp * PAIR_SLAB;
+        const uint32_t release = map_to(acc_empty, 0);
+        const int sub = warp & 3, c0 = 128 * (warp >> 2);
+        int n = 0;
+        for (int t = first; t < a.tiles; t += stride, ++n) {
+            const int pt = t % a.p_tiles, qt = t / a.p_tiles;
+            if (!mbar_wait(acc_full, (uint32_t)(n & 1), 2 * MM_WAIT_NS + 4000ull * (uint64_t)a.k_tiles)) failed = 1;
+            __syncwarp();
+            if (failed) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
+            uint32_t v[128];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tc_ld32_nowait(tmem + ((uint32_t)sub << 21) + c0 + 32 * j, v + 32 * j);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" : : : "memory");
+            asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
+            __syncwarp();
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" : : "r"(release) : "memory");
+            const int row0 = pt * PAIR_ROWS + rank * 128 + 32 * sub, col0 = qt * PAIR_COLS + c0;
+            if (a.vec32 && col0 + 128 <= a.n) {
+                if (row0 + lane < a.m) {
+                    const int64_t at = (int64_t)(row0 + lane) * a.ldo + col0;
+                    if (a.dtype == ZS_DTYPE_FP32) {
+                        float *o = static_cast<float *>(a.out) + at;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) st32(o + 8 * j, v + 8 * j);
+                    } else {
+                        uint16_t *o = static_cast<uint16_t *>(a.out) + at;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            uint32_t r[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                r[i] = mm_cast(__uint_as_float(v[16 * j + 2 * i]), a.dtype) |
+                                       (mm_cast(__uint_as_float(v[16 * j + 2 * i + 1]), a.dtype) << 16);
+                            st32(o + 16 * j, r);
+                        }
+                    }
+                }
+                continue;
+            }
+            // any alignment, ragged edges: 32 x 32 blocks through shared
+            // memory, so that lanes store neighbouring elements of a row
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    asm volatile("st.shared.b32 [%0], %1;" : : "r"(slab + 4 * (lane * 33 + i)), "r"(v[32 * j + i]) : "memory");
+                __syncwarp();
+                const int col = col0 + 32 * j + lane;
+                for (int i = 0; i < 32 && row0 + i < a.m; ++i) {
+                    float x;
+                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(slab + 4 * (i * 33 + lane)) : "memory");
+                    if (col < a.n) {
+                        const int64_t at = (int64_t)(row0 + i) * a.ldo + col;
+                        if (a.dtype == ZS_DTYPE_FP32) static_cast<float *>(a.out)[at] = x;
+                        else static_cast<uint16_t *>(a.out)[at] = (uint16_t)mm_cast(x, a.dtype);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+    __syncwarp();
+    if (warp == 8 && lane == 0 && failed) {
+        if (rank == 0)   // the leader's barriers count the loads of both CTAs
+            for (int i = issued > PAIR_STAGES ? issued - PAIR_STAGES : 0; i < issued; ++i)
+                mbar_wait(full(i % PAIR_STAGES), (uint32_t)((i / PAIR_STAGES) & 1), MM_WAIT_NS);
+        atomicAdd(&g_mx4_wait_timeouts, 1);
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
+    __syncthreads();
+    // neither CTA leaves while the other may still write to its barriers
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" : : : "memory");
+    if (warp == 0) {
+        asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" : : "r"(tmem));
+    }
+}
+
 // out = 0, for a product over no elements
 __global__ void mx4_zero_kernel(void *out, int64_t m, int64_t n, int64_t ldo, int fp32) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < m * n; i += (int64_t)gridDim.x * 256) {
@@ -342,10 +594,67 @@ static bool code_map(CUtensorMap *m, const void *codes, int64_t rows, int64_t ro
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale atoms as 32-bit words [row tiles][atoms * 128]: boxes of two atoms
+// (256 elements of k) by `box` row tiles; zero outside.
+static bool scale_map(CUtensorMap *m, const void *scales, int64_t rows, int64_t cols, int box) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    const cuuint64_t words = (cuuint64_t)mx4_atoms(cols) * (MX4_ATOM / 4);
+    const cuuint64_t dims[2] = {words, (cuuint64_t)mx4_row_tiles(rows)}, strides[1] = {4 * words};
+    const cuuint32_t boxes[2] = {2 * MX4_ATOM / 4, (cuuint32_t)box}, ones[2] = {1, 1};
+    return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(scales), dims, strides, boxes, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The device's SM count, once its kernel attributes are set (`set`, the same
+// from every host thread).
+static cudaError_t device_sms(std::atomic<int> (&known)[64], cudaError_t (*set)(), int *sms) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    *sms = known[dev].load(std::memory_order_relaxed);
+    if (*sms > 0) return cudaSuccess;
+    if ((e = set()) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    known[dev].store(*sms, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+static cudaError_t pair_attributes() {
+    return cudaFuncSetAttribute(mx4_matmul_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM);
+}
+
+static cudaError_t pair_launch(const CUtensorMap (&map)[4], const PairArgs &a, cudaStream_t s) {
+    static std::atomic<int> known[64];
+    int sms = 0;
+    cudaError_t e = device_sms(known, pair_attributes, &sms);
+    if (e != cudaSuccess) return e;
+    const int pairs = a.tiles < sms / 2 ? a.tiles : sms / 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(PAIR_THREADS);
+    cfg.dynamicSmemBytes = PAIR_SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, mx4_matmul_pair_kernel, map[0], map[1], map[2], map[3], a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <int BN, bool FLIP>
 static cudaError_t mm_launch(const CUtensorMap &p, const CUtensorMap &q, const MmArgs &a, cudaStream_t s) {
     using S = MmShape<BN>;
-    cudaError_t e = cudaFuncSetAttribute(mx4_matmul_kernel<BN, FLIP>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    static std::atomic<int> known[64];
+    int sms = 0;
+    cudaError_t e = device_sms(known, [] {
+        return cudaFuncSetAttribute(mx4_matmul_kernel<BN, FLIP>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    }, &sms);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)a.p_tiles * a.q_tiles * a.split));
@@ -402,12 +711,33 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const zs_mx4
     for (const void *p : four)
         if (!p || (reinterpret_cast<uintptr_t>(p) & 15))
             return zs_fail(ZS_EINVAL, "%s: codes or scales NULL or not 16-byte aligned", fn);
+    cudaError_t e;
+    const int64_t pair_p = (m + zsk::PAIR_ROWS - 1) / zsk::PAIR_ROWS, pair_q = (n + zsk::PAIR_COLS - 1) / zsk::PAIR_COLS;
+    if (m > 128 && pair_p * pair_q >= 38 && pair_p * pair_q < 0x7FFFFFFF) {
+        CUtensorMap map[4];
+        if (!zsk::code_map(&map[0], A->codes, m, mx4_row_bytes(k), 128) || !zsk::code_map(&map[1], B->codes, n, mx4_row_bytes(k), 128) ||
+            !zsk::scale_map(&map[2], A->scales, m, k, 1) || !zsk::scale_map(&map[3], B->scales, n, k, 2))
+            return zs_fail(ZS_ECUDA, "%s: cuTensorMapEncodeTiled failed", fn);
+        zsk::PairArgs a;
+        a.out = out;
+        a.ldo = ldo;
+        a.m = (int32_t)m;
+        a.n = (int32_t)n;
+        a.k_tiles = (int32_t)((k + 255) / 256);
+        a.p_tiles = (int32_t)pair_p;
+        a.tiles = (int32_t)(pair_p * pair_q);
+        a.dtype = dtype;
+        a.vec32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && ldo * size % 32 == 0;
+        e = zsk::pair_launch(map, a, s);
+        if (e != cudaSuccess) return zs_fail(ZS_ECUDA, "%s: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
+        zs_clear_error();
+        return ZS_OK;
+    }
     const bool flip = m <= 128;
     const int64_t np = flip ? n : m, nq = flip ? m : n;
     const zs_mx4 *P = flip ? B : A, *Q = flip ? A : B;
     int bn = 128;
     if (flip) bn = nq <= 16 ? 16 : nq <= 32 ? 32 : nq <= 64 ? 64 : 128;
-    else if (((np + 127) / 128) * ((nq + 255) / 256) >= 152) bn = 256;
     zsk::MmArgs a;
     a.p_scales = static_cast<const uint8_t *>(P->scales);
     a.q_scales = static_cast<const uint8_t *>(Q->scales);
@@ -431,12 +761,11 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const zs_mx4
         !zsk::code_map(&mq, Q->codes, nq, mx4_row_bytes(k), bn))
         return zs_fail(ZS_ECUDA, "%s: cuTensorMapEncodeTiled failed", fn);
     using namespace zsk;
-    cudaError_t e;
     if (flip)
         e = bn == 16 ? mm_launch<16, true>(mp, mq, a, s) : bn == 32 ? mm_launch<32, true>(mp, mq, a, s)
           : bn == 64 ? mm_launch<64, true>(mp, mq, a, s) : mm_launch<128, true>(mp, mq, a, s);
     else
-        e = bn == 256 ? mm_launch<256, false>(mp, mq, a, s) : mm_launch<128, false>(mp, mq, a, s);
+        e = mm_launch<128, false>(mp, mq, a, s);
     if (e != cudaSuccess) return zs_fail(ZS_ECUDA, "%s: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
     zs_clear_error();
     return ZS_OK;
