@@ -51,6 +51,46 @@ struct MmArgs {
     int32_t vec;              // 16-byte stores of whole runs
 };
 
+// mbar_wait without its look at the clock (a slow read) unless the barrier
+// stays closed for a while: these waits stand between the products.
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 <= limit_ns)
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try(bar, parity)) return true;
+    return false;
+}
+
+// One wait of a whole warp: the same answer in all lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xFFFFFFFFu, mm_wait(bar, parity, limit_ns));
+}
+
+// True in one lane of a converged warp.  The warps that issue loads and
+// products run their loops with all lanes and elect one for the issue: under
+// `if (lane == 0)` around the whole loop the compiler cannot know that the
+// operands are uniform and serialises each instruction, which took 858
+// cycles for a stage of products that elected take 512, the tensor cores' own
+// rate (2 x 128 x 256 x 256, operands already in shared memory).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 __device__ __forceinline__ uint64_t mm_desc(uint32_t addr, uint32_t sbo, uint64_t layout) {
     // shared-memory operand: start address, leading and stride byte offsets
     // (16-byte units), version 1, swizzle
@@ -136,7 +176,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     __shared__ __align__(8) uint64_t bars[2 * S::STAGES + 1];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int failed;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t bar0 = smem_u32(bars), done = bar0 + 16 * S::STAGES;
     auto full = [&](int s) { return bar0 + 8 * s; };
@@ -164,73 +204,78 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
     const uint32_t tmem = tmem_base;
 
-    int issued = 0;                        // stages that the loads of warp 4 were issued for
-    if (warp == 4 && lane == 0) {
+    int issued = 0;                        // stages that warp 4 issued loads for
+    if (warp == 4) {
         const uint8_t *sp = a.p_scales + ((int64_t)pt * a.atoms) * MX4_ATOM;
         for (int k = k0; k < k1; ++k) {
             const int i = k - k0, s = i % S::STAGES;
-            if (i >= S::STAGES && !mbar_wait(empty(s), (uint32_t)((i / S::STAGES - 1) & 1), MM_WAIT_NS)) {
+            if (i >= S::STAGES && !warp_wait(empty(s), (uint32_t)((i / S::STAGES - 1) & 1), MM_WAIT_NS)) {
                 failed = 1;
                 break;
             }
             const uint32_t p = base + s * S::STAGE, q = p + S::P_BYTES, scp = q + S::Q_BYTES, scq = scp + S::SP_BYTES;
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(S::STAGE) : "memory");
-            tma2d(p, &map_p, k * MM_KB, pt * MM_P, full(s));
-            tma2d(q, &map_q, k * MM_KB, qt * BN, full(s));
-            bulk(scp, sp + (int64_t)k * S::SP_BYTES, S::SP_BYTES, full(s));
+            if (elect_one()) {
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(S::STAGE) : "memory");
+                tma2d(p, &map_p, k * MM_KB, pt * MM_P, full(s));
+                tma2d(q, &map_q, k * MM_KB, qt * BN, full(s));
+                bulk(scp, sp + (int64_t)k * S::SP_BYTES, S::SP_BYTES, full(s));
 #pragma unroll
-            for (int j = 0; j < S::QA; ++j) {
-                // a row tile past the matrix's last scales no stored column
-                const int rt = min((int)((int64_t)qt * BN / 128) + j, (a.nq - 1) / 128);
-                bulk(scq + j * S::SP_BYTES, a.q_scales + ((int64_t)rt * a.atoms + 2 * k) * MX4_ATOM, S::SP_BYTES, full(s));
+                for (int j = 0; j < S::QA; ++j) {
+                    // a row tile past the matrix's last scales no stored column
+                    const int rt = min((int)((int64_t)qt * BN / 128) + j, (a.nq - 1) / 128);
+                    bulk(scq + j * S::SP_BYTES, a.q_scales + ((int64_t)rt * a.atoms + 2 * k) * MX4_ATOM, S::SP_BYTES, full(s));
+                }
             }
+            __syncwarp();
             issued = i + 1;
         }
-    } else if (warp == 5 && lane == 0) {
+    } else if (warp == 5) {
         // kind::mxf4: e2m1 x e2m1, ue8m0 scales, M = 128, N = BN
         const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(BN / 8) << 17) | (1u << 23) | (8u << 24);
         for (int k = k0; k < k1; ++k) {
             const int i = k - k0, s = i % S::STAGES;
-            if (!mbar_wait(full(s), (uint32_t)((i / S::STAGES) & 1), MM_WAIT_NS)) {
+            if (!warp_wait(full(s), (uint32_t)((i / S::STAGES) & 1), MM_WAIT_NS)) {
                 failed = 1;
                 break;
             }
             asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
             const uint32_t p = base + s * S::STAGE, q = p + S::P_BYTES, scp = q + S::Q_BYTES, scq = scp + S::SP_BYTES;
             const uint32_t tp = tmem + S::SP_COL + 8 * (i & 1), tq = tmem + S::SQ_COL + 8 * S::QA * (i & 1);
+            if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
-                             :
-                             : "r"(tp + 4 * j), "l"(mm_desc(scp + j * MX4_ATOM, 128, 0))
-                             : "memory");
-#pragma unroll
-                for (int h = 0; h < S::QA; ++h)
+                for (int j = 0; j < 2; ++j) {
                     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
                                  :
-                                 : "r"(tq + 4 * (S::QA * j + h)), "l"(mm_desc(scq + h * S::SP_BYTES + j * MX4_ATOM, 128, 0))
+                                 : "r"(tp + 4 * j), "l"(mm_desc(scp + j * MX4_ATOM, 128, 0))
                                  : "memory");
-            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t id = (uint32_t)(2 * (j & 1));        // scale bytes 0-1 or 2-3 of an atom
-                const uint32_t d = idesc | (id << 4) | (id << 29);
-                asm volatile(
-                    "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-                    "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-                    :
-                    : "r"(tmem), "l"(mm_desc(p + 32 * j, 1024, 2)), "l"(mm_desc(q + 32 * j, 1024, 2)), "r"(d),
-                      "r"(tp + 4 * (j >> 1)), "r"(tq + 4 * S::QA * (j >> 1)), "r"((uint32_t)(i > 0 || j > 0))
-                    : "memory");
+                    for (int h = 0; h < S::QA; ++h)
+                        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
+                                     :
+                                     : "r"(tq + 4 * (S::QA * j + h)), "l"(mm_desc(scq + h * S::SP_BYTES + j * MX4_ATOM, 128, 0))
+                                     : "memory");
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t id = (uint32_t)(2 * (j & 1));        // scale bytes 0-1 or 2-3 of an atom
+                    const uint32_t d = idesc | (id << 4) | (id << 29);
+                    asm volatile(
+                        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+                        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                        :
+                        : "r"(tmem), "l"(mm_desc(p + 32 * j, 1024, 2)), "l"(mm_desc(q + 32 * j, 1024, 2)), "r"(d),
+                          "r"(tp + 4 * (j >> 1)), "r"(tq + 4 * S::QA * (j >> 1)), "r"((uint32_t)(i > 0 || j > 0))
+                        : "memory");
+                }
+                tc_commit(empty(s));
             }
-            tc_commit(empty(s));
+            __syncwarp();
         }
-        tc_commit(done);
+        if (elect_one()) tc_commit(done);
+        __syncwarp();
     }
     // everyone waits until the products of this CTA are in tensor memory
-    // (the idle lanes of the two issuing warps only once their lane is through)
-    __syncwarp();
-    if (!mbar_wait(done, 0, 4 * MM_WAIT_NS + 4000ull * (uint64_t)(k1 - k0))) failed = 1;
+    if (!mm_wait(done, 0, 4 * MM_WAIT_NS + 4000ull * (uint64_t)(k1 - k0))) failed = 1;
     __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
     const int p0 = pt * MM_P, q0 = qt * BN;
@@ -293,7 +338,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     if (warp == 4 && lane == 0 && failed) {
         // let the loads already issued land before the shared memory goes away
         for (int i = issued > S::STAGES ? issued - S::STAGES : 0; i < issued; ++i)
-            mbar_wait(full(i % S::STAGES), (uint32_t)((i / S::STAGES) & 1), MM_WAIT_NS);
+            mm_wait(full(i % S::STAGES), (uint32_t)((i / S::STAGES) & 1), MM_WAIT_NS);
         atomicAdd(&g_mx4_wait_timeouts, 1);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
@@ -380,7 +425,7 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
     __shared__ __align__(8) uint64_t bars[2 * PAIR_STAGES + 2];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int failed;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8 * s; };
@@ -407,7 +452,7 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
     const uint32_t tmem = tmem_base;
 
     int issued = 0;
-    if (warp == 8 && lane == 0) {
+    if (warp == 8) {
         // loads of this CTA: its half of the rows of A and of B, the scales
         // of its rows of A, and all the tile's scales of B
         bool ok = true;
@@ -415,34 +460,37 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
             const int pt = t % a.p_tiles, qt = t / a.p_tiles;
             for (int k = 0; k < a.k_tiles; ++k, ++issued) {
                 const int s = issued % PAIR_STAGES;
-                if (issued >= PAIR_STAGES && !mbar_wait(empty(s), (uint32_t)((issued / PAIR_STAGES - 1) & 1), MM_WAIT_NS)) {
+                if (issued >= PAIR_STAGES && !warp_wait(empty(s), (uint32_t)((issued / PAIR_STAGES - 1) & 1), MM_WAIT_NS)) {
                     failed = 1;
                     ok = false;
                     break;
                 }
                 const uint32_t p = base + s * PAIR_STAGE, q = p + PAIR_P, sp = q + PAIR_Q, sq = sp + PAIR_SP;
-                const uint32_t bar = map_to(full(s), 0);       // the leader multiplies for both
-                if (rank == 0)
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(2 * PAIR_STAGE) : "memory");
-                tma2d_pair(p, &map_p, k * MM_KB, pt * PAIR_ROWS + rank * 128, bar);
-                tma2d_pair(q, &map_q, k * MM_KB, qt * PAIR_COLS + rank * 128, bar);
-                tma2d_pair(sp, &map_sp, k * (PAIR_SP / 4), pt * 2 + rank, bar);
-                tma2d_pair(sq, &map_sq, k * (PAIR_SP / 4), qt * 2, bar);
+                if (elect_one()) {
+                    const uint32_t bar = map_to(full(s), 0);       // the leader multiplies for both
+                    if (rank == 0)
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(2 * PAIR_STAGE) : "memory");
+                    tma2d_pair(p, &map_p, k * MM_KB, pt * PAIR_ROWS + rank * 128, bar);
+                    tma2d_pair(q, &map_q, k * MM_KB, qt * PAIR_COLS + rank * 128, bar);
+                    tma2d_pair(sp, &map_sp, k * (PAIR_SP / 4), pt * 2 + rank, bar);
+                    tma2d_pair(sq, &map_sq, k * (PAIR_SP / 4), qt * 2, bar);
+                }
+                __syncwarp();
             }
         }
-    } else if (warp == 9 && lane == 0 && rank == 0) {
+    } else if (warp == 9 && rank == 0) {
         const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(PAIR_COLS / 8) << 17) | (1u << 23) | (16u << 24);
         int i = 0, n = 0;
         bool ok = true;
         for (int t = first; t < a.tiles && ok; t += stride, ++n) {
-            if (n > 0 && !mbar_wait(acc_empty, (uint32_t)((n - 1) & 1), MM_WAIT_NS)) {
+            if (n > 0 && !warp_wait(acc_empty, (uint32_t)((n - 1) & 1), MM_WAIT_NS)) {
                 failed = 1;
                 break;
             }
             asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
             for (int k = 0; k < a.k_tiles; ++k, ++i) {
                 const int s = i % PAIR_STAGES;
-                if (!mbar_wait(full(s), (uint32_t)((i / PAIR_STAGES) & 1), MM_WAIT_NS)) {
+                if (!warp_wait(full(s), (uint32_t)((i / PAIR_STAGES) & 1), MM_WAIT_NS)) {
                     failed = 1;
                     ok = false;
                     break;
@@ -450,30 +498,34 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
                 asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
                 const uint32_t p = base + s * PAIR_STAGE, q = p + PAIR_P, sp = q + PAIR_Q, sq = sp + PAIR_SP;
                 const uint32_t tp = tmem + PAIR_SP_COL + 8 * (i & 1), tq = tmem + PAIR_SQ_COL + 16 * (i & 1);
+                if (elect_one()) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;"
-                                 : : "r"(tp + 4 * j), "l"(mm_desc(sp + j * MX4_ATOM, 128, 0)) : "memory");
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int j = 0; j < 2; ++j) {
                         asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;"
-                                     : : "r"(tq + 4 * (2 * j + h)), "l"(mm_desc(sq + h * PAIR_SP + j * MX4_ATOM, 128, 0)) : "memory");
-                }
+                                     : : "r"(tp + 4 * j), "l"(mm_desc(sp + j * MX4_ATOM, 128, 0)) : "memory");
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t id = (uint32_t)(2 * (j & 1));
-                    const uint32_t d = idesc | (id << 4) | (id << 29);
-                    asm volatile(
-                        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-                        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-                        :
-                        : "r"(tmem), "l"(mm_desc(p + 32 * j, 1024, 2)), "l"(mm_desc(q + 32 * j, 1024, 2)), "r"(d),
-                          "r"(tp + 4 * (j >> 1)), "r"(tq + 8 * (j >> 1)), "r"((uint32_t)(k > 0 || j > 0))
-                        : "memory");
+                        for (int h = 0; h < 2; ++h)
+                            asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;"
+                                         : : "r"(tq + 4 * (2 * j + h)), "l"(mm_desc(sq + h * PAIR_SP + j * MX4_ATOM, 128, 0)) : "memory");
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t id = (uint32_t)(2 * (j & 1));
+                        const uint32_t d = idesc | (id << 4) | (id << 29);
+                        asm volatile(
+                            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+                            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                            :
+                            : "r"(tmem), "l"(mm_desc(p + 32 * j, 1024, 2)), "l"(mm_desc(q + 32 * j, 1024, 2)), "r"(d),
+                              "r"(tp + 4 * (j >> 1)), "r"(tq + 8 * (j >> 1)), "r"((uint32_t)(k > 0 || j > 0))
+                            : "memory");
+                    }
+                    tc_commit_pair(empty(s));
                 }
-                tc_commit_pair(empty(s));
+                __syncwarp();
             }
-            tc_commit_pair(acc_full);
+            if (elect_one()) tc_commit_pair(acc_full);
+            __syncwarp();
         }
     } else if (warp < 8) {
         const uint32_t slab = base + PAIR_STAGES * PAIR_STAGE + warp * PAIR_SLAB;
@@ -482,9 +534,11 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
         int n = 0;
         for (int t = first; t < a.tiles; t += stride, ++n) {
             const int pt = t % a.p_tiles, qt = t / a.p_tiles;
-            if (!mbar_wait(acc_full, (uint32_t)(n & 1), 2 * MM_WAIT_NS + 4000ull * (uint64_t)a.k_tiles)) failed = 1;
-            __syncwarp();
-            if (failed) break;
+            if (!warp_wait(acc_full, (uint32_t)(n & 1), 2 * MM_WAIT_NS + 4000ull * (uint64_t)a.k_tiles) ||
+                __any_sync(0xFFFFFFFFu, failed)) {
+                failed = 1;
+                break;
+            }
             asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
             uint32_t v[128];
 #pragma unroll
@@ -543,7 +597,7 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
     if (warp == 8 && lane == 0 && failed) {
         if (rank == 0)   // the leader's barriers count the loads of both CTAs
             for (int i = issued > PAIR_STAGES ? issued - PAIR_STAGES : 0; i < issued; ++i)
-                mbar_wait(full(i % PAIR_STAGES), (uint32_t)((i / PAIR_STAGES) & 1), MM_WAIT_NS);
+                mm_wait(full(i % PAIR_STAGES), (uint32_t)((i / PAIR_STAGES) & 1), MM_WAIT_NS);
         atomicAdd(&g_mx4_wait_timeouts, 1);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
