@@ -362,7 +362,7 @@ constexpr int PAIR_THREADS = 320;         // 8 warps store, 1 loads, 1 multiplie
 constexpr int PAIR_P = 128 * MM_KB, PAIR_Q = 128 * MM_KB;
 constexpr int PAIR_SP = 2 * MX4_ATOM, PAIR_SQ = 4 * MX4_ATOM;
 constexpr int PAIR_STAGE = PAIR_P + PAIR_Q + PAIR_SP + PAIR_SQ;
-constexpr int PAIR_SLAB = 32 * 33 * 4;    // a storing warp's transposition buffer
+constexpr int PAIR_SLAB = 32 * 128;       // a storing warp's buffer: 32 rows of 128 bytes
 constexpr int PAIR_SMEM = PAIR_STAGES * PAIR_STAGE + 8 * PAIR_SLAB + 1024;
 constexpr int PAIR_SP_COL = 256, PAIR_SQ_COL = PAIR_SP_COL + 16;   // scales, two sets of each
 
@@ -401,21 +401,13 @@ __device__ __forceinline__ void tc_ld32_nowait(uint32_t addr, uint32_t *v) {
         : "r"(addr));
 }
 
-// 32 bytes to a 32-byte boundary: whole sectors from one lane
-__device__ __forceinline__ void st32(void *p, const uint32_t r[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 :
-                 : "l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
 struct PairArgs {
     void *out;
     int64_t ldo;
     int32_t m, n;
     int32_t k_tiles, p_tiles, tiles;
     int32_t dtype;
-    int32_t vec32;            // rows of out are 32-byte aligned
+    int32_t vec;              // rows of out are 16-byte aligned
 };
 
 __global__ void __launch_bounds__(PAIR_THREADS)
@@ -547,46 +539,61 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
             asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
             __syncwarp();
             if (lane == 0)
-                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" : : "r"(release) : "memory");
+                asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" : : "r"(release) : "memory");
             const int row0 = pt * PAIR_ROWS + rank * 128 + 32 * sub, col0 = qt * PAIR_COLS + c0;
-            if (a.vec32 && col0 + 128 <= a.n) {
-                if (row0 + lane < a.m) {
-                    const int64_t at = (int64_t)(row0 + lane) * a.ldo + col0;
-                    if (a.dtype == ZS_DTYPE_FP32) {
-                        float *o = static_cast<float *>(a.out) + at;
+            const bool fp32 = a.dtype == ZS_DTYPE_FP32;
+            if (!fp32) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) st32(o + 8 * j, v + 8 * j);
-                    } else {
-                        uint16_t *o = static_cast<uint16_t *>(a.out) + at;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            uint32_t r[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                r[i] = mm_cast(__uint_as_float(v[16 * j + 2 * i]), a.dtype) |
-                                       (mm_cast(__uint_as_float(v[16 * j + 2 * i + 1]), a.dtype) << 16);
-                            st32(o + 16 * j, r);
-                        }
-                    }
-                }
-                continue;
+                for (int i = 0; i < 64; ++i)
+                    v[i] = mm_cast(__uint_as_float(v[2 * i]), a.dtype) | (mm_cast(__uint_as_float(v[2 * i + 1]), a.dtype) << 16);
             }
-            // any alignment, ragged edges: 32 x 32 blocks through shared
-            // memory, so that lanes store neighbouring elements of a row
+            // 32 rows of 128 bytes at a time through this warp's slab, in
+            // 16-byte pieces whose place within a row is turned by the row
+            // (no bank conflicts); then lanes store neighbouring elements
+            const int pieces = fp32 ? 4 : 2, width = fp32 ? 32 : 64;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
+                if (j >= pieces) break;
+                const int col = col0 + j * width;
+                if (row0 >= a.m || col >= a.n) break;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    asm volatile("st.shared.b32 [%0], %1;" : : "r"(slab + 4 * (lane * 33 + i)), "r"(v[32 * j + i]) : "memory");
+                for (int c = 0; c < 8; ++c)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                 :
+                                 : "r"(slab + 128 * lane + 16 * (c ^ (lane & 7))), "r"(v[32 * j + 4 * c]), "r"(v[32 * j + 4 * c + 1]),
+                                   "r"(v[32 * j + 4 * c + 2]), "r"(v[32 * j + 4 * c + 3])
+                                 : "memory");
                 __syncwarp();
-                const int col = col0 + 32 * j + lane;
+                if (a.vec && col + width <= a.n) {
+                    // 4 whole lines a store
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = 4 * i + (lane >> 3);
+                        uint32_t x[4];
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                     : "r"(slab + 128 * row + 16 * ((lane & 7) ^ (row & 7)))
+                                     : "memory");
+                        if (row0 + row < a.m)
+                            *reinterpret_cast<uint4 *>(static_cast<char *>(a.out) + ((int64_t)(row0 + row) * a.ldo + col) * (fp32 ? 4 : 2) + 16 * (lane & 7)) =
+                                make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                    __syncwarp();
+                    continue;
+                }
                 for (int i = 0; i < 32 && row0 + i < a.m; ++i) {
-                    float x;
-                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(slab + 4 * (i * 33 + lane)) : "memory");
-                    if (col < a.n) {
-                        const int64_t at = (int64_t)(row0 + i) * a.ldo + col;
-                        if (a.dtype == ZS_DTYPE_FP32) static_cast<float *>(a.out)[at] = x;
-                        else static_cast<uint16_t *>(a.out)[at] = (uint16_t)mm_cast(x, a.dtype);
+                    const int64_t at = (int64_t)(row0 + i) * a.ldo + col;
+                    uint32_t x;
+                    if (fp32) {
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(slab + 128 * i + ((4 * lane) ^ (16 * (i & 7)))) : "memory");
+                        if (col + lane < a.n) static_cast<float *>(a.out)[at + lane] = __uint_as_float(x);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int e = 32 * h + lane;
+                            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(slab + 128 * i + ((2 * e) ^ (16 * (i & 7)))) : "memory");
+                            if (col + e < a.n) static_cast<uint16_t *>(a.out)[at + e] = (uint16_t)x;
+                        }
                     }
                 }
                 __syncwarp();
@@ -781,7 +788,7 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const zs_mx4
         a.p_tiles = (int32_t)pair_p;
         a.tiles = (int32_t)(pair_p * pair_q);
         a.dtype = dtype;
-        a.vec32 = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && ldo * size % 32 == 0;
+        a.vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ldo * size % 16 == 0;
         e = zsk::pair_launch(map, a, s);
         if (e != cudaSuccess) return zs_fail(ZS_ECUDA, "%s: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
         zs_clear_error();
