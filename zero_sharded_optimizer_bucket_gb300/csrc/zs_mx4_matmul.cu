@@ -34,7 +34,7 @@ struct MmShape {
     static constexpr int SP_COL = BN < 32 ? 32 : BN, SQ_COL = SP_COL + 16;
     static constexpr int USED = SQ_COL + 16 * QA;
     static constexpr int COLS = USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
-    static constexpr int RED = BN * MM_P * 4;                  // partial sums of a split
+    static constexpr int RED = BN * MM_P * 4 + 16 * (BN > MM_P ? BN : MM_P);   // the tile, rows 16 bytes apart
     static constexpr int BODY = STAGES * STAGE > RED ? STAGES * STAGE : RED;
     static constexpr int SMEM = BODY + 1024;                   // and room to align
 };
@@ -48,7 +48,7 @@ struct MmArgs {
     int32_t p_tiles, q_tiles;
     int32_t split;            // CTAs of the cluster that share the tile's k
     int32_t dtype;
-    int32_t vec;              // 16-byte stores of whole runs
+    int32_t vec;              // rows of out are aligned to 4 elements
 };
 
 // mbar_wait without its look at the clock (a slow read) unless the barrier
@@ -98,6 +98,12 @@ __device__ __forceinline__ uint64_t mm_desc(uint32_t addr, uint32_t sbo, uint64_
            ((uint64_t)1 << 46) | (layout << 61);
 }
 
+__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
 __device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
@@ -134,38 +140,6 @@ __device__ __forceinline__ uint32_t mm_cast(float x, int dtype) {
     return dtype == ZS_DTYPE_FP16 ? FP16T::from_f32(x) : BF16T::from_f32(x);
 }
 
-// 32 neighbouring results of one row of out, the first n of them inside
-__device__ __forceinline__ void store_run(const MmArgs &a, int64_t at, const float (&f)[32], int n) {
-    if (a.dtype == ZS_DTYPE_FP32) {
-        float *o = static_cast<float *>(a.out) + at;
-        if (a.vec && n >= 32) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                reinterpret_cast<float4 *>(o)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) if (i < n) o[i] = f[i];
-        }
-        return;
-    }
-    uint16_t *o = static_cast<uint16_t *>(a.out) + at;
-    uint32_t r[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) r[i] = mm_cast(f[i], a.dtype);
-    if (a.vec && n >= 32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) reinterpret_cast<uint4 *>(o)[i] = pack8(r + 8 * i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) if (i < n) o[i] = (uint16_t)r[i];
-    }
-}
-
-__device__ __forceinline__ void store_one(const MmArgs &a, int64_t at, float f) {
-    if (a.dtype == ZS_DTYPE_FP32) static_cast<float *>(a.out)[at] = f;
-    else static_cast<uint16_t *>(a.out)[at] = (uint16_t)mm_cast(f, a.dtype);
-}
-
 // FLIP: P are the rows of B (features) and Q those of A (tokens), for few
 // tokens: out[q][p].  Otherwise out[p][q].
 template <int BN, bool FLIP>
@@ -185,12 +159,37 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     const int tile = (int)(blockIdx.x / a.split);
     const int pt = tile % a.p_tiles, qt = tile / a.p_tiles;
     const int k0 = (int)((int64_t)a.k_tiles * part / a.split), k1 = (int)((int64_t)a.k_tiles * (part + 1) / a.split);
-    if (threadIdx.x == 0) {
-        failed = 0;
-        for (int i = 0; i < 2 * S::STAGES + 1; ++i)
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" : : "r"(bar0 + 8 * i) : "memory");
-        asm volatile("fence.mbarrier_init.release.cluster;" : : : "memory");
-        asm volatile("fence.proxy.async.shared::cta;" : : : "memory");
+    // the loading warp sets up the barriers and begins; the others join it
+    // behind the __syncthreads below
+    const uint8_t *sp = a.p_scales + ((int64_t)pt * a.atoms) * MX4_ATOM;
+    auto load = [&](int k) {
+        const int s = (k - k0) % S::STAGES;
+        const uint32_t p = base + s * S::STAGE, q = p + S::P_BYTES, scp = q + S::Q_BYTES, scq = scp + S::SP_BYTES;
+        if (elect_one()) {
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(S::STAGE) : "memory");
+            tma2d(p, &map_p, k * MM_KB, pt * MM_P, full(s));
+            tma2d(q, &map_q, k * MM_KB, qt * BN, full(s));
+            bulk(scp, sp + (int64_t)k * S::SP_BYTES, S::SP_BYTES, full(s));
+#pragma unroll
+            for (int j = 0; j < S::QA; ++j) {
+                // a row tile past the matrix's last scales no stored column
+                const int rt = min((int)((int64_t)qt * BN / 128) + j, (a.nq - 1) / 128);
+                bulk(scq + j * S::SP_BYTES, a.q_scales + ((int64_t)rt * a.atoms + 2 * k) * MX4_ATOM, S::SP_BYTES, full(s));
+            }
+        }
+        __syncwarp();
+    };
+    int issued = 0;                        // stages that warp 4 issued loads for
+    if (warp == 4) {
+        if (elect_one()) {
+            failed = 0;
+            for (int i = 0; i < 2 * S::STAGES + 1; ++i)
+                asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" : : "r"(bar0 + 8 * i) : "memory");
+            asm volatile("fence.mbarrier_init.release.cluster;" : : : "memory");
+            asm volatile("fence.proxy.async.shared::cta;" : : : "memory");
+        }
+        __syncwarp();
+        for (; issued < S::STAGES && k0 + issued < k1; ++issued) load(k0 + issued);
     }
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -204,30 +203,13 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
     const uint32_t tmem = tmem_base;
 
-    int issued = 0;                        // stages that warp 4 issued loads for
     if (warp == 4) {
-        const uint8_t *sp = a.p_scales + ((int64_t)pt * a.atoms) * MX4_ATOM;
-        for (int k = k0; k < k1; ++k) {
-            const int i = k - k0, s = i % S::STAGES;
-            if (i >= S::STAGES && !warp_wait(empty(s), (uint32_t)((i / S::STAGES - 1) & 1), MM_WAIT_NS)) {
+        for (; k0 + issued < k1; ++issued) {
+            if (!warp_wait(empty(issued % S::STAGES), (uint32_t)((issued / S::STAGES - 1) & 1), MM_WAIT_NS)) {
                 failed = 1;
                 break;
             }
-            const uint32_t p = base + s * S::STAGE, q = p + S::P_BYTES, scp = q + S::Q_BYTES, scq = scp + S::SP_BYTES;
-            if (elect_one()) {
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(S::STAGE) : "memory");
-                tma2d(p, &map_p, k * MM_KB, pt * MM_P, full(s));
-                tma2d(q, &map_q, k * MM_KB, qt * BN, full(s));
-                bulk(scp, sp + (int64_t)k * S::SP_BYTES, S::SP_BYTES, full(s));
-#pragma unroll
-                for (int j = 0; j < S::QA; ++j) {
-                    // a row tile past the matrix's last scales no stored column
-                    const int rt = min((int)((int64_t)qt * BN / 128) + j, (a.nq - 1) / 128);
-                    bulk(scq + j * S::SP_BYTES, a.q_scales + ((int64_t)rt * a.atoms + 2 * k) * MX4_ATOM, S::SP_BYTES, full(s));
-                }
-            }
-            __syncwarp();
-            issued = i + 1;
+            load(k0 + issued);
         }
     } else if (warp == 5) {
         // kind::mxf4: e2m1 x e2m1, ue8m0 scales, M = 128, N = BN
@@ -278,63 +260,82 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     if (!mm_wait(done, 0, 4 * MM_WAIT_NS + 4000ull * (uint64_t)(k1 - k0))) failed = 1;
     __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
-    const int p0 = pt * MM_P, q0 = qt * BN;
-    if (a.split > 1) {
-        // partial sums to shared memory as [q][p] (the loads and products
-        // that used it are done), then each CTA of the cluster adds its share of the columns, over
-        // the parts in order
-        if (warp < 4) {
-#pragma unroll 1
-            for (int c = 0; c < BN; c += 32) {
-                uint32_t v[32];
-                tc_ld32(tmem + ((uint32_t)warp << 21) + c, v);
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (BN >= 32 || i < BN)
-                        asm volatile("st.shared.b32 [%0], %1;" : : "r"(base + 4 * ((c + i) * MM_P + 32 * warp + lane)), "r"(v[i]) : "memory");
-            }
-        }
-        asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" : : : "memory");
-        const int c0 = BN * part / a.split, c1 = BN * (part + 1) / a.split;
-        if (!failed) {
-            for (int u = threadIdx.x; u < (c1 - c0) * MM_P; u += MM_THREADS) {
-                // neighbouring threads take neighbouring elements of out
-                const int w = c1 - c0;
-                const int q = FLIP ? c0 + u / MM_P : c0 + u % w, p = FLIP ? u % MM_P : u / w;
-                float sum = 0.0f;
-                for (int r = 0; r < a.split; ++r) {
-                    uint32_t remote;
-                    float x;
-                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(base + 4 * (q * MM_P + p)), "r"(r));
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(remote) : "memory");
-                    sum = __fadd_rn(sum, x);
-                }
-                if (p0 + p < a.np && q0 + q < a.nq)
-                    store_one(a, FLIP ? (int64_t)(q0 + q) * a.ldo + p0 + p : (int64_t)(p0 + p) * a.ldo + q0 + q, sum);
-            }
-        }
-        asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" : : : "memory");
-    } else if (warp < 4 && !failed) {
-        const int p = p0 + 32 * warp + lane;
+    // The tile goes to shared memory as rows of out (the loads and products
+    // that used it are done), then the CTAs of a split share it out, each
+    // element summed over the parts in order, and store neighbouring columns.
+    constexpr int ROWS = FLIP ? BN : MM_P, COLS = FLIP ? MM_P : BN, PITCH = 4 * COLS + 16;
+    const int row0 = FLIP ? qt * BN : pt * MM_P, col0 = FLIP ? pt * MM_P : qt * BN;
+    const int rows = min(ROWS, (FLIP ? a.nq : a.np) - row0), cols = min(COLS, (FLIP ? a.np : a.nq) - col0);
+    if (warp < 4) {
 #pragma unroll 1
         for (int c = 0; c < BN; c += 32) {
-            if (q0 + c >= a.nq) break;
+            if (FLIP && c >= rows) break;
             uint32_t v[32];
             tc_ld32(tmem + ((uint32_t)warp << 21) + c, v);
-            if (p < a.np) {
-                float f[32];
+            if (FLIP) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-                if (FLIP) {
+                for (int i = 0; i < 32; ++i)
+                    if (c + i < ROWS)
+                        asm volatile("st.shared.b32 [%0], %1;" : : "r"(base + PITCH * (c + i) + 4 * (32 * warp + lane)), "r"(v[i]) : "memory");
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < BN && q0 + c + i < a.nq) store_one(a, (int64_t)(q0 + c + i) * a.ldo + p, f[i]);
-                } else {
-                    store_run(a, (int64_t)p * a.ldo + q0 + c, f, a.nq - q0 - c);
-                }
+                for (int i = 0; i < 8; ++i)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                 :
+                                 : "r"(base + PITCH * (32 * warp + lane) + 4 * c + 16 * i), "r"(v[4 * i]), "r"(v[4 * i + 1]), "r"(v[4 * i + 2]), "r"(v[4 * i + 3])
+                                 : "memory");
             }
         }
     }
+    __syncwarp();
+    if (a.split > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" : : : "memory");
+    else __syncthreads();
+    if (!failed) {
+        const int es = a.dtype == ZS_DTYPE_FP32 ? 4 : 2;
+        for (int u = part * MM_THREADS + (int)threadIdx.x; u < rows * (COLS / 4); u += a.split * MM_THREADS) {
+            const int r = u / (COLS / 4), c = 4 * (u % (COLS / 4));
+            if (c >= cols) continue;
+            const uint32_t at = base + PITCH * r + 4 * c;
+            float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (a.split == 1) {
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(at) : "memory");
+            } else {
+#pragma unroll
+                for (int h = 0; h < 8; h += 4) {          // the parts' reads in flight together
+                    float x[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (h + i < a.split)
+                            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                         : "=f"(x[i][0]), "=f"(x[i][1]), "=f"(x[i][2]), "=f"(x[i][3])
+                                         : "r"(map_to(at, (uint32_t)(h + i)))
+                                         : "memory");
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (h + i < a.split)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) f[e] = __fadd_rn(f[e], x[i][e]);
+                }
+            }
+            char *o = static_cast<char *>(a.out) + ((int64_t)(row0 + r) * a.ldo + col0 + c) * es;
+            if (a.vec && c + 4 <= cols) {
+                if (es == 4) *reinterpret_cast<float4 *>(o) = make_float4(f[0], f[1], f[2], f[3]);
+                else
+                    *reinterpret_cast<uint2 *>(o) = make_uint2(mm_cast(f[0], a.dtype) | (mm_cast(f[1], a.dtype) << 16),
+                                                               mm_cast(f[2], a.dtype) | (mm_cast(f[3], a.dtype) << 16));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < cols) {
+                        if (es == 4) reinterpret_cast<float *>(o)[e] = f[e];
+                        else reinterpret_cast<uint16_t *>(o)[e] = (uint16_t)mm_cast(f[e], a.dtype);
+                    }
+            }
+        }
+    }
+    // no CTA leaves while another reads its part
+    __syncwarp();
+    if (a.split > 1) asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" : : : "memory");
     if (warp == 4 && lane == 0 && failed) {
         // let the loads already issued land before the shared memory goes away
         for (int i = issued > S::STAGES ? issued - S::STAGES : 0; i < issued; ++i)
@@ -365,12 +366,6 @@ constexpr int PAIR_STAGE = PAIR_P + PAIR_Q + PAIR_SP + PAIR_SQ;
 constexpr int PAIR_SLAB = 32 * 128;       // a storing warp's buffer: 32 rows of 128 bytes
 constexpr int PAIR_SMEM = PAIR_STAGES * PAIR_STAGE + 8 * PAIR_SLAB + 1024;
 constexpr int PAIR_SP_COL = 256, PAIR_SQ_COL = PAIR_SP_COL + 16;   // scales, two sets of each
-
-__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
 
 __device__ __forceinline__ void tma2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
     asm volatile(
@@ -816,7 +811,7 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const zs_mx4
     if (pt * qt * split > 0x7FFFFFFF) return zs_fail(ZS_EINVAL, "%s: too many tiles", fn);
     a.split = split;
     a.dtype = dtype;
-    a.vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ldo * size % 16 == 0;
+    a.vec = reinterpret_cast<uintptr_t>(out) % (4 * size) == 0 && ldo % 4 == 0;
     CUtensorMap mp, mq;
     if (!zsk::code_map(&mp, P->codes, np, mx4_row_bytes(k), zsk::MM_P) ||
         !zsk::code_map(&mq, Q->codes, nq, mx4_row_bytes(k), bn))
