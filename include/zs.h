@@ -718,32 +718,30 @@ zs_status zs_adam_tensors(const zs_tensors *list, const zs_adam_hparams *hp, int
  * a row, in tiles of 128 rows by 4 groups of 512 bytes each: row r, group g
  * in tile (r / 128, g / 4), at byte (r % 32) * 16 + (r % 128 / 32) * 4 + g % 4
  * of it, tiles row-major, their number along a row rounded up to even.
- * Columns past cols hold code 0, rows and groups past the matrix scale 0. */
-typedef struct {
-    void *codes;              /* rows * row_bytes bytes, 16-byte aligned */
-    void *scales;             /* scale_bytes bytes, 16-byte aligned      */
-} zs_mx4;
+ * Columns past cols hold code 0, rows and groups past the matrix scale 0.
+ * Codes and scales are device memory of the caller, 16-byte aligned. */
 
 /* Bytes of a matrix: of a row of codes, of all codes, of all scales. */
 zs_status zs_mx4_sizes(int64_t rows, int64_t cols, int64_t *row_bytes, int64_t *code_bytes,
                        int64_t *scale_bytes);
 
 /* Quantise x [rows][cols] (dtype, row stride ld >= cols elements; 16-byte
- * vectors when x and its rows are 16-byte aligned).  along_rows: x itself,
- * groups of 32 along its rows.  along_cols: the transposed matrix
- * [cols][rows], groups along x's columns (what the gradients' products read).
- * Either may be NULL; both come from one read.  A group with largest
+ * vectors when x and its rows are 16-byte aligned).  r_codes, r_scales: x
+ * itself, groups of 32 along its rows.  c_codes, c_scales: the transposed
+ * matrix [cols][rows], groups along x's columns (what the gradients' products
+ * read).  Either pair may be NULL; both come from one read.  A group with largest
  * magnitude max has s = floor(log2 max) - 2 + 127, at least 0 (s = 0 also
  * for a group of zeros or of fp32 subnormals), and the codes of
  * x * 2^(127-s) to nearest, ties to even, at most 6 in magnitude.  A group
  * with an infinity or NaN has s = 255 and codes 0: it is NaN in every
  * product.  Errors: ZS_EINVAL, ZS_ECUDA. */
 zs_status zs_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
-                          const zs_mx4 *along_rows, const zs_mx4 *along_cols, void *stream);
+                          void *r_codes, void *r_scales, void *c_codes, void *c_scales,
+                          void *stream);
 
 /* The values of a matrix: out [rows][cols] (dtype, row stride ldo). */
-zs_status zs_mx4_dequantize(const zs_mx4 *held, int64_t rows, int64_t cols, void *out, int64_t ldo,
-                            int32_t dtype, void *stream);
+zs_status zs_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols,
+                            void *out, int64_t ldo, int32_t dtype, void *stream);
 
 /* out[m][n] = sum over k of a[m][k] * b[n][k] (dtype, row stride ldo),
  * products and sums in fp32, rounded once.  For a linear layer y = x w^T:
@@ -752,8 +750,9 @@ zs_status zs_mx4_dequantize(const zs_mx4 *held, int64_t rows, int64_t cols, void
  *   dw = matmul(dy along cols, x along cols)     k = tokens
  * k = 0 gives zeros.  Errors: ZS_EINVAL, ZS_ECUDA; a device wait that gave
  * up is counted by zs_device_wait_timeouts. */
-zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const zs_mx4 *a, const zs_mx4 *b, void *out,
-                        int64_t ldo, int32_t dtype, void *stream);
+zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *a_codes, const void *a_scales,
+                        const void *b_codes, const void *b_scales, void *out, int64_t ldo,
+                        int32_t dtype, void *stream);
 
 #ifdef __cplusplus
 }

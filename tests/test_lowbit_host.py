@@ -1,6 +1,4 @@
 """The low-bit calls' refusals and host-side layout (no GPU: argument errors enqueue nothing), and the references' own pins."""
-import ctypes as C
-
 import numpy as np
 import pytest
 
@@ -92,36 +90,37 @@ def call(name, *a):
 
 
 def test_mx4_refusals():
-    ok, no, odd = (zs.zs_mx4(A16, A16), zs.zs_mx4(A16, None), zs.zs_mx4(A16 + 8, A16))
-    p = C.byref
+    a, odd = A16, A16 + 8
     q = "zs_mx4_quantize"
-    call(q, A16, 4, 64, 63, 0, p(ok), None, None)             # rows overlap
-    call(q, A16, -1, 64, 64, 0, p(ok), None, None)
-    call(q, A16, 4, 1 << 31, 1 << 31, 0, p(ok), None, None)
-    call(q, A16, 4, 64, 64, 3, p(ok), None, None)
-    call(q, A16, 4, 64, 64, 0, None, None, None)
-    call(q, None, 4, 64, 64, 0, p(ok), None, None)
-    call(q, A16 + 1, 4, 64, 64, 0, p(ok), None, None)
-    call(q, A16 + 2, 4, 64, 64, 2, p(ok), None, None)
-    call(q, A16, 4, 64, 64, 0, p(no), None, None)
-    call(q, A16, 4, 64, 64, 0, p(ok), p(odd), None)
+    call(q, a, 4, 64, 63, 0, a, a, None, None, None)             # rows overlap
+    call(q, a, -1, 64, 64, 0, a, a, None, None, None)
+    call(q, a, 4, 1 << 31, 1 << 31, 0, a, a, None, None, None)
+    call(q, a, 4, 64, 64, 3, a, a, None, None, None)
+    call(q, a, 4, 64, 64, 0, None, None, None, None, None)
+    call(q, None, 4, 64, 64, 0, a, a, None, None, None)
+    call(q, a + 1, 4, 64, 64, 0, a, a, None, None, None)
+    call(q, a + 2, 4, 64, 64, 2, a, a, None, None, None)
+    call(q, a, 4, 64, 64, 0, a, None, None, None, None)
+    call(q, a, 4, 64, 64, 0, None, a, None, None, None)
+    call(q, a, 4, 64, 64, 0, a, a, odd, a, None)
+    call(q, a, 4, 64, 64, 0, a, a, a, odd, None)
     d = "zs_mx4_dequantize"
-    call(d, None, 4, 64, A16, 64, 0, None)
-    call(d, p(no), 4, 64, A16, 64, 0, None)
-    call(d, p(ok), 4, 64, None, 64, 0, None)
-    call(d, p(ok), 4, 64, A16, 63, 0, None)
-    call(d, p(ok), 4, 64, A16, 64, -1, None)
+    call(d, None, a, 4, 64, a, 64, 0, None)
+    call(d, a, None, 4, 64, a, 64, 0, None)
+    call(d, a, a, 4, 64, None, 64, 0, None)
+    call(d, a, a, 4, 64, a, 63, 0, None)
+    call(d, a, a, 4, 64, a, 64, -1, None)
     m = "zs_mx4_matmul"
-    call(m, -1, 4, 64, p(ok), p(ok), A16, 4, 0, None)
-    call(m, 4, 4, 1 << 31, p(ok), p(ok), A16, 4, 0, None)
-    call(m, 4, 4, 64, p(ok), p(ok), A16, 3, 0, None)
-    call(m, 4, 4, 64, p(ok), p(ok), A16, 4, 7, None)
-    call(m, 4, 4, 64, None, p(ok), A16, 4, 0, None)
-    call(m, 4, 4, 64, p(ok), p(no), A16, 4, 0, None)
-    call(m, 4, 4, 64, p(odd), p(ok), A16, 4, 0, None)
-    call(m, 4, 4, 64, p(ok), p(ok), None, 4, 0, None)
-    call(m, 4, 4, 64, p(ok), p(ok), A16 + 1, 4, 0, None)
-    call(m, 4, 4, 64, p(ok), p(ok), A16 + 2, 4, 2, None)
+    call(m, -1, 4, 64, a, a, a, a, a, 4, 0, None)
+    call(m, 4, 4, 1 << 31, a, a, a, a, a, 4, 0, None)
+    call(m, 4, 4, 64, a, a, a, a, a, 3, 0, None)
+    call(m, 4, 4, 64, a, a, a, a, a, 4, 7, None)
+    call(m, 4, 4, 64, None, a, a, a, a, 4, 0, None)
+    call(m, 4, 4, 64, a, a, a, None, a, 4, 0, None)
+    call(m, 4, 4, 64, a, odd, a, a, a, 4, 0, None)
+    call(m, 4, 4, 64, a, a, a, a, None, 4, 0, None)
+    call(m, 4, 4, 64, a, a, a, a, a + 1, 4, 0, None)
+    call(m, 4, 4, 64, a, a, a, a, a + 2, 4, 2, None)
 
 
 def test_binding_refusals():

@@ -136,10 +136,6 @@ class zs_tensors_info_t(C.Structure):
                 ("device_table_bytes", C.c_int64)]
 
 
-class zs_mx4(C.Structure):
-    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p)]
-
-
 _P = C.c_void_p
 _i32, _i64, _f32 = C.c_int32, C.c_int64, C.c_float
 
@@ -204,10 +200,9 @@ _sig("zs_tensors_info", _i32, [_P, C.POINTER(zs_tensors_info_t)])
 _sig("zs_tensors_upload", _i32, [_P, _P, _i64, _P])
 _sig("zs_adam_tensors", _i32, [_P, C.POINTER(zs_adam_hparams), _i64, _i32, C.c_uint64, _P, _P, _P])
 _sig("zs_mx4_sizes", _i32, [_i64, _i64, C.POINTER(_i64), C.POINTER(_i64), C.POINTER(_i64)])
-_sig("zs_mx4_quantize", _i32, [_P, _i64, _i64, _i64, _i32, C.POINTER(zs_mx4), C.POINTER(zs_mx4), _P])
-_sig("zs_mx4_dequantize", _i32, [C.POINTER(zs_mx4), _i64, _i64, _P, _i64, _i32, _P])
-_sig("zs_mx4_matmul", _i32, [_i64, _i64, _i64, C.POINTER(zs_mx4), C.POINTER(zs_mx4), _P, _i64,
-                             _i32, _P])
+_sig("zs_mx4_quantize", _i32, [_P, _i64, _i64, _i64, _i32, _P, _P, _P, _P, _P])
+_sig("zs_mx4_dequantize", _i32, [_P, _P, _i64, _i64, _P, _i64, _i32, _P])
+_sig("zs_mx4_matmul", _i32, [_i64, _i64, _i64, _P, _P, _P, _P, _P, _i64, _i32, _P])
 
 
 def _check(status: int, fn: str) -> None:
@@ -224,13 +219,31 @@ def _ptr(x):
     return int(x)
 
 
+def _find_current_stream():
+    """The address of torch's current stream; from its second call on, by the
+    quickest way that this torch has (the public one takes about 4 us, as long
+    as a small kernel)."""
+    global _current_stream
+    try:
+        import torch
+        if not torch.cuda.is_available():
+            return None
+        stream = torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        if raw is not None and device is not None and raw(device()) == stream:
+            _current_stream = lambda: raw(device())
+        return stream
+    except Exception:  # torch without CUDA
+        return None
+
+
+_current_stream = _find_current_stream
+
+
 def _stream(s):
     if s is None:
-        try:
-            import torch
-            return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
-        except Exception:  # torch without CUDA
-            return None
+        return _current_stream()
     if hasattr(s, "cuda_stream"):
         return s.cuda_stream
     return int(s)
@@ -414,7 +427,7 @@ def zs_grad_norm(plan, grad_shards, persist_grads, norm_scratch, recompute: bool
 def _hp(hp) -> zs_adam_hparams:
     if isinstance(hp, zs_adam_hparams):
         return hp
-    d = dict(hp)
+    d = hp if type(hp) is dict else dict(hp)
     return zs_adam_hparams(float(d["lr"]), float(d["beta1"]), float(d["beta2"]), float(d["eps"]),
                            float(d["weight_decay"]), int(d.get("adamw", 1)),
                            int(d.get("bias_correction", 1)))
@@ -592,13 +605,18 @@ def zs_sched_log(sched) -> list:
 
 # ---------------------------------------------- training with little memory --
 
+_DTYPES: dict = {}
+
+
 def _dtype(t) -> int:
     """ZS_DTYPE_* of a torch tensor."""
-    name = str(t.dtype)
-    got = {"torch.bfloat16": ZS_DTYPE_BF16, "torch.float16": ZS_DTYPE_FP16,
-           "torch.float32": ZS_DTYPE_FP32}.get(name)
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: ZS_DTYPE_BF16, torch.float16: ZS_DTYPE_FP16,
+                        torch.float32: ZS_DTYPE_FP32})
+    got = _DTYPES.get(t.dtype)
     if got is None:
-        raise TypeError(f"bfloat16, float16 or float32 expected, got {name}")
+        raise TypeError(f"bfloat16, float16 or float32 expected, got {t.dtype}")
     return got
 
 
@@ -700,48 +718,59 @@ def zs_mx4_sizes(rows: int, cols: int) -> dict:
 
 
 def _mx4(held, rows: int, cols: int):
-    """zs_mx4 of a dict with "codes" [rows, row_bytes] and "scales" (uint8
+    """(codes, scales) addresses of a dict with "codes" and "scales" (uint8
     tensors, or addresses), whose tensors are large enough for rows x cols."""
     if held is None:
-        return None
-    if hasattr(held["codes"], "numel"):
-        size = zs_mx4_sizes(rows, cols)
-        for name, need in (("codes", size["code_bytes"]), ("scales", size["scale_bytes"])):
-            x = held[name]
-            if x.element_size() != 1 or x.numel() < need or not x.is_contiguous():
-                raise ValueError(f"{name}: {need} contiguous bytes expected for {rows} x {cols}")
-    return zs_mx4(_ptr(held["codes"]), _ptr(held["scales"]))
+        return None, None
+    codes, scales = held["codes"], held["scales"]
+    if not hasattr(codes, "data_ptr"):
+        return codes, scales
+    groups = (cols + 31) >> 5
+    for x, need in ((codes, 16 * rows * groups), (scales, ((rows + 127) >> 7) * ((groups + 7) >> 3) << 10)):
+        if x.numel() < need or x.itemsize != 1 or not x.is_contiguous():
+            raise ValueError(f"{need} contiguous bytes expected for {rows} x {cols}, got {tuple(x.shape)} of {x.dtype}")
+    return codes.data_ptr(), scales.data_ptr()
 
 
 def _matrix(x, what: str):
     """(rows, cols, row stride) of a 2-D torch tensor whose rows are contiguous."""
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError(f"{what}: a matrix with contiguous rows expected")
-    return x.shape[0], x.shape[1], max(x.stride(0), x.shape[1]) if x.shape[0] > 1 else x.shape[1]
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what}: a matrix expected, got {tuple(shape)}")
+    rows, cols = shape
+    ld, one = x.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{what}: rows are not contiguous")
+    return rows, cols, ld if rows > 1 else cols
 
 
 def zs_mx4_quantize(x, rows=None, cols=None, stream=None) -> None:
     """x: [r, c] torch matrix.  rows: the dict of x held along its rows
     ([r, c]); cols: of the transposed matrix ([c, r]); either may be None."""
     r, c, ld = _matrix(x, "x")
-    a, b = _mx4(rows, r, c), _mx4(cols, c, r)
-    _check(_lib.zs_mx4_quantize(_ptr(x), r, c, ld, _dtype(x), C.byref(a) if a else None,
-                                C.byref(b) if b else None, _stream(stream)), "zs_mx4_quantize")
+    rc, rs = _mx4(rows, r, c)
+    cc, cs = _mx4(cols, c, r)
+    st = _lib.zs_mx4_quantize(x.data_ptr(), r, c, ld, _dtype(x), rc, rs, cc, cs, _stream(stream))
+    if st:
+        _check(st, "zs_mx4_quantize")
 
 
 def zs_mx4_dequantize(held, out, stream=None):
     """out: [r, c] torch matrix that receives the values; returned."""
     r, c, ld = _matrix(out, "out")
-    h = _mx4(held, r, c)
-    _check(_lib.zs_mx4_dequantize(C.byref(h), r, c, _ptr(out), ld, _dtype(out), _stream(stream)),
-           "zs_mx4_dequantize")
+    hc, hs = _mx4(held, r, c)
+    st = _lib.zs_mx4_dequantize(hc, hs, r, c, out.data_ptr(), ld, _dtype(out), _stream(stream))
+    if st:
+        _check(st, "zs_mx4_dequantize")
     return out
 
 
 def zs_mx4_matmul(a, b, k: int, out, stream=None):
     """out [m, n] = a [m, k] b [n, k]^T of two held matrices; out is returned."""
     m, n, ld = _matrix(out, "out")
-    ha, hb = _mx4(a, m, k), _mx4(b, n, k)
-    _check(_lib.zs_mx4_matmul(m, n, int(k), C.byref(ha), C.byref(hb), _ptr(out), ld, _dtype(out),
-                              _stream(stream)), "zs_mx4_matmul")
+    ac, as_ = _mx4(a, m, k)
+    bc, bs = _mx4(b, n, k)
+    st = _lib.zs_mx4_matmul(m, n, k, ac, as_, bc, bs, out.data_ptr(), ld, _dtype(out), _stream(stream))
+    if st:
+        _check(st, "zs_mx4_matmul")
     return out

@@ -351,6 +351,29 @@ __device__ inline bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_n
     return false;
 }
 
+// mbar_wait without its look at the clock (a slow read) unless the barrier
+// stays closed for a while: for waits that stand between pieces of work.
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool mbar_wait_quick(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 <= limit_ns)
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try(bar, parity)) return true;
+    return false;
+}
+
 struct AdamC {
     float lr, b1, b2, omb1, omb2, eps, wd, lr_wd, bc1, bc2;
     int adamw;

@@ -229,8 +229,8 @@ bool al16(const void *p) { return p && (addr(p) & 15) == 0; }
 bool dtype_ok(int32_t t) { return t >= ZS_DTYPE_BF16 && t <= ZS_DTYPE_FP32; }
 constexpr int64_t MX4_MOST = (int64_t)1 << 31;       // rows, columns
 
-zs_status check_held(const zs_mx4 *h, int64_t rows, int64_t cols, const char *what, const char *fn) {
-    if (rows > 0 && cols > 0 && (!al16(h->codes) || !al16(h->scales)))
+zs_status check_held(const void *codes, const void *scales, int64_t rows, int64_t cols, const char *what, const char *fn) {
+    if (rows > 0 && cols > 0 && (!al16(codes) || !al16(scales)))
         return zs_fail(ZS_EINVAL, "%s: %s: codes or scales NULL or not 16-byte aligned", fn, what);
     return ZS_OK;
 }
@@ -269,23 +269,25 @@ zs_status zs_mx4_sizes(int64_t rows, int64_t cols, int64_t *row_bytes, int64_t *
 }
 
 zs_status zs_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
-                          const zs_mx4 *along_rows, const zs_mx4 *along_cols, void *stream) {
+                          void *r_codes, void *r_scales, void *c_codes, void *c_scales, void *stream) {
     const char *fn = "zs_mx4_quantize";
     zs_status r = check_matrix(rows, cols, x, ld, dtype, fn);
     if (r) return r;
-    if (!along_rows && !along_cols) return zs_fail(ZS_EINVAL, "%s: neither form is asked for", fn);
-    if (along_rows && (r = check_held(along_rows, rows, cols, "along_rows", fn))) return r;
-    if (along_cols && (r = check_held(along_cols, rows, cols, "along_cols", fn))) return r;
+    const bool along_rows = r_codes || r_scales, along_cols = c_codes || c_scales;
+    if (along_rows && (r = check_held(r_codes, r_scales, rows, cols, "along rows", fn))) return r;
+    if (along_cols && (r = check_held(c_codes, c_scales, rows, cols, "along columns", fn))) return r;
+    if (!along_rows && !along_cols && rows > 0 && cols > 0)
+        return zs_fail(ZS_EINVAL, "%s: neither form is asked for", fn);
     if (rows == 0 || cols == 0) {
         zs_clear_error();
         return ZS_OK;
     }
     zsk::Mx4Args a;
     a.x = x; a.rows = rows; a.cols = cols; a.ld = ld;
-    a.r_codes = along_rows ? static_cast<uint8_t *>(along_rows->codes) : nullptr;
-    a.r_scales = along_rows ? static_cast<uint8_t *>(along_rows->scales) : nullptr;
-    a.c_codes = along_cols ? static_cast<uint8_t *>(along_cols->codes) : nullptr;
-    a.c_scales = along_cols ? static_cast<uint8_t *>(along_cols->scales) : nullptr;
+    a.r_codes = static_cast<uint8_t *>(r_codes);
+    a.r_scales = static_cast<uint8_t *>(r_scales);
+    a.c_codes = static_cast<uint8_t *>(c_codes);
+    a.c_scales = static_cast<uint8_t *>(c_scales);
     // every scale atom is some tile's, the padding ones included
     a.tiles_c = along_rows ? mx4_atoms(cols) : mx4_row_tiles(cols);
     const int64_t tiles_r = along_cols ? mx4_atoms(rows) : mx4_row_tiles(rows);
@@ -302,13 +304,12 @@ zs_status zs_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld,
     return cuda_status(e, fn);
 }
 
-zs_status zs_mx4_dequantize(const zs_mx4 *held, int64_t rows, int64_t cols, void *out, int64_t ldo,
-                            int32_t dtype, void *stream) {
+zs_status zs_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols, void *out,
+                            int64_t ldo, int32_t dtype, void *stream) {
     const char *fn = "zs_mx4_dequantize";
-    if (!held) return zs_fail(ZS_EINVAL, "%s: NULL matrix", fn);
     zs_status r = check_matrix(rows, cols, out, ldo, dtype, fn);
     if (r) return r;
-    if ((r = check_held(held, rows, cols, "matrix", fn))) return r;
+    if ((r = check_held(codes, scales, rows, cols, "matrix", fn))) return r;
     if (rows == 0 || cols == 0) {
         zs_clear_error();
         return ZS_OK;
@@ -317,7 +318,7 @@ zs_status zs_mx4_dequantize(const zs_mx4 *held, int64_t rows, int64_t cols, void
     if (grid > 0x7FFFFFFF) return zs_fail(ZS_EINVAL, "%s: %lld x %lld too large", fn, (long long)rows, (long long)cols);
     const cudaStream_t s = (cudaStream_t)stream;
     const bool vec = (addr(out) & 15) == 0 && ldo % (dtype == ZS_DTYPE_FP32 ? 4 : 8) == 0;
-    const uint8_t *c = static_cast<const uint8_t *>(held->codes), *sc = static_cast<const uint8_t *>(held->scales);
+    const uint8_t *c = static_cast<const uint8_t *>(codes), *sc = static_cast<const uint8_t *>(scales);
     using namespace zsk;
     const dim3 g((unsigned)grid), b(256);
     if (dtype == ZS_DTYPE_FP32) {

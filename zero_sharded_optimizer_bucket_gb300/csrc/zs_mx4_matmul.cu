@@ -51,32 +51,9 @@ struct MmArgs {
     int32_t vec;              // rows of out are aligned to 4 elements
 };
 
-// mbar_wait without its look at the clock (a slow read) unless the barrier
-// stays closed for a while: these waits stand between the products.
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-__device__ __forceinline__ bool mm_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-    for (int i = 0; i < 64; ++i)
-        if (mbar_try(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    while (global_ns() - t0 <= limit_ns)
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try(bar, parity)) return true;
-    return false;
-}
-
 // One wait of a whole warp: the same answer in all lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-    return __all_sync(0xFFFFFFFFu, mm_wait(bar, parity, limit_ns));
+    return __all_sync(0xFFFFFFFFu, mbar_wait_quick(bar, parity, limit_ns));
 }
 
 // True in one lane of a converged warp.  The warps that issue loads and
@@ -257,7 +234,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
         __syncwarp();
     }
     // everyone waits until the products of this CTA are in tensor memory
-    if (!mm_wait(done, 0, 4 * MM_WAIT_NS + 4000ull * (uint64_t)(k1 - k0))) failed = 1;
+    if (!mbar_wait_quick(done, 0, 4 * MM_WAIT_NS + 4000ull * (uint64_t)(k1 - k0))) failed = 1;
     __syncwarp();
     asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
     // The tile goes to shared memory as rows of out (the loads and products
@@ -339,7 +316,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     if (warp == 4 && lane == 0 && failed) {
         // let the loads already issued land before the shared memory goes away
         for (int i = issued > S::STAGES ? issued - S::STAGES : 0; i < issued; ++i)
-            mm_wait(full(i % S::STAGES), (uint32_t)((i / S::STAGES) & 1), MM_WAIT_NS);
+            mbar_wait_quick(full(i % S::STAGES), (uint32_t)((i / S::STAGES) & 1), MM_WAIT_NS);
         atomicAdd(&g_mx4_wait_timeouts, 1);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
@@ -599,7 +576,7 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
     if (warp == 8 && lane == 0 && failed) {
         if (rank == 0)   // the leader's barriers count the loads of both CTAs
             for (int i = issued > PAIR_STAGES ? issued - PAIR_STAGES : 0; i < issued; ++i)
-                mm_wait(full(i % PAIR_STAGES), (uint32_t)((i / PAIR_STAGES) & 1), MM_WAIT_NS);
+                mbar_wait_quick(full(i % PAIR_STAGES), (uint32_t)((i / PAIR_STAGES) & 1), MM_WAIT_NS);
         atomicAdd(&g_mx4_wait_timeouts, 1);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
@@ -738,15 +715,15 @@ cudaError_t zsl_mx4_wait_timeouts(int *count, bool reset) {
     return e;
 }
 
-extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const zs_mx4 *A, const zs_mx4 *B, void *out,
-                                   int64_t ldo, int32_t dtype, void *stream) {
+extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *a_codes, const void *a_scales,
+                                   const void *b_codes, const void *b_scales, void *out, int64_t ldo, int32_t dtype,
+                                   void *stream) {
     const char *fn = "zs_mx4_matmul";
     constexpr int64_t MOST = (int64_t)1 << 31;
     if (m < 0 || n < 0 || k < 0 || m >= MOST || n >= MOST || k >= MOST)
         return zs_fail(ZS_EINVAL, "%s: m %lld, n %lld, k %lld out of range", fn, (long long)m, (long long)n, (long long)k);
     if (dtype < ZS_DTYPE_BF16 || dtype > ZS_DTYPE_FP32) return zs_fail(ZS_EINVAL, "%s: dtype %d", fn, dtype);
     if (ldo < n) return zs_fail(ZS_EINVAL, "%s: row stride %lld < n = %lld", fn, (long long)ldo, (long long)n);
-    if (!A || !B) return zs_fail(ZS_EINVAL, "%s: NULL matrix", fn);
     if (m == 0 || n == 0) {
         zs_clear_error();
         return ZS_OK;
@@ -763,7 +740,7 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const zs_mx4
         zs_clear_error();
         return ZS_OK;
     }
-    const void *four[4] = {A->codes, A->scales, B->codes, B->scales};
+    const void *four[4] = {a_codes, a_scales, b_codes, b_scales};
     for (const void *p : four)
         if (!p || (reinterpret_cast<uintptr_t>(p) & 15))
             return zs_fail(ZS_EINVAL, "%s: codes or scales NULL or not 16-byte aligned", fn);
@@ -771,8 +748,8 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const zs_mx4
     const int64_t pair_p = (m + zsk::PAIR_ROWS - 1) / zsk::PAIR_ROWS, pair_q = (n + zsk::PAIR_COLS - 1) / zsk::PAIR_COLS;
     if (m > 128 && pair_p * pair_q >= 38 && pair_p * pair_q < 0x7FFFFFFF) {
         CUtensorMap map[4];
-        if (!zsk::code_map(&map[0], A->codes, m, mx4_row_bytes(k), 128) || !zsk::code_map(&map[1], B->codes, n, mx4_row_bytes(k), 128) ||
-            !zsk::scale_map(&map[2], A->scales, m, k, 1) || !zsk::scale_map(&map[3], B->scales, n, k, 2))
+        if (!zsk::code_map(&map[0], a_codes, m, mx4_row_bytes(k), 128) || !zsk::code_map(&map[1], b_codes, n, mx4_row_bytes(k), 128) ||
+            !zsk::scale_map(&map[2], a_scales, m, k, 1) || !zsk::scale_map(&map[3], b_scales, n, k, 2))
             return zs_fail(ZS_ECUDA, "%s: cuTensorMapEncodeTiled failed", fn);
         zsk::PairArgs a;
         a.out = out;
@@ -789,14 +766,15 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const zs_mx4
         zs_clear_error();
         return ZS_OK;
     }
-    const bool flip = m <= 128;
+    const bool flip = m <= 64;
     const int64_t np = flip ? n : m, nq = flip ? m : n;
-    const zs_mx4 *P = flip ? B : A, *Q = flip ? A : B;
+    const void *p_codes = flip ? b_codes : a_codes, *p_scales = flip ? b_scales : a_scales;
+    const void *q_codes = flip ? a_codes : b_codes, *q_scales = flip ? a_scales : b_scales;
     int bn = 128;
-    if (flip) bn = nq <= 16 ? 16 : nq <= 32 ? 32 : nq <= 64 ? 64 : 128;
+    if (flip) bn = nq <= 16 ? 16 : nq <= 32 ? 32 : 64;   // one tile of Q: scale addresses are whole atoms
     zsk::MmArgs a;
-    a.p_scales = static_cast<const uint8_t *>(P->scales);
-    a.q_scales = static_cast<const uint8_t *>(Q->scales);
+    a.p_scales = static_cast<const uint8_t *>(p_scales);
+    a.q_scales = static_cast<const uint8_t *>(q_scales);
     a.out = out;
     a.ldo = ldo;
     a.np = (int32_t)np;
@@ -807,19 +785,18 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const zs_mx4
     a.p_tiles = (int32_t)pt;
     a.q_tiles = (int32_t)qt;
     int split = 1;
-    while (split < 8 && pt * qt * split * 2 <= 304 && a.k_tiles >= 4 * split) split *= 2;
+    while (split < 8 && pt * qt * split * 2 <= 152 && a.k_tiles >= (bn == 128 ? 8 : 4) * split) split *= 2;
     if (pt * qt * split > 0x7FFFFFFF) return zs_fail(ZS_EINVAL, "%s: too many tiles", fn);
     a.split = split;
     a.dtype = dtype;
     a.vec = reinterpret_cast<uintptr_t>(out) % (4 * size) == 0 && ldo % 4 == 0;
     CUtensorMap mp, mq;
-    if (!zsk::code_map(&mp, P->codes, np, mx4_row_bytes(k), zsk::MM_P) ||
-        !zsk::code_map(&mq, Q->codes, nq, mx4_row_bytes(k), bn))
+    if (!zsk::code_map(&mp, p_codes, np, mx4_row_bytes(k), zsk::MM_P) ||
+        !zsk::code_map(&mq, q_codes, nq, mx4_row_bytes(k), bn))
         return zs_fail(ZS_ECUDA, "%s: cuTensorMapEncodeTiled failed", fn);
     using namespace zsk;
     if (flip)
-        e = bn == 16 ? mm_launch<16, true>(mp, mq, a, s) : bn == 32 ? mm_launch<32, true>(mp, mq, a, s)
-          : bn == 64 ? mm_launch<64, true>(mp, mq, a, s) : mm_launch<128, true>(mp, mq, a, s);
+        e = bn == 16 ? mm_launch<16, true>(mp, mq, a, s) : bn == 32 ? mm_launch<32, true>(mp, mq, a, s) : mm_launch<64, true>(mp, mq, a, s);
     else
         e = mm_launch<128, false>(mp, mq, a, s);
     if (e != cudaSuccess) return zs_fail(ZS_ECUDA, "%s: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));

@@ -1,7 +1,7 @@
 // Adam(W) over a list of separate tensors in one launch, moments in 32 bits
 // or in 8 (zs_build_tensors, zs_adam_tensors).
 //
-// The host cuts every tensor into chunks of CHUNK elements and writes one
+// The host cuts every tensor into chunks and writes one
 // record per chunk, with the addresses already advanced to it, so that a CTA
 // finds all it needs in one load whatever the number of tensors.
 //
@@ -12,13 +12,19 @@
 // scale for each, 2^(floor(log2 max) - 7): e4m3 is a floating format, so a
 // power of two costs no precision, makes scaling exact and leaves its largest
 // value in [128, 256), which no rounding takes past 448.
+#include <atomic>
 #include <new>
 #include <vector>
 
 #include "zs_device.cuh"
 #include "zs_launch.h"
 
-constexpr int CHUNK = 8192;          // elements per CTA
+// Elements per CTA: a list long enough to fill the GPU takes the chunk at
+// which its kernel was fastest (32-bit moments 8192: 834 us for 202M
+// elements; 8-bit 6144: 470 us rounded to nearest, against 488 at 4096 and at
+// 8192); a short one takes small chunks, spread over more SMs.
+constexpr int CHUNK32 = 8192, CHUNK8 = 6144, CHUNK_SHORT = 2048;
+constexpr int64_t SHORT_ELEMS = 304ll * CHUNK8;     // two chunks an SM
 constexpr int STATE_BLOCK = 256;     // elements per scale: 8 a lane of one warp
 
 struct ZsChunk {
@@ -44,17 +50,37 @@ struct zs_tensors {
 namespace zsk {
 
 struct Adam8C {
-    float b1, b2, omb1, omb2, eps, wd, lr_wd, step_size, root;
+    float b1, b2, omb1, omb2, eps, wd, lr_wd, step_size, root, root_2_32, one, minus_one;
     int adamw;
     uint32_t k0, k1, step;
 };
 
+__device__ __forceinline__ void floats4(const uint4 &v, float o[4]) {
+    o[0] = __uint_as_float(v.x); o[1] = __uint_as_float(v.y);
+    o[2] = __uint_as_float(v.z); o[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 r;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+
+// Gradient types: 8 elements from global and from shared memory, or one.
 struct F32G {
+    static constexpr int SIZE = 4;
     static __device__ __forceinline__ void load8(const void *p, int64_t i, float g[8]) {
-        const float4 x = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i));
-        const float4 y = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + 4));
-        g[0] = x.x; g[1] = x.y; g[2] = x.z; g[3] = x.w;
-        g[4] = y.x; g[5] = y.y; g[6] = y.z; g[7] = y.w;
+        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i);
+        floats4(__ldg(q), g);
+        floats4(__ldg(q + 1), g + 4);
+    }
+    static __device__ __forceinline__ void shared8(uint32_t a, float g[8]) {
+        floats4(lds16(a), g);
+        floats4(lds16(a + 16), g + 4);
     }
     static __device__ __forceinline__ float load1(const void *p, int64_t i) {
         return static_cast<const float *>(p)[i];
@@ -62,11 +88,15 @@ struct F32G {
 };
 template <class T>
 struct H16G {
-    static __device__ __forceinline__ void load8(const void *p, int64_t i, float g[8]) {
-        const uint4 v = ldg16(static_cast<const uint16_t *>(p) + i);
+    static constexpr int SIZE = 2;
+    static __device__ __forceinline__ void convert(const uint4 &v, float g[8]) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[j] = T::to_f32(lane16(v, j));
     }
+    static __device__ __forceinline__ void load8(const void *p, int64_t i, float g[8]) {
+        convert(ldg16(static_cast<const uint16_t *>(p) + i), g);
+    }
+    static __device__ __forceinline__ void shared8(uint32_t a, float g[8]) { convert(lds16(a), g); }
     static __device__ __forceinline__ float load1(const void *p, int64_t i) {
         return T::to_f32(static_cast<const uint16_t *>(p)[i]);
     }
@@ -86,15 +116,21 @@ __device__ __forceinline__ void store8f(float *a, const float o[8]) {
 // The 16-bit copy of 8 new parameters (fp16: the type is a launch argument,
 // uniform over the grid).
 __device__ __forceinline__ uint4 cast8(const float p[8], bool fp16) {
-    uint32_t r[8];
+    uint32_t r[4];
     if (fp16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = FP16T::from_f32(p[i]);
+        for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(p[2 * i], p[2 * i + 1]);
+            r[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = BF16T::from_f32(p[i]);
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(p[2 * i], p[2 * i + 1]);
+            r[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
     }
-    return pack8(r);
+    return make_uint4(r[0], r[1], r[2], r[3]);
 }
 __device__ __forceinline__ uint16_t cast1(float p, bool fp16) {
     return (uint16_t)(fp16 ? FP16T::from_f32(p) : BF16T::from_f32(p));
@@ -144,12 +180,11 @@ __device__ __forceinline__ void philox7(uint32_t c0, uint32_t c1, uint32_t c2, u
                                         uint32_t k0, uint32_t k1, uint32_t w[4]) {
 #pragma unroll
     for (int r = 0; r < 7; ++r) {
-        const uint32_t h0 = __umulhi(c0, 0xD2511F53u), l0 = c0 * 0xD2511F53u;
-        const uint32_t h1 = __umulhi(c2, 0xCD9E8D57u), l1 = c2 * 0xCD9E8D57u;
-        c0 = h1 ^ c1 ^ k0;
-        c1 = l1;
-        c2 = h0 ^ c3 ^ k1;
-        c3 = l0;
+        const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
+        c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+        c1 = (uint32_t)p1;
+        c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+        c3 = (uint32_t)p0;
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
     }
@@ -176,148 +211,295 @@ __device__ __forceinline__ void e4m3_decode8(uint2 c, float o[8]) {
     }
 }
 
-// y (|y| < 256) to a value of e4m3, up when its 16 random bits say so: the
-// probability of the upper neighbour is y's place between the two, to 2^-16.
+// a >= 0 (< 256) to a value of e4m3, up when its 16 random bits say so: the
+// probability of the upper neighbour is a's place between the two, to 2^-16.
 // The equally spaced range below 2^-6 is shifted into the binade [2^-6, 2^-5),
 // whose spacing is the same 2^-9.  Adding to the bits below the kept mantissa
 // carries into it, and past it into the exponent, as rounding up does.
-__device__ __forceinline__ float e4m3_dither(float y, uint32_t random16) {
-    const float a = fabsf(y);
+__device__ __forceinline__ float e4m3_dither(float a, uint32_t random16) {
     const float off = a < 0.015625f ? 0.015625f : 0.0f;
     const uint32_t u = __float_as_uint(__fadd_rn(a, off)) + ((random16 << 4) | 8u);
-    return copysignf(__fsub_rn(__uint_as_float(u & 0xFFF00000u), off), y);
+    return __fsub_rn(__uint_as_float(u & 0xFFF00000u), off);
 }
 
 __device__ __forceinline__ bool finite_bits(float x) {
     return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
 }
 
-// The scale of a block's moment and the 8 codes of this lane.  All 32 lanes
-// call it.  ROOT: x >= 0, and a positive value never gets code 0 (it divides
-// the update).  Elements that are not finite become NaN codes and do not
-// count for the scale.
+// The e4m3 codes of 8 values x times inv (a power of two).  ROOT: x >= 0, and
+// a positive value never gets code 0 (it divides the update).
 template <bool ROOT, bool DITHER>
-__device__ __forceinline__ uint2 encode8(float x[8], const uint32_t random[8], float &scale) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    const bool odd = top >= 0x7F800000u;         // the same in every lane
-    if (odd) {
-        top = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (finite_bits(x[i])) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-    }
-    const uint32_t field = max(top >> 23, 8u);
-    scale = __uint_as_float((field - 7u) << 23);
-    const float inv = __uint_as_float((261u - field) << 23);
+__device__ __forceinline__ uint2 encode8(const float x[8], float inv, const uint32_t random[8]) {
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         y[i] = __fmul_rn(x[i], inv);
-        if (DITHER) y[i] = e4m3_dither(y[i], random[i]);
+        if (DITHER)
+            y[i] = ROOT ? e4m3_dither(y[i], random[i]) : copysignf(e4m3_dither(fabsf(y[i]), random[i]), y[i]);
         if (ROOT && x[i] > 0.0f) y[i] = fmaxf(y[i], 0.001953125f);
-        if (odd && !finite_bits(x[i])) y[i] = __uint_as_float(0x7FC00000u);
     }
     return make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16),
                       e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
 }
 
-// One warp takes a block at a time, 8 consecutive elements a lane.
-// 16 bytes an element with 16-bit gradients and a 16-bit copy.
+// A block's largest magnitude, as bits (a NaN's if there is one), from 8
+// values a lane.
+__device__ __forceinline__ uint32_t block_top(const float x[8]) {
+    float top = fabsf(x[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(x[i])));
+    return __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top) & 0x7FFFFFFFu);
+}
+
+__device__ __forceinline__ void random8(int64_t elem, int32_t tensor, const Adam8C &c, uint32_t lo[8], uint32_t hi[8]) {
+    const uint64_t q = (uint64_t)elem >> 2;
+    const uint32_t t = (uint32_t)tensor & 0x7FFFFFFFu;
+    uint32_t w[8];
+    philox7((uint32_t)q, (uint32_t)(q >> 32), t, c.step, c.k0, c.k1, w);
+    philox7((uint32_t)(q + 1), (uint32_t)((q + 1) >> 32), t, c.step, c.k0, c.k1, w + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        lo[i] = w[i] & 0xFFFFu;
+        hi[i] = w[i] >> 16;
+    }
+}
+
+// Pairs of floats: the paired instructions round each half as the scalar ones
+// do and issue once for two elements.  A paired sum of a paired product is
+// fused with it in spite of both .rn, which would round once where the update
+// rounds twice; so a sum is written as one operand times ONE, an argument that
+// the compiler does not know, plus the other.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 both(float x) { return f2pack(x, x); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b, const Adam8C &c) { return fma2(a, both(c.one), b); }
+__device__ __forceinline__ f2 sub2(f2 a, f2 b, const Adam8C &c) { return fma2(b, both(c.minus_one), a); }
+
+// 2^32 sqrt(v) of two, correctly rounded and without a branch, so that a
+// lane's roots overlap.  Markstein's correction of an approximate root s of
+// w = 2^64 v: the residual w - s s is exact in one fused operation, and
+// s + (w - s s) / (2 sqrt(w)) rounds as the root does.  2^64 keeps the
+// residual of the smallest v among the normal numbers.  Infinities and NaN
+// give NaN, and so does v >= 2^64.
+__device__ __forceinline__ f2 root_2_32(f2 v) {
+    const f2 w = mul2(v, both(18446744073709551616.0f));
+    float a, b;
+    f2unpack(w, a, b);
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(a) : "f"(fmaxf(a, 7.8886090522101181e-31f)));   // 2^-100: v = 0 gives 0
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(b) : "f"(fmaxf(b, 7.8886090522101181e-31f)));
+    const f2 y = f2pack(a, b), s = mul2(w, y);
+    const f2 minus = s ^ 0x8000000080000000ull;
+    return fma2(fma2(minus, s, w), mul2(both(0.5f), y), s);
+}
+
+// New moment and square of one element; g: the gradient times coef (and the
+// decay of Adam-L2), p: decayed (AdamW).
+__device__ __forceinline__ void adam8_moments(float &p, float &m, float &v, float g, float r, float sm, float sr,
+                                              float coef, const Adam8C &c) {
+    float gi = __fmul_rn(g, coef);
+    if (c.adamw)
+        p = __fsub_rn(p, __fmul_rn(c.lr_wd, p));
+    else
+        gi = __fadd_rn(gi, __fmul_rn(c.wd, p));
+    const float r0 = __fmul_rn(r, sr);
+    m = __fadd_rn(__fmul_rn(c.b1, __fmul_rn(m, sm)), __fmul_rn(c.omb1, gi));
+    v = __fadd_rn(__fmul_rn(c.b2, __fmul_rn(r0, r0)), __fmul_rn(c.omb2, __fmul_rn(gi, gi)));
+}
+
+// One block, any length and alignment, with moments that are not finite: such
+// an element becomes a NaN code and does not count for the scale.
 template <class G, bool DITHER>
-__global__ void __launch_bounds__(THREADS)
-tensors8_kernel(const ZsChunk *__restrict__ chunks, Adam8C c, const float *__restrict__ d_coef,
-                const int32_t *__restrict__ d_flags, bool fp16) {
-    if (d_flags && (*d_flags & ZS_SKIP_NONFINITE)) return;
-    const float coef = d_coef ? *d_coef : 1.0f;
-    const ZsChunk k = chunks[blockIdx.x];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __noinline__ void adam8_block(const ZsChunk *__restrict__ chunk, const Adam8C c, float coef, bool fp16, int b) {
+    const ZsChunk k = *chunk;
     uint8_t *cm = static_cast<uint8_t *>(k.m), *cv = static_cast<uint8_t *>(k.v);
     uint16_t *param = static_cast<uint16_t *>(k.param);
-    const bool aligned = k.tensor >= 0;
-    for (int b = warp; b * STATE_BLOCK < k.len; b += WARPS) {
-        const int x = b * STATE_BLOCK + 8 * lane;
-        const int n = min(8, k.len - x);         // of this lane, may be negative
-        const bool vec = aligned && n == 8;
-        float g[8], p[8], m[8], r[8];
-        uint2 qm = make_uint2(0, 0), qv = make_uint2(0, 0);
-        if (vec) {
-            G::load8(k.grad, x, g);
-            load8f(k.master + x, p);
-            qm = *reinterpret_cast<const uint2 *>(cm + x);
-            qv = *reinterpret_cast<const uint2 *>(cv + x);
-        } else {
+    const int lane = threadIdx.x & 31, x = b * STATE_BLOCK + 8 * lane;
+    const int n = min(8, k.len - x);             // of this lane, may be negative
+    float m[8], r[8];
+    const float sm = k.m_scale[b], sr = k.v_scale[b];
+    uint2 qm = make_uint2(0, 0), qr = make_uint2(0, 0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const bool in = i < n;
-                g[i] = in ? G::load1(k.grad, x + i) : 0.0f;
-                p[i] = in ? k.master[x + i] : 0.0f;
-                const uint32_t a = in ? cm[x + i] : 0u, d = in ? cv[x + i] : 0u;
-                if (i < 4) { qm.x |= a << (8 * i); qv.x |= d << (8 * i); }
-                else { qm.y |= a << (8 * i - 32); qv.y |= d << (8 * i - 32); }
-            }
-        }
-        const float sm = k.m_scale[b], sv = k.v_scale[b];
-        e4m3_decode8(qm, m);
-        e4m3_decode8(qv, r);
-        uint32_t lo[8], hi[8];
-        if (DITHER) {
-            const uint64_t q = (uint64_t)(k.elem + x) >> 2;
-            const uint32_t t = (uint32_t)k.tensor & 0x7FFFFFFFu;
-            uint32_t w[8];
-            philox7((uint32_t)q, (uint32_t)(q >> 32), t, c.step, c.k0, c.k1, w);
-            philox7((uint32_t)(q + 1), (uint32_t)((q + 1) >> 32), t, c.step, c.k0, c.k1, w + 4);
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t a = i < n ? cm[x + i] : 0u, d = i < n ? cv[x + i] : 0u;
+        if (i < 4) { qm.x |= a << (8 * i); qr.x |= d << (8 * i); }
+        else { qm.y |= a << (8 * i - 32); qr.y |= d << (8 * i - 32); }
+    }
+    e4m3_decode8(qm, m);
+    e4m3_decode8(qr, r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                lo[i] = w[i] & 0xFFFFu;
-                hi[i] = w[i] >> 16;
-            }
+    for (int i = 0; i < 8; ++i) {
+        if (i >= n) {
+            m[i] = r[i] = 0.0f;
+            continue;
         }
+        float p = k.master[x + i], v;
+        adam8_moments(p, m[i], v, G::load1(k.grad, x + i), r[i], sm, sr, coef, c);
+        r[i] = __fsqrt_rn(v);
+        const float den = __fadd_rn(__fmul_rn(r[i], c.root), c.eps);
+        p = __fsub_rn(p, __fmul_rn(c.step_size, __fdividef(m[i], den)));
+        k.master[x + i] = p;
+        if (param) param[x + i] = cast1(p, fp16);
+    }
+    bool bad_m[8], bad_r[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float gi = __fmul_rn(g[i], coef);
-            if (c.adamw)
-                p[i] = __fsub_rn(p[i], __fmul_rn(c.lr_wd, p[i]));
-            else
-                gi = __fadd_rn(gi, __fmul_rn(c.wd, p[i]));
-            const float r0 = __fmul_rn(r[i], sv);
-            m[i] = __fadd_rn(__fmul_rn(c.b1, __fmul_rn(m[i], sm)), __fmul_rn(c.omb1, gi));
-            r[i] = __fsqrt_rn(__fadd_rn(__fmul_rn(c.b2, __fmul_rn(r0, r0)),
-                                        __fmul_rn(c.omb2, __fmul_rn(gi, gi))));
-            const float den = __fadd_rn(__fmul_rn(r[i], c.root), c.eps);
-            p[i] = __fsub_rn(p[i], __fmul_rn(c.step_size, __fdiv_rn(m[i], den)));
-        }
-        float ns, nv;
-        if (n < 8) {   // past the end: nothing that the scales could see
+    for (int i = 0; i < 8; ++i) {
+        bad_m[i] = !finite_bits(m[i]);
+        bad_r[i] = !finite_bits(r[i]);
+        if (bad_m[i]) m[i] = 0.0f;
+        if (bad_r[i]) r[i] = 0.0f;
+    }
+    const uint32_t fm = max(block_top(m) >> 23, 8u), fr = max(block_top(r) >> 23, 8u);
+    uint32_t lo[8], hi[8];
+    if (DITHER) random8(k.elem + x, k.tensor, c, lo, hi);
+    qm = encode8<false, DITHER>(m, __uint_as_float((261u - fm) << 23), lo);
+    qr = encode8<true, DITHER>(r, __uint_as_float((261u - fr) << 23), hi);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i >= n) m[i] = r[i] = 0.0f;
-        }
-        qm = encode8<false, DITHER>(m, lo, ns);
-        qv = encode8<true, DITHER>(r, hi, nv);
-        if (vec) {
-            store8f(k.master + x, p);
-            *reinterpret_cast<uint2 *>(cm + x) = qm;
-            *reinterpret_cast<uint2 *>(cv + x) = qv;
-            if (param) *reinterpret_cast<uint4 *>(param + x) = cast8(p, fp16);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (i >= n) continue;
-                k.master[x + i] = p[i];
-                cm[x + i] = (uint8_t)((i < 4 ? qm.x : qm.y) >> (8 * (i & 3)));
-                cv[x + i] = (uint8_t)((i < 4 ? qv.x : qv.y) >> (8 * (i & 3)));
-                if (param) param[x + i] = cast1(p[i], fp16);
-            }
-        }
-        if (lane == 0) {
-            k.m_scale[b] = ns;
-            k.v_scale[b] = nv;
+    for (int i = 0; i < 8; ++i) {
+        if (i >= n) continue;
+        cm[x + i] = bad_m[i] ? 0x7F : (uint8_t)((i < 4 ? qm.x : qm.y) >> (8 * (i & 3)));
+        cv[x + i] = bad_r[i] ? 0x7F : (uint8_t)((i < 4 ? qr.x : qr.y) >> (8 * (i & 3)));
+    }
+    if (lane == 0) {
+        k.m_scale[b] = __uint_as_float((fm - 7u) << 23);
+        k.v_scale[b] = __uint_as_float((fr - 7u) << 23);
+    }
+}
+
+// Stages of a chunk in shared memory: GROUP blocks each, one a warp.
+constexpr int STAGES8 = CHUNK8 / STATE_BLOCK / WARPS;
+constexpr int STAGE_ELEMS = STATE_BLOCK * WARPS;
+template <class G>
+constexpr int SMEM8 = CHUNK8 * (G::SIZE + 4 + 1 + 1);
+constexpr uint64_t BULK_NS = 1000000000ull;      // one wait gives up after 1 s
+
+__device__ int g_tensors_wait_timeouts;          // waits that gave up
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :
+                 : "r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// A CTA has its whole chunk fetched by bulk copies at once, in stages of one
+// block a warp; a warp then takes its block of each stage as it lands, 8
+// consecutive elements a lane.  16 bytes an element with 16-bit gradients and
+// a 16-bit copy: at the copy bandwidth that leaves about 85 instructions an
+// element, so the arithmetic counts as much as the bytes, and the copies keep
+// memory busy while every warp of the SM computes.  The quotient m / den is
+// the quick one (its last two bits may be off: 2^-22 of one update, far below
+// a rounding of p); the root is exact, since codes hang on it.
+template <class G, bool DITHER>
+__global__ void __launch_bounds__(THREADS, 4)
+tensors8_kernel(const ZsChunk *__restrict__ chunks, Adam8C c, const float *__restrict__ d_coef,
+                const int32_t *__restrict__ d_flags, bool fp16) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[STAGES8];
+    const ZsChunk k = chunks[blockIdx.x];
+    const float coef = d_coef ? *d_coef : 1.0f;
+    if (d_flags && (*d_flags & ZS_SKIP_NONFINITE)) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int full = k.tensor >= 0 ? k.len / STATE_BLOCK : 0;    // blocks of the vector path
+    const uint32_t sg = smem_u32(smem), sp = sg + CHUNK8 * G::SIZE, sm = sp + CHUNK8 * 4, sr = sm + CHUNK8, bar = smem_u32(bars);
+    if (threadIdx.x == 0 && full > 0) {
+        for (int i = 0; i < STAGES8; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" : : "r"(bar + 8 * i) : "memory");
+        asm volatile("fence.proxy.async.shared::cta;" : : : "memory");
+        for (int i = 0, at = 0; at < full * STATE_BLOCK; ++i, at += STAGE_ELEMS) {
+            const uint32_t n = (uint32_t)min(STAGE_ELEMS, full * STATE_BLOCK - at);
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(bar + 8 * i), "r"(n * (G::SIZE + 6)) : "memory");
+            bulk_load(sg + at * G::SIZE, static_cast<const char *>(k.grad) + (int64_t)at * G::SIZE, n * G::SIZE, bar + 8 * i);
+            bulk_load(sp + at * 4, k.master + at, n * 4, bar + 8 * i);
+            bulk_load(sm + at, static_cast<const uint8_t *>(k.m) + at, n, bar + 8 * i);
+            bulk_load(sr + at, static_cast<const uint8_t *>(k.v) + at, n, bar + 8 * i);
         }
     }
+    // the warp's scales: block warp + 8 i in lane i
+    float hm = 0.0f, hr = 0.0f;
+    if (lane < STAGES8 && warp + WARPS * lane < full) {
+        hm = k.m_scale[warp + WARPS * lane];
+        hr = k.v_scale[warp + WARPS * lane];
+    }
+    __syncthreads();
+    for (int i = 0, b = warp; b * STATE_BLOCK < k.len; ++i, b += WARPS) {
+        if (b >= full) {
+            adam8_block<G, DITHER>(chunks + blockIdx.x, c, coef, fp16, b);
+            continue;
+        }
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_quick(bar + 8 * i, 0, BULK_NS))) {
+            if (lane == 0) atomicAdd(&g_tensors_wait_timeouts, 1);
+            continue;
+        }
+        const int x = b * STATE_BLOCK + 8 * lane;
+        float g[8], p[8], m[8], r[8];
+        G::shared8(sg + x * G::SIZE, g);
+        floats4(lds16(sp + 4 * x), p);
+        floats4(lds16(sp + 4 * x + 16), p + 4);
+        e4m3_decode8(lds8(sm + x), m);
+        e4m3_decode8(lds8(sr + x), r);
+        const float scale_m = __shfl_sync(0xFFFFFFFFu, hm, i), scale_r = __shfl_sync(0xFFFFFFFFu, hr, i);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            f2 g2 = mul2(f2pack(g[e], g[e + 1]), both(coef)), p2 = f2pack(p[e], p[e + 1]);
+            if (c.adamw)
+                p2 = sub2(p2, mul2(both(c.lr_wd), p2), c);
+            else
+                g2 = add2(g2, mul2(both(c.wd), p2), c);
+            const f2 m0 = mul2(f2pack(m[e], m[e + 1]), both(scale_m)), r0 = mul2(f2pack(r[e], r[e + 1]), both(scale_r));
+            const f2 v2 = add2(mul2(both(c.b2), mul2(r0, r0)), mul2(both(c.omb2), mul2(g2, g2)), c);
+            f2unpack(p2, p[e], p[e + 1]);
+            f2unpack(add2(mul2(both(c.b1), m0), mul2(both(c.omb1), g2), c), m[e], m[e + 1]);
+            f2unpack(root_2_32(v2), r[e], r[e + 1]);
+        }
+        const uint32_t tm = block_top(m), tr = block_top(r);
+        if (max(tm, tr) >= 0x7F800000u) {         // the same in all lanes; nothing is written yet
+            adam8_block<G, DITHER>(chunks + blockIdx.x, c, coef, fp16, b);
+            continue;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            float a, b;
+            f2unpack(add2(mul2(f2pack(r[e], r[e + 1]), both(c.root_2_32)), both(c.eps), c), a, b);
+            const f2 q = f2pack(__fdividef(m[e], a), __fdividef(m[e + 1], b));
+            f2unpack(sub2(f2pack(p[e], p[e + 1]), mul2(both(c.step_size), q), c), p[e], p[e + 1]);
+        }
+        store8f(k.master + x, p);
+        if (k.param) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(k.param) + x) = cast8(p, fp16);
+        const uint32_t fm = max(tm >> 23, 8u), fr = (uint32_t)max((int)(tr >> 23) - 32, 8);
+        uint32_t lo[8], hi[8];
+        if (DITHER) random8(k.elem + x, k.tensor, c, lo, hi);
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(k.m) + x) = encode8<false, DITHER>(m, __uint_as_float((261u - fm) << 23), lo);
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(k.v) + x) = encode8<true, DITHER>(r, __uint_as_float((229u - fr) << 23), hi);   // 2^-32 of the root's factor
+        if (lane == 0) {
+            k.m_scale[b] = __uint_as_float((fm - 7u) << 23);
+            k.v_scale[b] = __uint_as_float((fr - 7u) << 23);
+        }
+    }
+}
+
+template <class G, bool DITHER>
+static cudaError_t launch8(const zs_tensors *L, const Adam8C &c, const float *d_coef, const int32_t *d_flags, bool fp16,
+                           cudaStream_t s) {
+    static std::atomic<bool> set[64];            // the kernel's shared memory, per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!set[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(tensors8_kernel<G, DITHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM8<G>);
+        if (e != cudaSuccess) return e;
+        set[dev].store(true, std::memory_order_relaxed);
+    }
+    tensors8_kernel<G, DITHER><<<(unsigned)L->chunks.size(), THREADS, SMEM8<G>, s>>>(L->d_chunks, c, d_coef, d_flags, fp16);
+    return cudaGetLastError();
 }
 
 template <class G>
@@ -330,15 +512,21 @@ static cudaError_t launch(const zs_tensors *L, const ZsAdamScalars &a, const Ada
         c.lr = a.lr; c.b1 = a.b1; c.b2 = a.b2; c.omb1 = a.omb1; c.omb2 = a.omb2; c.eps = a.eps;
         c.wd = a.wd; c.lr_wd = a.lr_wd; c.bc1 = a.bc1; c.bc2 = a.bc2; c.adamw = a.adamw;
         tensors32_kernel<G><<<grid, THREADS, 0, s>>>(L->d_chunks, c, d_coef, d_flags, fp16);
-    } else if (dither) {
-        tensors8_kernel<G, true><<<grid, THREADS, 0, s>>>(L->d_chunks, c8, d_coef, d_flags, fp16);
-    } else {
-        tensors8_kernel<G, false><<<grid, THREADS, 0, s>>>(L->d_chunks, c8, d_coef, d_flags, fp16);
+        return cudaGetLastError();
     }
-    return cudaGetLastError();
+    return dither ? launch8<G, true>(L, c8, d_coef, d_flags, fp16, s) : launch8<G, false>(L, c8, d_coef, d_flags, fp16, s);
 }
 
 }  // namespace zsk
+
+cudaError_t zsl_tensors_wait_timeouts(int *count, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(count, zsk::g_tensors_wait_timeouts, sizeof(int));
+    if (e == cudaSuccess && reset) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(zsk::g_tensors_wait_timeouts, &zero, sizeof(int));
+    }
+    return e;
+}
 
 namespace {
 
@@ -364,7 +552,9 @@ zs_status zs_build_tensors(const zs_tensors_config *cfg, int32_t n, const zs_ten
     if (cfg->reserved != 0) return zs_fail(ZS_EINVAL, "%s: reserved must be 0", fn);
     const bool eight = cfg->state_bits == 8;
     const int gsize = dtype_size(cfg->grad_dtype);
-    int64_t chunks = 0;
+    int64_t chunks = 0, numel = 0;
+    for (int32_t i = 0; i < n && numel < SHORT_ELEMS; ++i) numel += t[i].numel > 0 && t[i].numel < SHORT_ELEMS ? t[i].numel : t[i].numel > 0 ? SHORT_ELEMS : 0;
+    const int64_t chunk = numel < SHORT_ELEMS ? CHUNK_SHORT : eight ? CHUNK8 : CHUNK32;
     for (int32_t i = 0; i < n; ++i) {
         const zs_tensor &x = t[i];
         if (x.numel < 0) return zs_fail(ZS_EINVAL, "%s: tensor %d: numel %lld < 0", fn, i, (long long)x.numel);
@@ -382,9 +572,9 @@ zs_status zs_build_tensors(const zs_tensors_config *cfg, int32_t n, const zs_ten
             if (it.used && (!it.p || addr(it.p) % it.size))
                 return zs_fail(ZS_EINVAL, "%s: tensor %d: %s NULL or not aligned to its elements", fn, i, it.name);
         if (x.numel > (int64_t)1 << 48) return zs_fail(ZS_EINVAL, "%s: tensor %d: numel too large", fn, i);
-        chunks += (x.numel + CHUNK - 1) / CHUNK;
+        chunks += (x.numel + chunk - 1) / chunk;
     }
-    if (chunks > 0x7FFFFFFF) return zs_fail(ZS_EINVAL, "%s: more than 2^31 chunks of %d elements", fn, CHUNK);
+    if (chunks > 0x7FFFFFFF) return zs_fail(ZS_EINVAL, "%s: more than 2^31 chunks of %d elements", fn, (int)chunk);
     zs_tensors *L = new (std::nothrow) zs_tensors;
     if (!L) return zs_fail(ZS_ENOMEM, "%s: out of host memory", fn);
     L->cfg = *cfg;
@@ -397,12 +587,11 @@ zs_status zs_build_tensors(const zs_tensors_config *cfg, int32_t n, const zs_ten
     }
     for (int32_t i = 0; i < n; ++i) {
         const zs_tensor &x = t[i];
-        const uintptr_t state = eight ? 8 : 16;
         const bool aligned = addr(x.grad) % 16 == 0 && addr(x.param) % 16 == 0 && addr(x.master) % 16 == 0 &&
-                             addr(x.exp_avg) % state == 0 && addr(x.exp_avg_sq) % state == 0;
+                             addr(x.exp_avg) % 16 == 0 && addr(x.exp_avg_sq) % 16 == 0;
         L->numel += x.numel;
         L->blocks += (x.numel + STATE_BLOCK - 1) / STATE_BLOCK;
-        for (int64_t e = 0; e < x.numel; e += CHUNK) {
+        for (int64_t e = 0; e < x.numel; e += chunk) {
             const int64_t w = eight ? 1 : 4;
             ZsChunk k;
             k.grad = static_cast<const char *>(x.grad) + e * gsize;
@@ -413,7 +602,7 @@ zs_status zs_build_tensors(const zs_tensors_config *cfg, int32_t n, const zs_ten
             k.m_scale = eight ? x.exp_avg_scale + e / STATE_BLOCK : nullptr;
             k.v_scale = eight ? x.exp_avg_sq_scale + e / STATE_BLOCK : nullptr;
             k.elem = e;
-            k.len = (int32_t)(x.numel - e < CHUNK ? x.numel - e : CHUNK);
+            k.len = (int32_t)(x.numel - e < chunk ? x.numel - e : chunk);
             k.tensor = aligned ? i : (int32_t)((uint32_t)i | 0x80000000u);
             L->chunks.push_back(k);
         }
@@ -475,7 +664,8 @@ zs_status zs_adam_tensors(const zs_tensors *L, const zs_adam_hparams *hp, int64_
     if (!L->d_chunks) return zs_fail(ZS_ESTATE, "%s: list not uploaded (call zs_tensors_upload first)", fn);
     zsk::Adam8C c;
     c.b1 = a.b1; c.b2 = a.b2; c.omb1 = a.omb1; c.omb2 = a.omb2; c.eps = a.eps;
-    c.wd = a.wd; c.lr_wd = a.lr_wd; c.step_size = a.step_size; c.root = a.root; c.adamw = a.adamw;
+    c.wd = a.wd; c.lr_wd = a.lr_wd; c.step_size = a.step_size; c.root = a.root; c.root_2_32 = a.root * 0x1p-32f;
+    c.one = 1.0f; c.minus_one = -1.0f; c.adamw = a.adamw;
     c.k0 = (uint32_t)seed;
     c.k1 = (uint32_t)(seed >> 32);
     c.step = (uint32_t)step;
