@@ -276,11 +276,14 @@ extern "C" {
 
 zs_status zs_device_wait_timeouts(int32_t *count, int32_t reset) {
     if (!count) return zs_fail(ZS_EINVAL, "zs_device_wait_timeouts: NULL count");
-    int c = 0, mx4 = 0, tensors = 0;
-    cudaError_t e = zsl_bulk_wait_timeouts(&c, reset != 0);
-    if (e == cudaSuccess) e = zsl_mx4_wait_timeouts(&mx4, reset != 0);
-    if (e == cudaSuccess) e = zsl_tensors_wait_timeouts(&tensors, reset != 0);
-    c += mx4 + tensors;
+    int c = 0;
+    cudaError_t e = cudaSuccess;
+    for (auto counter : {zsl_bulk_wait_timeouts, zsl_mx4_wait_timeouts, zsl_quantize_wait_timeouts,
+                         zsl_tensors_wait_timeouts}) {
+        int one = 0;
+        if (e == cudaSuccess) e = counter(&one, reset != 0);
+        c += one;
+    }
     if (e != cudaSuccess) return cuda_status(e, "zs_device_wait_timeouts");
     *count = c;
     if (c != 0)

@@ -80,6 +80,8 @@ cudaError_t zsl_gather(const ZsGatherArgs &a, const uint16_t *shards, uint16_t *
 cudaError_t zsl_bulk_wait_timeouts(int *count, bool reset);
 // One bounded wait on an mbarrier nothing arrives on (gives up after limit_ns).
 cudaError_t zsl_wait_timeout_test(int64_t limit_ns, cudaStream_t s);
-// The same of the 4-bit product and of the step over a list of tensors.
+// The same of the 4-bit product and quantiser and of the step over a list of
+// tensors.
 cudaError_t zsl_mx4_wait_timeouts(int *count, bool reset);
+cudaError_t zsl_quantize_wait_timeouts(int *count, bool reset);
 cudaError_t zsl_tensors_wait_timeouts(int *count, bool reset);

@@ -53,6 +53,37 @@ struct Row8 {
     }
 };
 
+// m = the larger magnitudes of two pairs of 16-bit values; a NaN stays
+template <class T>
+__device__ __forceinline__ void max_abs2(uint32_t &m, uint32_t w);
+template <>
+__device__ __forceinline__ void max_abs2<BF16T>(uint32_t &m, uint32_t w) {
+    asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %1;\n\tmax.NaN.bf16x2 %0, %0, a;\n\t}" : "+r"(m) : "r"(w));
+}
+template <>
+__device__ __forceinline__ void max_abs2<FP16T>(uint32_t &m, uint32_t w) {
+    asm("{\n\t.reg .b32 a;\n\tabs.f16x2 a, %1;\n\tmax.NaN.f16x2 %0, %0, a;\n\t}" : "+r"(m) : "r"(w));
+}
+
+// codes of 8 values times 2^(127 - byte)
+__device__ __forceinline__ uint32_t encode_floats(float y[8], unsigned long long inv) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        unsigned long long two = f2pack(y[i], y[i + 1]);
+        asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(two) : "l"(inv));
+        f2unpack(two, y[i], y[i + 1]);
+    }
+    return e2m1x8(y);
+}
+template <class T>
+__device__ __forceinline__ uint32_t encode_words(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, unsigned long long inv) {
+    float y[8];
+    const uint32_t w[4] = {w0, w1, w2, w3};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = T::to_f32(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu);
+    return encode_floats(y, inv);
+}
+
 // codes of 8 values of a group whose scale byte is known
 __device__ __forceinline__ uint32_t mx4_encode8(const float y[8], uint32_t byte) {
     if (byte == 255u) return 0u;
@@ -157,41 +188,194 @@ mx4_quantize_kernel(Mx4Args a) {
             reinterpret_cast<const uint4 *>(cs)[t - 32];
 }
 
-// 8 elements a thread: 4 bytes of codes to 16 or 32 bytes of values
+// 16-bit matrices whose rows are 16-byte aligned: a persistent CTA walks tiles,
+// fetched ahead by tensor copies (two boxes of 64 columns, 128-byte swizzle;
+// zeros outside the matrix) into a ring of stages, and makes both forms from
+// shared memory.  Along the rows 4 lanes share a group, 8 elements each; along
+// the columns a thread takes 32 rows of two neighbouring columns; neither
+// access has a bank conflict under the swizzle.  Bandwidth bounds it: 2 bytes
+// read and 0.53 written an element and form.
+// Both forms at once take 16 warps, 8 for each, on two CTAs an SM; one form 8
+// on three.
+constexpr int QS_BOX = 64 * 128 * 2, QS_STAGE = 2 * QS_BOX;
+template <bool BOTH>
+struct QsShape {
+    static constexpr int THREADS = BOTH ? 512 : 256, CTAS = BOTH ? 2 : 3, STAGES = BOTH ? 3 : 2;
+    static constexpr int SMEM = STAGES * QS_STAGE + 1024;
+};
+constexpr uint64_t QS_WAIT_NS = 1000000000ull;       // one wait gives up after 1 s
+
+__device__ int g_quantize_wait_timeouts;             // waits that gave up
+
+template <class T, bool ROWS, bool COLS>
+__global__ void __launch_bounds__(QsShape<ROWS && COLS>::THREADS, QsShape<ROWS && COLS>::CTAS)
+mx4_quantize_tiles_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, int tiles) {
+    constexpr int QS_STAGES = QsShape<ROWS && COLS>::STAGES;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(16) uint8_t rs[2][MX4_ATOM], cs[2][MX4_ATOM];
+    __shared__ __align__(8) uint64_t bars[QS_STAGES];
+    const int t = threadIdx.x & 255;
+    const bool do_rows = ROWS && (!COLS || threadIdx.x < 256), do_cols = COLS && (!ROWS || threadIdx.x >= 256);
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u, bar = smem_u32(bars);
+    const int tiles_c = (int)a.tiles_c;
+    auto fetch = [&](int i) {                        // the i-th tile of this CTA
+        const int tile = (int)blockIdx.x + i * (int)gridDim.x, s = i % QS_STAGES;
+        const int rt = tile / tiles_c, ct = tile - rt * tiles_c;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(bar + 8 * s), "r"(QS_STAGE) : "memory");
+        tma2d(base + s * QS_STAGE, &map, ct * QT, rt * QT, bar + 8 * s);
+        tma2d(base + s * QS_STAGE + QS_BOX, &map, ct * QT + 64, rt * QT, bar + 8 * s);
+    };
+    const int mine = ((int)(tiles - blockIdx.x) + (int)gridDim.x - 1) / (int)gridDim.x;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < QS_STAGES; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" : : "r"(bar + 8 * i) : "memory");
+        asm volatile("fence.proxy.async.shared::cta;" : : : "memory");
+        for (int i = 0; i < QS_STAGES && i < mine; ++i) fetch(i);
+    }
+    __syncthreads();
+    const int64_t r_bytes = mx4_row_bytes(a.cols), c_bytes = mx4_row_bytes(a.rows);
+    const int64_t r_atoms = mx4_atoms(a.cols), c_atoms = mx4_atoms(a.rows);
+    for (int i = 0; i < mine; ++i) {
+        const int tile = (int)blockIdx.x + i * (int)gridDim.x, s = i % QS_STAGES;
+        const int64_t rt = tile / tiles_c, ct = tile - rt * tiles_c;
+        const int64_t row0 = rt * QT, col0 = ct * QT;
+        const uint32_t at = base + s * QS_STAGE;
+        if (!__syncthreads_and(mbar_wait_quick(bar + 8 * s, (uint32_t)((i / QS_STAGES) & 1), QS_WAIT_NS))) {
+            // give up, once the copies in flight have landed
+            if (threadIdx.x == 0) {
+                atomicAdd(&g_quantize_wait_timeouts, 1);
+                for (int j = i; j < i + QS_STAGES && j < mine; ++j)
+                    mbar_wait_quick(bar + 8 * (j % QS_STAGES), (uint32_t)((j / QS_STAGES) & 1), QS_WAIT_NS);
+            }
+            __syncthreads();
+            return;
+        }
+        if (do_rows) {
+            // a thread takes a group: 4 lanes a row, 8 rows a warp.  The second
+            // box's pieces are read two apart in turn, so that 8 lanes meet 8
+            // different pieces of the banks.
+            const int g = t & 3, box = g >> 1;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = 64 * j + (t >> 2);
+                uint32_t w[16], two = 0;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const int piece = 4 * (g & 1) + (h ^ (2 * box));
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[4 * h]), "=r"(w[4 * h + 1]), "=r"(w[4 * h + 2]), "=r"(w[4 * h + 3])
+                                 : "r"(at + box * QS_BOX + 128 * r + 16 * (piece ^ (r & 7))));
+                }
+#pragma unroll
+                for (int h = 0; h < 16; ++h) max_abs2<T>(two, w[h]);
+                const uint32_t byte = mx4_scale_byte(__float_as_uint(T::to_f32(max(two & 0xFFFFu, two >> 16))) >> 23);
+                const float inv = byte == 255u ? 0.0f : mx4_inverse(byte);
+                uint32_t q[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    q[h] = byte == 255u ? 0u : encode_words<T>(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3], f2pack(inv, inv));
+                rs[i & 1][mx4_in_atom(r, g)] = (uint8_t)byte;
+                if (row0 + r < a.rows && col0 / 2 + 16 * g < r_bytes)
+                    *reinterpret_cast<uint4 *>(a.r_codes + (row0 + r) * r_bytes + col0 / 2 + 16 * g) =
+                        box ? make_uint4(q[2], q[3], q[0], q[1]) : make_uint4(q[0], q[1], q[2], q[3]);
+            }
+        }
+        if (do_cols) {
+            // a thread takes 32 rows of two columns; lanes 16 on the same
+            // columns' next 32, so that a warp's stores fill sectors.  They
+            // read rows 4 apart in turn: other pieces of the banks.
+            const int upper = (t >> 4) & 1, g = 2 * (t >> 7) + upper;
+            const int box = (t >> 5) & 1, word = 16 * ((t >> 6) & 1) + (t & 15), c = 64 * box + 2 * word;
+            uint32_t w[32], two = 0;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const int r = e ^ (4 * upper);
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[e]) : "r"(at + box * QS_BOX + 4096 * g + 128 * r + 16 * ((word >> 2) ^ (r & 7)) + 4 * (word & 3)));
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) max_abs2<T>(two, w[e]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t byte = mx4_scale_byte(__float_as_uint(T::to_f32(j ? two >> 16 : two & 0xFFFFu)) >> 23);
+                const float inv = byte == 255u ? 0.0f : mx4_inverse(byte);
+                cs[i & 1][mx4_in_atom(c + j, g)] = (uint8_t)byte;
+                uint32_t q[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    float y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = T::to_f32(j ? w[8 * h + e] >> 16 : w[8 * h + e] & 0xFFFFu);
+                    const uint32_t x = byte == 255u ? 0u : encode_floats(y, f2pack(inv, inv));
+                    q[h] = upper ? __funnelshift_l(x, x, 16) : x;
+                }
+                if (col0 + c + j < a.cols && row0 / 2 + 16 * g < c_bytes)
+                    *reinterpret_cast<uint4 *>(a.c_codes + (col0 + c + j) * c_bytes + row0 / 2 + 16 * g) = make_uint4(q[0], q[1], q[2], q[3]);
+            }
+        }
+        __syncthreads();                             // the stage is read, the scales are in rs and cs
+        if (threadIdx.x == 0 && i + QS_STAGES < mine) fetch(i + QS_STAGES);
+        if (do_rows && t >= 32 && t < 64 && rt < mx4_row_tiles(a.rows))
+            reinterpret_cast<uint4 *>(a.r_scales + (rt * r_atoms + ct) * MX4_ATOM)[t - 32] = reinterpret_cast<const uint4 *>(rs[i & 1])[t - 32];
+        if (do_cols && t >= 64 && t < 96 && ct < mx4_row_tiles(a.cols))
+            reinterpret_cast<uint4 *>(a.c_scales + (ct * c_atoms + rt) * MX4_ATOM)[t - 64] = reinterpret_cast<const uint4 *>(cs[i & 1])[t - 64];
+    }
+}
+
+// 32 bytes of values a thread (8 or 16 elements), in 4 rows at a time, so
+// that loads overlap and a warp stores whole lines.  Bandwidth bounds it.
+constexpr int DQ_ROWS = 4;
+__host__ __device__ constexpr int dq_cols(bool f32) { return (f32 ? 8 : 16) * 256; }
 template <class T, bool F32, bool VEC>
 __global__ void __launch_bounds__(256)
 mx4_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
-                      int64_t rows, int64_t cols, void *__restrict__ out, int64_t ldo) {
-    const int64_t row_bytes = mx4_row_bytes(cols), per = row_bytes / 4, atoms = mx4_atoms(cols);
-    const int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (u >= rows * per) return;
-    const int64_t row = u / per, c = 8 * (u - row * per), g = c / MX4_GROUP;
-    const uint32_t q = __ldg(reinterpret_cast<const uint32_t *>(codes) + u);
-    const float s = mx4_scale(__ldg(scales + ((row >> 7) * atoms + (g >> 2)) * MX4_ATOM + mx4_in_atom((int)(row & 127), (int)(g & 3))));
-    float y[8];
-    e2m1_decode8(q, y);
+                      int64_t rows, int64_t cols, void *__restrict__ out, int64_t ldo, uint32_t tiles_c) {
+    constexpr int E = F32 ? 8 : 16;
+    const int64_t row_bytes = mx4_row_bytes(cols), atoms = mx4_atoms(cols);
+    const uint32_t rt = blockIdx.x / tiles_c, ct = blockIdx.x - rt * tiles_c;
+    const int64_t row0 = (int64_t)rt * DQ_ROWS, c = (int64_t)ct * dq_cols(F32) + E * (int)threadIdx.x;
+    if (c >= cols) return;
+    const int64_t g = c / MX4_GROUP;
+    const int n = (int)min((int64_t)E, cols - c);
+    uint2 q[DQ_ROWS];
+    uint32_t byte[DQ_ROWS];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(y[i], s);
-    const int n = (int)min((int64_t)8, cols - c);
-    if (F32) {
-        float *o = static_cast<float *>(out) + row * ldo + c;
-        if (VEC && n == 8) {
-            reinterpret_cast<float4 *>(o)[0] = make_float4(y[0], y[1], y[2], y[3]);
-            reinterpret_cast<float4 *>(o)[1] = make_float4(y[4], y[5], y[6], y[7]);
+    for (int i = 0; i < DQ_ROWS; ++i) {
+        const int64_t row = row0 + i;
+        if (row >= rows) continue;
+        if (F32) q[i].x = __ldg(reinterpret_cast<const uint32_t *>(codes + row * row_bytes + c / 2));
+        else q[i] = __ldg(reinterpret_cast<const uint2 *>(codes + row * row_bytes + c / 2));
+        byte[i] = __ldg(scales + ((row >> 7) * atoms + (g >> 2)) * MX4_ATOM + mx4_in_atom((int)(row & 127), (int)(g & 3)));
+    }
+#pragma unroll
+    for (int i = 0; i < DQ_ROWS; ++i) {
+        const int64_t row = row0 + i;
+        if (row >= rows) continue;
+        const float s = mx4_scale(byte[i]);
+        float y[E];
+        e2m1_decode8(q[i].x, y);
+        if (!F32) e2m1_decode8(q[i].y, y + E - 8);
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = __fmul_rn(y[e], s);
+        if (F32) {
+            float *o = static_cast<float *>(out) + row * ldo + c;
+            if (VEC && n == E) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) reinterpret_cast<float4 *>(o)[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) if (e < n) o[e] = y[e];
+            }
         } else {
+            uint16_t *o = static_cast<uint16_t *>(out) + row * ldo + c;
+            uint32_t r[E];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) if (i < n) o[i] = y[i];
-        }
-    } else {
-        uint16_t *o = static_cast<uint16_t *>(out) + row * ldo + c;
-        uint32_t r[8];
+            for (int e = 0; e < E; ++e) r[e] = T::from_f32(y[e]);
+            if (VEC && n == E) {
+                reinterpret_cast<uint4 *>(o)[0] = pack8(r);
+                reinterpret_cast<uint4 *>(o)[1] = pack8(r + E - 8);
+            } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = T::from_f32(y[i]);
-        if (VEC && n == 8) {
-            *reinterpret_cast<uint4 *>(o) = pack8(r);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) if (i < n) o[i] = (uint16_t)r[i];
+                for (int e = 0; e < E; ++e) if (e < n) o[e] = (uint16_t)r[e];
+            }
         }
     }
 }
@@ -213,6 +397,42 @@ static cudaError_t quantize_launch(const Mx4Args &a, int64_t grid, cudaStream_t 
     return cudaGetLastError();
 }
 
+template <class T, bool ROWS, bool COLS>
+static cudaError_t tiles_launch(const Mx4Args &a, int64_t tiles, cudaStream_t s) {
+    using S = QsShape<ROWS && COLS>;
+    static std::atomic<int> known[64];           // SMs, once the kernel's shared memory is set
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int sms = known[dev].load(std::memory_order_relaxed);
+    if (sms <= 0) {
+        e = cudaFuncSetAttribute(mx4_quantize_tiles_kernel<T, ROWS, COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        known[dev].store(sms, std::memory_order_relaxed);
+    }
+    const EncodeTiled f = encode_tiled();
+    if (!f) return cudaErrorNotSupported;
+    CUtensorMap map;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.cols, (cuuint64_t)a.rows}, strides[1] = {(cuuint64_t)a.ld * 2};
+    const cuuint32_t boxes[2] = {64, 128}, ones[2] = {1, 1};
+    if (f(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(a.x), dims, strides, boxes, ones,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    const int64_t wave = S::CTAS * (int64_t)sms, grid = tiles < wave ? tiles : wave;
+    mx4_quantize_tiles_kernel<T, ROWS, COLS><<<(unsigned)grid, S::THREADS, S::SMEM, s>>>(map, a, (int)tiles);
+    return cudaGetLastError();
+}
+
+template <class T>
+static cudaError_t tiles_ways(const Mx4Args &a, int64_t tiles, cudaStream_t s) {
+    if (a.r_codes && a.c_codes) return tiles_launch<T, true, true>(a, tiles, s);
+    if (a.r_codes) return tiles_launch<T, true, false>(a, tiles, s);
+    return tiles_launch<T, false, true>(a, tiles, s);
+}
+
 template <class T, bool F32, bool VEC>
 static cudaError_t quantize_ways(const Mx4Args &a, int64_t grid, cudaStream_t s) {
     if (a.r_codes && a.c_codes) return quantize_launch<T, F32, VEC, true, true>(a, grid, s);
@@ -221,6 +441,15 @@ static cudaError_t quantize_ways(const Mx4Args &a, int64_t grid, cudaStream_t s)
 }
 
 }  // namespace zsk
+
+cudaError_t zsl_quantize_wait_timeouts(int *count, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(count, zsk::g_quantize_wait_timeouts, sizeof(int));
+    if (e == cudaSuccess && reset) {
+        const int zero = 0;
+        e = cudaMemcpyToSymbol(zsk::g_quantize_wait_timeouts, &zero, sizeof(int));
+    }
+    return e;
+}
 
 namespace {
 
@@ -299,8 +528,8 @@ zs_status zs_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld,
     using namespace zsk;
     cudaError_t e;
     if (dtype == ZS_DTYPE_FP32) e = vec ? quantize_ways<F32X, true, true>(a, grid, s) : quantize_ways<F32X, true, false>(a, grid, s);
-    else if (dtype == ZS_DTYPE_FP16) e = vec ? quantize_ways<FP16T, false, true>(a, grid, s) : quantize_ways<FP16T, false, false>(a, grid, s);
-    else e = vec ? quantize_ways<BF16T, false, true>(a, grid, s) : quantize_ways<BF16T, false, false>(a, grid, s);
+    else if (dtype == ZS_DTYPE_FP16) e = vec ? tiles_ways<FP16T>(a, grid, s) : quantize_ways<FP16T, false, false>(a, grid, s);
+    else e = vec ? tiles_ways<BF16T>(a, grid, s) : quantize_ways<BF16T, false, false>(a, grid, s);
     return cuda_status(e, fn);
 }
 
@@ -314,7 +543,7 @@ zs_status zs_mx4_dequantize(const void *codes, const void *scales, int64_t rows,
         zs_clear_error();
         return ZS_OK;
     }
-    const int64_t units = rows * (mx4_row_bytes(cols) / 4), grid = (units + 255) / 256;
+    const int64_t span = zsk::dq_cols(dtype == ZS_DTYPE_FP32), tiles_c = (cols + span - 1) / span, grid = tiles_c * ((rows + zsk::DQ_ROWS - 1) / zsk::DQ_ROWS);
     if (grid > 0x7FFFFFFF) return zs_fail(ZS_EINVAL, "%s: %lld x %lld too large", fn, (long long)rows, (long long)cols);
     const cudaStream_t s = (cudaStream_t)stream;
     const bool vec = (addr(out) & 15) == 0 && ldo % (dtype == ZS_DTYPE_FP32 ? 4 : 8) == 0;
@@ -322,14 +551,14 @@ zs_status zs_mx4_dequantize(const void *codes, const void *scales, int64_t rows,
     using namespace zsk;
     const dim3 g((unsigned)grid), b(256);
     if (dtype == ZS_DTYPE_FP32) {
-        if (vec) mx4_dequantize_kernel<F32X, true, true><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo);
-        else mx4_dequantize_kernel<F32X, true, false><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo);
+        if (vec) mx4_dequantize_kernel<F32X, true, true><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo, (uint32_t)tiles_c);
+        else mx4_dequantize_kernel<F32X, true, false><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo, (uint32_t)tiles_c);
     } else if (dtype == ZS_DTYPE_FP16) {
-        if (vec) mx4_dequantize_kernel<FP16T, false, true><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo);
-        else mx4_dequantize_kernel<FP16T, false, false><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo);
+        if (vec) mx4_dequantize_kernel<FP16T, false, true><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo, (uint32_t)tiles_c);
+        else mx4_dequantize_kernel<FP16T, false, false><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo, (uint32_t)tiles_c);
     } else {
-        if (vec) mx4_dequantize_kernel<BF16T, false, true><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo);
-        else mx4_dequantize_kernel<BF16T, false, false><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo);
+        if (vec) mx4_dequantize_kernel<BF16T, false, true><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo, (uint32_t)tiles_c);
+        else mx4_dequantize_kernel<BF16T, false, false><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo, (uint32_t)tiles_c);
     }
     return cuda_status(cudaGetLastError(), fn);
 }

@@ -2,6 +2,10 @@
 // and the product.
 #pragma once
 
+#include <cuda.h>
+
+#include <atomic>
+
 #include "zs_device.cuh"
 
 constexpr int MX4_GROUP = 32;          // elements that share a scale
@@ -67,6 +71,49 @@ __device__ __forceinline__ void e2m1_decode8(uint32_t codes, float o[8]) {
         o[2 * j] = f.x;
         o[2 * j + 1] = f.y;
     }
+}
+
+// One wait of a whole warp: the same answer in all lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_quick(bar, parity, limit_ns));
+}
+
+// True in one lane of a converged warp.  The warps that issue loads and
+// products run their loops with all lanes and elect one for the issue: under
+// `if (lane == 0)` around the whole loop the compiler cannot know that the
+// operands are uniform and serialises each instruction, which took 858
+// cycles for a stage of products that elected take 512, the tensor cores' own
+// rate (2 x 128 x 256 x 256, operands already in shared memory).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+__device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        :
+        : "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// cuTensorMapEncodeTiled, through the runtime (no link against the driver).
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiled encode_tiled() {
+    static std::atomic<void *> fn{nullptr};
+    void *p = fn.load(std::memory_order_relaxed);
+    if (!p) {
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn.store(p, std::memory_order_relaxed);
+    }
+    return reinterpret_cast<EncodeTiled>(p);
 }
 
 }  // namespace zsk

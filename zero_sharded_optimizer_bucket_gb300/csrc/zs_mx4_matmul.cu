@@ -6,8 +6,6 @@
 // 256 elements of k: 128 bytes a row, one 128-byte swizzled TMA box an
 // operand, and two scale atoms a 128 rows, which tcgen05.cp moves to tensor
 // memory.  A warp loads, one thread issues the products, four warps store.
-#include <cuda.h>
-
 #include <atomic>
 
 #include "zs_launch.h"
@@ -51,23 +49,6 @@ struct MmArgs {
     int32_t vec;              // rows of out are aligned to 4 elements
 };
 
-// One wait of a whole warp: the same answer in all lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_quick(bar, parity, limit_ns));
-}
-
-// True in one lane of a converged warp.  The warps that issue loads and
-// products run their loops with all lanes and elect one for the issue: under
-// `if (lane == 0)` around the whole loop the compiler cannot know that the
-// operands are uniform and serialises each instruction, which took 858
-// cycles for a stage of products that elected take 512, the tensor cores' own
-// rate (2 x 128 x 256 x 256, operands already in shared memory).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 __device__ __forceinline__ uint64_t mm_desc(uint32_t addr, uint32_t sbo, uint64_t layout) {
     // shared-memory operand: start address, leading and stride byte offsets
     // (16-byte units), version 1, swizzle
@@ -79,14 +60,6 @@ __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
-}
-
-__device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-        :
-        : "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
-        : "memory");
 }
 
 __device__ __forceinline__ void bulk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -596,23 +569,6 @@ __global__ void mx4_zero_kernel(void *out, int64_t m, int64_t n, int64_t ldo, in
         if (fp32) static_cast<float *>(out)[at] = 0.0f;
         else static_cast<uint16_t *>(out)[at] = 0;
     }
-}
-
-typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiled encode_tiled() {
-    static std::atomic<void *> fn{nullptr};
-    void *p = fn.load(std::memory_order_relaxed);
-    if (!p) {
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        fn.store(p, std::memory_order_relaxed);
-    }
-    return reinterpret_cast<EncodeTiled>(p);
 }
 
 // Codes as bytes [rows][row_bytes]: boxes of 128 bytes (256 elements) by
