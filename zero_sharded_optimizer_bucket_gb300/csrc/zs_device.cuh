@@ -374,6 +374,38 @@ __device__ __forceinline__ bool mbar_wait_quick(uint32_t bar, uint32_t parity, u
     return false;
 }
 
+// Programmatic dependent launch (kernels launched by launch_dependent below):
+// wait until the previous kernel of the stream has finished and its writes are
+// visible; let the next such kernel place its CTAs, which wait the same way.
+// Launched ordinarily, neither has an effect.  What the previous kernel may
+// have written is read by ordinary loads or bulk copies, not by read-only ones
+// (__ldg), which may assume that nothing writes during the kernel.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" : : : "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" : : : "memory"); }
+
+// A launch as a programmatic dependent of the stream's previous kernel, in
+// clusters of `cluster` CTAs: back-to-back calls lose most of the gap between
+// two kernels, which is as long as a small one.
+template <class... P, class... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, unsigned cluster,
+                                    cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 struct AdamC {
     float lr, b1, b2, omb1, omb2, eps, wd, lr_wd, bc1, bc2;
     int adamw;

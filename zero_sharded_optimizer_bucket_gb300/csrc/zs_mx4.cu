@@ -25,7 +25,7 @@ struct Row8 {
         } else if (VEC && n >= 8) {
             const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(x) + at * (F32 ? 4 : 2));
 #pragma unroll
-            for (int i = 0; i < (F32 ? 2 : 1); ++i) w[i] = __ldg(p + i);
+            for (int i = 0; i < (F32 ? 2 : 1); ++i) w[i] = p[i];
         } else {
             uint32_t r[8];
 #pragma unroll
@@ -111,6 +111,8 @@ mx4_quantize_kernel(Mx4Args a) {
     __shared__ __align__(16) uint8_t rs[MX4_ATOM], cs[MX4_ATOM];
     constexpr int ES = F32 ? 4 : 2;
     const int t = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
     const int64_t rt = blockIdx.x / a.tiles_c, ct = blockIdx.x - rt * a.tiles_c;
     const int64_t row0 = rt * QT, col0 = ct * QT;
     const int c8 = (t & 15) * 8;
@@ -229,6 +231,8 @@ mx4_quantize_tiles_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, in
     if (threadIdx.x == 0) {
         for (int i = 0; i < QS_STAGES; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" : : "r"(bar + 8 * i) : "memory");
         asm volatile("fence.proxy.async.shared::cta;" : : : "memory");
+        pdl_wait();
+        pdl_trigger();
         for (int i = 0; i < QS_STAGES && i < mine; ++i) fetch(i);
     }
     __syncthreads();
@@ -326,12 +330,14 @@ constexpr int DQ_ROWS = 4;
 __host__ __device__ constexpr int dq_cols(bool f32) { return (f32 ? 8 : 16) * 256; }
 template <class T, bool F32, bool VEC>
 __global__ void __launch_bounds__(256)
-mx4_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
-                      int64_t rows, int64_t cols, void *__restrict__ out, int64_t ldo, uint32_t tiles_c) {
+mx4_dequantize_kernel(const uint8_t *codes, const uint8_t *scales,
+                      int64_t rows, int64_t cols, void *out, int64_t ldo, uint32_t tiles_c) {
     constexpr int E = F32 ? 8 : 16;
     const int64_t row_bytes = mx4_row_bytes(cols), atoms = mx4_atoms(cols);
     const uint32_t rt = blockIdx.x / tiles_c, ct = blockIdx.x - rt * tiles_c;
     const int64_t row0 = (int64_t)rt * DQ_ROWS, c = (int64_t)ct * dq_cols(F32) + E * (int)threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
     if (c >= cols) return;
     const int64_t g = c / MX4_GROUP;
     const int n = (int)min((int64_t)E, cols - c);
@@ -341,9 +347,9 @@ mx4_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restri
     for (int i = 0; i < DQ_ROWS; ++i) {
         const int64_t row = row0 + i;
         if (row >= rows) continue;
-        if (F32) q[i].x = __ldg(reinterpret_cast<const uint32_t *>(codes + row * row_bytes + c / 2));
-        else q[i] = __ldg(reinterpret_cast<const uint2 *>(codes + row * row_bytes + c / 2));
-        byte[i] = __ldg(scales + ((row >> 7) * atoms + (g >> 2)) * MX4_ATOM + mx4_in_atom((int)(row & 127), (int)(g & 3)));
+        if (F32) q[i].x = *reinterpret_cast<const uint32_t *>(codes + row * row_bytes + c / 2);
+        else q[i] = *reinterpret_cast<const uint2 *>(codes + row * row_bytes + c / 2);
+        byte[i] = scales[((row >> 7) * atoms + (g >> 2)) * MX4_ATOM + mx4_in_atom((int)(row & 127), (int)(g & 3))];
     }
 #pragma unroll
     for (int i = 0; i < DQ_ROWS; ++i) {
@@ -393,8 +399,7 @@ static cudaError_t quantize_launch(const Mx4Args &a, int64_t grid, cudaStream_t 
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    mx4_quantize_kernel<T, F32, VEC, ROWS, COLS><<<(unsigned)grid, 256, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(mx4_quantize_kernel<T, F32, VEC, ROWS, COLS>, (unsigned)grid, 256, (size_t)smem, 1, s, a);
 }
 
 template <class T, bool ROWS, bool COLS>
@@ -422,8 +427,7 @@ static cudaError_t tiles_launch(const Mx4Args &a, int64_t tiles, cudaStream_t s)
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     const int64_t wave = S::CTAS * (int64_t)sms, grid = tiles < wave ? tiles : wave;
-    mx4_quantize_tiles_kernel<T, ROWS, COLS><<<(unsigned)grid, S::THREADS, S::SMEM, s>>>(map, a, (int)tiles);
-    return cudaGetLastError();
+    return launch_dependent(mx4_quantize_tiles_kernel<T, ROWS, COLS>, (unsigned)grid, S::THREADS, S::SMEM, 1, s, map, a, (int)tiles);
 }
 
 template <class T>
@@ -549,18 +553,14 @@ zs_status zs_mx4_dequantize(const void *codes, const void *scales, int64_t rows,
     const bool vec = (addr(out) & 15) == 0 && ldo % (dtype == ZS_DTYPE_FP32 ? 4 : 8) == 0;
     const uint8_t *c = static_cast<const uint8_t *>(codes), *sc = static_cast<const uint8_t *>(scales);
     using namespace zsk;
-    const dim3 g((unsigned)grid), b(256);
-    if (dtype == ZS_DTYPE_FP32) {
-        if (vec) mx4_dequantize_kernel<F32X, true, true><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo, (uint32_t)tiles_c);
-        else mx4_dequantize_kernel<F32X, true, false><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo, (uint32_t)tiles_c);
-    } else if (dtype == ZS_DTYPE_FP16) {
-        if (vec) mx4_dequantize_kernel<FP16T, false, true><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo, (uint32_t)tiles_c);
-        else mx4_dequantize_kernel<FP16T, false, false><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo, (uint32_t)tiles_c);
-    } else {
-        if (vec) mx4_dequantize_kernel<BF16T, false, true><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo, (uint32_t)tiles_c);
-        else mx4_dequantize_kernel<BF16T, false, false><<<g, b, 0, s>>>(c, sc, rows, cols, out, ldo, (uint32_t)tiles_c);
-    }
-    return cuda_status(cudaGetLastError(), fn);
+    auto launch = [&](auto kernel) {
+        return launch_dependent(kernel, (unsigned)grid, 256, 0, 1, s, c, sc, rows, cols, out, ldo, (uint32_t)tiles_c);
+    };
+    cudaError_t e;
+    if (dtype == ZS_DTYPE_FP32) e = vec ? launch(mx4_dequantize_kernel<F32X, true, true>) : launch(mx4_dequantize_kernel<F32X, true, false>);
+    else if (dtype == ZS_DTYPE_FP16) e = vec ? launch(mx4_dequantize_kernel<FP16T, false, true>) : launch(mx4_dequantize_kernel<FP16T, false, false>);
+    else e = vec ? launch(mx4_dequantize_kernel<BF16T, false, true>) : launch(mx4_dequantize_kernel<BF16T, false, false>);
+    return cuda_status(e, fn);
 }
 
 }  // extern "C"

@@ -139,8 +139,14 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
             asm volatile("fence.proxy.async.shared::cta;" : : : "memory");
         }
         __syncwarp();
+        pdl_wait();
         for (; issued < S::STAGES && k0 + issued < k1; ++issued) load(k0 + issued);
     }
+    if (warp == 5 && elect_one()) {
+        asm volatile("prefetch.tensormap [%0];" : : "l"(&map_p) : "memory");
+        asm volatile("prefetch.tensormap [%0];" : : "l"(&map_q) : "memory");
+    }
+    __syncwarp();
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      :
@@ -152,6 +158,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
     const uint32_t tmem = tmem_base;
+    pdl_trigger();                         // tensor memory is allocated: the next kernel may wait for its own
 
     if (warp == 4) {
         for (; k0 + issued < k1; ++issued) {
@@ -387,9 +394,11 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" : : : "memory");
     asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
     const uint32_t tmem = tmem_base;
+    pdl_trigger();                         // tensor memory is allocated: the next kernel may wait for its own
 
     int issued = 0;
     if (warp == 8) {
+        pdl_wait();
         // loads of this CTA: its half of the rows of A and of B, the scales
         // of its rows of A, and all the tile's scales of B
         bool ok = true;
@@ -621,19 +630,7 @@ static cudaError_t pair_launch(const CUtensorMap (&map)[4], const PairArgs &a, c
     cudaError_t e = device_sms(known, pair_attributes, &sms);
     if (e != cudaSuccess) return e;
     const int pairs = a.tiles < sms / 2 ? a.tiles : sms / 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * pairs));
-    cfg.blockDim = dim3(PAIR_THREADS);
-    cfg.dynamicSmemBytes = PAIR_SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, mx4_matmul_pair_kernel, map[0], map[1], map[2], map[3], a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_dependent(mx4_matmul_pair_kernel, (unsigned)(2 * pairs), PAIR_THREADS, PAIR_SMEM, 2, s, map[0], map[1], map[2], map[3], a);
 }
 
 template <int BN, bool FLIP>
@@ -645,19 +642,8 @@ static cudaError_t mm_launch(const CUtensorMap &p, const CUtensorMap &q, const M
         return cudaFuncSetAttribute(mx4_matmul_kernel<BN, FLIP>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     }, &sms);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)a.p_tiles * a.q_tiles * a.split));
-    cfg.blockDim = dim3(MM_THREADS);
-    cfg.dynamicSmemBytes = S::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)a.split;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, mx4_matmul_kernel<BN, FLIP>, p, q, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_dependent(mx4_matmul_kernel<BN, FLIP>, (unsigned)((int64_t)a.p_tiles * a.q_tiles * a.split), MM_THREADS, S::SMEM,
+                            (unsigned)a.split, s, p, q, a);
 }
 
 }  // namespace zsk

@@ -75,8 +75,8 @@ struct F32G {
     static constexpr int SIZE = 4;
     static __device__ __forceinline__ void load8(const void *p, int64_t i, float g[8]) {
         const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i);
-        floats4(__ldg(q), g);
-        floats4(__ldg(q + 1), g + 4);
+        floats4(q[0], g);
+        floats4(q[1], g + 4);
     }
     static __device__ __forceinline__ void shared8(uint32_t a, float g[8]) {
         floats4(lds16(a), g);
@@ -94,7 +94,7 @@ struct H16G {
         for (int j = 0; j < 8; ++j) g[j] = T::to_f32(lane16(v, j));
     }
     static __device__ __forceinline__ void load8(const void *p, int64_t i, float g[8]) {
-        convert(ldg16(static_cast<const uint16_t *>(p) + i), g);
+        convert(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i), g);
     }
     static __device__ __forceinline__ void shared8(uint32_t a, float g[8]) { convert(lds16(a), g); }
     static __device__ __forceinline__ float load1(const void *p, int64_t i) {
@@ -141,11 +141,13 @@ __device__ __forceinline__ uint16_t cast1(float p, bool fp16) {
 // adam_elem, so that a list over a plan's shards gives zs_adam_step's bits.
 template <class G>
 __global__ void __launch_bounds__(THREADS)
-tensors32_kernel(const ZsChunk *__restrict__ chunks, AdamC c, const float *__restrict__ d_coef,
-                 const int32_t *__restrict__ d_flags, bool fp16) {
-    if (d_flags && (*d_flags & ZS_SKIP_NONFINITE)) return;
-    const float coef = d_coef ? *d_coef : 1.0f;
+tensors32_kernel(const ZsChunk *chunks, AdamC c, const float *d_coef,
+                 const int32_t *d_flags, bool fp16) {
+    pdl_wait();
+    pdl_trigger();
     const ZsChunk k = chunks[blockIdx.x];
+    const float coef = d_coef ? *d_coef : 1.0f;
+    if (d_flags && (*d_flags & ZS_SKIP_NONFINITE)) return;
     float *pm = static_cast<float *>(k.m), *pv = static_cast<float *>(k.v);
     uint16_t *param = static_cast<uint16_t *>(k.param);
     const int vec = k.tensor < 0 ? 0 : k.len & ~7;
@@ -318,7 +320,7 @@ __device__ __forceinline__ void adam8_moments(float &p, float &m, float &v, floa
 // One block, any length and alignment, with moments that are not finite: such
 // an element becomes a NaN code and does not count for the scale.
 template <class G, bool DITHER>
-__device__ __noinline__ void adam8_block(const ZsChunk *__restrict__ chunk, const Adam8C c, float coef, bool fp16, int b) {
+__device__ __noinline__ void adam8_block(const ZsChunk *chunk, const Adam8C c, float coef, bool fp16, int b) {
     const ZsChunk k = *chunk;
     uint8_t *cm = static_cast<uint8_t *>(k.m), *cv = static_cast<uint8_t *>(k.v);
     uint16_t *param = static_cast<uint16_t *>(k.param);
@@ -400,10 +402,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 // a rounding of p); the root is exact, since codes hang on it.
 template <class G, bool DITHER>
 __global__ void __launch_bounds__(THREADS, 4)
-tensors8_kernel(const ZsChunk *__restrict__ chunks, Adam8C c, const float *__restrict__ d_coef,
-                const int32_t *__restrict__ d_flags, bool fp16) {
+tensors8_kernel(const ZsChunk *chunks, Adam8C c, const float *d_coef,
+                const int32_t *d_flags, bool fp16) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[STAGES8];
+    pdl_wait();
+    pdl_trigger();
     const ZsChunk k = chunks[blockIdx.x];
     const float coef = d_coef ? *d_coef : 1.0f;
     if (d_flags && (*d_flags & ZS_SKIP_NONFINITE)) return;
@@ -498,8 +502,8 @@ static cudaError_t launch8(const zs_tensors *L, const Adam8C &c, const float *d_
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_relaxed);
     }
-    tensors8_kernel<G, DITHER><<<(unsigned)L->chunks.size(), THREADS, SMEM8<G>, s>>>(L->d_chunks, c, d_coef, d_flags, fp16);
-    return cudaGetLastError();
+    return launch_dependent(tensors8_kernel<G, DITHER>, (unsigned)L->chunks.size(), THREADS, SMEM8<G>, 1, s, L->d_chunks, c,
+                            d_coef, d_flags, fp16);
 }
 
 template <class G>
@@ -511,8 +515,7 @@ static cudaError_t launch(const zs_tensors *L, const ZsAdamScalars &a, const Ada
         AdamC c;
         c.lr = a.lr; c.b1 = a.b1; c.b2 = a.b2; c.omb1 = a.omb1; c.omb2 = a.omb2; c.eps = a.eps;
         c.wd = a.wd; c.lr_wd = a.lr_wd; c.bc1 = a.bc1; c.bc2 = a.bc2; c.adamw = a.adamw;
-        tensors32_kernel<G><<<grid, THREADS, 0, s>>>(L->d_chunks, c, d_coef, d_flags, fp16);
-        return cudaGetLastError();
+        return launch_dependent(tensors32_kernel<G>, grid, THREADS, 0, 1, s, L->d_chunks, c, d_coef, d_flags, fp16);
     }
     return dither ? launch8<G, true>(L, c8, d_coef, d_flags, fp16, s) : launch8<G, false>(L, c8, d_coef, d_flags, fp16, s);
 }
