@@ -424,6 +424,10 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
                 __syncwarp();
             }
         }
+        // every signal to this CTA's barriers has come before it leaves
+        for (int i = issued > PAIR_STAGES ? issued - PAIR_STAGES : 0; ok && i < issued; ++i)
+            ok = warp_wait(empty(i % PAIR_STAGES), (uint32_t)((i / PAIR_STAGES) & 1), MM_WAIT_NS);
+        if (!ok) failed = 1;
     } else if (warp == 9 && rank == 0) {
         const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(PAIR_COLS / 8) << 17) | (1u << 23) | (16u << 24);
         int i = 0, n = 0;
