@@ -243,7 +243,9 @@ mx4_quantize_tiles_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, in
         const int64_t rt = tile / tiles_c, ct = tile - rt * tiles_c;
         const int64_t row0 = rt * QT, col0 = ct * QT;
         const uint32_t at = base + s * QS_STAGE;
-        if (!__syncthreads_and(mbar_wait_quick(bar + 8 * s, (uint32_t)((i / QS_STAGES) & 1), QS_WAIT_NS))) {
+        bool landed = true;
+        if (threadIdx.x < 32) landed = mbar_wait_quick(bar + 8 * s, (uint32_t)((i / QS_STAGES) & 1), QS_WAIT_NS);
+        if (!__syncthreads_and(landed)) {
             // give up, once the copies in flight have landed
             if (threadIdx.x == 0) {
                 atomicAdd(&g_quantize_wait_timeouts, 1);
@@ -291,9 +293,11 @@ mx4_quantize_tiles_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, in
             const int box = (t >> 5) & 1, word = 16 * ((t >> 6) & 1) + (t & 15), c = 64 * box + 2 * word;
             uint32_t w[32], two = 0;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 8; ++e) {            // rows e, e + 8, ...: the same turn of the swizzle
                 const int r = e ^ (4 * upper);
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[e]) : "r"(at + box * QS_BOX + 4096 * g + 128 * r + 16 * ((word >> 2) ^ (r & 7)) + 4 * (word & 3)));
+                const uint32_t from = at + box * QS_BOX + 4096 * g + 128 * r + 16 * ((word >> 2) ^ r) + 4 * (word & 3);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[8 * h + e]) : "r"(from + 1024 * h));
             }
 #pragma unroll
             for (int e = 0; e < 32; ++e) max_abs2<T>(two, w[e]);

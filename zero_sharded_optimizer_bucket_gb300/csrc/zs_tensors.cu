@@ -213,15 +213,19 @@ __device__ __forceinline__ void e4m3_decode8(uint2 c, float o[8]) {
     }
 }
 
-// a >= 0 (< 256) to a value of e4m3, up when its 16 random bits say so: the
-// probability of the upper neighbour is a's place between the two, to 2^-16.
-// The equally spaced range below 2^-6 is shifted into the binade [2^-6, 2^-5),
-// whose spacing is the same 2^-9.  Adding to the bits below the kept mantissa
-// carries into it, and past it into the exponent, as rounding up does.
-__device__ __forceinline__ float e4m3_dither(float a, uint32_t random16) {
-    const float off = a < 0.015625f ? 0.015625f : 0.0f;
-    const uint32_t u = __float_as_uint(__fadd_rn(a, off)) + ((random16 << 4) | 8u);
-    return __fsub_rn(__uint_as_float(u & 0xFFF00000u), off);
+// a >= 0 (< 256) to a value of e4m3, up when its random bits say so: random
+// is 16 r + 8 for 16 random bits r, the middle of the interval that they name,
+// so the probability of the upper neighbour is a's place between the two, to
+// 2^-16.  The equally spaced range below 2^-6 is shifted into the binade
+// [2^-6, 2^-5), whose spacing is the same 2^-9.  Adding to the bits below the
+// kept mantissa carries into it, and past it into the exponent, as rounding up
+// does.  (2^-6 - a) 2^100, saturated, is 1 below 2^-6 and 0 from it on: fused
+// products keep the comparison off the integer pipe, which is the busier one.
+__device__ __forceinline__ float e4m3_dither(float a, uint32_t random) {
+    float low;
+    asm("fma.rn.sat.f32 %0, %1, 0fF1800000, 0f6E800000;" : "=f"(low) : "f"(a));     // -2^100, 2^94
+    const uint32_t u = __float_as_uint(__fmaf_rn(low, 0.015625f, a)) + random;
+    return __fmaf_rn(low, -0.015625f, __uint_as_float(u & 0xFFF00000u));
 }
 
 __device__ __forceinline__ bool finite_bits(float x) {
@@ -232,13 +236,14 @@ __device__ __forceinline__ bool finite_bits(float x) {
 // a positive value never gets code 0 (it divides the update).
 template <bool ROOT, bool DITHER>
 __device__ __forceinline__ uint2 encode8(const float x[8], float inv, const uint32_t random[8]) {
+    constexpr float BIG = 1.2676506002282294e30f;    // 2^100: takes the smallest positive root past 2^-9
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         y[i] = __fmul_rn(x[i], inv);
         if (DITHER)
             y[i] = ROOT ? e4m3_dither(y[i], random[i]) : copysignf(e4m3_dither(fabsf(y[i]), random[i]), y[i]);
-        if (ROOT && x[i] > 0.0f) y[i] = fmaxf(y[i], 0.001953125f);
+        if (ROOT) y[i] = fmaxf(y[i], fminf(__fmul_rn(x[i], BIG), 0.001953125f));   // 0 for 0
     }
     return make_uint2(e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16),
                       e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16));
@@ -258,11 +263,11 @@ __device__ __forceinline__ void random8(int64_t elem, int32_t tensor, const Adam
     const uint32_t t = (uint32_t)tensor & 0x7FFFFFFFu;
     uint32_t w[8];
     philox7((uint32_t)q, (uint32_t)(q >> 32), t, c.step, c.k0, c.k1, w);
-    philox7((uint32_t)(q + 1), (uint32_t)((q + 1) >> 32), t, c.step, c.k0, c.k1, w + 4);
+    philox7((uint32_t)q | 1u, (uint32_t)(q >> 32), t, c.step, c.k0, c.k1, w + 4);    // q is even
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        lo[i] = w[i] & 0xFFFFu;
-        hi[i] = w[i] >> 16;
+        lo[i] = (w[i] & 0xFFFFu) * 16u + 8u;
+        hi[i] = (w[i] >> 16) * 16u + 8u;
     }
 }
 
@@ -293,14 +298,13 @@ __device__ __forceinline__ f2 sub2(f2 a, f2 b, const Adam8C &c) { return fma2(b,
 // residual of the smallest v among the normal numbers.  Infinities and NaN
 // give NaN, and so does v >= 2^64.
 __device__ __forceinline__ f2 root_2_32(f2 v) {
-    const f2 w = mul2(v, both(18446744073709551616.0f));
+    const f2 w = mul2(v, both(18446744073709551616.0f)), minus_w = mul2(v, both(-18446744073709551616.0f));
     float a, b;
     f2unpack(w, a, b);
     asm("rsqrt.approx.f32 %0, %1;" : "=f"(a) : "f"(fmaxf(a, 7.8886090522101181e-31f)));   // 2^-100: v = 0 gives 0
     asm("rsqrt.approx.f32 %0, %1;" : "=f"(b) : "f"(fmaxf(b, 7.8886090522101181e-31f)));
     const f2 y = f2pack(a, b), s = mul2(w, y);
-    const f2 minus = s ^ 0x8000000080000000ull;
-    return fma2(fma2(minus, s, w), mul2(both(0.5f), y), s);
+    return fma2(fma2(s, s, minus_w), mul2(both(-0.5f), y), s);
 }
 
 // New moment and square of one element; g: the gradient times coef (and the
