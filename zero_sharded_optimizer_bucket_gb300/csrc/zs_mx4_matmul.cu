@@ -539,19 +539,36 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
                     __syncwarp();
                     continue;
                 }
-                for (int i = 0; i < 32 && row0 + i < a.m; ++i) {
-                    const int64_t at = (int64_t)(row0 + i) * a.ldo + col;
-                    uint32_t x;
-                    if (fp32) {
-                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(slab + 128 * i + ((4 * lane) ^ (16 * (i & 7)))) : "memory");
-                        if (col + lane < a.n) static_cast<float *>(a.out)[at + lane] = __uint_as_float(x);
-                    } else {
+                const int rows = min(32, a.m - row0);
+                // 8 reads, then their stores
+                if (fp32) {
+                    float *o = static_cast<float *>(a.out) + (int64_t)row0 * a.ldo + col + lane;
+#pragma unroll 1
+                    for (int i = 0; i < rows; i += 8, o += 8 * a.ldo) {
+                        uint32_t x[8];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int e = 32 * h + lane;
-                            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(slab + 128 * i + ((2 * e) ^ (16 * (i & 7)))) : "memory");
-                            if (col + e < a.n) static_cast<uint16_t *>(a.out)[at + e] = (uint16_t)x;
+                        for (int e = 0; e < 8; ++e)
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[e]) : "r"(slab + 128 * (i + e) + ((4 * lane) ^ (16 * e))) : "memory");
+                        if (col + lane < a.n) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (i + e < rows) o[e * a.ldo] = __uint_as_float(x[e]);
                         }
+                    }
+                } else {
+                    uint16_t *o = static_cast<uint16_t *>(a.out) + (int64_t)row0 * a.ldo + col + lane;
+#pragma unroll 1
+                    for (int i = 0; i < rows; i += 4, o += 4 * a.ldo) {
+                        uint32_t x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            asm volatile("ld.shared.u16 %0, [%1];"
+                                         : "=r"(x[e])
+                                         : "r"(slab + 128 * (i + e / 2) + ((2 * (32 * (e & 1) + lane)) ^ (16 * ((i + e / 2) & 7))))
+                                         : "memory");
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (i + e / 2 < rows && col + 32 * (e & 1) + lane < a.n) o[(e / 2) * a.ldo + 32 * (e & 1)] = (uint16_t)x[e];
                     }
                 }
                 __syncwarp();
