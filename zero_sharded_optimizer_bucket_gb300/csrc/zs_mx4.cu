@@ -197,27 +197,21 @@ mx4_quantize_kernel(Mx4Args a) {
 // the columns a thread takes 32 rows of two neighbouring columns; neither
 // access has a bank conflict under the swizzle.  Bandwidth bounds it: 2 bytes
 // read and 0.53 written an element and form.
-// Both forms at once take 16 warps, 8 for each, on two CTAs an SM; one form 8
-// on three.
-constexpr int QS_BOX = 64 * 128 * 2, QS_STAGE = 2 * QS_BOX;
-template <bool BOTH>
-struct QsShape {
-    static constexpr int THREADS = BOTH ? 512 : 256, CTAS = BOTH ? 2 : 3, STAGES = BOTH ? 3 : 2;
-    static constexpr int SMEM = STAGES * QS_STAGE + 1024;
-};
+// 8 warps on three CTAs an SM; for both forms every warp makes one after the
+// other (8 warps for each on two CTAs took 34 us for 14336 x 4096, this 30).
+constexpr int QS_BOX = 64 * 128 * 2, QS_STAGE = 2 * QS_BOX, QS_STAGES = 2, QS_CTAS = 3;
+constexpr int QS_SMEM = QS_STAGES * QS_STAGE + 1024;
 constexpr uint64_t QS_WAIT_NS = 1000000000ull;       // one wait gives up after 1 s
 
 __device__ int g_quantize_wait_timeouts;             // waits that gave up
 
 template <class T, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(QsShape<ROWS && COLS>::THREADS, QsShape<ROWS && COLS>::CTAS)
+__global__ void __launch_bounds__(256, QS_CTAS)
 mx4_quantize_tiles_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, int tiles) {
-    constexpr int QS_STAGES = QsShape<ROWS && COLS>::STAGES;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(16) uint8_t rs[2][MX4_ATOM], cs[2][MX4_ATOM];
     __shared__ __align__(8) uint64_t bars[QS_STAGES];
-    const int t = threadIdx.x & 255;
-    const bool do_rows = ROWS && (!COLS || threadIdx.x < 256), do_cols = COLS && (!ROWS || threadIdx.x >= 256);
+    const int t = threadIdx.x;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u, bar = smem_u32(bars);
     const int tiles_c = (int)a.tiles_c;
     auto fetch = [&](int i) {                        // the i-th tile of this CTA
@@ -228,7 +222,7 @@ mx4_quantize_tiles_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, in
         tma2d(base + s * QS_STAGE + QS_BOX, &map, ct * QT + 64, rt * QT, bar + 8 * s);
     };
     const int mine = ((int)(tiles - blockIdx.x) + (int)gridDim.x - 1) / (int)gridDim.x;
-    if (threadIdx.x == 0) {
+    if (t == 0) {
         for (int i = 0; i < QS_STAGES; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" : : "r"(bar + 8 * i) : "memory");
         asm volatile("fence.proxy.async.shared::cta;" : : : "memory");
         pdl_wait();
@@ -244,10 +238,10 @@ mx4_quantize_tiles_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, in
         const int64_t row0 = rt * QT, col0 = ct * QT;
         const uint32_t at = base + s * QS_STAGE;
         bool landed = true;
-        if (threadIdx.x < 32) landed = mbar_wait_quick(bar + 8 * s, (uint32_t)((i / QS_STAGES) & 1), QS_WAIT_NS);
+        if (t < 32) landed = mbar_wait_quick(bar + 8 * s, (uint32_t)((i / QS_STAGES) & 1), QS_WAIT_NS);
         if (!__syncthreads_and(landed)) {
             // give up, once the copies in flight have landed
-            if (threadIdx.x == 0) {
+            if (t == 0) {
                 atomicAdd(&g_quantize_wait_timeouts, 1);
                 for (int j = i; j < i + QS_STAGES && j < mine; ++j)
                     mbar_wait_quick(bar + 8 * (j % QS_STAGES), (uint32_t)((j / QS_STAGES) & 1), QS_WAIT_NS);
@@ -255,7 +249,7 @@ mx4_quantize_tiles_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, in
             __syncthreads();
             return;
         }
-        if (do_rows) {
+        if (ROWS) {
             // a thread takes a group: 4 lanes a row, 8 rows a warp.  The second
             // box's pieces are read two apart in turn, so that 8 lanes meet 8
             // different pieces of the banks.
@@ -285,7 +279,7 @@ mx4_quantize_tiles_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, in
                         box ? make_uint4(q[2], q[3], q[0], q[1]) : make_uint4(q[0], q[1], q[2], q[3]);
             }
         }
-        if (do_cols) {
+        if (COLS) {
             // a thread takes 32 rows of two columns; lanes 16 on the same
             // columns' next 32, so that a warp's stores fill sectors.  They
             // read rows 4 apart in turn: other pieces of the banks.
@@ -320,10 +314,10 @@ mx4_quantize_tiles_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, in
             }
         }
         __syncthreads();                             // the stage is read, the scales are in rs and cs
-        if (threadIdx.x == 0 && i + QS_STAGES < mine) fetch(i + QS_STAGES);
-        if (do_rows && t >= 32 && t < 64 && rt < mx4_row_tiles(a.rows))
+        if (t == 0 && i + QS_STAGES < mine) fetch(i + QS_STAGES);
+        if (ROWS && t >= 32 && t < 64 && rt < mx4_row_tiles(a.rows))
             reinterpret_cast<uint4 *>(a.r_scales + (rt * r_atoms + ct) * MX4_ATOM)[t - 32] = reinterpret_cast<const uint4 *>(rs[i & 1])[t - 32];
-        if (do_cols && t >= 64 && t < 96 && ct < mx4_row_tiles(a.cols))
+        if (COLS && t >= 64 && t < 96 && ct < mx4_row_tiles(a.cols))
             reinterpret_cast<uint4 *>(a.c_scales + (ct * c_atoms + rt) * MX4_ATOM)[t - 64] = reinterpret_cast<const uint4 *>(cs[i & 1])[t - 64];
     }
 }
@@ -421,7 +415,6 @@ static cudaError_t quantize_launch(const Mx4Args &a, int64_t grid, cudaStream_t 
 
 template <class T, bool ROWS, bool COLS>
 static cudaError_t tiles_launch(const Mx4Args &a, int64_t tiles, cudaStream_t s) {
-    using S = QsShape<ROWS && COLS>;
     static std::atomic<int> known[64];           // SMs, once the kernel's shared memory is set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -429,7 +422,7 @@ static cudaError_t tiles_launch(const Mx4Args &a, int64_t tiles, cudaStream_t s)
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     int sms = known[dev].load(std::memory_order_relaxed);
     if (sms <= 0) {
-        e = cudaFuncSetAttribute(mx4_quantize_tiles_kernel<T, ROWS, COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        e = cudaFuncSetAttribute(mx4_quantize_tiles_kernel<T, ROWS, COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize, QS_SMEM);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return e;
         known[dev].store(sms, std::memory_order_relaxed);
@@ -443,8 +436,8 @@ static cudaError_t tiles_launch(const Mx4Args &a, int64_t tiles, cudaStream_t s)
           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    const int64_t wave = S::CTAS * (int64_t)sms, grid = tiles < wave ? tiles : wave;
-    return launch_dependent(mx4_quantize_tiles_kernel<T, ROWS, COLS>, (unsigned)grid, S::THREADS, S::SMEM, 1, s, map, a, (int)tiles);
+    const int64_t wave = QS_CTAS * (int64_t)sms, grid = tiles < wave ? tiles : wave;
+    return launch_dependent(mx4_quantize_tiles_kernel<T, ROWS, COLS>, (unsigned)grid, 256, QS_SMEM, 1, s, map, a, (int)tiles);
 }
 
 template <class T>
