@@ -636,8 +636,8 @@ class Tensors:
             self._h = None
 
 
-_TENSOR_ITEMS = ("grad", "param", "master", "exp_avg", "exp_avg_sq", "exp_avg_scale",
-                 "exp_avg_sq_scale")
+# names of zs_tensor's fields, 8 bytes each, by place
+_TENSOR_AT = {name: i for i, (name, _) in enumerate(zs_tensor._fields_)}
 
 
 def zs_build_tensors(tensors, state_bits: int = 32, grad_dtype=None, param_dtype=None) -> Tensors:
@@ -647,33 +647,39 @@ def zs_build_tensors(tensors, state_bits: int = 32, grad_dtype=None, param_dtype
     dtypes themselves; all gradients have one, all parameters one."""
     size = {"master": 4, "exp_avg": state_bits // 8, "exp_avg_sq": state_bits // 8,
             "exp_avg_scale": 4, "exp_avg_sq_scale": 4}
+    dtypes = {"grad": grad_dtype, "param": param_dtype}
     n = len(tensors)
-    arr = (zs_tensor * max(n, 1))()
+    rows = []          # the fields of each zs_tensor
     for i, t in enumerate(tensors):
-        unknown = set(t) - set(_TENSOR_ITEMS) - {"numel"}
-        if unknown:
-            raise TypeError(f"tensor {i}: unknown {sorted(unknown)}")
-        numel = int(t["numel"]) if "numel" in t else t["master"].numel()
-        arr[i].numel = numel
-        for name in _TENSOR_ITEMS:
-            x = t.get(name)
-            if x is None:
+        numel = t.get("numel")
+        numel = t["master"].numel() if numel is None else int(numel)
+        blocks = -(-numel // ZS_STATE_BLOCK)
+        row = [numel, 0, 0, 0, 0, 0, 0, 0]
+        for name, x in t.items():
+            at = _TENSOR_AT.get(name)
+            if at is None:
+                raise TypeError(f"tensor {i}: unknown {name}")
+            if at == 0 or x is None:
                 continue
-            if hasattr(x, "data_ptr"):
-                need = -(-numel // ZS_STATE_BLOCK) if name.endswith("_scale") else numel
-                if x.numel() < need or not x.is_contiguous():
-                    raise ValueError(f"tensor {i}: {name} is not {need} contiguous elements")
-                if name in ("grad", "param"):
-                    d = _dtype(x)
-                    if name == "grad":
-                        grad_dtype = d if grad_dtype is None else grad_dtype
-                    else:
-                        param_dtype = d if param_dtype is None else param_dtype
-                    if d != (grad_dtype if name == "grad" else param_dtype):
-                        raise TypeError(f"tensor {i}: {name} is {x.dtype}, another type than before it")
-                elif x.element_size() != size[name]:
-                    raise TypeError(f"tensor {i}: {name} is {x.dtype}, {size[name]} bytes an element expected")
-            setattr(arr[i], name, _ptr(x))
+            if not hasattr(x, "data_ptr"):
+                row[at] = int(x)
+                continue
+            need = blocks if at >= 6 else numel
+            if x.numel() < need or not x.is_contiguous():
+                raise ValueError(f"tensor {i}: {name} is not {need} contiguous elements")
+            if at <= 2:
+                d = _dtype(x)
+                if dtypes[name] is None:
+                    dtypes[name] = d
+                elif dtypes[name] != d:
+                    raise TypeError(f"tensor {i}: {name} is {x.dtype}, another type than before it")
+            elif x.itemsize != size[name]:
+                raise TypeError(f"tensor {i}: {name} is {x.dtype}, {size[name]} bytes an element expected")
+            row[at] = x.data_ptr()
+        rows += row
+    flat = (_i64 * max(len(rows), 1))(*[r - (1 << 64) if r >= 1 << 63 else r for r in rows])
+    arr = C.cast(flat, C.POINTER(zs_tensor))
+    grad_dtype, param_dtype = dtypes["grad"], dtypes["param"]
     cfg = zs_tensors_config(int(state_bits), ZS_DTYPE_BF16 if grad_dtype is None else int(grad_dtype),
                             ZS_DTYPE_BF16 if param_dtype is None else int(param_dtype), 0)
     out = _P()
