@@ -170,7 +170,7 @@ def random_held(rng, rows, k, lo=120, hi=134):
 PRODUCTS = [(1, 1, 1), (1, 8, 32), (1, 129, 31), (2, 130, 33), (16, 128, 256), (17, 256, 257), (33, 100, 700), (64, 300, 512),
             (65, 128, 1000), (128, 257, 2048), (129, 1, 96), (130, 127, 64), (200, 300, 500), (256, 256, 4096), (300, 513, 1056),
             (1, 1024, 8192), (1000, 77, 40), (520, 9000, 288), (2600, 2600, 544),
-            (129, 9800, 256), (385, 5121, 1300), (4097, 640, 3000), (1024, 2560, 512)]
+            (129, 9800, 256), (385, 5121, 1300), (4097, 640, 3000), (1024, 2560, 512), (10100, 100, 300)]
 
 
 @pytest.mark.parametrize("m,n,k", PRODUCTS)

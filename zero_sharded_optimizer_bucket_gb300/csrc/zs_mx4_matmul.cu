@@ -3,9 +3,18 @@
 //
 // tcgen05.mma kind::mxf4 multiplies e2m1 codes, applies both scales and adds
 // in float32 in tensor memory, 64 elements of k an instruction.  A stage is
-// 256 elements of k: 128 bytes a row, one 128-byte swizzled TMA box an
+// 256 elements of k: 128 bytes a row, one 128-byte swizzled tensor copy an
 // operand, and two scale atoms a 128 rows, which tcgen05.cp moves to tensor
-// memory.  A warp loads, one thread issues the products, four warps store.
+// memory.  One warp loads, one issues the products, the others store.
+//
+// Two kernels, by the work there is:
+//  - products that give every pair of SMs about a 256 x 256 tile or more:
+//    mx4_matmul_pair_kernel.  8192 x 14336 x 4096 bf16: 143 us, 6.7 PFLOP/s in
+//    short runs; 156-160 us, 6.0-6.2 PFLOP/s in long ones, which run at the
+//    board's 1.4 kW (the clock falls to 1.9 GHz and below).
+//  - smaller ones: mx4_matmul_kernel, tiles of 128 rows, k shared out over a
+//    cluster when the tiles are few.  One token through 4096 x 14336: 6.0 us,
+//    4.9 TB/s of weight bytes; 256 x 4096 x 4096: 10 us.
 #include <atomic>
 
 #include "zs_launch.h"
@@ -23,15 +32,14 @@ __device__ int g_mx4_wait_timeouts;       // waits that gave up
 // P holds the tile's 128 rows, Q its BN; D[p][q].
 template <int BN>
 struct MmShape {
-    static constexpr int QA = (BN + 127) / 128;                 // scale atoms of Q per 4 groups
     static constexpr int P_BYTES = MM_P * MM_KB, Q_BYTES = BN * MM_KB;
-    static constexpr int SP_BYTES = 2 * MX4_ATOM, SQ_BYTES = 2 * QA * MX4_ATOM;
+    static constexpr int SP_BYTES = 2 * MX4_ATOM, SQ_BYTES = 2 * MX4_ATOM;
     static constexpr int STAGE = P_BYTES + Q_BYTES + SP_BYTES + SQ_BYTES;    // a multiple of 1024
-    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 3 : 4;
+    static constexpr int STAGES = BN == 128 ? 3 : 4;      // 6 or 8 took as long: the issue of a stage bounds it
     // tensor memory: accumulator, then two sets of scales
     static constexpr int SP_COL = BN < 32 ? 32 : BN, SQ_COL = SP_COL + 16;
-    static constexpr int USED = SQ_COL + 16 * QA;
-    static constexpr int COLS = USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
+    static constexpr int USED = SQ_COL + 16;
+    static constexpr int COLS = USED <= 64 ? 64 : USED <= 128 ? 128 : 256;   // two CTAs of an SM fit
     static constexpr int RED = BN * MM_P * 4 + 16 * (BN > MM_P ? BN : MM_P);   // the tile, rows 16 bytes apart
     static constexpr int BODY = STAGES * STAGE > RED ? STAGES * STAGE : RED;
     static constexpr int SMEM = BODY + 1024;                   // and room to align
@@ -73,7 +81,7 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" : : "r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&v)[32]) {
+__device__ __forceinline__ void tc_ld32_nowait(uint32_t addr, uint32_t *v) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -83,6 +91,10 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t (&v)[32]) {
           "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(addr));
+}
+
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t *v) {
+    tc_ld32_nowait(addr, v);
     asm volatile("tcgen05.wait::ld.sync.aligned;" : : : "memory");
 }
 
@@ -90,8 +102,13 @@ __device__ __forceinline__ uint32_t mm_cast(float x, int dtype) {
     return dtype == ZS_DTYPE_FP16 ? FP16T::from_f32(x) : BF16T::from_f32(x);
 }
 
-// FLIP: P are the rows of B (features) and Q those of A (tokens), for few
-// tokens: out[q][p].  Otherwise out[p][q].
+// Tiles of 128 rows of P by BN of Q.  FLIP: P are the rows of B (features) and
+// Q those of A (tokens), for up to 64 tokens: out[q][p]; the tensor cores'
+// 128 rows are then filled by features, and a product over few tokens reads
+// the weight's bytes and little else.  Otherwise out[p][q].  split > 1: the
+// CTAs of a cluster take parts of k and add their tiles through distributed
+// shared memory, in the order of the parts, so that a result has the same bits
+// every time.
 template <int BN, bool FLIP>
 __global__ void __launch_bounds__(MM_THREADS)
 mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, MmArgs a) {
@@ -120,12 +137,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
             tma2d(p, &map_p, k * MM_KB, pt * MM_P, full(s));
             tma2d(q, &map_q, k * MM_KB, qt * BN, full(s));
             bulk(scp, sp + (int64_t)k * S::SP_BYTES, S::SP_BYTES, full(s));
-#pragma unroll
-            for (int j = 0; j < S::QA; ++j) {
-                // a row tile past the matrix's last scales no stored column
-                const int rt = min((int)((int64_t)qt * BN / 128) + j, (a.nq - 1) / 128);
-                bulk(scq + j * S::SP_BYTES, a.q_scales + ((int64_t)rt * a.atoms + 2 * k) * MX4_ATOM, S::SP_BYTES, full(s));
-            }
+            bulk(scq, a.q_scales + ((int64_t)(BN == 128 ? qt : 0) * a.atoms + 2 * k) * MX4_ATOM, S::SQ_BYTES, full(s));
         }
         __syncwarp();
     };
@@ -179,7 +191,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
             }
             asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
             const uint32_t p = base + s * S::STAGE, q = p + S::P_BYTES, scp = q + S::Q_BYTES, scq = scp + S::SP_BYTES;
-            const uint32_t tp = tmem + S::SP_COL + 8 * (i & 1), tq = tmem + S::SQ_COL + 8 * S::QA * (i & 1);
+            const uint32_t tp = tmem + S::SP_COL + 8 * (i & 1), tq = tmem + S::SQ_COL + 8 * (i & 1);
             if (elect_one()) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -187,12 +199,10 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
                                  :
                                  : "r"(tp + 4 * j), "l"(mm_desc(scp + j * MX4_ATOM, 128, 0))
                                  : "memory");
-#pragma unroll
-                    for (int h = 0; h < S::QA; ++h)
-                        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
-                                     :
-                                     : "r"(tq + 4 * (S::QA * j + h)), "l"(mm_desc(scq + h * S::SP_BYTES + j * MX4_ATOM, 128, 0))
-                                     : "memory");
+                    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
+                                 :
+                                 : "r"(tq + 4 * j), "l"(mm_desc(scq + j * MX4_ATOM, 128, 0))
+                                 : "memory");
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -203,7 +213,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
                         "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
                         :
                         : "r"(tmem), "l"(mm_desc(p + 32 * j, 1024, 2)), "l"(mm_desc(q + 32 * j, 1024, 2)), "r"(d),
-                          "r"(tp + 4 * (j >> 1)), "r"(tq + 4 * S::QA * (j >> 1)), "r"((uint32_t)(i > 0 || j > 0))
+                          "r"(tp + 4 * (j >> 1)), "r"(tq + 4 * (j >> 1)), "r"((uint32_t)(i > 0 || j > 0))
                         : "memory");
                 }
                 tc_commit(empty(s));
@@ -313,7 +323,15 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
 // those of B in its shared memory, so that a byte of B is read once for
 // 256 rows.  Persistent: a pair walks tiles, the loads running ahead over
 // the tile boundary, while 8 warps of each CTA empty the accumulator of the
-// previous tile into registers, release it, and store.
+// previous tile into registers, release it, and store.  (Two accumulators of
+// 256 columns would leave no tensor memory for the scales.)
+// A stage takes the tensor cores 512 cycles and brings 35 KB to each SM; a
+// tile of 16 stages measured about 10,300 cycles with the launch alone, 350 to
+// 400 of them between its last product and the next tile's first.  What is
+// left is power: in long runs the board holds 1.36 kW.  Clusters of two pairs
+// that share B by multicast took as long (144 of the 152 SMs fit such
+// clusters), and so did scales placed by tcgen05.st in the place of tcgen05.cp
+// when they did not take longer.
 constexpr int PAIR_ROWS = 256, PAIR_COLS = 256;
 constexpr int PAIR_STAGES = 5;
 constexpr int PAIR_THREADS = 320;         // 8 warps store, 1 loads, 1 multiplies (leader only)
@@ -339,18 +357,6 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
         :
         : "r"(bar), "h"((uint16_t)3)
         : "memory");
-}
-
-__device__ __forceinline__ void tc_ld32_nowait(uint32_t addr, uint32_t *v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(addr));
 }
 
 struct PairArgs {
@@ -708,8 +714,11 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *
         if (!p || (reinterpret_cast<uintptr_t>(p) & 15))
             return zs_fail(ZS_EINVAL, "%s: codes or scales NULL or not 16-byte aligned", fn);
     cudaError_t e;
+    // The pair kernel from half a tile a pair on: 768 x 4096 x 4096 (48 tiles)
+    // takes it 10.8 us, the other kernel 12; 512 x 4096 x 4096 (32 tiles) 10.6
+    // and 10.3.
     const int64_t pair_p = (m + zsk::PAIR_ROWS - 1) / zsk::PAIR_ROWS, pair_q = (n + zsk::PAIR_COLS - 1) / zsk::PAIR_COLS;
-    if (m > 128 && pair_p * pair_q >= 38 && pair_p * pair_q < 0x7FFFFFFF) {
+    if (m > 128 && pair_p * pair_q >= 38 && pair_p * pair_q < 0x7FFF0000) {
         CUtensorMap map[4];
         if (!zsk::code_map(&map[0], a_codes, m, mx4_row_bytes(k), 128) || !zsk::code_map(&map[1], b_codes, n, mx4_row_bytes(k), 128) ||
             !zsk::scale_map(&map[2], a_scales, m, k, 1) || !zsk::scale_map(&map[3], b_scales, n, k, 2))
@@ -729,6 +738,8 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *
         zs_clear_error();
         return ZS_OK;
     }
+    // 128 features a tile for up to 64 tokens: 64 x 4096 x 4096 6.4 us, 6.5 with
+    // 128 tokens a tile; 16 tokens 5.5 us against 6.5.
     const bool flip = m <= 64;
     const int64_t np = flip ? n : m, nq = flip ? m : n;
     const void *p_codes = flip ? b_codes : a_codes, *p_scales = flip ? b_scales : a_scales;
@@ -747,6 +758,10 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *
     const int64_t pt = (np + 127) / 128, qt = (nq + bn - 1) / bn;
     a.p_tiles = (int32_t)pt;
     a.q_tiles = (int32_t)qt;
+    // k is shared out while that leaves an SM to every CTA and each enough
+    // stages to hide its part of the sum: one token through 4096 x 4096 takes
+    // 6.4, 5.8, 5.1 and 5.9 us in 1, 2, 4 and 8 parts (32 tiles), and more CTAs
+    // than SMs lose: 14336 x 4096 (112 tiles) 6.7 us in one part, 9.5 in four.
     int split = 1;
     while (split < 8 && pt * qt * split * 2 <= 152 && a.k_tiles >= (bn == 128 ? 8 : 4) * split) split *= 2;
     if (pt * qt * split > 0x7FFFFFFF) return zs_fail(ZS_EINVAL, "%s: too many tiles", fn);
