@@ -259,31 +259,10 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     else __syncthreads();
     if (!failed) {
         const int es = a.dtype == ZS_DTYPE_FP32 ? 4 : 2;
-        for (int u = part * MM_THREADS + (int)threadIdx.x; u < rows * (COLS / 4); u += a.split * MM_THREADS) {
+        const int units = rows * (COLS / 4), step = a.split * MM_THREADS;      // runs of 4 columns
+        auto store = [&](int u, const float (&f)[4]) {
             const int r = u / (COLS / 4), c = 4 * (u % (COLS / 4));
-            if (c >= cols) continue;
-            const uint32_t at = base + PITCH * r + 4 * c;
-            float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (a.split == 1) {
-                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(at) : "memory");
-            } else {
-#pragma unroll
-                for (int h = 0; h < 8; h += 4) {          // the parts' reads in flight together
-                    float x[4][4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (h + i < a.split)
-                            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                         : "=f"(x[i][0]), "=f"(x[i][1]), "=f"(x[i][2]), "=f"(x[i][3])
-                                         : "r"(map_to(at, (uint32_t)(h + i)))
-                                         : "memory");
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (h + i < a.split)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) f[e] = __fadd_rn(f[e], x[i][e]);
-                }
-            }
+            if (c >= cols) return;
             char *o = static_cast<char *>(a.out) + ((int64_t)(row0 + r) * a.ldo + col0 + c) * es;
             if (a.vec && c + 4 <= cols) {
                 if (es == 4) *reinterpret_cast<float4 *>(o) = make_float4(f[0], f[1], f[2], f[3]);
@@ -297,6 +276,47 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
                         if (es == 4) reinterpret_cast<float *>(o)[e] = f[e];
                         else reinterpret_cast<uint16_t *>(o)[e] = (uint16_t)mm_cast(f[e], a.dtype);
                     }
+            }
+        };
+        auto place = [&](int u) { return base + PITCH * (u / (COLS / 4)) + 16 * (u % (COLS / 4)); };
+        if (a.split == 1) {
+            for (int u = threadIdx.x; u < units; u += MM_THREADS) {
+                float f[4];
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(place(u)) : "memory");
+                store(u, f);
+            }
+        } else {
+            // several runs and parts at a time, so that the reads of the other
+            // CTAs' shared memory overlap
+            constexpr int RUNS = BN == 128 ? 4 : 1, PARTS = BN == 128 ? 2 : 4;
+            for (int u0 = part * MM_THREADS + (int)threadIdx.x; u0 < units; u0 += RUNS * step) {
+                float f[RUNS][4];
+#pragma unroll
+                for (int i = 0; i < RUNS; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[i][e] = 0.0f;
+                for (int h = 0; h < a.split; h += PARTS) {
+                    float x[PARTS][RUNS][4];
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+                        for (int i = 0; i < RUNS; ++i)
+                            if (u0 + i * step < units && h + p < a.split)
+                                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                             : "=f"(x[p][i][0]), "=f"(x[p][i][1]), "=f"(x[p][i][2]), "=f"(x[p][i][3])
+                                             : "r"(map_to(place(u0 + i * step), (uint32_t)(h + p)))
+                                             : "memory");
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p)
+                        if (h + p < a.split)
+#pragma unroll
+                            for (int i = 0; i < RUNS; ++i)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) f[i][e] = __fadd_rn(f[i][e], x[p][i][e]);
+                }
+#pragma unroll
+                for (int i = 0; i < RUNS; ++i)
+                    if (u0 + i * step < units) store(u0 + i * step, f[i]);
             }
         }
     }
