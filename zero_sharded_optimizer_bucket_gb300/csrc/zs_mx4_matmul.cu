@@ -2,10 +2,11 @@
 // cores (zs_mx4_matmul): out[m][n] = sum over k of A[m][k] * B[n][k].
 //
 // tcgen05.mma kind::mxf4 multiplies e2m1 codes, applies both scales and adds
-// in float32 in tensor memory, 64 elements of k an instruction.  A stage is
-// 256 elements of k: 128 bytes a row, one 128-byte swizzled tensor copy an
-// operand, and two scale atoms a 128 rows, which tcgen05.cp moves to tensor
-// memory.  One warp loads, one issues the products, the others store.
+// in float32 in tensor memory, 64 elements of k an instruction.  256 elements
+// of k are 128 bytes a row, one 128-byte swizzled tensor copy an operand, and
+// two scale atoms a 128 rows, which tcgen05.cp moves to tensor memory; a stage
+// holds them once or twice.  One warp loads, one issues the products, the
+// others store.
 //
 // Two kernels, by the work there is:
 //  - products that give every pair of SMs about a 256 x 256 tile or more:
@@ -13,8 +14,10 @@
 //    short runs; 156-160 us, 6.0-6.2 PFLOP/s in long ones, which run at the
 //    board's 1.4 kW (the clock falls to 1.9 GHz and below).
 //  - smaller ones: mx4_matmul_kernel, tiles of 128 rows, k shared out over a
-//    cluster when the tiles are few.  One token through 4096 x 14336: 6.0 us,
-//    4.9 TB/s of weight bytes; 256 x 4096 x 4096: 10 us.
+//    cluster when the tiles are few.  One token through 4096 x 14336: 6.2 us,
+//    5.1 TB/s of weight bytes; 16 through 14336 x 4096: 5.3 us, 6.0 TB/s;
+//    256 x 4096 x 4096: 8.0 us.  What is left there is the latency of a chain
+//    of few stages and the 2.1 us of a launch that computes nothing.
 #include <atomic>
 
 #include "zs_launch.h"
@@ -34,11 +37,20 @@ template <int BN>
 struct MmShape {
     static constexpr int P_BYTES = MM_P * MM_KB, Q_BYTES = BN * MM_KB;
     static constexpr int SP_BYTES = 2 * MX4_ATOM, SQ_BYTES = 2 * MX4_ATOM;
-    static constexpr int STAGE = P_BYTES + Q_BYTES + SP_BYTES + SQ_BYTES;    // a multiple of 1024
-    static constexpr int STAGES = BN == 128 ? 3 : 4;      // 6 or 8 took as long: the issue of a stage bounds it
+    static constexpr int SUB = P_BYTES + Q_BYTES + SP_BYTES + SQ_BYTES;      // 256 elements of k, a multiple of 1024
+    // Of them a stage.  Waiting for a stage and releasing it costs the issuing
+    // warp about as much as its products, so two where they fit: 16 x 14336 x
+    // 4096 takes 6.46 us with four stages of one, 5.32 with two of two.  What
+    // two CTAs of an SM cannot hold loses, because the next kernel's CTAs then
+    // begin later: three of two 5.05 us there, but 16 x 4096 x 4096 4.50
+    // against 4.20; for 128 columns two of two lose, 128 x 4096 x 4096 7.9 us
+    // against 7.6.
+    static constexpr int KS = BN == 128 ? 1 : 2;
+    static constexpr int STAGE = KS * SUB;
+    static constexpr int STAGES = BN == 128 ? 3 : 2;
     // tensor memory: accumulator, then two sets of scales
-    static constexpr int SP_COL = BN < 32 ? 32 : BN, SQ_COL = SP_COL + 16;
-    static constexpr int USED = SQ_COL + 16;
+    static constexpr int SP_COL = BN < 32 ? 32 : BN, SQ_COL = SP_COL + 16 * KS;
+    static constexpr int USED = SQ_COL + 16 * KS;
     static constexpr int COLS = USED <= 64 ? 64 : USED <= 128 ? 128 : 256;   // two CTAs of an SM fit
     static constexpr int RED = BN * MM_P * 4 + 16 * (BN > MM_P ? BN : MM_P);   // the tile, rows 16 bytes apart
     static constexpr int BODY = STAGES * STAGE > RED ? STAGES * STAGE : RED;
@@ -129,15 +141,22 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     // the loading warp sets up the barriers and begins; the others join it
     // behind the __syncthreads below
     const uint8_t *sp = a.p_scales + ((int64_t)pt * a.atoms) * MX4_ATOM;
-    auto load = [&](int k) {
-        const int s = (k - k0) % S::STAGES;
-        const uint32_t p = base + s * S::STAGE, q = p + S::P_BYTES, scp = q + S::Q_BYTES, scq = scp + S::SP_BYTES;
+    const int steps = (k1 - k0 + S::KS - 1) / S::KS;
+    auto load = [&](int i) {
+        const int s = i % S::STAGES;
         if (elect_one()) {
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(S::STAGE) : "memory");
-            tma2d(p, &map_p, k * MM_KB, pt * MM_P, full(s));
-            tma2d(q, &map_q, k * MM_KB, qt * BN, full(s));
-            bulk(scp, sp + (int64_t)k * S::SP_BYTES, S::SP_BYTES, full(s));
-            bulk(scq, a.q_scales + ((int64_t)(BN == 128 ? qt : 0) * a.atoms + 2 * k) * MX4_ATOM, S::SQ_BYTES, full(s));
+            const int n = min(S::KS, k1 - k0 - i * S::KS);
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(n * S::SUB) : "memory");
+#pragma unroll
+            for (int h = 0; h < S::KS; ++h) {
+                if (h >= n) break;
+                const int k = k0 + i * S::KS + h;
+                const uint32_t p = base + s * S::STAGE + h * S::SUB, q = p + S::P_BYTES, scp = q + S::Q_BYTES, scq = scp + S::SP_BYTES;
+                tma2d(p, &map_p, k * MM_KB, pt * MM_P, full(s));
+                tma2d(q, &map_q, k * MM_KB, qt * BN, full(s));
+                bulk(scp, sp + (int64_t)k * S::SP_BYTES, S::SP_BYTES, full(s));
+                bulk(scq, a.q_scales + ((int64_t)(BN == 128 ? qt : 0) * a.atoms + 2 * k) * MX4_ATOM, S::SQ_BYTES, full(s));
+            }
         }
         __syncwarp();
     };
@@ -152,7 +171,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
         }
         __syncwarp();
         pdl_wait();
-        for (; issued < S::STAGES && k0 + issued < k1; ++issued) load(k0 + issued);
+        for (; issued < S::STAGES && issued < steps; ++issued) load(issued);
     }
     if (warp == 5 && elect_one()) {
         asm volatile("prefetch.tensormap [%0];" : : "l"(&map_p) : "memory");
@@ -173,48 +192,53 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     pdl_trigger();                         // tensor memory is allocated: the next kernel may wait for its own
 
     if (warp == 4) {
-        for (; k0 + issued < k1; ++issued) {
+        for (; issued < steps; ++issued) {
             if (!warp_wait(empty(issued % S::STAGES), (uint32_t)((issued / S::STAGES - 1) & 1), MM_WAIT_NS)) {
                 failed = 1;
                 break;
             }
-            load(k0 + issued);
+            load(issued);
         }
     } else if (warp == 5) {
         // kind::mxf4: e2m1 x e2m1, ue8m0 scales, M = 128, N = BN
         const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(BN / 8) << 17) | (1u << 23) | (8u << 24);
-        for (int k = k0; k < k1; ++k) {
-            const int i = k - k0, s = i % S::STAGES;
+        for (int i = 0; i < steps; ++i) {
+            const int s = i % S::STAGES;
             if (!warp_wait(full(s), (uint32_t)((i / S::STAGES) & 1), MM_WAIT_NS)) {
                 failed = 1;
                 break;
             }
             asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
-            const uint32_t p = base + s * S::STAGE, q = p + S::P_BYTES, scp = q + S::Q_BYTES, scq = scp + S::SP_BYTES;
-            const uint32_t tp = tmem + S::SP_COL + 8 * (i & 1), tq = tmem + S::SQ_COL + 8 * (i & 1);
+            const int n = min(S::KS, k1 - k0 - i * S::KS);
             if (elect_one()) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
-                                 :
-                                 : "r"(tp + 4 * j), "l"(mm_desc(scp + j * MX4_ATOM, 128, 0))
-                                 : "memory");
-                    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
-                                 :
-                                 : "r"(tq + 4 * j), "l"(mm_desc(scq + j * MX4_ATOM, 128, 0))
-                                 : "memory");
-                }
+                for (int h = 0; h < S::KS; ++h) {
+                    if (h >= n) break;
+                    const uint32_t p = base + s * S::STAGE + h * S::SUB, q = p + S::P_BYTES, scp = q + S::Q_BYTES, scq = scp + S::SP_BYTES;
+                    const uint32_t tp = tmem + S::SP_COL + 8 * (S::KS * (i & 1) + h), tq = tmem + S::SQ_COL + 8 * (S::KS * (i & 1) + h);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t id = (uint32_t)(2 * (j & 1));        // scale bytes 0-1 or 2-3 of an atom
-                    const uint32_t d = idesc | (id << 4) | (id << 29);
-                    asm volatile(
-                        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-                        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-                        :
-                        : "r"(tmem), "l"(mm_desc(p + 32 * j, 1024, 2)), "l"(mm_desc(q + 32 * j, 1024, 2)), "r"(d),
-                          "r"(tp + 4 * (j >> 1)), "r"(tq + 4 * (j >> 1)), "r"((uint32_t)(i > 0 || j > 0))
-                        : "memory");
+                    for (int j = 0; j < 2; ++j) {
+                        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
+                                     :
+                                     : "r"(tp + 4 * j), "l"(mm_desc(scp + j * MX4_ATOM, 128, 0))
+                                     : "memory");
+                        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
+                                     :
+                                     : "r"(tq + 4 * j), "l"(mm_desc(scq + j * MX4_ATOM, 128, 0))
+                                     : "memory");
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t id = (uint32_t)(2 * (j & 1));        // scale bytes 0-1 or 2-3 of an atom
+                        const uint32_t d = idesc | (id << 4) | (id << 29);
+                        asm volatile(
+                            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+                            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                            :
+                            : "r"(tmem), "l"(mm_desc(p + 32 * j, 1024, 2)), "l"(mm_desc(q + 32 * j, 1024, 2)), "r"(d),
+                              "r"(tp + 4 * (j >> 1)), "r"(tq + 4 * (j >> 1)), "r"((uint32_t)(i > 0 || h > 0 || j > 0))
+                            : "memory");
+                    }
                 }
                 tc_commit(empty(s));
             }
@@ -350,8 +374,8 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
 // 400 of them between its last product and the next tile's first.  What is
 // left is power: in long runs the board holds 1.36 kW.  Clusters of two pairs
 // that share B by multicast took as long (144 of the 152 SMs fit such
-// clusters), and so did scales placed by tcgen05.st in the place of tcgen05.cp
-// when they did not take longer.
+// clusters); scales placed by tcgen05.st in the place of tcgen05.cp took 8192 x
+// 8192 x 8192 387 us and more, where this form took 246 at the time (153 now).
 constexpr int PAIR_ROWS = 256, PAIR_COLS = 256;
 constexpr int PAIR_STAGES = 5;
 constexpr int PAIR_THREADS = 320;         // 8 warps store, 1 loads, 1 multiplies (leader only)
@@ -734,9 +758,10 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *
         if (!p || (reinterpret_cast<uintptr_t>(p) & 15))
             return zs_fail(ZS_EINVAL, "%s: codes or scales NULL or not 16-byte aligned", fn);
     cudaError_t e;
-    // The pair kernel from half a tile a pair on: 768 x 4096 x 4096 (48 tiles)
-    // takes it 10.8 us, the other kernel 12; 512 x 4096 x 4096 (32 tiles) 10.6
-    // and 10.3.
+    // The pair kernel from half a tile a pair on: 640 x 4096 x 4096 (48 tiles)
+    // takes it 10.4 us, the other kernel 11.2; 1024 x 4096 x 14336 (64 tiles)
+    // 21.3 and 25.1; 512 x 4096 x 4096 and 2048 x 1024 x 4096 (32 tiles) 9.6
+    // and 8.5.
     const int64_t pair_p = (m + zsk::PAIR_ROWS - 1) / zsk::PAIR_ROWS, pair_q = (n + zsk::PAIR_COLS - 1) / zsk::PAIR_COLS;
     if (m > 128 && pair_p * pair_q >= 38 && pair_p * pair_q < 0x7FFF0000) {
         CUtensorMap map[4];
@@ -758,8 +783,8 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *
         zs_clear_error();
         return ZS_OK;
     }
-    // 128 features a tile for up to 64 tokens: 64 x 4096 x 4096 6.4 us, 6.5 with
-    // 128 tokens a tile; 16 tokens 5.5 us against 6.5.
+    // 128 features a tile for up to 64 tokens: 64 x 4096 x 4096 5.2 us, 5.8 with
+    // 128 tokens a tile; 48 x 1024 x 4096 4.3 us against 5.0.
     const bool flip = m <= 64;
     const int64_t np = flip ? n : m, nq = flip ? m : n;
     const void *p_codes = flip ? b_codes : a_codes, *p_scales = flip ? b_scales : a_scales;
@@ -779,9 +804,10 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *
     a.p_tiles = (int32_t)pt;
     a.q_tiles = (int32_t)qt;
     // k is shared out while that leaves an SM to every CTA and each enough
-    // stages to hide its part of the sum: one token through 4096 x 4096 takes
-    // 6.4, 5.8, 5.1 and 5.9 us in 1, 2, 4 and 8 parts (32 tiles), and more CTAs
-    // than SMs lose: 14336 x 4096 (112 tiles) 6.7 us in one part, 9.5 in four.
+    // stages to hide its part of the sum.  One token through 4096 x 4096 (32
+    // tiles) took 5.8, 4.9, 4.2 and 4.5 us in 1, 2, 4 and 8 parts, 256 x 4096 x
+    // 14336 (64 tiles) 17.3, 12.5 and 14.4 us in 1, 2 and 4; more CTAs than SMs
+    // lose: 16 x 14336 x 4096 (112 tiles) 6.2 us in one part, 9.7 in four.
     int split = 1;
     while (split < 8 && pt * qt * split * 2 <= 152 && a.k_tiles >= (bn == 128 ? 8 : 4) * split) split *= 2;
     if (pt * qt * split > 0x7FFFFFFF) return zs_fail(ZS_EINVAL, "%s: too many tiles", fn);
