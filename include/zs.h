@@ -431,7 +431,8 @@ zs_status zs_all_gather_coalesced(const zs_plan *plan, int32_t n, const int32_t 
  * its bytes with TMA bulk copies through shared memory, one mbarrier wait
  * per chunk; a wait that does not complete within a bound (about a second)
  * is abandoned, the gather's output is then incomplete, and this counter
- * goes up.  Synchronous (reads device memory).  reset != 0 sets it back to
+ * goes up.  zs_adam_tensors with 8-bit moments, zs_mx4_quantize and
+ * zs_mx4_matmul bound and count their waits the same way.  Synchronous (reads device memory).  reset != 0 sets it back to
  * 0.  Returns ZS_ETIMEOUT, with *count filled, when the count is not 0.
  * Has no counterpart in the pages: it is this library's report of its own
  * bounded waits.  Errors: ZS_EINVAL (NULL count), ZS_ECUDA. */
@@ -625,7 +626,10 @@ zs_status zs_sched_log(const zs_sched *sched, zs_sched_event *out, int64_t cap, 
  * parameters that the products read in 0.53 instead of 2.  They have no
  * counterpart on the pages and need no plan: they work on any device
  * memory, a plan's buffers among it (a rank's shard row, a gathered
- * parameter, a reduce bucket entry).
+ * parameter, a reduce bucket entry).  Their kernels are launched so that a
+ * following call's may begin to set up while they finish (programmatic
+ * dependent launch); it touches memory only after they have completed, so
+ * stream order holds as for every other call.
  *
  * Adam(W) over a list of tensors. */
 typedef struct zs_tensors zs_tensors;   /* opaque, host memory */
@@ -641,7 +645,7 @@ typedef struct {
 } zs_tensors_config;
 
 /* One tensor: device pointers, each aligned to its element type at least
- * (16 bytes on all of them, 8 on 8-bit moments, takes the vector path).
+ * (16 bytes on all of them but the scales takes the vector path).
  * With state_bits 8 the moments are blocks of 256 consecutive elements (the
  * last block may be short): codes of one byte each in IEEE-like e4m3 and one
  * float32 scale a block, so that
@@ -692,7 +696,9 @@ zs_status zs_tensors_upload(zs_tensors *list, void *d_table, int64_t bytes, void
  *   AdamW: p = p - (lr*wd)*p        |  Adam-L2: g = g + wd*p
  *   m = b1*m + (1-b1)*g;  r = sqrt(b2*(r*r) + (1-b2)*(g*g))
  *   p = p - (lr/bc1) * (m / (r*(1/sqrt(bc2)) + eps));  param = rne16(p)
- *   with lr/bc1 and 1/sqrt(bc2) computed in double and rounded to fp32; then
+ *   with lr/bc1 and 1/sqrt(bc2) computed in double and rounded to fp32, and
+ *   the quotient m/(..) good to 2 units in its last place, 2^-22 of one
+ *   update (every other operation is correctly rounded); then
  *   a block's scale is 2^(floor(log2 max) - 7) of its new |m| (of its r), at
  *   least 2^-126, and the codes are m/scale and r/scale in e4m3.
  *   ZS_ROUND_NEAREST: to nearest even.  ZS_ROUND_STOCHASTIC: to one of the
@@ -706,7 +712,8 @@ zs_status zs_tensors_upload(zs_tensors *list, void *d_table, int64_t bytes, void
  *   A positive r never gets code 0, which would divide an update by eps.
  *   An element whose m or r is not finite gets a NaN code and does not count
  *   for the scale.
- * step >= 1.  Errors: ZS_EINVAL, ZS_ESTATE (not uploaded), ZS_ECUDA. */
+ * step >= 1.  Errors: ZS_EINVAL, ZS_ESTATE (not uploaded), ZS_ECUDA; a
+ * device wait that gave up is counted by zs_device_wait_timeouts. */
 zs_status zs_adam_tensors(const zs_tensors *list, const zs_adam_hparams *hp, int64_t step,
                           int32_t rounding, uint64_t seed, const float *d_clip_coef,
                           const int32_t *d_flags, void *stream);
@@ -734,7 +741,8 @@ zs_status zs_mx4_sizes(int64_t rows, int64_t cols, int64_t *row_bytes, int64_t *
  * for a group of zeros or of fp32 subnormals), and the codes of
  * x * 2^(127-s) to nearest, ties to even, at most 6 in magnitude.  A group
  * with an infinity or NaN has s = 255 and codes 0: it is NaN in every
- * product.  Errors: ZS_EINVAL, ZS_ECUDA. */
+ * product.  Errors: ZS_EINVAL, ZS_ECUDA; a device wait that gave up is
+ * counted by zs_device_wait_timeouts. */
 zs_status zs_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
                           void *r_codes, void *r_scales, void *c_codes, void *c_scales,
                           void *stream);

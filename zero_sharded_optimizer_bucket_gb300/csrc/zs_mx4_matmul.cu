@@ -14,10 +14,11 @@
 //    short runs; 156-160 us, 6.0-6.2 PFLOP/s in long ones, which run at the
 //    board's 1.4 kW (the clock falls to 1.9 GHz and below).
 //  - smaller ones: mx4_matmul_kernel, tiles of 128 rows, k shared out over a
-//    cluster when the tiles are few.  One token through 4096 x 14336: 6.2 us,
-//    5.1 TB/s of weight bytes; 16 through 14336 x 4096: 5.3 us, 6.0 TB/s;
-//    256 x 4096 x 4096: 8.0 us.  What is left there is the latency of a chain
-//    of few stages and the 2.1 us of a launch that computes nothing.
+//    cluster when the tiles are few.  One token through 4096 x 14336: 8.1 us
+//    from HBM, 3.8 TB/s of weight bytes, 6.2 from L2; 16 through 14336 x 4096:
+//    7.4 and 5.3 us; 256 x 4096 x 4096 from L2: 8.4 us.  What is left there is
+//    the latency of a chain of few stages and the 2.1 us of a launch that
+//    computes nothing.
 #include <atomic>
 
 #include "zs_launch.h"
@@ -39,22 +40,26 @@ struct MmShape {
     static constexpr int SP_BYTES = 2 * MX4_ATOM, SQ_BYTES = 2 * MX4_ATOM;
     static constexpr int SUB = P_BYTES + Q_BYTES + SP_BYTES + SQ_BYTES;      // 256 elements of k, a multiple of 1024
     // Of them a stage.  Waiting for a stage and releasing it costs the issuing
-    // warp about as much as its products, so two where they fit: 16 x 14336 x
-    // 4096 takes 6.46 us with four stages of one, 5.32 with two of two.  What
-    // two CTAs of an SM cannot hold loses, because the next kernel's CTAs then
-    // begin later: three of two 5.05 us there, but 16 x 4096 x 4096 4.50
-    // against 4.20; for 128 columns two of two lose, 128 x 4096 x 4096 7.9 us
-    // against 7.6.
+    // warp about as much as its products, so two where enough fit: 16 x 14336
+    // x 4096 from L2 takes 6.46 us with four stages of one, 5.32 with two of
+    // two; for 128 columns two of two lost to three of one, 128 x 4096 x 4096
+    // 7.9 us against 7.6.
     static constexpr int KS = BN == 128 ? 1 : 2;
     static constexpr int STAGE = KS * SUB;
-    static constexpr int STAGES = BN == 128 ? 3 : 2;
+    // At most; a launch takes no more than its parts of k fill, so that two
+    // CTAs share an SM where parts are short and the next kernel's begin
+    // early (1 x 4096 x 4096 3.9 us, with four always 4.2).  Bytes in flight
+    // count where the matrix is not in L2: 1 x 4096 x 14336 9.6, 8.5, 8.1 and
+    // 8.3 us with 2, 3, 4 and 5 of two; 256 x 4096 x 14336 16.8, 15.0 and 13.7
+    // with 3, 4 and 6 of one (from L2, 256 x 4096 x 4096 8.0, 8.2 and 8.4).
+    static constexpr int STAGES = BN == 128 ? 6 : 4;
     // tensor memory: accumulator, then two sets of scales
     static constexpr int SP_COL = BN < 32 ? 32 : BN, SQ_COL = SP_COL + 16 * KS;
     static constexpr int USED = SQ_COL + 16 * KS;
     static constexpr int COLS = USED <= 64 ? 64 : USED <= 128 ? 128 : 256;   // two CTAs of an SM fit
     static constexpr int RED = BN * MM_P * 4 + 16 * (BN > MM_P ? BN : MM_P);   // the tile, rows 16 bytes apart
-    static constexpr int BODY = STAGES * STAGE > RED ? STAGES * STAGE : RED;
-    static constexpr int SMEM = BODY + 1024;                   // and room to align
+    static constexpr int smem(int stages) { return (stages * STAGE > RED ? stages * STAGE : RED) + 1024; }   // with room to align
+    static constexpr int SMEM = smem(STAGES);
 };
 
 struct MmArgs {
@@ -65,6 +70,7 @@ struct MmArgs {
     int32_t k_tiles, atoms;   // stages along k, scale atoms a row tile
     int32_t p_tiles, q_tiles;
     int32_t split;            // CTAs of the cluster that share the tile's k
+    int32_t stages;           // of the ring
     int32_t dtype;
     int32_t vec;              // rows of out are aligned to 4 elements
 };
@@ -134,6 +140,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     const uint32_t bar0 = smem_u32(bars), done = bar0 + 16 * S::STAGES;
     auto full = [&](int s) { return bar0 + 8 * s; };
     auto empty = [&](int s) { return bar0 + 8 * (S::STAGES + s); };
+    const int stages = a.stages;
     const int part = a.split > 1 ? (int)(blockIdx.x % a.split) : 0;
     const int tile = (int)(blockIdx.x / a.split);
     const int pt = tile % a.p_tiles, qt = tile / a.p_tiles;
@@ -142,8 +149,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     // behind the __syncthreads below
     const uint8_t *sp = a.p_scales + ((int64_t)pt * a.atoms) * MX4_ATOM;
     const int steps = (k1 - k0 + S::KS - 1) / S::KS;
-    auto load = [&](int i) {
-        const int s = i % S::STAGES;
+    auto load = [&](int i, int s) {
         if (elect_one()) {
             const int n = min(S::KS, k1 - k0 - i * S::KS);
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(n * S::SUB) : "memory");
@@ -160,7 +166,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
         }
         __syncwarp();
     };
-    int issued = 0;                        // stages that warp 4 issued loads for
+    int issued = 0, slot = 0;              // stages that warp 4 issued loads for; the next one's place
     if (warp == 4) {
         if (elect_one()) {
             failed = 0;
@@ -171,7 +177,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
         }
         __syncwarp();
         pdl_wait();
-        for (; issued < S::STAGES && issued < steps; ++issued) load(issued);
+        for (; issued < stages && issued < steps; ++issued) load(issued, issued);
     }
     if (warp == 5 && elect_one()) {
         asm volatile("prefetch.tensormap [%0];" : : "l"(&map_p) : "memory");
@@ -192,19 +198,25 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     pdl_trigger();                         // tensor memory is allocated: the next kernel may wait for its own
 
     if (warp == 4) {
+        uint32_t phase = 0;
         for (; issued < steps; ++issued) {
-            if (!warp_wait(empty(issued % S::STAGES), (uint32_t)((issued / S::STAGES - 1) & 1), MM_WAIT_NS)) {
+            if (!warp_wait(empty(slot), phase, MM_WAIT_NS)) {
                 failed = 1;
                 break;
             }
-            load(issued);
+            load(issued, slot);
+            if (++slot == stages) {
+                slot = 0;
+                phase ^= 1;
+            }
         }
     } else if (warp == 5) {
         // kind::mxf4: e2m1 x e2m1, ue8m0 scales, M = 128, N = BN
         const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(BN / 8) << 17) | (1u << 23) | (8u << 24);
+        int s = 0;
+        uint32_t phase = 0;
         for (int i = 0; i < steps; ++i) {
-            const int s = i % S::STAGES;
-            if (!warp_wait(full(s), (uint32_t)((i / S::STAGES) & 1), MM_WAIT_NS)) {
+            if (!warp_wait(full(s), phase, MM_WAIT_NS)) {
                 failed = 1;
                 break;
             }
@@ -243,6 +255,10 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
                 tc_commit(empty(s));
             }
             __syncwarp();
+            if (++s == stages) {
+                s = 0;
+                phase ^= 1;
+            }
         }
         if (elect_one()) tc_commit(done);
         __syncwarp();
@@ -349,8 +365,8 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     if (a.split > 1) asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" : : : "memory");
     if (warp == 4 && lane == 0 && failed) {
         // let the loads already issued land before the shared memory goes away
-        for (int i = issued > S::STAGES ? issued - S::STAGES : 0; i < issued; ++i)
-            mbar_wait_quick(full(i % S::STAGES), (uint32_t)((i / S::STAGES) & 1), MM_WAIT_NS);
+        for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+            mbar_wait_quick(full(i % stages), (uint32_t)((i / stages) & 1), MM_WAIT_NS);
         atomicAdd(&g_mx4_wait_timeouts, 1);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
@@ -705,7 +721,7 @@ static cudaError_t pair_launch(const CUtensorMap (&map)[4], const PairArgs &a, c
 }
 
 template <int BN, bool FLIP>
-static cudaError_t mm_launch(const CUtensorMap &p, const CUtensorMap &q, const MmArgs &a, cudaStream_t s) {
+static cudaError_t mm_launch(const CUtensorMap &p, const CUtensorMap &q, MmArgs &a, cudaStream_t s) {
     using S = MmShape<BN>;
     static std::atomic<int> known[64];
     int sms = 0;
@@ -713,7 +729,9 @@ static cudaError_t mm_launch(const CUtensorMap &p, const CUtensorMap &q, const M
         return cudaFuncSetAttribute(mx4_matmul_kernel<BN, FLIP>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     }, &sms);
     if (e != cudaSuccess) return e;
-    return launch_dependent(mx4_matmul_kernel<BN, FLIP>, (unsigned)((int64_t)a.p_tiles * a.q_tiles * a.split), MM_THREADS, S::SMEM,
+    const int steps = ((a.k_tiles + a.split - 1) / a.split + S::KS - 1) / S::KS;     // of the longest part
+    a.stages = steps < S::STAGES ? steps : S::STAGES;
+    return launch_dependent(mx4_matmul_kernel<BN, FLIP>, (unsigned)((int64_t)a.p_tiles * a.q_tiles * a.split), MM_THREADS, S::smem(a.stages),
                             (unsigned)a.split, s, p, q, a);
 }
 
