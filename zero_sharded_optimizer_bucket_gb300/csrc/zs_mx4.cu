@@ -14,45 +14,6 @@ namespace zsk {
 constexpr int QT = 128;      // a CTA takes a tile of 128 x 128: one scale atom each way
 
 
-// 8 consecutive elements of a row as floats, zero outside the matrix
-template <class T, bool F32, bool VEC>
-struct Row8 {
-    uint4 w[F32 ? 2 : 1];
-    __device__ __forceinline__ void load(const void *x, int64_t at, int n) {
-        if (n <= 0) {
-#pragma unroll
-            for (auto &v : w) v = make_uint4(0, 0, 0, 0);
-        } else if (VEC && n >= 8) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(x) + at * (F32 ? 4 : 2));
-#pragma unroll
-            for (int i = 0; i < (F32 ? 2 : 1); ++i) w[i] = p[i];
-        } else {
-            uint32_t r[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                r[i] = i < n ? (F32 ? static_cast<const uint32_t *>(x)[at + i]
-                                    : (uint32_t)static_cast<const uint16_t *>(x)[at + i]) : 0u;
-            if (F32) {
-                w[0] = make_uint4(r[0], r[1], r[2], r[3]);
-                w[F32 ? 1 : 0] = make_uint4(r[4], r[5], r[6], r[7]);
-            } else {
-                w[0] = pack8(r);
-            }
-        }
-    }
-    __device__ __forceinline__ void get(float y[8]) const {
-        if (F32) {
-            y[0] = __uint_as_float(w[0].x); y[1] = __uint_as_float(w[0].y);
-            y[2] = __uint_as_float(w[0].z); y[3] = __uint_as_float(w[0].w);
-            y[4] = __uint_as_float(w[F32 ? 1 : 0].x); y[5] = __uint_as_float(w[F32 ? 1 : 0].y);
-            y[6] = __uint_as_float(w[F32 ? 1 : 0].z); y[7] = __uint_as_float(w[F32 ? 1 : 0].w);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = T::to_f32(lane16(w[0], i));
-        }
-    }
-};
-
 // m = the larger magnitudes of two pairs of 16-bit values; a NaN stays
 template <class T>
 __device__ __forceinline__ void max_abs2(uint32_t &m, uint32_t w);
@@ -75,26 +36,10 @@ __device__ __forceinline__ uint32_t encode_floats(float y[8], unsigned long long
     }
     return e2m1x8(y);
 }
-template <class T>
-__device__ __forceinline__ uint32_t encode_words(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, unsigned long long inv) {
-    float y[8];
-    const uint32_t w[4] = {w0, w1, w2, w3};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = T::to_f32(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu);
-    return encode_floats(y, inv);
+// m = the larger of m and |x|; a NaN stays
+__device__ __forceinline__ void max_abs(float &m, float x) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(x)));
 }
-
-// codes of 8 values of a group whose scale byte is known
-__device__ __forceinline__ uint32_t mx4_encode8(const float y[8], uint32_t byte) {
-    if (byte == 255u) return 0u;
-    const float inv = mx4_inverse(byte);
-    float z[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = __fmul_rn(y[i], inv);
-    return e2m1x8(z);
-}
-
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 struct Mx4Args {
     const void *x;
@@ -104,188 +49,177 @@ struct Mx4Args {
     int64_t tiles_c;                 // tiles along the columns of the grid
 };
 
-template <class T, bool F32, bool VEC, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(256)
-mx4_quantize_kernel(Mx4Args a) {
-    extern __shared__ __align__(16) uint8_t tile[];              // COLS: the tile as it was read
-    __shared__ __align__(16) uint8_t rs[MX4_ATOM], cs[MX4_ATOM];
-    constexpr int ES = F32 ? 4 : 2;
-    const int t = threadIdx.x;
-    pdl_wait();
-    pdl_trigger();
-    const int64_t rt = blockIdx.x / a.tiles_c, ct = blockIdx.x - rt * a.tiles_c;
-    const int64_t row0 = rt * QT, col0 = ct * QT;
-    const int c8 = (t & 15) * 8;
-    const int ncol = (int)min((int64_t)QT, a.cols - col0) - c8;  // of this thread's 8
-    constexpr int PASSES = QT / 16;
-    Row8<T, F32, VEC> v[PASSES];
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const int64_t row = row0 + 16 * i + (t >> 4);
-        v[i].load(a.x, row * a.ld + col0 + c8, row < a.rows ? ncol : 0);
-    }
-    const int64_t row_bytes = mx4_row_bytes(a.cols);
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const int r = 16 * i + (t >> 4);
-        if (COLS) {
-            uint4 *dst = reinterpret_cast<uint4 *>(tile + ((size_t)r * QT + c8) * ES);
-#pragma unroll
-            for (int j = 0; j < (F32 ? 2 : 1); ++j) dst[j] = v[i].w[j];
-        }
-        if (ROWS) {
-            float y[8];
-            v[i].get(y);
-            uint32_t top = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) top = max(top, abs_bits(y[j]));
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            const uint32_t byte = mx4_scale_byte(top >> 23);
-            if ((t & 3) == 0) rs[mx4_in_atom(r, (t & 15) >> 2)] = (uint8_t)byte;
-            const int64_t at = (col0 + c8) / 2;
-            if (row0 + r < a.rows && at < row_bytes)
-                *reinterpret_cast<uint32_t *>(a.r_codes + (row0 + r) * row_bytes + at) = mx4_encode8(y, byte);
-        }
-    }
-    __syncthreads();
-    if (COLS) {
-        // a thread takes 32 rows of two neighbouring columns
-        const int c = 2 * (t & 63), g = t >> 6;
-        float y[2][32];
-        uint32_t top[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const size_t at = (size_t)(32 * g + i) * QT + c;
-            if (F32) {
-                const float2 w = *reinterpret_cast<const float2 *>(tile + at * ES);
-                y[0][i] = w.x;
-                y[1][i] = w.y;
-            } else {
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(tile + at * ES);
-                y[0][i] = T::to_f32(w & 0xFFFFu);
-                y[1][i] = T::to_f32(w >> 16);
-            }
-            top[0] = max(top[0], abs_bits(y[0][i]));
-            top[1] = max(top[1], abs_bits(y[1][i]));
-        }
-        const int64_t bytes = mx4_row_bytes(a.rows), at = row0 / 2 + 16 * g;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t byte = mx4_scale_byte(top[j] >> 23);
-            cs[mx4_in_atom(c + j, g)] = (uint8_t)byte;
-            if (col0 + c + j < a.cols && at < bytes)
-                *reinterpret_cast<uint4 *>(a.c_codes + (col0 + c + j) * bytes + at) =
-                    make_uint4(mx4_encode8(y[j], byte), mx4_encode8(y[j] + 8, byte),
-                               mx4_encode8(y[j] + 16, byte), mx4_encode8(y[j] + 24, byte));
-        }
-        __syncthreads();
-    }
-    // the tile's scale atoms, padding (zero values: scale byte 0) included
-    if (ROWS && t < 32 && rt < mx4_row_tiles(a.rows))
-        reinterpret_cast<uint4 *>(a.r_scales + (rt * mx4_atoms(a.cols) + ct) * MX4_ATOM)[t] =
-            reinterpret_cast<const uint4 *>(rs)[t];
-    if (COLS && t >= 32 && t < 64 && ct < mx4_row_tiles(a.cols))
-        reinterpret_cast<uint4 *>(a.c_scales + (ct * mx4_atoms(a.rows) + rt) * MX4_ATOM)[t - 32] =
-            reinterpret_cast<const uint4 *>(cs)[t - 32];
+// The scale byte of a group and the factor of its values (0 for a NaN group,
+// whose codes are 0), from its largest magnitude.
+struct Mx4Scale {
+    uint32_t byte;
+    float inv;
+    // a code word of the group
+    __device__ __forceinline__ uint32_t codes(float y[8]) const { return byte == 255u ? 0u : encode_floats(y, f2pack(inv, inv)); }
+};
+__device__ __forceinline__ Mx4Scale mx4_scale(float top) {
+    const uint32_t byte = mx4_scale_byte(__float_as_uint(top) >> 23);
+    return {byte, byte == 255u ? 0.0f : mx4_inverse(byte)};
 }
 
-// 16-bit matrices whose rows are 16-byte aligned: a persistent CTA walks tiles,
-// fetched ahead by tensor copies (two boxes of 64 columns, 128-byte swizzle;
-// zeros outside the matrix) into a ring of stages, and makes both forms from
-// shared memory.  Along the rows 4 lanes share a group, 8 elements each; along
-// the columns a thread takes 32 rows of two neighbouring columns; neither
-// access has a bank conflict under the swizzle.  Bandwidth bounds it: 2 bytes
-// read and 0.53 written an element and form.
+// A persistent CTA walks tiles, each in units of 32 KB (a tile of 16-bit
+// values, or half the columns of an fp32 one), and makes both forms from shared
+// memory.  A unit lies there as two boxes of 128 rows by 128 bytes, 16-byte
+// pieces turned by the row (128-byte swizzle).  Along the rows a thread takes
+// groups of 32 elements; along the columns, 32 rows of two neighbouring
+// columns (fp32: of one); neither has a bank conflict under the swizzle, and a
+// warp's stores fill sectors.  Bandwidth bounds it: 2 or 4 bytes read and 0.53
+// written an element and form.
+// BOXES: the rows of x are 16-byte aligned, and tensor copies fetch the units
+// ahead into a ring of stages, with zeros outside the matrix.  Otherwise lanes
+// load neighbouring elements of a row, whatever its address; the CTAs of an SM
+// overlap one another's loads.
 // 8 warps on three CTAs an SM; for both forms every warp makes one after the
 // other (8 warps for each on two CTAs took 34 us for 14336 x 4096, this 30).
-constexpr int QS_BOX = 64 * 128 * 2, QS_STAGE = 2 * QS_BOX, QS_STAGES = 2, QS_CTAS = 3;
-constexpr int QS_SMEM = QS_STAGES * QS_STAGE + 1024;
+constexpr int QS_BOX = 128 * 128, QS_STAGE = 2 * QS_BOX, QS_STAGES = 2, QS_CTAS = 3;
 constexpr uint64_t QS_WAIT_NS = 1000000000ull;       // one wait gives up after 1 s
+constexpr int qs_smem(bool boxes) { return (boxes ? QS_STAGES : 1) * QS_STAGE + 1024; }
 
 __device__ int g_quantize_wait_timeouts;             // waits that gave up
 
-template <class T, bool ROWS, bool COLS>
+template <class T, bool F32, bool BOXES, bool ROWS, bool COLS>
 __global__ void __launch_bounds__(256, QS_CTAS)
-mx4_quantize_tiles_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, int tiles) {
+mx4_quantize_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, int tiles) {
+    constexpr int UNITS = F32 ? 2 : 1;               // of a tile
+    constexpr int BOX_COLS = F32 ? 32 : 64, UNIT_COLS = 2 * BOX_COLS;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(16) uint8_t rs[2][MX4_ATOM], cs[2][MX4_ATOM];
     __shared__ __align__(8) uint64_t bars[QS_STAGES];
     const int t = threadIdx.x;
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u, bar = smem_u32(bars);
     const int tiles_c = (int)a.tiles_c;
-    auto fetch = [&](int i) {                        // the i-th tile of this CTA
-        const int tile = (int)blockIdx.x + i * (int)gridDim.x, s = i % QS_STAGES;
+    auto fetch = [&](int u) {                        // the u-th unit of this CTA
+        const int tile = (int)blockIdx.x + u / UNITS * (int)gridDim.x, s = u % QS_STAGES;
         const int rt = tile / tiles_c, ct = tile - rt * tiles_c;
+        const int col = ct * QT + u % UNITS * UNIT_COLS;
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(bar + 8 * s), "r"(QS_STAGE) : "memory");
-        tma2d(base + s * QS_STAGE, &map, ct * QT, rt * QT, bar + 8 * s);
-        tma2d(base + s * QS_STAGE + QS_BOX, &map, ct * QT + 64, rt * QT, bar + 8 * s);
+        tma2d(base + s * QS_STAGE, &map, col, rt * QT, bar + 8 * s);
+        tma2d(base + s * QS_STAGE + QS_BOX, &map, col + BOX_COLS, rt * QT, bar + 8 * s);
     };
-    const int mine = ((int)(tiles - blockIdx.x) + (int)gridDim.x - 1) / (int)gridDim.x;
-    if (t == 0) {
+    const int mine = ((int)(tiles - blockIdx.x) + (int)gridDim.x - 1) / (int)gridDim.x * UNITS;
+    if (BOXES && t == 0) {
         for (int i = 0; i < QS_STAGES; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" : : "r"(bar + 8 * i) : "memory");
         asm volatile("fence.proxy.async.shared::cta;" : : : "memory");
+    }
+    if (!BOXES || t == 0) {
         pdl_wait();
         pdl_trigger();
-        for (int i = 0; i < QS_STAGES && i < mine; ++i) fetch(i);
     }
+    if (BOXES && t == 0)
+        for (int u = 0; u < QS_STAGES && u < mine; ++u) fetch(u);
     __syncthreads();
     const int64_t r_bytes = mx4_row_bytes(a.cols), c_bytes = mx4_row_bytes(a.rows);
     const int64_t r_atoms = mx4_atoms(a.cols), c_atoms = mx4_atoms(a.rows);
-    for (int i = 0; i < mine; ++i) {
-        const int tile = (int)blockIdx.x + i * (int)gridDim.x, s = i % QS_STAGES;
+    for (int u = 0; u < mine; ++u) {
+        const int i = u / UNITS, half = u % UNITS;
+        const int tile = (int)blockIdx.x + i * (int)gridDim.x, s = BOXES ? u % QS_STAGES : 0;
         const int64_t rt = tile / tiles_c, ct = tile - rt * tiles_c;
-        const int64_t row0 = rt * QT, col0 = ct * QT;
+        const int64_t row0 = rt * QT, col0 = ct * QT + half * UNIT_COLS;
         const uint32_t at = base + s * QS_STAGE;
-        bool landed = true;
-        if (t < 32) landed = mbar_wait_quick(bar + 8 * s, (uint32_t)((i / QS_STAGES) & 1), QS_WAIT_NS);
-        if (!__syncthreads_and(landed)) {
-            // give up, once the copies in flight have landed
-            if (t == 0) {
-                atomicAdd(&g_quantize_wait_timeouts, 1);
-                for (int j = i; j < i + QS_STAGES && j < mine; ++j)
-                    mbar_wait_quick(bar + 8 * (j % QS_STAGES), (uint32_t)((j / QS_STAGES) & 1), QS_WAIT_NS);
+        if (BOXES) {
+            bool landed = true;
+            if (t < 32) landed = mbar_wait_quick(bar + 8 * s, (uint32_t)((u / QS_STAGES) & 1), QS_WAIT_NS);
+            if (!__syncthreads_and(landed)) {
+                // give up, once the copies in flight have landed
+                if (t == 0) {
+                    atomicAdd(&g_quantize_wait_timeouts, 1);
+                    for (int j = u; j < u + QS_STAGES && j < mine; ++j)
+                        mbar_wait_quick(bar + 8 * (j % QS_STAGES), (uint32_t)((j / QS_STAGES) & 1), QS_WAIT_NS);
+                }
+                __syncthreads();
+                return;
             }
-            __syncthreads();
-            return;
-        }
-        if (ROWS) {
-            // a thread takes a group: 4 lanes a row, 8 rows a warp.  The second
-            // box's pieces are read two apart in turn, so that 8 lanes meet 8
-            // different pieces of the banks.
-            const int g = t & 3, box = g >> 1;
+        } else {
+            // a warp takes every 8th row; LOADS loads of a lane in flight
+            constexpr int A_ROW = UNIT_COLS / 32, LOADS = 32, PER = LOADS / A_ROW;
+            const int lane = t & 31;
+#pragma unroll 1
+            for (int r0 = t >> 5; r0 < QT; r0 += 8 * PER) {
+                uint32_t w[LOADS];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = 64 * j + (t >> 2);
-                uint32_t w[16], two = 0;
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int piece = 4 * (g & 1) + (h ^ (2 * box));
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[4 * h]), "=r"(w[4 * h + 1]), "=r"(w[4 * h + 2]), "=r"(w[4 * h + 3])
-                                 : "r"(at + box * QS_BOX + 128 * r + 16 * (piece ^ (r & 7))));
+                for (int j = 0; j < LOADS; ++j) {
+                    const int64_t row = row0 + r0 + 8 * (j / A_ROW), col = col0 + 32 * (j % A_ROW) + lane;
+                    w[j] = 0;
+                    if (row < a.rows && col < a.cols)
+                        w[j] = F32 ? static_cast<const uint32_t *>(a.x)[row * a.ld + col]
+                                   : (uint32_t)static_cast<const uint16_t *>(a.x)[row * a.ld + col];
                 }
 #pragma unroll
-                for (int h = 0; h < 16; ++h) max_abs2<T>(two, w[h]);
-                const uint32_t byte = mx4_scale_byte(__float_as_uint(T::to_f32(max(two & 0xFFFFu, two >> 16))) >> 23);
-                const float inv = byte == 255u ? 0.0f : mx4_inverse(byte);
-                uint32_t q[4];
+                for (int j = 0; j < LOADS; ++j) {
+                    const int r = r0 + 8 * (j / A_ROW), c = 32 * (j % A_ROW) + lane, b = (c % BOX_COLS) * (F32 ? 4 : 2);
+                    const uint32_t to = at + c / BOX_COLS * QS_BOX + 128 * r + 16 * ((b >> 4) ^ (r & 7)) + (b & 15);
+                    if (F32) asm volatile("st.shared.b32 [%0], %1;" : : "r"(to), "r"(w[j]) : "memory");
+                    else asm volatile("st.shared.u16 [%0], %1;" : : "r"(to), "h"((uint16_t)w[j]) : "memory");
+                }
+            }
+            __syncthreads();
+        }
+        if (ROWS) {
+            // a thread takes a group, of 64 or 128 bytes of a row.  The second
+            // box's pieces are read two (fp32: four) apart in turn, so that 8
+            // lanes meet 8 different pieces of the banks.
+            constexpr int A_ROW = UNIT_COLS / 32;    // groups
+            const int g = t % A_ROW, box = g / (A_ROW / 2);
 #pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    q[h] = byte == 255u ? 0u : encode_words<T>(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3], f2pack(inv, inv));
-                rs[i & 1][mx4_in_atom(r, g)] = (uint8_t)byte;
+            for (int j = 0; j < A_ROW / 2; ++j) {
+                const int r = 256 / A_ROW * j + t / A_ROW;
+                uint32_t q[4];
+                uint32_t byte;
+                if constexpr (F32) {
+                    float w[32], top = 0.0f;
+#pragma unroll
+                    for (int h = 0; h < 8; ++h)
+                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(w[4 * h]), "=f"(w[4 * h + 1]), "=f"(w[4 * h + 2]), "=f"(w[4 * h + 3])
+                                     : "r"(at + box * QS_BOX + 128 * r + 16 * (h ^ (4 * box) ^ (r & 7))));
+#pragma unroll
+                    for (int h = 0; h < 32; ++h) max_abs(top, w[h]);
+                    const Mx4Scale sc = mx4_scale(top);
+                    byte = sc.byte;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) q[h] = sc.codes(w + 8 * h);
+                } else {
+                    uint32_t w[16], two = 0;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const int piece = 4 * (g & 1) + (h ^ (2 * box));
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[4 * h]), "=r"(w[4 * h + 1]), "=r"(w[4 * h + 2]), "=r"(w[4 * h + 3])
+                                     : "r"(at + box * QS_BOX + 128 * r + 16 * (piece ^ (r & 7))));
+                    }
+#pragma unroll
+                    for (int h = 0; h < 16; ++h) max_abs2<T>(two, w[h]);
+                    const Mx4Scale sc = mx4_scale(T::to_f32(max(two & 0xFFFFu, two >> 16)));
+                    byte = sc.byte;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        float y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = T::to_f32(e & 1 ? w[4 * h + (e >> 1)] >> 16 : w[4 * h + (e >> 1)] & 0xFFFFu);
+                        q[h] = sc.codes(y);
+                    }
+                }
+                rs[i & 1][mx4_in_atom(r, A_ROW * half + g)] = (uint8_t)byte;
                 if (row0 + r < a.rows && col0 / 2 + 16 * g < r_bytes)
                     *reinterpret_cast<uint4 *>(a.r_codes + (row0 + r) * r_bytes + col0 / 2 + 16 * g) =
                         box ? make_uint4(q[2], q[3], q[0], q[1]) : make_uint4(q[0], q[1], q[2], q[3]);
             }
         }
         if (COLS) {
-            // a thread takes 32 rows of two columns; lanes 16 on the same
-            // columns' next 32, so that a warp's stores fill sectors.  They
-            // read rows 4 apart in turn: other pieces of the banks.
+            // a thread takes 32 rows of a word (two columns, or one fp32);
+            // lanes 16 on the same words' next 32, so that a warp's stores
+            // fill sectors.  They read rows 4 apart in turn: other pieces of
+            // the banks.
+            constexpr int COLUMNS = F32 ? 1 : 2;     // of a word
             const int upper = (t >> 4) & 1, g = 2 * (t >> 7) + upper;
-            const int box = (t >> 5) & 1, word = 16 * ((t >> 6) & 1) + (t & 15), c = 64 * box + 2 * word;
+            const int box = (t >> 5) & 1, word = 16 * ((t >> 6) & 1) + (t & 15), c = BOX_COLS * box + COLUMNS * word;
             uint32_t w[32], two = 0;
+            float top = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {            // rows e, e + 8, ...: the same turn of the swizzle
                 const int r = e ^ (4 * upper);
@@ -294,19 +228,23 @@ mx4_quantize_tiles_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, in
                 for (int h = 0; h < 4; ++h) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[8 * h + e]) : "r"(from + 1024 * h));
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) max_abs2<T>(two, w[e]);
+            for (int e = 0; e < 32; ++e) {
+                if constexpr (F32) max_abs(top, __uint_as_float(w[e]));
+                else max_abs2<T>(two, w[e]);
+            }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t byte = mx4_scale_byte(__float_as_uint(T::to_f32(j ? two >> 16 : two & 0xFFFFu)) >> 23);
-                const float inv = byte == 255u ? 0.0f : mx4_inverse(byte);
-                cs[i & 1][mx4_in_atom(c + j, g)] = (uint8_t)byte;
+            for (int j = 0; j < COLUMNS; ++j) {
+                if constexpr (!F32) top = T::to_f32(j ? two >> 16 : two & 0xFFFFu);
+                const Mx4Scale sc = mx4_scale(top);
+                cs[i & 1][mx4_in_atom(half * UNIT_COLS + c + j, g)] = (uint8_t)sc.byte;
                 uint32_t q[4];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     float y[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = T::to_f32(j ? w[8 * h + e] >> 16 : w[8 * h + e] & 0xFFFFu);
-                    const uint32_t x = byte == 255u ? 0u : encode_floats(y, f2pack(inv, inv));
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = F32 ? __uint_as_float(w[8 * h + e]) : T::to_f32(j ? w[8 * h + e] >> 16 : w[8 * h + e] & 0xFFFFu);
+                    const uint32_t x = sc.codes(y);
                     q[h] = upper ? __funnelshift_l(x, x, 16) : x;
                 }
                 if (col0 + c + j < a.cols && row0 / 2 + 16 * g < c_bytes)
@@ -314,7 +252,8 @@ mx4_quantize_tiles_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, in
             }
         }
         __syncthreads();                             // the stage is read, the scales are in rs and cs
-        if (t == 0 && i + QS_STAGES < mine) fetch(i + QS_STAGES);
+        if (BOXES && t == 0 && u + QS_STAGES < mine) fetch(u + QS_STAGES);
+        if (half != UNITS - 1) continue;
         if (ROWS && t >= 32 && t < 64 && rt < mx4_row_tiles(a.rows))
             reinterpret_cast<uint4 *>(a.r_scales + (rt * r_atoms + ct) * MX4_ATOM)[t - 32] = reinterpret_cast<const uint4 *>(rs[i & 1])[t - 32];
         if (COLS && t >= 64 && t < 96 && ct < mx4_row_tiles(a.cols))
@@ -402,19 +341,8 @@ struct F32X {
     static __device__ __forceinline__ uint32_t from_f32(float) { return 0u; }
 };
 
-template <class T, bool F32, bool VEC, bool ROWS, bool COLS>
-static cudaError_t quantize_launch(const Mx4Args &a, int64_t grid, cudaStream_t s) {
-    const int smem = COLS ? QT * QT * (F32 ? 4 : 2) : 0;
-    if (smem > 48 * 1024 - 2 * MX4_ATOM) {
-        const cudaError_t e = cudaFuncSetAttribute(mx4_quantize_kernel<T, F32, VEC, ROWS, COLS>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_dependent(mx4_quantize_kernel<T, F32, VEC, ROWS, COLS>, (unsigned)grid, 256, (size_t)smem, 1, s, a);
-}
-
-template <class T, bool ROWS, bool COLS>
-static cudaError_t tiles_launch(const Mx4Args &a, int64_t tiles, cudaStream_t s) {
+template <class T, bool F32, bool BOXES, bool ROWS, bool COLS>
+static cudaError_t quantize_launch(const Mx4Args &a, int64_t tiles, cudaStream_t s) {
     static std::atomic<int> known[64];           // SMs, once the kernel's shared memory is set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -422,36 +350,36 @@ static cudaError_t tiles_launch(const Mx4Args &a, int64_t tiles, cudaStream_t s)
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     int sms = known[dev].load(std::memory_order_relaxed);
     if (sms <= 0) {
-        e = cudaFuncSetAttribute(mx4_quantize_tiles_kernel<T, ROWS, COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize, QS_SMEM);
+        e = cudaFuncSetAttribute(mx4_quantize_kernel<T, F32, BOXES, ROWS, COLS>, cudaFuncAttributeMaxDynamicSharedMemorySize, qs_smem(BOXES));
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return e;
         known[dev].store(sms, std::memory_order_relaxed);
     }
-    const EncodeTiled f = encode_tiled();
-    if (!f) return cudaErrorNotSupported;
-    CUtensorMap map;
-    const cuuint64_t dims[2] = {(cuuint64_t)a.cols, (cuuint64_t)a.rows}, strides[1] = {(cuuint64_t)a.ld * 2};
-    const cuuint32_t boxes[2] = {64, 128}, ones[2] = {1, 1};
-    if (f(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(a.x), dims, strides, boxes, ones,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
+    CUtensorMap map = {};
+    if (BOXES) {
+        const EncodeTiled f = encode_tiled();
+        if (!f) return cudaErrorNotSupported;
+        const cuuint64_t dims[2] = {(cuuint64_t)a.cols, (cuuint64_t)a.rows}, strides[1] = {(cuuint64_t)a.ld * (F32 ? 4 : 2)};
+        const cuuint32_t boxes[2] = {F32 ? 32 : 64, 128}, ones[2] = {1, 1};
+        if (f(&map, F32 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(a.x), dims, strides, boxes, ones,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
     const int64_t wave = QS_CTAS * (int64_t)sms, grid = tiles < wave ? tiles : wave;
-    return launch_dependent(mx4_quantize_tiles_kernel<T, ROWS, COLS>, (unsigned)grid, 256, QS_SMEM, 1, s, map, a, (int)tiles);
+    return launch_dependent(mx4_quantize_kernel<T, F32, BOXES, ROWS, COLS>, (unsigned)grid, 256, qs_smem(BOXES), 1, s, map, a, (int)tiles);
 }
 
-template <class T>
-static cudaError_t tiles_ways(const Mx4Args &a, int64_t tiles, cudaStream_t s) {
-    if (a.r_codes && a.c_codes) return tiles_launch<T, true, true>(a, tiles, s);
-    if (a.r_codes) return tiles_launch<T, true, false>(a, tiles, s);
-    return tiles_launch<T, false, true>(a, tiles, s);
+template <class T, bool F32, bool BOXES>
+static cudaError_t quantize_ways(const Mx4Args &a, int64_t tiles, cudaStream_t s) {
+    if (a.r_codes && a.c_codes) return quantize_launch<T, F32, BOXES, true, true>(a, tiles, s);
+    if (a.r_codes) return quantize_launch<T, F32, BOXES, true, false>(a, tiles, s);
+    return quantize_launch<T, F32, BOXES, false, true>(a, tiles, s);
 }
 
-template <class T, bool F32, bool VEC>
-static cudaError_t quantize_ways(const Mx4Args &a, int64_t grid, cudaStream_t s) {
-    if (a.r_codes && a.c_codes) return quantize_launch<T, F32, VEC, true, true>(a, grid, s);
-    if (a.r_codes) return quantize_launch<T, F32, VEC, true, false>(a, grid, s);
-    return quantize_launch<T, F32, VEC, false, true>(a, grid, s);
+template <class T, bool F32>
+static cudaError_t quantize_rows(const Mx4Args &a, int64_t tiles, bool boxes, cudaStream_t s) {
+    return boxes ? quantize_ways<T, F32, true>(a, tiles, s) : quantize_ways<T, F32, false>(a, tiles, s);
 }
 
 }  // namespace zsk
@@ -538,12 +466,13 @@ zs_status zs_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld,
     if (grid > 0x7FFFFFFF) return zs_fail(ZS_EINVAL, "%s: %lld tiles", fn, (long long)grid);
     const cudaStream_t s = (cudaStream_t)stream;
     const int64_t per16 = dtype == ZS_DTYPE_FP32 ? 4 : 8;
-    const bool vec = (addr(x) & 15) == 0 && ld % per16 == 0;
+    // tensor copies: aligned rows, and a stride that a tensor map holds (2^40 bytes)
+    const bool boxes = (addr(x) & 15) == 0 && ld % per16 == 0 && ld < ((int64_t)1 << 37);
     using namespace zsk;
     cudaError_t e;
-    if (dtype == ZS_DTYPE_FP32) e = vec ? quantize_ways<F32X, true, true>(a, grid, s) : quantize_ways<F32X, true, false>(a, grid, s);
-    else if (dtype == ZS_DTYPE_FP16) e = vec ? tiles_ways<FP16T>(a, grid, s) : quantize_ways<FP16T, false, false>(a, grid, s);
-    else e = vec ? tiles_ways<BF16T>(a, grid, s) : quantize_ways<BF16T, false, false>(a, grid, s);
+    if (dtype == ZS_DTYPE_FP32) e = quantize_rows<F32X, true>(a, grid, boxes, s);
+    else if (dtype == ZS_DTYPE_FP16) e = quantize_rows<FP16T, false>(a, grid, boxes, s);
+    else e = quantize_rows<BF16T, false>(a, grid, boxes, s);
     return cuda_status(e, fn);
 }
 
