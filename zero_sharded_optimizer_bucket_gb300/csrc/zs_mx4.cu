@@ -73,9 +73,12 @@ __device__ __forceinline__ Mx4Scale mx4_scale(float top) {
 // BOXES: the rows of x are 16-byte aligned, and tensor copies fetch the units
 // ahead into a ring of stages, with zeros outside the matrix.  Otherwise lanes
 // load neighbouring elements of a row, whatever its address; the CTAs of an SM
-// overlap one another's loads.
+// overlap one another's loads, and how many are in flight bounds it.
 // 8 warps on three CTAs an SM; for both forms every warp makes one after the
 // other (8 warps for each on two CTAs took 34 us for 14336 x 4096, this 30).
+// 14336 x 4096 along the rows, the columns, both: bf16 24, 25 and 30 us (6.1,
+// 5.9, 6.0 TB/s), fp32 41, 41 and 48 (6.5, 6.4, 6.2); 14335 x 4095: bf16 42, 47
+// and 58 us (3.6, 3.2, 3.1 TB/s), fp32 46, 51 and 62 (5.7, 5.2, 4.8).
 constexpr int QS_BOX = 128 * 128, QS_STAGE = 2 * QS_BOX, QS_STAGES = 2, QS_CTAS = 3;
 constexpr uint64_t QS_WAIT_NS = 1000000000ull;       // one wait gives up after 1 s
 constexpr int qs_smem(bool boxes) { return (boxes ? QS_STAGES : 1) * QS_STAGE + 1024; }
@@ -135,7 +138,9 @@ mx4_quantize_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, int tile
                 return;
             }
         } else {
-            // a warp takes every 8th row; LOADS loads of a lane in flight
+            // a warp takes every 8th row, with LOADS loads of a lane in flight
+            // (14335 x 4095 bf16 along the rows: 54 us with half as many; pairs
+            // of elements in one load, which odd rows cannot use, 54 and more)
             constexpr int A_ROW = UNIT_COLS / 32, LOADS = 32, PER = LOADS / A_ROW;
             const int lane = t & 31;
 #pragma unroll 1
@@ -266,7 +271,7 @@ mx4_quantize_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, int tile
 // Where the rows of out are not 16-byte aligned a warp turns its 256 values
 // through shared memory, and its lanes store neighbours (stored by the thread
 // that decoded them, 14335 x 4095 bf16 took 312 us instead of 33; fp32 goes this
-// way always, 56 -> 42 us for 14336 x 4096).
+// way always, 56 -> 41 us for 14336 x 4096, 6.5 TB/s; bf16 26 us, 5.8 TB/s).
 constexpr int DQ_ROWS = 4;
 __host__ __device__ constexpr int dq_each(bool f32, bool vec) { return vec && !f32 ? 16 : 8; }
 template <class T, bool F32, bool VEC>

@@ -20,7 +20,7 @@
 #include "zs_launch.h"
 
 // Elements per CTA: a list long enough to fill the GPU takes the chunk at
-// which its kernel was fastest (32-bit moments 8192: 834 us for 202M
+// which its kernel was fastest (32-bit moments 8192: 833 us for 202M
 // elements; 8-bit 6144: 470 us rounded to nearest, against 488 at 4096 and at
 // 8192); a short one takes small chunks, spread over more SMs.
 constexpr int CHUNK32 = 8192, CHUNK8 = 6144, CHUNK_SHORT = 2048;
@@ -139,6 +139,7 @@ __device__ __forceinline__ uint16_t cast1(float p, bool fp16) {
 // ------------------------------------------------------ 32-bit moments --
 // 28 bytes an element with 16-bit gradients and a 16-bit copy; the update is
 // adam_elem, so that a list over a plan's shards gives zs_adam_step's bits.
+// Bandwidth bounds it: 202M elements in 833 us, 6.8 TB/s, the rate of a copy.
 template <class G>
 __global__ void __launch_bounds__(THREADS)
 tensors32_kernel(const ZsChunk *chunks, AdamC c, const float *d_coef,
@@ -295,8 +296,9 @@ __device__ __forceinline__ f2 sub2(f2 a, f2 b, const Adam8C &c) { return fma2(b,
 // lane's roots overlap.  Markstein's correction of an approximate root s of
 // w = 2^64 v: the residual w - s s is exact in one fused operation, and
 // s + (w - s s) / (2 sqrt(w)) rounds as the root does.  2^64 keeps the
-// residual of the smallest v among the normal numbers.  Infinities and NaN
-// give NaN, and so does v >= 2^64.
+// residual of the smallest v among the normal numbers; checked against the
+// library's root on every positive v below 2^64.  Infinities and NaN give NaN,
+// and so does v >= 2^64.
 __device__ __forceinline__ f2 root_2_32(f2 v) {
     const f2 w = mul2(v, both(18446744073709551616.0f)), minus_w = mul2(v, both(-18446744073709551616.0f));
     float a, b;
@@ -401,7 +403,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 // consecutive elements a lane.  16 bytes an element with 16-bit gradients and
 // a 16-bit copy: at the copy bandwidth that leaves about 85 instructions an
 // element, so the arithmetic counts as much as the bytes, and the copies keep
-// memory busy while every warp of the SM computes.  The quotient m / den is
+// memory busy while every warp of the SM computes (loads into registers took
+// 623 us and more for 202M elements).  Rounded to nearest 470 us, 6.9 TB/s;
+// stochastically 529 us, 6.1 TB/s: there the issue of instructions bounds it,
+// 81 an element, 26 of them the random bits and their rounding.  The quotient m / den is
 // the quick one (its last two bits may be off: 2^-22 of one update, far below
 // a rounding of p); the root is exact, since codes hang on it.
 template <class G, bool DITHER>
