@@ -78,6 +78,32 @@ def test_quantize(rows, cols, kind):
                 check_held(hc, want.T)
 
 
+@pytest.mark.parametrize("extra,offset", [(4, 0), (3, 1)])
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_quantize_long(kind, extra, offset):
+    """More tiles than a GPU takes at once: the same bytes as its parts one by one, which are few tiles each."""
+    rows, cols, part = 20000, 1100, 2560
+    x = matrix(rows, cols, kind, 5, cols + extra, offset)
+    (hr, er), (hc, ec) = room(rows, cols), room(cols, rows)
+    zs.zs_mx4_quantize(x, rows=hr, cols=hc)
+    torch.cuda.synchronize()
+    assert ends_ok(er) and ends_ok(ec)
+    for r in range(0, rows, part):
+        n = min(part, rows - r)
+        (h, _), size = room(n, cols), zs.zs_mx4_sizes(n, cols)
+        zs.zs_mx4_quantize(x[r:r + n], rows=h)
+        at, per = r * size["row_bytes"], size["scale_bytes"] // (-(-n // 128)) * (r // 128)
+        assert torch.equal(hr["codes"][at:at + size["code_bytes"]], h["codes"])
+        assert torch.equal(hr["scales"][per:per + size["scale_bytes"]], h["scales"])
+    for c in range(0, cols, 128):
+        n = min(128, cols - c)
+        (h, _), size = room(n, rows), zs.zs_mx4_sizes(n, rows)
+        zs.zs_mx4_quantize(x[:, c:c + n], cols=h)
+        at, per = c * size["row_bytes"], size["scale_bytes"] * (c // 128)
+        assert torch.equal(hc["codes"][at:at + size["code_bytes"]], h["codes"])
+        assert torch.equal(hc["scales"][per:per + size["scale_bytes"]], h["scales"])
+
+
 @pytest.mark.parametrize("kind", list(KINDS))
 def test_quantize_ties_and_ends(kind):
     """Every midpoint of the grid, both neighbours of each, values that saturate, signs and zeros."""
