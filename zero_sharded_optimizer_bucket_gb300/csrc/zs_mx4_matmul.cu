@@ -11,8 +11,8 @@
 // Two kernels, by the work there is:
 //  - products that give every pair of SMs about a 256 x 256 tile or more:
 //    mx4_matmul_pair_kernel.  8192 x 14336 x 4096 bf16: 143 us, 6.7 PFLOP/s in
-//    short runs; 156-160 us, 6.0-6.2 PFLOP/s in long ones, which run at the
-//    board's 1.4 kW (the clock falls to 1.9 GHz and below).
+//    short runs, 156 us, 6.2 PFLOP/s in long ones, which run at the board's
+//    power limit; 8192 x 8192 x 8192 147 us, 7.5 PFLOP/s, and 163 us.
 //  - smaller ones: mx4_matmul_kernel, tiles of 128 rows, k shared out over a
 //    cluster when the tiles are few.  One token through 4096 x 14336: 8.1 us
 //    from HBM, 3.8 TB/s of weight bytes, 6.2 from L2; 16 through 14336 x 4096:
@@ -385,22 +385,35 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
 // the tile boundary, while 8 warps of each CTA empty the accumulator of the
 // previous tile into registers, release it, and store.  (Two accumulators of
 // 256 columns would leave no tensor memory for the scales.)
-// A stage takes the tensor cores 512 cycles and brings 35 KB to each SM; a
-// tile of 16 stages measured about 10,300 cycles with the launch alone, 350 to
-// 400 of them between its last product and the next tile's first.  What is
-// left is power: in long runs the board holds 1.36 kW.  Clusters of two pairs
-// that share B by multicast took as long (144 of the 152 SMs fit such
-// clusters); scales placed by tcgen05.st in the place of tcgen05.cp took 8192 x
-// 8192 x 8192 387 us and more, where this form took 246 at the time (153 now).
+// A stage takes the tensor cores 512 cycles and brings 35 KB to each SM.  With 5
+// in flight 8192 x 8192 x 8192 took 630 cycles a stage all in all, with 4 650,
+// with 3 760: the way from a product's end over its barrier and the loads to the
+// next product is what remains, besides 400 cycles a tile between its last
+// product and the next one's first.  (Loads beside the products do not slow
+// them, and the same loads from a few hot lines gained 4 %.)  Then power: the
+// SMs run at 1.86 GHz in short runs, at 1.62 to 1.67 in long ones, at 1.36 kW.
+// Clusters of two pairs that share B by multicast took as long (144 of the 152
+// SMs fit such clusters); scales placed by tcgen05.st in the place of
+// tcgen05.cp took 8192 x 8192 x 8192 387 us and more, where this form took 246
+// at the time.
 constexpr int PAIR_ROWS = 256, PAIR_COLS = 256;
-constexpr int PAIR_STAGES = 5;
 constexpr int PAIR_THREADS = 320;         // 8 warps store, 1 loads, 1 multiplies (leader only)
 constexpr int PAIR_P = 128 * MM_KB, PAIR_Q = 128 * MM_KB;
 constexpr int PAIR_SP = 2 * MX4_ATOM, PAIR_SQ = 4 * MX4_ATOM;
 constexpr int PAIR_STAGE = PAIR_P + PAIR_Q + PAIR_SP + PAIR_SQ;
-constexpr int PAIR_SLAB = 32 * 128;       // a storing warp's buffer: 32 rows of 128 bytes
-constexpr int PAIR_SMEM = PAIR_STAGES * PAIR_STAGE + 8 * PAIR_SLAB + 1024;
 constexpr int PAIR_SP_COL = 256, PAIR_SQ_COL = PAIR_SP_COL + 16;   // scales, two sets of each
+
+// A ring of 5 stages leaves every storing warp a slab of 32 rows of 128 bytes,
+// one of 6 rows of 64.
+template <int STAGES>
+struct PairShape {
+    static constexpr int ROW = STAGES == 6 ? 64 : 128;
+    static constexpr int SLAB = 32 * ROW;
+    static constexpr int BARS = STAGES * PAIR_STAGE + 8 * SLAB;      // the barriers are after them
+    static constexpr int SMEM = BARS + 256;
+    // the 16-byte pieces of a row are turned by this: no bank conflicts
+    static __device__ __forceinline__ int turn(int row) { return ROW == 128 ? row & 7 : (row >> 1) & 3; }
+};
 
 __device__ __forceinline__ void tma2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
     asm volatile(
@@ -428,24 +441,25 @@ struct PairArgs {
     int32_t vec;              // rows of out are 16-byte aligned
 };
 
+template <int STAGES>
 __global__ void __launch_bounds__(PAIR_THREADS)
 mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                        const __grid_constant__ CUtensorMap map_sp, const __grid_constant__ CUtensorMap map_sq, PairArgs a) {
-    extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[2 * PAIR_STAGES + 2];
-    __shared__ uint32_t tmem_base;
-    __shared__ volatile int failed;
+    using S = PairShape<STAGES>;
+    // the swizzle wants 1024-byte alignment; nothing static, so that none of it is lost
+    extern __shared__ __align__(1024) uint8_t pair_raw[];
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-    const uint32_t bar0 = smem_u32(bars);
+    const uint32_t base = smem_u32(pair_raw), bar0 = base + S::BARS;
+    uint32_t &tmem_base = *reinterpret_cast<uint32_t *>(pair_raw + S::BARS + 8 * (2 * STAGES + 2));
+    volatile int &failed = *reinterpret_cast<volatile int *>(pair_raw + S::BARS + 8 * (2 * STAGES + 3));
     auto full = [&](int s) { return bar0 + 8 * s; };
-    auto empty = [&](int s) { return bar0 + 8 * (PAIR_STAGES + s); };
-    const uint32_t acc_full = bar0 + 16 * PAIR_STAGES, acc_empty = acc_full + 8;
+    auto empty = [&](int s) { return bar0 + 8 * (STAGES + s); };
+    const uint32_t acc_full = bar0 + 16 * STAGES, acc_empty = acc_full + 8;
     const int rank = (int)(blockIdx.x & 1);
     const int first = (int)(blockIdx.x >> 1), stride = (int)(gridDim.x >> 1);
     if (threadIdx.x == 0) {
         failed = 0;
-        for (int i = 0; i < 2 * PAIR_STAGES + 1; ++i)
+        for (int i = 0; i < 2 * STAGES + 1; ++i)
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" : : "r"(bar0 + 8 * i) : "memory");
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 16;" : : "r"(acc_empty) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" : : : "memory");
@@ -471,8 +485,8 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
         for (int t = first; t < a.tiles && ok; t += stride) {
             const int pt = t % a.p_tiles, qt = t / a.p_tiles;
             for (int k = 0; k < a.k_tiles; ++k, ++issued) {
-                const int s = issued % PAIR_STAGES;
-                if (issued >= PAIR_STAGES && !warp_wait(empty(s), (uint32_t)((issued / PAIR_STAGES - 1) & 1), MM_WAIT_NS)) {
+                const int s = issued % STAGES;
+                if (issued >= STAGES && !warp_wait(empty(s), (uint32_t)((issued / STAGES - 1) & 1), MM_WAIT_NS)) {
                     failed = 1;
                     ok = false;
                     break;
@@ -491,8 +505,8 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
             }
         }
         // every signal to this CTA's barriers has come before it leaves
-        for (int i = issued > PAIR_STAGES ? issued - PAIR_STAGES : 0; ok && i < issued; ++i)
-            ok = warp_wait(empty(i % PAIR_STAGES), (uint32_t)((i / PAIR_STAGES) & 1), MM_WAIT_NS);
+        for (int i = issued > STAGES ? issued - STAGES : 0; ok && i < issued; ++i)
+            ok = warp_wait(empty(i % STAGES), (uint32_t)((i / STAGES) & 1), MM_WAIT_NS);
         if (!ok) failed = 1;
     } else if (warp == 9 && rank == 0) {
         const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(PAIR_COLS / 8) << 17) | (1u << 23) | (16u << 24);
@@ -505,8 +519,8 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
             }
             asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
             for (int k = 0; k < a.k_tiles; ++k, ++i) {
-                const int s = i % PAIR_STAGES;
-                if (!warp_wait(full(s), (uint32_t)((i / PAIR_STAGES) & 1), MM_WAIT_NS)) {
+                const int s = i % STAGES;
+                if (!warp_wait(full(s), (uint32_t)((i / STAGES) & 1), MM_WAIT_NS)) {
                     failed = 1;
                     ok = false;
                     break;
@@ -544,7 +558,7 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
             __syncwarp();
         }
     } else if (warp < 8) {
-        const uint32_t slab = base + PAIR_STAGES * PAIR_STAGE + warp * PAIR_SLAB;
+        const uint32_t slab = base + STAGES * PAIR_STAGE + warp * S::SLAB;
         const uint32_t release = map_to(acc_empty, 0);
         const int sub = warp & 3, c0 = 128 * (warp >> 2);
         int n = 0;
@@ -571,70 +585,76 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
                 for (int i = 0; i < 64; ++i)
                     v[i] = mm_cast(__uint_as_float(v[2 * i]), a.dtype) | (mm_cast(__uint_as_float(v[2 * i + 1]), a.dtype) << 16);
             }
-            // 32 rows of 128 bytes at a time through this warp's slab, in
-            // 16-byte pieces whose place within a row is turned by the row
-            // (no bank conflicts); then lanes store neighbouring elements
-            const int pieces = fp32 ? 4 : 2, width = fp32 ? 32 : 64;
+            // 32 rows of ROW bytes at a time through this warp's slab; then
+            // lanes store neighbouring elements
+            constexpr int PER = S::ROW / 16;          // pieces of a row
+            const int times = (fp32 ? 512 : 256) / S::ROW, width = S::ROW / (fp32 ? 4 : 2);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (j >= pieces) break;
+            for (int j = 0; j < 512 / S::ROW; ++j) {
+                if (j >= times) break;
                 const int col = col0 + j * width;
                 if (row0 >= a.m || col >= a.n) break;
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
+                for (int c = 0; c < PER; ++c)
                     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
                                  :
-                                 : "r"(slab + 128 * lane + 16 * (c ^ (lane & 7))), "r"(v[32 * j + 4 * c]), "r"(v[32 * j + 4 * c + 1]),
-                                   "r"(v[32 * j + 4 * c + 2]), "r"(v[32 * j + 4 * c + 3])
+                                 : "r"(slab + S::ROW * lane + 16 * (c ^ S::turn(lane))), "r"(v[4 * PER * j + 4 * c]), "r"(v[4 * PER * j + 4 * c + 1]),
+                                   "r"(v[4 * PER * j + 4 * c + 2]), "r"(v[4 * PER * j + 4 * c + 3])
                                  : "memory");
                 __syncwarp();
                 if (a.vec && col + width <= a.n) {
-                    // 4 whole lines a store
+                    // whole lines (or their halves) of several rows a store
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = 4 * i + (lane >> 3);
+                    for (int i = 0; i < PER; ++i) {
+                        const int row = 32 / PER * i + lane / PER;
                         uint32_t x[4];
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                     : "r"(slab + 128 * row + 16 * ((lane & 7) ^ (row & 7)))
+                                     : "r"(slab + S::ROW * row + 16 * (lane % PER ^ S::turn(row)))
                                      : "memory");
                         if (row0 + row < a.m)
-                            *reinterpret_cast<uint4 *>(static_cast<char *>(a.out) + ((int64_t)(row0 + row) * a.ldo + col) * (fp32 ? 4 : 2) + 16 * (lane & 7)) =
+                            *reinterpret_cast<uint4 *>(static_cast<char *>(a.out) + ((int64_t)(row0 + row) * a.ldo + col) * (fp32 ? 4 : 2) + 16 * (lane % PER)) =
                                 make_uint4(x[0], x[1], x[2], x[3]);
                     }
                     __syncwarp();
                     continue;
                 }
                 const int rows = min(32, a.m - row0);
-                // 8 reads, then their stores
+                // 8 reads, then their stores: a row of fp32 slabs is 16 or 32
+                // elements, of 16-bit ones 32 or 64
+                auto element = [&](int row, int byte) { return slab + S::ROW * row + (byte ^ (16 * S::turn(row))); };
                 if (fp32) {
-                    float *o = static_cast<float *>(a.out) + (int64_t)row0 * a.ldo + col + lane;
+                    constexpr int WIDTH = S::ROW / 4, SKIP = 32 / WIDTH;         // rows a read
+                    const int c = lane % WIDTH;
 #pragma unroll 1
-                    for (int i = 0; i < rows; i += 8, o += 8 * a.ldo) {
+                    for (int i = lane / WIDTH; i < rows; i += 8 * SKIP) {
                         uint32_t x[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[e]) : "r"(slab + 128 * (i + e) + ((4 * lane) ^ (16 * e))) : "memory");
-                        if (col + lane < a.n) {
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[e]) : "r"(element(i + SKIP * e, 4 * c)) : "memory");
+                        float *o = static_cast<float *>(a.out) + (int64_t)(row0 + i) * a.ldo + col + c;
+                        if (col + c < a.n) {
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
-                                if (i + e < rows) o[e * a.ldo] = __uint_as_float(x[e]);
+                                if (i + SKIP * e < rows) o[SKIP * e * a.ldo] = __uint_as_float(x[e]);
                         }
                     }
                 } else {
+                    constexpr int TIMES = S::ROW / 64;                           // reads a row
                     uint16_t *o = static_cast<uint16_t *>(a.out) + (int64_t)row0 * a.ldo + col + lane;
 #pragma unroll 1
-                    for (int i = 0; i < rows; i += 4, o += 4 * a.ldo) {
+                    for (int i = 0; i < rows; i += 8 / TIMES, o += 8 / TIMES * a.ldo) {
                         uint32_t x[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             asm volatile("ld.shared.u16 %0, [%1];"
                                          : "=r"(x[e])
-                                         : "r"(slab + 128 * (i + e / 2) + ((2 * (32 * (e & 1) + lane)) ^ (16 * ((i + e / 2) & 7))))
+                                         : "r"(element(i + e / TIMES, 2 * (32 * (e % TIMES) + lane)))
                                          : "memory");
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            if (i + e / 2 < rows && col + 32 * (e & 1) + lane < a.n) o[(e / 2) * a.ldo + 32 * (e & 1)] = (uint16_t)x[e];
+                            if (i + e / TIMES < rows && col + 32 * (e % TIMES) + lane < a.n)
+                                o[(e / TIMES) * a.ldo + 32 * (e % TIMES)] = (uint16_t)x[e];
                     }
                 }
                 __syncwarp();
@@ -644,8 +664,8 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
     __syncwarp();
     if (warp == 8 && lane == 0 && failed) {
         if (rank == 0)   // the leader's barriers count the loads of both CTAs
-            for (int i = issued > PAIR_STAGES ? issued - PAIR_STAGES : 0; i < issued; ++i)
-                mbar_wait_quick(full(i % PAIR_STAGES), (uint32_t)((i / PAIR_STAGES) & 1), MM_WAIT_NS);
+            for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+                mbar_wait_quick(full(i % STAGES), (uint32_t)((i / STAGES) & 1), MM_WAIT_NS);
         atomicAdd(&g_mx4_wait_timeouts, 1);
     }
     asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
@@ -707,17 +727,16 @@ static cudaError_t device_sms(std::atomic<int> (&known)[64], cudaError_t (*set)(
     return cudaSuccess;
 }
 
-static cudaError_t pair_attributes() {
-    return cudaFuncSetAttribute(mx4_matmul_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM);
-}
-
+template <int STAGES>
 static cudaError_t pair_launch(const CUtensorMap (&map)[4], const PairArgs &a, cudaStream_t s) {
     static std::atomic<int> known[64];
     int sms = 0;
-    cudaError_t e = device_sms(known, pair_attributes, &sms);
+    const cudaError_t e = device_sms(known, [] {
+        return cudaFuncSetAttribute(mx4_matmul_pair_kernel<STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, PairShape<STAGES>::SMEM);
+    }, &sms);
     if (e != cudaSuccess) return e;
     const int pairs = a.tiles < sms / 2 ? a.tiles : sms / 2;
-    return launch_dependent(mx4_matmul_pair_kernel, (unsigned)(2 * pairs), PAIR_THREADS, PAIR_SMEM, 2, s, map[0], map[1], map[2], map[3], a);
+    return launch_dependent(mx4_matmul_pair_kernel<STAGES>, (unsigned)(2 * pairs), PAIR_THREADS, PairShape<STAGES>::SMEM, 2, s, map[0], map[1], map[2], map[3], a);
 }
 
 template <int BN, bool FLIP>
@@ -796,7 +815,12 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *
         a.tiles = (int32_t)(pair_p * pair_q);
         a.dtype = dtype;
         a.vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ldo * size % 16 == 0;
-        e = zsk::pair_launch(map, a, s);
+        // Every pair of the 76 has (tiles / 76) k_tiles stages.  When they are
+        // many, 6 in flight: 8192 x 8192 x 8192 154 -> 148 us (fp32 out 169 ->
+        // 160), 4096 x 4096 x 11008 59.6 -> 58.7; when few, the store after the
+        // last tile counts, and slabs of whole lines: 1024 x 4096 x 4096 10.6 us
+        // against 11.4, 4097 x 4100 x 4096 (64 stages) 28.6 against 29.1.
+        e = (pair_p * pair_q + 75) / 76 * a.k_tiles >= 128 ? zsk::pair_launch<6>(map, a, s) : zsk::pair_launch<5>(map, a, s);
         if (e != cudaSuccess) return zs_fail(ZS_ECUDA, "%s: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
         zs_clear_error();
         return ZS_OK;
