@@ -303,10 +303,18 @@ __device__ __forceinline__ f2 root_2_32(f2 v) {
     const f2 w = mul2(v, both(18446744073709551616.0f)), minus_w = mul2(v, both(-18446744073709551616.0f));
     float a, b;
     f2unpack(w, a, b);
-    asm("rsqrt.approx.f32 %0, %1;" : "=f"(a) : "f"(fmaxf(a, 7.8886090522101181e-31f)));   // 2^-100: v = 0 gives 0
-    asm("rsqrt.approx.f32 %0, %1;" : "=f"(b) : "f"(fmaxf(b, 7.8886090522101181e-31f)));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(fmaxf(a, 7.8886090522101181e-31f)));   // 2^-100: v = 0 gives 0
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(fmaxf(b, 7.8886090522101181e-31f)));
     const f2 y = f2pack(a, b), s = mul2(w, y);
     return fma2(fma2(s, s, minus_w), mul2(both(-0.5f), y), s);
+}
+
+// a / b to 2 units in the last place, b normal or 0 (a root times at least 1,
+// plus eps): without the scaling that other denominators need.
+__device__ __forceinline__ float quick_quotient(float a, float b) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(b));
+    return __fmul_rn(a, y);
 }
 
 // New moment and square of one element; g: the gradient times coef (and the
@@ -353,7 +361,7 @@ __device__ __noinline__ void adam8_block(const ZsChunk *chunk, const Adam8C c, f
         adam8_moments(p, m[i], v, G::load1(k.grad, x + i), r[i], sm, sr, coef, c);
         r[i] = __fsqrt_rn(v);
         const float den = __fadd_rn(__fmul_rn(r[i], c.root), c.eps);
-        p = __fsub_rn(p, __fmul_rn(c.step_size, __fdividef(m[i], den)));
+        p = __fsub_rn(p, __fmul_rn(c.step_size, quick_quotient(m[i], den)));
         k.master[x + i] = p;
         if (param) param[x + i] = cast1(p, fp16);
     }
@@ -449,6 +457,7 @@ tensors8_kernel(const ZsChunk *chunks, Adam8C c, const float *d_coef,
         }
         if (!__all_sync(0xFFFFFFFFu, mbar_wait_quick(bar + 8 * i, 0, BULK_NS))) {
             if (lane == 0) atomicAdd(&g_tensors_wait_timeouts, 1);
+            mbar_wait_quick(bar + 8 * i, 0, BULK_NS);       // shared memory stays until the copies land
             continue;
         }
         const int x = b * STATE_BLOCK + 8 * lane;
@@ -481,7 +490,7 @@ tensors8_kernel(const ZsChunk *chunks, Adam8C c, const float *d_coef,
         for (int e = 0; e < 8; e += 2) {
             float a, b;
             f2unpack(add2(mul2(f2pack(r[e], r[e + 1]), both(c.root_2_32)), both(c.eps), c), a, b);
-            const f2 q = f2pack(__fdividef(m[e], a), __fdividef(m[e + 1], b));
+            const f2 q = f2pack(quick_quotient(m[e], a), quick_quotient(m[e + 1], b));
             f2unpack(sub2(f2pack(p[e], p[e + 1]), mul2(both(c.step_size), q), c), p[e], p[e + 1]);
         }
         store8f(k.master + x, p);
@@ -675,7 +684,8 @@ zs_status zs_adam_tensors(const zs_tensors *L, const zs_adam_hparams *hp, int64_
     }
     if (!L->d_chunks) return zs_fail(ZS_ESTATE, "%s: list not uploaded (call zs_tensors_upload first)", fn);
     zsk::Adam8C c;
-    c.b1 = a.b1; c.b2 = a.b2; c.omb1 = a.omb1; c.omb2 = a.omb2; c.eps = a.eps;
+    c.b1 = a.b1; c.b2 = a.b2; c.omb1 = a.omb1; c.omb2 = a.omb2;
+    c.eps = a.eps > 0.0f && a.eps < 0x1p-126f ? 0x1p-126f : a.eps;      // the quick quotient takes no subnormal denominator
     c.wd = a.wd; c.lr_wd = a.lr_wd; c.step_size = a.step_size; c.root = a.root; c.root_2_32 = a.root * 0x1p-32f;
     c.one = 1.0f; c.minus_one = -1.0f; c.adamw = a.adamw;
     c.k0 = (uint32_t)seed;
