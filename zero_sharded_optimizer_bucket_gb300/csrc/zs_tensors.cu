@@ -13,6 +13,7 @@
 // power of two costs no precision, makes scaling exact and leaves its largest
 // value in [128, 256), which no rounding takes past 448.
 #include <atomic>
+#include <cstring>
 #include <new>
 #include <vector>
 
@@ -50,9 +51,11 @@ struct zs_tensors {
 namespace zsk {
 
 struct Adam8C {
-    float b1, b2, omb1, omb2, eps, wd, lr_wd, step_size, root, root_2_32, one, minus_one;
+    float b1, b2, omb1, omb2, eps, wd, lr_wd, step_size, root, root_2_32;
     int adamw;
     uint32_t k0, k1, step;
+    // the same and 1 twice, for the paired instructions
+    struct { unsigned long long b1, b2, omb1, omb2, eps, wd, lr_wd, step_size, root_2_32, one, minus_one; } two;
 };
 
 __device__ __forceinline__ void floats4(const uint4 &v, float o[4]) {
@@ -289,8 +292,8 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
-__device__ __forceinline__ f2 add2(f2 a, f2 b, const Adam8C &c) { return fma2(a, both(c.one), b); }
-__device__ __forceinline__ f2 sub2(f2 a, f2 b, const Adam8C &c) { return fma2(b, both(c.minus_one), a); }
+__device__ __forceinline__ f2 add2(f2 a, f2 b, const Adam8C &c) { return fma2(a, c.two.one, b); }
+__device__ __forceinline__ f2 sub2(f2 a, f2 b, const Adam8C &c) { return fma2(b, c.two.minus_one, a); }
 
 // 2^32 sqrt(v) of two, correctly rounded and without a branch, so that a
 // lane's roots overlap.  Markstein's correction of an approximate root s of
@@ -472,13 +475,13 @@ tensors8_kernel(const ZsChunk *chunks, Adam8C c, const float *d_coef,
         for (int e = 0; e < 8; e += 2) {
             f2 g2 = mul2(f2pack(g[e], g[e + 1]), both(coef)), p2 = f2pack(p[e], p[e + 1]);
             if (c.adamw)
-                p2 = sub2(p2, mul2(both(c.lr_wd), p2), c);
+                p2 = sub2(p2, mul2(c.two.lr_wd, p2), c);
             else
-                g2 = add2(g2, mul2(both(c.wd), p2), c);
+                g2 = add2(g2, mul2(c.two.wd, p2), c);
             const f2 m0 = mul2(f2pack(m[e], m[e + 1]), both(scale_m)), r0 = mul2(f2pack(r[e], r[e + 1]), both(scale_r));
-            const f2 v2 = add2(mul2(both(c.b2), mul2(r0, r0)), mul2(both(c.omb2), mul2(g2, g2)), c);
+            const f2 v2 = add2(mul2(c.two.b2, mul2(r0, r0)), mul2(c.two.omb2, mul2(g2, g2)), c);
             f2unpack(p2, p[e], p[e + 1]);
-            f2unpack(add2(mul2(both(c.b1), m0), mul2(both(c.omb1), g2), c), m[e], m[e + 1]);
+            f2unpack(add2(mul2(c.two.b1, m0), mul2(c.two.omb1, g2), c), m[e], m[e + 1]);
             f2unpack(root_2_32(v2), r[e], r[e + 1]);
         }
         const uint32_t tm = block_top(m), tr = block_top(r);
@@ -489,9 +492,9 @@ tensors8_kernel(const ZsChunk *chunks, Adam8C c, const float *d_coef,
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
             float a, b;
-            f2unpack(add2(mul2(f2pack(r[e], r[e + 1]), both(c.root_2_32)), both(c.eps), c), a, b);
+            f2unpack(add2(mul2(f2pack(r[e], r[e + 1]), c.two.root_2_32), c.two.eps, c), a, b);
             const f2 q = f2pack(quick_quotient(m[e], a), quick_quotient(m[e + 1], b));
-            f2unpack(sub2(f2pack(p[e], p[e + 1]), mul2(both(c.step_size), q), c), p[e], p[e + 1]);
+            f2unpack(sub2(f2pack(p[e], p[e + 1]), mul2(c.two.step_size, q), c), p[e], p[e + 1]);
         }
         store8f(k.master + x, p);
         if (k.param) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(k.param) + x) = cast8(p, fp16);
@@ -687,7 +690,14 @@ zs_status zs_adam_tensors(const zs_tensors *L, const zs_adam_hparams *hp, int64_
     c.b1 = a.b1; c.b2 = a.b2; c.omb1 = a.omb1; c.omb2 = a.omb2;
     c.eps = a.eps > 0.0f && a.eps < 0x1p-126f ? 0x1p-126f : a.eps;      // the quick quotient takes no subnormal denominator
     c.wd = a.wd; c.lr_wd = a.lr_wd; c.step_size = a.step_size; c.root = a.root; c.root_2_32 = a.root * 0x1p-32f;
-    c.one = 1.0f; c.minus_one = -1.0f; c.adamw = a.adamw;
+    c.adamw = a.adamw;
+    auto both = [](float x) {
+        uint32_t u;
+        memcpy(&u, &x, 4);
+        return (unsigned long long)u << 32 | u;
+    };
+    c.two = {both(c.b1), both(c.b2), both(c.omb1), both(c.omb2), both(c.eps), both(c.wd), both(c.lr_wd), both(c.step_size),
+             both(c.root_2_32), both(1.0f), both(-1.0f)};
     c.k0 = (uint32_t)seed;
     c.k1 = (uint32_t)(seed >> 32);
     c.step = (uint32_t)step;
