@@ -698,7 +698,8 @@ zs_status zs_tensors_upload(zs_tensors *list, void *d_table, int64_t bytes, void
  *   p = p - (lr/bc1) * (m / (r*(1/sqrt(bc2)) + eps));  param = rne16(p)
  *   with lr/bc1 and 1/sqrt(bc2) computed in double and rounded to fp32, and
  *   the quotient m/(..) good to 2 units in its last place, 2^-22 of one
- *   update (every other operation is correctly rounded); then
+ *   update (every other operation is correctly rounded; an eps below 2^-126
+ *   that is not 0 counts as 2^-126); then
  *   a block's scale is 2^(floor(log2 max) - 7) of its new |m| (of its r), at
  *   least 2^-126, and the codes are m/scale and r/scale in e4m3.
  *   ZS_ROUND_NEAREST: to nearest even.  ZS_ROUND_STOCHASTIC: to one of the
