@@ -222,6 +222,32 @@ def test_product(m, n, k, kind):
         assert np.all(np.abs(product(ca, sa, cb, sb, k, kind, ldo, offset) - want) <= tol)
 
 
+# parts of k that go around every ring of stages several times, by kernel and tile: 16, 32 and 64 tokens, 128, pairs of SMs
+# with few stages and with many
+@pytest.mark.parametrize("m,n,k", [(5, 9800, 2592), (20, 9801, 2592), (48, 9800, 4128), (100, 9900, 4128), (1290, 1801, 4128),
+                                   (1290, 1801, 32800)])
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_product_deep(m, n, k, kind):
+    """Scales of 1: sums are multiples of 1/4 below 2^22, exact in 32 bits in any order, and rounded once."""
+    g = torch.Generator(device="cuda").manual_seed(m + n + k)
+    table = torch.tensor(ref.E2M1, dtype=torch.float32, device="cuda")
+
+    def held(rows):
+        size = zs.zs_mx4_sizes(rows, k)
+        codes = torch.randint(0, 256, (rows, size["row_bytes"]), dtype=torch.uint8, device="cuda", generator=g)
+        values = table[torch.stack((codes & 15, codes >> 4), 2).long()].view(rows, k)
+        return dict(codes=codes, scales=torch.full((size["scale_bytes"],), 127, dtype=torch.uint8, device="cuda")), values
+
+    (a, va), (b, vb) = held(m), held(n)
+    want = (va @ vb.T).to(KINDS[kind])
+    for ldo in (n, n + (-n) % 8 + 8):
+        out = torch.full((m, ldo), 77.0, dtype=KINDS[kind], device="cuda")
+        zs.zs_mx4_matmul(a, b, k, out[:, :n])
+        assert torch.equal(out[:, :n], want)
+        assert bool((out[:, n:] == 77.0).all())
+    assert zs.zs_device_wait_timeouts() == 0
+
+
 @pytest.mark.parametrize("m,n", [(1, 200), (40, 130), (300, 260)])
 def test_product_scales(m, n):
     """Each group's scale reaches its own row and elements: one nonzero element a row, all scales different."""
