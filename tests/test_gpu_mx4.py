@@ -361,3 +361,34 @@ def test_gradients_of_rounded_matrices():
     for got, a, b in zip(linear(x, w, dy), (v(x), v(dy), v(dy.T)), (v(w), v(w.T), v(x.T))):
         tol = (-(-a.shape[1] // 64) + 8) * 2.0 ** -22 * (np.abs(a) @ np.abs(b).T) + 2.0 ** -24 * np.abs(a @ b.T)
         assert np.all(np.abs(got - a @ b.T) <= tol)
+
+
+def test_past_32_bits():
+    """2.3e9 elements: the last rows (of the transposed form: the last columns) equal those of a small matrix."""
+    rows, cols, k = 70000, 32768, 64
+    last = 539 * 128                                                   # the first row of the last scale tiles
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(9))
+    (hr, er), (hc, ec) = room(rows, cols), room(cols, rows)
+    zs.zs_mx4_quantize(x, rows=hr, cols=hc)
+    assert ends_ok(er) and ends_ok(ec)
+    (tail, _), size = room(rows - last, cols), zs.zs_mx4_sizes(rows - last, cols)
+    zs.zs_mx4_quantize(x[last:].clone(), rows=tail)
+    assert torch.equal(hr["codes"][-size["code_bytes"]:], tail["codes"])
+    assert torch.equal(hr["scales"][-size["scale_bytes"]:], tail["scales"])
+    (tail_c, _), size = room(128, rows), zs.zs_mx4_sizes(128, rows)
+    zs.zs_mx4_quantize(x[:, -128:].clone(), cols=tail_c)
+    assert torch.equal(hc["codes"][-size["code_bytes"]:], tail_c["codes"])
+    assert torch.equal(hc["scales"][-size["scale_bytes"]:], tail_c["scales"])
+    # values, into x
+    zs.zs_mx4_dequantize(hr, x)
+    out = torch.empty(rows - last, cols, dtype=torch.bfloat16, device="cuda")
+    zs.zs_mx4_dequantize(tail, out)
+    assert torch.equal(x[last:], out)
+    # a product into x
+    a, b = x[:, :k].clone(), x[:cols, k:2 * k].clone()
+    (ha, _), (hb, _), (ta, _) = room(rows, k), room(cols, k), room(rows - last, k)
+    for m, h in ((a, ha), (b, hb), (a[last:], ta)):
+        zs.zs_mx4_quantize(m, rows=h)
+    zs.zs_mx4_matmul(ha, hb, k, x)
+    zs.zs_mx4_matmul(ta, hb, k, out)
+    assert torch.equal(x[last:], out)

@@ -348,3 +348,27 @@ def test_same_bits_twice():
         out.append({k: b.t.clone() for k, b in bufs[0].items()})
     for k in out[0]:
         assert torch.equal(out[0][k].view(torch.uint8), out[1][k].view(torch.uint8)), k
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_past_32_bits(bits):
+    """A tensor of more than 2^31 elements: its end equals a small tensor's."""
+    n, tail = 2 ** 31 + 5003, 4 * 6144 + 5003
+    dev = dict(device="cuda")
+    t = dict(grad=torch.zeros(n, dtype=torch.bfloat16, **dev), param=torch.zeros(n, dtype=torch.bfloat16, **dev), master=torch.zeros(n, **dev))
+    kind = torch.uint8 if bits == 8 else torch.float32
+    t.update(exp_avg=torch.zeros(n, dtype=kind, **dev), exp_avg_sq=torch.zeros(n, dtype=kind, **dev))
+    if bits == 8:
+        blocks = -(-n // 256)
+        t.update(exp_avg_scale=torch.zeros(blocks, **dev), exp_avg_sq_scale=torch.zeros(blocks, **dev))
+    g = torch.Generator(device="cuda").manual_seed(3)
+    t["grad"][-tail:].normal_(0, 1e-3, generator=g)
+    t["master"][-tail:].normal_(0, 0.02, generator=g)
+    small = {k: v[-(-(-tail // 256)):].clone() if k.endswith("scale") else v[-tail:].clone() for k, v in t.items()}
+    a, b = upload([t], bits), upload([small], bits)
+    for step in (1, 2):
+        zs.zs_adam_tensors(a, HP, step)
+        zs.zs_adam_tensors(b, HP, step)
+    for k, v in small.items():
+        assert torch.equal(t[k][-len(v):], v), k
+    assert not t["master"][:-tail].any()
