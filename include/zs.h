@@ -446,6 +446,18 @@ zs_status zs_device_wait_timeouts(int32_t *count, int32_t reset);
  * no counterpart in the pages.  Errors: ZS_EINVAL (limit), ZS_ECUDA. */
 zs_status zs_test_wait_timeout(int64_t limit_ns, void *stream);
 
+/* What a CTA of the kernel asks of its SM that zs_mx4_matmul launches for a
+ * product of these sizes (for tests; host only). */
+typedef struct {
+    int32_t cluster;               /* CTAs of a cluster                        */
+    int32_t split;                 /* CTAs that share the k of a tile          */
+    int32_t stages;                /* of the ring of operands                  */
+    int32_t shared_bytes;          /* dynamic shared memory                    */
+    int32_t tmem_columns;          /* columns of tensor memory                 */
+    int32_t reserved;
+} zs_mx4_launch;
+zs_status zs_test_mx4_launch(int64_t m, int64_t n, int64_t k, zs_mx4_launch *out);
+
 /* A2 over the consecutive buckets [first_bucket, first_bucket + n_buckets)
  * in one launch, for buckets that become ready back to back ([ZeRO-3
  * chapter] §6.2: a full IPG bucket is reduced and scattered; when several

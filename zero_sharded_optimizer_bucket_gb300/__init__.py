@@ -136,6 +136,10 @@ class zs_tensors_info_t(C.Structure):
                 ("device_table_bytes", C.c_int64)]
 
 
+class zs_mx4_launch(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("cluster", "split", "stages", "shared_bytes", "tmem_columns", "reserved")]
+
+
 _P = C.c_void_p
 _i32, _i64, _f32 = C.c_int32, C.c_int64, C.c_float
 
@@ -202,6 +206,7 @@ _sig("zs_adam_tensors", _i32, [_P, C.POINTER(zs_adam_hparams), _i64, _i32, C.c_u
 _sig("zs_mx4_sizes", _i32, [_i64, _i64, C.POINTER(_i64), C.POINTER(_i64), C.POINTER(_i64)])
 _sig("zs_mx4_quantize", _i32, [_P, _i64, _i64, _i64, _i32, _P, _P, _P, _P, _P])
 _sig("zs_mx4_dequantize", _i32, [_P, _P, _i64, _i64, _P, _i64, _i32, _P])
+_sig("zs_test_mx4_launch", _i32, [_i64, _i64, _i64, C.POINTER(zs_mx4_launch)])
 _sig("zs_mx4_matmul", _i32, [_i64, _i64, _i64, _P, _P, _P, _P, _P, _i64, _i32, _P])
 
 
@@ -780,3 +785,10 @@ def zs_mx4_matmul(a, b, k: int, out, stream=None):
     if st:
         _check(st, "zs_mx4_matmul")
     return out
+
+
+def zs_test_mx4_launch(m: int, n: int, k: int) -> dict:
+    """What a CTA of zs_mx4_matmul's launch asks of its SM (for tests)."""
+    o = zs_mx4_launch()
+    _check(_lib.zs_test_mx4_launch(int(m), int(n), int(k), C.byref(o)), "zs_test_mx4_launch")
+    return _to_dict(o)

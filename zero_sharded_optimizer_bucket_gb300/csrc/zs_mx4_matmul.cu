@@ -33,6 +33,17 @@ constexpr uint64_t MM_WAIT_NS = 1000000000ull;   // one wait gives up after 1 s
 
 __device__ int g_mx4_wait_timeouts;       // waits that gave up
 
+// The least shared memory of a CTA that allocates `cols` columns of an SM's
+// 512 of tensor memory: the CTAs that fit an SM by their shared memory then
+// never want more columns than it has, whichever calls they are of.  (128
+// columns are one of four shares, and five do not fit.)  A CTA of a split
+// keeps its columns until its cluster's others have their sums, and
+// tcgen05.alloc waits without a bound: without this, clusters of several
+// streams that share SMs could each wait for columns that another one keeps.
+constexpr int SM_SHARED = 228 * 1024;
+constexpr int tmem_share(int cols) { return cols / 128 * ((SM_SHARED / 5 + 1024) / 1024 * 1024); }
+static_assert(5 * tmem_share(128) > SM_SHARED, "more than 512 columns would fit an SM");
+
 // P holds the tile's 128 rows, Q its BN; D[p][q].
 template <int BN>
 struct MmShape {
@@ -56,10 +67,12 @@ struct MmShape {
     // tensor memory: accumulator, then two sets of scales
     static constexpr int SP_COL = BN < 32 ? 32 : BN, SQ_COL = SP_COL + 16 * KS;
     static constexpr int USED = SQ_COL + 16 * KS;
-    static constexpr int COLS = USED <= 64 ? 64 : USED <= 128 ? 128 : 256;   // two CTAs of an SM fit
+    static constexpr int COLS = USED <= 128 ? 128 : 256;                     // two CTAs of an SM fit
     static constexpr int RED = BN * MM_P * 4 + 16 * (BN > MM_P ? BN : MM_P);   // the tile, rows 16 bytes apart
-    static constexpr int smem(int stages) { return (stages * STAGE > RED ? stages * STAGE : RED) + 1024; }   // with room to align
+    static constexpr int need(int stages) { return (stages * STAGE > RED ? stages * STAGE : RED) + 1024; }   // with room to align
+    static constexpr int smem(int stages) { return need(stages) > tmem_share(COLS) ? need(stages) : tmem_share(COLS); }
     static constexpr int SMEM = smem(STAGES);
+    static_assert(COLS % 128 == 0 && smem(1) >= tmem_share(COLS), "CTAs that share an SM have to find their columns");
 };
 
 struct MmArgs {
@@ -411,6 +424,7 @@ struct PairShape {
     static constexpr int SLAB = 32 * ROW;
     static constexpr int BARS = STAGES * PAIR_STAGE + 8 * SLAB;      // the barriers are after them
     static constexpr int SMEM = BARS + 256;
+    static_assert(SMEM >= tmem_share(512), "nothing else of tensor memory shares the SM");
     // the 16-byte pieces of a row are turned by this: no bank conflicts
     static __device__ __forceinline__ int turn(int row) { return ROW == 128 ? row & 7 : (row >> 1) & 3; }
 };
@@ -739,19 +753,76 @@ static cudaError_t pair_launch(const CUtensorMap (&map)[4], const PairArgs &a, c
     return launch_dependent(mx4_matmul_pair_kernel<STAGES>, (unsigned)(2 * pairs), PAIR_THREADS, PairShape<STAGES>::SMEM, 2, s, map[0], map[1], map[2], map[3], a);
 }
 
-template <int BN, bool FLIP>
-static cudaError_t mm_launch(const CUtensorMap &p, const CUtensorMap &q, MmArgs &a, cudaStream_t s) {
+// What zs_mx4_matmul launches for a product.
+struct MmPlan {
+    bool pair, flip;
+    int bn, split, stages;
+    int smem, columns;        // of a CTA: shared memory, tensor memory
+    int64_t p_tiles, q_tiles;
+};
+
+template <int BN>
+static void mm_ring(MmPlan &r, int k_tiles) {
     using S = MmShape<BN>;
+    const int steps = ((k_tiles + r.split - 1) / r.split + S::KS - 1) / S::KS;     // of the longest part
+    r.stages = steps < S::STAGES ? steps : S::STAGES;
+    r.smem = S::smem(r.stages);
+    r.columns = S::COLS;
+}
+
+static MmPlan mm_plan(int64_t m, int64_t n, int64_t k) {
+    MmPlan r = {};
+    const int k_tiles = (int)((k + 255) / 256);
+    // The pair kernel from half a tile a pair on: 640 x 4096 x 4096 (48 tiles)
+    // takes it 10.4 us, the other kernel 11.2; 1024 x 4096 x 14336 (64 tiles)
+    // 21.3 and 25.1; 512 x 4096 x 4096 and 2048 x 1024 x 4096 (32 tiles) 9.6
+    // and 8.5.
+    r.p_tiles = (m + PAIR_ROWS - 1) / PAIR_ROWS;
+    r.q_tiles = (n + PAIR_COLS - 1) / PAIR_COLS;
+    if (m > 128 && r.p_tiles * r.q_tiles >= 38 && r.p_tiles * r.q_tiles < 0x7FFF0000) {
+        r.pair = true;
+        r.bn = PAIR_COLS;
+        r.split = 1;
+        // Every pair of the 76 has (tiles / 76) k_tiles stages.  When they are
+        // many, 6 in flight: 8192 x 8192 x 8192 154 -> 148 us (fp32 out 169 ->
+        // 160), 4096 x 4096 x 11008 59.6 -> 58.7; when few, the store after the
+        // last tile counts, and slabs of whole lines: 1024 x 4096 x 4096 10.6 us
+        // against 11.4, 4097 x 4100 x 4096 (64 stages) 28.6 against 29.1.
+        r.stages = (r.p_tiles * r.q_tiles + 75) / 76 * k_tiles >= 128 ? 6 : 5;
+        r.smem = r.stages == 6 ? PairShape<6>::SMEM : PairShape<5>::SMEM;
+        r.columns = 512;
+        return r;
+    }
+    // 128 features a tile for up to 64 tokens: 64 x 4096 x 4096 5.2 us, 5.8 with
+    // 128 tokens a tile; 48 x 1024 x 4096 4.3 us against 5.0.
+    r.flip = m <= 64;
+    r.bn = !r.flip ? 128 : m <= 16 ? 16 : m <= 32 ? 32 : 64;   // flipped, one tile of Q: scale addresses are whole atoms
+    r.p_tiles = ((r.flip ? n : m) + MM_P - 1) / MM_P;
+    r.q_tiles = ((r.flip ? m : n) + r.bn - 1) / r.bn;
+    // k is shared out while that leaves an SM to every CTA and each enough
+    // stages to hide its part of the sum.  One token through 4096 x 4096 (32
+    // tiles) took 5.8, 4.9, 4.2 and 4.5 us in 1, 2, 4 and 8 parts, 256 x 4096 x
+    // 14336 (64 tiles) 17.3, 12.5 and 14.4 us in 1, 2 and 4; more CTAs than SMs
+    // lose: 16 x 14336 x 4096 (112 tiles) 6.2 us in one part, 9.7 in four.
+    r.split = 1;
+    while (r.split < 8 && r.p_tiles * r.q_tiles * r.split * 2 <= 152 && k_tiles >= (r.bn == 128 ? 8 : 4) * r.split) r.split *= 2;
+    if (r.bn == 16) mm_ring<16>(r, k_tiles);
+    else if (r.bn == 32) mm_ring<32>(r, k_tiles);
+    else if (r.bn == 64) mm_ring<64>(r, k_tiles);
+    else mm_ring<128>(r, k_tiles);
+    return r;
+}
+
+template <int BN, bool FLIP>
+static cudaError_t mm_launch(const MmPlan &r, const CUtensorMap &p, const CUtensorMap &q, const MmArgs &a, cudaStream_t s) {
     static std::atomic<int> known[64];
     int sms = 0;
     cudaError_t e = device_sms(known, [] {
-        return cudaFuncSetAttribute(mx4_matmul_kernel<BN, FLIP>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        return cudaFuncSetAttribute(mx4_matmul_kernel<BN, FLIP>, cudaFuncAttributeMaxDynamicSharedMemorySize, MmShape<BN>::SMEM);
     }, &sms);
     if (e != cudaSuccess) return e;
-    const int steps = ((a.k_tiles + a.split - 1) / a.split + S::KS - 1) / S::KS;     // of the longest part
-    a.stages = steps < S::STAGES ? steps : S::STAGES;
-    return launch_dependent(mx4_matmul_kernel<BN, FLIP>, (unsigned)((int64_t)a.p_tiles * a.q_tiles * a.split), MM_THREADS, S::smem(a.stages),
-                            (unsigned)a.split, s, p, q, a);
+    return launch_dependent(mx4_matmul_kernel<BN, FLIP>, (unsigned)(r.p_tiles * r.q_tiles * r.split), MM_THREADS, r.smem,
+                            (unsigned)r.split, s, p, q, a);
 }
 
 }  // namespace zsk
@@ -794,78 +865,65 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *
     for (const void *p : four)
         if (!p || (reinterpret_cast<uintptr_t>(p) & 15))
             return zs_fail(ZS_EINVAL, "%s: codes or scales NULL or not 16-byte aligned", fn);
+    using namespace zsk;
+    const MmPlan r = mm_plan(m, n, k);
     cudaError_t e;
-    // The pair kernel from half a tile a pair on: 640 x 4096 x 4096 (48 tiles)
-    // takes it 10.4 us, the other kernel 11.2; 1024 x 4096 x 14336 (64 tiles)
-    // 21.3 and 25.1; 512 x 4096 x 4096 and 2048 x 1024 x 4096 (32 tiles) 9.6
-    // and 8.5.
-    const int64_t pair_p = (m + zsk::PAIR_ROWS - 1) / zsk::PAIR_ROWS, pair_q = (n + zsk::PAIR_COLS - 1) / zsk::PAIR_COLS;
-    if (m > 128 && pair_p * pair_q >= 38 && pair_p * pair_q < 0x7FFF0000) {
+    if (r.pair) {
         CUtensorMap map[4];
-        if (!zsk::code_map(&map[0], a_codes, m, mx4_row_bytes(k), 128) || !zsk::code_map(&map[1], b_codes, n, mx4_row_bytes(k), 128) ||
-            !zsk::scale_map(&map[2], a_scales, m, k, 1) || !zsk::scale_map(&map[3], b_scales, n, k, 2))
+        if (!code_map(&map[0], a_codes, m, mx4_row_bytes(k), 128) || !code_map(&map[1], b_codes, n, mx4_row_bytes(k), 128) ||
+            !scale_map(&map[2], a_scales, m, k, 1) || !scale_map(&map[3], b_scales, n, k, 2))
             return zs_fail(ZS_ECUDA, "%s: cuTensorMapEncodeTiled failed", fn);
-        zsk::PairArgs a;
+        PairArgs a;
         a.out = out;
         a.ldo = ldo;
         a.m = (int32_t)m;
         a.n = (int32_t)n;
         a.k_tiles = (int32_t)((k + 255) / 256);
-        a.p_tiles = (int32_t)pair_p;
-        a.tiles = (int32_t)(pair_p * pair_q);
+        a.p_tiles = (int32_t)r.p_tiles;
+        a.tiles = (int32_t)(r.p_tiles * r.q_tiles);
         a.dtype = dtype;
         a.vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ldo * size % 16 == 0;
-        // Every pair of the 76 has (tiles / 76) k_tiles stages.  When they are
-        // many, 6 in flight: 8192 x 8192 x 8192 154 -> 148 us (fp32 out 169 ->
-        // 160), 4096 x 4096 x 11008 59.6 -> 58.7; when few, the store after the
-        // last tile counts, and slabs of whole lines: 1024 x 4096 x 4096 10.6 us
-        // against 11.4, 4097 x 4100 x 4096 (64 stages) 28.6 against 29.1.
-        e = (pair_p * pair_q + 75) / 76 * a.k_tiles >= 128 ? zsk::pair_launch<6>(map, a, s) : zsk::pair_launch<5>(map, a, s);
+        e = r.stages == 6 ? pair_launch<6>(map, a, s) : pair_launch<5>(map, a, s);
         if (e != cudaSuccess) return zs_fail(ZS_ECUDA, "%s: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
         zs_clear_error();
         return ZS_OK;
     }
-    // 128 features a tile for up to 64 tokens: 64 x 4096 x 4096 5.2 us, 5.8 with
-    // 128 tokens a tile; 48 x 1024 x 4096 4.3 us against 5.0.
-    const bool flip = m <= 64;
-    const int64_t np = flip ? n : m, nq = flip ? m : n;
-    const void *p_codes = flip ? b_codes : a_codes, *p_scales = flip ? b_scales : a_scales;
-    const void *q_codes = flip ? a_codes : b_codes, *q_scales = flip ? a_scales : b_scales;
-    int bn = 128;
-    if (flip) bn = nq <= 16 ? 16 : nq <= 32 ? 32 : 64;   // one tile of Q: scale addresses are whole atoms
-    zsk::MmArgs a;
-    a.p_scales = static_cast<const uint8_t *>(p_scales);
-    a.q_scales = static_cast<const uint8_t *>(q_scales);
+    if (r.p_tiles * r.q_tiles * r.split > 0x7FFFFFFF) return zs_fail(ZS_EINVAL, "%s: too many tiles", fn);
+    const int64_t np = r.flip ? n : m, nq = r.flip ? m : n;
+    MmArgs a;
+    a.p_scales = static_cast<const uint8_t *>(r.flip ? b_scales : a_scales);
+    a.q_scales = static_cast<const uint8_t *>(r.flip ? a_scales : b_scales);
     a.out = out;
     a.ldo = ldo;
     a.np = (int32_t)np;
     a.nq = (int32_t)nq;
     a.k_tiles = (int32_t)((k + 255) / 256);
     a.atoms = (int32_t)mx4_atoms(k);
-    const int64_t pt = (np + 127) / 128, qt = (nq + bn - 1) / bn;
-    a.p_tiles = (int32_t)pt;
-    a.q_tiles = (int32_t)qt;
-    // k is shared out while that leaves an SM to every CTA and each enough
-    // stages to hide its part of the sum.  One token through 4096 x 4096 (32
-    // tiles) took 5.8, 4.9, 4.2 and 4.5 us in 1, 2, 4 and 8 parts, 256 x 4096 x
-    // 14336 (64 tiles) 17.3, 12.5 and 14.4 us in 1, 2 and 4; more CTAs than SMs
-    // lose: 16 x 14336 x 4096 (112 tiles) 6.2 us in one part, 9.7 in four.
-    int split = 1;
-    while (split < 8 && pt * qt * split * 2 <= 152 && a.k_tiles >= (bn == 128 ? 8 : 4) * split) split *= 2;
-    if (pt * qt * split > 0x7FFFFFFF) return zs_fail(ZS_EINVAL, "%s: too many tiles", fn);
-    a.split = split;
+    a.p_tiles = (int32_t)r.p_tiles;
+    a.q_tiles = (int32_t)r.q_tiles;
+    a.split = r.split;
+    a.stages = r.stages;
     a.dtype = dtype;
     a.vec = reinterpret_cast<uintptr_t>(out) % (4 * size) == 0 && ldo % 4 == 0;
     CUtensorMap mp, mq;
-    if (!zsk::code_map(&mp, p_codes, np, mx4_row_bytes(k), zsk::MM_P) ||
-        !zsk::code_map(&mq, q_codes, nq, mx4_row_bytes(k), bn))
+    if (!code_map(&mp, r.flip ? b_codes : a_codes, np, mx4_row_bytes(k), MM_P) ||
+        !code_map(&mq, r.flip ? a_codes : b_codes, nq, mx4_row_bytes(k), r.bn))
         return zs_fail(ZS_ECUDA, "%s: cuTensorMapEncodeTiled failed", fn);
-    using namespace zsk;
-    if (flip)
-        e = bn == 16 ? mm_launch<16, true>(mp, mq, a, s) : bn == 32 ? mm_launch<32, true>(mp, mq, a, s) : mm_launch<64, true>(mp, mq, a, s);
+    if (r.flip)
+        e = r.bn == 16 ? mm_launch<16, true>(r, mp, mq, a, s) : r.bn == 32 ? mm_launch<32, true>(r, mp, mq, a, s) : mm_launch<64, true>(r, mp, mq, a, s);
     else
-        e = mm_launch<128, false>(mp, mq, a, s);
+        e = mm_launch<128, false>(r, mp, mq, a, s);
     if (e != cudaSuccess) return zs_fail(ZS_ECUDA, "%s: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
+    zs_clear_error();
+    return ZS_OK;
+}
+
+extern "C" zs_status zs_test_mx4_launch(int64_t m, int64_t n, int64_t k, zs_mx4_launch *out) {
+    constexpr int64_t MOST = (int64_t)1 << 31;
+    if (!out || m < 1 || n < 1 || k < 1 || m >= MOST || n >= MOST || k >= MOST)
+        return zs_fail(ZS_EINVAL, "zs_test_mx4_launch: NULL result or m, n, k out of range");
+    const zsk::MmPlan r = zsk::mm_plan(m, n, k);
+    *out = {r.pair ? 2 : r.split, r.split, r.stages, r.smem, r.columns, 0};
     zs_clear_error();
     return ZS_OK;
 }
