@@ -446,6 +446,13 @@ zs_status zs_device_wait_timeouts(int32_t *count, int32_t reset);
  * no counterpart in the pages.  Errors: ZS_EINVAL (limit), ZS_ECUDA. */
 zs_status zs_test_wait_timeout(int64_t limit_ns, void *stream);
 
+/* Test hook for calls that begin while the previous kernel still works
+ * (programmatic dependent launch): one CTA that lets its dependents begin at
+ * once, works on for delay_ns nanoseconds (0 < delay_ns <= 2e9), and then
+ * copies src to dst (device memory, 16-byte aligned, a multiple of 16
+ * bytes).  Errors: ZS_EINVAL, ZS_ECUDA. */
+zs_status zs_test_late_copy(void *dst, const void *src, int64_t bytes, int64_t delay_ns, void *stream);
+
 /* What a CTA of the kernel asks of its SM that zs_mx4_matmul launches for a
  * product of these sizes (for tests; host only). */
 typedef struct {

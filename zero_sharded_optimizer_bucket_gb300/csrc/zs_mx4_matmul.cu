@@ -489,10 +489,12 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
     asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
     const uint32_t tmem = tmem_base;
     pdl_trigger();                         // tensor memory is allocated: the next kernel may wait for its own
+    // every role: the limits of the waits below begin when the loads can, not
+    // while the previous kernel still works
+    pdl_wait();
 
     int issued = 0;
     if (warp == 8) {
-        pdl_wait();
         // loads of this CTA: its half of the rows of A and of B, the scales
         // of its rows of A, and all the tile's scales of B
         bool ok = true;
