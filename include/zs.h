@@ -453,6 +453,15 @@ zs_status zs_test_wait_timeout(int64_t limit_ns, void *stream);
  * bytes).  Errors: ZS_EINVAL, ZS_ECUDA. */
 zs_status zs_test_late_copy(void *dst, const void *src, int64_t bytes, int64_t delay_ns, void *stream);
 
+/* Test hook for the waits of zs_mx4_matmul: in every call from now on (of any
+ * thread) the operands of stage `at` (0, 1, ..: in the order in which a CTA,
+ * or a pair of them, takes its stages; where CTAs share the k of a tile, in
+ * the last part alone) seem to lack bytes that never come, and the wait for
+ * them gives up at its limit.  The tiles that it is part of are NaN or as they were,
+ * zs_device_wait_timeouts counts it, and the context stays usable.  -1: none
+ * (the state at first).  Errors: ZS_EINVAL. */
+zs_status zs_test_give_up(int32_t at);
+
 /* What a CTA of the kernel asks of its SM that zs_mx4_matmul launches for a
  * product of these sizes (for tests; host only). */
 typedef struct {
@@ -777,7 +786,8 @@ zs_status zs_mx4_dequantize(const void *codes, const void *scales, int64_t rows,
  *   dx = matmul(dy along rows, w along cols)     k = outputs
  *   dw = matmul(dy along cols, x along cols)     k = tokens
  * k = 0 gives zeros.  Errors: ZS_EINVAL, ZS_ECUDA; a device wait that gave
- * up is counted by zs_device_wait_timeouts. */
+ * up is counted by zs_device_wait_timeouts; the tiles of out that it held up
+ * are NaN or as they were. */
 zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *a_codes, const void *a_scales,
                         const void *b_codes, const void *b_scales, void *out, int64_t ldo,
                         int32_t dtype, void *stream);

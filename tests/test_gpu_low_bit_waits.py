@@ -93,3 +93,46 @@ def test_previous_kernel_past_the_limit(name):
     assert time.perf_counter() - t0 > 1.4 * LIMIT
     assert torch.equal(early, late) and torch.equal(got, results[0]) and not torch.equal(got, results[1])
     assert zs.zs_device_wait_timeouts(reset=True) == 0
+
+
+@pytest.fixture
+def give_up():
+    zs.zs_device_wait_timeouts(reset=True)
+    yield zs.zs_test_give_up
+    zs.zs_test_give_up(-1)
+    torch.cuda.synchronize()
+    zs.zs_device_wait_timeouts(reset=True)
+
+
+# sizes, the stage whose wait runs out, and how many tiles of 256 x 256 a pair has finished before (None: not the pairs' kernel)
+KINDS = {20: torch.bfloat16, 64: torch.float16, 1290: torch.bfloat16}      # by m; else fp32
+GIVE_UP = [(5, 300, 8192, 0, None), (5, 300, 8192, 1, None), (20, 300, 8192, 1, None), (64, 300, 8192, 0, None), (200, 300, 8192, 0, None),
+           (200, 300, 8192, 3, None), (100, 9900, 512, 1, None), (5, 40000, 8192, 7, None), (1290, 1801, 704, 0, 0), (1290, 1801, 704, 2, 0),
+           (1290, 1801, 4096, 9, 0), (1290, 1801, 33024, 100, 0), (4096, 5120, 512, 3, 1), (4096, 5120, 512, 4, 2)]
+
+
+@pytest.mark.parametrize("m,n,k,at,finished", GIVE_UP)
+def test_product_gives_up(m, n, k, at, finished, give_up):
+    """A wait for operands that gives up: no CTA of its tile stores a sum of some parts (pairs leave the tile as it was, the other
+    kernel writes NaN); it is counted; the next call is right."""
+    a, b = held(m, k, 1), held(n, k, 2)
+    launch = zs.zs_test_mx4_launch(m, n, k)
+    assert (launch["tmem_columns"] == 512) == (finished is not None)
+    out = torch.full((m, n), 77.0, device="cuda", dtype=KINDS.get(m, torch.float32))
+    want = zs.zs_mx4_matmul(a, b, k, torch.empty_like(out))
+    give_up(at)
+    zs.zs_mx4_matmul(a, b, k, out)
+    give_up(-1)
+    torch.cuda.synchronize()
+    assert zs.zs_device_wait_timeouts(reset=True) > 0
+    kept = out == 77.0
+    if finished is None:
+        assert bool(out.isnan().all())
+    else:                              # tiles go down the columns of tiles, the pairs one after the other
+        tiles = -(-m // 256)
+        order = (torch.arange(m, device="cuda") // 256)[:, None] + tiles * (torch.arange(n, device="cuda") // 256)[None, :]
+        done = order < finished * (torch.cuda.get_device_properties(0).multi_processor_count // 2)
+        assert torch.equal(out[done], want[done]) and bool(kept[~done].all())
+    zs.zs_mx4_matmul(a, b, k, out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and zs.zs_device_wait_timeouts() == 0

@@ -85,3 +85,5 @@ cudaError_t zsl_wait_timeout_test(int64_t limit_ns, cudaStream_t s);
 cudaError_t zsl_mx4_wait_timeouts(int *count, bool reset);
 cudaError_t zsl_quantize_wait_timeouts(int *count, bool reset);
 cudaError_t zsl_tensors_wait_timeouts(int *count, bool reset);
+// The stage of operands whose wait is to give up (zs_test_give_up), or -1.
+int zsl_test_give_up();

@@ -86,6 +86,7 @@ struct MmArgs {
     int32_t stages;           // of the ring
     int32_t dtype;
     int32_t vec;              // rows of out are aligned to 4 elements
+    int32_t give_up;          // for tests: the stage of the last part whose wait runs out, or -1
 };
 
 __device__ __forceinline__ uint64_t mm_desc(uint32_t addr, uint32_t sbo, uint64_t layout) {
@@ -162,10 +163,12 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     // behind the __syncthreads below
     const uint8_t *sp = a.p_scales + ((int64_t)pt * a.atoms) * MX4_ATOM;
     const int steps = (k1 - k0 + S::KS - 1) / S::KS;
+    const int give_up = part == a.split - 1 ? a.give_up : -1;
     auto load = [&](int i, int s) {
         if (elect_one()) {
             const int n = min(S::KS, k1 - k0 - i * S::KS);
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(n * S::SUB) : "memory");
+            // (give_up: 16 bytes that never come)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(n * S::SUB + (i == give_up ? 16 : 0)) : "memory");
 #pragma unroll
             for (int h = 0; h < S::KS; ++h) {
                 if (h >= n) break;
@@ -230,7 +233,12 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
         uint32_t phase = 0;
         for (int i = 0; i < steps; ++i) {
             if (!warp_wait(full(s), phase, MM_WAIT_NS)) {
+                // the storing warps are to know it, and to find no load in
+                // flight to where they write, when they see `done`
+                for (int j = i + 1; j < steps && j < i + stages; ++j)
+                    if (!warp_wait(full(j % stages), (uint32_t)((j / stages) & 1), MM_WAIT_NS)) break;
                 failed = 1;
+                __threadfence_block();
                 break;
             }
             asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
@@ -273,12 +281,15 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
                 phase ^= 1;
             }
         }
+        __syncwarp();
         if (elect_one()) tc_commit(done);
         __syncwarp();
     }
     // everyone waits until the products of this CTA are in tensor memory
     if (!mbar_wait_quick(done, 0, 4 * MM_WAIT_NS + 4000ull * (uint64_t)(k1 - k0))) failed = 1;
     __syncwarp();
+    // an unfinished sum is NaN, for the other parts of a split too
+    const bool unfinished = failed;
     asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory");
     // The tile goes to shared memory as rows of out (the loads and products
     // that used it are done), then the CTAs of a split share it out, each
@@ -292,6 +303,10 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
             if (FLIP && c >= rows) break;
             uint32_t v[32];
             tc_ld32(tmem + ((uint32_t)warp << 21) + c, v);
+            if (unfinished) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0x7FC00000u;
+            }
             if (FLIP) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
@@ -310,7 +325,7 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
     __syncwarp();
     if (a.split > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" : : : "memory");
     else __syncthreads();
-    if (!failed) {
+    {
         const int es = a.dtype == ZS_DTYPE_FP32 ? 4 : 2;
         const int units = rows * (COLS / 4), step = a.split * MM_THREADS;      // runs of 4 columns
         auto store = [&](int u, const float (&f)[4]) {
@@ -453,6 +468,7 @@ struct PairArgs {
     int32_t k_tiles, p_tiles, tiles;
     int32_t dtype;
     int32_t vec;              // rows of out are 16-byte aligned
+    int32_t give_up;          // for tests: the stage (of a pair's) whose wait runs out, or -1
 };
 
 template <int STAGES>
@@ -511,7 +527,7 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
                 if (elect_one()) {
                     const uint32_t bar = map_to(full(s), 0);       // the leader multiplies for both
                     if (rank == 0)
-                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(2 * PAIR_STAGE) : "memory");
+                        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(full(s)), "r"(2 * PAIR_STAGE + (issued == a.give_up ? 16 : 0)) : "memory");
                     tma2d_pair(p, &map_p, k * MM_KB, pt * PAIR_ROWS + rank * 128, bar);
                     tma2d_pair(q, &map_q, k * MM_KB, qt * PAIR_COLS + rank * 128, bar);
                     tma2d_pair(sp, &map_sp, k * (PAIR_SP / 4), pt * 2 + rank, bar);
@@ -570,7 +586,9 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
                 }
                 __syncwarp();
             }
-            if (elect_one()) tc_commit_pair(acc_full);
+            // an unfinished sum is never signalled: the storing warps of both
+            // CTAs give up in their turn and leave the tile as it was
+            if (ok && elect_one()) tc_commit_pair(acc_full);
             __syncwarp();
         }
     } else if (warp < 8) {
@@ -885,6 +903,7 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *
         a.tiles = (int32_t)(r.p_tiles * r.q_tiles);
         a.dtype = dtype;
         a.vec = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ldo * size % 16 == 0;
+        a.give_up = zsl_test_give_up();
         e = r.stages == 6 ? pair_launch<6>(map, a, s) : pair_launch<5>(map, a, s);
         if (e != cudaSuccess) return zs_fail(ZS_ECUDA, "%s: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
         zs_clear_error();
@@ -907,6 +926,7 @@ extern "C" zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *
     a.stages = r.stages;
     a.dtype = dtype;
     a.vec = reinterpret_cast<uintptr_t>(out) % (4 * size) == 0 && ldo % 4 == 0;
+    a.give_up = zsl_test_give_up();
     CUtensorMap mp, mq;
     if (!code_map(&mp, r.flip ? b_codes : a_codes, np, mx4_row_bytes(k), MM_P) ||
         !code_map(&mq, r.flip ? a_codes : b_codes, nq, mx4_row_bytes(k), r.bn))

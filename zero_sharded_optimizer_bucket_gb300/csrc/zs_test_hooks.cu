@@ -1,7 +1,20 @@
 // Kernels and switches for tests of the bounded waits: they make the rare
 // event that a wait must survive, and nothing faults, traps or hangs.
+#include <atomic>
+
 #include "zs_device.cuh"
 #include "zs_launch.h"
+
+static std::atomic<int> g_give_up{-1};       // zs_test_give_up
+
+int zsl_test_give_up() { return g_give_up.load(std::memory_order_relaxed); }
+
+extern "C" zs_status zs_test_give_up(int32_t at) {
+    if (at < -1) return zs_fail(ZS_EINVAL, "zs_test_give_up: %d", at);
+    g_give_up.store(at, std::memory_order_relaxed);
+    zs_clear_error();
+    return ZS_OK;
+}
 
 namespace zsk {
 
