@@ -696,14 +696,15 @@ mx4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_c
         }
     }
     __syncwarp();
+    asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
+    __syncthreads();                       // every role has said whether it gave up
     if (warp == 8 && lane == 0 && failed) {
         if (rank == 0)   // the leader's barriers count the loads of both CTAs
             for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
                 mbar_wait_quick(full(i % STAGES), (uint32_t)((i / STAGES) & 1), MM_WAIT_NS);
         atomicAdd(&g_mx4_wait_timeouts, 1);
     }
-    asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory");
-    __syncthreads();
+    __syncwarp();
     // neither CTA leaves while the other may still write to its barriers
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" : : : "memory");
     if (warp == 0) {
