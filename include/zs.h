@@ -453,13 +453,14 @@ zs_status zs_test_wait_timeout(int64_t limit_ns, void *stream);
  * bytes).  Errors: ZS_EINVAL, ZS_ECUDA. */
 zs_status zs_test_late_copy(void *dst, const void *src, int64_t bytes, int64_t delay_ns, void *stream);
 
-/* Test hook for the waits of zs_mx4_matmul: in every call from now on (of any
+/* Test hook for the waits of zs_mx4_matmul, zs_mx4_quantize and
+ * zs_adam_tensors with 8-bit moments: in every call from now on (of any
  * thread) the operands of stage `at` (0, 1, ..: in the order in which a CTA,
  * or a pair of them, takes its stages; where CTAs share the k of a tile, in
  * the last part alone) seem to lack bytes that never come, and the wait for
- * them gives up at its limit.  The tiles that it is part of are NaN or as they were,
- * zs_device_wait_timeouts counts it, and the context stays usable.  -1: none
- * (the state at first).  Errors: ZS_EINVAL. */
+ * them gives up at its limit.  What hangs on them is left as it was, or NaN
+ * in a product, zs_device_wait_timeouts counts it, and the context stays
+ * usable.  -1: none (the state at first).  Errors: ZS_EINVAL. */
 zs_status zs_test_give_up(int32_t at);
 
 /* What a CTA of the kernel asks of its SM that zs_mx4_matmul launches for a
@@ -742,7 +743,8 @@ zs_status zs_tensors_upload(zs_tensors *list, void *d_table, int64_t bytes, void
  *   An element whose m or r is not finite gets a NaN code and does not count
  *   for the scale.
  * step >= 1.  Errors: ZS_EINVAL, ZS_ESTATE (not uploaded), ZS_ECUDA; a
- * device wait that gave up is counted by zs_device_wait_timeouts. */
+ * device wait that gave up is counted by zs_device_wait_timeouts, and leaves
+ * the blocks that it held up as they were. */
 zs_status zs_adam_tensors(const zs_tensors *list, const zs_adam_hparams *hp, int64_t step,
                           int32_t rounding, uint64_t seed, const float *d_clip_coef,
                           const int32_t *d_flags, void *stream);
@@ -771,7 +773,7 @@ zs_status zs_mx4_sizes(int64_t rows, int64_t cols, int64_t *row_bytes, int64_t *
  * x * 2^(127-s) to nearest, ties to even, at most 6 in magnitude.  A group
  * with an infinity or NaN has s = 255 and codes 0: it is NaN in every
  * product.  Errors: ZS_EINVAL, ZS_ECUDA; a device wait that gave up is
- * counted by zs_device_wait_timeouts. */
+ * counted by zs_device_wait_timeouts, and leaves tiles as they were. */
 zs_status zs_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
                           void *r_codes, void *r_scales, void *c_codes, void *c_scales,
                           void *stream);

@@ -136,3 +136,78 @@ def test_product_gives_up(m, n, k, at, finished, give_up):
     zs.zs_mx4_matmul(a, b, k, out)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and zs.zs_device_wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("at", [0, 1, 3])
+def test_quantiser_gives_up(kind, at, give_up):
+    """A CTA whose wait for its unit `at` gives up writes nothing from there on: tiles go row by row, the CTAs one after the other."""
+    rows, cols = 20000, 1100
+    x = torch.randn(rows, cols + 4, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).to(kind)[:, :cols]
+    size = zs.zs_mx4_sizes(rows, cols)
+
+    def run():
+        h = dict(codes=torch.full((rows, size["row_bytes"]), 0xA5, dtype=torch.uint8, device="cuda"),
+                 scales=torch.full((size["scale_bytes"],), 0xA5, dtype=torch.uint8, device="cuda"))
+        zs.zs_mx4_quantize(x, rows=h)
+        torch.cuda.synchronize()
+        return h
+
+    want = run()
+    give_up(at)
+    got = run()
+    give_up(-1)
+    assert zs.zs_device_wait_timeouts(reset=True) > 0
+    ctas = 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    tiles_c = size["scale_bytes"] // 512 // -(-rows // 128)
+    # the units of a tile are its columns 0..127, or (fp32) 0..63 and 64..127; 64 bytes a row of a tile
+    units = 2 if kind == torch.float32 else 1
+    row, byte = torch.meshgrid(torch.arange(rows, device="cuda"), torch.arange(size["row_bytes"], device="cuda"), indexing="ij")
+    tile = row // 128 * tiles_c + byte // 64
+    unit = tile // ctas * units + (byte % 64) // (64 // units)
+    done = unit < at
+    assert torch.equal(got["codes"][done], want["codes"][done]) and bool((got["codes"][~done] == 0xA5).all())
+    tile = torch.arange(size["scale_bytes"], device="cuda") // 512
+    done = tile // ctas * units + units - 1 < at       # a tile's scales come with its last unit
+    assert torch.equal(got["scales"][done], want["scales"][done]) and bool((got["scales"][~done] == 0xA5).all())
+    for name, t in run().items():
+        assert torch.equal(t, want[name])
+    assert zs.zs_device_wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("at", [0, 2])
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rounding", ["nearest", "stochastic"])
+def test_update_gives_up(at, kind, rounding, give_up):
+    """The blocks of the stage whose wait gives up (8 blocks of 256 of each chunk of 6144) stay as they were, the others are updated."""
+    n = 2_000_128                                       # a last block of 256
+    g = torch.Generator(device="cuda").manual_seed(5)
+    first = dict(grad=(torch.randn(n, device="cuda", generator=g) * 1e-3).to(kind), param=torch.zeros(n, dtype=torch.bfloat16, device="cuda"),
+                 master=torch.randn(n, device="cuda", generator=g), exp_avg=torch.full((n,), 0x30, dtype=torch.uint8, device="cuda"),
+                 exp_avg_sq=torch.full((n,), 0x31, dtype=torch.uint8, device="cuda"), exp_avg_scale=torch.full((n // 256,), 1e-5, device="cuda"),
+                 exp_avg_sq_scale=torch.full((n // 256,), 1e-5, device="cuda"))
+
+    def run():
+        t = {k: v.clone() for k, v in first.items()}
+        lst = zs.zs_build_tensors([t], state_bits=8)
+        info = zs.zs_tensors_info(lst)
+        assert info["n_chunks"] == -(-n // 6144)
+        table = torch.empty(info["device_table_bytes"], dtype=torch.uint8, device="cuda")
+        zs.zs_tensors_upload(lst, table, table.numel())
+        zs.zs_adam_tensors(lst, dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01), 2, rounding=rounding, seed=7)
+        torch.cuda.synchronize()
+        return t
+
+    want = run()
+    give_up(at)
+    got = run()
+    give_up(-1)
+    assert zs.zs_device_wait_timeouts(reset=True) > 0
+    kept = torch.arange(n, device="cuda") % 6144 // 2048 == at
+    for name, t in got.items():
+        held_up = kept[::256] if name.endswith("scale") else kept
+        assert torch.equal(t[held_up], first[name][held_up]), name
+        assert torch.equal(t[~held_up], want[name][~held_up]), name
+    for name, t in run().items():
+        assert torch.equal(t, want[name])
+    assert zs.zs_device_wait_timeouts() == 0

@@ -795,7 +795,7 @@ def zs_test_late_copy(dst, src, nbytes: int, delay_ns: int, stream=None) -> None
 
 
 def zs_test_give_up(at: int = -1) -> None:
-    """From now on the waits for stage `at` of a product's operands run out; -1: none (test hook)."""
+    """From now on the waits for stage `at` of the low-memory kernels' operands run out; -1: none (test hook)."""
     _check(_lib.zs_test_give_up(int(at)), "zs_test_give_up")
 
 

@@ -47,6 +47,7 @@ struct Mx4Args {
     uint8_t *r_codes, *r_scales;     // along the rows; NULL: not wanted
     uint8_t *c_codes, *c_scales;     // along the columns
     int64_t tiles_c;                 // tiles along the columns of the grid
+    int32_t give_up;                 // for tests: the unit of each CTA whose wait runs out, or -1
 };
 
 // The scale byte of a group and the factor of its values (0 for a NaN group,
@@ -100,7 +101,7 @@ mx4_quantize_kernel(const __grid_constant__ CUtensorMap map, Mx4Args a, int tile
         const int tile = (int)blockIdx.x + u / UNITS * (int)gridDim.x, s = u % QS_STAGES;
         const int rt = tile / tiles_c, ct = tile - rt * tiles_c;
         const int col = ct * QT + u % UNITS * UNIT_COLS;
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(bar + 8 * s), "r"(QS_STAGE) : "memory");
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(bar + 8 * s), "r"(QS_STAGE + (u == a.give_up ? 16 : 0)) : "memory");
         tma2d(base + s * QS_STAGE, &map, col, rt * QT, bar + 8 * s);
         tma2d(base + s * QS_STAGE + QS_BOX, &map, col + BOX_COLS, rt * QT, bar + 8 * s);
     };
@@ -460,6 +461,7 @@ zs_status zs_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld,
     }
     zsk::Mx4Args a;
     a.x = x; a.rows = rows; a.cols = cols; a.ld = ld;
+    a.give_up = zsl_test_give_up();
     a.r_codes = static_cast<uint8_t *>(r_codes);
     a.r_scales = static_cast<uint8_t *>(r_scales);
     a.c_codes = static_cast<uint8_t *>(c_codes);

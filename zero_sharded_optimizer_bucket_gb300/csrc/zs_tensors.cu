@@ -422,10 +422,12 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 // SM 520 us and more).  The quotient m / den is
 // the quick one (its last two bits may be off: 2^-22 of one update, far below
 // a rounding of p); the root is exact, since codes hang on it.
+// give_up, for tests: the stage whose wait runs out (its barrier expects bytes
+// that never come), or -1.
 template <class G, bool DITHER>
 __global__ void __launch_bounds__(THREADS, 4)
 tensors8_kernel(const ZsChunk *chunks, Adam8C c, const float *d_coef,
-                const int32_t *d_flags, bool fp16) {
+                const int32_t *d_flags, bool fp16, int give_up) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[STAGES8];
     pdl_wait();
@@ -441,7 +443,7 @@ tensors8_kernel(const ZsChunk *chunks, Adam8C c, const float *d_coef,
         asm volatile("fence.proxy.async.shared::cta;" : : : "memory");
         for (int i = 0, at = 0; at < full * STATE_BLOCK; ++i, at += STAGE_ELEMS) {
             const uint32_t n = (uint32_t)min(STAGE_ELEMS, full * STATE_BLOCK - at);
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(bar + 8 * i), "r"(n * (G::SIZE + 6)) : "memory");
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" : : "r"(bar + 8 * i), "r"(n * (G::SIZE + 6) + (i == give_up ? 16 : 0)) : "memory");
             bulk_load(sg + at * G::SIZE, static_cast<const char *>(k.grad) + (int64_t)at * G::SIZE, n * G::SIZE, bar + 8 * i);
             bulk_load(sp + at * 4, k.master + at, n * 4, bar + 8 * i);
             bulk_load(sm + at, static_cast<const uint8_t *>(k.m) + at, n, bar + 8 * i);
@@ -526,7 +528,7 @@ static cudaError_t launch8(const zs_tensors *L, const Adam8C &c, const float *d_
         set[dev].store(true, std::memory_order_relaxed);
     }
     return launch_dependent(tensors8_kernel<G, DITHER>, (unsigned)L->chunks.size(), THREADS, SMEM8<G>, 1, s, L->d_chunks, c,
-                            d_coef, d_flags, fp16);
+                            d_coef, d_flags, fp16, zsl_test_give_up());
 }
 
 template <class G>
