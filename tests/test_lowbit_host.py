@@ -188,3 +188,21 @@ def test_reference_adam():
         opt.step()
         q, m, v = ref.adam64(q, m, v, g, HP, step, 0.5)
         assert np.allclose(q, p.detach().numpy(), rtol=1e-12, atol=1e-15)
+
+
+def test_list_keeps_its_tensors():
+    """The list holds addresses, so it keeps the tensors themselves, whatever becomes of the caller's dicts."""
+    import gc
+    import weakref
+
+    import torch
+    t = dict(grad=torch.zeros(300), master=torch.zeros(300), exp_avg=torch.zeros(300), exp_avg_sq=torch.zeros(300))
+    alive = [weakref.ref(x) for x in t.values()]
+    lst = zs.zs_build_tensors([t], state_bits=32)
+    t["grad"] = torch.zeros(300)                     # a training loop's next gradient
+    t.clear()
+    gc.collect()
+    assert all(r() is not None for r in alive)
+    del lst
+    gc.collect()
+    assert all(r() is None for r in alive)

@@ -628,7 +628,7 @@ def _dtype(t) -> int:
 
 
 class Tensors:
-    """Owner of a zs_tensors* (freed with the object); keeps the tensors alive."""
+    """Owner of a zs_tensors* (freed with the object); keeps the torch tensors alive."""
 
     def __init__(self, handle: int, keep):
         self._h, self._keep, self._table = handle, keep, None
@@ -657,6 +657,7 @@ def zs_build_tensors(tensors, state_bits: int = 32, grad_dtype=None, param_dtype
     dtypes = {"grad": grad_dtype, "param": param_dtype}
     n = len(tensors)
     rows = []          # the fields of each zs_tensor
+    keep = []          # the torch tensors (a caller may put others into its dicts)
     for i, t in enumerate(tensors):
         numel = t.get("numel")
         numel = t["master"].numel() if numel is None else int(numel)
@@ -683,6 +684,7 @@ def zs_build_tensors(tensors, state_bits: int = 32, grad_dtype=None, param_dtype
             elif x.itemsize != size[name]:
                 raise TypeError(f"tensor {i}: {name} is {x.dtype}, {size[name]} bytes an element expected")
             row[at] = x.data_ptr()
+            keep.append(x)
         rows += row
     flat = (_i64 * max(len(rows), 1))(*[r - (1 << 64) if r >= 1 << 63 else r for r in rows])
     arr = C.cast(flat, C.POINTER(zs_tensor))
@@ -691,7 +693,7 @@ def zs_build_tensors(tensors, state_bits: int = 32, grad_dtype=None, param_dtype
                             ZS_DTYPE_BF16 if param_dtype is None else int(param_dtype), 0)
     out = _P()
     _check(_lib.zs_build_tensors(C.byref(cfg), n, arr, C.byref(out)), "zs_build_tensors")
-    return Tensors(out.value, list(tensors))
+    return Tensors(out.value, keep)
 
 
 def zs_free_tensors(tensors: Tensors) -> None:
