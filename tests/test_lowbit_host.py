@@ -206,3 +206,20 @@ def test_list_keeps_its_tensors():
     del lst
     gc.collect()
     assert all(r() is None for r in alive)
+
+
+def test_tensors_of_another_device_are_refused():
+    """A CPU tensor's address never reaches a kernel: refused before the C call, with its name."""
+    import torch
+    x = torch.zeros(4, 32)
+    size = zs.zs_mx4_sizes(4, 32)
+    held = dict(codes=torch.zeros(size["code_bytes"], dtype=torch.uint8), scales=torch.zeros(size["scale_bytes"], dtype=torch.uint8))
+    for call in (lambda: zs.zs_mx4_quantize(x, rows=held), lambda: zs.zs_mx4_dequantize(held, x), lambda: zs.zs_mx4_matmul(held, held, 32, torch.zeros(4, 4))):
+        with pytest.raises(ValueError, match="got cpu"):
+            call()
+    t = dict(grad=torch.zeros(300), master=torch.zeros(300), exp_avg=torch.zeros(300), exp_avg_sq=torch.zeros(300))
+    lst = zs.zs_build_tensors([t], state_bits=32)                                    # host only
+    with pytest.raises(ValueError, match="got cpu"):
+        zs.zs_tensors_upload(lst, A16, 1 << 20)
+    with pytest.raises(ValueError, match="got cpu"):
+        zs.zs_tensors_upload(zs.zs_build_tensors([tensor()]), torch.zeros(1 << 12, dtype=torch.uint8), 1 << 12)

@@ -230,7 +230,7 @@ def _find_current_stream():
     """The address of torch's current stream; from its second call on, by the
     quickest way that this torch has (the public one takes about 4 us, as long
     as a small kernel)."""
-    global _current_stream
+    global _current_stream, _current_device
     try:
         import torch
         if not torch.cuda.is_available():
@@ -240,12 +240,25 @@ def _find_current_stream():
         device = getattr(torch._C, "_cuda_getDevice", None)
         if raw is not None and device is not None and raw(device()) == stream:
             _current_stream = lambda: raw(device())
+            if device() == torch.cuda.current_device():
+                _current_device = device
         return stream
     except Exception:  # torch without CUDA
         return None
 
 
+def _find_current_device() -> int:
+    """The index of torch's current device (-2: no CUDA); from the first stream
+    on by the quickest way, as above."""
+    try:
+        import torch
+        return torch.cuda.current_device() if torch.cuda.is_available() else -2
+    except Exception:  # torch without CUDA
+        return -2
+
+
 _current_stream = _find_current_stream
+_current_device = _find_current_device
 
 
 def _stream(s):
@@ -627,11 +640,31 @@ def _dtype(t) -> int:
     return got
 
 
+def _elsewhere(x, what: str, device: int) -> None:
+    """Refuse a torch tensor that is not on the current device, unless the
+    device reaches it all the same (pinned host memory) or nothing is in it."""
+    if x.numel() == 0 or x.get_device() < 0 and device >= 0 and x.is_pinned():
+        return
+    raise ValueError(f"{what}: a tensor on " + (f"cuda:{device}" if device >= 0 else "a GPU") + f" expected, got {x.device}")
+
+
+def _device_address(x, what: str, device: int):
+    """The address of a torch tensor on the device, or the address (or None) x."""
+    try:
+        at = x.data_ptr()
+    except AttributeError:
+        return None if x is None else int(x)
+    if x.get_device() != device:
+        _elsewhere(x, what, device)
+    return at
+
+
 class Tensors:
     """Owner of a zs_tensors* (freed with the object); keeps the torch tensors alive."""
 
     def __init__(self, handle: int, keep):
         self._h, self._keep, self._table = handle, keep, None
+        self._device = None              # of the torch tensors, once uploaded
 
     @property
     def handle(self):
@@ -669,7 +702,9 @@ def zs_build_tensors(tensors, state_bits: int = 32, grad_dtype=None, param_dtype
                 raise TypeError(f"tensor {i}: unknown {name}")
             if at == 0 or x is None:
                 continue
-            if not hasattr(x, "data_ptr"):
+            try:
+                row[at] = x.data_ptr()
+            except AttributeError:
                 row[at] = int(x)
                 continue
             need = blocks if at >= 6 else numel
@@ -683,7 +718,6 @@ def zs_build_tensors(tensors, state_bits: int = 32, grad_dtype=None, param_dtype
                     raise TypeError(f"tensor {i}: {name} is {x.dtype}, another type than before it")
             elif x.itemsize != size[name]:
                 raise TypeError(f"tensor {i}: {name} is {x.dtype}, {size[name]} bytes an element expected")
-            row[at] = x.data_ptr()
             keep.append(x)
         rows += row
     flat = (_i64 * max(len(rows), 1))(*[r - (1 << 64) if r >= 1 << 63 else r for r in rows])
@@ -709,6 +743,14 @@ def zs_tensors_info(tensors) -> dict:
 
 
 def zs_tensors_upload(tensors, d_table, nbytes: int, stream=None) -> None:
+    device = _current_device()
+    if not {x.get_device() for x in tensors._keep} <= {device}:
+        for x in tensors._keep:
+            if x.get_device() != device:
+                _elsewhere(x, "zs_tensors_upload", device)
+    _device_address(d_table, "zs_tensors_upload", device)
+    if tensors._keep:
+        tensors._device = device
     _check(_lib.zs_tensors_upload(tensors.handle, _ptr(d_table), int(nbytes), _stream(stream)),
            "zs_tensors_upload")
     tensors._table = d_table
@@ -720,10 +762,17 @@ _ROUNDING = {"nearest": ZS_ROUND_NEAREST, "stochastic": ZS_ROUND_STOCHASTIC}
 def zs_adam_tensors(tensors, hp, step: int, d_clip_coef=None, d_flags=None, rounding="nearest",
                     seed: int = 0, stream=None) -> None:
     h = _hp(hp)
-    _check(_lib.zs_adam_tensors(tensors.handle, C.byref(h), int(step),
-                                _ROUNDING[rounding] if isinstance(rounding, str) else int(rounding),
-                                int(seed) & 0xFFFFFFFFFFFFFFFF, _ptr(d_clip_coef), _ptr(d_flags),
-                                _stream(stream)), "zs_adam_tensors")
+    device = _current_device()
+    if tensors._device != device and tensors._device is not None:
+        raise ValueError(f"zs_adam_tensors: the list is of cuda:{tensors._device}, the current device is cuda:{device}")
+    st = _lib.zs_adam_tensors(tensors.handle, C.byref(h), int(step),
+                              _ROUNDING[rounding] if isinstance(rounding, str) else int(rounding),
+                              int(seed) & 0xFFFFFFFFFFFFFFFF,
+                              None if d_clip_coef is None else _device_address(d_clip_coef, "zs_adam_tensors", device),
+                              None if d_flags is None else _device_address(d_flags, "zs_adam_tensors", device),
+                              _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "zs_adam_tensors")
 
 
 def zs_mx4_sizes(rows: int, cols: int) -> dict:
@@ -732,23 +781,32 @@ def zs_mx4_sizes(rows: int, cols: int) -> dict:
     return dict(row_bytes=r.value, code_bytes=c.value, scale_bytes=s.value)
 
 
-def _mx4(held, rows: int, cols: int):
+def _mx4(held, rows: int, cols: int, device: int):
     """(codes, scales) addresses of a dict with "codes" and "scales" (uint8
-    tensors, or addresses), whose tensors are large enough for rows x cols."""
+    tensors on the device, or addresses), whose tensors are large enough for
+    rows x cols."""
     if held is None:
         return None, None
     codes, scales = held["codes"], held["scales"]
-    if not hasattr(codes, "data_ptr"):
-        return codes, scales
+    try:
+        at = codes.data_ptr(), scales.data_ptr()
+    except AttributeError:
+        return _device_address(codes, "codes", device), _device_address(scales, "scales", device)
     groups = (cols + 31) >> 5
-    for x, need in ((codes, 16 * rows * groups), (scales, ((rows + 127) >> 7) * ((groups + 7) >> 3) << 10)):
-        if x.numel() < need or x.itemsize != 1 or not x.is_contiguous():
-            raise ValueError(f"{need} contiguous bytes expected for {rows} x {cols}, got {tuple(x.shape)} of {x.dtype}")
-    return codes.data_ptr(), scales.data_ptr()
+    if (codes.nbytes < 16 * rows * groups or scales.nbytes < ((rows + 127) >> 7) * ((groups + 7) >> 3) << 10
+            or codes.itemsize != 1 or scales.itemsize != 1 or not codes.is_contiguous() or not scales.is_contiguous()):
+        raise ValueError(f"{16 * rows * groups} and {((rows + 127) >> 7) * ((groups + 7) >> 3) << 10} contiguous bytes expected for "
+                         f"{rows} x {cols}, got {tuple(codes.shape)} of {codes.dtype} and {tuple(scales.shape)} of {scales.dtype}")
+    if codes.get_device() != device or scales.get_device() != device:
+        for name, x in (("codes", codes), ("scales", scales)):
+            if x.get_device() != device:
+                _elsewhere(x, name, device)
+    return at
 
 
-def _matrix(x, what: str):
-    """(rows, cols, row stride) of a 2-D torch tensor whose rows are contiguous."""
+def _matrix(x, what: str, device: int):
+    """(rows, cols, row stride, dtype) of a 2-D torch tensor on the device whose
+    rows are contiguous."""
     shape = x.shape
     if len(shape) != 2:
         raise ValueError(f"{what}: a matrix expected, got {tuple(shape)}")
@@ -756,25 +814,30 @@ def _matrix(x, what: str):
     ld, one = x.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{what}: rows are not contiguous")
-    return rows, cols, ld if rows > 1 else cols
+    dtype = _dtype(x)
+    if x.get_device() != device:
+        _elsewhere(x, what, device)
+    return rows, cols, ld if rows > 1 else cols, dtype
 
 
 def zs_mx4_quantize(x, rows=None, cols=None, stream=None) -> None:
     """x: [r, c] torch matrix.  rows: the dict of x held along its rows
     ([r, c]); cols: of the transposed matrix ([c, r]); either may be None."""
-    r, c, ld = _matrix(x, "x")
-    rc, rs = _mx4(rows, r, c)
-    cc, cs = _mx4(cols, c, r)
-    st = _lib.zs_mx4_quantize(x.data_ptr(), r, c, ld, _dtype(x), rc, rs, cc, cs, _stream(stream))
+    device = _current_device()
+    r, c, ld, dtype = _matrix(x, "x", device)
+    rc, rs = _mx4(rows, r, c, device)
+    cc, cs = _mx4(cols, c, r, device)
+    st = _lib.zs_mx4_quantize(x.data_ptr(), r, c, ld, dtype, rc, rs, cc, cs, _current_stream() if stream is None else _stream(stream))
     if st:
         _check(st, "zs_mx4_quantize")
 
 
 def zs_mx4_dequantize(held, out, stream=None):
     """out: [r, c] torch matrix that receives the values; returned."""
-    r, c, ld = _matrix(out, "out")
-    hc, hs = _mx4(held, r, c)
-    st = _lib.zs_mx4_dequantize(hc, hs, r, c, out.data_ptr(), ld, _dtype(out), _stream(stream))
+    device = _current_device()
+    r, c, ld, dtype = _matrix(out, "out", device)
+    hc, hs = _mx4(held, r, c, device)
+    st = _lib.zs_mx4_dequantize(hc, hs, r, c, out.data_ptr(), ld, dtype, _current_stream() if stream is None else _stream(stream))
     if st:
         _check(st, "zs_mx4_dequantize")
     return out
@@ -782,10 +845,11 @@ def zs_mx4_dequantize(held, out, stream=None):
 
 def zs_mx4_matmul(a, b, k: int, out, stream=None):
     """out [m, n] = a [m, k] b [n, k]^T of two held matrices; out is returned."""
-    m, n, ld = _matrix(out, "out")
-    ac, as_ = _mx4(a, m, k)
-    bc, bs = _mx4(b, n, k)
-    st = _lib.zs_mx4_matmul(m, n, k, ac, as_, bc, bs, out.data_ptr(), ld, _dtype(out), _stream(stream))
+    device = _current_device()
+    m, n, ld, dtype = _matrix(out, "out", device)
+    ac, as_ = _mx4(a, m, k, device)
+    bc, bs = _mx4(b, n, k, device)
+    st = _lib.zs_mx4_matmul(m, n, k, ac, as_, bc, bs, out.data_ptr(), ld, dtype, _current_stream() if stream is None else _stream(stream))
     if st:
         _check(st, "zs_mx4_matmul")
     return out
