@@ -46,3 +46,35 @@ def test_lists():
         torch.cuda.synchronize()
         want = own["master"] if want is None else want
         assert torch.equal(own["master"], want) and not torch.equal(want, t["master"])
+
+
+def test_larger_buffers():
+    """More room than a matrix needs: flat, or more rows of the same width."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, w = torch.randn(40, 200, device="cuda", generator=g), torch.randn(50, 200, device="cuda", generator=g)
+    size = zs.zs_mx4_sizes(64, 200)
+    want = None
+    for shape in ((40 * size["row_bytes"],), (40, size["row_bytes"]), (64, size["row_bytes"]), (1 << 16,)):
+        a = dict(codes=torch.zeros(shape, dtype=torch.uint8, device="cuda"), scales=torch.zeros(1 << 13, dtype=torch.uint8, device="cuda"))
+        b = room(50, 200)
+        zs.zs_mx4_quantize(x, rows=a)
+        zs.zs_mx4_quantize(w, rows=b)
+        got = zs.zs_mx4_matmul(a, b, 200, torch.empty(40, 50, device="cuda"))
+        want = got if want is None else want
+        assert torch.equal(got, want) and bool(want.any())
+
+
+@pytest.mark.parametrize("k", [1, 32, 96, 480])
+def test_another_k_is_refused(k):
+    """A matrix held with 512 columns is not one of fewer: its rows are farther apart."""
+    def held(rows, cols):
+        size = zs.zs_mx4_sizes(rows, cols)
+        return dict(codes=torch.zeros(rows, size["row_bytes"], dtype=torch.uint8, device="cuda"),
+                    scales=torch.zeros(size["scale_bytes"], dtype=torch.uint8, device="cuda"))
+
+    out = torch.full((8, 16), 7.0, device="cuda")
+    for a, b in ((held(8, 512), held(16, 512)), (held(8, 512), held(16, k)), (held(8, k), held(16, 512))):
+        with pytest.raises(ValueError, match="bytes a row expected"):
+            zs.zs_mx4_matmul(a, b, k, out)
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all())

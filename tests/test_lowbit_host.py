@@ -223,3 +223,22 @@ def test_tensors_of_another_device_are_refused():
         zs.zs_tensors_upload(lst, A16, 1 << 20)
     with pytest.raises(ValueError, match="got cpu"):
         zs.zs_tensors_upload(zs.zs_build_tensors([tensor()]), torch.zeros(1 << 12, dtype=torch.uint8), 1 << 12)
+
+
+@pytest.mark.parametrize("k", [1, 32, 96, 480])
+def test_another_k_is_refused(k):
+    """A matrix held with 512 columns is not one of fewer: its rows are farther apart."""
+    import torch
+
+    def held(rows, cols):
+        size = zs.zs_mx4_sizes(rows, cols)
+        return dict(codes=torch.zeros(rows, size["row_bytes"], dtype=torch.uint8), scales=torch.zeros(size["scale_bytes"], dtype=torch.uint8))
+
+    out = torch.empty(8, 16)
+    for a, b in ((held(8, 512), held(16, 512)), (held(8, 512), held(16, k))):
+        with pytest.raises(ValueError, match="bytes a row expected"):
+            zs.zs_mx4_matmul(a, b, k, out)
+    for call in (lambda: zs.zs_mx4_dequantize(held(8, 512), torch.empty(8, k)), lambda: zs.zs_mx4_quantize(torch.empty(8, k), rows=held(8, 512)),
+                 lambda: zs.zs_mx4_quantize(torch.empty(k, 8), cols=held(8, 512))):
+        with pytest.raises(ValueError, match="bytes a row expected"):
+            call()

@@ -784,7 +784,8 @@ def zs_mx4_sizes(rows: int, cols: int) -> dict:
 def _mx4(held, rows: int, cols: int, device: int):
     """(codes, scales) addresses of a dict with "codes" and "scales" (uint8
     tensors on the device, or addresses), whose tensors are large enough for
-    rows x cols."""
+    rows x cols.  Codes are flat, or a row of the matrix a row: the kernels
+    take the distance of rows from cols, so another one is another matrix."""
     if held is None:
         return None, None
     codes, scales = held["codes"], held["scales"]
@@ -797,6 +798,8 @@ def _mx4(held, rows: int, cols: int, device: int):
             or codes.itemsize != 1 or scales.itemsize != 1 or not codes.is_contiguous() or not scales.is_contiguous()):
         raise ValueError(f"{16 * rows * groups} and {((rows + 127) >> 7) * ((groups + 7) >> 3) << 10} contiguous bytes expected for "
                          f"{rows} x {cols}, got {tuple(codes.shape)} of {codes.dtype} and {tuple(scales.shape)} of {scales.dtype}")
+    if codes.nbytes != 16 * rows * groups and codes.dim() > 1 and codes.shape[-1] != 16 * groups:
+        raise ValueError(f"codes are {tuple(codes.shape)}: {16 * groups} bytes a row expected for {cols} columns")
     if codes.get_device() != device or scales.get_device() != device:
         for name, x in (("codes", codes), ("scales", scales)):
             if x.get_device() != device:
@@ -804,9 +807,9 @@ def _mx4(held, rows: int, cols: int, device: int):
     return at
 
 
-def _matrix(x, what: str, device: int):
-    """(rows, cols, row stride, dtype) of a 2-D torch tensor on the device whose
-    rows are contiguous."""
+def _matrix(x, what: str):
+    """(rows, cols, row stride, dtype) of a 2-D torch tensor whose rows are
+    contiguous."""
     shape = x.shape
     if len(shape) != 2:
         raise ValueError(f"{what}: a matrix expected, got {tuple(shape)}")
@@ -814,19 +817,18 @@ def _matrix(x, what: str, device: int):
     ld, one = x.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{what}: rows are not contiguous")
-    dtype = _dtype(x)
-    if x.get_device() != device:
-        _elsewhere(x, what, device)
-    return rows, cols, ld if rows > 1 else cols, dtype
+    return rows, cols, ld if rows > 1 else cols, _dtype(x)
 
 
 def zs_mx4_quantize(x, rows=None, cols=None, stream=None) -> None:
     """x: [r, c] torch matrix.  rows: the dict of x held along its rows
     ([r, c]); cols: of the transposed matrix ([c, r]); either may be None."""
     device = _current_device()
-    r, c, ld, dtype = _matrix(x, "x", device)
+    r, c, ld, dtype = _matrix(x, "x")
     rc, rs = _mx4(rows, r, c, device)
     cc, cs = _mx4(cols, c, r, device)
+    if x.get_device() != device:
+        _elsewhere(x, "x", device)
     st = _lib.zs_mx4_quantize(x.data_ptr(), r, c, ld, dtype, rc, rs, cc, cs, _current_stream() if stream is None else _stream(stream))
     if st:
         _check(st, "zs_mx4_quantize")
@@ -835,8 +837,10 @@ def zs_mx4_quantize(x, rows=None, cols=None, stream=None) -> None:
 def zs_mx4_dequantize(held, out, stream=None):
     """out: [r, c] torch matrix that receives the values; returned."""
     device = _current_device()
-    r, c, ld, dtype = _matrix(out, "out", device)
+    r, c, ld, dtype = _matrix(out, "out")
     hc, hs = _mx4(held, r, c, device)
+    if out.get_device() != device:
+        _elsewhere(out, "out", device)
     st = _lib.zs_mx4_dequantize(hc, hs, r, c, out.data_ptr(), ld, dtype, _current_stream() if stream is None else _stream(stream))
     if st:
         _check(st, "zs_mx4_dequantize")
@@ -846,9 +850,11 @@ def zs_mx4_dequantize(held, out, stream=None):
 def zs_mx4_matmul(a, b, k: int, out, stream=None):
     """out [m, n] = a [m, k] b [n, k]^T of two held matrices; out is returned."""
     device = _current_device()
-    m, n, ld, dtype = _matrix(out, "out", device)
+    m, n, ld, dtype = _matrix(out, "out")
     ac, as_ = _mx4(a, m, k, device)
     bc, bs = _mx4(b, n, k, device)
+    if out.get_device() != device:
+        _elsewhere(out, "out", device)
     st = _lib.zs_mx4_matmul(m, n, k, ac, as_, bc, bs, out.data_ptr(), ld, dtype, _current_stream() if stream is None else _stream(stream))
     if st:
         _check(st, "zs_mx4_matmul")
