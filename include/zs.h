@@ -463,6 +463,11 @@ zs_status zs_test_late_copy(void *dst, const void *src, int64_t bytes, int64_t d
  * usable.  -1: none (the state at first).  Errors: ZS_EINVAL. */
 zs_status zs_test_give_up(int32_t at);
 
+/* Test of the root that zs_adam_tensors takes for 8-bit moments: *d_count
+ * (device memory) becomes the number of floats v in [0, 2^64) for which it is
+ * not the correctly rounded one (0).  Errors: ZS_EINVAL, ZS_ECUDA. */
+zs_status zs_test_root(int64_t *d_count, void *stream);
+
 /* What a CTA of the kernel asks of its SM that zs_mx4_matmul launches for a
  * product of these sizes (for tests; host only). */
 typedef struct {

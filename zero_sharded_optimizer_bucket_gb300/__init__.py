@@ -207,6 +207,7 @@ _sig("zs_mx4_sizes", _i32, [_i64, _i64, C.POINTER(_i64), C.POINTER(_i64), C.POIN
 _sig("zs_mx4_quantize", _i32, [_P, _i64, _i64, _i64, _i32, _P, _P, _P, _P, _P])
 _sig("zs_mx4_dequantize", _i32, [_P, _P, _i64, _i64, _P, _i64, _i32, _P])
 _sig("zs_test_late_copy", _i32, [_P, _P, _i64, _i64, _P])
+_sig("zs_test_root", _i32, [_P, _P])
 _sig("zs_test_give_up", _i32, [_i32])
 _sig("zs_test_mx4_launch", _i32, [_i64, _i64, _i64, C.POINTER(zs_mx4_launch)])
 _sig("zs_mx4_matmul", _i32, [_i64, _i64, _i64, _P, _P, _P, _P, _P, _i64, _i32, _P])
@@ -864,6 +865,11 @@ def zs_mx4_matmul(a, b, k: int, out, stream=None):
 def zs_test_late_copy(dst, src, nbytes: int, delay_ns: int, stream=None) -> None:
     """A kernel that lets the next one begin, and copies src to dst delay_ns later (test hook)."""
     _check(_lib.zs_test_late_copy(_ptr(dst), _ptr(src), int(nbytes), int(delay_ns), _stream(stream)), "zs_test_late_copy")
+
+
+def zs_test_root(d_count, stream=None) -> None:
+    """Counts the floats whose root the 8-bit update would not round correctly (test)."""
+    _check(_lib.zs_test_root(_ptr(d_count), _stream(stream)), "zs_test_root")
 
 
 def zs_test_give_up(at: int = -1) -> None:

@@ -299,9 +299,9 @@ __device__ __forceinline__ f2 sub2(f2 a, f2 b, const Adam8C &c) { return fma2(b,
 // lane's roots overlap.  Markstein's correction of an approximate root s of
 // w = 2^64 v: the residual w - s s is exact in one fused operation, and
 // s + (w - s s) / (2 sqrt(w)) rounds as the root does.  2^64 keeps the
-// residual of the smallest v among the normal numbers; checked against the
-// library's root on every positive v below 2^64.  Infinities and NaN give NaN,
-// and so does v >= 2^64.
+// residual of the smallest v among the normal numbers; zs_test_root compares
+// it with the library's root on every v below 2^64.  Infinities and NaN give
+// NaN, and so does v >= 2^64.
 __device__ __forceinline__ f2 root_2_32(f2 v) {
     const f2 w = mul2(v, both(18446744073709551616.0f)), minus_w = mul2(v, both(-18446744073709551616.0f));
     float a, b;
@@ -310,6 +310,19 @@ __device__ __forceinline__ f2 root_2_32(f2 v) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(fmaxf(b, 7.8886090522101181e-31f)));
     const f2 y = f2pack(a, b), s = mul2(w, y);
     return fma2(fma2(s, s, minus_w), mul2(both(-0.5f), y), s);
+}
+
+constexpr uint32_t ROOT_END = 0x5F800000u;       // 2^64
+__global__ void root_test_kernel(unsigned long long *bad) {
+    unsigned long long mine = 0;
+    for (uint32_t u = 2 * (blockIdx.x * blockDim.x + threadIdx.x); u < ROOT_END; u += 2 * gridDim.x * blockDim.x) {
+        const float a = __uint_as_float(u), b = __uint_as_float(u + 1);
+        float x, y;
+        f2unpack(root_2_32(f2pack(a, b)), x, y);
+        mine += (__float_as_uint(x) != __float_as_uint(__fmul_rn(__fsqrt_rn(a), 4294967296.0f))) +
+                (__float_as_uint(y) != __float_as_uint(__fmul_rn(__fsqrt_rn(b), 4294967296.0f)));
+    }
+    if (mine) atomicAdd(bad, mine);
 }
 
 // a / b to 2 units in the last place, b normal or 0 (a root times at least 1,
@@ -669,6 +682,19 @@ zs_status zs_tensors_upload(zs_tensors *L, void *d_table, int64_t bytes, void *s
             return zs_fail(ZS_ECUDA, "%s: cudaMemcpyAsync: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
         L->d_chunks = static_cast<const ZsChunk *>(d_table);
     }
+    zs_clear_error();
+    return ZS_OK;
+}
+
+zs_status zs_test_root(int64_t *d_count, void *stream) {
+    if (!d_count || addr(d_count) % 8) return zs_fail(ZS_EINVAL, "zs_test_root: count NULL or misaligned");
+    const cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = cudaMemsetAsync(d_count, 0, 8, s);
+    if (e == cudaSuccess) {
+        zsk::root_test_kernel<<<1216, zsk::THREADS, 0, s>>>(reinterpret_cast<unsigned long long *>(d_count));
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return zs_fail(ZS_ECUDA, "zs_test_root: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
     zs_clear_error();
     return ZS_OK;
 }
