@@ -432,10 +432,11 @@ zs_status zs_all_gather_coalesced(const zs_plan *plan, int32_t n, const int32_t 
  * per chunk; a wait that does not complete within a bound (about a second)
  * is abandoned, the gather's output is then incomplete, and this counter
  * goes up.  zs_adam_tensors with 8-bit moments, zs_mx4_quantize and
- * zs_mx4_matmul bound and count their waits the same way.  Synchronous (reads device memory).  reset != 0 sets it back to
- * 0.  Returns ZS_ETIMEOUT, with *count filled, when the count is not 0.
- * Has no counterpart in the pages: it is this library's report of its own
- * bounded waits.  Errors: ZS_EINVAL (NULL count), ZS_ECUDA. */
+ * zs_mx4_matmul bound and count their waits the same way.  Synchronous
+ * (reads device memory).  reset != 0 sets it back to 0.  Returns
+ * ZS_ETIMEOUT, with *count filled, when the count is not 0.  Has no
+ * counterpart in the pages: it is this library's report of its own bounded
+ * waits.  Errors: ZS_EINVAL (NULL count), ZS_ECUDA. */
 zs_status zs_device_wait_timeouts(int32_t *count, int32_t reset);
 
 /* Test hook for the timeout path: enqueues one thread that waits, with the
@@ -747,6 +748,8 @@ zs_status zs_tensors_upload(zs_tensors *list, void *d_table, int64_t bytes, void
  *   A positive r never gets code 0, which would divide an update by eps.
  *   An element whose m or r is not finite gets a NaN code and does not count
  *   for the scale.
+ * A captured call keeps step, seed and the hyper-parameters: a replay repeats
+ * the update of that step, with its bias corrections and its random bits.
  * step >= 1.  Errors: ZS_EINVAL, ZS_ESTATE (not uploaded), ZS_ECUDA; a
  * device wait that gave up is counted by zs_device_wait_timeouts, and leaves
  * the blocks that it held up as they were. */
@@ -787,8 +790,13 @@ zs_status zs_mx4_quantize(const void *x, int64_t rows, int64_t cols, int64_t ld,
 zs_status zs_mx4_dequantize(const void *codes, const void *scales, int64_t rows, int64_t cols,
                             void *out, int64_t ldo, int32_t dtype, void *stream);
 
-/* out[m][n] = sum over k of a[m][k] * b[n][k] (dtype, row stride ldo),
- * products and sums in fp32, rounded once.  For a linear layer y = x w^T:
+/* out[m][n] = sum over k of a[m][k] * b[n][k] (dtype, row stride ldo).  The
+ * product of two codes and their scales is exact.  The tensor cores add 64 of
+ * them at a time to an fp32 accumulator, each time off by at most 2^-22 of the
+ * sum of the magnitudes (they may cut off instead of rounding); up to 8 parts
+ * of k are added in fp32, in their order.  So before its one rounding to
+ * dtype, out is within (ceil(k / 64) + 8) 2^-22 sum |a b| of the sum, and a
+ * call gives the same bits every time.  For a linear layer y = x w^T:
  *   y  = matmul(x along rows,  w along rows)     k = inputs
  *   dx = matmul(dy along rows, w along cols)     k = outputs
  *   dw = matmul(dy along cols, x along cols)     k = tokens

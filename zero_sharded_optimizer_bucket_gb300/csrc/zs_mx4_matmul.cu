@@ -10,13 +10,13 @@
 //
 // Two kernels, by the work there is:
 //  - products that give every pair of SMs about a 256 x 256 tile or more:
-//    mx4_matmul_pair_kernel.  8192 x 14336 x 4096 bf16: 143 us, 6.7 PFLOP/s in
+//    mx4_matmul_pair_kernel.  8192 x 14336 x 4096 bf16: 139 us, 6.9 PFLOP/s in
 //    short runs, 156 us, 6.2 PFLOP/s in long ones, which run at the board's
 //    power limit; 8192 x 8192 x 8192 147 us, 7.5 PFLOP/s, and 163 us.
 //  - smaller ones: mx4_matmul_kernel, tiles of 128 rows, k shared out over a
-//    cluster when the tiles are few.  One token through 4096 x 14336: 8.1 us
-//    from HBM, 3.8 TB/s of weight bytes, 6.2 from L2; 16 through 14336 x 4096:
-//    7.4 and 5.3 us; 256 x 4096 x 4096 from L2: 8.4 us.  What is left there is
+//    cluster when the tiles are few.  One token through 4096 x 14336: 8.0 us
+//    from HBM, 3.9 TB/s of weight bytes, 6.0 from L2; 16 through 14336 x 4096:
+//    7.3 and 5.1 us; 256 x 4096 x 4096 from L2: 8.3 us.  What is left there is
 //    the latency of a chain of few stages and the 2.1 us of a launch that
 //    computes nothing.
 #include <atomic>
@@ -413,9 +413,11 @@ mx4_matmul_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_consta
 // the tile boundary, while 8 warps of each CTA empty the accumulator of the
 // previous tile into registers, release it, and store.  (Two accumulators of
 // 256 columns would leave no tensor memory for the scales.)
-// A stage takes the tensor cores 512 cycles and brings 35 KB to each SM.  With 5
-// in flight 8192 x 8192 x 8192 took 630 cycles a stage all in all, with 4 650,
-// with 3 760: the way from a product's end over its barrier and the loads to the
+// A stage takes the tensor cores 512 cycles (four instructions of K = 64; the
+// PTX ISA lists K = 96 for sm_103a too, whose 48-byte steps would cross the
+// 128-byte rows of a stage: not tried) and brings 35 KB to each SM.  With 6
+// in flight 8192 x 8192 x 8192 takes 620 cycles a stage all in all, with 5 630,
+// with 4 650, with 3 760: the way from a product's end over its barrier and the loads to the
 // next product is what remains, besides 400 cycles a tile between its last
 // product and the next one's first.  (Loads beside the products do not slow
 // them, and the same loads from a few hot lines gained 4 %.)  Then power: the

@@ -428,9 +428,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 // a 16-bit copy: at the copy bandwidth that leaves about 85 instructions an
 // element, so the arithmetic counts as much as the bytes, and the copies keep
 // memory busy while every warp of the SM computes (loads into registers took
-// 623 us and more for 202M elements).  Rounded to nearest 467 us, 7.0 TB/s;
-// stochastically 497 us, 6.5 TB/s: there instructions bound it, 74 an element,
-// 26 of them the random bits and their rounding (529 us with 81, before the
+// 623 us and more for 202M elements).  Rounded to nearest 465 us, 7.0 TB/s;
+// stochastically 491 us, 6.6 TB/s: there instructions bound it, 73 an element,
+// 24 of them the random bits and their rounding (529 us with 81, before the
 // estimates of the reciprocal and the root went without scaling; 3 or 5 CTAs an
 // SM 520 us and more).  The quotient m / den is
 // the quick one (its last two bits may be off: 2^-22 of one update, far below
