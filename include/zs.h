@@ -757,6 +757,31 @@ zs_status zs_adam_tensors(const zs_tensors *list, const zs_adam_hparams *hp, int
                           int32_t rounding, uint64_t seed, const float *d_clip_coef,
                           const int32_t *d_flags, void *stream);
 
+/* The global gradient norm of a list, as zs_grad_norm's over a plan: norm =
+ * sqrt(sum of squares of every gradient) / S, coef = min(1, max_norm / (norm +
+ * 1e-6)) / S (clip 1 when max_norm <= 0), where S is the loss scale of scaler
+ * (NULL: 1, and nothing is updated); a norm that is not finite sets
+ * ZS_SKIP_NONFINITE and reports coef 1.  The scaler is then updated as
+ * zs_unscale_and_clip does.  d_norm, d_clip_coef and d_flags are what
+ * zs_adam_tensors takes.  Squares are added with the error of each addition
+ * carried along (float32 pairs, float64 where magnitudes leave [2^-40, 2^56)
+ * and above a thread), so that before its one rounding to float32 the root is
+ * good to about 2^-32; a call gives the same bits every time.
+ * scratch: device memory of the caller, at least n_chunks doubles
+ * (zs_tensors_info), which a call overwrites: calls that overlap on the GPU,
+ * captured ones among them, need one each.  Reads the gradients once.  Errors:
+ * ZS_EINVAL, ZS_ESTATE (not uploaded), ZS_ECUDA. */
+zs_status zs_norm_tensors(const zs_tensors *list, double *scratch, float max_norm,
+                          const zs_loss_scaler *scaler, float *d_norm, float *d_clip_coef,
+                          int32_t *d_flags, void *stream);
+
+/* Clipping in place, for an update that takes no coefficient: every gradient
+ * of the list becomes rne(float(grad) * *d_clip_coef).  With ZS_SKIP_NONFINITE
+ * in d_flags (NULL: never), or a coefficient of 1, nothing is written.  The
+ * gradients have to be writable.  Errors: as zs_norm_tensors. */
+zs_status zs_clip_tensors(const zs_tensors *list, const float *d_clip_coef, const int32_t *d_flags,
+                          void *stream);
+
 /* Microscaled 4-bit matrices.  A matrix [rows][cols] is held as e2m1 codes
  * (0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives), two a byte, the element
  * of even column in the low half, rows of 16 * ceil(cols / 32) bytes; and

@@ -203,6 +203,8 @@ _sig("zs_free_tensors", None, [_P])
 _sig("zs_tensors_info", _i32, [_P, C.POINTER(zs_tensors_info_t)])
 _sig("zs_tensors_upload", _i32, [_P, _P, _i64, _P])
 _sig("zs_adam_tensors", _i32, [_P, C.POINTER(zs_adam_hparams), _i64, _i32, C.c_uint64, _P, _P, _P])
+_sig("zs_norm_tensors", _i32, [_P, _P, _f32, C.POINTER(zs_loss_scaler), _P, _P, _P, _P])
+_sig("zs_clip_tensors", _i32, [_P, _P, _P, _P])
 _sig("zs_mx4_sizes", _i32, [_i64, _i64, C.POINTER(_i64), C.POINTER(_i64), C.POINTER(_i64)])
 _sig("zs_mx4_quantize", _i32, [_P, _i64, _i64, _i64, _i32, _P, _P, _P, _P, _P])
 _sig("zs_mx4_dequantize", _i32, [_P, _P, _i64, _i64, _P, _i64, _i32, _P])
@@ -666,10 +668,17 @@ class Tensors:
     def __init__(self, handle: int, keep):
         self._h, self._keep, self._table = handle, keep, None
         self._device = None              # of the torch tensors, once uploaded
+        self._n_chunks = None
 
     @property
     def handle(self):
         return self._h
+
+    @property
+    def n_chunks(self) -> int:
+        if self._n_chunks is None:
+            self._n_chunks = zs_tensors_info(self)["n_chunks"]
+        return self._n_chunks
 
     def __del__(self):
         if getattr(self, "_h", None):
@@ -774,6 +783,49 @@ def zs_adam_tensors(tensors, hp, step: int, d_clip_coef=None, d_flags=None, roun
                               _current_stream() if stream is None else _stream(stream))
     if st:
         _check(st, "zs_adam_tensors")
+
+
+def _on_list(tensors, fn: str) -> int:
+    """The current device, which has to be the list's."""
+    device = _current_device()
+    if tensors._device != device and tensors._device is not None:
+        raise ValueError(f"{fn}: the list is of cuda:{tensors._device}, the current device is cuda:{device}")
+    return device
+
+
+def _scalar(x, what: str, device: int, itemsize: int = 4):
+    """The address of a device scalar (an address, or None, as it is)."""
+    if x is None:
+        return None
+    at = _device_address(x, what, device)
+    if hasattr(x, "data_ptr") and (x.numel() < 1 or x.itemsize != itemsize):
+        raise TypeError(f"{what}: a scalar of {itemsize} bytes expected, got {tuple(x.shape)} of {x.dtype}")
+    return at
+
+
+def zs_norm_tensors(tensors, scratch, max_norm: float, d_norm, d_clip_coef, d_flags, scaler=None,
+                    stream=None) -> None:
+    """scratch: at least zs_tensors_info's n_chunks float64 (tensor or address);
+    scaler: of make_loss_scaler, or None."""
+    device = _on_list(tensors, "zs_norm_tensors")
+    d_scratch = _device_address(scratch, "scratch", device)
+    if hasattr(scratch, "data_ptr"):
+        need = 8 * tensors.n_chunks
+        if scratch.nbytes < need or not scratch.is_contiguous():
+            raise ValueError(f"scratch: {need} contiguous bytes expected, got {tuple(scratch.shape)} of {scratch.dtype}")
+    st = _lib.zs_norm_tensors(tensors.handle, d_scratch, max_norm, None if scaler is None else C.byref(scaler),
+                              _scalar(d_norm, "d_norm", device), _scalar(d_clip_coef, "d_clip_coef", device),
+                              _scalar(d_flags, "d_flags", device), _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "zs_norm_tensors")
+
+
+def zs_clip_tensors(tensors, d_clip_coef, d_flags=None, stream=None) -> None:
+    device = _on_list(tensors, "zs_clip_tensors")
+    st = _lib.zs_clip_tensors(tensors.handle, _scalar(d_clip_coef, "d_clip_coef", device), _scalar(d_flags, "d_flags", device),
+                              _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "zs_clip_tensors")
 
 
 def zs_mx4_sizes(rows: int, cols: int) -> dict:

@@ -272,6 +272,24 @@ zs_status zs_gather_impl(const zs_plan *P, int32_t n, const int32_t *params,
     return ZS_OK;
 }
 
+zs_status zs_scale_args(const zs_loss_scaler *scaler, ZsScaleArgs *out, const char *fn) {
+    if (!scaler || !al(scaler->d_scale, 4))
+        return zs_fail(ZS_EINVAL, "%s: scaler or its d_scale NULL / misaligned", fn);
+    if (scaler->reserved != 0) return zs_fail(ZS_EINVAL, "%s: scaler reserved field must be 0", fn);
+    if (scaler->scale_window > 0) {
+        if (!al(scaler->d_good_steps, 4))
+            return zs_fail(ZS_EINVAL, "%s: d_good_steps NULL or misaligned", fn);
+        if (!(scaler->scale_factor > 1.0f) || !(scaler->min_scale > 0.0f))
+            return zs_fail(ZS_EINVAL, "%s: need scale_factor > 1 and min_scale > 0", fn);
+    }
+    out->d_scale = scaler->d_scale;
+    out->d_good = scaler->scale_window > 0 ? scaler->d_good_steps : nullptr;
+    out->factor = scaler->scale_factor;
+    out->min_scale = scaler->min_scale;
+    out->window = scaler->scale_window;
+    return ZS_OK;
+}
+
 extern "C" {
 
 zs_status zs_device_wait_timeouts(int32_t *count, int32_t reset) {
@@ -313,15 +331,8 @@ zs_status zs_unscale_and_clip(const zs_plan *P, const void *grad_shards, const v
     const char *fn = "zs_unscale_and_clip";
     zs_status r = need_table(P, fn);
     if (r) return r;
-    if (!scaler || !al(scaler->d_scale, 4))
-        return zs_fail(ZS_EINVAL, "%s: scaler or its d_scale NULL / misaligned", fn);
-    if (scaler->reserved != 0) return zs_fail(ZS_EINVAL, "%s: scaler reserved field must be 0", fn);
-    if (scaler->scale_window > 0) {
-        if (!al(scaler->d_good_steps, 4))
-            return zs_fail(ZS_EINVAL, "%s: d_good_steps NULL or misaligned", fn);
-        if (!(scaler->scale_factor > 1.0f) || !(scaler->min_scale > 0.0f))
-            return zs_fail(ZS_EINVAL, "%s: need scale_factor > 1 and min_scale > 0", fn);
-    }
+    ZsScaleArgs sc;
+    if ((r = zs_scale_args(scaler, &sc, fn))) return r;
     if ((r = check_scratch(P, norm_scratch, fn))) return r;
     if ((r = check_scalars(d_norm, d_clip_coef, d_flags, fn))) return r;
     if (recompute) {
@@ -330,12 +341,6 @@ zs_status zs_unscale_and_clip(const zs_plan *P, const void *grad_shards, const v
         if (P->Pn_alloc > 0 && !al(persist_grads, 16))
             return zs_fail(ZS_EINVAL, "%s: persist_grads NULL or not 16-byte aligned", fn);
     }
-    ZsScaleArgs sc;
-    sc.d_scale = scaler->d_scale;
-    sc.d_good = scaler->scale_window > 0 ? scaler->d_good_steps : nullptr;
-    sc.factor = scaler->scale_factor;
-    sc.min_scale = scaler->min_scale;
-    sc.window = scaler->scale_window;
     return cuda_status(zsl_norm(P->d_tiles, (int64_t)P->tiles.size(), P->n_level1, P->cfg.dtype,
                                 static_cast<const uint16_t *>(grad_shards),
                                 static_cast<const uint16_t *>(persist_grads), norm_scratch,

@@ -24,6 +24,9 @@ struct ZsScaleArgs {
     int32_t window;
 };
 
+// Those of a loss scaler, checked (ZS_EINVAL in the name of fn).
+zs_status zs_scale_args(const zs_loss_scaler *scaler, ZsScaleArgs *out, const char *fn);
+
 // One bucket: launch positions [tile0, tile0 + ntiles); position i works on
 // tile d_order[i] (the plan's per-bucket largest-first permutation).
 cudaError_t zsl_reduce_scatter(const ZsTile *d_tiles, const int32_t *d_order, int64_t tile0,

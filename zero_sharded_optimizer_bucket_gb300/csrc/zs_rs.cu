@@ -15,6 +15,7 @@
 
 #include "zs_device.cuh"
 #include "zs_launch.h"
+#include "zs_norm.cuh"
 
 namespace zsk {
 
@@ -419,9 +420,7 @@ norm_level1_kernel(const double *__restrict__ partials, int64_t n, double *__res
     if (threadIdx.x == 0) level1[blockIdx.x] = s;
 }
 
-// Finish: total, norm = float(sqrt(total)) / S, clip coefficient / S,
-// flags; then the loss-scale update when a scaler is given.  S = 1 without
-// one, which leaves every result bit-identical to the unscaled formula.
+// Finish: the total of the first level, and what norm_finish makes of it.
 __global__ void __launch_bounds__(THREADS)
 norm_finish_kernel(const double *__restrict__ level1, int64_t n1, float max_norm,
                    float *__restrict__ d_norm, float *__restrict__ d_coef,
@@ -430,38 +429,7 @@ norm_finish_kernel(const double *__restrict__ level1, int64_t n1, float max_norm
     double v = 0.0;
     for (int64_t i = threadIdx.x; i < n1; i += THREADS) v = __dadd_rn(v, level1[i]);
     const double s = block_sum(v, red);
-    if (threadIdx.x == 0) {
-        const float S = sc.d_scale ? *sc.d_scale : 1.0f;
-        const float norm = __fdiv_rn((float)sqrt(s), S);
-        const bool finite = isfinite(norm);
-        float coef = 1.0f;
-        if (finite) {
-            float clip = 1.0f;
-            if (max_norm > 0.0f) {
-                const float c = __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f));
-                clip = c < 1.0f ? c : 1.0f;
-            }
-            coef = __fdiv_rn(clip, S);
-        }
-        *d_norm = norm;
-        *d_coef = coef;
-        *d_flags = finite ? 0 : ZS_SKIP_NONFINITE;
-        if (sc.d_scale && sc.window > 0) {
-            if (!finite) {
-                const float d = __fdiv_rn(S, sc.factor);
-                *sc.d_scale = d > sc.min_scale ? d : sc.min_scale;
-                *sc.d_good = 0;
-            } else {
-                const int32_t g = *sc.d_good + 1;
-                if (g >= sc.window) {
-                    *sc.d_scale = __fmul_rn(S, sc.factor);
-                    *sc.d_good = 0;
-                } else {
-                    *sc.d_good = g;
-                }
-            }
-        }
-    }
+    if (threadIdx.x == 0) norm_finish(s, max_norm, d_norm, d_coef, d_flags, sc);
 }
 
 }  // namespace zsk
