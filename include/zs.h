@@ -832,6 +832,54 @@ zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *a_codes, co
                         const void *b_codes, const void *b_scales, void *out, int64_t ldo,
                         int32_t dtype, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm in front of a linear layer.  A matrix is [rows][cols]
+ * of one dtype, rows contiguous, with a row stride of its own (in elements, >=
+ * cols); weight has a type of its own.  In fp32, in this order:
+ *   h = x + residual (x alone when residual is NULL);  sum = rne(h)
+ *   rstd = 1 / sqrt(mean over the row of h h + eps)
+ *   y = (h * rstd) * weight, rounded to dtype
+ * sum (the new residual stream) belongs to a residual and only to one; it may
+ * be x's or residual's own memory with the same stride.  out: y, or NULL.
+ * r_codes, r_scales and c_codes, c_scales: y held in 4 bits along its rows and
+ * its columns, bit for bit what zs_mx4_quantize makes of y (either pair may be
+ * NULL; of the three results one at least is asked for).  Past 12288 columns
+ * the form along the columns needs out.  rstd [rows] is what the backward
+ * pass reads.  The sum of squares is made to 2^-40 of itself (squares below
+ * 2^-126 are lost), and rstd is the fp32 number nearest to its formula's value
+ * unless that lies within 2^-40 of the middle of two.  A row with an infinity
+ * or NaN gives what the formula gives.  eps >= 0: of a row of zeros with eps 0
+ * the result is NaN.  No rows or no columns: nothing is written.  Errors:
+ * ZS_EINVAL, ZS_ECUDA. */
+zs_status zs_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                      const void *weight, int32_t weight_dtype, int64_t rows, int64_t cols,
+                      int32_t dtype, float eps, void *sum, int64_t lds, void *out, int64_t ldo,
+                      float *rstd, void *r_codes, void *r_scales, void *c_codes, void *c_scales,
+                      void *stream);
+
+/* Bytes of device memory that the backward pass needs as scratch. */
+zs_status zs_rms_norm_scratch(int64_t rows, int64_t cols, int64_t *bytes);
+
+/* Its backward pass.  x: what was normalised (sum, where there was a
+ * residual), rstd as it came back, dy the gradient of y, residual (or NULL)
+ * the gradient that reaches the residual stream on its other way.  In fp32:
+ *   g = dy * weight;  c = rstd^2 * mean over the row of g x
+ *   dx = rne((g - x c) * rstd + residual)   (of x and of the residual alike)
+ *   dw = sum over the rows of dy * (x * rstd), added in fp32 in an order that
+ *        the sizes alone set, rounded once to dw_dtype
+ * with the mean made to 2^-40 of the mean of the magnitudes.  dx may be dy's or
+ * residual's own memory with the same stride.  r_codes .. c_scales: dx held in
+ * 4 bits, as the products of the layer below read it, as zs_mx4_quantize makes
+ * of dx.  dw [cols] may be NULL; otherwise scratch (16-byte aligned,
+ * zs_rms_norm_scratch bytes) is overwritten: calls that overlap on the GPU need
+ * one each.  No rows: dw is 0.  Errors: ZS_EINVAL, ZS_ECUDA. */
+zs_status zs_rms_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                               const void *weight, int32_t weight_dtype, const float *rstd,
+                               const void *residual, int64_t ldr, int64_t rows, int64_t cols,
+                               int32_t dtype, void *dx, int64_t lddx, void *dw, int32_t dw_dtype,
+                               float *scratch, void *r_codes, void *r_scales, void *c_codes,
+                               void *c_scales, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

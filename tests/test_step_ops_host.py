@@ -23,3 +23,35 @@ def test_norm_and_clip_refusals():
     with pytest.raises(zs.ZsError):
         zs._check(zs._lib.zs_clip_tensors(None, a, None, None), "zs_clip_tensors")
     zs.zs_clip_tensors(zs.zs_build_tensors([]), a)      # nothing to do, no launch
+
+
+def call(name, *a):
+    got = getattr(zs._lib, name)(*a)
+    assert got == zs.ZS_EINVAL, (name, a, got)
+    assert zs.zs_last_error() != ""
+
+
+def test_rms_norm_refusals():
+    a = A16
+    good = dict(x=a, ldx=64, residual=a, ldr=64, weight=a, weight_dtype=0, rows=4, cols=64, dtype=0, eps=1e-5, sum=a, lds=64, out=a, ldo=64,
+                rstd=a, r_codes=a, r_scales=a, c_codes=a, c_scales=a, stream=None)
+    for bad in (dict(x=None), dict(x=a + 1), dict(ldx=63), dict(ldr=63), dict(lds=63), dict(ldo=63), dict(sum=None), dict(residual=None), dict(weight=None),
+                dict(weight=a + 1), dict(weight_dtype=3), dict(dtype=-1), dict(dtype=3), dict(rows=-1), dict(cols=1 << 31), dict(eps=-1.0),
+                dict(eps=float("nan")), dict(eps=float("inf")), dict(out=a + 1), dict(rstd=None), dict(rstd=a + 2), dict(r_codes=None), dict(r_scales=None),
+                dict(r_codes=a + 8), dict(c_codes=a + 8), dict(c_scales=None), dict(c_scales=a + 4),
+                dict(out=None, r_codes=None, r_scales=None, c_codes=None, c_scales=None),
+                dict(out=None, cols=12289, ldx=12289, ldr=12289, lds=12289)):
+        call("zs_rms_norm", *dict(good, **bad).values())
+    back = dict(dy=a, lddy=64, x=a, ldx=64, weight=a, weight_dtype=0, rstd=a, residual=a, ldr=64, rows=4, cols=64, dtype=0, dx=a, lddx=64, dw=a,
+                dw_dtype=2, scratch=a, r_codes=a, r_scales=a, c_codes=a, c_scales=a, stream=None)
+    for bad in (dict(dy=None), dict(dy=a + 1), dict(lddy=63), dict(x=None), dict(ldx=63), dict(weight=None), dict(weight_dtype=-1), dict(rstd=None),
+                dict(rstd=a + 1), dict(ldr=63), dict(rows=1 << 31), dict(cols=-1), dict(dtype=3), dict(dx=None), dict(lddx=63), dict(dw=a + 2),
+                dict(dw_dtype=3), dict(scratch=None), dict(scratch=a + 8), dict(r_scales=None), dict(c_codes=None), dict(c_codes=a + 1)):
+        call("zs_rms_norm_backward", *dict(back, **bad).values())
+    refuses(zs.zs_rms_norm_scratch, -1, 4)
+    refuses(zs.zs_rms_norm_scratch, 4, 1 << 31)
+    assert zs.zs_rms_norm_scratch(0, 64) == 0 and zs.zs_rms_norm_scratch(64, 0) == 0
+    # no more than a few hundred parts, each a row of floats
+    for rows, cols in ((1, 1), (33, 100), (5000, 4096), (1 << 20, 8192), (1 << 20, 20000)):
+        got = zs.zs_rms_norm_scratch(rows, cols)
+        assert got % (4 * cols) == 0 and 1 <= got // (4 * cols) <= 304

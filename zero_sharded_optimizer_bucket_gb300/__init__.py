@@ -208,6 +208,10 @@ _sig("zs_clip_tensors", _i32, [_P, _P, _P, _P])
 _sig("zs_mx4_sizes", _i32, [_i64, _i64, C.POINTER(_i64), C.POINTER(_i64), C.POINTER(_i64)])
 _sig("zs_mx4_quantize", _i32, [_P, _i64, _i64, _i64, _i32, _P, _P, _P, _P, _P])
 _sig("zs_mx4_dequantize", _i32, [_P, _P, _i64, _i64, _P, _i64, _i32, _P])
+_sig("zs_rms_norm", _i32, [_P, _i64, _P, _i64, _P, _i32, _i64, _i64, _i32, _f32, _P, _i64, _P, _i64, _P, _P, _P, _P, _P, _P])
+_sig("zs_rms_norm_scratch", _i32, [_i64, _i64, C.POINTER(_i64)])
+_sig("zs_rms_norm_backward", _i32, [_P, _i64, _P, _i64, _P, _i32, _P, _P, _i64, _i64, _i64, _i32, _P, _i64, _P, _i32, _P, _P, _P,
+                                    _P, _P, _P])
 _sig("zs_test_late_copy", _i32, [_P, _P, _i64, _i64, _P])
 _sig("zs_test_root", _i32, [_P, _P])
 _sig("zs_test_give_up", _i32, [_i32])
@@ -912,6 +916,75 @@ def zs_mx4_matmul(a, b, k: int, out, stream=None):
     if st:
         _check(st, "zs_mx4_matmul")
     return out
+
+
+def _like(m, what: str, rows: int, cols: int, dtype: int, device: int):
+    """(address, row stride) of a matrix of these sizes and type, or of none."""
+    if m is None:
+        return None, 0
+    r, c, ld, d = _matrix(m, what)
+    if r != rows or c != cols or d != dtype:
+        raise ValueError(f"{what}: {rows} x {cols} of x's type expected, got {tuple(m.shape)} of {m.dtype}")
+    return _device_address(m, what, device), ld
+
+
+def _vector(v, what: str, n: int, device: int, dtype=None):
+    """(address, dtype) of a contiguous vector of n elements, or of none."""
+    if v is None:
+        return None, ZS_DTYPE_FP32
+    d = _dtype(v)
+    if v.shape != (n,) or n > 1 and v.stride(0) != 1 or dtype is not None and d != dtype:
+        raise ValueError(f"{what}: {n} contiguous elements{' of float32' if dtype == ZS_DTYPE_FP32 else ''} expected, "
+                         f"got {tuple(v.shape)} of {v.dtype}")
+    return _device_address(v, what, device), d
+
+
+def zs_rms_norm(x, weight, eps: float, rstd, residual=None, sum=None, out=None, rows=None, cols=None, stream=None) -> None:
+    """x, residual, sum, out: [r, c] torch matrices of one type; weight [c];
+    rstd [r] float32.  rows: the dict of the result held along its rows, cols:
+    along its columns (of the transposed matrix)."""
+    device = _current_device()
+    r, c, ldx, dtype = _matrix(x, "x")
+    ra, ldr = _like(residual, "residual", r, c, dtype, device)
+    sa, lds = _like(sum, "sum", r, c, dtype, device)
+    oa, ldo = _like(out, "out", r, c, dtype, device)
+    wa, wd = _vector(weight, "weight", c, device)
+    rc, rs = _mx4(rows, r, c, device)
+    cc, cs = _mx4(cols, c, r, device)
+    st = _lib.zs_rms_norm(_device_address(x, "x", device), ldx, ra, ldr, wa, wd, r, c, dtype, eps, sa, lds, oa, ldo,
+                          _vector(rstd, "rstd", r, device, ZS_DTYPE_FP32)[0], rc, rs, cc, cs,
+                          _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "zs_rms_norm")
+
+
+def zs_rms_norm_scratch(rows: int, cols: int) -> int:
+    n = _i64()
+    _check(_lib.zs_rms_norm_scratch(int(rows), int(cols), C.byref(n)), "zs_rms_norm_scratch")
+    return n.value
+
+
+def zs_rms_norm_backward(dy, x, weight, rstd, dx, residual=None, dw=None, scratch=None, rows=None, cols=None, stream=None) -> None:
+    """dy, x, residual, dx: [r, c] torch matrices of one type; weight, dw [c];
+    rstd [r] float32; scratch: zs_rms_norm_scratch's bytes, for dw.  rows, cols:
+    the dicts of dx held along its rows and its columns."""
+    device = _current_device()
+    r, c, ldx, dtype = _matrix(x, "x")
+    ya, ldy = _like(dy, "dy", r, c, dtype, device)
+    ra, ldr = _like(residual, "residual", r, c, dtype, device)
+    da, ldd = _like(dx, "dx", r, c, dtype, device)
+    wa, wd = _vector(weight, "weight", c, device)
+    dwa, dwd = _vector(dw, "dw", c, device)
+    rc, rs = _mx4(rows, r, c, device)
+    cc, cs = _mx4(cols, c, r, device)
+    sa = _device_address(scratch, "scratch", device)
+    if dw is not None and hasattr(scratch, "data_ptr") and (scratch.nbytes < zs_rms_norm_scratch(r, c) or not scratch.is_contiguous()):
+        raise ValueError(f"scratch: {zs_rms_norm_scratch(r, c)} contiguous bytes expected, got {tuple(scratch.shape)} of {scratch.dtype}")
+    st = _lib.zs_rms_norm_backward(ya, ldy, _device_address(x, "x", device), ldx, wa, wd,
+                                   _vector(rstd, "rstd", r, device, ZS_DTYPE_FP32)[0], ra, ldr, r, c, dtype, da, ldd, dwa, dwd, sa,
+                                   rc, rs, cc, cs, _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "zs_rms_norm_backward")
 
 
 def zs_test_late_copy(dst, src, nbytes: int, delay_ns: int, stream=None) -> None:
