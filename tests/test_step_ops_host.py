@@ -55,3 +55,12 @@ def test_rms_norm_refusals():
     for rows, cols in ((1, 1), (33, 100), (5000, 4096), (1 << 20, 8192), (1 << 20, 20000)):
         got = zs.zs_rms_norm_scratch(rows, cols)
         assert got % (4 * cols) == 0 and 1 <= got // (4 * cols) <= 304
+
+
+def test_matvec_refusals():
+    a = A16
+    good = dict(m=3, n=40, k=64, x=a, ldx=64, dtype=0, codes=a, scales=a, out=a, ldo=40, out_dtype=2, stream=None)
+    for bad in (dict(m=-1), dict(m=zs.ZS_MATVEC_MAX_TOKENS + 1), dict(n=-1), dict(n=1 << 31), dict(k=1 << 31), dict(x=None), dict(x=a + 1), dict(ldx=63),
+                dict(dtype=3), dict(dtype=2, x=a + 2), dict(codes=None), dict(codes=a + 8), dict(scales=None), dict(scales=a + 1), dict(out=None),
+                dict(out=a + 2), dict(ldo=39), dict(out_dtype=-1)):
+        call("zs_mx4_matvec", *dict(good, **bad).values())

@@ -33,6 +33,7 @@ ZS_SKIP_NONFINITE = 1
 ZS_DTYPE_BF16, ZS_DTYPE_FP16, ZS_DTYPE_FP32 = 0, 1, 2
 ZS_ROUND_NEAREST, ZS_ROUND_STOCHASTIC = 0, 1
 ZS_STATE_BLOCK = 256     # elements that share the scales of 8-bit moments
+ZS_MATVEC_MAX_TOKENS = 1024
 ZS_NOALLOC_NORM_MAX_SCRATCH = 1 << 20
 TILE_DTYPE = [("dst", "<i8"), ("src", "<i8"), ("flat", "<i8"), ("win", "<i8"),
               ("len", "<i4"), ("valid", "<i4"), ("flat_len", "<i4"), ("bucket", "<i4")]
@@ -208,6 +209,7 @@ _sig("zs_clip_tensors", _i32, [_P, _P, _P, _P])
 _sig("zs_mx4_sizes", _i32, [_i64, _i64, C.POINTER(_i64), C.POINTER(_i64), C.POINTER(_i64)])
 _sig("zs_mx4_quantize", _i32, [_P, _i64, _i64, _i64, _i32, _P, _P, _P, _P, _P])
 _sig("zs_mx4_dequantize", _i32, [_P, _P, _i64, _i64, _P, _i64, _i32, _P])
+_sig("zs_mx4_matvec", _i32, [_i64, _i64, _i64, _P, _i64, _i32, _P, _P, _P, _i64, _i32, _P])
 _sig("zs_rms_norm", _i32, [_P, _i64, _P, _i64, _P, _i32, _i64, _i64, _i32, _f32, _P, _i64, _P, _i64, _P, _P, _P, _P, _P, _P])
 _sig("zs_rms_norm_scratch", _i32, [_i64, _i64, C.POINTER(_i64)])
 _sig("zs_rms_norm_backward", _i32, [_P, _i64, _P, _i64, _P, _i32, _P, _P, _i64, _i64, _i64, _i32, _P, _i64, _P, _i32, _P, _P, _P,
@@ -915,6 +917,21 @@ def zs_mx4_matmul(a, b, k: int, out, stream=None):
     st = _lib.zs_mx4_matmul(m, n, k, ac, as_, bc, bs, out.data_ptr(), ld, dtype, _current_stream() if stream is None else _stream(stream))
     if st:
         _check(st, "zs_mx4_matmul")
+    return out
+
+
+def zs_mx4_matvec(x, w, out, stream=None):
+    """out [m, n] = x [m, k] w [n, k]^T of a torch matrix and a held weight; out is returned."""
+    device = _current_device()
+    m, k, ldx, dtype = _matrix(x, "x")
+    rows, n, ldo, out_dtype = _matrix(out, "out")
+    if rows != m:
+        raise ValueError(f"out: {m} rows expected, got {rows}")
+    wc, ws = _mx4(w, n, k, device)
+    st = _lib.zs_mx4_matvec(m, n, k, _device_address(x, "x", device), ldx, dtype, wc, ws, _device_address(out, "out", device), ldo, out_dtype,
+                            _current_stream() if stream is None else _stream(stream))
+    if st:
+        _check(st, "zs_mx4_matvec")
     return out
 
 
