@@ -836,17 +836,15 @@ zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *a_codes, co
  * row stride ldx) through a weight held in 4 bits along its rows (zs_mx4_matmul
  * wants both operands in 4 bits; this one is for generating from the weights
  * that training holds, and for tokens too few to fill its tiles).  out:
- * out_dtype, row stride ldo.  bf16 and fp16 tokens are taken exactly but for
- * values below 2^-29 of their row's largest, which keep an error of 2^-39 of
- * it at most; fp32 ones to 2^-22 of a value, and 2^-50 of the largest.  The 32
- * products of a group are added in the tensor cores, 16 at a time, to an fp32
- * accumulator (each time off by at most 2^-22 of the magnitudes), times its
- * scale in fp32 to the sum of the groups, whose parts are added in an order
- * that the sizes alone set: out is within (ceil(k / 32) + 24) 2^-22 sum |x w|
- * before its one rounding to out_dtype.  Sums are held on the scale of the
- * largest token of the call's: they are finite while its largest magnitude times
- * the sum of a row's |w| is.  A NaN group is NaN, k = 0 gives zeros.  m at most
- * ZS_MATVEC_MAX_TOKENS.  Errors: ZS_EINVAL, ZS_ECUDA. */
+ * out_dtype, row stride ldo.  fp16 tokens are taken exactly, bf16 ones too but
+ * for values below 2^-29 of the largest of the 32 that meet a group of w, which
+ * keep an error of 2^-39 of it at most; fp32 ones to 2^-22 of a value and 2^-50
+ * of that largest.  The 32 products of a group are added in the tensor cores, 16
+ * at a time, to an fp32 accumulator (each time off by at most 2^-22 of the
+ * magnitudes), times the group's scale in fp32 to the sum of the groups, whose
+ * parts are added in an order that the sizes alone set: out is within
+ * (ceil(k / 32) + 24) 2^-22 sum |x w| before its one rounding to out_dtype.
+ * A NaN group is NaN, k = 0 gives zeros.  m at most ZS_MATVEC_MAX_TOKENS.  Errors: ZS_EINVAL, ZS_ECUDA. */
 #define ZS_MATVEC_MAX_TOKENS 1024
 zs_status zs_mx4_matvec(int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, int32_t dtype,
                         const void *w_codes, const void *w_scales, void *out, int64_t ldo,

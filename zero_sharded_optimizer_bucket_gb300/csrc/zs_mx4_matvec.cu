@@ -1,11 +1,12 @@
 // A few tokens of 16 or 32 bits through a weight held in 4 bits
 // (zs_mx4_matvec): out[m][n] = sum over k of x[m][k] w[n][k].
 //
-// The weight's 0.53 bytes an element are read once and decoded in registers;
-// products go to the tensor cores in fp16 (mma m16n8k16): a code is exact
-// there, a token's values are after a power of two of their own (fp32 ones as
-// two numbers of 11 bits), sums are fp32, and a group's scale is multiplied to
-// its 32 products' sum.
+// The weight's 0.53 bytes an element are read once, and each is decoded once
+// for 8, 16 or 32 tokens.  Products go to the tensor cores in fp16 (mma
+// m16n8k16): a code is exact there, and so are a token's values, 32 of them
+// (those that meet a group of the weight) times a power of two of their own;
+// fp32 ones are two numbers of 11 bits each.  The 32 products' sum in fp32 is
+// multiplied by both powers of two and added to the row's.
 #include <atomic>
 #include <cooperative_groups.h>
 
@@ -21,200 +22,391 @@ struct MatvecArgs {
     const uint8_t *codes, *scales;
     void *out;
     int64_t m, n, k, ldx, ldo;
-    int32_t out_kind, row_tiles;     // row tiles of 16 a CTA (1, 2, 4, 8)
+    int32_t out_kind;
+    int32_t warps_n, warps_k;        // warps of a CTA along the rows and along k
+    int32_t stage;                   // chunks of k whose tokens lie in shared memory at a time
+    int32_t columns;                 // of shared memory: tokens, two each for fp32
+    uint32_t per_token, per_row;     // 2^32 over the pieces of a token's stage, over the rows of a CTA
+    bool vec;                        // 16-byte aligned rows of x
 };
 
+constexpr int MV_THREADS = 512, MV_WARPS = MV_THREADS / 32;
 constexpr int MV_CHUNK = 128;        // k of one atom of scales: 4 groups
-// k of x that lies in shared memory at a time
-__host__ __device__ constexpr int mv_stage(int nb) { return nb == 1 ? 4096 : nb == 2 ? 2048 : 1024; }
-__host__ __device__ constexpr int mv_pitch(int nb) { return mv_stage(nb) + 32; }         // halves; 64 bytes past 128: two tokens' pieces side by side
-__host__ __device__ constexpr int mv_smem(int nb) { return 8 * nb * mv_pitch(nb) * 2; }
+constexpr int MV_ROW = 80;           // bytes from row to row of 64 bytes of codes: 8 rows' words meet 32 banks
+constexpr int MV_PIECES = 5;         // pieces of 8 values of x that a thread holds for the next stage
+// NB: tiles of 8 columns of tokens; a warp takes mv_tiles(NB) tiles of 16 rows
+// (so that a token's values, once loaded, meet as many rows as registers hold),
+// with MV_DEPTH chunks in flight.
+__host__ __device__ constexpr int mv_tiles(int nb) { return nb == 1 ? 1 : 2; }
+constexpr int MV_DEPTH = 3;
+__host__ __device__ constexpr int mv_chunk_bytes(int nb) { return mv_tiles(nb) * (16 * MV_ROW + 64); }
+__host__ __device__ constexpr int mv_ring_bytes(int nb) { return MV_WARPS * MV_DEPTH * mv_chunk_bytes(nb); }
+__host__ __device__ constexpr int mv_most_stage(int nb) { return nb == 1 ? 16 : nb == 2 ? 10 : 5; }
+// columns are 64 bytes past a multiple of 128 apart: two of them side by side in the banks
+__host__ __device__ constexpr int mv_pitch(int stage) { return stage * MV_CHUNK + 32; }      // halves
+// a stage's powers of two, one a group and column, and its columns
+__host__ __device__ constexpr int mv_powers(int columns) { return (columns + 1) & ~1; }
+__host__ __device__ constexpr int mv_stage_bytes(int stage, int columns) { return ((16 * stage * mv_powers(columns) + 15) & ~15) + columns * mv_pitch(stage) * 2; }
 
-// codes j and j + 4 of 8 as two halves, 2^-14 of their values: the sign to the
-// top, exponent and mantissa to the lowest exponent bits and the highest
-// mantissa bit (1/2 is subnormal there, and exact)
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) {
-    const uint32_t t = j == 3 ? w : w << (12 - 4 * j);
-    return (t & 0x80008000u) | ((t >> 3) & 0x0E000E00u);
+// the values of 8 codes as four pairs of halves
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t o[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
 }
 
-__device__ __forceinline__ void mma16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+// four scale bytes as floats (0: 2^-127, 255: NaN)
+__device__ __forceinline__ void scales4(uint32_t w, float o[4]) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %0, a;\n\t"
+        "cvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+    o[0] = __uint_as_float(lo << 16);
+    o[1] = __uint_as_float(lo & 0xFFFF0000u);
+    o[2] = __uint_as_float(hi << 16);
+    o[3] = __uint_as_float(hi & 0xFFFF0000u);
+}
+
+// the products of 16 rows, 32 of k and 8 columns
+__device__ __forceinline__ void mma_group(float d[4], const uint32_t lo[4], const uint32_t hi[4], const uint4 &v) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]), "r"(v.x), "r"(v.y), "f"(0.0f));
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]), "r"(v.z), "r"(v.w));
 }
 
+// 16 or 4 bytes to shared memory, zeros where there is nothing
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" : : "r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void *from, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" : : "r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
+}
+
+__device__ __forceinline__ float mv_power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }     // 2^e, normal
+
+// 8 values of a token as they lie in memory
 template <int KIND>
-__device__ __forceinline__ float mv_value(const void *x, int64_t at) {
-    if (KIND == ZS_DTYPE_FP32) return static_cast<const float *>(x)[at];
-    const uint32_t b = static_cast<const uint16_t *>(x)[at];
-    return KIND == ZS_DTYPE_FP16 ? FP16T::to_f32(b) : BF16T::to_f32(b);
+struct Piece {
+    uint4 a;
+};
+template <>
+struct Piece<ZS_DTYPE_FP32> {
+    uint4 a, b;
+};
+template <int KIND>
+__device__ __forceinline__ Piece<KIND> mv_load(const void *x, int64_t at, int n, bool vec) {
+    Piece<KIND> p;
+    if constexpr (KIND == ZS_DTYPE_FP32) {
+        const uint32_t *q = static_cast<const uint32_t *>(x) + at;
+        if (vec && n >= 8) {
+            p.a = *reinterpret_cast<const uint4 *>(q);
+            p.b = *reinterpret_cast<const uint4 *>(q + 4);
+        } else {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < n ? q[i] : 0u;
+            p.a = make_uint4(v[0], v[1], v[2], v[3]);
+            p.b = make_uint4(v[4], v[5], v[6], v[7]);
+        }
+    } else {
+        const uint16_t *q = static_cast<const uint16_t *>(x) + at;
+        if (vec && n >= 8) {
+            p.a = *reinterpret_cast<const uint4 *>(q);
+        } else {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < n ? (uint32_t)q[i] : 0u;
+            p.a = pack8(v);
+        }
+    }
+    return p;
+}
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// floor(log2) of a token's largest magnitude, from its bits; at least what
-// float32 has powers of two for
-__device__ __forceinline__ int mv_exponent(int top) { return max((int)((uint32_t)top >> 23) - 127, -112); }
-__device__ __forceinline__ float mv_power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }     // e of normal numbers
-
-// A CTA takes 16 * row_tiles rows of the weight and, of a cluster of S, one
-// S-th of k, its warps sharing both; 8 NB columns of tokens (fp32: two columns
-// a token) lie in shared memory as halves.
+// A CTA takes 16 * mv_tiles * warps_n rows of the weight and, of a cluster of
+// S, one S-th of k, whose chunks its warps_k warps of the same rows take in
+// turn.  A warp copies its chunks' codes and scales ahead into a ring of its
+// own; all share the tokens, which lie in shared memory as halves: of all the
+// CTA's k where there is room, otherwise for a stage of chunks at a time while
+// the next stage's are on their way to registers.
+// Sums go from the warps to the CTA and from there to the cluster in a fixed
+// order.
 template <int KIND, int NB>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(MV_THREADS, NB == 1 ? 2 : 1)
 mx4_matvec_kernel(MatvecArgs a) {
-    constexpr int COLS = 8 * NB, PER = KIND == ZS_DTYPE_FP32 ? 2 : 1, TOKENS = COLS / PER, PITCH = mv_pitch(NB);
+    constexpr bool HALVES = KIND == ZS_DTYPE_FP16;
+    constexpr int PER = KIND == ZS_DTYPE_FP32 ? 2 : 1, TOKENS = 8 * NB / PER, TILES = mv_tiles(NB), DEPTH = MV_DEPTH, CHUNK = mv_chunk_bytes(NB);
+    constexpr int HOLD = KIND == ZS_DTYPE_FP32 ? (MV_PIECES + 1) / 2 : MV_PIECES;
     extern __shared__ __align__(16) uint8_t raw[];
-    __half *xs = reinterpret_cast<__half *>(raw);
-    __shared__ float share[COLS * 128];
-    __shared__ int top[TOKENS];
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane >> 2, t = lane & 3;
-    const int parts = WARPS / a.row_tiles, part = warp / a.row_tiles, tile = warp % a.row_tiles;
-    const int64_t row0 = ((int64_t)(blockIdx.x / ranks) * a.row_tiles + tile) * 16, token0 = (int64_t)blockIdx.y * TOKENS;
+    const int wn = warp / a.warps_k, wk = warp % a.warps_k;
+    const bool works = wn < a.warps_n;
+    const int64_t row0 = ((int64_t)(blockIdx.x / ranks) * a.warps_n + wn) * (16 * TILES), token0 = (int64_t)blockIdx.y * TOKENS;
     const int tokens = (int)min((int64_t)TOKENS, a.m - token0);
-    const int64_t groups = mx4_groups(a.k), chunks = (groups + 3) / 4, row_bytes = mx4_row_bytes(a.k), atoms = mx4_atoms(a.k);
-    const int64_t first = chunks * rank / ranks, last = chunks * (rank + 1) / ranks;
-    if (threadIdx.x < TOKENS) top[threadIdx.x] = 0;
-    __syncthreads();
+    const int groups = (int)mx4_groups(a.k), chunks = (groups + 3) / 4, atoms = (int)mx4_atoms(a.k);
+    const int64_t row_bytes = mx4_row_bytes(a.k);
+    const int first = (int)((int64_t)chunks * rank / ranks), last = (int)((int64_t)chunks * (rank + 1) / ranks);
+    const int stage = a.stage, pitch = mv_pitch(stage);
+    const uint32_t ring = smem_u32(raw) + warp * (DEPTH * CHUNK);
+    uint8_t *area = raw + mv_ring_bytes(NB);                              // one or two stages of tokens
+    const int powers = mv_powers(a.columns), area_bytes = mv_stage_bytes(stage, a.columns), xs_at = area_bytes - a.columns * pitch * 2;
     pdl_wait();
     pdl_trigger();
-    // the largest finite magnitude of each token in this part of k
-    const int64_t k0 = first * MV_CHUNK, k1 = min(last * MV_CHUNK, a.k);
-    for (int i = 0; i < tokens; ++i) {
-        uint32_t most = 0;
-        for (int64_t k = k0 + threadIdx.x; k < k1; k += THREADS) {
-            const uint32_t b = __float_as_uint(mv_value<KIND>(a.x, (token0 + i) * a.ldx + k)) & 0x7FFFFFFFu;
-            if (b < 0x7F800000u) most = max(most, b);
+    // a warp's chunks: every warps_k-th (a stage is a multiple of them)
+    int ahead = first + wk, slot = 0;                                     // the next chunk to be copied, and its place
+    const int64_t row = row0 + q, scale_row = row0 + lane;                // of the copies: 4 lanes a row
+    const uint8_t *codes = a.codes + row * row_bytes + 64 * (int64_t)ahead + 16 * t;
+    const uint8_t *scales = a.scales + ((scale_row >> 7) * atoms + ahead) * MX4_ATOM + mx4_in_atom((int)(scale_row & 127), 0);
+    const int codes_n = works ? (int)min((int64_t)(16 * TILES), max((int64_t)0, a.n - row0)) : 0;     // rows that there are
+    auto copy = [&] {
+        const uint32_t to = ring + slot * CHUNK;
+        if (ahead < last && codes_n > 0) {
+            const bool inside = 4 * ahead + t < groups;
+#pragma unroll
+            for (int i = 0; i < 2 * TILES; ++i) {
+                const bool there = inside && q + 8 * i < codes_n;
+                copy16(to + (8 * i + q) * MV_ROW + 16 * t, there ? codes + 8 * i * row_bytes : a.codes, there);
+            }
+            if (lane < 16 * TILES) copy4(to + 16 * TILES * MV_ROW + 4 * lane, lane < codes_n ? scales : a.scales, lane < codes_n);
         }
-        most = __reduce_max_sync(0xFFFFFFFFu, most);
-        if (lane == 0) atomicMax(&top[i], (int)most);
-    }
-    __syncthreads();
-    // sums are held as those of the largest token, so that none overflows before it does
-    int most = 0;
-    for (int i = 0; i < tokens; ++i) most = max(most, top[i]);
-    const int common = mv_exponent(most);
-    const float up = mv_power(min(common, 126));
-    float acc[NB][4] = {};
-    const int64_t ra = row0 + q, rb = ra + 8;
-    const bool has_a = ra < a.n, has_b = rb < a.n;
-    const uint8_t *ca = a.codes + ra * row_bytes + 4 * t, *cb = a.codes + rb * row_bytes + 4 * t;
-    const uint8_t *sa = a.scales + (ra >> 7) * atoms * MX4_ATOM + mx4_in_atom((int)(ra & 127), 0);
-    const uint8_t *sb = a.scales + (rb >> 7) * atoms * MX4_ATOM + mx4_in_atom((int)(rb & 127), 0);
-    constexpr int STAGE = mv_stage(NB) / MV_CHUNK;
-    for (int64_t c0 = first; c0 < last; c0 += STAGE) {
-        const int n = (int)min((int64_t)STAGE, last - c0);
-        if (c0 > first) __syncthreads();
-        // tokens to halves, times 2^(14 - E), element 8 i + j at 8 i + 2 (j % 4) + j / 4: a lane's 8 codes in the order of its pairs
-        for (int i = warp; i < tokens; i += WARPS) {
-            const float f = mv_power(14 - mv_exponent(top[i]));
-            for (int kk = lane; kk < n * MV_CHUNK; kk += 32) {
-                const int64_t k = c0 * MV_CHUNK + kk;
-                const float v = k < a.k ? __fmul_rn(mv_value<KIND>(a.x, (token0 + i) * a.ldx + k), f) : 0.0f;
-                const int at = (kk & ~7) + 2 * (kk & 3) + ((kk >> 2) & 1);
-                const __half h = __float2half_rn(v);
-                xs[PER * i * PITCH + at] = h;
-                if (PER == 2) xs[(PER * i + 1) * PITCH + at] = __hisinf(h) || __hisnan(h) ? __half(0.0f) : __float2half_rn(__fmul_rn(__fsub_rn(v, __half2float(h)), 2048.0f));
+        ahead += a.warps_k;
+        codes += 64 * (int64_t)a.warps_k;
+        scales += (int64_t)MX4_ATOM * a.warps_k;
+        slot = slot + 1 == DEPTH ? 0 : slot + 1;
+        asm volatile("cp.async.commit_group;" : : : "memory");
+    };
+#pragma unroll
+    for (int u = 0; u < DEPTH - 1; ++u) copy();
+    Piece<KIND> held[HOLD];
+    const int pieces = 16 * stage;                                        // of a token
+    // pieces j0, j0 + 1, .. of this thread in the stage from chunk c0 on
+    auto load = [&](int c0, int j0) {
+        const int64_t k0 = (int64_t)c0 * MV_CHUNK;
+#pragma unroll
+        for (int j = 0; j < HOLD; ++j) {
+            if (MV_THREADS * (j0 + j) >= tokens * pieces) break;
+            const int p = (int)threadIdx.x + MV_THREADS * (j0 + j), token = (int)__umulhi((uint32_t)p, a.per_token);
+            const int64_t k = k0 + 8 * (p - token * pieces);
+            const int n = token < tokens ? (int)max((int64_t)0, min((int64_t)8, a.k - k)) : 0;
+            held[j] = mv_load<KIND>(a.x, (token0 + token) * a.ldx + k, n, a.vec);
+        }
+    };
+    auto put = [&](int buffer, int j0) {
+        float *fe = reinterpret_cast<float *>(area + buffer * area_bytes);
+        uint8_t *xs = area + buffer * area_bytes + xs_at;
+#pragma unroll
+        for (int j = 0; j < HOLD; ++j) {
+            if (MV_THREADS * (j0 + j) >= tokens * pieces) break;
+            const int p = (int)threadIdx.x + MV_THREADS * (j0 + j), token = (int)__umulhi((uint32_t)p, a.per_token), at = p - token * pieces;
+            if constexpr (HALVES) {
+                if (token < tokens) *reinterpret_cast<uint4 *>(xs + token * pitch * 2 + 16 * at) = held[j].a;
+            } else {
+                float v[8];
+                if constexpr (KIND == ZS_DTYPE_FP32) {
+                    const uint32_t u[8] = {held[j].a.x, held[j].a.y, held[j].a.z, held[j].a.w, held[j].b.x, held[j].b.y, held[j].b.z, held[j].b.w};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = BF16T::to_f32(lane16(held[j].a, i));
+                }
+                uint32_t top = 0;                                         // of the finite ones
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+                    top = max(top, b < 0x7F800000u ? b : 0u);
+                }
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                // the largest to [2^14, 2^15), as far as the inverse is a normal number
+                const int e = max((int)(top >> 23) - 127, PER == 2 ? -101 : -112);
+                const float f = mv_power(14 - e);
+                if (token < tokens) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) h[i] = half_pair(__fmul_rn(v[2 * i], f), __fmul_rn(v[2 * i + 1], f));
+                    *reinterpret_cast<uint4 *>(xs + PER * token * pitch * 2 + 16 * at) = make_uint4(h[0], h[1], h[2], h[3]);
+                    if constexpr (PER == 2) {                             // what 11 bits left; nothing of an infinity or NaN
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 w = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+                            const float l0 = __fmul_rn(__fsub_rn(__fmul_rn(v[2 * i], f), w.x), 2048.0f), l1 = __fmul_rn(__fsub_rn(__fmul_rn(v[2 * i + 1], f), w.y), 2048.0f);
+                            h[i] = half_pair(fabsf(l0) < 65504.0f ? l0 : 0.0f, fabsf(l1) < 65504.0f ? l1 : 0.0f);
+                        }
+                        *reinterpret_cast<uint4 *>(xs + (PER * token + 1) * pitch * 2 + 16 * at) = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                    if ((lane & 3) == 0) {
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) fe[(at >> 2) * powers + PER * token + i] = mv_power(e - 14 - 11 * i);
+                    }
+                }
             }
         }
+    };
+    for (int j0 = 0; MV_THREADS * j0 < tokens * pieces; j0 += HOLD) {
+        load(first, j0);
+        put(0, j0);
+    }
+    __syncthreads();
+    float acc[TILES][NB][4] = {};
+    int place = 0;
+    for (int c0 = first, s = 0; c0 < last; c0 += stage, ++s) {
+        if (c0 + stage < last) load(c0 + stage, 0);
+        const float *fe = reinterpret_cast<const float *>(area + (s & 1) * area_bytes);
+        const uint8_t *xs = area + (s & 1) * area_bytes + xs_at;
+        for (int c = wk; c < stage; c += a.warps_k) {                     // in the stage
+            copy();
+            asm volatile("cp.async.wait_group %0;" : : "n"(DEPTH - 1) : "memory");
+            __syncwarp();
+            if (codes_n > 0 && c0 + c < last) {
+                const uint8_t *from = raw + warp * (DEPTH * CHUNK) + place * CHUNK;
+                float fs[TILES][2][4];
+#pragma unroll
+                for (int r = 0; r < TILES; ++r) {
+                    scales4(*reinterpret_cast<const uint32_t *>(from + 16 * TILES * MV_ROW + 4 * (16 * r + q)), fs[r][0]);
+                    scales4(*reinterpret_cast<const uint32_t *>(from + 16 * TILES * MV_ROW + 4 * (16 * r + q + 8)), fs[r][1]);
+                }
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    uint32_t lo[TILES][4], hi[TILES][4];
+#pragma unroll
+                    for (int r = 0; r < TILES; ++r) {
+                        uint32_t pa[4], pb[4];
+                        code_pairs(*reinterpret_cast<const uint32_t *>(from + (16 * r + q) * MV_ROW + 16 * g + 4 * t), pa);
+                        code_pairs(*reinterpret_cast<const uint32_t *>(from + (16 * r + q + 8) * MV_ROW + 16 * g + 4 * t), pb);
+                        lo[r][0] = pa[0]; lo[r][1] = pb[0]; lo[r][2] = pa[1]; lo[r][3] = pb[1];
+                        hi[r][0] = pa[2]; hi[r][1] = pb[2]; hi[r][2] = pa[3]; hi[r][3] = pb[3];
+                    }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (8 * b + q < PER * tokens) v = *reinterpret_cast<const uint4 *>(xs + (8 * b + q) * pitch * 2 + 2 * (c * MV_CHUNK + 32 * g + 8 * t));
+                        float2 f = make_float2(1.0f, 1.0f);
+                        if (!HALVES) f = *reinterpret_cast<const float2 *>(fe + (4 * c + g) * powers + 8 * b + 2 * t);
+#pragma unroll
+                        for (int r = 0; r < TILES; ++r) {
+                            float d[4];
+                            mma_group(d, lo[r], hi[r], v);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                acc[r][b][j] = __fmaf_rn(HALVES ? d[j] : __fmul_rn(d[j], j & 1 ? f.y : f.x), fs[r][j >> 1][g], acc[r][b][j]);
+                        }
+                    }
+                }
+            }
+            place = place + 1 == DEPTH ? 0 : place + 1;
+            __syncwarp();                                                 // the chunk's place may be filled again
+        }
+        if (c0 + stage < last) put((s + 1) & 1, 0);
         __syncthreads();
-        for (int c = part; c < n; c += parts) {
-            const int64_t g0 = 4 * (c0 + c);
-            uint32_t wa[4], wb[4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                wa[g] = has_a && g0 + g < groups ? *reinterpret_cast<const uint32_t *>(ca + 16 * (g0 + g)) : 0u;
-                wb[g] = has_b && g0 + g < groups ? *reinterpret_cast<const uint32_t *>(cb + 16 * (g0 + g)) : 0u;
-            }
-            const uint32_t za = has_a ? *reinterpret_cast<const uint32_t *>(sa + (c0 + c) * MX4_ATOM) : 0u;
-            const uint32_t zb = has_b ? *reinterpret_cast<const uint32_t *>(sb + (c0 + c) * MX4_ATOM) : 0u;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                uint32_t pa[4], pb[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    pa[j] = code_pair(wa[g], j);
-                    pb[j] = code_pair(wb[g], j);
-                }
-                const float fa = __fmul_rn(mx4_scale((za >> (8 * g)) & 255u), up), fb = __fmul_rn(mx4_scale((zb >> (8 * g)) & 255u), up);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (8 * b + q < PER * tokens) v = *reinterpret_cast<const uint4 *>(xs + (8 * b + q) * PITCH + c * MV_CHUNK + 32 * g + 8 * t);
-                    float d[4] = {};
-                    mma16816(d, pa[0], pb[0], pa[1], pb[1], v.x, v.y);
-                    mma16816(d, pa[2], pb[2], pa[3], pb[3], v.z, v.w);
-                    acc[b][0] = __fmaf_rn(d[0], fa, acc[b][0]);
-                    acc[b][1] = __fmaf_rn(d[1], fa, acc[b][1]);
-                    acc[b][2] = __fmaf_rn(d[2], fb, acc[b][2]);
-                    acc[b][3] = __fmaf_rn(d[3], fb, acc[b][3]);
-                }
-            }
-        }
     }
+    asm volatile("cp.async.wait_all;" : : : "memory");
     __syncthreads();
-    // the warps' parts of k, in their order: [warp][column][16 rows]
-    float *red = reinterpret_cast<float *>(raw);
+    // the warps' sums: [warp][column][rows of a warp]
+    constexpr int ROWS = 16 * TILES;
+    float *red = reinterpret_cast<float *>(raw), *share = reinterpret_cast<float *>(area);
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int r = 0; r < TILES; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) red[(warp * COLS + 8 * b + 2 * t + (i & 1)) * 16 + q + 8 * (i >> 1)] = acc[b][i];
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) red[(warp * 8 * NB + 8 * b + 2 * t + (j & 1)) * ROWS + 16 * r + q + 8 * (j >> 1)] = acc[r][b][j];
     __syncthreads();
-    const int rows = 16 * a.row_tiles;
-    for (int i = threadIdx.x; i < tokens * rows; i += THREADS) {
-        const int token = i / rows, r = i % rows;
-        const int down = mv_exponent(top[token]) - min(common, 126);
+    const int rows = ROWS * a.warps_n;
+    for (int i = threadIdx.x; i < tokens * rows; i += MV_THREADS) {
+        const int token = (int)__umulhi((uint32_t)i, a.per_row), r = i - token * rows;
         float s[PER];
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
             s[p] = 0.0f;
-            for (int w = 0; w < parts; ++w) s[p] = __fadd_rn(s[p], red[((w * a.row_tiles + r / 16) * COLS + PER * token + p) * 16 + r % 16]);
+            for (int w = 0; w < a.warps_k; ++w)
+                s[p] = __fadd_rn(s[p], red[((r / ROWS * a.warps_k + w) * 8 * NB + PER * token + p) * ROWS + r % ROWS]);
         }
-        float v = s[0];
-        if (PER == 2) v = __fmaf_rn(s[PER - 1], 1.0f / 2048, v);
-        // the codes' 2^-14 and the token's 2^14 are one another's
-        share[token * rows + r] = __fmul_rn(__fmul_rn(v, mv_power(down >> 1)), mv_power(down - (down >> 1)));
+        share[i] = PER == 2 ? __fadd_rn(s[0], s[PER - 1]) : s[0];
     }
-    cluster.sync();
+    if (ranks > 1) cluster.sync();
+    else __syncthreads();
     const int64_t block0 = (int64_t)(blockIdx.x / ranks) * rows;
-    for (int i = rank * THREADS + threadIdx.x; i < tokens * rows; i += THREADS * ranks) {
-        float s = 0.0f;
-        for (int r = 0; r < ranks; ++r) s = __fadd_rn(s, cluster.map_shared_rank(share, r)[i]);
-        const int64_t row = block0 + i % rows, at = (token0 + i / rows) * a.ldo + row;
-        if (row >= a.n) continue;
+    for (int i = rank * MV_THREADS + threadIdx.x; i < tokens * rows; i += MV_THREADS * ranks) {
+        float s = share[i];
+        if (ranks > 1) {
+            s = 0.0f;
+            for (int r = 0; r < ranks; ++r) s = __fadd_rn(s, cluster.map_shared_rank(share, r)[i]);
+        }
+        const int token = (int)__umulhi((uint32_t)i, a.per_row);
+        const int64_t o = block0 + i - token * rows, at = (token0 + token) * a.ldo + o;
+        if (o >= a.n) continue;
         if (a.out_kind == ZS_DTYPE_FP32) static_cast<float *>(a.out)[at] = s;
         else static_cast<uint16_t *>(a.out)[at] = (uint16_t)(a.out_kind == ZS_DTYPE_FP16 ? FP16T::from_f32(s) : BF16T::from_f32(s));
     }
-    cluster.sync();                  // the others may still read this CTA's sums
+    if (ranks > 1) cluster.sync();   // the others may still read this CTA's sums
 }
 
 template <int KIND, int NB>
 static cudaError_t matvec_launch(MatvecArgs a, cudaStream_t s) {
     static std::atomic<bool> set[64];
+    constexpr int PER = KIND == ZS_DTYPE_FP32 ? 2 : 1, TOKENS = 8 * NB / PER;
+    constexpr int ROOM = 227 * 1024 - mv_ring_bytes(NB);                 // of tokens, a CTA alone on its SM
+    static_assert(2 * mv_stage_bytes(mv_most_stage(NB), 8 * NB) <= ROOM, "shared memory");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!set[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(mx4_matvec_kernel<KIND, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, mv_smem(NB));
+        e = cudaFuncSetAttribute(mx4_matvec_kernel<KIND, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_relaxed);
     }
-    const int64_t tokens = 8 * NB / (KIND == ZS_DTYPE_FP32 ? 2 : 1), ty = (a.m + tokens - 1) / tokens, tiles = (a.n + 15) / 16;
+    const int64_t ty = (a.m + TOKENS - 1) / TOKENS, tiles = (a.n + 16 * mv_tiles(NB) - 1) / (16 * mv_tiles(NB));
     const int64_t chunks = (mx4_groups(a.k) + 3) / 4;
-    // enough CTAs for two an SM: first by parts of k, then by fewer rows each
+    // How warps and CTAs share rows and k.  In units of about 100 cycles: a step
+    // of an SM's 16 warps 5 where instructions bound it, and 2 of latency; a
+    // CTA's beginning and end 15 (tokens to halves, the sums), an exchange 4.
+    int64_t best = -1;
     int split = 1;
-    a.row_tiles = 8;
-    auto ctas = [&] { return (tiles + a.row_tiles - 1) / a.row_tiles * split * ty; };
-    while (ctas() < 304 && split < 8 && chunks >= 2 * split * (WARPS / a.row_tiles)) split *= 2;
-    while (ctas() < 304 && a.row_tiles > 1 && chunks >= 2 * split * (WARPS / a.row_tiles)) a.row_tiles /= 2;
-    const int64_t blocks = (tiles + a.row_tiles - 1) / a.row_tiles * split;
-    if (blocks > 0x7FFFFFFF || ty > 65535) return cudaErrorInvalidValue;
+    for (int wk = 1; wk <= mv_most_stage(NB); ++wk) {
+        if (wk > 1 && wk > chunks) break;
+        const int64_t wn = tiles < MV_WARPS / wk ? tiles : MV_WARPS / wk, blocks = (tiles + wn - 1) / wn * ty;
+        for (int sp = 1; sp <= 8 && (sp == 1 || chunks >= (int64_t)sp * wk); ++sp) {
+            const int64_t steps = ((chunks + sp - 1) / sp + wk - 1) / wk, cost = (blocks * sp + 151) / 152 * (5 * steps + 15) + 2 * steps + (sp > 1 ? 4 : 0);
+            if (best >= 0 && cost >= best) continue;
+            best = cost;
+            a.warps_k = wk;
+            a.warps_n = (int)wn;
+            split = sp;
+        }
+    }
+    a.columns = (int)(a.m < TOKENS ? a.m : TOKENS) * PER;
+    const int64_t whole = ((chunks + split - 1) / split + a.warps_k - 1) / a.warps_k * a.warps_k;
+    const bool fits = whole <= 1024 && mv_stage_bytes((int)whole, a.columns) <= (NB == 1 ? 113 * 1024 - mv_ring_bytes(NB) : ROOM);     // two CTAs an SM, one
+    a.stage = fits ? (int)whole : mv_most_stage(NB) / a.warps_k * a.warps_k;
+    // exact for the numbers below 2^16 that are divided
+    a.per_token = (uint32_t)(((uint64_t)1 << 32) / (16 * a.stage) + 1);
+    a.per_row = (uint32_t)(((uint64_t)1 << 32) / (16 * mv_tiles(NB) * a.warps_n) + 1);
+    const int64_t grid = (tiles + a.warps_n - 1) / a.warps_n * split;
+    if (grid > 0x7FFFFFFF || ty > 65535) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks, (unsigned)ty);
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = mv_smem(NB);
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)ty);
+    cfg.blockDim = dim3(MV_THREADS);
+    cfg.dynamicSmemBytes = mv_ring_bytes(NB) + (fits ? 1 : 2) * mv_stage_bytes(a.stage, a.columns);
+    const int share = 16 * mv_tiles(NB) * a.warps_n * (a.columns / PER) * 4;     // the CTA's sums, in the tokens' place
+    if ((int)cfg.dynamicSmemBytes < mv_ring_bytes(NB) + share) cfg.dynamicSmemBytes = mv_ring_bytes(NB) + share;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -223,7 +415,7 @@ static cudaError_t matvec_launch(MatvecArgs a, cudaStream_t s) {
     attr[1].val.clusterDim.x = (unsigned)split;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = split > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, mx4_matvec_kernel<KIND, NB>, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -263,6 +455,7 @@ extern "C" zs_status zs_mx4_matvec(int64_t m, int64_t n, int64_t k, const void *
         zsk::MatvecArgs a;
         a.x = x; a.codes = static_cast<const uint8_t *>(w_codes); a.scales = static_cast<const uint8_t *>(w_scales); a.out = out;
         a.m = m; a.n = n; a.k = k; a.ldx = ldx; a.ldo = ldo; a.out_kind = out_dtype;
+        a.vec = addr(x) % 16 == 0 && (m == 1 || ldx * size(dtype) % 16 == 0);
         e = dtype == ZS_DTYPE_FP32 ? zsk::matvec_of<ZS_DTYPE_FP32>(a, s)
           : dtype == ZS_DTYPE_FP16 ? zsk::matvec_of<ZS_DTYPE_FP16>(a, s) : zsk::matvec_of<ZS_DTYPE_BF16>(a, s);
     }
