@@ -16,6 +16,7 @@
 namespace zsk {
 
 namespace cg = cooperative_groups;
+typedef unsigned long long f2;
 
 struct MatvecArgs {
     const void *x;
@@ -24,29 +25,37 @@ struct MatvecArgs {
     int64_t m, n, k, ldx, ldo;
     int32_t out_kind;
     int32_t warps_n, warps_k;        // warps of a CTA along the rows and along k
-    int32_t stage;                   // chunks of k whose tokens lie in shared memory at a time
+    int32_t depth;                   // units of a warp's ring
+    int32_t units;                   // of k, of each CTA of a cluster
+    int32_t stage;                   // units of k whose tokens lie in shared memory at a time
     int32_t columns;                 // of shared memory: tokens, two each for fp32
-    uint32_t per_token, per_row;     // 2^32 over the pieces of a token's stage, over the rows of a CTA
-    bool vec;                        // 16-byte aligned rows of x
+    // 2^32 over the pieces of a token's stage, a quarter of a CTA's rows, warps_k, rounded up
+    uint32_t per_token, per_row, per_warp;
+    bool vec_out;                    // 16-byte aligned rows of out
+    bool vec;                        // rows of x are 16-byte aligned and whole pieces of 8 values
 };
 
-constexpr int MV_THREADS = 512, MV_WARPS = MV_THREADS / 32;
-constexpr int MV_CHUNK = 128;        // k of one atom of scales: 4 groups
-constexpr int MV_ROW = 80;           // bytes from row to row of 64 bytes of codes: 8 rows' words meet 32 banks
+// 16 warps at 128 registers, or for 32 columns, whose sums take 64, 12 at 168
+// (24 warps at 80 registers for 8 columns: 15.2 us for 1 x 4096 x 14336, not 11.7).
+__host__ __device__ constexpr int mv_warps(int nb) { return nb == 4 ? 12 : 16; }
 constexpr int MV_PIECES = 5;         // pieces of 8 values of x that a thread holds for the next stage
-// NB: tiles of 8 columns of tokens; a warp takes mv_tiles(NB) tiles of 16 rows
-// (so that a token's values, once loaded, meet as many rows as registers hold),
-// with MV_DEPTH chunks in flight.
-__host__ __device__ constexpr int mv_tiles(int nb) { return nb == 1 ? 1 : 2; }
-constexpr int MV_DEPTH = 3;
-__host__ __device__ constexpr int mv_chunk_bytes(int nb) { return mv_tiles(nb) * (16 * MV_ROW + 64); }
-__host__ __device__ constexpr int mv_ring_bytes(int nb) { return MV_WARPS * MV_DEPTH * mv_chunk_bytes(nb); }
-__host__ __device__ constexpr int mv_most_stage(int nb) { return nb == 1 ? 16 : nb == 2 ? 10 : 5; }
+// A warp's unit is 32 rows by 128 of k, one atom of scales wide: each token's
+// values, once loaded, meet two tiles of 16 rows.
+constexpr int MV_TILES = 2, MV_ROWS = 16 * MV_TILES, MV_SPAN = 128;
+// bytes from row to row of a unit's codes: 16 past them, so that 8 rows' words meet 32 banks
+constexpr int MV_ROW = MV_SPAN / 2 + 16, MV_UNIT = MV_ROWS * MV_ROW + 4 * MV_ROWS;
+// NB: tiles of 8 columns of tokens
+// units of a warp's ring: as many as the tokens leave room for
+constexpr int MV_LEAST_DEPTH = 2, MV_MOST_DEPTH = 4;
+__host__ __device__ constexpr int mv_ring_bytes(int nb, int depth) { return mv_warps(nb) * depth * MV_UNIT; }
+__host__ __device__ constexpr int mv_most_stage(int nb) { return nb == 1 ? 16 : nb == 2 ? 10 : 3; }
 // columns are 64 bytes past a multiple of 128 apart: two of them side by side in the banks
-__host__ __device__ constexpr int mv_pitch(int stage) { return stage * MV_CHUNK + 32; }      // halves
+__host__ __device__ constexpr int mv_pitch(int stage) { return stage * MV_SPAN + 32; }      // halves
 // a stage's powers of two, one a group and column, and its columns
 __host__ __device__ constexpr int mv_powers(int columns) { return (columns + 1) & ~1; }
-__host__ __device__ constexpr int mv_stage_bytes(int stage, int columns) { return ((16 * stage * mv_powers(columns) + 15) & ~15) + columns * mv_pitch(stage) * 2; }
+__host__ __device__ constexpr int mv_stage_bytes(int stage, int columns) {
+    return ((16 * stage * mv_powers(columns) + 15) & ~15) + columns * mv_pitch(stage) * 2;
+}
 
 // the values of 8 codes as four pairs of halves
 __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t o[4]) {
@@ -85,12 +94,12 @@ __device__ __forceinline__ void mma_group(float d[4], const uint32_t lo[4], cons
         : "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]), "r"(v.z), "r"(v.w));
 }
 
-// 16 or 4 bytes to shared memory, zeros where there is nothing
-__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" : : "r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+// 16 or 4 bytes to shared memory
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" : : "r"(to), "l"(from) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t to, const void *from, bool there) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" : : "r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
+__device__ __forceinline__ void copy4(uint32_t to, const void *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" : : "r"(to), "l"(from) : "memory");
 }
 
 __device__ __forceinline__ float mv_power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }     // 2^e, normal
@@ -105,106 +114,101 @@ struct Piece<ZS_DTYPE_FP32> {
     uint4 a, b;
 };
 template <int KIND>
-__device__ __forceinline__ Piece<KIND> mv_load(const void *x, int64_t at, int n, bool vec) {
-    Piece<KIND> p;
+__device__ __forceinline__ Piece<KIND> mv_load(const void *x, int64_t at) {
     if constexpr (KIND == ZS_DTYPE_FP32) {
-        const uint32_t *q = static_cast<const uint32_t *>(x) + at;
-        if (vec && n >= 8) {
-            p.a = *reinterpret_cast<const uint4 *>(q);
-            p.b = *reinterpret_cast<const uint4 *>(q + 4);
-        } else {
-            uint32_t v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < n ? q[i] : 0u;
-            p.a = make_uint4(v[0], v[1], v[2], v[3]);
-            p.b = make_uint4(v[4], v[5], v[6], v[7]);
-        }
+        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(x) + at);
+        return {q[0], q[1]};
     } else {
-        const uint16_t *q = static_cast<const uint16_t *>(x) + at;
-        if (vec && n >= 8) {
-            p.a = *reinterpret_cast<const uint4 *>(q);
-        } else {
-            uint32_t v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < n ? (uint32_t)q[i] : 0u;
-            p.a = pack8(v);
-        }
+        return {*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + at)};
     }
-    return p;
+}
+// n of them, at any address
+template <int KIND>
+__device__ __noinline__ Piece<KIND> mv_load_some(const void *x, int64_t at, int n) {
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = i >= n ? 0u : KIND == ZS_DTYPE_FP32 ? static_cast<const uint32_t *>(x)[at + i] : (uint32_t)static_cast<const uint16_t *>(x)[at + i];
+    if constexpr (KIND == ZS_DTYPE_FP32) return {make_uint4(v[0], v[1], v[2], v[3]), make_uint4(v[4], v[5], v[6], v[7])};
+    else return {pack8(v)};
 }
 __device__ __forceinline__ uint32_t half_pair(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// A CTA takes 16 * mv_tiles * warps_n rows of the weight and, of a cluster of
-// S, one S-th of k, whose chunks its warps_k warps of the same rows take in
-// turn.  A warp copies its chunks' codes and scales ahead into a ring of its
+// A CTA takes 32 * warps_n rows of the weight and, of a cluster of
+// S, one S-th of k, whose units its warps_k warps of the same rows take in
+// turn.  A warp copies its units' codes and scales ahead into a ring of its
 // own; all share the tokens, which lie in shared memory as halves: of all the
-// CTA's k where there is room, otherwise for a stage of chunks at a time while
-// the next stage's are on their way to registers.
-// Sums go from the warps to the CTA and from there to the cluster in a fixed
-// order.
+// CTA's k where there is room, otherwise for a stage of units at a time while
+// the next stage's are on their way to registers.  Sums go from the warps to
+// the CTA and from there to the cluster in a fixed order.
 template <int KIND, int NB>
-__global__ void __launch_bounds__(MV_THREADS, NB == 1 ? 2 : 1)
+__global__ void __launch_bounds__(32 * mv_warps(NB))
 mx4_matvec_kernel(MatvecArgs a) {
     constexpr bool HALVES = KIND == ZS_DTYPE_FP16;
-    constexpr int PER = KIND == ZS_DTYPE_FP32 ? 2 : 1, TOKENS = 8 * NB / PER, TILES = mv_tiles(NB), DEPTH = MV_DEPTH, CHUNK = mv_chunk_bytes(NB);
+    constexpr int PER = KIND == ZS_DTYPE_FP32 ? 2 : 1, TOKENS = 8 * NB / PER, TILES = MV_TILES, UNIT = MV_UNIT;
+    constexpr int THREADS = 32 * mv_warps(NB);
+    constexpr int GROUPS = MV_SPAN / MX4_GROUP, SPAN = MV_SPAN, ROW = MV_ROW;
     constexpr int HOLD = KIND == ZS_DTYPE_FP32 ? (MV_PIECES + 1) / 2 : MV_PIECES;
     extern __shared__ __align__(16) uint8_t raw[];
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane >> 2, t = lane & 3;
-    const int wn = warp / a.warps_k, wk = warp % a.warps_k;
-    const bool works = wn < a.warps_n;
-    const int64_t row0 = ((int64_t)(blockIdx.x / ranks) * a.warps_n + wn) * (16 * TILES), token0 = (int64_t)blockIdx.y * TOKENS;
+    const int wn = a.warps_k == 1 ? warp : (int)__umulhi((uint32_t)warp, a.per_warp), wk = warp - wn * a.warps_k;
+    uint32_t block;                                                       // of rows: a cluster's
+    asm("mov.u32 %0, %%clusterid.x;" : "=r"(block));
+    const int64_t row0 = ((int64_t)block * a.warps_n + wn) * MV_ROWS, token0 = (int64_t)blockIdx.y * TOKENS;
     const int tokens = (int)min((int64_t)TOKENS, a.m - token0);
-    const int groups = (int)mx4_groups(a.k), chunks = (groups + 3) / 4, atoms = (int)mx4_atoms(a.k);
-    const int64_t row_bytes = mx4_row_bytes(a.k);
-    const int first = (int)((int64_t)chunks * rank / ranks), last = (int)((int64_t)chunks * (rank + 1) / ranks);
+    const int64_t row_bytes = mx4_row_bytes(a.k), atoms = mx4_atoms(a.k);
+    const int first = rank * a.units, last = min(first + a.units, (int)((mx4_groups(a.k) + GROUPS - 1) / GROUPS));
     const int stage = a.stage, pitch = mv_pitch(stage);
-    const uint32_t ring = smem_u32(raw) + warp * (DEPTH * CHUNK);
-    uint8_t *area = raw + mv_ring_bytes(NB);                              // one or two stages of tokens
+    const int depth = a.depth, around = depth * UNIT;
+    uint8_t *area = raw + mv_ring_bytes(NB, depth);                              // one or two stages of tokens
     const int powers = mv_powers(a.columns), area_bytes = mv_stage_bytes(stage, a.columns), xs_at = area_bytes - a.columns * pitch * 2;
     pdl_wait();
     pdl_trigger();
-    // a warp's chunks: every warps_k-th (a stage is a multiple of them)
-    int ahead = first + wk, slot = 0;                                     // the next chunk to be copied, and its place
-    const int64_t row = row0 + q, scale_row = row0 + lane;                // of the copies: 4 lanes a row
-    const uint8_t *codes = a.codes + row * row_bytes + 64 * (int64_t)ahead + 16 * t;
-    const uint8_t *scales = a.scales + ((scale_row >> 7) * atoms + ahead) * MX4_ATOM + mx4_in_atom((int)(scale_row & 127), 0);
-    const int codes_n = works ? (int)min((int64_t)(16 * TILES), max((int64_t)0, a.n - row0)) : 0;     // rows that there are
-    auto copy = [&] {
-        const uint32_t to = ring + slot * CHUNK;
-        if (ahead < last && codes_n > 0) {
-            const bool inside = 4 * ahead + t < groups;
+    // A warp's units: every warps_k-th (a stage is a multiple of them).  Rows
+    // behind the last one are copies of it, whose sums nobody takes; groups
+    // behind a row's last are copies of that one, and meet zeros of x and the
+    // scales' padding, which is 2^-127.
+    const uint32_t ring = smem_u32(raw) + warp * around, to_codes = ring + q * ROW + 16 * t;     // of the copies: 4 lanes a row
+    int ahead = first + wk, slot = 0;                                     // the next unit to be copied, and its place
+    const uint8_t *codes[4];
 #pragma unroll
-            for (int i = 0; i < 2 * TILES; ++i) {
-                const bool there = inside && q + 8 * i < codes_n;
-                copy16(to + (8 * i + q) * MV_ROW + 16 * t, there ? codes + 8 * i * row_bytes : a.codes, there);
-            }
-            if (lane < 16 * TILES) copy4(to + 16 * TILES * MV_ROW + 4 * lane, lane < codes_n ? scales : a.scales, lane < codes_n);
+    for (int i = 0; i < 4; ++i) codes[i] = a.codes + min(row0 + q + 8 * i, a.n - 1) * row_bytes;
+    const int64_t scale_row = min(row0 + lane, a.n - 1);
+    const uint8_t *scales = a.scales + ((scale_row >> 7) * atoms + ahead) * MX4_ATOM + mx4_in_atom((int)(scale_row & 127), 0);
+    const bool works = wn < a.warps_n && row0 < a.n;
+    const int end = works ? last : 0;
+    auto copy = [&] {
+        if (ahead < end) {
+            const uint32_t at = min(SPAN / 2 * (uint32_t)ahead + 16u * t, (uint32_t)row_bytes - 16u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) copy16(to_codes + slot + 8 * i * ROW, codes[i] + at);
+            copy4(ring + slot + MV_ROWS * ROW + 4 * lane, scales);
         }
         ahead += a.warps_k;
-        codes += 64 * (int64_t)a.warps_k;
-        scales += (int64_t)MX4_ATOM * a.warps_k;
-        slot = slot + 1 == DEPTH ? 0 : slot + 1;
+        scales += MX4_ATOM * a.warps_k;
+        slot = slot + UNIT == around ? 0 : slot + UNIT;
         asm volatile("cp.async.commit_group;" : : : "memory");
     };
-#pragma unroll
-    for (int u = 0; u < DEPTH - 1; ++u) copy();
+    for (int u = 0; u < depth - 1; ++u) copy();
     Piece<KIND> held[HOLD];
-    const int pieces = 16 * stage;                                        // of a token
-    // pieces j0, j0 + 1, .. of this thread in the stage from chunk c0 on
-    auto load = [&](int c0, int j0) {
-        const int64_t k0 = (int64_t)c0 * MV_CHUNK;
+    const int pieces = SPAN / 8 * stage;                                  // of a token
+    // pieces j0, j0 + 1, .. of this thread in the stage from unit u0 on
+    auto load = [&](int u0, int j0) {
+        const int left = (int)min((int64_t)0x7FFFFFFF, a.k - (int64_t)u0 * SPAN);      // of k from there on
+        const int64_t from = token0 * a.ldx + (int64_t)u0 * SPAN;
 #pragma unroll
         for (int j = 0; j < HOLD; ++j) {
-            if (MV_THREADS * (j0 + j) >= tokens * pieces) break;
-            const int p = (int)threadIdx.x + MV_THREADS * (j0 + j), token = (int)__umulhi((uint32_t)p, a.per_token);
-            const int64_t k = k0 + 8 * (p - token * pieces);
-            const int n = token < tokens ? (int)max((int64_t)0, min((int64_t)8, a.k - k)) : 0;
-            held[j] = mv_load<KIND>(a.x, (token0 + token) * a.ldx + k, n, a.vec);
+            if (THREADS * (j0 + j) >= tokens * pieces) break;
+            const int p = (int)threadIdx.x + THREADS * (j0 + j), token = (int)__umulhi((uint32_t)p, a.per_token), at = 8 * (p - token * pieces);
+            held[j] = {};
+            if (token >= tokens || at >= left) continue;
+            if (a.vec) held[j] = mv_load<KIND>(a.x, from + token * a.ldx + at);
+            else held[j] = mv_load_some<KIND>(a.x, from + token * a.ldx + at, left - at);
         }
     };
     auto put = [&](int buffer, int j0) {
@@ -212,25 +216,42 @@ mx4_matvec_kernel(MatvecArgs a) {
         uint8_t *xs = area + buffer * area_bytes + xs_at;
 #pragma unroll
         for (int j = 0; j < HOLD; ++j) {
-            if (MV_THREADS * (j0 + j) >= tokens * pieces) break;
-            const int p = (int)threadIdx.x + MV_THREADS * (j0 + j), token = (int)__umulhi((uint32_t)p, a.per_token), at = p - token * pieces;
+            if (THREADS * (j0 + j) >= tokens * pieces) break;
+            const int p = (int)threadIdx.x + THREADS * (j0 + j), token = (int)__umulhi((uint32_t)p, a.per_token), at = p - token * pieces;
+            uint8_t *to = xs + PER * token * pitch * 2 + 16 * at;
             if constexpr (HALVES) {
-                if (token < tokens) *reinterpret_cast<uint4 *>(xs + token * pitch * 2 + 16 * at) = held[j].a;
+                if (token < tokens) *reinterpret_cast<uint4 *>(to) = held[j].a;
             } else {
+                // the exponent of the largest of 4 lanes' values, bits of the
+                // magnitude; infinities and NaN, which are rare, do not count
                 float v[8];
+                uint32_t top;
                 if constexpr (KIND == ZS_DTYPE_FP32) {
                     const uint32_t u[8] = {held[j].a.x, held[j].a.y, held[j].a.z, held[j].a.w, held[j].b.x, held[j].b.y, held[j].b.z, held[j].b.w};
+                    top = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+                    for (int i = 0; i < 8; ++i) {
+                        v[i] = __uint_as_float(u[i]);
+                        top = max(top, u[i] & 0x7FFFFFFFu);
+                    }
                 } else {
+                    const uint32_t u[4] = {held[j].a.x, held[j].a.y, held[j].a.z, held[j].a.w};
+                    uint32_t two = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = BF16T::to_f32(lane16(held[j].a, i));
+                    for (int i = 0; i < 4; ++i) {
+                        v[2 * i] = __uint_as_float(u[i] << 16);
+                        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+                        two = __vmaxu2(two, u[i] & 0x7FFF7FFFu);
+                    }
+                    top = max(two << 16, two & 0xFFFF0000u);
                 }
-                uint32_t top = 0;                                         // of the finite ones
+                if (__any_sync(0xFFFFFFFFu, top >= 0x7F800000u)) {
+                    top = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-                    top = max(top, b < 0x7F800000u ? b : 0u);
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+                        top = max(top, b < 0x7F800000u ? b : 0u);
+                    }
                 }
                 top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
@@ -241,7 +262,7 @@ mx4_matvec_kernel(MatvecArgs a) {
                     uint32_t h[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) h[i] = half_pair(__fmul_rn(v[2 * i], f), __fmul_rn(v[2 * i + 1], f));
-                    *reinterpret_cast<uint4 *>(xs + PER * token * pitch * 2 + 16 * at) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(h[0], h[1], h[2], h[3]);
                     if constexpr (PER == 2) {                             // what 11 bits left; nothing of an infinity or NaN
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -249,7 +270,7 @@ mx4_matvec_kernel(MatvecArgs a) {
                             const float l0 = __fmul_rn(__fsub_rn(__fmul_rn(v[2 * i], f), w.x), 2048.0f), l1 = __fmul_rn(__fsub_rn(__fmul_rn(v[2 * i + 1], f), w.y), 2048.0f);
                             h[i] = half_pair(fabsf(l0) < 65504.0f ? l0 : 0.0f, fabsf(l1) < 65504.0f ? l1 : 0.0f);
                         }
-                        *reinterpret_cast<uint4 *>(xs + (PER * token + 1) * pitch * 2 + 16 * at) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4 *>(to + pitch * 2) = make_uint4(h[0], h[1], h[2], h[3]);
                     }
                     if ((lane & 3) == 0) {
 #pragma unroll
@@ -259,163 +280,246 @@ mx4_matvec_kernel(MatvecArgs a) {
             }
         }
     };
-    for (int j0 = 0; MV_THREADS * j0 < tokens * pieces; j0 += HOLD) {
-        load(first, j0);
-        put(0, j0);
+    if (HALVES && a.vec) {                                                // as they are: copied
+        const int left = (int)min((int64_t)0x7FFFFFFF, a.k - (int64_t)first * SPAN);
+        const uint16_t *from = static_cast<const uint16_t *>(a.x) + token0 * a.ldx + (int64_t)first * SPAN;
+        // each cluster begins elsewhere: all of them read the same lines
+        const int total = tokens * pieces, turn = (int)(block * (uint32_t)THREADS % (uint32_t)total);
+        for (int i = threadIdx.x; i < total; i += THREADS) {
+            const int p = i + turn < total ? i + turn : i + turn - total;
+            const int token = (int)__umulhi((uint32_t)p, a.per_token), at = p - token * pieces;
+            uint8_t *to = area + xs_at + token * pitch * 2 + 16 * at;
+            if (8 * at < left) copy16(smem_u32(to), from + token * a.ldx + 8 * at);
+            else *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("cp.async.wait_all;" : : : "memory");
+    } else {
+        for (int j0 = 0; THREADS * j0 < tokens * pieces; j0 += HOLD) {
+            load(first, j0);
+            put(0, j0);
+        }
     }
     __syncthreads();
-    float acc[TILES][NB][4] = {};
+    f2 acc[TILES][NB][2];                                                 // pairs of neighbouring columns: rows q and q + 8
+#pragma unroll
+    for (int r = 0; r < TILES; ++r)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[r][b][0] = acc[r][b][1] = 0;
+    // a lane's columns of tokens; where there is none another one, whose sums nobody takes
+    uint32_t column[NB], power[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        column[b] = min(8 * b + q, a.columns - 1) * pitch * 2 + 16 * t;
+        power[b] = 4 * min(8 * b + 2 * t, powers - 2);
+    }
+    const uint8_t *mine = raw + warp * around + q * ROW + 4 * t;  // of a unit's codes
+    const uint8_t *mine_s = raw + warp * around + MV_ROWS * ROW + 4 * q;
     int place = 0;
-    for (int c0 = first, s = 0; c0 < last; c0 += stage, ++s) {
-        if (c0 + stage < last) load(c0 + stage, 0);
-        const float *fe = reinterpret_cast<const float *>(area + (s & 1) * area_bytes);
-        const uint8_t *xs = area + (s & 1) * area_bytes + xs_at;
-        for (int c = wk; c < stage; c += a.warps_k) {                     // in the stage
+    for (int u0 = first, s = 0; u0 < last; u0 += stage, ++s) {
+        if (u0 + stage < last) load(u0 + stage, 0);
+        const uint8_t *fe = area + (s & 1) * area_bytes, *xs = fe + xs_at;
+        for (int u = wk; u < stage; u += a.warps_k) {                     // in the stage
             copy();
-            asm volatile("cp.async.wait_group %0;" : : "n"(DEPTH - 1) : "memory");
+            if (depth == 4) asm volatile("cp.async.wait_group 3;" : : : "memory");
+            else if (depth == 3) asm volatile("cp.async.wait_group 2;" : : : "memory");
+            else asm volatile("cp.async.wait_group 1;" : : : "memory");
             __syncwarp();
-            if (codes_n > 0 && c0 + c < last) {
-                const uint8_t *from = raw + warp * (DEPTH * CHUNK) + place * CHUNK;
+            if (u0 + u < end) {
                 float fs[TILES][2][4];
 #pragma unroll
                 for (int r = 0; r < TILES; ++r) {
-                    scales4(*reinterpret_cast<const uint32_t *>(from + 16 * TILES * MV_ROW + 4 * (16 * r + q)), fs[r][0]);
-                    scales4(*reinterpret_cast<const uint32_t *>(from + 16 * TILES * MV_ROW + 4 * (16 * r + q + 8)), fs[r][1]);
+                    scales4(*reinterpret_cast<const uint32_t *>(mine_s + place + 64 * r), fs[r][0]);
+                    scales4(*reinterpret_cast<const uint32_t *>(mine_s + place + 64 * r + 32), fs[r][1]);
                 }
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < GROUPS; ++g) {
                     uint32_t lo[TILES][4], hi[TILES][4];
 #pragma unroll
                     for (int r = 0; r < TILES; ++r) {
                         uint32_t pa[4], pb[4];
-                        code_pairs(*reinterpret_cast<const uint32_t *>(from + (16 * r + q) * MV_ROW + 16 * g + 4 * t), pa);
-                        code_pairs(*reinterpret_cast<const uint32_t *>(from + (16 * r + q + 8) * MV_ROW + 16 * g + 4 * t), pb);
+                        code_pairs(*reinterpret_cast<const uint32_t *>(mine + place + 16 * r * ROW + 16 * g), pa);
+                        code_pairs(*reinterpret_cast<const uint32_t *>(mine + place + (16 * r + 8) * ROW + 16 * g), pb);
                         lo[r][0] = pa[0]; lo[r][1] = pb[0]; lo[r][2] = pa[1]; lo[r][3] = pb[1];
                         hi[r][0] = pa[2]; hi[r][1] = pb[2]; hi[r][2] = pa[3]; hi[r][3] = pb[3];
                     }
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (8 * b + q < PER * tokens) v = *reinterpret_cast<const uint4 *>(xs + (8 * b + q) * pitch * 2 + 2 * (c * MV_CHUNK + 32 * g + 8 * t));
-                        float2 f = make_float2(1.0f, 1.0f);
-                        if (!HALVES) f = *reinterpret_cast<const float2 *>(fe + (4 * c + g) * powers + 8 * b + 2 * t);
+                        const uint4 v = *reinterpret_cast<const uint4 *>(xs + column[b] + 2 * (u * SPAN + 32 * g));
+                        f2 f = 0;
+                        if (!HALVES) f = *reinterpret_cast<const f2 *>(fe + power[b] + 4 * (GROUPS * u + g) * powers);
 #pragma unroll
                         for (int r = 0; r < TILES; ++r) {
                             float d[4];
                             mma_group(d, lo[r], hi[r], v);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                acc[r][b][j] = __fmaf_rn(HALVES ? d[j] : __fmul_rn(d[j], j & 1 ? f.y : f.x), fs[r][j >> 1][g], acc[r][b][j]);
+                            for (int j = 0; j < 2; ++j) {
+                                f2 two = f2pack(d[2 * j], d[2 * j + 1]);
+                                const f2 scale = f2pack(fs[r][j][g], fs[r][j][g]);
+                                if (!HALVES) asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(two) : "l"(f));
+                                asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[r][b][j]) : "l"(two), "l"(scale));
+                            }
                         }
                     }
                 }
             }
-            place = place + 1 == DEPTH ? 0 : place + 1;
-            __syncwarp();                                                 // the chunk's place may be filled again
+            place = place + UNIT == around ? 0 : place + UNIT;
+            __syncwarp();                                                 // the unit's place may be filled again
         }
-        if (c0 + stage < last) put((s + 1) & 1, 0);
+        if (u0 + stage < last) put((s + 1) & 1, 0);
         __syncthreads();
     }
     asm volatile("cp.async.wait_all;" : : : "memory");
     __syncthreads();
-    // the warps' sums: [warp][column][rows of a warp]
-    constexpr int ROWS = 16 * TILES;
-    float *red = reinterpret_cast<float *>(raw), *share = reinterpret_cast<float *>(area);
+    // The warps' sums: [warp][column][rows of a warp], 36 apart so that a store's
+    // lanes meet 32 banks; then four rows a thread.
+    constexpr int APART = MV_ROWS + 4;
+    float *red = reinterpret_cast<float *>(raw);
+    float4 *share = reinterpret_cast<float4 *>(area);
 #pragma unroll
     for (int r = 0; r < TILES; ++r)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) red[(warp * 8 * NB + 8 * b + 2 * t + (j & 1)) * ROWS + 16 * r + q + 8 * (j >> 1)] = acc[r][b][j];
+            for (int j = 0; j < 2; ++j) {
+                float *to = red + (warp * 8 * NB + 8 * b + 2 * t) * APART + 16 * r + q + 8 * j;
+                f2unpack(acc[r][b][j], to[0], to[APART]);
+            }
     __syncthreads();
-    const int rows = ROWS * a.warps_n;
-    for (int i = threadIdx.x; i < tokens * rows; i += MV_THREADS) {
-        const int token = (int)__umulhi((uint32_t)i, a.per_row), r = i - token * rows;
-        float s[PER];
-#pragma unroll
-        for (int p = 0; p < PER; ++p) {
-            s[p] = 0.0f;
-            for (int w = 0; w < a.warps_k; ++w)
-                s[p] = __fadd_rn(s[p], red[((r / ROWS * a.warps_k + w) * 8 * NB + PER * token + p) * ROWS + r % ROWS]);
+    const int rows4 = MV_ROWS / 4 * a.warps_n, values4 = tokens * rows4;
+    const int64_t block0 = (int64_t)block * (4 * rows4);
+    auto add = [](float4 x, float4 y) { return make_float4(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y), __fadd_rn(x.z, y.z), __fadd_rn(x.w, y.w)); };
+    auto write = [&](int token, int r, float4 v) {
+        const int64_t o = block0 + 4 * r, at = (token0 + token) * a.ldo + o;
+        const float s[4] = {v.x, v.y, v.z, v.w};
+        const bool all = a.vec_out && o + 4 <= a.n;
+        if (a.out_kind == ZS_DTYPE_FP32) {
+            float *to = static_cast<float *>(a.out) + at;
+            if (all) *reinterpret_cast<float4 *>(to) = v;
+            else
+                for (int j = 0; j < 4; ++j) if (o + j < a.n) to[j] = s[j];
+            return;
         }
-        share[i] = PER == 2 ? __fadd_rn(s[0], s[PER - 1]) : s[0];
+        uint16_t *to = static_cast<uint16_t *>(a.out) + at;
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = a.out_kind == ZS_DTYPE_FP16 ? FP16T::from_f32(s[j]) : BF16T::from_f32(s[j]);
+        if (all) *reinterpret_cast<uint2 *>(to) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+        else
+            for (int j = 0; j < 4; ++j) if (o + j < a.n) to[j] = (uint16_t)h[j];
+    };
+    for (int i = threadIdx.x; i < values4; i += THREADS) {
+        const int token = (int)__umulhi((uint32_t)i, a.per_row), r = i - token * rows4;
+        const float *from = red + ((r >> 3) * a.warps_k * 8 * NB + PER * token) * APART + 4 * (r & 7);
+        float4 s[PER];
+#pragma unroll
+        for (int p = 0; p < PER; ++p) s[p] = *reinterpret_cast<const float4 *>(from + p * APART);
+#pragma unroll 4
+        for (int w = 1; w < a.warps_k; ++w)
+#pragma unroll
+            for (int p = 0; p < PER; ++p) s[p] = add(s[p], *reinterpret_cast<const float4 *>(from + (w * 8 * NB + p) * APART));
+        const float4 v = PER == 2 ? add(s[0], s[PER - 1]) : s[0];
+        if (ranks == 1) write(token, r, v);
+        else share[i] = v;
     }
-    if (ranks > 1) cluster.sync();
-    else __syncthreads();
-    const int64_t block0 = (int64_t)(blockIdx.x / ranks) * rows;
-    for (int i = rank * MV_THREADS + threadIdx.x; i < tokens * rows; i += MV_THREADS * ranks) {
-        float s = share[i];
-        if (ranks > 1) {
-            s = 0.0f;
-            for (int r = 0; r < ranks; ++r) s = __fadd_rn(s, cluster.map_shared_rank(share, r)[i]);
+    if (ranks == 1) return;
+    cluster.sync();
+    for (int i = rank * THREADS + threadIdx.x; i < values4; i += THREADS * ranks) {
+        float4 v[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            if (r >= ranks) break;
+            v[r] = cluster.map_shared_rank(share, r)[i];
+        }
+#pragma unroll
+        for (int r = 1; r < 8; ++r) {
+            if (r >= ranks) break;
+            v[0] = add(v[0], v[r]);
         }
         const int token = (int)__umulhi((uint32_t)i, a.per_row);
-        const int64_t o = block0 + i - token * rows, at = (token0 + token) * a.ldo + o;
-        if (o >= a.n) continue;
-        if (a.out_kind == ZS_DTYPE_FP32) static_cast<float *>(a.out)[at] = s;
-        else static_cast<uint16_t *>(a.out)[at] = (uint16_t)(a.out_kind == ZS_DTYPE_FP16 ? FP16T::from_f32(s) : BF16T::from_f32(s));
+        write(token, i - token * rows4, v[0]);
     }
-    if (ranks > 1) cluster.sync();   // the others may still read this CTA's sums
+    cluster.sync();                  // the others may still read this CTA's sums
 }
 
 template <int KIND, int NB>
 static cudaError_t matvec_launch(MatvecArgs a, cudaStream_t s) {
-    static std::atomic<bool> set[64];
     constexpr int PER = KIND == ZS_DTYPE_FP32 ? 2 : 1, TOKENS = 8 * NB / PER;
-    constexpr int ROOM = 227 * 1024 - mv_ring_bytes(NB);                 // of tokens, a CTA alone on its SM
+    constexpr int ROOM = 227 * 1024 - mv_ring_bytes(NB, MV_LEAST_DEPTH), THREADS = 32 * mv_warps(NB);      // of tokens
     static_assert(2 * mv_stage_bytes(mv_most_stage(NB), 8 * NB) <= ROOM, "shared memory");
+    static_assert(8 * NB * 16 * mv_most_stage(NB) <= MV_PIECES * THREADS, "pieces");
+    static std::atomic<int> seats[64][9];        // CTAs in clusters of S that the device has room for at once
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!set[dev].load(std::memory_order_relaxed)) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(THREADS);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    if (!seats[dev][8].load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(mx4_matvec_kernel<KIND, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+        for (int sp = 1; sp <= 8 && e == cudaSuccess; ++sp) {
+            int clusters = 0;
+            attr[0].val.clusterDim.x = (unsigned)sp;
+            cfg.gridDim = dim3((unsigned)sp);
+            cfg.dynamicSmemBytes = 227 * 1024;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&clusters, mx4_matvec_kernel<KIND, NB>, &cfg);
+            seats[dev][sp].store(clusters > 0 ? clusters * sp : sp, std::memory_order_release);
+        }
         if (e != cudaSuccess) return e;
-        set[dev].store(true, std::memory_order_relaxed);
     }
-    const int64_t ty = (a.m + TOKENS - 1) / TOKENS, tiles = (a.n + 16 * mv_tiles(NB) - 1) / (16 * mv_tiles(NB));
-    const int64_t chunks = (mx4_groups(a.k) + 3) / 4;
-    // How warps and CTAs share rows and k.  In units of about 100 cycles: a step
-    // of an SM's 16 warps 5 where instructions bound it, and 2 of latency; a
-    // CTA's beginning and end 15 (tokens to halves, the sums), an exchange 4.
+    const int ty = (int)((a.m + TOKENS - 1) / TOKENS), tiles = (int)((a.n + MV_ROWS - 1) / MV_ROWS), units = (int)((mx4_groups(a.k) + 3) / 4);
+    a.columns = (int)(a.m < TOKENS ? a.m : TOKENS) * PER;
+    auto fits = [&](int whole) { return whole <= 512 && mv_stage_bytes(whole, a.columns) <= ROOM; };
+    // How warps and CTAs share rows and k, by the time that an SM takes, in ns as
+    // measured: a step (a unit of each warp) 54, 75 or 130 a warp, and 450 at
+    // least; a CTA's beginning and end 2000, with 280 for each 8 values of tokens
+    // a thread, an exchange 700.
+    constexpr int STEP = NB == 1 ? 54 : NB == 2 ? 75 : 130, MOST_WARPS = mv_warps(NB);
     int64_t best = -1;
     int split = 1;
-    for (int wk = 1; wk <= mv_most_stage(NB); ++wk) {
-        if (wk > 1 && wk > chunks) break;
-        const int64_t wn = tiles < MV_WARPS / wk ? tiles : MV_WARPS / wk, blocks = (tiles + wn - 1) / wn * ty;
-        for (int sp = 1; sp <= 8 && (sp == 1 || chunks >= (int64_t)sp * wk); ++sp) {
-            const int64_t steps = ((chunks + sp - 1) / sp + wk - 1) / wk, cost = (blocks * sp + 151) / 152 * (5 * steps + 15) + 2 * steps + (sp > 1 ? 4 : 0);
+    for (const int wk : {1, 2, 3, 4, 6, 8, 12, 16}) {
+        if (wk > MOST_WARPS || (wk > 1 && wk > units)) break;
+        const int most_n = tiles < MOST_WARPS / wk ? tiles : MOST_WARPS / wk, blocks = (tiles + most_n - 1) / most_n, wn = (tiles + blocks - 1) / blocks;
+        for (const int sp : {1, 2, 3, 4, 6, 8}) {
+            if (sp > 1 && units < sp * wk) break;
+            const int slice = (units + sp - 1) / sp, steps = (slice + wk - 1) / wk, room = seats[dev][sp].load(std::memory_order_relaxed);
+            const bool once = fits(steps * wk);
+            if (slice * (sp - 1) >= units || (!once && wk > mv_most_stage(NB))) continue;
+            const int step = wn * wk * STEP, pieces = a.columns / PER * steps * wk * 16 / THREADS;
+            const int64_t one = 2000 + (int64_t)steps * (step > 450 ? step : 450) + 280 * pieces + (once ? 0 : 500) + (sp > 1 ? 700 : 0);
+            const int64_t cost = ((int64_t)blocks * ty * sp + room - 1) / room * one;
             if (best >= 0 && cost >= best) continue;
             best = cost;
             a.warps_k = wk;
-            a.warps_n = (int)wn;
+            a.warps_n = wn;
             split = sp;
         }
     }
-    a.columns = (int)(a.m < TOKENS ? a.m : TOKENS) * PER;
-    const int64_t whole = ((chunks + split - 1) / split + a.warps_k - 1) / a.warps_k * a.warps_k;
-    const bool fits = whole <= 1024 && mv_stage_bytes((int)whole, a.columns) <= (NB == 1 ? 113 * 1024 - mv_ring_bytes(NB) : ROOM);     // two CTAs an SM, one
-    a.stage = fits ? (int)whole : mv_most_stage(NB) / a.warps_k * a.warps_k;
+    a.units = (units + split - 1) / split;
+    const int whole = (a.units + a.warps_k - 1) / a.warps_k * a.warps_k;
+    const bool once = fits(whole);
+    a.stage = once ? whole : mv_most_stage(NB) / a.warps_k * a.warps_k;
     // exact for the numbers below 2^16 that are divided
     a.per_token = (uint32_t)(((uint64_t)1 << 32) / (16 * a.stage) + 1);
-    a.per_row = (uint32_t)(((uint64_t)1 << 32) / (16 * mv_tiles(NB) * a.warps_n) + 1);
-    const int64_t grid = (tiles + a.warps_n - 1) / a.warps_n * split;
+    a.per_row = (uint32_t)(((uint64_t)1 << 32) / (MV_ROWS / 4 * a.warps_n) + 1);
+    a.per_warp = (uint32_t)(((uint64_t)1 << 32) / a.warps_k + 1);
+    const int64_t grid = (int64_t)((tiles + a.warps_n - 1) / a.warps_n) * split;
     if (grid > 0x7FFFFFFF || ty > 65535) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, (unsigned)ty);
-    cfg.blockDim = dim3(MV_THREADS);
-    cfg.dynamicSmemBytes = mv_ring_bytes(NB) + (fits ? 1 : 2) * mv_stage_bytes(a.stage, a.columns);
-    const int share = 16 * mv_tiles(NB) * a.warps_n * (a.columns / PER) * 4;     // the CTA's sums, in the tokens' place
-    if ((int)cfg.dynamicSmemBytes < mv_ring_bytes(NB) + share) cfg.dynamicSmemBytes = mv_ring_bytes(NB) + share;
+    const int room = (once ? 1 : 2) * mv_stage_bytes(a.stage, a.columns);
+    const int share = MV_ROWS * a.warps_n * (a.columns / PER) * 4;     // the CTA's sums, in the tokens' place
+    const int left = 227 * 1024 - (room > share ? room : share);
+    a.depth = left / mv_ring_bytes(NB, 1) < MV_MOST_DEPTH ? left / mv_ring_bytes(NB, 1) : MV_MOST_DEPTH;
+    cfg.dynamicSmemBytes = mv_ring_bytes(NB, a.depth) + (room > share ? room : share);
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)split;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 2 : 1;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, mx4_matvec_kernel<KIND, NB>, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -455,7 +559,8 @@ extern "C" zs_status zs_mx4_matvec(int64_t m, int64_t n, int64_t k, const void *
         zsk::MatvecArgs a;
         a.x = x; a.codes = static_cast<const uint8_t *>(w_codes); a.scales = static_cast<const uint8_t *>(w_scales); a.out = out;
         a.m = m; a.n = n; a.k = k; a.ldx = ldx; a.ldo = ldo; a.out_kind = out_dtype;
-        a.vec = addr(x) % 16 == 0 && (m == 1 || ldx * size(dtype) % 16 == 0);
+        a.vec_out = addr(out) % 16 == 0 && (m == 1 || ldo * size(out_dtype) % 16 == 0);
+        a.vec = addr(x) % 16 == 0 && k % 8 == 0 && (m == 1 || ldx * size(dtype) % 16 == 0);
         e = dtype == ZS_DTYPE_FP32 ? zsk::matvec_of<ZS_DTYPE_FP32>(a, s)
           : dtype == ZS_DTYPE_FP16 ? zsk::matvec_of<ZS_DTYPE_FP16>(a, s) : zsk::matvec_of<ZS_DTYPE_BF16>(a, s);
     }
