@@ -31,56 +31,74 @@ __device__ __forceinline__ bool finite_f32(float x) { return (__float_as_uint(x)
 
 // ------------------------------------------------------ 8 values a lane --
 
+template <class T>
+__device__ __forceinline__ void max_two(uint32_t &m, uint32_t w);        // the larger magnitudes of two pairs; a NaN stays
+template <>
+__device__ __forceinline__ void max_two<BF16T>(uint32_t &m, uint32_t w) {
+    asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %1;\n\tmax.NaN.bf16x2 %0, %0, a;\n\t}" : "+r"(m) : "r"(w));
+}
+template <>
+__device__ __forceinline__ void max_two<FP16T>(uint32_t &m, uint32_t w) {
+    asm("{\n\t.reg .b32 a;\n\tabs.f16x2 a, %1;\n\tmax.NaN.f16x2 %0, %0, a;\n\t}" : "+r"(m) : "r"(w));
+}
+__device__ __forceinline__ void max_abs3(float &m, float a, float b) {
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(a)), "f"(fabsf(b)));
+}
+
+// Raw: 8 elements of a lane as they lie in memory.
 struct RowF32 {
     static constexpr int SIZE = 4;
-    struct Raw { uint4 a, b; };
-    static __device__ __forceinline__ Raw load(const void *p, int64_t at) {
-        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + at);
-        return {q[0], q[1]};
-    }
-    static __device__ __forceinline__ Raw some(const void *p, int64_t at, int n) {
-        uint32_t v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? static_cast<const uint32_t *>(p)[at + i] : 0u;
-        return {make_uint4(v[0], v[1], v[2], v[3]), make_uint4(v[4], v[5], v[6], v[7])};
-    }
+    typedef uint32_t Elem;
+    struct __align__(16) Raw { uint4 a, b; };
+    static __device__ __forceinline__ Raw zero() { return {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}; }
+    static __device__ __forceinline__ Raw of(const uint32_t v[8]) { return {make_uint4(v[0], v[1], v[2], v[3]), make_uint4(v[4], v[5], v[6], v[7])}; }
     static __device__ __forceinline__ void floats(const Raw &r, float o[8]) {
         const uint32_t v[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(v[i]);
     }
     static __device__ __forceinline__ Raw rounded(const float o[8]) {
-        return {make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3])),
-                make_uint4(__float_as_uint(o[4]), __float_as_uint(o[5]), __float_as_uint(o[6]), __float_as_uint(o[7]))};
-    }
-    static __device__ __forceinline__ void store(void *p, int64_t at, int n, bool vec, const Raw &r) {
-        if (vec && n == 8) {
-            uint4 *q = reinterpret_cast<uint4 *>(static_cast<float *>(p) + at);
-            q[0] = r.a;
-            q[1] = r.b;
-            return;
-        }
-        const uint32_t v[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+        uint32_t v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) if (i < n) static_cast<uint32_t *>(p)[at + i] = v[i];
+        for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(o[i]);
+        return of(v);
+    }
+    static __device__ __forceinline__ Elem element(const Raw &r, int i) {
+        const uint4 &q = i < 4 ? r.a : r.b;
+        return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+    }
+    // the largest magnitude of the four neighbouring lanes' values
+    static __device__ __forceinline__ float top4(const Raw &r) {
+        float v[8], top = 0.0f;
+        floats(r, v);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) max_abs3(top, v[i], v[i + 1]);
+        max_abs3(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1), 0.0f);
+        max_abs3(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2), 0.0f);
+        return top;
     }
 };
 template <class T, bool FP16>
 struct Row16 {
     static constexpr int SIZE = 2;
+    typedef uint16_t Elem;
+    typedef T Type;
     typedef uint4 Raw;
-    static __device__ __forceinline__ Raw load(const void *p, int64_t at) {
-        return *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at);
-    }
-    static __device__ __forceinline__ Raw some(const void *p, int64_t at, int n) {
-        uint32_t v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? (uint32_t)static_cast<const uint16_t *>(p)[at + i] : 0u;
-        return pack8(v);
-    }
+    static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
+    static __device__ __forceinline__ Raw of(const uint32_t v[8]) { return pack8(v); }
     static __device__ __forceinline__ void floats(const Raw &r, float o[8]) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = T::to_f32(lane16(r, i));
+        for (int i = 0; i < 4; ++i) {
+            if (FP16) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                o[2 * i] = f.x;
+                o[2 * i + 1] = f.y;
+            } else {
+                o[2 * i] = __uint_as_float(w[i] << 16);
+                o[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
     }
     static __device__ __forceinline__ Raw rounded(const float o[8]) {
         uint32_t r[4];
@@ -96,34 +114,92 @@ struct Row16 {
         }
         return make_uint4(r[0], r[1], r[2], r[3]);
     }
-    static __device__ __forceinline__ void store(void *p, int64_t at, int n, bool vec, const Raw &r) {
-        uint16_t *q = static_cast<uint16_t *>(p) + at;
-        if (vec && n == 8) {
-            *reinterpret_cast<uint4 *>(q) = r;
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) if (i < n) q[i] = (uint16_t)lane16(r, i);
+    static __device__ __forceinline__ Elem element(const Raw &r, int i) { return (Elem)lane16(r, i); }
+    static __device__ __forceinline__ float top4(const Raw &r) {
+        uint32_t m = 0;
+        max_two<T>(m, r.x);
+        max_two<T>(m, r.y);
+        max_two<T>(m, r.z);
+        max_two<T>(m, r.w);
+        max_two<T>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        max_two<T>(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        return T::to_f32(max(m & 0xFFFFu, m >> 16));
     }
 };
 typedef Row16<BF16T, false> RowBF16;
 typedef Row16<FP16T, true> RowFP16;
 
+// A lane's 8 of a block of 256 columns, `there` of which exist (any integer).
+// vec: the row is 16-byte aligned.  Otherwise lanes load neighbouring elements,
+// which turn (256 elements of the warp's shared memory) deals out: 8 loads of 2
+// or 4 bytes a lane instead of 8 that each meet another sector.
 template <class R>
-__device__ __forceinline__ typename R::Raw fetch8(const void *p, int64_t at, int n, bool vec) {
-    return vec && n == 8 ? R::load(p, at) : R::some(p, at, n);
+__device__ __forceinline__ typename R::Raw block_load(const void *p, int64_t at, int there, bool vec, typename R::Elem *turn) {
+    const int lane = threadIdx.x & 31, n = there - 8 * lane;
+    const typename R::Elem *q = static_cast<const typename R::Elem *>(p) + at;
+    if (vec && n >= 8) return *reinterpret_cast<const typename R::Raw *>(q + 8 * lane);
+    if (vec) {
+        if (n <= 0) return R::zero();
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? (uint32_t)q[8 * lane + i] : 0u;
+        return R::of(v);
+    }
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 32 * i + lane < there ? (uint32_t)q[32 * i + lane] : 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn[32 * i + lane] = (typename R::Elem)v[i];
+    __syncwarp();
+    const typename R::Raw r = *reinterpret_cast<const typename R::Raw *>(turn + 8 * lane);
+    __syncwarp();
+    return r;
+}
+template <class R>
+__device__ __forceinline__ void block_store(void *p, int64_t at, int there, bool vec, typename R::Elem *turn, const typename R::Raw &r) {
+    const int lane = threadIdx.x & 31, n = there - 8 * lane;
+    typename R::Elem *q = static_cast<typename R::Elem *>(p) + at;
+    if (vec) {
+        if (n >= 8) *reinterpret_cast<typename R::Raw *>(q + 8 * lane) = r;
+        else
+#pragma unroll
+            for (int i = 0; i < 8; ++i) if (i < n) q[8 * lane + i] = R::element(r, i);
+        return;
+    }
+    *reinterpret_cast<typename R::Raw *>(turn + 8 * lane) = r;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) if (32 * i + lane < there) q[32 * i + lane] = turn[32 * i + lane];
+    __syncwarp();
 }
 
-// n of 8 weights of any type
-__device__ __forceinline__ void weights8(const void *w, int kind, int64_t at, int n, bool vec, float o[8]) {
-    if (kind == ZS_DTYPE_FP32) RowF32::floats(fetch8<RowF32>(w, at, n, vec), o);
-    else if (kind == ZS_DTYPE_FP16) RowFP16::floats(fetch8<RowFP16>(w, at, n, vec), o);
-    else RowBF16::floats(fetch8<RowBF16>(w, at, n, vec), o);
+// 8 weights of any type from column `at` on, n of which exist
+__device__ __forceinline__ void weights8(const void *w, int kind, bool vec, int64_t at, int n, float o[8]) {
+    if (kind == ZS_DTYPE_FP32) {
+        const float *q = static_cast<const float *>(w) + at;
+        if (vec && n >= 8) RowF32::floats(*reinterpret_cast<const RowF32::Raw *>(q), o);
+        else
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = i < n ? q[i] : 0.0f;
+        return;
+    }
+    const uint16_t *q = static_cast<const uint16_t *>(w) + at;
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0;
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (vec && n >= 8) r = *reinterpret_cast<const uint4 *>(q);
+    else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? (uint32_t)q[i] : 0u;
+        r = pack8(v);
+    }
+    if (kind == ZS_DTYPE_FP16) RowFP16::floats(r, o);
+    else RowBF16::floats(r, o);
 }
 
-__device__ __forceinline__ int part(int64_t cols, int64_t at) {      // of 8 columns from `at` on, how many there are
-    return (int)max((int64_t)0, min((int64_t)8, cols - at));
-}
+// of the 256 columns from `at` on, how many exist (0 and less: none)
+__device__ __forceinline__ int part(int64_t cols, int64_t at) { return (int)max((int64_t)-1, min((int64_t)256, cols - at)); }
 
 // ------------------------------------------------------- sums of a row --
 
@@ -165,9 +241,25 @@ struct Dot {
     }
 };
 
-__device__ __forceinline__ void max_abs3(float &m, float a, float b) {
-    asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmax.NaN.f32 %0, %0, t;\n\t}" : "+f"(m) : "f"(fabsf(a)), "f"(fabsf(b)));
+// Paired products and sums.  A paired sum of a paired product would be fused
+// with it in spite of both roundings, so such a sum is written as a product with
+// a 1 that the compiler does not know, plus the other.
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 both(float x) { return f2pack(x, x); }
 
 // A row's pair over the lanes of a warp; the same in all of them.
 __device__ __forceinline__ void warp_pair(float &hi, float &lo) {
@@ -175,6 +267,32 @@ __device__ __forceinline__ void warp_pair(float &hi, float &lo) {
     for (int off = 16; off > 0; off >>= 1) {
         const float h2 = __shfl_xor_sync(0xFFFFFFFFu, hi, off), l2 = __shfl_xor_sync(0xFFFFFFFFu, lo, off);
         add22(hi, lo, h2, l2);
+    }
+}
+// The pairs of four rows at once: halves of the warp keep two rows each, then
+// quarters one; afterwards lane l has row l / 8.
+__device__ __forceinline__ void warp_pair4(float (&hi)[4], float (&lo)[4]) {
+    const int lane = threadIdx.x & 31;
+    const bool up = lane & 16, odd = lane & 8;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float h = __shfl_xor_sync(0xFFFFFFFFu, up ? hi[k] : hi[2 + k], 16), l = __shfl_xor_sync(0xFFFFFFFFu, up ? lo[k] : lo[2 + k], 16);
+        if (up) {
+            hi[k] = hi[2 + k];
+            lo[k] = lo[2 + k];
+        }
+        add22(hi[k], lo[k], h, l);
+    }
+    const float h = __shfl_xor_sync(0xFFFFFFFFu, odd ? hi[0] : hi[1], 8), l = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo[0] : lo[1], 8);
+    if (odd) {
+        hi[0] = hi[1];
+        lo[0] = lo[1];
+    }
+    add22(hi[0], lo[0], h, l);
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) {
+        const float h2 = __shfl_xor_sync(0xFFFFFFFFu, hi[0], off), l2 = __shfl_xor_sync(0xFFFFFFFFu, lo[0], off);
+        add22(hi[0], lo[0], h2, l2);
     }
 }
 __device__ __forceinline__ double warp_double(double v) {
@@ -231,46 +349,41 @@ struct NormHeld {
     int64_t rows, cols;
 };
 
+// codes of 8 values times inv
+__device__ __forceinline__ uint32_t encode8(const float v[8], float inv) {
+    float y[8];
+    const f2 two = both(inv);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) f2unpack(mul2(f2pack(v[i], v[i + 1]), two), y[i], y[i + 1]);
+    return e2m1x8(y);
+}
+
 // 8 values a lane, 4 neighbouring lanes a group along the row; y is 0 past the
 // matrix.  `row` may lie past the matrix, in the tile of scales that holds it.
-__device__ __forceinline__ void hold_rows(const NormHeld &h, int64_t row, int64_t col, const float v[8]) {
-    float top = 0.0f, y[8];
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) max_abs3(top, v[i], v[i + 1]);
-#pragma unroll
-    for (int off = 1; off < 4; off <<= 1) {
-        const float o = __shfl_xor_sync(0xFFFFFFFFu, top, off);
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(o));
-    }
-    const uint32_t byte = mx4_scale_byte(__float_as_uint(top) >> 23);
-    const float inv = byte == 255u ? 0.0f : mx4_inverse(byte);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(v[i], inv);
-    const uint32_t word = byte == 255u ? 0u : e2m1x8(y);
+template <class R>
+__device__ __forceinline__ void hold_rows(const NormHeld &h, int64_t row, int64_t col, const typename R::Raw &y) {
+    const uint32_t byte = mx4_scale_byte(__float_as_uint(R::top4(y)) >> 23);
+    float v[8];
+    R::floats(y, v);
+    const uint32_t word = byte == 255u ? 0u : encode8(v, byte == 255u ? 0.0f : mx4_inverse(byte));
     const int64_t g = col / MX4_GROUP;
     if (row < h.rows && g < mx4_groups(h.cols))
         *reinterpret_cast<uint32_t *>(h.r_codes + row * mx4_row_bytes(h.cols) + col / 2) = word;
-    if ((threadIdx.x & 3) == 0 && row < 128 * mx4_row_tiles(h.rows) && g < 4 * mx4_atoms(h.cols))
-        h.r_scales[((row >> 7) * mx4_atoms(h.cols) + (g >> 2)) * MX4_ATOM + mx4_in_atom((int)(row & 127), (int)(g & 3))] = (uint8_t)byte;
+    // the scales of a row's four groups lie side by side: one lane writes them
+    uint32_t four = byte << (8 * (g & 3));
+    four |= __shfl_xor_sync(0xFFFFFFFFu, four, 4);
+    four |= __shfl_xor_sync(0xFFFFFFFFu, four, 8);
+    if ((threadIdx.x & 15) == 0 && row < 128 * mx4_row_tiles(h.rows) && g < 4 * mx4_atoms(h.cols))
+        *reinterpret_cast<uint32_t *>(h.r_scales + ((row >> 7) * mx4_atoms(h.cols) + (g >> 2)) * MX4_ATOM + mx4_in_atom((int)(row & 127), 0)) = four;
 }
 
-// The 32 rows from 32 * g on of one column, in shared memory `pitch` floats apart.
-__device__ __forceinline__ void hold_column(const NormHeld &h, int64_t g, int64_t col, const float *from, int pitch) {
-    float v[32], top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = from[i * pitch];
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) max_abs3(top, v[i], v[i + 1]);
+// 32 values of one column: the rows from 32 g on
+__device__ __forceinline__ void hold_column(const NormHeld &h, int64_t g, int64_t col, float top, const float v[32]) {
     const uint32_t byte = mx4_scale_byte(__float_as_uint(top) >> 23);
     const float inv = byte == 255u ? 0.0f : mx4_inverse(byte);
     uint32_t q[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(v[8 * j + i], inv);
-        q[j] = byte == 255u ? 0u : e2m1x8(y);
-    }
+    for (int j = 0; j < 4; ++j) q[j] = byte == 255u ? 0u : encode8(v + 8 * j, inv);
     if (col < h.cols && g < mx4_groups(h.rows))
         *reinterpret_cast<uint4 *>(h.c_codes + col * mx4_row_bytes(h.rows) + 16 * g) = make_uint4(q[0], q[1], q[2], q[3]);
     if (col < 128 * mx4_row_tiles(h.cols) && g < 4 * mx4_atoms(h.rows))
@@ -285,7 +398,7 @@ struct NormArgs {
     float *rstd;
     int64_t ldx, ldr, lds, ldo;
     int32_t w_kind;
-    bool vec;                        // every matrix has 16-byte aligned rows
+    bool vec, vec_w;                 // every matrix has 16-byte aligned rows; so does the weight
     float eps;
     Mean mean;
     NormHeld held;
@@ -300,19 +413,21 @@ rms_rows_kernel(NormArgs a) {
     constexpr int ROWS = WARPS / WPR, KEEP = NB > 0 ? NB : 1;
     __shared__ float2 parts[WARPS];
     __shared__ double wides[WARPS];
+    __shared__ __align__(16) typename R::Elem turns[WARPS][256];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % WPR;
     const int64_t rows = a.held.rows, cols = a.held.cols, row = (int64_t)blockIdx.x * ROWS + warp / WPR;
     const int blocks = NB > 0 ? NB : (int)((cols + 256 * WPR - 1) / (256 * WPR));
     const bool there = row < rows;
+    typename R::Elem *turn = turns[warp];
     pdl_wait();
     pdl_trigger();
     auto input = [&](int b, float h[8]) {
-        const int64_t c = 256 * (int64_t)(mine + WPR * b) + 8 * lane;
+        const int64_t c = 256 * (int64_t)(mine + WPR * b);
         const int n = there ? part(cols, c) : 0;
-        R::floats(fetch8<R>(a.x, row * a.ldx + c, n, a.vec), h);
+        R::floats(block_load<R>(a.x, row * a.ldx + c, n, a.vec, turn), h);
         if (!a.residual) return;
         float r[8];
-        R::floats(fetch8<R>(a.residual, row * a.ldr + c, n, a.vec), r);
+        R::floats(block_load<R>(a.residual, row * a.ldr + c, n, a.vec, turn), r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = __fadd_rn(h[i], r[i]);
     };
@@ -378,7 +493,7 @@ rms_rows_kernel(NormArgs a) {
     if (there && mine == 0 && lane == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int b = 0; b < blocks; ++b) {
-        const int64_t c = 256 * (int64_t)(mine + WPR * b) + 8 * lane;
+        const int64_t c = 256 * (int64_t)(mine + WPR * b);
         const int n = there ? part(cols, c) : 0;
         float v[8], w[8];
         if constexpr (NB > 0) {
@@ -387,18 +502,13 @@ rms_rows_kernel(NormArgs a) {
         } else {
             input(b, v);
         }
-        if (a.sum) R::store(a.sum, row * a.lds + c, n, a.vec, R::rounded(v));
-        weights8(a.w, a.w_kind, c, n, a.vec, w);
+        if (a.sum) block_store<R>(a.sum, row * a.lds + c, n, a.vec, turn, R::rounded(v));
+        weights8(a.w, a.w_kind, a.vec_w, c + 8 * lane, n - 8 * lane, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], rstd), w[i]);
+        for (int i = 0; i < 8; ++i) v[i] = 8 * lane + i < n ? __fmul_rn(__fmul_rn(v[i], rstd), w[i]) : 0.0f;
         const typename R::Raw y = R::rounded(v);
-        if (a.out) R::store(a.out, row * a.ldo + c, n, a.vec, y);
-        if (a.held.r_codes) {
-            R::floats(y, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) if (i >= n) v[i] = 0.0f;
-            hold_rows(a.held, row, c, v);
-        }
+        if (a.out) block_store<R>(a.out, row * a.ldo + c, n, a.vec, turn, y);
+        if (a.held.r_codes) hold_rows<R>(a.held, row, c + 8 * lane, y);
     }
 }
 
@@ -408,11 +518,54 @@ constexpr int TILE_ROWS = 32;
 constexpr int TILE_COLS = 512;       // of 8 warps; K times as many of a CTA
 constexpr int tile_smem(int k) { return TILE_ROWS * TILE_COLS * k * 4; }
 constexpr int64_t TILE_MOST = 8 * 3 * TILE_COLS;     // columns that a cluster holds
+constexpr int ROWS_EACH = TILE_ROWS / WARPS;         // rows of a warp, 512 columns of each
 
-// Place of 8 columns from 8 * lane on in a block of 256 floats: pieces of four
-// side by side over the lanes, so that no two lanes meet in a bank.
-__device__ __forceinline__ float4 *piece(float *block, int lane, int half) { return reinterpret_cast<float4 *>(block + 128 * half + 4 * lane); }
-__device__ __forceinline__ int column_at(int place) {        // the column of a place, in its block of 256
+__device__ __forceinline__ void async16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" : : "r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void async_wait(int pending) {            // for all but the last `pending` groups; a constant where it is inlined
+    if (pending >= 3) asm volatile("cp.async.wait_group 3;" : : : "memory");
+    else if (pending == 2) asm volatile("cp.async.wait_group 2;" : : : "memory");
+    else if (pending == 1) asm volatile("cp.async.wait_group 1;" : : : "memory");
+    else asm volatile("cp.async.wait_group 0;" : : : "memory");
+}
+
+// A row of a tile in shared memory, 16 bits: as it is, a lane's 8 side by side;
+// 32 bits: in each block of 256 pieces of four side by side over the lanes, so
+// that no two lanes of a load meet in a bank.
+template <class R>
+struct TileRow {
+    typename R::Elem *at;            // of a block of 256 columns
+    __device__ __forceinline__ uint4 *piece(int lane, int half) const {
+        return reinterpret_cast<uint4 *>(at + (R::SIZE == 2 ? 8 * lane : 128 * half + 4 * lane));
+    }
+    __device__ __forceinline__ typename R::Raw get() const {
+        const int lane = threadIdx.x & 31;
+        if constexpr (R::SIZE == 2) return *piece(lane, 0);
+        else return {*piece(lane, 0), *piece(lane, 1)};
+    }
+    __device__ __forceinline__ void put(const typename R::Raw &r) const {
+        const int lane = threadIdx.x & 31;
+        if constexpr (R::SIZE == 2) *piece(lane, 0) = r;
+        else {
+            *piece(lane, 0) = r.a;
+            *piece(lane, 1) = r.b;
+        }
+    }
+    // the block of a matrix on its way here; `there` columns exist.  What a lane
+    // gets is its own to read once its copies have landed (vec), or at once.
+    __device__ __forceinline__ void fetch(const void *p, int64_t from, int there, bool vec, typename R::Elem *turn) const {
+        const int lane = threadIdx.x & 31;
+        if (vec && there - 8 * lane >= 8) {
+            const typename R::Elem *q = static_cast<const typename R::Elem *>(p) + from + 8 * lane;
+            async16(piece(lane, 0), q);
+            if (R::SIZE == 4) async16(piece(lane, 1), q + 4);
+        } else {
+            put(block_load<R>(p, from, there, vec, turn));
+        }
+    }
+};
+__device__ __forceinline__ int column_at(int place) {        // the column of a 32-bit place, in its block of 256
     return 8 * ((place & 127) >> 2) + 4 * ((place >> 7) & 1) + (place & 3);
 }
 
@@ -422,90 +575,166 @@ struct Exchange {
     double wides[TILE_ROWS][4];
 };
 
-// A cluster of ceil(cols / (512 K)) CTAs takes 32 rows.  A warp takes 4 of
-// them, 512 columns of each: loads, the rows' sums of squares, the inputs to
-// shared memory as floats; the exchange; then the result, its form along the
-// rows from registers (4 lanes a group), and through shared memory the one
-// along the columns (a thread 32 rows of a column).
+// The form along the columns of a tile of 32 rows: a thread takes two columns
+// (the two of a word of 16-bit values), and 32 rows of each.
+template <class R, int K>
+__device__ __forceinline__ void hold_tile(const NormHeld &h, int64_t rb, int64_t col0, const typename R::Elem *tile) {
+    constexpr int PITCH = TILE_COLS * K;
+    float v[32];
+    if constexpr (R::SIZE == 2) {
+        const uint32_t *from = reinterpret_cast<const uint32_t *>(tile) + threadIdx.x;
+        uint32_t w[32], two = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = from[i * (PITCH / 2)];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) max_two<typename R::Type>(two, w[i]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = R::Type::to_f32(j ? w[i] >> 16 : w[i] & 0xFFFFu);
+            hold_column(h, rb, col0 + 2 * (int)threadIdx.x + j, R::Type::to_f32(j ? two >> 16 : two & 0xFFFFu), v);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int place = (int)threadIdx.x + j * (PITCH / 2);
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(tile[i * PITCH + place]);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) max_abs3(top, v[i], v[i + 1]);
+            hold_column(h, rb, col0 + (place & ~255) + column_at(place & 255), top, v);
+        }
+    }
+}
+
+// A cluster of ceil(cols / (512 K)) CTAs takes 32 rows, a warp 4 of them, 512
+// columns of each.  All of a warp's inputs are on their way to shared memory at
+// once (what is in flight decides: with loads into registers, two rows at a
+// time, 4096 x 4096 bf16 in both forms took 57 us).  The rows' sums of squares;
+// the exchange; then the result in its own type in x's place, its form along the
+// rows from registers (4 lanes a group), and through shared memory the one along
+// the columns.  16 bits: x and the residual lie there and are added again for
+// the result; 32 bits: their sum takes x's place.
 template <class R, int K>
 __global__ void __launch_bounds__(THREADS *K, K == 1 ? 3 : 1)
 rms_tile_kernel(NormArgs a) {
-    extern __shared__ __align__(16) float tile[];
+    extern __shared__ __align__(16) uint8_t raw[];
     __shared__ Exchange ex;
     __shared__ float rstds[TILE_ROWS];
+    __shared__ __align__(16) typename R::Elem turns[WARPS * K][256];
+    constexpr int PITCH = TILE_COLS * K;
+    constexpr bool TWO = R::SIZE == 2;               // both inputs in shared memory
+    typename R::Elem *xs = reinterpret_cast<typename R::Elem *>(raw), *rs = xs + TILE_ROWS * PITCH;
     const cg::cluster_group cluster = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kk = warp / WARPS, rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
     const int64_t rows = a.held.rows, cols = a.held.cols, rb = blockIdx.x / ranks, row0 = TILE_ROWS * rb;
-    const int64_t col0 = (int64_t)rank * TILE_COLS * K + TILE_COLS * kk + 8 * lane;      // and 256 on
-    constexpr int PITCH = TILE_COLS * K;
+    const int64_t col0 = (int64_t)rank * PITCH + TILE_COLS * kk;                         // of the warp
+    const int there[2] = {part(cols, col0), part(cols, col0 + 256)};
+    typename R::Elem *turn = turns[warp];
+    auto row_at = [&](typename R::Elem *of, int i, int b) { return TileRow<R>{of + (warp % WARPS + WARPS * i) * PITCH + TILE_COLS * kk + 256 * b}; };
     pdl_wait();
     pdl_trigger();
-#pragma unroll 2
-    for (int i = 0; i < TILE_ROWS / WARPS; ++i) {
-        const int r = warp % WARPS + WARPS * i;
-        const int64_t row = row0 + r;
-        float h[2][8], top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < ROWS_EACH; ++i) {
+        const int64_t row = row0 + warp % WARPS + WARPS * i;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const int64_t c = col0 + 256 * b;
-            const int n = row < rows ? part(cols, c) : 0;
-            R::floats(fetch8<R>(a.x, row * a.ldx + c, n, a.vec), h[b]);
-            if (a.residual) {
-                float q[8];
-                R::floats(fetch8<R>(a.residual, row * a.ldr + c, n, a.vec), q);
+            const int n = row < rows ? there[b] : 0;
+            row_at(xs, i, b).fetch(a.x, row * a.ldx + col0 + 256 * b, n, a.vec, turn);
+            if (TWO && a.residual) row_at(rs, i, b).fetch(a.residual, row * a.ldr + col0 + 256 * b, n, a.vec, turn);
+        }
+        asm volatile("cp.async.commit_group;" : : : "memory");
+    }
+    auto input = [&](int i, int b, int64_t row, f2 h[4]) {           // x + residual
+        float v[8], q[8];
+        R::floats(row_at(xs, i, b).get(), v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) h[b][j] = __fadd_rn(h[b][j], q[j]);
-                R::store(a.sum, row * a.lds + c, n, a.vec, R::rounded(h[b]));
+        for (int j = 0; j < 4; ++j) h[j] = f2pack(v[2 * j], v[2 * j + 1]);
+        if (!a.residual) return;
+        if constexpr (TWO) R::floats(row_at(rs, i, b).get(), q);
+        else R::floats(block_load<R>(a.residual, row * a.ldr + col0 + 256 * b, row < rows ? there[b] : 0, a.vec, turn), q);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = add2(h[j], f2pack(q[2 * j], q[2 * j + 1]));
+    };
+    float hi[ROWS_EACH], lo[ROWS_EACH];
+#pragma unroll
+    for (int i = 0; i < ROWS_EACH; ++i) {
+        const int64_t row = row0 + warp % WARPS + WARPS * i;
+        async_wait(ROWS_EACH - 1 - i);
+        f2 h[2][4];
+        float top = 0.0f;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            input(i, b, row, h[b]);
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f2unpack(h[b][j], v[2 * j], v[2 * j + 1]);
+                max_abs3(top, v[2 * j], v[2 * j + 1]);
             }
-            float *block = tile + r * PITCH + TILE_COLS * kk + 256 * b;
-            *piece(block, lane, 0) = make_float4(h[b][0], h[b][1], h[b][2], h[b][3]);
-            *piece(block, lane, 1) = make_float4(h[b][4], h[b][5], h[b][6], h[b][7]);
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) max_abs3(top, h[b][j], h[b][j + 1]);
+            if (a.residual) {
+                block_store<R>(a.sum, row * a.lds + col0 + 256 * b, row < rows ? there[b] : 0, a.vec, turn, R::rounded(v));
+                if (!TWO) row_at(xs, i, b).put(R::rounded(v));
+            }
         }
         Dot d;
         const bool ok = d.begin<2>(top, top);
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const f2 p = f2pack(h[b][j], h[b][j + 1]);
-                d.add(p, p);
-            }
-        float hi, lo;
-        d.end(hi, lo);
-        if (!ok) hi = __uint_as_float(0x7F800000u);
-        warp_pair(hi, lo);
-        if (lane == 0) ex.pairs[0][r][kk] = make_float2(hi, lo);
+            for (int j = 0; j < 4; ++j) d.add(h[b][j], h[b][j]);
+        d.end(hi[i], lo[i]);
+        if (!ok) hi[i] = __uint_as_float(0x7F800000u);
     }
+    warp_pair4(hi, lo);
+    if ((lane & 7) == 0) ex.pairs[0][warp % WARPS + WARPS * (lane >> 3)][kk] = make_float2(hi[0], lo[0]);
     cluster.sync();
-    float hi = 0.0f, lo = 0.0f;
+    float all = 0.0f, rest = 0.0f;
     if (threadIdx.x < TILE_ROWS) {
         for (int q = 0; q < ranks; ++q) {
             const Exchange *other = cluster.map_shared_rank(&ex, q);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 const float2 p = other->pairs[0][threadIdx.x][k];
-                add22(hi, lo, p.x, p.y);
+                add22(all, rest, p.x, p.y);
             }
         }
-        rstds[threadIdx.x] = rstd_of(hi, lo, a.mean, a.eps);
+        rstds[threadIdx.x] = rstd_of(all, rest, a.mean, a.eps);
     }
+    // the sum as the result is made from it: the residual is added again where it lies beside x
+    auto total = [&](int i, int b, int64_t row, f2 h[4]) {
+        if constexpr (TWO) {
+            input(i, b, row, h);
+        } else {
+            float v[8];
+            R::floats(row_at(xs, i, b).get(), v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = f2pack(v[2 * j], v[2 * j + 1]);
+        }
+    };
     // too large for float32's squares (or not finite): in 64 bits; every CTA of
     // the cluster has seen the same sums and comes here, or none does
-    if (__syncthreads_or(!finite_f32(hi))) {
-        for (int i = 0; i < TILE_ROWS / WARPS; ++i) {
-            const int r = warp % WARPS + WARPS * i;
+    if (__syncthreads_or(!finite_f32(all))) {
+#pragma unroll 1
+        for (int i = 0; i < ROWS_EACH; ++i) {
             double s = 0.0;
-            for (int j = lane; j < TILE_COLS; j += 32) {
-                const double v = tile[r * PITCH + TILE_COLS * kk + j];
-                s = __dadd_rn(s, __dmul_rn(v, v));
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                f2 h[4];
+                total(i, b, row0 + warp % WARPS + WARPS * i, h);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float x, y;
+                    f2unpack(h[j], x, y);
+                    s = __dadd_rn(s, __dadd_rn(__dmul_rn((double)x, (double)x), __dmul_rn((double)y, (double)y)));
+                }
             }
             s = warp_double(s);
-            if (lane == 0) ex.wides[r][kk] = s;
+            if (lane == 0) ex.wides[warp % WARPS + WARPS * i][kk] = s;
         }
         cluster.sync();
-        if (threadIdx.x < TILE_ROWS && !finite_f32(hi)) {
+        if (threadIdx.x < TILE_ROWS && !finite_f32(all)) {
             double s = 0.0;
             for (int q = 0; q < ranks; ++q)
                 for (int k = 0; k < K; ++k) s = __dadd_rn(s, cluster.map_shared_rank(&ex, q)->wides[threadIdx.x][k]);
@@ -517,33 +746,30 @@ rms_tile_kernel(NormArgs a) {
 #pragma unroll 1
     for (int b = 0; b < 2; ++b) {
         const int64_t c = col0 + 256 * b;
-        const int nc = part(cols, c);
         float w[8];
-        weights8(a.w, a.w_kind, c, nc, a.vec, w);
+        weights8(a.w, a.w_kind, a.vec_w, c + 8 * lane, there[b] - 8 * lane, w);
 #pragma unroll 2
-        for (int i = 0; i < TILE_ROWS / WARPS; ++i) {
-            const int r = warp % WARPS + WARPS * i;
-            const int64_t row = row0 + r;
-            const int n = row < rows ? nc : 0;
-            float *block = tile + r * PITCH + TILE_COLS * kk + 256 * b;
-            const float4 p = *piece(block, lane, 0), q = *piece(block, lane, 1);
-            float v[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-            const float rstd = rstds[r];
+        for (int i = 0; i < ROWS_EACH; ++i) {
+            const int64_t row = row0 + warp % WARPS + WARPS * i;
+            const int n = row < rows ? there[b] : 0;
+            f2 h[4];
+            total(i, b, row, h);
+            const f2 rstd = both(rstds[warp % WARPS + WARPS * i]);
+            float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fmul_rn(v[j], rstd), w[j]);
+            for (int j = 0; j < 4; ++j) f2unpack(mul2(mul2(h[j], rstd), f2pack(w[2 * j], w[2 * j + 1])), v[2 * j], v[2 * j + 1]);
+            if (n < 256) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) if (8 * lane + j >= n) v[j] = 0.0f;
+            }
             const typename R::Raw y = R::rounded(v);
-            if (a.out) R::store(a.out, row * a.ldo + c, n, a.vec, y);
-            R::floats(y, v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) if (j >= n) v[j] = 0.0f;
-            *piece(block, lane, 0) = make_float4(v[0], v[1], v[2], v[3]);
-            *piece(block, lane, 1) = make_float4(v[4], v[5], v[6], v[7]);
-            if (a.held.r_codes) hold_rows(a.held, row, c, v);
+            if (a.out) block_store<R>(a.out, row * a.ldo + c, n, a.vec, turn, y);
+            row_at(xs, i, b).put(y);
+            if (a.held.r_codes) hold_rows<R>(a.held, row, c + 8 * lane, y);
         }
     }
     __syncthreads();
-    for (int place = threadIdx.x; place < PITCH; place += THREADS * K)
-        hold_column(a.held, rb, (int64_t)rank * PITCH + (place & ~255) + column_at(place & 255), tile + place, PITCH);
+    hold_tile<R, K>(a.held, rb, (int64_t)rank * PITCH, xs);
     cluster.sync();                  // the others may still read this CTA's sums
 }
 
@@ -556,7 +782,8 @@ struct BackArgs {
     float *dw_parts;                 // [clusters][cols], or NULL
     int64_t lddy, ldx, ldr, ldd;
     int32_t w_kind;
-    bool vec;
+    bool vec, vec_w;
+    float minus_one;                 // -1, which the compiler does not know
     Mean mean;
     NormHeld held;
     int64_t row_blocks;
@@ -564,162 +791,168 @@ struct BackArgs {
 
 // As rms_tile_kernel, a cluster taking row blocks b, b + clusters, ...: a lane
 // adds up its columns' part of dw over all of them.  Shared memory keeps both
-// inputs of 16 bits in the place of a float; of 32 bits x alone, and dy is read
-// again.
+// inputs of 16 bits; of 32 bits x alone, and dy is read again.
 template <class R, int K>
 __global__ void __launch_bounds__(THREADS *K, K == 1 ? 2 : 1)
 rms_back_kernel(BackArgs a) {
-    extern __shared__ __align__(16) float tile[];
+    extern __shared__ __align__(16) uint8_t raw[];
     __shared__ Exchange ex;
     __shared__ float slopes[TILE_ROWS], rstds[TILE_ROWS];
+    __shared__ __align__(16) typename R::Elem turns[WARPS * K][256];
+    constexpr int PITCH = TILE_COLS * K;
+    constexpr bool TWO = R::SIZE == 2;
+    typename R::Elem *xs = reinterpret_cast<typename R::Elem *>(raw), *ys = xs + TILE_ROWS * PITCH;
     const cg::cluster_group cluster = cg::this_cluster();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kk = warp / WARPS, rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-    const int64_t rows = a.held.rows, cols = a.held.cols;
-    const int64_t col0 = (int64_t)rank * TILE_COLS * K + TILE_COLS * kk + 8 * lane;
-    constexpr int PITCH = TILE_COLS * K;
+    const int64_t rows = a.held.rows, cols = a.held.cols, col0 = (int64_t)rank * PITCH + TILE_COLS * kk;
+    const int there[2] = {part(cols, col0), part(cols, col0 + 256)};
+    typename R::Elem *turn = turns[warp];
+    auto row_at = [&](typename R::Elem *of, int i, int b) { return TileRow<R>{of + (warp % WARPS + WARPS * i) * PITCH + TILE_COLS * kk + 256 * b}; };
     pdl_wait();
     pdl_trigger();
-    float w[2][8], dw[2][8] = {};
+    f2 w[2][4], dw[2][4] = {};
 #pragma unroll
-    for (int b = 0; b < 2; ++b) weights8(a.w, a.w_kind, col0 + 256 * b, part(cols, col0 + 256 * b), a.vec, w[b]);
-    int turn = 0;
-    for (int64_t rb = blockIdx.x / ranks; rb < a.row_blocks; rb += gridDim.x / ranks, turn ^= 1) {
+    for (int b = 0; b < 2; ++b) {
+        float v[8];
+        weights8(a.w, a.w_kind, a.vec_w, col0 + 256 * b + 8 * lane, there[b] - 8 * lane, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[b][j] = f2pack(v[2 * j], v[2 * j + 1]);
+    }
+    int turns_taken = 0;
+    for (int64_t rb = blockIdx.x / ranks; rb < a.row_blocks; rb += gridDim.x / ranks, turns_taken ^= 1) {
         const int64_t row0 = TILE_ROWS * rb;
-#pragma unroll 1
-        for (int i = 0; i < TILE_ROWS / WARPS; ++i) {
-            const int r = warp % WARPS + WARPS * i;
-            const int64_t row = row0 + r;
-            const float rstd = row < rows ? a.rstd[row] : 0.0f;
-            float g[2][8], x[2][8], tg = 0.0f, tx = 0.0f;
+#pragma unroll
+        for (int i = 0; i < ROWS_EACH; ++i) {
+            const int64_t row = row0 + warp % WARPS + WARPS * i;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int64_t c = col0 + 256 * b;
-                const int n = row < rows ? part(cols, c) : 0;
-                const typename R::Raw rd = fetch8<R>(a.dy, row * a.lddy + c, n, a.vec), rx = fetch8<R>(a.x, row * a.ldx + c, n, a.vec);
-                float *block = tile + r * PITCH + TILE_COLS * kk + 256 * b;
-                R::floats(rd, g[b]);
-                R::floats(rx, x[b]);
-                if constexpr (R::SIZE == 2) {
-                    uint32_t u[8];
+                const int n = row < rows ? there[b] : 0;
+                row_at(xs, i, b).fetch(a.x, row * a.ldx + col0 + 256 * b, n, a.vec, turn);
+                if (TWO) row_at(ys, i, b).fetch(a.dy, row * a.lddy + col0 + 256 * b, n, a.vec, turn);
+            }
+            asm volatile("cp.async.commit_group;" : : : "memory");
+        }
+        auto gradient = [&](int i, int b, int64_t row, f2 g[4]) {
+            float v[8];
+            if constexpr (TWO) R::floats(row_at(ys, i, b).get(), v);
+            else R::floats(block_load<R>(a.dy, row * a.lddy + col0 + 256 * b, row < rows ? there[b] : 0, a.vec, turn), v);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) u[j] = lane16(rd, j) | lane16(rx, j) << 16;
-                    *reinterpret_cast<uint4 *>(piece(block, lane, 0)) = make_uint4(u[0], u[1], u[2], u[3]);
-                    *reinterpret_cast<uint4 *>(piece(block, lane, 1)) = make_uint4(u[4], u[5], u[6], u[7]);
-                } else {
-                    *piece(block, lane, 0) = make_float4(x[b][0], x[b][1], x[b][2], x[b][3]);
-                    *piece(block, lane, 1) = make_float4(x[b][4], x[b][5], x[b][6], x[b][7]);
-                }
+            for (int j = 0; j < 4; ++j) g[j] = f2pack(v[2 * j], v[2 * j + 1]);
+        };
+        float hi[ROWS_EACH], lo[ROWS_EACH];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    dw[b][j] = __fmaf_rn(g[b][j], __fmul_rn(x[b][j], rstd), dw[b][j]);
-                    g[b][j] = __fmul_rn(g[b][j], w[b][j]);
-                }
+        for (int i = 0; i < ROWS_EACH; ++i) {
+            const int64_t row = row0 + warp % WARPS + WARPS * i;
+            const f2 rstd = both(row < rows ? a.rstd[row] : 0.0f);
+            async_wait(ROWS_EACH - 1 - i);
+            f2 g[2][4], x[2][4];
+            float tg = 0.0f, tx = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    max_abs3(tg, g[b][j], g[b][j + 1]);
-                    max_abs3(tx, x[b][j], x[b][j + 1]);
+            for (int b = 0; b < 2; ++b) {
+                float v[8];
+                gradient(i, b, row, g[b]);
+                R::floats(row_at(xs, i, b).get(), v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[b][j] = f2pack(v[2 * j], v[2 * j + 1]);
+                    dw[b][j] = fma2(g[b][j], mul2(x[b][j], rstd), dw[b][j]);
+                    g[b][j] = mul2(g[b][j], w[b][j]);
+                    float p, q;
+                    f2unpack(g[b][j], p, q);
+                    max_abs3(tg, p, q);
+                    max_abs3(tx, v[2 * j], v[2 * j + 1]);
                 }
             }
             Dot d;
-            const bool ok = d.begin<2>(tg, tx);
+            if (d.begin<2>(tg, tx)) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) d.add(f2pack(g[b][j], g[b][j + 1]), f2pack(x[b][j], x[b][j + 1]));
-            float hi, lo;
-            d.end(hi, lo);
-            if (!ok) {                               // far outside of any gradient's range: in 64 bits
+                    for (int j = 0; j < 4; ++j) d.add(g[b][j], x[b][j]);
+                d.end(hi[i], lo[i]);
+            } else {                                 // far outside of any gradient's range: in 64 bits
                 double s = 0.0;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s = __dadd_rn(s, __dmul_rn((double)g[b][j], (double)x[b][j]));
-                hi = (float)s;
-                lo = finite_f32(hi) ? (float)(s - (double)hi) : 0.0f;
+                    for (int j = 0; j < 4; ++j) {
+                        float p, q, u, v;
+                        f2unpack(g[b][j], p, q);
+                        f2unpack(x[b][j], u, v);
+                        s = __dadd_rn(s, __dadd_rn(__dmul_rn((double)p, (double)u), __dmul_rn((double)q, (double)v)));
+                    }
+                hi[i] = (float)s;
+                lo[i] = finite_f32(hi[i]) ? (float)(s - (double)hi[i]) : 0.0f;
             }
-            warp_pair(hi, lo);
-            if (lane == 0) ex.pairs[turn][r][kk] = make_float2(hi, lo);
         }
+        warp_pair4(hi, lo);
+        if ((lane & 7) == 0) ex.pairs[turns_taken][warp % WARPS + WARPS * (lane >> 3)][kk] = make_float2(hi[0], lo[0]);
         cluster.sync();
         if (threadIdx.x < TILE_ROWS) {
-            float hi = 0.0f, lo = 0.0f;
+            float all = 0.0f, rest = 0.0f;
             for (int q = 0; q < ranks; ++q) {
                 const Exchange *other = cluster.map_shared_rank(&ex, q);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    const float2 p = other->pairs[turn][threadIdx.x][k];
-                    add22(hi, lo, p.x, p.y);
+                    const float2 p = other->pairs[turns_taken][threadIdx.x][k];
+                    add22(all, rest, p.x, p.y);
                 }
             }
             const float rstd = row0 + threadIdx.x < rows ? a.rstd[row0 + threadIdx.x] : 0.0f;
             rstds[threadIdx.x] = rstd;
-            slopes[threadIdx.x] = slope_of(hi, lo, a.mean, rstd);
+            slopes[threadIdx.x] = slope_of(all, rest, a.mean, rstd);
         }
         __syncthreads();
-#pragma unroll 1
-        for (int i = 0; i < TILE_ROWS / WARPS; ++i) {
-            const int r = warp % WARPS + WARPS * i;
-            const int64_t row = row0 + r;
-            const float rstd = rstds[r], slope = slopes[r];
+        const f2 minus = both(a.minus_one);
+#pragma unroll 2
+        for (int i = 0; i < ROWS_EACH; ++i) {
+            const int64_t row = row0 + warp % WARPS + WARPS * i;
+            const f2 rstd = both(rstds[warp % WARPS + WARPS * i]), slope = both(slopes[warp % WARPS + WARPS * i]);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const int64_t c = col0 + 256 * b;
-                const int n = row < rows ? part(cols, c) : 0;
-                float *block = tile + r * PITCH + TILE_COLS * kk + 256 * b;
-                float v[8], x[8];
-                if constexpr (R::SIZE == 2) {
-                    const uint4 p = *reinterpret_cast<const uint4 *>(piece(block, lane, 0)), q = *reinterpret_cast<const uint4 *>(piece(block, lane, 1));
-                    const uint32_t u[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-                    uint32_t ud[8], ux[8];
+                const int n = row < rows ? there[b] : 0;
+                float x[8], v[8];
+                typename R::Raw q;
+                if (a.residual) q = block_load<R>(a.residual, row * a.ldr + c, n, a.vec, turn);
+                f2 g[4];
+                gradient(i, b, row, g);
+                R::floats(row_at(xs, i, b).get(), x);
+                // (g w - x slope) rstd, each rounded
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        ud[j] = u[j] & 0xFFFFu;
-                        ux[j] = u[j] >> 16;
-                    }
-                    R::floats(pack8(ud), v);
-                    R::floats(pack8(ux), x);
-                } else {
-                    const float4 p = *piece(block, lane, 0), q = *piece(block, lane, 1);
-                    x[0] = p.x; x[1] = p.y; x[2] = p.z; x[3] = p.w;
-                    x[4] = q.x; x[5] = q.y; x[6] = q.z; x[7] = q.w;
-                    R::floats(fetch8<R>(a.dy, row * a.lddy + c, n, a.vec), v);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] = __fmul_rn(__fsub_rn(__fmul_rn(v[j], w[b][j]), __fmul_rn(x[j], slope)), rstd);
+                for (int j = 0; j < 4; ++j)
+                    f2unpack(mul2(fma2(mul2(f2pack(x[2 * j], x[2 * j + 1]), slope), minus, mul2(g[j], w[b][j])), rstd), v[2 * j], v[2 * j + 1]);
                 if (a.residual) {
-                    float q[8];
-                    R::floats(fetch8<R>(a.residual, row * a.ldr + c, n, a.vec), q);
+                    float r[8];
+                    R::floats(q, r);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], q[j]);
+                    for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], r[j]);
+                }
+                if (n < 256) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) if (8 * lane + j >= n) v[j] = 0.0f;
                 }
                 const typename R::Raw y = R::rounded(v);
-                R::store(a.dx, row * a.ldd + c, n, a.vec, y);
-                if (!a.held.r_codes && !a.held.c_codes) continue;
-                R::floats(y, v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) if (j >= n) v[j] = 0.0f;
-                if (a.held.c_codes) {
-                    *piece(block, lane, 0) = make_float4(v[0], v[1], v[2], v[3]);
-                    *piece(block, lane, 1) = make_float4(v[4], v[5], v[6], v[7]);
-                }
-                if (a.held.r_codes) hold_rows(a.held, row, c, v);
+                block_store<R>(a.dx, row * a.ldd + c, n, a.vec, turn, y);
+                if (a.held.c_codes) row_at(xs, i, b).put(y);
+                if (a.held.r_codes) hold_rows<R>(a.held, row, c + 8 * lane, y);
             }
         }
         __syncthreads();
         if (a.held.c_codes) {
-            for (int place = threadIdx.x; place < PITCH; place += THREADS * K)
-                hold_column(a.held, rb, (int64_t)rank * PITCH + (place & ~255) + column_at(place & 255), tile + place, PITCH);
+            hold_tile<R, K>(a.held, rb, (int64_t)rank * PITCH, xs);
             __syncthreads();
         }
     }
     // the 8 warps' parts of dw, in their order
     if (a.dw_parts) {
+        float *tile = reinterpret_cast<float *>(raw);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            float *block = tile + (warp % WARPS) * PITCH + TILE_COLS * kk + 256 * b;
-            *piece(block, lane, 0) = make_float4(dw[b][0], dw[b][1], dw[b][2], dw[b][3]);
-            *piece(block, lane, 1) = make_float4(dw[b][4], dw[b][5], dw[b][6], dw[b][7]);
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f2unpack(dw[b][j], v[2 * j], v[2 * j + 1]);
+            TileRow<RowF32>{reinterpret_cast<uint32_t *>(tile + (warp % WARPS) * PITCH + TILE_COLS * kk + 256 * b)}.put(RowF32::rounded(v));
         }
         __syncthreads();
         for (int place = threadIdx.x; place < PITCH; place += THREADS * K) {
@@ -738,20 +971,26 @@ template <class R>
 __global__ void __launch_bounds__(THREADS)
 rms_back_rows_kernel(BackArgs a) {
     __shared__ float2 parts[WARPS];
+    __shared__ __align__(16) typename R::Elem turns[WARPS][256];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = blockIdx.x, cols = a.held.cols;
+    typename R::Elem *turn = turns[warp];
     pdl_wait();
     pdl_trigger();
     const float rstd = a.rstd[row];
     float hi = 0.0f, lo = 0.0f;
-    for (int64_t c = 8 * (int64_t)threadIdx.x; c < cols; c += 8 * THREADS) {
+    auto inputs = [&](int64_t c, float g[8], float x[8]) {           // g: times the weight
+        float w[8];
         const int n = part(cols, c);
-        float g[8], x[8], w[8], tg = 0.0f, tx = 0.0f;
-        R::floats(fetch8<R>(a.dy, row * a.lddy + c, n, a.vec), g);
-        R::floats(fetch8<R>(a.x, row * a.ldx + c, n, a.vec), x);
-        weights8(a.w, a.w_kind, c, n, a.vec, w);
+        R::floats(block_load<R>(a.dy, row * a.lddy + c, n, a.vec, turn), g);
+        R::floats(block_load<R>(a.x, row * a.ldx + c, n, a.vec, turn), x);
+        weights8(a.w, a.w_kind, a.vec_w, c + 8 * lane, n - 8 * lane, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) g[j] = __fmul_rn(g[j], w[j]);
+    };
+    for (int64_t c = 256 * warp; c < cols; c += 8 * THREADS) {
+        float g[8], x[8], tg = 0.0f, tx = 0.0f;
+        inputs(c, g, x);
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
             max_abs3(tg, g[j], g[j + 1]);
@@ -779,28 +1018,28 @@ rms_back_rows_kernel(BackArgs a) {
     lo = parts[0].y;
     for (int k = 1; k < WARPS; ++k) add22(hi, lo, parts[k].x, parts[k].y);
     const float slope = slope_of(hi, lo, a.mean, rstd);
-    for (int64_t c = 8 * (int64_t)threadIdx.x; c < cols; c += 8 * THREADS) {
+    for (int64_t c = 256 * warp; c < cols; c += 8 * THREADS) {
+        float v[8], x[8];
         const int n = part(cols, c);
-        float v[8], x[8], w[8];
-        R::floats(fetch8<R>(a.dy, row * a.lddy + c, n, a.vec), v);
-        R::floats(fetch8<R>(a.x, row * a.ldx + c, n, a.vec), x);
-        weights8(a.w, a.w_kind, c, n, a.vec, w);
+        inputs(c, v, x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fsub_rn(__fmul_rn(v[j], w[j]), __fmul_rn(x[j], slope)), rstd);
+        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fsub_rn(v[j], __fmul_rn(x[j], slope)), rstd);
         if (a.residual) {
             float q[8];
-            R::floats(fetch8<R>(a.residual, row * a.ldr + c, n, a.vec), q);
+            R::floats(block_load<R>(a.residual, row * a.ldr + c, n, a.vec, turn), q);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], q[j]);
         }
-        R::store(a.dx, row * a.ldd + c, n, a.vec, R::rounded(v));
+        block_store<R>(a.dx, row * a.ldd + c, n, a.vec, turn, R::rounded(v));
     }
 }
 // Their part of dw: 2048 columns of the rows b, b + gridDim.y, ...
 template <class R>
 __global__ void __launch_bounds__(THREADS)
 rms_back_weight_kernel(BackArgs a) {
-    const int64_t cols = a.held.cols, c = 8 * ((int64_t)blockIdx.x * THREADS + threadIdx.x);
+    __shared__ __align__(16) typename R::Elem turns[WARPS][256];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t cols = a.held.cols, c = 256 * ((int64_t)blockIdx.x * WARPS + warp);
     const int n = part(cols, c);
     pdl_wait();
     pdl_trigger();
@@ -808,13 +1047,13 @@ rms_back_weight_kernel(BackArgs a) {
     for (int64_t row = blockIdx.y; row < a.held.rows; row += gridDim.y) {
         const float rstd = a.rstd[row];
         float v[8], x[8];
-        R::floats(fetch8<R>(a.dy, row * a.lddy + c, n, a.vec), v);
-        R::floats(fetch8<R>(a.x, row * a.ldx + c, n, a.vec), x);
+        R::floats(block_load<R>(a.dy, row * a.lddy + c, n, a.vec, turns[warp]), v);
+        R::floats(block_load<R>(a.x, row * a.ldx + c, n, a.vec, turns[warp]), x);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[j] = __fmaf_rn(v[j], __fmul_rn(x[j], rstd), dw[j]);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) if (j < n) a.dw_parts[blockIdx.y * cols + c + j] = dw[j];
+    for (int j = 0; j < 8; ++j) if (8 * lane + j < n) a.dw_parts[blockIdx.y * cols + c + 8 * lane + j] = dw[j];
 }
 
 // dw from its parts, in their order: 32 columns a CTA, 8 shares of the parts.
@@ -826,8 +1065,17 @@ rms_weight_kernel(const float *parts, int n, int64_t cols, void *dw, int kind) {
     pdl_wait();
     pdl_trigger();
     float s = 0.0f;
-    if (c < cols)
-        for (int i = warp; i < n; i += WARPS) s = __fadd_rn(s, parts[i * cols + c]);
+    if (c < cols) {
+        int i = warp;
+        for (; i + 7 * WARPS < n; i += 8 * WARPS) {          // 8 loads in flight
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = parts[(i + j * WARPS) * cols + c];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = __fadd_rn(s, v[j]);
+        }
+        for (; i < n; i += WARPS) s = __fadd_rn(s, parts[i * cols + c]);
+    }
     share[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || c >= cols) return;
@@ -889,15 +1137,10 @@ static cudaError_t back_tile(const BackArgs &a, unsigned ctas, int64_t clusters,
     return tile_launch(rms_back_kernel<R, K>, set, K, ctas, clusters, s, a);
 }
 
-// Parts of dw: clusters that are resident at once (a number of the sizes
-// alone, so that a sum has the same bits whatever forms are asked for).
+// Parts of dw: a number of the sizes alone, so that a sum has the same bits
+// whatever forms are asked for.  256 of them keep scratch small and the GPU busy.
 static int64_t back_parts(int64_t rows, int64_t cols) {
-    const int64_t blocks = (rows + TILE_ROWS - 1) / TILE_ROWS;
-    if (cols > TILE_MOST) return blocks < 64 ? blocks : 64;
-    unsigned ctas;
-    int k;
-    tile_shape(cols, ctas, k);
-    const int64_t most = (k == 1 ? 304 : 152) / (int64_t)ctas;
+    const int64_t blocks = (rows + TILE_ROWS - 1) / TILE_ROWS, most = cols > TILE_MOST ? 64 : 256;
     return blocks < most ? blocks : most;
 }
 
@@ -953,7 +1196,7 @@ zs_status check_vector(const void *p, int32_t kind, bool need, bool *vec, const 
     if (!p) return need ? zs_fail(ZS_EINVAL, "%s: %s NULL", fn, name) : ZS_OK;
     if (!dtype_ok(kind)) return zs_fail(ZS_EINVAL, "%s: %s: dtype %d", fn, name, kind);
     if (addr(p) % dtype_size(kind)) return zs_fail(ZS_EINVAL, "%s: %s not aligned to its elements", fn, name);
-    if (vec && addr(p) % 16) *vec = false;
+    if (vec) *vec = addr(p) % 16 == 0;
     return ZS_OK;
 }
 
@@ -978,7 +1221,7 @@ zs_status zs_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t 
                       float *rstd, void *r_codes, void *r_scales, void *c_codes, void *c_scales, void *stream) {
     const char *fn = "zs_rms_norm";
     const Matrix m[] = {{x, ldx, true, "x"}, {residual, ldr, false, "residual"}, {sum, lds, residual != nullptr, "sum"}, {out, ldo, false, "out"}};
-    bool vec;
+    bool vec, vec_w = true;
     zs_status r = check(m, rows, cols, dtype, &vec, fn);
     if (r) return r;
     if (sum && !residual) return zs_fail(ZS_EINVAL, "%s: sum without a residual is x itself", fn);
@@ -988,7 +1231,7 @@ zs_status zs_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t 
         zs_clear_error();
         return ZS_OK;
     }
-    if ((r = check_vector(weight, weight_dtype, true, &vec, "weight", fn)) || (r = check_vector(rstd, ZS_DTYPE_FP32, true, nullptr, "rstd", fn)))
+    if ((r = check_vector(weight, weight_dtype, true, &vec_w, "weight", fn)) || (r = check_vector(rstd, ZS_DTYPE_FP32, true, nullptr, "rstd", fn)))
         return r;
     if (!out && !r_codes && !c_codes) return zs_fail(ZS_EINVAL, "%s: no form of the result is asked for", fn);
     using namespace zsk;
@@ -997,7 +1240,7 @@ zs_status zs_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t 
     NormArgs a;
     a.x = x; a.residual = residual; a.w = weight; a.sum = sum; a.out = out; a.rstd = rstd;
     a.ldx = ldx; a.ldr = ldr; a.lds = lds; a.ldo = ldo;
-    a.w_kind = weight_dtype; a.vec = vec; a.eps = eps; a.mean = mean_of(cols);
+    a.w_kind = weight_dtype; a.vec = vec; a.vec_w = vec_w; a.eps = eps; a.mean = mean_of(cols);
     const bool tiles = c_codes && cols <= TILE_MOST;
     a.held = {static_cast<uint8_t *>(r_codes), static_cast<uint8_t *>(r_scales), tiles ? static_cast<uint8_t *>(c_codes) : nullptr,
               tiles ? static_cast<uint8_t *>(c_scales) : nullptr, rows, cols};
@@ -1037,7 +1280,7 @@ zs_status zs_rms_norm_backward(const void *dy, int64_t lddy, const void *x, int6
                                void *c_codes, void *c_scales, void *stream) {
     const char *fn = "zs_rms_norm_backward";
     const Matrix m[] = {{dy, lddy, true, "dy"}, {x, ldx, true, "x"}, {residual, ldr, false, "residual"}, {dx, lddx, true, "dx"}};
-    bool vec;
+    bool vec, vec_w = true;
     zs_status r = check(m, rows, cols, dtype, &vec, fn);
     if (r) return r;
     if ((r = check_held(r_codes, r_scales, "along rows", fn)) || (r = check_held(c_codes, c_scales, "along columns", fn))) return r;
@@ -1048,7 +1291,7 @@ zs_status zs_rms_norm_backward(const void *dy, int64_t lddy, const void *x, int6
         zs_clear_error();
         return ZS_OK;
     }
-    if ((r = check_vector(weight, weight_dtype, true, &vec, "weight", fn)) || (r = check_vector(rstd, ZS_DTYPE_FP32, true, nullptr, "rstd", fn)))
+    if ((r = check_vector(weight, weight_dtype, true, &vec_w, "weight", fn)) || (r = check_vector(rstd, ZS_DTYPE_FP32, true, nullptr, "rstd", fn)))
         return r;
     if (dw && (!scratch || addr(scratch) % 16)) return zs_fail(ZS_EINVAL, "%s: scratch NULL or not 16-byte aligned", fn);
     using namespace zsk;
@@ -1056,7 +1299,7 @@ zs_status zs_rms_norm_backward(const void *dy, int64_t lddy, const void *x, int6
     BackArgs a;
     a.dy = dy; a.x = x; a.w = weight; a.residual = residual; a.rstd = rstd; a.dx = dx; a.dw_parts = dw ? scratch : nullptr;
     a.lddy = lddy; a.ldx = ldx; a.ldr = ldr; a.ldd = lddx;
-    a.w_kind = weight_dtype; a.vec = vec; a.mean = mean_of(cols);
+    a.w_kind = weight_dtype; a.vec = vec; a.vec_w = vec_w; a.minus_one = -1.0f; a.mean = mean_of(cols);
     a.held = {static_cast<uint8_t *>(r_codes), static_cast<uint8_t *>(r_scales), static_cast<uint8_t *>(c_codes),
               static_cast<uint8_t *>(c_scales), rows, cols};
     a.row_blocks = c_codes ? 4 * mx4_atoms(rows) : r_codes ? 4 * mx4_row_tiles(rows) : (rows + TILE_ROWS - 1) / TILE_ROWS;
