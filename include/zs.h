@@ -861,9 +861,8 @@ zs_status zs_mx4_matvec(int64_t m, int64_t n, int64_t k, const void *x, int64_t 
  * be x's or residual's own memory with the same stride.  out: y, or NULL.
  * r_codes, r_scales and c_codes, c_scales: y held in 4 bits along its rows and
  * its columns, bit for bit what zs_mx4_quantize makes of y (either pair may be
- * NULL; of the three results one at least is asked for).  Past 12288 columns
- * the form along the columns needs out.  rstd [rows] is what the backward
- * pass reads.  The sum of squares is made to 2^-40 of itself (squares below
+ * NULL; of the three results one at least is asked for).  rstd [rows] is what
+ * the backward pass reads.  The sum of squares is made to 2^-40 of itself (squares below
  * 2^-126 are lost), and rstd is the fp32 number nearest to its formula's value
  * unless that lies within 2^-40 of the middle of two.  A row with an infinity
  * or NaN gives what the formula gives.  eps >= 0: of a row of zeros with eps 0
@@ -888,7 +887,7 @@ zs_status zs_rms_norm_scratch(int64_t rows, int64_t cols, int64_t *bytes);
  * with the mean made to 2^-40 of the mean of the magnitudes.  dx may be dy's or
  * residual's own memory with the same stride.  r_codes .. c_scales: dx held in
  * 4 bits, as the products of the layer below read it, as zs_mx4_quantize makes
- * of dx.  dw [cols] may be NULL; otherwise scratch (16-byte aligned,
+ * of dx.  dw [cols] may be NULL.  scratch (16-byte aligned,
  * zs_rms_norm_scratch bytes) is overwritten: calls that overlap on the GPU need
  * one each.  No rows: dw is 0.  Errors: ZS_EINVAL, ZS_ECUDA. */
 zs_status zs_rms_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,

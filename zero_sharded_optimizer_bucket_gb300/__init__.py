@@ -981,9 +981,9 @@ def zs_rms_norm_scratch(rows: int, cols: int) -> int:
     return n.value
 
 
-def zs_rms_norm_backward(dy, x, weight, rstd, dx, residual=None, dw=None, scratch=None, rows=None, cols=None, stream=None) -> None:
+def zs_rms_norm_backward(dy, x, weight, rstd, dx, scratch, residual=None, dw=None, rows=None, cols=None, stream=None) -> None:
     """dy, x, residual, dx: [r, c] torch matrices of one type; weight, dw [c];
-    rstd [r] float32; scratch: zs_rms_norm_scratch's bytes, for dw.  rows, cols:
+    rstd [r] float32; scratch: zs_rms_norm_scratch's bytes.  rows, cols:
     the dicts of dx held along its rows and its columns."""
     device = _current_device()
     r, c, ldx, dtype = _matrix(x, "x")
@@ -995,7 +995,7 @@ def zs_rms_norm_backward(dy, x, weight, rstd, dx, residual=None, dw=None, scratc
     rc, rs = _mx4(rows, r, c, device)
     cc, cs = _mx4(cols, c, r, device)
     sa = _device_address(scratch, "scratch", device)
-    if dw is not None and hasattr(scratch, "data_ptr") and (scratch.nbytes < zs_rms_norm_scratch(r, c) or not scratch.is_contiguous()):
+    if hasattr(scratch, "data_ptr") and (scratch.nbytes < zs_rms_norm_scratch(r, c) or not scratch.is_contiguous()):
         raise ValueError(f"scratch: {zs_rms_norm_scratch(r, c)} contiguous bytes expected, got {tuple(scratch.shape)} of {scratch.dtype}")
     st = _lib.zs_rms_norm_backward(ya, ldy, _device_address(x, "x", device), ldx, wa, wd,
                                    _vector(rstd, "rstd", r, device, ZS_DTYPE_FP32)[0], ra, ldr, r, c, dtype, da, ldd, dwa, dwd, sa,

@@ -14,17 +14,19 @@
 // formula's value but where that lies within 2^-40 of the middle of two.
 //
 // A result held along its columns needs 32 rows at a time, which no SM holds
-// whole: a cluster shares them out by columns and exchanges the rows' sums
-// through distributed shared memory.
+// whole.  One kernel makes the rows' sums, another takes tiles of 32 rows by 512
+// columns; the second reading of the inputs comes from L2, since long matrices
+// go by as many rows as fit there.  (Clusters that hold 32 rows and exchange
+// their sums through distributed shared memory read once, but took 41 us for
+// 4096 x 4096 bf16 in both forms: 57 of them fit the GPU, and the 128 blocks of
+// rows need three turns of all that lies between two barriers.)
 #include <atomic>
-#include <cooperative_groups.h>
 
 #include "zs_launch.h"
 #include "zs_mx4.cuh"
 
 namespace zsk {
 
-namespace cg = cooperative_groups;
 typedef unsigned long long f2;
 
 __device__ __forceinline__ bool finite_f32(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
@@ -269,32 +271,6 @@ __device__ __forceinline__ void warp_pair(float &hi, float &lo) {
         add22(hi, lo, h2, l2);
     }
 }
-// The pairs of four rows at once: halves of the warp keep two rows each, then
-// quarters one; afterwards lane l has row l / 8.
-__device__ __forceinline__ void warp_pair4(float (&hi)[4], float (&lo)[4]) {
-    const int lane = threadIdx.x & 31;
-    const bool up = lane & 16, odd = lane & 8;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const float h = __shfl_xor_sync(0xFFFFFFFFu, up ? hi[k] : hi[2 + k], 16), l = __shfl_xor_sync(0xFFFFFFFFu, up ? lo[k] : lo[2 + k], 16);
-        if (up) {
-            hi[k] = hi[2 + k];
-            lo[k] = lo[2 + k];
-        }
-        add22(hi[k], lo[k], h, l);
-    }
-    const float h = __shfl_xor_sync(0xFFFFFFFFu, odd ? hi[0] : hi[1], 8), l = __shfl_xor_sync(0xFFFFFFFFu, odd ? lo[0] : lo[1], 8);
-    if (odd) {
-        hi[0] = hi[1];
-        lo[0] = lo[1];
-    }
-    add22(hi[0], lo[0], h, l);
-#pragma unroll
-    for (int off = 4; off > 0; off >>= 1) {
-        const float h2 = __shfl_xor_sync(0xFFFFFFFFu, hi[0], off), l2 = __shfl_xor_sync(0xFFFFFFFFu, lo[0], off);
-        add22(hi[0], lo[0], h2, l2);
-    }
-}
 __device__ __forceinline__ double warp_double(double v) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v = __dadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
@@ -358,36 +334,52 @@ __device__ __forceinline__ uint32_t encode8(const float v[8], float inv) {
     return e2m1x8(y);
 }
 
-// 8 values a lane, 4 neighbouring lanes a group along the row; y is 0 past the
-// matrix.  `row` may lie past the matrix, in the tile of scales that holds it.
-template <class R>
-__device__ __forceinline__ void hold_rows(const NormHeld &h, int64_t row, int64_t col, const typename R::Raw &y) {
-    const uint32_t byte = mx4_scale_byte(__float_as_uint(R::top4(y)) >> 23);
-    float v[8];
-    R::floats(y, v);
-    const uint32_t word = byte == 255u ? 0u : encode8(v, byte == 255u ? 0.0f : mx4_inverse(byte));
-    const int64_t g = col / MX4_GROUP;
-    if (row < h.rows && g < mx4_groups(h.cols))
-        *reinterpret_cast<uint32_t *>(h.r_codes + row * mx4_row_bytes(h.cols) + col / 2) = word;
-    // the scales of a row's four groups lie side by side: one lane writes them
-    uint32_t four = byte << (8 * (g & 3));
-    four |= __shfl_xor_sync(0xFFFFFFFFu, four, 4);
-    four |= __shfl_xor_sync(0xFFFFFFFFu, four, 8);
-    if ((threadIdx.x & 15) == 0 && row < 128 * mx4_row_tiles(h.rows) && g < 4 * mx4_atoms(h.cols))
-        *reinterpret_cast<uint32_t *>(h.r_scales + ((row >> 7) * mx4_atoms(h.cols) + (g >> 2)) * MX4_ATOM + mx4_in_atom((int)(row & 127), 0)) = four;
-}
+// A warp's index in a form that the compiler knows to be the same in all lanes:
+// what follows from it is then worked out once a warp.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0); }
 
-// 32 values of one column: the rows from 32 g on
-__device__ __forceinline__ void hold_column(const NormHeld &h, int64_t g, int64_t col, float top, const float v[32]) {
+// Where the values of a warp's block of 256 columns from `col` on, of the rows
+// from `row` on, go in the form along the rows: worked out once, since offsets of
+// 64 bits cost as much as the values do.
+struct RowsOut {
+    uint8_t *codes, *scales;         // of the lane's 8 columns
+    int64_t bytes;                   // of a row of codes
+    uint32_t in, writes;             // bit b: of this block and the next, the group exists; this lane writes the scales of the row's four
+    __device__ __forceinline__ RowsOut(const NormHeld &h, int64_t row, int64_t col) {
+        const int lane = threadIdx.x & 31;
+        bytes = mx4_row_bytes(h.cols);
+        codes = h.r_codes + (row * bytes + col / 2) + 4 * lane;
+        const int64_t atoms = mx4_atoms(h.cols), atom = col / (4 * MX4_GROUP);
+        scales = h.r_scales + ((row >> 7) * atoms + atom) * MX4_ATOM + mx4_in_atom((int)(row & 127), 0) + MX4_ATOM * (lane >> 4);
+        const int groups = (int)min((int64_t)16, mx4_groups(h.cols) - col / MX4_GROUP), left = row < 128 * mx4_row_tiles(h.rows) ? (int)min((int64_t)4, atoms - atom) : 0;
+        in = ((lane >> 2) < groups ? 1u : 0u) | (8 + (lane >> 2) < groups ? 2u : 0u);
+        writes = (lane & 15) ? 0u : ((lane >> 4) < left ? 1u : 0u) | (2 + (lane >> 4) < left ? 2u : 0u);
+    }
+    // y: 8 values a lane, 4 neighbouring lanes a group, 0 past the matrix; of the
+    // row `down` below, inside the same 32, which exists or not
+    template <class R>
+    __device__ __forceinline__ void hold(const typename R::Raw &y, int down, int block, bool exists) const {
+        const uint32_t byte = mx4_scale_byte(__float_as_uint(R::top4(y)) >> 23);
+        float v[8];
+        R::floats(y, v);
+        const uint32_t word = byte == 255u ? 0u : encode8(v, byte == 255u ? 0.0f : mx4_inverse(byte));
+        if ((in >> block & 1) && exists) *reinterpret_cast<uint32_t *>(codes + down * bytes + 128 * block) = word;
+        uint32_t four = byte << (8 * ((threadIdx.x >> 2) & 3));
+        four |= __shfl_xor_sync(0xFFFFFFFFu, four, 4);
+        four |= __shfl_xor_sync(0xFFFFFFFFu, four, 8);
+        if (writes >> block & 1) *reinterpret_cast<uint32_t *>(scales + 16 * down + 2 * MX4_ATOM * block) = four;
+    }
+};
+
+// 32 values of one column: the rows from 32 g on.  codes, scale: where they go, or NULL.
+__device__ __forceinline__ void hold_column(uint8_t *codes, uint8_t *scale, float top, const float v[32]) {
     const uint32_t byte = mx4_scale_byte(__float_as_uint(top) >> 23);
     const float inv = byte == 255u ? 0.0f : mx4_inverse(byte);
     uint32_t q[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) q[j] = byte == 255u ? 0u : encode8(v + 8 * j, inv);
-    if (col < h.cols && g < mx4_groups(h.rows))
-        *reinterpret_cast<uint4 *>(h.c_codes + col * mx4_row_bytes(h.rows) + 16 * g) = make_uint4(q[0], q[1], q[2], q[3]);
-    if (col < 128 * mx4_row_tiles(h.cols) && g < 4 * mx4_atoms(h.rows))
-        h.c_scales[((col >> 7) * mx4_atoms(h.rows) + (g >> 2)) * MX4_ATOM + mx4_in_atom((int)(col & 127), (int)(g & 3))] = (uint8_t)byte;
+    if (codes) *reinterpret_cast<uint4 *>(codes) = make_uint4(q[0], q[1], q[2], q[3]);
+    if (scale) *scale = (uint8_t)byte;
 }
 
 // ------------------------------------------------------- forward, rows --
@@ -508,17 +500,143 @@ rms_rows_kernel(NormArgs a) {
         for (int i = 0; i < 8; ++i) v[i] = 8 * lane + i < n ? __fmul_rn(__fmul_rn(v[i], rstd), w[i]) : 0.0f;
         const typename R::Raw y = R::rounded(v);
         if (a.out) block_store<R>(a.out, row * a.ldo + c, n, a.vec, turn, y);
-        if (a.held.r_codes) hold_rows<R>(a.held, row, c + 8 * lane, y);
+        if (a.held.r_codes) RowsOut(a.held, row, c).template hold<R>(y, 0, 0, there);
     }
 }
 
-// ---------------------------------------------- 32 rows, shared by columns --
+// ------------------------------------------------- the sums of many rows --
 
-constexpr int TILE_ROWS = 32;
-constexpr int TILE_COLS = 512;       // of 8 warps; K times as many of a CTA
-constexpr int tile_smem(int k) { return TILE_ROWS * TILE_COLS * k * 4; }
-constexpr int64_t TILE_MOST = 8 * 3 * TILE_COLS;     // columns that a cluster holds
-constexpr int ROWS_EACH = TILE_ROWS / WARPS;         // rows of a warp, 512 columns of each
+// rstd of every row (h: x + residual), or of the backward pass c, rstd^2 times
+// the mean of g x: WPR warps a row, four blocks of 256 columns of both inputs in
+// flight at a time.  Bandwidth bounds it.
+struct SumArgs {
+    const void *x, *other, *w;       // other: the residual or NULL; dy
+    int64_t ldx, ldo, rows, cols, row0;
+    int32_t w_kind;
+    bool vec, vec_w;
+    float eps;
+    Mean mean;
+    const float *rstd;               // of the backward pass
+    float *result;                   // [rows]
+};
+
+template <class R, int WPR, bool BACK>
+__global__ void __launch_bounds__(THREADS)
+rms_sums_kernel(SumArgs a) {
+    constexpr int BLOCKS = 4;
+    __shared__ float2 parts[WARPS];
+    __shared__ double wides[WARPS];
+    __shared__ __align__(16) typename R::Elem turns[WARPS][256];
+    const int lane = threadIdx.x & 31, warp = warp_index(), mine = warp % WPR;
+    const int64_t row = a.row0 + (int64_t)blockIdx.x * (WARPS / WPR) + warp / WPR;
+    const bool there = row < a.rows;
+    typename R::Elem *turn = turns[warp];
+    pdl_wait();
+    pdl_trigger();
+    // block c: u v summed over its columns, u = v = h or u = g, v = x
+    auto inputs = [&](const typename R::Raw &rx, const typename R::Raw &ro, int64_t c, int n, f2 u[4], f2 v[4]) {
+        float x[8], o[8];
+        R::floats(rx, x);
+        R::floats(ro, o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = f2pack(x[2 * j], x[2 * j + 1]);
+        if constexpr (BACK) {
+            float w[8];
+            weights8(a.w, a.w_kind, a.vec_w, c + 8 * lane, n - 8 * lane, w);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = mul2(f2pack(o[2 * j], o[2 * j + 1]), f2pack(w[2 * j], w[2 * j + 1]));
+        } else {
+            if (a.other)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = add2(v[j], f2pack(o[2 * j], o[2 * j + 1]));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = v[j];
+        }
+    };
+    float hi = 0.0f, lo = 0.0f;
+    for (int64_t c0 = 256 * mine; c0 < a.cols; c0 += 256 * WPR * BLOCKS) {
+        typename R::Raw rx[BLOCKS], ro[BLOCKS];
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) {
+            const int64_t c = c0 + 256 * WPR * b;
+            const int n = there ? part(a.cols, c) : 0;
+            rx[b] = block_load<R>(a.x, row * a.ldx + c, n, a.vec, turn);
+            ro[b] = a.other ? block_load<R>(a.other, row * a.ldo + c, n, a.vec, turn) : R::zero();
+        }
+        f2 u[BLOCKS][4], v[BLOCKS][4];
+        float tu = 0.0f, tv = 0.0f;
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) {
+            const int64_t c = c0 + 256 * WPR * b;
+            inputs(rx[b], ro[b], c, there ? part(a.cols, c) : 0, u[b], v[b]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float p, q;
+                f2unpack(v[b][j], p, q);
+                max_abs3(tv, p, q);
+                if (BACK) {
+                    f2unpack(u[b][j], p, q);
+                    max_abs3(tu, p, q);
+                }
+            }
+        }
+        Dot d;
+        const bool ok = d.begin<BLOCKS>(BACK ? tu : tv, tv);
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d.add(u[b][j], v[b][j]);
+        float dh, dl;
+        d.end(dh, dl);
+        add22(hi, lo, ok ? dh : __uint_as_float(0x7F800000u), dl);
+    }
+    warp_pair(hi, lo);
+    if (WPR > 1) {
+        if (lane == 0) parts[warp] = make_float2(hi, lo);
+        __syncthreads();
+        const int first = warp - mine;
+        hi = parts[first].x;
+        lo = parts[first].y;
+#pragma unroll
+        for (int k = 1; k < WPR; ++k) add22(hi, lo, parts[first + k].x, parts[first + k].y);
+    }
+    const float given = BACK && there ? a.rstd[row] : 0.0f;
+    float result = BACK ? slope_of(hi, lo, a.mean, given) : rstd_of(hi, lo, a.mean, a.eps);
+    // too large for float32's products (or not finite): in 64 bits
+    if (__syncthreads_or(!finite_f32(hi))) {
+        double s = 0.0;
+#pragma unroll 1
+        for (int64_t c = 256 * mine; c < a.cols; c += 256 * WPR) {
+            const int n = there ? part(a.cols, c) : 0;
+            const typename R::Raw rx = block_load<R>(a.x, row * a.ldx + c, n, a.vec, turn);
+            const typename R::Raw ro = a.other ? block_load<R>(a.other, row * a.ldo + c, n, a.vec, turn) : R::zero();
+            f2 u[4], v[4];
+            inputs(rx, ro, c, n, u, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float p, q, y, z;
+                f2unpack(u[j], p, q);
+                f2unpack(v[j], y, z);
+                s = __dadd_rn(s, __dadd_rn(__dmul_rn((double)p, (double)y), __dmul_rn((double)q, (double)z)));
+            }
+        }
+        s = warp_double(s);
+        if (lane == 0) wides[warp] = s;
+        __syncthreads();
+        s = 0.0;
+        for (int k = 0; k < WPR; ++k) s = __dadd_rn(s, wides[warp - mine + k]);
+        if (!finite_f32(hi)) {
+            if (BACK) result = (float)__dmul_rn(__ddiv_rn(s, (double)a.cols), __dmul_rn((double)given, (double)given));
+            else result = rstd_of(s, (double)a.cols, a.eps);
+        }
+    }
+    if (there && mine == 0 && lane == 0) a.result[row] = result;
+}
+
+// --------------------------------------------- tiles of 32 rows, 512 columns --
+
+constexpr int TILE_ROWS = 32, TILE_COLS = 512;
+constexpr int ROWS_EACH = TILE_ROWS / WARPS;         // rows of a warp
 
 __device__ __forceinline__ void async16(void *to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" : : "r"(smem_u32(to)), "l"(from) : "memory");
@@ -552,225 +670,181 @@ struct TileRow {
             *piece(lane, 1) = r.b;
         }
     }
-    // the block of a matrix on its way here; `there` columns exist.  What a lane
-    // gets is its own to read once its copies have landed (vec), or at once.
-    __device__ __forceinline__ void fetch(const void *p, int64_t from, int there, bool vec, typename R::Elem *turn) const {
+    // a lane's 8 on their way here: its own to read once the copies have landed
+    __device__ __forceinline__ void fetch(const typename R::Elem *q, bool exists) const {
         const int lane = threadIdx.x & 31;
-        if (vec && there - 8 * lane >= 8) {
-            const typename R::Elem *q = static_cast<const typename R::Elem *>(p) + from + 8 * lane;
-            async16(piece(lane, 0), q);
-            if (R::SIZE == 4) async16(piece(lane, 1), q + 4);
-        } else {
-            put(block_load<R>(p, from, there, vec, turn));
-        }
+        if (!exists) return put(R::zero());
+        async16(piece(lane, 0), q);
+        if (R::SIZE == 4) async16(piece(lane, 1), q + 4);
     }
 };
 __device__ __forceinline__ int column_at(int place) {        // the column of a 32-bit place, in its block of 256
     return 8 * ((place & 127) >> 2) + 4 * ((place >> 7) & 1) + (place & 3);
 }
 
-// What a cluster's CTAs tell one another: a pair for each row and 8 warps.
-struct Exchange {
-    float2 pairs[2][TILE_ROWS][4];
-    double wides[TILE_ROWS][4];
-};
-
-// The form along the columns of a tile of 32 rows: a thread takes two columns
-// (the two of a word of 16-bit values), and 32 rows of each.
-template <class R, int K>
+// The form along the columns of a tile: a thread takes two columns (the two of a
+// word of 16-bit values), and 32 rows of each.
+template <class R>
 __device__ __forceinline__ void hold_tile(const NormHeld &h, int64_t rb, int64_t col0, const typename R::Elem *tile) {
-    constexpr int PITCH = TILE_COLS * K;
+    const int64_t bytes = mx4_row_bytes(h.rows), atoms = mx4_atoms(h.rows), most = 128 * mx4_row_tiles(h.cols);
+    const bool in = rb < mx4_groups(h.rows);
+    auto column = [&](int64_t col, float top, const float v[32]) {
+        hold_column(in && col < h.cols ? h.c_codes + col * bytes + 16 * rb : nullptr,
+                    col < most ? h.c_scales + ((col >> 7) * atoms + (rb >> 2)) * MX4_ATOM + mx4_in_atom((int)(col & 127), (int)(rb & 3)) : nullptr, top, v);
+    };
     float v[32];
     if constexpr (R::SIZE == 2) {
         const uint32_t *from = reinterpret_cast<const uint32_t *>(tile) + threadIdx.x;
         uint32_t w[32], two = 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] = from[i * (PITCH / 2)];
+        for (int i = 0; i < 32; ++i) w[i] = from[i * (TILE_COLS / 2)];
 #pragma unroll
         for (int i = 0; i < 32; ++i) max_two<typename R::Type>(two, w[i]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = R::Type::to_f32(j ? w[i] >> 16 : w[i] & 0xFFFFu);
-            hold_column(h, rb, col0 + 2 * (int)threadIdx.x + j, R::Type::to_f32(j ? two >> 16 : two & 0xFFFFu), v);
+            column(col0 + 2 * (int)threadIdx.x + j, R::Type::to_f32(j ? two >> 16 : two & 0xFFFFu), v);
         }
     } else {
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < 2; ++j) {
-            const int place = (int)threadIdx.x + j * (PITCH / 2);
+            const int place = (int)threadIdx.x + j * (TILE_COLS / 2);
             float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(tile[i * PITCH + place]);
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(tile[i * TILE_COLS + place]);
 #pragma unroll
             for (int i = 0; i < 32; i += 2) max_abs3(top, v[i], v[i + 1]);
-            hold_column(h, rb, col0 + (place & ~255) + column_at(place & 255), top, v);
+            column(col0 + (place & ~255) + column_at(place & 255), top, v);
         }
     }
 }
 
-// A cluster of ceil(cols / (512 K)) CTAs takes 32 rows, a warp 4 of them, 512
-// columns of each.  All of a warp's inputs are on their way to shared memory at
-// once (what is in flight decides: with loads into registers, two rows at a
-// time, 4096 x 4096 bf16 in both forms took 57 us).  The rows' sums of squares;
-// the exchange; then the result in its own type in x's place, its form along the
-// rows from registers (4 lanes a group), and through shared memory the one along
-// the columns.  16 bits: x and the residual lie there and are added again for
-// the result; 32 bits: their sum takes x's place.
-template <class R, int K>
-__global__ void __launch_bounds__(THREADS *K, K == 1 ? 3 : 1)
-rms_tile_kernel(NormArgs a) {
+// A warp's share of a matrix: 4 rows, 8 apart, and two blocks of 256 columns.
+// VEC: rows are 16-byte aligned and whole pieces of 8, a lane's at `at`.
+template <class R, bool VEC>
+struct Share {
+    typename R::Elem *at;
+    int64_t step;
+    __device__ __forceinline__ Share(const void *p, int64_t ld, int64_t row, int64_t col)
+        : at(static_cast<typename R::Elem *>(const_cast<void *>(p)) + (row * ld + col) + (VEC ? 8 * (threadIdx.x & 31) : 0)), step(8 * ld) {}
+    __device__ __forceinline__ typename R::Elem *of(int i, int b) const { return at + i * step + 256 * b; }
+    // `there`: of the block's 256 columns, how many exist
+    __device__ __forceinline__ typename R::Raw load(int i, int b, int there, typename R::Elem *turn) const {
+        if constexpr (VEC) {
+            if (8 * (int)(threadIdx.x & 31) >= there) return R::zero();
+            return *reinterpret_cast<const typename R::Raw *>(of(i, b));
+        } else {
+            return block_load<R>(of(i, b), 0, there, false, turn);
+        }
+    }
+    __device__ __forceinline__ void store(int i, int b, int there, typename R::Elem *turn, const typename R::Raw &r) const {
+        if constexpr (VEC) {
+            if (8 * (int)(threadIdx.x & 31) < there) *reinterpret_cast<typename R::Raw *>(of(i, b)) = r;
+        } else {
+            block_store<R>(of(i, b), 0, there, false, turn, r);
+        }
+    }
+    __device__ __forceinline__ void fetch(const TileRow<R> &to, int i, int b, int there, typename R::Elem *turn) const {
+        if constexpr (VEC) to.fetch(of(i, b), 8 * (int)(threadIdx.x & 31) < there);
+        else to.put(load(i, b, there, turn));
+    }
+    // y with nothing past the matrix
+    static __device__ __forceinline__ typename R::Raw cut(const float v[8], int there) {
+        const int lane = threadIdx.x & 31;
+        typename R::Raw y = R::rounded(v);
+        if (there >= 256) return y;
+        if (VEC) return 8 * lane >= there ? R::zero() : y;
+        float u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = 8 * lane + j >= there ? 0.0f : v[j];
+        return R::rounded(u);
+    }
+};
+
+// Bytes of shared memory: inputs of 16 bits lie there (x, and the residual; of
+// the backward pass x, dy and what reaches the stream), of 32 bits x alone.
+template <class R>
+constexpr int tile_smem(bool back) { return TILE_ROWS * TILE_COLS * (R::SIZE == 4 ? 4 : back ? 6 : 4); }
+template <class R>
+constexpr int tile_ctas(bool back) { return R::SIZE == 4 || !back ? 3 : 2; }         // an SM
+
+// The result of a tile, rstd being known: a warp takes 4 rows, and all of its
+// inputs are on their way to shared memory at once.  The new stream; the result
+// in its own type in x's place, its form along the rows from registers (4 lanes
+// a group), and through shared memory the one along the columns.
+template <class R, bool VEC>
+__global__ void __launch_bounds__(THREADS, tile_ctas<R>(false))
+rms_tile_kernel(NormArgs a, int64_t block0, int col_blocks) {
     extern __shared__ __align__(16) uint8_t raw[];
-    __shared__ Exchange ex;
-    __shared__ float rstds[TILE_ROWS];
-    __shared__ __align__(16) typename R::Elem turns[WARPS * K][256];
-    constexpr int PITCH = TILE_COLS * K;
+    __shared__ __align__(16) typename R::Elem turns[VEC ? 1 : WARPS][VEC ? 8 : 256];
     constexpr bool TWO = R::SIZE == 2;               // both inputs in shared memory
-    typename R::Elem *xs = reinterpret_cast<typename R::Elem *>(raw), *rs = xs + TILE_ROWS * PITCH;
-    const cg::cluster_group cluster = cg::this_cluster();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kk = warp / WARPS, rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-    const int64_t rows = a.held.rows, cols = a.held.cols, rb = blockIdx.x / ranks, row0 = TILE_ROWS * rb;
-    const int64_t col0 = (int64_t)rank * PITCH + TILE_COLS * kk;                         // of the warp
-    const int there[2] = {part(cols, col0), part(cols, col0 + 256)};
-    typename R::Elem *turn = turns[warp];
-    auto row_at = [&](typename R::Elem *of, int i, int b) { return TileRow<R>{of + (warp % WARPS + WARPS * i) * PITCH + TILE_COLS * kk + 256 * b}; };
+    const int lane = threadIdx.x & 31, warp = warp_index();
+    const int64_t rb = block0 + blockIdx.x / col_blocks, row0 = TILE_ROWS * rb, col0 = (int64_t)(blockIdx.x % col_blocks) * TILE_COLS;
+    const int64_t rows = a.held.rows, cols = a.held.cols;
+    const int exist = (int)min((int64_t)TILE_ROWS, max((int64_t)0, rows - row0)), first = part(cols, col0), second = part(cols, col0 + 256);
+    typename R::Elem *turn = turns[VEC ? 0 : warp];
+    typename R::Elem *xs = reinterpret_cast<typename R::Elem *>(raw), *mine = xs + warp * TILE_COLS, *mine_r = mine + TILE_ROWS * TILE_COLS;
+    auto there = [&](int i, int b) { return warp + WARPS * i >= exist ? 0 : b ? second : first; };
+    auto place = [&](typename R::Elem *of, int i, int b) { return TileRow<R>{of + WARPS * i * TILE_COLS + 256 * b}; };
+    const Share<R, VEC> x(a.x, a.ldx, row0 + warp, col0), residual(a.residual, a.ldr, row0 + warp, col0), sum(a.sum, a.lds, row0 + warp, col0),
+        out(a.out, a.ldo, row0 + warp, col0);
+    const RowsOut rows_out(a.held, row0 + warp, col0);
     pdl_wait();
     pdl_trigger();
 #pragma unroll
     for (int i = 0; i < ROWS_EACH; ++i) {
-        const int64_t row = row0 + warp % WARPS + WARPS * i;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const int n = row < rows ? there[b] : 0;
-            row_at(xs, i, b).fetch(a.x, row * a.ldx + col0 + 256 * b, n, a.vec, turn);
-            if (TWO && a.residual) row_at(rs, i, b).fetch(a.residual, row * a.ldr + col0 + 256 * b, n, a.vec, turn);
+            x.fetch(place(mine, i, b), i, b, there(i, b), turn);
+            if (TWO && a.residual) residual.fetch(place(mine_r, i, b), i, b, there(i, b), turn);
         }
         asm volatile("cp.async.commit_group;" : : : "memory");
     }
-    auto input = [&](int i, int b, int64_t row, f2 h[4]) {           // x + residual
-        float v[8], q[8];
-        R::floats(row_at(xs, i, b).get(), v);
+    float rstds[ROWS_EACH];
+    f2 w[2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = f2pack(v[2 * j], v[2 * j + 1]);
-        if (!a.residual) return;
-        if constexpr (TWO) R::floats(row_at(rs, i, b).get(), q);
-        else R::floats(block_load<R>(a.residual, row * a.ldr + col0 + 256 * b, row < rows ? there[b] : 0, a.vec, turn), q);
+    for (int i = 0; i < ROWS_EACH; ++i) rstds[i] = warp + WARPS * i < exist ? a.rstd[row0 + warp + WARPS * i] : 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = add2(h[j], f2pack(q[2 * j], q[2 * j + 1]));
-    };
-    float hi[ROWS_EACH], lo[ROWS_EACH];
+    for (int b = 0; b < 2; ++b) {
+        float v[8];
+        weights8(a.w, a.w_kind, a.vec_w, col0 + 256 * b + 8 * lane, (b ? second : first) - 8 * lane, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[b][j] = f2pack(v[2 * j], v[2 * j + 1]);
+    }
 #pragma unroll
     for (int i = 0; i < ROWS_EACH; ++i) {
-        const int64_t row = row0 + warp % WARPS + WARPS * i;
         async_wait(ROWS_EACH - 1 - i);
-        f2 h[2][4];
-        float top = 0.0f;
+        const f2 rstd = both(rstds[i]);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            input(i, b, row, h[b]);
+            const int n = there(i, b);
+            f2 h[4];
             float v[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                f2unpack(h[b][j], v[2 * j], v[2 * j + 1]);
-                max_abs3(top, v[2 * j], v[2 * j + 1]);
-            }
-            if (a.residual) {
-                block_store<R>(a.sum, row * a.lds + col0 + 256 * b, row < rows ? there[b] : 0, a.vec, turn, R::rounded(v));
-                if (!TWO) row_at(xs, i, b).put(R::rounded(v));
-            }
-        }
-        Dot d;
-        const bool ok = d.begin<2>(top, top);
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d.add(h[b][j], h[b][j]);
-        d.end(hi[i], lo[i]);
-        if (!ok) hi[i] = __uint_as_float(0x7F800000u);
-    }
-    warp_pair4(hi, lo);
-    if ((lane & 7) == 0) ex.pairs[0][warp % WARPS + WARPS * (lane >> 3)][kk] = make_float2(hi[0], lo[0]);
-    cluster.sync();
-    float all = 0.0f, rest = 0.0f;
-    if (threadIdx.x < TILE_ROWS) {
-        for (int q = 0; q < ranks; ++q) {
-            const Exchange *other = cluster.map_shared_rank(&ex, q);
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const float2 p = other->pairs[0][threadIdx.x][k];
-                add22(all, rest, p.x, p.y);
-            }
-        }
-        rstds[threadIdx.x] = rstd_of(all, rest, a.mean, a.eps);
-    }
-    // the sum as the result is made from it: the residual is added again where it lies beside x
-    auto total = [&](int i, int b, int64_t row, f2 h[4]) {
-        if constexpr (TWO) {
-            input(i, b, row, h);
-        } else {
-            float v[8];
-            R::floats(row_at(xs, i, b).get(), v);
+            R::floats(place(mine, i, b).get(), v);
 #pragma unroll
             for (int j = 0; j < 4; ++j) h[j] = f2pack(v[2 * j], v[2 * j + 1]);
-        }
-    };
-    // too large for float32's squares (or not finite): in 64 bits; every CTA of
-    // the cluster has seen the same sums and comes here, or none does
-    if (__syncthreads_or(!finite_f32(all))) {
-#pragma unroll 1
-        for (int i = 0; i < ROWS_EACH; ++i) {
-            double s = 0.0;
-#pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
-                f2 h[4];
-                total(i, b, row0 + warp % WARPS + WARPS * i, h);
+            if (a.residual) {
+                float q[8];
+                if constexpr (TWO) R::floats(place(mine_r, i, b).get(), q);
+                else R::floats(residual.load(i, b, n, turn), q);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float x, y;
-                    f2unpack(h[j], x, y);
-                    s = __dadd_rn(s, __dadd_rn(__dmul_rn((double)x, (double)x), __dmul_rn((double)y, (double)y)));
+                    h[j] = add2(h[j], f2pack(q[2 * j], q[2 * j + 1]));
+                    f2unpack(h[j], v[2 * j], v[2 * j + 1]);
                 }
+                sum.store(i, b, n, turn, R::rounded(v));
             }
-            s = warp_double(s);
-            if (lane == 0) ex.wides[warp % WARPS + WARPS * i][kk] = s;
-        }
-        cluster.sync();
-        if (threadIdx.x < TILE_ROWS && !finite_f32(all)) {
-            double s = 0.0;
-            for (int q = 0; q < ranks; ++q)
-                for (int k = 0; k < K; ++k) s = __dadd_rn(s, cluster.map_shared_rank(&ex, q)->wides[threadIdx.x][k]);
-            rstds[threadIdx.x] = rstd_of(s, (double)cols, a.eps);
-        }
-        __syncthreads();
-    }
-    if (rank == 0 && threadIdx.x < TILE_ROWS && row0 + threadIdx.x < rows) a.rstd[row0 + threadIdx.x] = rstds[threadIdx.x];
-#pragma unroll 1
-    for (int b = 0; b < 2; ++b) {
-        const int64_t c = col0 + 256 * b;
-        float w[8];
-        weights8(a.w, a.w_kind, a.vec_w, c + 8 * lane, there[b] - 8 * lane, w);
-#pragma unroll 2
-        for (int i = 0; i < ROWS_EACH; ++i) {
-            const int64_t row = row0 + warp % WARPS + WARPS * i;
-            const int n = row < rows ? there[b] : 0;
-            f2 h[4];
-            total(i, b, row, h);
-            const f2 rstd = both(rstds[warp % WARPS + WARPS * i]);
-            float v[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f2unpack(mul2(mul2(h[j], rstd), f2pack(w[2 * j], w[2 * j + 1])), v[2 * j], v[2 * j + 1]);
-            if (n < 256) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) if (8 * lane + j >= n) v[j] = 0.0f;
-            }
-            const typename R::Raw y = R::rounded(v);
-            if (a.out) block_store<R>(a.out, row * a.ldo + c, n, a.vec, turn, y);
-            row_at(xs, i, b).put(y);
-            if (a.held.r_codes) hold_rows<R>(a.held, row, c + 8 * lane, y);
+            for (int j = 0; j < 4; ++j) f2unpack(mul2(mul2(h[j], rstd), w[b][j]), v[2 * j], v[2 * j + 1]);
+            const typename R::Raw y = Share<R, VEC>::cut(v, n);
+            if (a.out) out.store(i, b, n, turn, y);
+            place(mine, i, b).put(y);
+            if (a.held.r_codes) rows_out.template hold<R>(y, WARPS * i, b, warp + WARPS * i < exist);
         }
     }
     __syncthreads();
-    hold_tile<R, K>(a.held, rb, (int64_t)rank * PITCH, xs);
-    cluster.sync();                  // the others may still read this CTA's sums
+    hold_tile<R>(a.held, rb, col0, xs);
 }
 
 // ------------------------------------------------------------- backward --
@@ -779,286 +853,129 @@ struct BackArgs {
     const void *dy, *x, *w, *residual;
     const float *rstd;
     void *dx;
-    float *dw_parts;                 // [clusters][cols], or NULL
-    int64_t lddy, ldx, ldr, ldd;
+    float *dw_parts;                 // [parts][parts_pitch(cols)], or NULL
+    float *slopes;                   // [rows]
+    int64_t lddy, ldx, ldr, ldd, parts;
     int32_t w_kind;
     bool vec, vec_w;
     float minus_one;                 // -1, which the compiler does not know
     Mean mean;
     NormHeld held;
-    int64_t row_blocks;
 };
 
-// As rms_tile_kernel, a cluster taking row blocks b, b + clusters, ...: a lane
-// adds up its columns' part of dw over all of them.  Shared memory keeps both
-// inputs of 16 bits; of 32 bits x alone, and dy is read again.
-template <class R, int K>
-__global__ void __launch_bounds__(THREADS *K, K == 1 ? 2 : 1)
-rms_back_kernel(BackArgs a) {
+// The same of the backward pass, c being known: a CTA takes its 512 columns of
+// the row blocks b, b + parts, ... and adds up their part of dw (add: to what
+// the rows before have left).
+template <class R, bool VEC>
+__global__ void __launch_bounds__(THREADS, tile_ctas<R>(true))
+rms_back_kernel(BackArgs a, int64_t block0, int64_t block1, int col_blocks, int64_t pitch, bool add) {
     extern __shared__ __align__(16) uint8_t raw[];
-    __shared__ Exchange ex;
-    __shared__ float slopes[TILE_ROWS], rstds[TILE_ROWS];
-    __shared__ __align__(16) typename R::Elem turns[WARPS * K][256];
-    constexpr int PITCH = TILE_COLS * K;
+    __shared__ __align__(16) typename R::Elem turns[VEC ? 1 : WARPS][VEC ? 8 : 256];
     constexpr bool TWO = R::SIZE == 2;
-    typename R::Elem *xs = reinterpret_cast<typename R::Elem *>(raw), *ys = xs + TILE_ROWS * PITCH;
-    const cg::cluster_group cluster = cg::this_cluster();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kk = warp / WARPS, rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-    const int64_t rows = a.held.rows, cols = a.held.cols, col0 = (int64_t)rank * PITCH + TILE_COLS * kk;
-    const int there[2] = {part(cols, col0), part(cols, col0 + 256)};
-    typename R::Elem *turn = turns[warp];
-    auto row_at = [&](typename R::Elem *of, int i, int b) { return TileRow<R>{of + (warp % WARPS + WARPS * i) * PITCH + TILE_COLS * kk + 256 * b}; };
+    constexpr int TILE = TILE_ROWS * TILE_COLS;
+    const int lane = threadIdx.x & 31, warp = warp_index();
+    const int64_t part_index = blockIdx.x / col_blocks, col0 = (int64_t)(blockIdx.x % col_blocks) * TILE_COLS;
+    const int64_t rows = a.held.rows, cols = a.held.cols;
+    const int first = part(cols, col0), second = part(cols, col0 + 256);
+    typename R::Elem *turn = turns[VEC ? 0 : warp];
+    typename R::Elem *xs = reinterpret_cast<typename R::Elem *>(raw), *mine = xs + warp * TILE_COLS;
+    auto place = [&](int matrix, int i, int b) { return TileRow<R>{mine + matrix * TILE + WARPS * i * TILE_COLS + 256 * b}; };
     pdl_wait();
     pdl_trigger();
     f2 w[2][4], dw[2][4] = {};
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         float v[8];
-        weights8(a.w, a.w_kind, a.vec_w, col0 + 256 * b + 8 * lane, there[b] - 8 * lane, v);
+        weights8(a.w, a.w_kind, a.vec_w, col0 + 256 * b + 8 * lane, (b ? second : first) - 8 * lane, v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[b][j] = f2pack(v[2 * j], v[2 * j + 1]);
     }
-    int turns_taken = 0;
-    for (int64_t rb = blockIdx.x / ranks; rb < a.row_blocks; rb += gridDim.x / ranks, turns_taken ^= 1) {
+    const f2 minus = both(a.minus_one);
+    for (int64_t rb = block0 + part_index; rb < block1; rb += a.parts) {
         const int64_t row0 = TILE_ROWS * rb;
+        const int exist = (int)min((int64_t)TILE_ROWS, max((int64_t)0, rows - row0));
+        auto there = [&](int i, int b) { return warp + WARPS * i >= exist ? 0 : b ? second : first; };
+        const Share<R, VEC> x(a.x, a.ldx, row0 + warp, col0), dy(a.dy, a.lddy, row0 + warp, col0), residual(a.residual, a.ldr, row0 + warp, col0),
+            dx(a.dx, a.ldd, row0 + warp, col0);
+        const RowsOut rows_out(a.held, row0 + warp, col0);
 #pragma unroll
         for (int i = 0; i < ROWS_EACH; ++i) {
-            const int64_t row = row0 + warp % WARPS + WARPS * i;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int n = row < rows ? there[b] : 0;
-                row_at(xs, i, b).fetch(a.x, row * a.ldx + col0 + 256 * b, n, a.vec, turn);
-                if (TWO) row_at(ys, i, b).fetch(a.dy, row * a.lddy + col0 + 256 * b, n, a.vec, turn);
+                x.fetch(place(0, i, b), i, b, there(i, b), turn);
+                if (TWO) dy.fetch(place(1, i, b), i, b, there(i, b), turn);
+                if (TWO && a.residual) residual.fetch(place(2, i, b), i, b, there(i, b), turn);
             }
             asm volatile("cp.async.commit_group;" : : : "memory");
         }
-        auto gradient = [&](int i, int b, int64_t row, f2 g[4]) {
-            float v[8];
-            if constexpr (TWO) R::floats(row_at(ys, i, b).get(), v);
-            else R::floats(block_load<R>(a.dy, row * a.lddy + col0 + 256 * b, row < rows ? there[b] : 0, a.vec, turn), v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) g[j] = f2pack(v[2 * j], v[2 * j + 1]);
-        };
-        float hi[ROWS_EACH], lo[ROWS_EACH];
+        float rstds[ROWS_EACH], slopes[ROWS_EACH];
 #pragma unroll
         for (int i = 0; i < ROWS_EACH; ++i) {
-            const int64_t row = row0 + warp % WARPS + WARPS * i;
-            const f2 rstd = both(row < rows ? a.rstd[row] : 0.0f);
+            const bool in = warp + WARPS * i < exist;
+            rstds[i] = in ? a.rstd[row0 + warp + WARPS * i] : 0.0f;
+            slopes[i] = in ? a.slopes[row0 + warp + WARPS * i] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS_EACH; ++i) {
             async_wait(ROWS_EACH - 1 - i);
-            f2 g[2][4], x[2][4];
-            float tg = 0.0f, tx = 0.0f;
+            const f2 rstd = both(rstds[i]), slope = both(slopes[i]);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                float v[8];
-                gradient(i, b, row, g[b]);
-                R::floats(row_at(xs, i, b).get(), v);
+                const int n = there(i, b);
+                float u[8], v[8];
+                if constexpr (TWO) R::floats(place(1, i, b).get(), v);
+                else R::floats(dy.load(i, b, n, turn), v);
+                R::floats(place(0, i, b).get(), u);
+                // dw; (g w - x slope) rstd, each rounded
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x[b][j] = f2pack(v[2 * j], v[2 * j + 1]);
-                    dw[b][j] = fma2(g[b][j], mul2(x[b][j], rstd), dw[b][j]);
-                    g[b][j] = mul2(g[b][j], w[b][j]);
-                    float p, q;
-                    f2unpack(g[b][j], p, q);
-                    max_abs3(tg, p, q);
-                    max_abs3(tx, v[2 * j], v[2 * j + 1]);
+                    const f2 g = f2pack(v[2 * j], v[2 * j + 1]), z = f2pack(u[2 * j], u[2 * j + 1]);
+                    dw[b][j] = fma2(g, mul2(z, rstd), dw[b][j]);
+                    f2unpack(mul2(fma2(mul2(z, slope), minus, mul2(g, w[b][j])), rstd), v[2 * j], v[2 * j + 1]);
                 }
-            }
-            Dot d;
-            if (d.begin<2>(tg, tx)) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) d.add(g[b][j], x[b][j]);
-                d.end(hi[i], lo[i]);
-            } else {                                 // far outside of any gradient's range: in 64 bits
-                double s = 0.0;
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float p, q, u, v;
-                        f2unpack(g[b][j], p, q);
-                        f2unpack(x[b][j], u, v);
-                        s = __dadd_rn(s, __dadd_rn(__dmul_rn((double)p, (double)u), __dmul_rn((double)q, (double)v)));
-                    }
-                hi[i] = (float)s;
-                lo[i] = finite_f32(hi[i]) ? (float)(s - (double)hi[i]) : 0.0f;
-            }
-        }
-        warp_pair4(hi, lo);
-        if ((lane & 7) == 0) ex.pairs[turns_taken][warp % WARPS + WARPS * (lane >> 3)][kk] = make_float2(hi[0], lo[0]);
-        cluster.sync();
-        if (threadIdx.x < TILE_ROWS) {
-            float all = 0.0f, rest = 0.0f;
-            for (int q = 0; q < ranks; ++q) {
-                const Exchange *other = cluster.map_shared_rank(&ex, q);
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    const float2 p = other->pairs[turns_taken][threadIdx.x][k];
-                    add22(all, rest, p.x, p.y);
-                }
-            }
-            const float rstd = row0 + threadIdx.x < rows ? a.rstd[row0 + threadIdx.x] : 0.0f;
-            rstds[threadIdx.x] = rstd;
-            slopes[threadIdx.x] = slope_of(all, rest, a.mean, rstd);
-        }
-        __syncthreads();
-        const f2 minus = both(a.minus_one);
-#pragma unroll 2
-        for (int i = 0; i < ROWS_EACH; ++i) {
-            const int64_t row = row0 + warp % WARPS + WARPS * i;
-            const f2 rstd = both(rstds[warp % WARPS + WARPS * i]), slope = both(slopes[warp % WARPS + WARPS * i]);
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int64_t c = col0 + 256 * b;
-                const int n = row < rows ? there[b] : 0;
-                float x[8], v[8];
-                typename R::Raw q;
-                if (a.residual) q = block_load<R>(a.residual, row * a.ldr + c, n, a.vec, turn);
-                f2 g[4];
-                gradient(i, b, row, g);
-                R::floats(row_at(xs, i, b).get(), x);
-                // (g w - x slope) rstd, each rounded
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    f2unpack(mul2(fma2(mul2(f2pack(x[2 * j], x[2 * j + 1]), slope), minus, mul2(g[j], w[b][j])), rstd), v[2 * j], v[2 * j + 1]);
                 if (a.residual) {
                     float r[8];
-                    R::floats(q, r);
+                    if constexpr (TWO) R::floats(place(2, i, b).get(), r);
+                    else R::floats(residual.load(i, b, n, turn), r);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], r[j]);
                 }
-                if (n < 256) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) if (8 * lane + j >= n) v[j] = 0.0f;
-                }
-                const typename R::Raw y = R::rounded(v);
-                block_store<R>(a.dx, row * a.ldd + c, n, a.vec, turn, y);
-                if (a.held.c_codes) row_at(xs, i, b).put(y);
-                if (a.held.r_codes) hold_rows<R>(a.held, row, c + 8 * lane, y);
+                const typename R::Raw y = Share<R, VEC>::cut(v, n);
+                dx.store(i, b, n, turn, y);
+                if (a.held.c_codes) place(0, i, b).put(y);
+                if (a.held.r_codes) rows_out.template hold<R>(y, WARPS * i, b, warp + WARPS * i < exist);
             }
         }
-        __syncthreads();
         if (a.held.c_codes) {
-            hold_tile<R, K>(a.held, rb, (int64_t)rank * PITCH, xs);
+            __syncthreads();
+            hold_tile<R>(a.held, rb, col0, xs);
             __syncthreads();
         }
     }
     // the 8 warps' parts of dw, in their order
-    if (a.dw_parts) {
-        float *tile = reinterpret_cast<float *>(raw);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f2unpack(dw[b][j], v[2 * j], v[2 * j + 1]);
-            TileRow<RowF32>{reinterpret_cast<uint32_t *>(tile + (warp % WARPS) * PITCH + TILE_COLS * kk + 256 * b)}.put(RowF32::rounded(v));
-        }
-        __syncthreads();
-        for (int place = threadIdx.x; place < PITCH; place += THREADS * K) {
-            float s = tile[place];
-#pragma unroll
-            for (int i = 1; i < WARPS; ++i) s = __fadd_rn(s, tile[i * PITCH + place]);
-            const int64_t col = (int64_t)rank * PITCH + (place & ~255) + column_at(place & 255);
-            if (col < cols) a.dw_parts[blockIdx.x / ranks * cols + col] = s;
-        }
-    }
-    cluster.sync();                  // the others may still read this CTA's sums
-}
-
-// Rows longer than a cluster holds: a CTA a row, both inputs read twice.
-template <class R>
-__global__ void __launch_bounds__(THREADS)
-rms_back_rows_kernel(BackArgs a) {
-    __shared__ float2 parts[WARPS];
-    __shared__ __align__(16) typename R::Elem turns[WARPS][256];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = blockIdx.x, cols = a.held.cols;
-    typename R::Elem *turn = turns[warp];
-    pdl_wait();
-    pdl_trigger();
-    const float rstd = a.rstd[row];
-    float hi = 0.0f, lo = 0.0f;
-    auto inputs = [&](int64_t c, float g[8], float x[8]) {           // g: times the weight
-        float w[8];
-        const int n = part(cols, c);
-        R::floats(block_load<R>(a.dy, row * a.lddy + c, n, a.vec, turn), g);
-        R::floats(block_load<R>(a.x, row * a.ldx + c, n, a.vec, turn), x);
-        weights8(a.w, a.w_kind, a.vec_w, c + 8 * lane, n - 8 * lane, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = __fmul_rn(g[j], w[j]);
-    };
-    for (int64_t c = 256 * warp; c < cols; c += 8 * THREADS) {
-        float g[8], x[8], tg = 0.0f, tx = 0.0f;
-        inputs(c, g, x);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            max_abs3(tg, g[j], g[j + 1]);
-            max_abs3(tx, x[j], x[j + 1]);
-        }
-        Dot d;
-        float dh, dl;
-        if (d.begin<1>(tg, tx)) {
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) d.add(f2pack(g[j], g[j + 1]), f2pack(x[j], x[j + 1]));
-            d.end(dh, dl);
-        } else {
-            double s = 0.0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s = __dadd_rn(s, __dmul_rn((double)g[j], (double)x[j]));
-            dh = (float)s;
-            dl = finite_f32(dh) ? (float)(s - (double)dh) : 0.0f;
-        }
-        add22(hi, lo, dh, dl);
-    }
-    warp_pair(hi, lo);
-    if (lane == 0) parts[warp] = make_float2(hi, lo);
+    if (!a.dw_parts) return;
     __syncthreads();
-    hi = parts[0].x;
-    lo = parts[0].y;
-    for (int k = 1; k < WARPS; ++k) add22(hi, lo, parts[k].x, parts[k].y);
-    const float slope = slope_of(hi, lo, a.mean, rstd);
-    for (int64_t c = 256 * warp; c < cols; c += 8 * THREADS) {
-        float v[8], x[8];
-        const int n = part(cols, c);
-        inputs(c, v, x);
+    float *tile = reinterpret_cast<float *>(raw);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fsub_rn(v[j], __fmul_rn(x[j], slope)), rstd);
-        if (a.residual) {
-            float q[8];
-            R::floats(block_load<R>(a.residual, row * a.ldr + c, n, a.vec, turn), q);
+    for (int b = 0; b < 2; ++b) {
+        float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], q[j]);
-        }
-        block_store<R>(a.dx, row * a.ldd + c, n, a.vec, turn, R::rounded(v));
+        for (int j = 0; j < 4; ++j) f2unpack(dw[b][j], v[2 * j], v[2 * j + 1]);
+        TileRow<RowF32>{reinterpret_cast<uint32_t *>(tile + warp * TILE_COLS + 256 * b)}.put(RowF32::rounded(v));
     }
-}
-// Their part of dw: 2048 columns of the rows b, b + gridDim.y, ...
-template <class R>
-__global__ void __launch_bounds__(THREADS)
-rms_back_weight_kernel(BackArgs a) {
-    __shared__ __align__(16) typename R::Elem turns[WARPS][256];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t cols = a.held.cols, c = 256 * ((int64_t)blockIdx.x * WARPS + warp);
-    const int n = part(cols, c);
-    pdl_wait();
-    pdl_trigger();
-    float dw[8] = {};
-    for (int64_t row = blockIdx.y; row < a.held.rows; row += gridDim.y) {
-        const float rstd = a.rstd[row];
-        float v[8], x[8];
-        R::floats(block_load<R>(a.dy, row * a.lddy + c, n, a.vec, turns[warp]), v);
-        R::floats(block_load<R>(a.x, row * a.ldx + c, n, a.vec, turns[warp]), x);
+    __syncthreads();
+    for (int at = threadIdx.x; at < TILE_COLS; at += THREADS) {
+        float s = tile[at];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw[j] = __fmaf_rn(v[j], __fmul_rn(x[j], rstd), dw[j]);
+        for (int i = 1; i < WARPS; ++i) s = __fadd_rn(s, tile[i * TILE_COLS + at]);
+        float *to = a.dw_parts + part_index * pitch + col0 + (at & ~255) + column_at(at & 255);
+        *to = add ? __fadd_rn(*to, s) : s;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) if (8 * lane + j < n) a.dw_parts[blockIdx.y * cols + c + 8 * lane + j] = dw[j];
 }
 
 // dw from its parts, in their order: 32 columns a CTA, 8 shares of the parts.
 __global__ void __launch_bounds__(THREADS)
-rms_weight_kernel(const float *parts, int n, int64_t cols, void *dw, int kind) {
+rms_weight_kernel(const float *parts, int n, int64_t cols, int64_t pitch, void *dw, int kind) {
     __shared__ float share[WARPS][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = 32 * (int64_t)blockIdx.x + lane;
@@ -1070,11 +987,11 @@ rms_weight_kernel(const float *parts, int n, int64_t cols, void *dw, int kind) {
         for (; i + 7 * WARPS < n; i += 8 * WARPS) {          // 8 loads in flight
             float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = parts[(i + j * WARPS) * cols + c];
+            for (int j = 0; j < 8; ++j) v[j] = parts[(i + j * WARPS) * pitch + c];
 #pragma unroll
             for (int j = 0; j < 8; ++j) s = __fadd_rn(s, v[j]);
         }
-        for (; i < n; i += WARPS) s = __fadd_rn(s, parts[i * cols + c]);
+        for (; i < n; i += WARPS) s = __fadd_rn(s, parts[i * pitch + c]);
     }
     share[warp][lane] = s;
     __syncthreads();
@@ -1106,42 +1023,87 @@ static cudaError_t rows_of(const NormArgs &a, int64_t grid_rows, cudaStream_t s)
     return rows_launch<R, 8, 0>(a, grid_rows, s);
 }
 
-// CTAs of a cluster, and warps of a CTA by 8, for rows of these columns.
-static void tile_shape(int64_t cols, unsigned &ctas, int &k) {
-    k = cols <= 8 * TILE_COLS ? 1 : cols <= 16 * TILE_COLS ? 2 : 3;
-    ctas = (unsigned)((cols + TILE_COLS * k - 1) / (TILE_COLS * k));
+// Rows whose two inputs take about half of L2, a multiple of 256 (whole atoms of
+// the scales along the columns): they are summed, and read again from there.
+static int64_t rows_at_once(int64_t cols, int size) {
+    const int64_t fit = ((int64_t)64 << 20) / (2 * cols * size) / 256 * 256;
+    return fit > 256 ? fit : 256;
+}
+
+template <class R, bool BACK>
+static cudaError_t sums_launch(const SumArgs &a, int64_t end, cudaStream_t s) {
+    // as many warps a row as give every SM 16
+    const int64_t rows = end - a.row0;
+    auto go = [&](auto kernel, int wpr) { return launch_dependent(kernel, (unsigned)((rows * wpr + WARPS - 1) / WARPS), THREADS, 0, 1, s, a); };
+    if (rows >= 2432 || a.cols <= 1024) return go(rms_sums_kernel<R, 1, BACK>, 1);
+    if (rows >= 1216 || a.cols <= 2048) return go(rms_sums_kernel<R, 2, BACK>, 2);
+    if (rows >= 608 || a.cols <= 4096) return go(rms_sums_kernel<R, 4, BACK>, 4);
+    return go(rms_sums_kernel<R, 8, BACK>, 8);
 }
 
 template <class... P>
-static cudaError_t tile_launch(void (*kernel)(P...), std::atomic<bool> (&set)[64], int k, unsigned ctas, int64_t clusters, cudaStream_t s, const P &...args) {
+static cudaError_t tile_launch(void (*kernel)(P...), std::atomic<bool> (&set)[64], int smem, int64_t grid, cudaStream_t s, const P &...args) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (dev < 0 || dev >= 64 || grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
     if (!set[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tile_smem(k));
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_relaxed);
     }
-    return launch_dependent(kernel, (unsigned)(ctas * clusters), THREADS * k, tile_smem(k), ctas, s, args...);
+    return launch_dependent(kernel, (unsigned)grid, THREADS, smem, 1, s, args...);
 }
 
-template <class R, int K>
-static cudaError_t norm_tile(const NormArgs &a, unsigned ctas, cudaStream_t s) {
+static int col_blocks_of(int64_t cols) { return (int)((cols + TILE_COLS - 1) / TILE_COLS); }
+
+template <class R, bool VEC>
+static cudaError_t norm_tile(const NormArgs &a, int64_t block0, int64_t blocks, cudaStream_t s) {
     static std::atomic<bool> set[64];
-    return tile_launch(rms_tile_kernel<R, K>, set, K, ctas, 4 * mx4_atoms(a.held.rows), s, a);
+    const int cb = col_blocks_of(a.held.cols);
+    return tile_launch(rms_tile_kernel<R, VEC>, set, tile_smem<R>(false), blocks * cb, s, a, block0, cb);
 }
-template <class R, int K>
-static cudaError_t back_tile(const BackArgs &a, unsigned ctas, int64_t clusters, cudaStream_t s) {
-    static std::atomic<bool> set[64];
-    return tile_launch(rms_back_kernel<R, K>, set, K, ctas, clusters, s, a);
+template <class R>
+static cudaError_t norm_tiles(const NormArgs &a, cudaStream_t s) {
+    const int64_t rows = a.held.rows, cols = a.held.cols, step = rows_at_once(cols, R::SIZE), all = 4 * mx4_atoms(rows);
+    const bool pieces = a.vec && cols % 8 == 0;
+    for (int64_t r = 0; r < rows; r += step) {
+        const int64_t end = rows - r > step ? r + step : rows, block0 = r / TILE_ROWS, blocks = (end == rows ? all : end / TILE_ROWS) - block0;
+        const SumArgs sums = {a.x, a.residual, nullptr, a.ldx, a.ldr, rows, cols, r, 0, a.vec, true, a.eps, a.mean, nullptr, a.rstd};
+        cudaError_t e = sums_launch<R, false>(sums, end, s);
+        if (e == cudaSuccess) e = pieces ? norm_tile<R, true>(a, block0, blocks, s) : norm_tile<R, false>(a, block0, blocks, s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 // Parts of dw: a number of the sizes alone, so that a sum has the same bits
 // whatever forms are asked for.  256 of them keep scratch small and the GPU busy.
-static int64_t back_parts(int64_t rows, int64_t cols) {
-    const int64_t blocks = (rows + TILE_ROWS - 1) / TILE_ROWS, most = cols > TILE_MOST ? 64 : 256;
-    return blocks < most ? blocks : most;
+static int64_t back_parts(int64_t rows) {
+    const int64_t blocks = (rows + TILE_ROWS - 1) / TILE_ROWS;
+    return blocks < 256 ? blocks : 256;
+}
+static int64_t parts_pitch(int64_t cols) { return (cols + TILE_COLS - 1) / TILE_COLS * TILE_COLS; }
+
+template <class R, bool VEC>
+static cudaError_t back_tile(const BackArgs &a, int64_t block0, int64_t block1, bool add, cudaStream_t s) {
+    static std::atomic<bool> set[64];
+    const int cb = col_blocks_of(a.held.cols);
+    return tile_launch(rms_back_kernel<R, VEC>, set, tile_smem<R>(true), a.parts * cb, s, a, block0, block1, cb, parts_pitch(a.held.cols), add);
+}
+template <class R>
+static cudaError_t back_tiles(const BackArgs &a, cudaStream_t s) {
+    const int64_t rows = a.held.rows, cols = a.held.cols, step = rows_at_once(cols, R::SIZE);
+    const int64_t all = a.held.c_codes ? 4 * mx4_atoms(rows) : a.held.r_codes ? 4 * mx4_row_tiles(rows) : (rows + TILE_ROWS - 1) / TILE_ROWS;
+    const bool pieces = a.vec && cols % 8 == 0;
+    for (int64_t r = 0; r < rows; r += step) {
+        const int64_t end = rows - r > step ? r + step : rows, block0 = r / TILE_ROWS, block1 = end == rows ? all : end / TILE_ROWS;
+        const SumArgs sums = {a.x, a.dy, a.w, a.ldx, a.lddy, rows, cols, r, a.w_kind, a.vec, a.vec_w, 0.0f, a.mean, a.rstd, a.slopes};
+        cudaError_t e = sums_launch<R, true>(sums, end, s);
+        if (e == cudaSuccess) e = pieces ? back_tile<R, true>(a, block0, block1, r > 0, s) : back_tile<R, false>(a, block0, block1, r > 0, s);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 template <class F>
@@ -1235,33 +1197,18 @@ zs_status zs_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t 
         return r;
     if (!out && !r_codes && !c_codes) return zs_fail(ZS_EINVAL, "%s: no form of the result is asked for", fn);
     using namespace zsk;
-    if (c_codes && cols > TILE_MOST && !out)
-        return zs_fail(ZS_EINVAL, "%s: along the columns of more than %d columns needs out", fn, (int)TILE_MOST);
     NormArgs a;
     a.x = x; a.residual = residual; a.w = weight; a.sum = sum; a.out = out; a.rstd = rstd;
     a.ldx = ldx; a.ldr = ldr; a.lds = lds; a.ldo = ldo;
     a.w_kind = weight_dtype; a.vec = vec; a.vec_w = vec_w; a.eps = eps; a.mean = mean_of(cols);
-    const bool tiles = c_codes && cols <= TILE_MOST;
-    a.held = {static_cast<uint8_t *>(r_codes), static_cast<uint8_t *>(r_scales), tiles ? static_cast<uint8_t *>(c_codes) : nullptr,
-              tiles ? static_cast<uint8_t *>(c_scales) : nullptr, rows, cols};
+    a.held = {static_cast<uint8_t *>(r_codes), static_cast<uint8_t *>(r_scales), static_cast<uint8_t *>(c_codes), static_cast<uint8_t *>(c_scales), rows, cols};
     const cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e;
-    if (tiles) {
-        unsigned ctas;
-        int k;
-        tile_shape(cols, ctas, k);
-        if (4 * mx4_atoms(rows) * ctas > 0x7FFFFFFF) return zs_fail(ZS_EINVAL, "%s: %lld x %lld too large", fn, (long long)rows, (long long)cols);
-        e = by_type(dtype, [&](auto t) {
-            typedef decltype(t) R;
-            return k == 1 ? norm_tile<R, 1>(a, ctas, s) : k == 2 ? norm_tile<R, 2>(a, ctas, s) : norm_tile<R, 3>(a, ctas, s);
-        });
-        return cuda_status(e, fn);
+    if (!c_codes) {
+        // the rows' tiles of scales have to be whole
+        const int64_t grid_rows = r_codes ? 128 * mx4_row_tiles(rows) : rows;
+        return cuda_status(by_type(dtype, [&](auto t) { return rows_of<decltype(t)>(a, grid_rows, s); }), fn);
     }
-    // the rows' tiles of scales have to be whole
-    const int64_t grid_rows = r_codes ? 128 * mx4_row_tiles(rows) : rows;
-    e = by_type(dtype, [&](auto t) { return rows_of<decltype(t)>(a, grid_rows, s); });
-    if (e != cudaSuccess || !c_codes) return cuda_status(e, fn);
-    return zs_mx4_quantize(out, rows, cols, ldo, dtype, nullptr, nullptr, c_codes, c_scales, stream);
+    return cuda_status(by_type(dtype, [&](auto t) { return norm_tiles<decltype(t)>(a, s); }), fn);
 }
 
 zs_status zs_rms_norm_scratch(int64_t rows, int64_t cols, int64_t *bytes) {
@@ -1269,7 +1216,7 @@ zs_status zs_rms_norm_scratch(int64_t rows, int64_t cols, int64_t *bytes) {
     if (!bytes) return zs_fail(ZS_EINVAL, "%s: NULL result", fn);
     if (rows < 0 || cols < 0 || rows >= MOST || cols >= MOST)
         return zs_fail(ZS_EINVAL, "%s: %lld x %lld out of range", fn, (long long)rows, (long long)cols);
-    *bytes = rows > 0 && cols > 0 ? zsk::back_parts(rows, cols) * cols * 4 : 0;
+    *bytes = rows > 0 && cols > 0 ? 4 * (zsk::back_parts(rows) * zsk::parts_pitch(cols) + rows) : 0;
     zs_clear_error();
     return ZS_OK;
 }
@@ -1293,49 +1240,21 @@ zs_status zs_rms_norm_backward(const void *dy, int64_t lddy, const void *x, int6
     }
     if ((r = check_vector(weight, weight_dtype, true, &vec_w, "weight", fn)) || (r = check_vector(rstd, ZS_DTYPE_FP32, true, nullptr, "rstd", fn)))
         return r;
-    if (dw && (!scratch || addr(scratch) % 16)) return zs_fail(ZS_EINVAL, "%s: scratch NULL or not 16-byte aligned", fn);
+    if (!scratch || addr(scratch) % 16) return zs_fail(ZS_EINVAL, "%s: scratch NULL or not 16-byte aligned", fn);
     using namespace zsk;
-    const bool tiles = cols <= TILE_MOST;
     BackArgs a;
-    a.dy = dy; a.x = x; a.w = weight; a.residual = residual; a.rstd = rstd; a.dx = dx; a.dw_parts = dw ? scratch : nullptr;
+    a.dy = dy; a.x = x; a.w = weight; a.residual = residual; a.rstd = rstd; a.dx = dx;
+    a.parts = back_parts(rows);
+    a.dw_parts = dw ? scratch : nullptr;
+    a.slopes = scratch + a.parts * parts_pitch(cols);
     a.lddy = lddy; a.ldx = ldx; a.ldr = ldr; a.ldd = lddx;
     a.w_kind = weight_dtype; a.vec = vec; a.vec_w = vec_w; a.minus_one = -1.0f; a.mean = mean_of(cols);
     a.held = {static_cast<uint8_t *>(r_codes), static_cast<uint8_t *>(r_scales), static_cast<uint8_t *>(c_codes),
               static_cast<uint8_t *>(c_scales), rows, cols};
-    a.row_blocks = c_codes ? 4 * mx4_atoms(rows) : r_codes ? 4 * mx4_row_tiles(rows) : (rows + TILE_ROWS - 1) / TILE_ROWS;
-    const int64_t parts = back_parts(rows, cols);
-    cudaError_t e;
-    if (tiles) {
-        unsigned ctas;
-        int k;
-        tile_shape(cols, ctas, k);
-        e = by_type(dtype, [&](auto t) {
-            typedef decltype(t) R;
-            return k == 1 ? back_tile<R, 1>(a, ctas, parts, s) : k == 2 ? back_tile<R, 2>(a, ctas, parts, s) : back_tile<R, 3>(a, ctas, parts, s);
-        });
-    } else {
-        e = by_type(dtype, [&](auto t) {
-            typedef decltype(t) R;
-            cudaError_t f = cudaSuccess;
-            if (dw) {                                // first: dx may be dy's memory
-                cudaLaunchConfig_t cfg = {};
-                cfg.gridDim = dim3((unsigned)((cols + 8 * THREADS - 1) / (8 * THREADS)), (unsigned)parts);
-                cfg.blockDim = dim3(THREADS);
-                cfg.stream = s;
-                cudaLaunchAttribute attr[1];
-                attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-                attr[0].val.programmaticStreamSerializationAllowed = 1;
-                cfg.attrs = attr;
-                cfg.numAttrs = 1;
-                f = cudaLaunchKernelEx(&cfg, rms_back_weight_kernel<R>, a);
-            }
-            return f != cudaSuccess ? f : launch_dependent(rms_back_rows_kernel<R>, (unsigned)rows, THREADS, 0, 1, s, a);
-        });
-    }
+    cudaError_t e = by_type(dtype, [&](auto t) { return back_tiles<decltype(t)>(a, s); });
     if (e == cudaSuccess && dw)
-        e = launch_dependent(rms_weight_kernel, (unsigned)((cols + 31) / 32), THREADS, 0, 1, s, scratch, (int)parts, cols, dw, dw_dtype);
-    if (e != cudaSuccess || tiles || (!r_codes && !c_codes)) return cuda_status(e, fn);
-    return zs_mx4_quantize(dx, rows, cols, lddx, dtype, r_codes, r_scales, c_codes, c_scales, stream);
+        e = launch_dependent(rms_weight_kernel, (unsigned)((cols + 31) / 32), THREADS, 0, 1, s, a.dw_parts, (int)a.parts, cols, parts_pitch(cols), dw, dw_dtype);
+    return cuda_status(e, fn);
 }
 
 }  // extern "C"
