@@ -344,16 +344,16 @@ __device__ __forceinline__ int warp_index() { return __shfl_sync(0xFFFFFFFFu, (i
 struct RowsOut {
     uint8_t *codes, *scales;         // of the lane's 8 columns
     int64_t bytes;                   // of a row of codes
-    uint32_t in, writes;             // bit b: of this block and the next, the group exists; this lane writes the scales of the row's four
+    uint32_t in, writes;             // bit b: of this block and the next, the group exists; this lane writes its scale
     __device__ __forceinline__ RowsOut(const NormHeld &h, int64_t row, int64_t col) {
         const int lane = threadIdx.x & 31;
         bytes = mx4_row_bytes(h.cols);
         codes = h.r_codes + (row * bytes + col / 2) + 4 * lane;
         const int64_t atoms = mx4_atoms(h.cols), atom = col / (4 * MX4_GROUP);
-        scales = h.r_scales + ((row >> 7) * atoms + atom) * MX4_ATOM + mx4_in_atom((int)(row & 127), 0) + MX4_ATOM * (lane >> 4);
+        scales = h.r_scales + ((row >> 7) * atoms + atom) * MX4_ATOM + mx4_in_atom((int)(row & 127), 0) + MX4_ATOM * (lane >> 4) + ((lane >> 2) & 3);
         const int groups = (int)min((int64_t)16, mx4_groups(h.cols) - col / MX4_GROUP), left = row < 128 * mx4_row_tiles(h.rows) ? (int)min((int64_t)4, atoms - atom) : 0;
         in = ((lane >> 2) < groups ? 1u : 0u) | (8 + (lane >> 2) < groups ? 2u : 0u);
-        writes = (lane & 15) ? 0u : ((lane >> 4) < left ? 1u : 0u) | (2 + (lane >> 4) < left ? 2u : 0u);
+        writes = (lane & 3) ? 0u : ((lane >> 4) < left ? 1u : 0u) | (2 + (lane >> 4) < left ? 2u : 0u);
     }
     // y: 8 values a lane, 4 neighbouring lanes a group, 0 past the matrix; of the
     // row `down` below, inside the same 32, which exists or not
@@ -364,10 +364,7 @@ struct RowsOut {
         R::floats(y, v);
         const uint32_t word = byte == 255u ? 0u : encode8(v, byte == 255u ? 0.0f : mx4_inverse(byte));
         if ((in >> block & 1) && exists) *reinterpret_cast<uint32_t *>(codes + down * bytes + 128 * block) = word;
-        uint32_t four = byte << (8 * ((threadIdx.x >> 2) & 3));
-        four |= __shfl_xor_sync(0xFFFFFFFFu, four, 4);
-        four |= __shfl_xor_sync(0xFFFFFFFFu, four, 8);
-        if (writes >> block & 1) *reinterpret_cast<uint32_t *>(scales + 16 * down + 2 * MX4_ATOM * block) = four;
+        if (writes >> block & 1) scales[16 * down + 2 * MX4_ATOM * block] = (uint8_t)byte;
     }
 };
 
@@ -507,32 +504,38 @@ rms_rows_kernel(NormArgs a) {
 // ------------------------------------------------- the sums of many rows --
 
 // rstd of every row (h: x + residual), or of the backward pass c, rstd^2 times
-// the mean of g x: WPR warps a row, four blocks of 256 columns of both inputs in
-// flight at a time.  Bandwidth bounds it.
+// the mean of g x: WPR warps a row, two blocks of 256 columns of both inputs on
+// their way while two are summed.  Bandwidth bounds it.  VEC: rows are 16-byte
+// aligned and whole pieces of 8.
 struct SumArgs {
     const void *x, *other, *w;       // other: the residual or NULL; dy
     int64_t ldx, ldo, rows, cols, row0;
     int32_t w_kind;
-    bool vec, vec_w;
+    bool vec_w;
     float eps;
     Mean mean;
     const float *rstd;               // of the backward pass
     float *result;                   // [rows]
 };
 
-template <class R, int WPR, bool BACK>
-__global__ void __launch_bounds__(THREADS)
+template <class R, int WPR, bool BACK, bool VEC>
+__global__ void __launch_bounds__(THREADS, R::SIZE == 2 ? 4 : 3)
 rms_sums_kernel(SumArgs a) {
-    constexpr int BLOCKS = 4;
+    constexpr int BLOCKS = 2;
     __shared__ float2 parts[WARPS];
     __shared__ double wides[WARPS];
-    __shared__ __align__(16) typename R::Elem turns[WARPS][256];
+    __shared__ __align__(16) typename R::Elem turns[VEC ? 1 : WARPS][VEC ? 8 : 256];
     const int lane = threadIdx.x & 31, warp = warp_index(), mine = warp % WPR;
     const int64_t row = a.row0 + (int64_t)blockIdx.x * (WARPS / WPR) + warp / WPR;
     const bool there = row < a.rows;
-    typename R::Elem *turn = turns[warp];
+    typename R::Elem *turn = turns[VEC ? 0 : warp];
+    const typename R::Elem *x = static_cast<const typename R::Elem *>(a.x) + row * a.ldx, *other = static_cast<const typename R::Elem *>(a.other) + row * a.ldo;
     pdl_wait();
     pdl_trigger();
+    auto load = [&](const typename R::Elem *p, int64_t c, int n) {
+        if constexpr (VEC) return 8 * lane < n ? *reinterpret_cast<const typename R::Raw *>(p + c + 8 * lane) : R::zero();
+        else return block_load<R>(p, c, n, false, turn);
+    };
     // block c: u v summed over its columns, u = v = h or u = g, v = x
     auto inputs = [&](const typename R::Raw &rx, const typename R::Raw &ro, int64_t c, int n, f2 u[4], f2 v[4]) {
         float x[8], o[8];
@@ -554,15 +557,26 @@ rms_sums_kernel(SumArgs a) {
         }
     };
     float hi = 0.0f, lo = 0.0f;
-    for (int64_t c0 = 256 * mine; c0 < a.cols; c0 += 256 * WPR * BLOCKS) {
-        typename R::Raw rx[BLOCKS], ro[BLOCKS];
+    typename R::Raw next_x[BLOCKS], next_o[BLOCKS];
+    auto fetch = [&](int64_t c0) {
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b) {
             const int64_t c = c0 + 256 * WPR * b;
             const int n = there ? part(a.cols, c) : 0;
-            rx[b] = block_load<R>(a.x, row * a.ldx + c, n, a.vec, turn);
-            ro[b] = a.other ? block_load<R>(a.other, row * a.ldo + c, n, a.vec, turn) : R::zero();
+            next_x[b] = load(x, c, n);
+            next_o[b] = a.other ? load(other, c, n) : R::zero();
         }
+    };
+    fetch(256 * mine);
+#pragma unroll 1
+    for (int64_t c0 = 256 * mine; c0 < a.cols; c0 += 256 * WPR * BLOCKS) {
+        typename R::Raw rx[BLOCKS], ro[BLOCKS];
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b) {
+            rx[b] = next_x[b];
+            ro[b] = next_o[b];
+        }
+        if (c0 + 256 * WPR * BLOCKS < a.cols) fetch(c0 + 256 * WPR * BLOCKS);
         f2 u[BLOCKS][4], v[BLOCKS][4];
         float tu = 0.0f, tv = 0.0f;
 #pragma unroll
@@ -608,8 +622,7 @@ rms_sums_kernel(SumArgs a) {
 #pragma unroll 1
         for (int64_t c = 256 * mine; c < a.cols; c += 256 * WPR) {
             const int n = there ? part(a.cols, c) : 0;
-            const typename R::Raw rx = block_load<R>(a.x, row * a.ldx + c, n, a.vec, turn);
-            const typename R::Raw ro = a.other ? block_load<R>(a.other, row * a.ldo + c, n, a.vec, turn) : R::zero();
+            const typename R::Raw rx = load(x, c, n), ro = a.other ? load(other, c, n) : R::zero();
             f2 u[4], v[4];
             inputs(rx, ro, c, n, u, v);
 #pragma unroll
@@ -1030,15 +1043,15 @@ static int64_t rows_at_once(int64_t cols, int size) {
     return fit > 256 ? fit : 256;
 }
 
-template <class R, bool BACK>
+template <class R, bool BACK, bool VEC>
 static cudaError_t sums_launch(const SumArgs &a, int64_t end, cudaStream_t s) {
-    // as many warps a row as give every SM 16
+    // as many warps a row as give every SM 16 (with 32, 4096 x 4096 bf16 took 2 us more)
     const int64_t rows = end - a.row0;
     auto go = [&](auto kernel, int wpr) { return launch_dependent(kernel, (unsigned)((rows * wpr + WARPS - 1) / WARPS), THREADS, 0, 1, s, a); };
-    if (rows >= 2432 || a.cols <= 1024) return go(rms_sums_kernel<R, 1, BACK>, 1);
-    if (rows >= 1216 || a.cols <= 2048) return go(rms_sums_kernel<R, 2, BACK>, 2);
-    if (rows >= 608 || a.cols <= 4096) return go(rms_sums_kernel<R, 4, BACK>, 4);
-    return go(rms_sums_kernel<R, 8, BACK>, 8);
+    if (rows >= 2432 || a.cols <= 1024) return go(rms_sums_kernel<R, 1, BACK, VEC>, 1);
+    if (rows >= 1216 || a.cols <= 2048) return go(rms_sums_kernel<R, 2, BACK, VEC>, 2);
+    if (rows >= 608 || a.cols <= 4096) return go(rms_sums_kernel<R, 4, BACK, VEC>, 4);
+    return go(rms_sums_kernel<R, 8, BACK, VEC>, 8);
 }
 
 template <class... P>
@@ -1069,8 +1082,8 @@ static cudaError_t norm_tiles(const NormArgs &a, cudaStream_t s) {
     const bool pieces = a.vec && cols % 8 == 0;
     for (int64_t r = 0; r < rows; r += step) {
         const int64_t end = rows - r > step ? r + step : rows, block0 = r / TILE_ROWS, blocks = (end == rows ? all : end / TILE_ROWS) - block0;
-        const SumArgs sums = {a.x, a.residual, nullptr, a.ldx, a.ldr, rows, cols, r, 0, a.vec, true, a.eps, a.mean, nullptr, a.rstd};
-        cudaError_t e = sums_launch<R, false>(sums, end, s);
+        const SumArgs sums = {a.x, a.residual, nullptr, a.ldx, a.ldr, rows, cols, r, 0, true, a.eps, a.mean, nullptr, a.rstd};
+        cudaError_t e = pieces ? sums_launch<R, false, true>(sums, end, s) : sums_launch<R, false, false>(sums, end, s);
         if (e == cudaSuccess) e = pieces ? norm_tile<R, true>(a, block0, blocks, s) : norm_tile<R, false>(a, block0, blocks, s);
         if (e != cudaSuccess) return e;
     }
@@ -1098,8 +1111,8 @@ static cudaError_t back_tiles(const BackArgs &a, cudaStream_t s) {
     const bool pieces = a.vec && cols % 8 == 0;
     for (int64_t r = 0; r < rows; r += step) {
         const int64_t end = rows - r > step ? r + step : rows, block0 = r / TILE_ROWS, block1 = end == rows ? all : end / TILE_ROWS;
-        const SumArgs sums = {a.x, a.dy, a.w, a.ldx, a.lddy, rows, cols, r, a.w_kind, a.vec, a.vec_w, 0.0f, a.mean, a.rstd, a.slopes};
-        cudaError_t e = sums_launch<R, true>(sums, end, s);
+        const SumArgs sums = {a.x, a.dy, a.w, a.ldx, a.lddy, rows, cols, r, a.w_kind, a.vec_w, 0.0f, a.mean, a.rstd, a.slopes};
+        cudaError_t e = pieces ? sums_launch<R, true, true>(sums, end, s) : sums_launch<R, true, false>(sums, end, s);
         if (e == cudaSuccess) e = pieces ? back_tile<R, true>(a, block0, block1, r > 0, s) : back_tile<R, false>(a, block0, block1, r > 0, s);
         if (e != cudaSuccess) return e;
     }
