@@ -928,32 +928,45 @@ def zs_mx4_matvec(x, w, out, stream=None):
     if rows != m:
         raise ValueError(f"out: {m} rows expected, got {rows}")
     wc, ws = _mx4(w, n, k, device)
-    st = _lib.zs_mx4_matvec(m, n, k, _device_address(x, "x", device), ldx, dtype, wc, ws, _device_address(out, "out", device), ldo, out_dtype,
+    if x.get_device() != device or out.get_device() != device:
+        for name, y in (("x", x), ("out", out)):
+            if y.get_device() != device:
+                _elsewhere(y, name, device)
+    st = _lib.zs_mx4_matvec(m, n, k, x.data_ptr(), ldx, dtype, wc, ws, out.data_ptr(), ldo, out_dtype,
                             _current_stream() if stream is None else _stream(stream))
     if st:
         _check(st, "zs_mx4_matvec")
     return out
 
 
-def _like(m, what: str, rows: int, cols: int, dtype: int, device: int):
-    """(address, row stride) of a matrix of these sizes and type, or of none."""
+def _like(m, what: str, x, device: int):
+    """(address, row stride) of a matrix of x's sizes and type, or of none."""
     if m is None:
         return None, 0
-    r, c, ld, d = _matrix(m, what)
-    if r != rows or c != cols or d != dtype:
-        raise ValueError(f"{what}: {rows} x {cols} of x's type expected, got {tuple(m.shape)} of {m.dtype}")
-    return _device_address(m, what, device), ld
+    if m.shape != x.shape or m.dtype != x.dtype:
+        raise ValueError(f"{what}: {tuple(x.shape)} of {x.dtype} expected, got {tuple(m.shape)} of {m.dtype}")
+    rows, cols = m.shape
+    ld, one = m.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{what}: rows are not contiguous")
+    if m.get_device() != device:
+        _elsewhere(m, what, device)
+    return m.data_ptr(), ld if rows > 1 else cols
 
 
 def _vector(v, what: str, n: int, device: int, dtype=None):
     """(address, dtype) of a contiguous vector of n elements, or of none."""
     if v is None:
         return None, ZS_DTYPE_FP32
-    d = _dtype(v)
-    if v.shape != (n,) or n > 1 and v.stride(0) != 1 or dtype is not None and d != dtype:
+    d = _DTYPES.get(v.dtype)
+    if d is None:
+        d = _dtype(v)
+    if v.dim() != 1 or v.numel() != n or n > 1 and v.stride(0) != 1 or dtype is not None and d != dtype:
         raise ValueError(f"{what}: {n} contiguous elements{' of float32' if dtype == ZS_DTYPE_FP32 else ''} expected, "
                          f"got {tuple(v.shape)} of {v.dtype}")
-    return _device_address(v, what, device), d
+    if v.get_device() != device:
+        _elsewhere(v, what, device)
+    return v.data_ptr(), d
 
 
 def zs_rms_norm(x, weight, eps: float, rstd, residual=None, sum=None, out=None, rows=None, cols=None, stream=None) -> None:
@@ -962,13 +975,15 @@ def zs_rms_norm(x, weight, eps: float, rstd, residual=None, sum=None, out=None, 
     along its columns (of the transposed matrix)."""
     device = _current_device()
     r, c, ldx, dtype = _matrix(x, "x")
-    ra, ldr = _like(residual, "residual", r, c, dtype, device)
-    sa, lds = _like(sum, "sum", r, c, dtype, device)
-    oa, ldo = _like(out, "out", r, c, dtype, device)
+    ra, ldr = _like(residual, "residual", x, device)
+    sa, lds = _like(sum, "sum", x, device)
+    oa, ldo = _like(out, "out", x, device)
     wa, wd = _vector(weight, "weight", c, device)
     rc, rs = _mx4(rows, r, c, device)
     cc, cs = _mx4(cols, c, r, device)
-    st = _lib.zs_rms_norm(_device_address(x, "x", device), ldx, ra, ldr, wa, wd, r, c, dtype, eps, sa, lds, oa, ldo,
+    if x.get_device() != device:
+        _elsewhere(x, "x", device)
+    st = _lib.zs_rms_norm(x.data_ptr(), ldx, ra, ldr, wa, wd, r, c, dtype, eps, sa, lds, oa, ldo,
                           _vector(rstd, "rstd", r, device, ZS_DTYPE_FP32)[0], rc, rs, cc, cs,
                           _current_stream() if stream is None else _stream(stream))
     if st:
@@ -987,17 +1002,19 @@ def zs_rms_norm_backward(dy, x, weight, rstd, dx, scratch, residual=None, dw=Non
     the dicts of dx held along its rows and its columns."""
     device = _current_device()
     r, c, ldx, dtype = _matrix(x, "x")
-    ya, ldy = _like(dy, "dy", r, c, dtype, device)
-    ra, ldr = _like(residual, "residual", r, c, dtype, device)
-    da, ldd = _like(dx, "dx", r, c, dtype, device)
+    ya, ldy = _like(dy, "dy", x, device)
+    ra, ldr = _like(residual, "residual", x, device)
+    da, ldd = _like(dx, "dx", x, device)
     wa, wd = _vector(weight, "weight", c, device)
     dwa, dwd = _vector(dw, "dw", c, device)
     rc, rs = _mx4(rows, r, c, device)
     cc, cs = _mx4(cols, c, r, device)
     sa = _device_address(scratch, "scratch", device)
+    if x.get_device() != device:
+        _elsewhere(x, "x", device)
     if hasattr(scratch, "data_ptr") and (scratch.nbytes < zs_rms_norm_scratch(r, c) or not scratch.is_contiguous()):
         raise ValueError(f"scratch: {zs_rms_norm_scratch(r, c)} contiguous bytes expected, got {tuple(scratch.shape)} of {scratch.dtype}")
-    st = _lib.zs_rms_norm_backward(ya, ldy, _device_address(x, "x", device), ldx, wa, wd,
+    st = _lib.zs_rms_norm_backward(ya, ldy, x.data_ptr(), ldx, wa, wd,
                                    _vector(rstd, "rstd", r, device, ZS_DTYPE_FP32)[0], ra, ldr, r, c, dtype, da, ldd, dwa, dwd, sa,
                                    rc, rs, cc, cs, _current_stream() if stream is None else _stream(stream))
     if st:

@@ -131,48 +131,52 @@ struct Row16 {
 typedef Row16<BF16T, false> RowBF16;
 typedef Row16<FP16T, true> RowFP16;
 
-// A lane's 8 of a block of 256 columns, `there` of which exist (any integer).
-// vec: the row is 16-byte aligned.  Otherwise lanes load neighbouring elements,
-// which turn (256 elements of the warp's shared memory) deals out: 8 loads of 2
-// or 4 bytes a lane instead of 8 that each meet another sector.
-template <class R>
-__device__ __forceinline__ typename R::Raw block_load(const void *p, int64_t at, int there, bool vec, typename R::Elem *turn) {
-    const int lane = threadIdx.x & 31, n = there - 8 * lane;
-    const typename R::Elem *q = static_cast<const typename R::Elem *>(p) + at;
-    if (vec && n >= 8) return *reinterpret_cast<const typename R::Raw *>(q + 8 * lane);
-    if (vec) {
-        if (n <= 0) return R::zero();
-        uint32_t v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? (uint32_t)q[8 * lane + i] : 0u;
-        return R::of(v);
+// A lane's 8 of a block of 256 columns from p on, `there` of which exist (any
+// integer), on their way.  VEC: rows are 16-byte aligned and whole pieces of 8.
+// Otherwise lanes load neighbouring elements (8 loads of 2 or 4 bytes that share
+// their sectors, instead of 8 that each meet another one), which the warp's turn
+// (256 elements of shared memory) deals out once all of them are needed.
+template <class R, bool VEC>
+struct Load {
+    typename R::Raw r;
+    __device__ __forceinline__ Load() {}
+    __device__ __forceinline__ Load(const typename R::Elem *p, int there) {
+        const int lane = threadIdx.x & 31;
+        r = 8 * lane < there ? *reinterpret_cast<const typename R::Raw *>(p + 8 * lane) : R::zero();
     }
+    __device__ __forceinline__ typename R::Raw take(typename R::Elem *) const { return r; }
+};
+template <class R>
+struct Load<R, false> {
     uint32_t v[8];
+    __device__ __forceinline__ Load() {}
+    __device__ __forceinline__ Load(const typename R::Elem *p, int there) {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 32 * i + lane < there ? (uint32_t)q[32 * i + lane] : 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) turn[32 * i + lane] = (typename R::Elem)v[i];
-    __syncwarp();
-    const typename R::Raw r = *reinterpret_cast<const typename R::Raw *>(turn + 8 * lane);
-    __syncwarp();
-    return r;
-}
-template <class R>
-__device__ __forceinline__ void block_store(void *p, int64_t at, int there, bool vec, typename R::Elem *turn, const typename R::Raw &r) {
-    const int lane = threadIdx.x & 31, n = there - 8 * lane;
-    typename R::Elem *q = static_cast<typename R::Elem *>(p) + at;
-    if (vec) {
-        if (n >= 8) *reinterpret_cast<typename R::Raw *>(q + 8 * lane) = r;
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i) if (i < n) q[8 * lane + i] = R::element(r, i);
-        return;
+        for (int i = 0; i < 8; ++i) v[i] = 32 * i + lane < there ? (uint32_t)p[32 * i + lane] : 0u;
     }
-    *reinterpret_cast<typename R::Raw *>(turn + 8 * lane) = r;
-    __syncwarp();
+    __device__ __forceinline__ typename R::Raw take(typename R::Elem *turn) const {
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) if (32 * i + lane < there) q[32 * i + lane] = turn[32 * i + lane];
-    __syncwarp();
+        for (int i = 0; i < 8; ++i) turn[32 * i + lane] = (typename R::Elem)v[i];
+        __syncwarp();
+        const typename R::Raw r = *reinterpret_cast<const typename R::Raw *>(turn + 8 * lane);
+        __syncwarp();
+        return r;
+    }
+};
+template <class R, bool VEC>
+__device__ __forceinline__ void block_store(typename R::Elem *p, int there, typename R::Elem *turn, const typename R::Raw &r) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (VEC) {
+        if (8 * lane < there) *reinterpret_cast<typename R::Raw *>(p + 8 * lane) = r;
+    } else {
+        *reinterpret_cast<typename R::Raw *>(turn + 8 * lane) = r;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) if (32 * i + lane < there) p[32 * i + lane] = turn[32 * i + lane];
+        __syncwarp();
+    }
 }
 
 // 8 weights of any type from column `at` on, n of which exist
@@ -396,29 +400,36 @@ struct NormArgs {
 // WPR warps take a row, 8 values a lane and block of 256 columns; a lane keeps
 // its NB blocks (NB 0: more than registers hold, read again).  Bandwidth
 // bounds many rows, the way through the sum's exchange a few.
-template <class R, int WPR, int NB>
+template <class R, int WPR, int NB, bool VEC>
 __global__ void __launch_bounds__(THREADS)
 rms_rows_kernel(NormArgs a) {
     constexpr int ROWS = WARPS / WPR, KEEP = NB > 0 ? NB : 1;
     __shared__ float2 parts[WARPS];
     __shared__ double wides[WARPS];
-    __shared__ __align__(16) typename R::Elem turns[WARPS][256];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp % WPR;
+    __shared__ __align__(16) typename R::Elem turns[VEC ? 1 : WARPS][VEC ? 8 : 256];
+    const int lane = threadIdx.x & 31, warp = warp_index(), mine = warp % WPR;
     const int64_t rows = a.held.rows, cols = a.held.cols, row = (int64_t)blockIdx.x * ROWS + warp / WPR;
     const int blocks = NB > 0 ? NB : (int)((cols + 256 * WPR - 1) / (256 * WPR));
     const bool there = row < rows;
-    typename R::Elem *turn = turns[warp];
+    typedef typename R::Elem Elem;
+    Elem *turn = turns[VEC ? 0 : warp];
+    const Elem *x = static_cast<const Elem *>(a.x) + row * a.ldx, *residual = static_cast<const Elem *>(a.residual) + row * a.ldr;
+    Elem *sum = static_cast<Elem *>(a.sum) + row * a.lds, *out = static_cast<Elem *>(a.out) + row * a.ldo;
+    auto column = [&](int b) { return 256 * (int64_t)(mine + WPR * b); };
+    auto exist = [&](int b) { return there ? part(cols, column(b)) : 0; };
     pdl_wait();
     pdl_trigger();
-    auto input = [&](int b, float h[8]) {
-        const int64_t c = 256 * (int64_t)(mine + WPR * b);
-        const int n = there ? part(cols, c) : 0;
-        R::floats(block_load<R>(a.x, row * a.ldx + c, n, a.vec, turn), h);
+    auto add = [&](const Load<R, VEC> &first, const Load<R, VEC> &second, float h[8]) {
+        R::floats(first.take(turn), h);
         if (!a.residual) return;
         float r[8];
-        R::floats(block_load<R>(a.residual, row * a.ldr + c, n, a.vec, turn), r);
+        R::floats(second.take(turn), r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] = __fadd_rn(h[i], r[i]);
+    };
+    auto input = [&](int b, float h[8]) {
+        const Load<R, VEC> first(x + column(b), exist(b)), second(residual + column(b), a.residual ? exist(b) : 0);
+        add(first, second, h);
     };
     float h[KEEP][8];
     float hi = 0.0f, lo = 0.0f;
@@ -443,8 +454,14 @@ rms_rows_kernel(NormArgs a) {
         add22(hi, lo, ok ? dh : __uint_as_float(0x7F800000u), dl);
     };
     if constexpr (NB > 0) {
+        Load<R, VEC> first[KEEP], second[KEEP];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) input(b, h[b]);
+        for (int b = 0; b < NB; ++b) {
+            first[b] = Load<R, VEC>(x + column(b), exist(b));
+            second[b] = Load<R, VEC>(residual + column(b), a.residual ? exist(b) : 0);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) add(first[b], second[b], h[b]);
         square(h);
     } else {
         for (int b = 0; b < blocks; ++b) {
@@ -482,8 +499,8 @@ rms_rows_kernel(NormArgs a) {
     if (there && mine == 0 && lane == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int b = 0; b < blocks; ++b) {
-        const int64_t c = 256 * (int64_t)(mine + WPR * b);
-        const int n = there ? part(cols, c) : 0;
+        const int64_t c = column(b);
+        const int n = exist(b);
         float v[8], w[8];
         if constexpr (NB > 0) {
 #pragma unroll
@@ -491,12 +508,12 @@ rms_rows_kernel(NormArgs a) {
         } else {
             input(b, v);
         }
-        if (a.sum) block_store<R>(a.sum, row * a.lds + c, n, a.vec, turn, R::rounded(v));
+        if (a.sum) block_store<R, VEC>(sum + c, n, turn, R::rounded(v));
         weights8(a.w, a.w_kind, a.vec_w, c + 8 * lane, n - 8 * lane, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 8 * lane + i < n ? __fmul_rn(__fmul_rn(v[i], rstd), w[i]) : 0.0f;
         const typename R::Raw y = R::rounded(v);
-        if (a.out) block_store<R>(a.out, row * a.ldo + c, n, a.vec, turn, y);
+        if (a.out) block_store<R, VEC>(out + c, n, turn, y);
         if (a.held.r_codes) RowsOut(a.held, row, c).template hold<R>(y, 0, 0, there);
     }
 }
@@ -532,10 +549,6 @@ rms_sums_kernel(SumArgs a) {
     const typename R::Elem *x = static_cast<const typename R::Elem *>(a.x) + row * a.ldx, *other = static_cast<const typename R::Elem *>(a.other) + row * a.ldo;
     pdl_wait();
     pdl_trigger();
-    auto load = [&](const typename R::Elem *p, int64_t c, int n) {
-        if constexpr (VEC) return 8 * lane < n ? *reinterpret_cast<const typename R::Raw *>(p + c + 8 * lane) : R::zero();
-        else return block_load<R>(p, c, n, false, turn);
-    };
     // block c: u v summed over its columns, u = v = h or u = g, v = x
     auto inputs = [&](const typename R::Raw &rx, const typename R::Raw &ro, int64_t c, int n, f2 u[4], f2 v[4]) {
         float x[8], o[8];
@@ -557,14 +570,14 @@ rms_sums_kernel(SumArgs a) {
         }
     };
     float hi = 0.0f, lo = 0.0f;
-    typename R::Raw next_x[BLOCKS], next_o[BLOCKS];
+    Load<R, VEC> next_x[BLOCKS], next_o[BLOCKS];
     auto fetch = [&](int64_t c0) {
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b) {
             const int64_t c = c0 + 256 * WPR * b;
             const int n = there ? part(a.cols, c) : 0;
-            next_x[b] = load(x, c, n);
-            next_o[b] = a.other ? load(other, c, n) : R::zero();
+            next_x[b] = Load<R, VEC>(x + c, n);
+            next_o[b] = Load<R, VEC>(other + c, a.other ? n : 0);
         }
     };
     fetch(256 * mine);
@@ -573,8 +586,8 @@ rms_sums_kernel(SumArgs a) {
         typename R::Raw rx[BLOCKS], ro[BLOCKS];
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b) {
-            rx[b] = next_x[b];
-            ro[b] = next_o[b];
+            rx[b] = next_x[b].take(turn);
+            ro[b] = next_o[b].take(turn);
         }
         if (c0 + 256 * WPR * BLOCKS < a.cols) fetch(c0 + 256 * WPR * BLOCKS);
         f2 u[BLOCKS][4], v[BLOCKS][4];
@@ -622,7 +635,7 @@ rms_sums_kernel(SumArgs a) {
 #pragma unroll 1
         for (int64_t c = 256 * mine; c < a.cols; c += 256 * WPR) {
             const int n = there ? part(a.cols, c) : 0;
-            const typename R::Raw rx = load(x, c, n), ro = a.other ? load(other, c, n) : R::zero();
+            const typename R::Raw rx = Load<R, VEC>(x + c, n).take(turn), ro = Load<R, VEC>(other + c, a.other ? n : 0).take(turn);
             f2 u[4], v[4];
             inputs(rx, ro, c, n, u, v);
 #pragma unroll
@@ -690,6 +703,14 @@ struct TileRow {
         async16(piece(lane, 0), q);
         if (R::SIZE == 4) async16(piece(lane, 1), q + 4);
     }
+    // neighbouring elements, for the whole warp to read after its __syncwarp()
+    __device__ __forceinline__ void put(const Load<R, false> &l) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = 32 * i + (threadIdx.x & 31);
+            at[R::SIZE == 2 ? c : 128 * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3)] = (typename R::Elem)l.v[i];
+        }
+    }
 };
 __device__ __forceinline__ int column_at(int place) {        // the column of a 32-bit place, in its block of 256
     return 8 * ((place & 127) >> 2) + 4 * ((place >> 7) & 1) + (place & 3);
@@ -734,33 +755,22 @@ __device__ __forceinline__ void hold_tile(const NormHeld &h, int64_t rb, int64_t
 }
 
 // A warp's share of a matrix: 4 rows, 8 apart, and two blocks of 256 columns.
-// VEC: rows are 16-byte aligned and whole pieces of 8, a lane's at `at`.
 template <class R, bool VEC>
 struct Share {
     typename R::Elem *at;
     int64_t step;
     __device__ __forceinline__ Share(const void *p, int64_t ld, int64_t row, int64_t col)
-        : at(static_cast<typename R::Elem *>(const_cast<void *>(p)) + (row * ld + col) + (VEC ? 8 * (threadIdx.x & 31) : 0)), step(8 * ld) {}
+        : at(static_cast<typename R::Elem *>(const_cast<void *>(p)) + (row * ld + col)), step(8 * ld) {}
     __device__ __forceinline__ typename R::Elem *of(int i, int b) const { return at + i * step + 256 * b; }
     // `there`: of the block's 256 columns, how many exist
-    __device__ __forceinline__ typename R::Raw load(int i, int b, int there, typename R::Elem *turn) const {
-        if constexpr (VEC) {
-            if (8 * (int)(threadIdx.x & 31) >= there) return R::zero();
-            return *reinterpret_cast<const typename R::Raw *>(of(i, b));
-        } else {
-            return block_load<R>(of(i, b), 0, there, false, turn);
-        }
-    }
+    __device__ __forceinline__ Load<R, VEC> load(int i, int b, int there) const { return Load<R, VEC>(of(i, b), there); }
     __device__ __forceinline__ void store(int i, int b, int there, typename R::Elem *turn, const typename R::Raw &r) const {
-        if constexpr (VEC) {
-            if (8 * (int)(threadIdx.x & 31) < there) *reinterpret_cast<typename R::Raw *>(of(i, b)) = r;
-        } else {
-            block_store<R>(of(i, b), 0, there, false, turn, r);
-        }
+        block_store<R, VEC>(of(i, b), there, turn, r);
     }
-    __device__ __forceinline__ void fetch(const TileRow<R> &to, int i, int b, int there, typename R::Elem *turn) const {
-        if constexpr (VEC) to.fetch(of(i, b), 8 * (int)(threadIdx.x & 31) < there);
-        else to.put(load(i, b, there, turn));
+    __device__ __forceinline__ void fetch(const TileRow<R> &to, int i, int b, int there) const {
+        const int lane = threadIdx.x & 31;
+        if constexpr (VEC) to.fetch(of(i, b) + 8 * lane, 8 * lane < there);
+        else to.put(load(i, b, there));
     }
     // y with nothing past the matrix
     static __device__ __forceinline__ typename R::Raw cut(const float v[8], int there) {
@@ -809,11 +819,12 @@ rms_tile_kernel(NormArgs a, int64_t block0, int col_blocks) {
     for (int i = 0; i < ROWS_EACH; ++i) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            x.fetch(place(mine, i, b), i, b, there(i, b), turn);
-            if (TWO && a.residual) residual.fetch(place(mine_r, i, b), i, b, there(i, b), turn);
+            x.fetch(place(mine, i, b), i, b, there(i, b));
+            if (TWO && a.residual) residual.fetch(place(mine_r, i, b), i, b, there(i, b));
         }
         asm volatile("cp.async.commit_group;" : : : "memory");
     }
+    if (!VEC) __syncwarp();
     float rstds[ROWS_EACH];
     f2 w[2][4];
 #pragma unroll
@@ -840,7 +851,7 @@ rms_tile_kernel(NormArgs a, int64_t block0, int col_blocks) {
             if (a.residual) {
                 float q[8];
                 if constexpr (TWO) R::floats(place(mine_r, i, b).get(), q);
-                else R::floats(residual.load(i, b, n, turn), q);
+                else R::floats(residual.load(i, b, n).take(turn), q);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     h[j] = add2(h[j], f2pack(q[2 * j], q[2 * j + 1]));
@@ -915,12 +926,13 @@ rms_back_kernel(BackArgs a, int64_t block0, int64_t block1, int col_blocks, int6
         for (int i = 0; i < ROWS_EACH; ++i) {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                x.fetch(place(0, i, b), i, b, there(i, b), turn);
-                if (TWO) dy.fetch(place(1, i, b), i, b, there(i, b), turn);
-                if (TWO && a.residual) residual.fetch(place(2, i, b), i, b, there(i, b), turn);
+                x.fetch(place(0, i, b), i, b, there(i, b));
+                if (TWO) dy.fetch(place(1, i, b), i, b, there(i, b));
+                if (TWO && a.residual) residual.fetch(place(2, i, b), i, b, there(i, b));
             }
             asm volatile("cp.async.commit_group;" : : : "memory");
         }
+        if (!VEC) __syncwarp();
         float rstds[ROWS_EACH], slopes[ROWS_EACH];
 #pragma unroll
         for (int i = 0; i < ROWS_EACH; ++i) {
@@ -937,7 +949,7 @@ rms_back_kernel(BackArgs a, int64_t block0, int64_t block1, int col_blocks, int6
                 const int n = there(i, b);
                 float u[8], v[8];
                 if constexpr (TWO) R::floats(place(1, i, b).get(), v);
-                else R::floats(dy.load(i, b, n, turn), v);
+                else R::floats(dy.load(i, b, n).take(turn), v);
                 R::floats(place(0, i, b).get(), u);
                 // dw; (g w - x slope) rstd, each rounded
 #pragma unroll
@@ -949,7 +961,7 @@ rms_back_kernel(BackArgs a, int64_t block0, int64_t block1, int col_blocks, int6
                 if (a.residual) {
                     float r[8];
                     if constexpr (TWO) R::floats(place(2, i, b).get(), r);
-                    else R::floats(residual.load(i, b, n, turn), r);
+                    else R::floats(residual.load(i, b, n).take(turn), r);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], r[j]);
                 }
@@ -1020,7 +1032,8 @@ template <class R, int WPR, int NB>
 static cudaError_t rows_launch(const NormArgs &a, int64_t grid_rows, cudaStream_t s) {
     const int64_t per = WARPS / WPR, grid = (grid_rows + per - 1) / per;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    return launch_dependent(rms_rows_kernel<R, WPR, NB>, (unsigned)grid, THREADS, 0, 1, s, a);
+    auto go = [&](auto kernel) { return launch_dependent(kernel, (unsigned)grid, THREADS, 0, 1, s, a); };
+    return a.vec && a.held.cols % 8 == 0 ? go(rms_rows_kernel<R, WPR, NB, true>) : go(rms_rows_kernel<R, WPR, NB, false>);
 }
 // As many warps a row as give each lane 16 values; past 8 warps more values.
 template <class R>
