@@ -491,7 +491,8 @@ static cudaError_t matvec_launch(MatvecArgs a, cudaStream_t s) {
             const int slice = (units + sp - 1) / sp, steps = (slice + wk - 1) / wk, room = seats[dev][sp].load(std::memory_order_relaxed);
             const bool once = fits(steps * wk);
             if (slice * (sp - 1) >= units || (!once && wk > mv_most_stage(NB))) continue;
-            const int step = wn * wk * STEP, pieces = a.columns / PER * steps * wk * 16 / THREADS;
+            const int step = wn * wk * STEP;
+            const int64_t pieces = (int64_t)(a.columns / PER) * steps * wk * 16 / THREADS;
             const int64_t one = 2000 + (int64_t)steps * (step > 450 ? step : 450) + 280 * pieces + (once ? 0 : 500) + (sp > 1 ? 700 : 0);
             const int64_t cost = ((int64_t)blocks * ty * sp + room - 1) / room * one;
             if (best >= 0 && cost >= best) continue;

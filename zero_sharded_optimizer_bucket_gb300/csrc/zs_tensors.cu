@@ -24,6 +24,7 @@
 // elements; 8-bit 6144: 470 us rounded to nearest, against 488 at 4096 and at
 // 8192); a short one takes small chunks, spread over more SMs.
 constexpr int CHUNK32 = 8192, CHUNK8 = 6144, CHUNK_SHORT = 2048;
+static_assert(CHUNK32 <= CHUNK_MOST && CHUNK8 <= CHUNK_MOST, "chunks");
 constexpr int64_t SHORT_ELEMS = 304ll * CHUNK8;     // two chunks an SM
 constexpr int STATE_BLOCK = 256;     // elements per scale: 8 a lane of one warp
 

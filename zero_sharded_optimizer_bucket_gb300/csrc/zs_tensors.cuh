@@ -5,6 +5,8 @@
 
 #include "zs_device.cuh"
 
+constexpr int CHUNK_MOST = 8192;     // elements of a chunk
+
 struct ZsChunk {
     const void *grad;
     void *param;                     // 16-bit copy, or NULL

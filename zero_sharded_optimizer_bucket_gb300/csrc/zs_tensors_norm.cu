@@ -17,6 +17,7 @@ namespace zsk {
 // threads with more groups share the work that a thread has with a chunk over
 // more squares (256 threads of 4 groups: 94 us for 202M bf16 gradients).
 constexpr int NORM_THREADS = 128, NORM_GROUPS = 8, NORM_DEPTH = 2;
+static_assert(8 * NORM_THREADS * NORM_GROUPS >= CHUNK_MOST, "a chunk at a time");
 template <class G>
 __host__ __device__ constexpr int norm_stage() { return 8 * NORM_THREADS * NORM_GROUPS * G::SIZE; }
 template <class G>
