@@ -387,3 +387,65 @@ def test_refused_tensors():
         zs.zs_rms_norm_backward(x, x, w, rstd, out, torch.empty(16, dtype=torch.uint8, device="cuda"), dw=w)
     with pytest.raises(ValueError):
         zs.zs_rms_norm_backward(x[:3], x, w, rstd, out, torch.empty(1 << 16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("cols", [1, 31, 256, 500, 512, 513, 1490, 2048, 2056, 4096, 4099, 8192, 8193])
+@pytest.mark.parametrize("kind,w_kind", [("bf16", "fp32"), ("fp16", "fp16"), ("fp32", "fp32")])
+def test_backward_whole(cols, kind, w_kind):
+    """dx that is not held: one reading where a row fits the registers; the same bits twice."""
+    for rows, with_res, extra, shift, dw in ((1, True, 0, 0, True), (7, False, 3, 1, True), (9, True, 8, 0, True), (700, True, 0, 0, True), (2500, True, 5, 3, False)):
+        dy, x, w, rstd, res = back_data(rows, cols, kind, w_kind, seed=rows)
+        dy[rows // 2] = 0                              # a row that no loss reaches
+        m = Mat(rows, cols, kind, dy, extra, shift)
+        got = back(m.t, x, w, rstd, res if with_res else None, kind, w_kind, dw, (), extra, shift)
+        check_backward(dy, x, w, rstd, res if with_res else None, got, kind, w_kind)
+        again = back(m.t, x, w, rstd, res if with_res else None, kind, w_kind, dw, (), extra, shift)
+        assert same(got["dx"].t, again["dx"].t) and (not dw or same(got["dw"], again["dw"]))
+
+
+@pytest.mark.parametrize("cols", [40, 1490, 2048, 6000])
+@pytest.mark.parametrize("held", [(), ("cols",)])
+def test_backward_range(cols, held):
+    """Rows whose products leave float32, and rows that are not finite, beside ordinary ones."""
+    rows = 45
+    dy, x, w, rstd, _ = back_data(rows, cols, "bf16", "fp32", seed=8)
+    big = [1, 6, 17]
+    x[big] = (x[big].float() * 2.0 ** 62).bfloat16()   # x x past 2^124: mean(g x) is float32's in the end
+    rstd[big] = rstd[big] * 2.0 ** -62
+    dy[big] = (dy[big].float() * 2.0 ** 70).bfloat16()
+    x[20, cols // 2] = float("inf")
+    dy[33, 0] = float("nan")
+    dy[40, cols - 1] = float("-inf")
+    got = back(dy, x, w, rstd, None, "bf16", "fp32", False, held)
+    finite = torch.tensor([r not in (20, 33, 40) for r in range(rows)], device="cuda")
+    rest = dict(dx=Mat(int(finite.sum()), cols, "bf16", got["dx"].t[finite]))
+    check_backward(dy[finite], x[finite], w, rstd[finite], None, rest, "bf16", "fp32")
+    # c is an infinity or NaN: of 20 and 33 and 40 nothing stays finite
+    assert not bool(torch.isfinite(got["dx"].t[~finite]).any())
+
+
+def test_backward_whole_streams_and_graphs():
+    """Two captured graphs with a scratch each, replayed at once, and a call on another stream."""
+    rows, cols = 900, 1490
+    dy, x, w, rstd, res = back_data(rows, cols, "fp16", "fp32")
+    want = back(dy, x, w, rstd, res, "fp16")
+    runs = []
+    for _ in range(3):
+        dx, dw = torch.empty_like(x), torch.empty(cols, device="cuda")
+        scratch = torch.empty(zs.zs_rms_norm_scratch(rows, cols), dtype=torch.uint8, device="cuda")
+        runs.append((dx, dw, scratch))
+    torch.cuda.synchronize()
+    graphs = []
+    for dx, dw, scratch in runs[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            zs.zs_rms_norm_backward(dy, x, w, rstd, dx, scratch, residual=res, dw=dw)
+        graphs.append(g)
+    for g in graphs:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            g.replay()
+    dx, dw, scratch = runs[2]
+    zs.zs_rms_norm_backward(dy, x, w, rstd, dx, scratch, residual=res, dw=dw, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    for dx, dw, _ in runs:
+        assert same(dx, want["dx"].t) and same(dw, want["dw"])

@@ -887,6 +887,8 @@ struct BackArgs {
     NormHeld held;
 };
 
+__host__ __device__ constexpr int64_t parts_pitch(int64_t cols) { return (cols + TILE_COLS - 1) / TILE_COLS * TILE_COLS; }
+
 // The same of the backward pass, c being known: a CTA takes its 512 columns of
 // the row blocks b, b + parts, ... and adds up their part of dw (add: to what
 // the rows before have left).
@@ -998,30 +1000,269 @@ rms_back_kernel(BackArgs a, int64_t block0, int64_t block1, int col_blocks, int6
     }
 }
 
-// dw from its parts, in their order: 32 columns a CTA, 8 shares of the parts.
-__global__ void __launch_bounds__(THREADS)
+// The backward pass of a dx that is not held, in one reading: WPR warps take a
+// row, two blocks of 256 columns each, from its sum to its result.  VEC: the next
+// rows' x, dy and residual are on their way to shared memory, a lane's 8 to a
+// place of its own (32 bits: two fours, each beside the neighbours', since a
+// warp's copies then read whole sectors; 4096 x 4096: 49 us, not 76); other rows
+// go through registers.  A CTA takes WARPS / WPR
+// rows at a time and leaves its part of dw.  Bandwidth bounds many rows, the way
+// through a row's sum a few.  4096 x 4096 bf16: 30 us with rms_weight_kernel (the
+// two readings of rms_back_kernel: 39), fp32 49 (107), 1333 x 1490 fp16 10 (20).
+// Three CTAs an SM spill; a ring of four rows takes as long as one of three.
+__host__ __device__ constexpr int whole_cta_warps(int wpr) { return wpr > WARPS ? wpr : WARPS; }
+template <class R, bool VEC>
+__host__ __device__ constexpr int whole_ctas(int wpr) { return wpr > WARPS ? 1 : VEC && R::SIZE == 2 ? 2 : 2; }      // an SM
+template <class R>
+__host__ __device__ constexpr int whole_depth(int wpr) { return R::SIZE == 4 ? 2 : 3; }           // rows of the ring
+template <class R>
+__host__ __device__ constexpr int whole_stage(int wpr) { return 3 * 2 * 8 * R::SIZE * 32 * whole_cta_warps(wpr); }
+// bytes of shared memory: the ring, and the warps' parts of dw in its place
+template <class R, bool VEC>
+constexpr int whole_smem(int wpr) { return VEC ? whole_depth<R>(wpr) * whole_stage<R>(wpr) : whole_cta_warps(wpr) * 2 * 256 * 4; }
+
+template <class R, int WPR, bool VEC>
+__global__ void __launch_bounds__(32 * whole_cta_warps(WPR), whole_ctas<R, VEC>(WPR))
+rms_back_rows_kernel(BackArgs a) {
+    constexpr int NB = 2, W = whole_cta_warps(WPR), ROWS = W / WPR, DEPTH = whole_depth<R>(WPR), STAGE = whole_stage<R>(WPR), PIECES = R::SIZE / 2;
+    extern __shared__ __align__(16) uint8_t raw[];
+    __shared__ float2 parts[2][W];
+    __shared__ double wides[W];
+    __shared__ __align__(16) typename R::Elem turns[VEC ? 1 : W][VEC ? 8 : 256];
+    typedef typename R::Elem Elem;
+    const int lane = threadIdx.x & 31, warp = warp_index(), mine = warp % WPR, sub = warp / WPR;
+    const int64_t rows = a.held.rows, cols = a.held.cols, step = a.parts * ROWS;
+    Elem *turn = turns[VEC ? 0 : warp];
+    auto column = [&](int b) { return 256 * (mine + WPR * b); };
+    const int exist[NB] = {part(cols, column(0)), part(cols, column(1))};
+    constexpr bool FOURS = VEC && R::SIZE == 4;
+    auto four = [&](int h) { return FOURS ? 128 * h + 4 * lane : 8 * lane + 4 * h; };       // the first column of half h of a lane's 8
+    pdl_wait();
+    pdl_trigger();
+    f2 w[NB][4], dw[NB][4] = {};
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        float v[8];
+        if constexpr (FOURS) {
+            float u[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                weights8(a.w, a.w_kind, false, column(b) + four(h), min(4, exist[b] - four(h)), u);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[4 * h + j] = u[j];
+            }
+        } else {
+            weights8(a.w, a.w_kind, a.vec_w, column(b) + 8 * lane, exist[b] - 8 * lane, v);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[b][j] = f2pack(v[2 * j], v[2 * j + 1]);
+    }
+    const f2 minus = both(a.minus_one);
+    const int64_t first = (int64_t)blockIdx.x * ROWS + sub;
+    int64_t ahead = first;                           // the next row of the ring
+    int slot = 0, place = 0;
+    uint8_t *own = raw + 16 * threadIdx.x;
+    auto piece = [&](int at, int matrix, int b, int h) { return own + at + ((matrix * NB + b) * PIECES + h) * (16 * 32 * W); };
+    auto copy = [&] {
+        if constexpr (VEC) {
+            if (ahead < rows) {
+                const Elem *from[3] = {static_cast<const Elem *>(a.x) + ahead * a.ldx, static_cast<const Elem *>(a.dy) + ahead * a.lddy,
+                                       static_cast<const Elem *>(a.residual) + ahead * a.ldr};
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int h = 0; h < PIECES; ++h)
+                        if (four(h) < exist[b])
+#pragma unroll
+                            for (int k = 0; k < 3; ++k)
+                                if (k < 2 || a.residual) async16(piece(slot, k, b, h), from[k] + column(b) + four(h));
+            }
+            asm volatile("cp.async.commit_group;" : : : "memory");
+            slot = slot + STAGE == DEPTH * STAGE ? 0 : slot + STAGE;
+            ahead += step;
+        }
+    };
+    for (int i = 0; i < DEPTH - 1; ++i) copy();
+    int at = 0;                                      // of the two places for the warps' sums
+    for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < rows; row0 += step, at ^= 1) {
+        const int64_t row = row0 + sub;
+        const bool there = row < rows;
+        const float given = there ? a.rstd[row] : 0.0f;
+        typename R::Raw held[3][VEC ? 1 : NB];       // x, dy and the residual of a row that is not VEC
+        if constexpr (VEC) {
+            copy();
+            async_wait(DEPTH - 1);
+        } else {
+            Load<R, false> l[3][NB];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int n = there ? exist[b] : 0;
+                l[0][b] = Load<R, false>(static_cast<const Elem *>(a.x) + row * a.ldx + column(b), n);
+                l[1][b] = Load<R, false>(static_cast<const Elem *>(a.dy) + row * a.lddy + column(b), n);
+                l[2][b] = Load<R, false>(static_cast<const Elem *>(a.residual) + row * a.ldr + column(b), a.residual ? n : 0);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int k = 0; k < 3; ++k) held[k][b] = l[k][b].take(turn);
+        }
+        auto values = [&](int k, int b, float v[8]) {
+            if constexpr (VEC) {
+                uint4 r[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+#pragma unroll
+                for (int h = 0; h < PIECES; ++h)
+                    if (there && four(h) < exist[b]) r[h] = *reinterpret_cast<const uint4 *>(piece(place, k, b, h));
+                if constexpr (R::SIZE == 2) R::floats(r[0], v);
+                else R::floats({r[0], r[1]}, v);
+            } else {
+                R::floats(held[k][b], v);
+            }
+        };
+        // dy and x of block b in pairs
+        auto inputs = [&](int b, f2 u[4], f2 v[4]) {
+            float x[8], y[8];
+            values(0, b, x);
+            values(1, b, y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = f2pack(x[2 * j], x[2 * j + 1]);
+                u[j] = f2pack(y[2 * j], y[2 * j + 1]);
+            }
+        };
+        f2 g[NB][4], z[NB][4];
+        float tu = 0.0f, tv = 0.0f, hi, lo;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            inputs(b, g[b], z[b]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float p, q;
+                f2unpack(mul2(g[b][j], w[b][j]), p, q);
+                max_abs3(tu, p, q);
+                f2unpack(z[b][j], p, q);
+                max_abs3(tv, p, q);
+            }
+        }
+        {
+            Dot d;
+            const bool ok = d.begin<NB>(tu, tv);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d.add(mul2(g[b][j], w[b][j]), z[b][j]);
+            d.end(hi, lo);
+            if (!ok) hi = __uint_as_float(0x7F800000u);
+        }
+        warp_pair(hi, lo);
+        // too large for float32's products (or not finite): the row in 64 bits
+        bool wide = !(fabsf(hi) <= 1e30f);           // sixteen such sums are finite
+        int any = wide;
+        if (WPR > 1) {
+            if (lane == 0) parts[at][warp] = make_float2(hi, lo);
+            any = __syncthreads_or(wide);
+            const float2 *of = parts[at] + (warp - mine);
+            hi = of[0].x;
+            lo = of[0].y;
+            wide = !(fabsf(hi) <= 1e30f);
+#pragma unroll
+            for (int k = 1; k < WPR; ++k) {
+                wide |= !(fabsf(of[k].x) <= 1e30f);
+                add22(hi, lo, of[k].x, of[k].y);
+            }
+        }
+        float c = slope_of(hi, lo, a.mean, given);
+        if (any) {
+            double s = 0.0;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float p, q, x, y;
+                    f2unpack(mul2(g[b][j], w[b][j]), p, q);
+                    f2unpack(z[b][j], x, y);
+                    s = __dadd_rn(s, __dadd_rn(__dmul_rn((double)p, (double)x), __dmul_rn((double)q, (double)y)));
+                }
+            s = warp_double(s);
+            if (WPR > 1) {
+                if (lane == 0) wides[warp] = s;
+                __syncthreads();
+                s = 0.0;
+                for (int k = 0; k < WPR; ++k) s = __dadd_rn(s, wides[warp - mine + k]);
+            }
+            if (wide) c = (float)__dmul_rn(__ddiv_rn(s, (double)cols), __dmul_rn((double)given, (double)given));
+        }
+        const f2 rstd = both(given), slope = both(c);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                dw[b][j] = fma2(g[b][j], mul2(z[b][j], rstd), dw[b][j]);
+                f2unpack(mul2(fma2(mul2(z[b][j], slope), minus, mul2(g[b][j], w[b][j])), rstd), v[2 * j], v[2 * j + 1]);
+            }
+            if (a.residual) {
+                float r[8];
+                values(2, b, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], r[j]);
+            }
+            Elem *to = static_cast<Elem *>(a.dx) + row * a.ldd + column(b);
+            if constexpr (FOURS) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (there && four(h) < exist[b]) *reinterpret_cast<float4 *>(to + four(h)) = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+            } else {
+                block_store<R, VEC>(to, there ? exist[b] : 0, turn, R::rounded(v));
+            }
+        }
+        place = place + STAGE == DEPTH * STAGE ? 0 : place + STAGE;
+    }
+    if (!a.dw_parts) return;
+    // the rows' parts of dw, in their order
+    __syncthreads();
+    float *tile = reinterpret_cast<float *>(raw);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f2unpack(dw[b][j], v[2 * j], v[2 * j + 1]);
+        TileRow<RowF32>{reinterpret_cast<uint32_t *>(tile + (warp * NB + b) * 256)}.put(RowF32::rounded(v));
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < WPR * NB * 256; i += 32 * W) {
+        const int block = i >> 8, from = (block % WPR * NB + block / WPR) * 256 + (i & 255), col = 256 * block + (FOURS ? i & 255 : column_at(i & 255));
+        float s = tile[from];
+#pragma unroll
+        for (int k = 1; k < ROWS; ++k) s = __fadd_rn(s, tile[k * (WPR * NB * 256) + from]);
+        if (col < cols) a.dw_parts[blockIdx.x * parts_pitch(cols) + col] = s;
+    }
+}
+
+// dw from its parts: 32 columns a CTA, 32 warps' shares of the parts, then a
+// tree over the shares.
+constexpr int WEIGHT_WARPS = 32;
+__global__ void __launch_bounds__(32 * WEIGHT_WARPS)
 rms_weight_kernel(const float *parts, int n, int64_t cols, int64_t pitch, void *dw, int kind) {
-    __shared__ float share[WARPS][32];
+    __shared__ float share[WEIGHT_WARPS][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = 32 * (int64_t)blockIdx.x + lane;
+    const int64_t c0 = 32 * (int64_t)blockIdx.x;
     pdl_wait();
     pdl_trigger();
     float s = 0.0f;
-    if (c < cols) {
-        int i = warp;
-        for (; i + 7 * WARPS < n; i += 8 * WARPS) {          // 8 loads in flight
-            float v[8];
+    if (c0 + lane < cols) {
+        float v[10];                                 // all loads in flight; n is 304 at most
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = parts[(i + j * WARPS) * pitch + c];
+        for (int j = 0; j < 10; ++j) v[j] = warp + j * WEIGHT_WARPS < n ? parts[(warp + j * WEIGHT_WARPS) * pitch + c0 + lane] : 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s = __fadd_rn(s, v[j]);
-        }
-        for (; i < n; i += WARPS) s = __fadd_rn(s, parts[i * pitch + c]);
+        for (int j = 0; j < 10; ++j) s = __fadd_rn(s, v[j]);
     }
     share[warp][lane] = s;
     __syncthreads();
-    if (warp != 0 || c >= cols) return;
-    for (int i = 1; i < WARPS; ++i) s = __fadd_rn(s, share[i][lane]);
+    s = share[lane][warp];                           // a column a warp
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, off));
+    const int64_t c = c0 + warp;
+    if (lane != 0 || c >= cols) return;
     if (kind == ZS_DTYPE_FP32) static_cast<float *>(dw)[c] = s;
     else static_cast<uint16_t *>(dw)[c] = (uint16_t)(kind == ZS_DTYPE_FP16 ? FP16T::from_f32(s) : BF16T::from_f32(s));
 }
@@ -1068,7 +1309,7 @@ static cudaError_t sums_launch(const SumArgs &a, int64_t end, cudaStream_t s) {
 }
 
 template <class... P>
-static cudaError_t tile_launch(void (*kernel)(P...), std::atomic<bool> (&set)[64], int smem, int64_t grid, cudaStream_t s, const P &...args) {
+static cudaError_t tile_launch(void (*kernel)(P...), std::atomic<bool> (&set)[64], int smem, int64_t grid, int threads, cudaStream_t s, const P &...args) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1078,7 +1319,7 @@ static cudaError_t tile_launch(void (*kernel)(P...), std::atomic<bool> (&set)[64
         if (e != cudaSuccess) return e;
         set[dev].store(true, std::memory_order_relaxed);
     }
-    return launch_dependent(kernel, (unsigned)grid, THREADS, smem, 1, s, args...);
+    return launch_dependent(kernel, (unsigned)grid, threads, smem, 1, s, args...);
 }
 
 static int col_blocks_of(int64_t cols) { return (int)((cols + TILE_COLS - 1) / TILE_COLS); }
@@ -1087,7 +1328,7 @@ template <class R, bool VEC>
 static cudaError_t norm_tile(const NormArgs &a, int64_t block0, int64_t blocks, cudaStream_t s) {
     static std::atomic<bool> set[64];
     const int cb = col_blocks_of(a.held.cols);
-    return tile_launch(rms_tile_kernel<R, VEC>, set, tile_smem<R>(false), blocks * cb, s, a, block0, cb);
+    return tile_launch(rms_tile_kernel<R, VEC>, set, tile_smem<R>(false), blocks * cb, THREADS, s, a, block0, cb);
 }
 template <class R>
 static cudaError_t norm_tiles(const NormArgs &a, cudaStream_t s) {
@@ -1103,19 +1344,43 @@ static cudaError_t norm_tiles(const NormArgs &a, cudaStream_t s) {
     return cudaSuccess;
 }
 
-// Parts of dw: a number of the sizes alone, so that a sum has the same bits
-// whatever forms are asked for.  256 of them keep scratch small and the GPU busy.
+// Parts of dw, of a dx that is held and of one that is not: numbers of the sizes
+// alone, so that a sum has the same bits every time.  256 of the former keep
+// scratch small and the GPU busy; the latter are two CTAs an SM.
 static int64_t back_parts(int64_t rows) {
     const int64_t blocks = (rows + TILE_ROWS - 1) / TILE_ROWS;
     return blocks < 256 ? blocks : 256;
 }
-static int64_t parts_pitch(int64_t cols) { return (cols + TILE_COLS - 1) / TILE_COLS * TILE_COLS; }
+
+// One reading of a row: as many warps as give each lane 16 columns.
+constexpr int64_t WHOLE_MOST = 8192;                 // columns
+static int whole_warps(int64_t cols) { return cols <= 512 ? 1 : cols <= 2048 ? 4 : cols <= 4096 ? 8 : 16; }
+static int64_t whole_parts(int64_t rows, int64_t cols, int ctas) {
+    const int64_t per = cols <= 2048 ? WARPS / whole_warps(cols) : 1, n = (rows + per - 1) / per;
+    return n < 152 * ctas ? n : 152 * ctas;
+}
+
+template <class R, int WPR, bool VEC>
+static cudaError_t whole_launch(BackArgs &a, cudaStream_t s) {
+    static std::atomic<bool> set[64];
+    a.parts = whole_parts(a.held.rows, a.held.cols, whole_ctas<R, VEC>(WPR));
+    return tile_launch(rms_back_rows_kernel<R, WPR, VEC>, set, whole_smem<R, VEC>(WPR), a.parts, 32 * whole_cta_warps(WPR), s, a);
+}
+template <class R, bool VEC>
+static cudaError_t back_whole(BackArgs &a, cudaStream_t s) {
+    switch (whole_warps(a.held.cols)) {
+        case 1: return whole_launch<R, 1, VEC>(a, s);
+        case 4: return whole_launch<R, 4, VEC>(a, s);
+        case 8: return whole_launch<R, 8, VEC>(a, s);
+        default: return whole_launch<R, 16, VEC>(a, s);
+    }
+}
 
 template <class R, bool VEC>
 static cudaError_t back_tile(const BackArgs &a, int64_t block0, int64_t block1, bool add, cudaStream_t s) {
     static std::atomic<bool> set[64];
     const int cb = col_blocks_of(a.held.cols);
-    return tile_launch(rms_back_kernel<R, VEC>, set, tile_smem<R>(true), a.parts * cb, s, a, block0, block1, cb, parts_pitch(a.held.cols), add);
+    return tile_launch(rms_back_kernel<R, VEC>, set, tile_smem<R>(true), a.parts * cb, THREADS, s, a, block0, block1, cb, parts_pitch(a.held.cols), add);
 }
 template <class R>
 static cudaError_t back_tiles(const BackArgs &a, cudaStream_t s) {
@@ -1242,7 +1507,9 @@ zs_status zs_rms_norm_scratch(int64_t rows, int64_t cols, int64_t *bytes) {
     if (!bytes) return zs_fail(ZS_EINVAL, "%s: NULL result", fn);
     if (rows < 0 || cols < 0 || rows >= MOST || cols >= MOST)
         return zs_fail(ZS_EINVAL, "%s: %lld x %lld out of range", fn, (long long)rows, (long long)cols);
-    *bytes = rows > 0 && cols > 0 ? 4 * (zsk::back_parts(rows) * zsk::parts_pitch(cols) + rows) : 0;
+    int64_t parts = zsk::back_parts(rows);
+    if (cols <= zsk::WHOLE_MOST && zsk::whole_parts(rows, cols, 2) > parts) parts = zsk::whole_parts(rows, cols, 2);
+    *bytes = rows > 0 && cols > 0 ? 4 * (parts * zsk::parts_pitch(cols) + rows) : 0;
     zs_clear_error();
     return ZS_OK;
 }
@@ -1270,16 +1537,22 @@ zs_status zs_rms_norm_backward(const void *dy, int64_t lddy, const void *x, int6
     using namespace zsk;
     BackArgs a;
     a.dy = dy; a.x = x; a.w = weight; a.residual = residual; a.rstd = rstd; a.dx = dx;
-    a.parts = back_parts(rows);
+    // one reading where a row fits the registers, unless columns or rows of 4 bits want the tiles
+    const bool whole = !r_codes && !c_codes && cols <= WHOLE_MOST;
+    a.parts = whole ? 0 : back_parts(rows);     // 0: set with the launch
     a.dw_parts = dw ? scratch : nullptr;
     a.slopes = scratch + a.parts * parts_pitch(cols);
     a.lddy = lddy; a.ldx = ldx; a.ldr = ldr; a.ldd = lddx;
     a.w_kind = weight_dtype; a.vec = vec; a.vec_w = vec_w; a.minus_one = -1.0f; a.mean = mean_of(cols);
     a.held = {static_cast<uint8_t *>(r_codes), static_cast<uint8_t *>(r_scales), static_cast<uint8_t *>(c_codes),
               static_cast<uint8_t *>(c_scales), rows, cols};
-    cudaError_t e = by_type(dtype, [&](auto t) { return back_tiles<decltype(t)>(a, s); });
+    cudaError_t e = by_type(dtype, [&](auto t) {
+        using R = decltype(t);
+        if (!whole) return back_tiles<R>(a, s);
+        return a.vec && cols % 8 == 0 ? back_whole<R, true>(a, s) : back_whole<R, false>(a, s);
+    });
     if (e == cudaSuccess && dw)
-        e = launch_dependent(rms_weight_kernel, (unsigned)((cols + 31) / 32), THREADS, 0, 1, s, a.dw_parts, (int)a.parts, cols, parts_pitch(cols), dw, dw_dtype);
+        e = launch_dependent(rms_weight_kernel, (unsigned)((cols + 31) / 32), 32 * WEIGHT_WARPS, 0, 1, s, a.dw_parts, (int)a.parts, cols, parts_pitch(cols), dw, dw_dtype);
     return cuda_status(e, fn);
 }
 

@@ -31,7 +31,7 @@ struct Raw8;
 template <class T>
 struct Raw8<H16G<T>> {
     uint4 w;
-    __device__ __forceinline__ void shared(uint32_t at) { w = lds16(at); }
+    __device__ __forceinline__ void shared(uint32_t at, bool) { w = lds16(at); }
     __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
     // element i of the 8
     __device__ __forceinline__ void put(const void *p, int x, int i) {
@@ -43,9 +43,9 @@ struct Raw8<H16G<T>> {
 template <>
 struct Raw8<F32G> {
     uint4 a, b;
-    __device__ __forceinline__ void shared(uint32_t at) {
+    __device__ __forceinline__ void shared(uint32_t at, bool second) {
         a = lds16(at);
-        b = lds16(at + 16 * NORM_THREADS);
+        if (second) b = lds16(at + 16 * NORM_THREADS);
     }
     __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void put(const void *p, int x, int i) {
@@ -153,7 +153,10 @@ template <class G>
 __global__ void __launch_bounds__(NORM_THREADS, norm_ctas<G>())
 norm_tensors_kernel(const ZsChunk *chunks, int n_chunks, double *partials) {
     extern __shared__ __align__(16) uint8_t ring[];
-    constexpr int EACH = 8 * G::SIZE;                // bytes of a group
+    // a group is one or two pieces of 16 bytes, each beside the neighbours': a
+    // warp's copies then read whole sectors (two pieces side by side: 59 us for 51M
+    // fp32 gradients, 38 so)
+    constexpr int PIECES = G::SIZE / 2, ONE = 16 / G::SIZE;
     __shared__ double red[NORM_THREADS / 32];
     pdl_wait();
     pdl_trigger();
@@ -171,12 +174,9 @@ norm_tensors_kernel(const ZsChunk *chunks, int n_chunks, double *partials) {
     };
     auto copy = [&] {
 #pragma unroll
-        for (int g = 0; g < NORM_GROUPS; ++g) {
-            const int x = 8 * (t + NORM_THREADS * g);
-            if (x >= vec) break;
-#pragma unroll
-            for (int h = 0; h < EACH / 16; ++h)
-                async16(mine + slot + (g * (EACH / 16) + h) * (16 * NORM_THREADS), static_cast<const char *>(grad) + (int64_t)x * G::SIZE + 16 * h);
+        for (int p = 0; p < NORM_GROUPS * PIECES; ++p) {
+            if (ONE * (t + NORM_THREADS * p) >= vec) break;
+            async16(mine + slot + p * (16 * NORM_THREADS), static_cast<const char *>(grad) + 16 * (t + NORM_THREADS * p));
         }
         asm volatile("cp.async.commit_group;" : : : "memory");
         slot = slot + norm_stage<G>() == norm_ring<G>() ? 0 : slot + norm_stage<G>();
@@ -200,14 +200,15 @@ norm_tensors_kernel(const ZsChunk *chunks, int n_chunks, double *partials) {
         copy();
         const int len = chunks[c].len, whole = chunks[c].tensor < 0 ? 0 : len & ~7;
         asm volatile("cp.async.wait_group %0;" : : "n"(NORM_DEPTH - 1) : "memory");
-        if (8 * t < whole) {
+        if (ONE * t < whole) {
             Raw8<G> r[NORM_GROUPS];
             int n = 0;
 #pragma unroll
             for (int g = 0; g < NORM_GROUPS; ++g) {
                 r[g].zero();
-                if (8 * (t + NORM_THREADS * g) < whole) {
-                    r[g].shared(mine + place + g * (EACH / 16) * (16 * NORM_THREADS));
+                const int x = ONE * (t + NORM_THREADS * PIECES * g);
+                if (x < whole) {
+                    r[g].shared(mine + place + g * PIECES * (16 * NORM_THREADS), x + ONE * NORM_THREADS < whole);
                     n = g + 1;
                 }
             }
