@@ -15,11 +15,14 @@
 //
 // A result held along its columns needs 32 rows at a time, which no SM holds
 // whole.  One kernel makes the rows' sums, another takes tiles of 32 rows by 512
-// columns; the second reading of the inputs comes from L2, since long matrices
-// go by as many rows as fit there.  (Clusters that hold 32 rows and exchange
-// their sums through distributed shared memory read once, but took 41 us for
-// 4096 x 4096 bf16 in both forms: 57 of them fit the GPU, and the 128 blocks of
-// rows need three turns of all that lies between two barriers.)
+// columns and reads the inputs again, from L2 as far as they lie there: 4096 x
+// 4096 bf16 in both forms takes 36 us, backward 51.  Taking long matrices by as
+// many rows as fit L2 costs more in the kernels' ends than it gains (backward
+// pass of 16384 x 4096 bf16: 215 us by 64 MB, 186 by 128 MB, 161 whole), and the
+// reverse order of tiles changes nothing (within 1 %).  Clusters that hold 32 rows and
+// exchange their sums through distributed shared memory read once, but took 41
+// us: 57 of them fit the GPU, and the 128 blocks of rows need three turns of all
+// that lies between two barriers.
 #include <atomic>
 
 #include "zs_launch.h"
@@ -526,7 +529,7 @@ rms_rows_kernel(NormArgs a) {
 // aligned and whole pieces of 8.
 struct SumArgs {
     const void *x, *other, *w;       // other: the residual or NULL; dy
-    int64_t ldx, ldo, rows, cols, row0;
+    int64_t ldx, ldo, rows, cols;
     int32_t w_kind;
     bool vec_w;
     float eps;
@@ -543,7 +546,7 @@ rms_sums_kernel(SumArgs a) {
     __shared__ double wides[WARPS];
     __shared__ __align__(16) typename R::Elem turns[VEC ? 1 : WARPS][VEC ? 8 : 256];
     const int lane = threadIdx.x & 31, warp = warp_index(), mine = warp % WPR;
-    const int64_t row = a.row0 + (int64_t)blockIdx.x * (WARPS / WPR) + warp / WPR;
+    const int64_t row = (int64_t)blockIdx.x * (WARPS / WPR) + warp / WPR;
     const bool there = row < a.rows;
     typename R::Elem *turn = turns[VEC ? 0 : warp];
     const typename R::Elem *x = static_cast<const typename R::Elem *>(a.x) + row * a.ldx, *other = static_cast<const typename R::Elem *>(a.other) + row * a.ldo;
@@ -798,12 +801,12 @@ constexpr int tile_ctas(bool back) { return R::SIZE == 4 || !back ? 3 : 2; }    
 // a group), and through shared memory the one along the columns.
 template <class R, bool VEC>
 __global__ void __launch_bounds__(THREADS, tile_ctas<R>(false))
-rms_tile_kernel(NormArgs a, int64_t block0, int col_blocks) {
+rms_tile_kernel(NormArgs a, int col_blocks) {
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ __align__(16) typename R::Elem turns[VEC ? 1 : WARPS][VEC ? 8 : 256];
     constexpr bool TWO = R::SIZE == 2;               // both inputs in shared memory
     const int lane = threadIdx.x & 31, warp = warp_index();
-    const int64_t rb = block0 + blockIdx.x / col_blocks, row0 = TILE_ROWS * rb, col0 = (int64_t)(blockIdx.x % col_blocks) * TILE_COLS;
+    const int64_t rb = blockIdx.x / col_blocks, row0 = TILE_ROWS * rb, col0 = (int64_t)(blockIdx.x % col_blocks) * TILE_COLS;
     const int64_t rows = a.held.rows, cols = a.held.cols;
     const int exist = (int)min((int64_t)TILE_ROWS, max((int64_t)0, rows - row0)), first = part(cols, col0), second = part(cols, col0 + 256);
     typename R::Elem *turn = turns[VEC ? 0 : warp];
@@ -890,11 +893,10 @@ struct BackArgs {
 __host__ __device__ constexpr int64_t parts_pitch(int64_t cols) { return (cols + TILE_COLS - 1) / TILE_COLS * TILE_COLS; }
 
 // The same of the backward pass, c being known: a CTA takes its 512 columns of
-// the row blocks b, b + parts, ... and adds up their part of dw (add: to what
-// the rows before have left).
+// the row blocks b, b + parts, ... and adds up their part of dw.
 template <class R, bool VEC>
 __global__ void __launch_bounds__(THREADS, tile_ctas<R>(true))
-rms_back_kernel(BackArgs a, int64_t block0, int64_t block1, int col_blocks, int64_t pitch, bool add) {
+rms_back_kernel(BackArgs a, int64_t blocks, int col_blocks) {
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ __align__(16) typename R::Elem turns[VEC ? 1 : WARPS][VEC ? 8 : 256];
     constexpr bool TWO = R::SIZE == 2;
@@ -917,7 +919,7 @@ rms_back_kernel(BackArgs a, int64_t block0, int64_t block1, int col_blocks, int6
         for (int j = 0; j < 4; ++j) w[b][j] = f2pack(v[2 * j], v[2 * j + 1]);
     }
     const f2 minus = both(a.minus_one);
-    for (int64_t rb = block0 + part_index; rb < block1; rb += a.parts) {
+    for (int64_t rb = part_index; rb < blocks; rb += a.parts) {
         const int64_t row0 = TILE_ROWS * rb;
         const int exist = (int)min((int64_t)TILE_ROWS, max((int64_t)0, rows - row0));
         auto there = [&](int i, int b) { return warp + WARPS * i >= exist ? 0 : b ? second : first; };
@@ -995,8 +997,7 @@ rms_back_kernel(BackArgs a, int64_t block0, int64_t block1, int col_blocks, int6
         float s = tile[at];
 #pragma unroll
         for (int i = 1; i < WARPS; ++i) s = __fadd_rn(s, tile[i * TILE_COLS + at]);
-        float *to = a.dw_parts + part_index * pitch + col0 + (at & ~255) + column_at(at & 255);
-        *to = add ? __fadd_rn(*to, s) : s;
+        a.dw_parts[part_index * parts_pitch(cols) + col0 + (at & ~255) + column_at(at & 255)] = s;
     }
 }
 
@@ -1290,17 +1291,10 @@ static cudaError_t rows_of(const NormArgs &a, int64_t grid_rows, cudaStream_t s)
     return rows_launch<R, 8, 0>(a, grid_rows, s);
 }
 
-// Rows whose two inputs take about half of L2, a multiple of 256 (whole atoms of
-// the scales along the columns): they are summed, and read again from there.
-static int64_t rows_at_once(int64_t cols, int size) {
-    const int64_t fit = ((int64_t)64 << 20) / (2 * cols * size) / 256 * 256;
-    return fit > 256 ? fit : 256;
-}
-
 template <class R, bool BACK, bool VEC>
-static cudaError_t sums_launch(const SumArgs &a, int64_t end, cudaStream_t s) {
+static cudaError_t sums_launch(const SumArgs &a, cudaStream_t s) {
     // as many warps a row as give every SM 16 (with 32, 4096 x 4096 bf16 took 2 us more)
-    const int64_t rows = end - a.row0;
+    const int64_t rows = a.rows;
     auto go = [&](auto kernel, int wpr) { return launch_dependent(kernel, (unsigned)((rows * wpr + WARPS - 1) / WARPS), THREADS, 0, 1, s, a); };
     if (rows >= 2432 || a.cols <= 1024) return go(rms_sums_kernel<R, 1, BACK, VEC>, 1);
     if (rows >= 1216 || a.cols <= 2048) return go(rms_sums_kernel<R, 2, BACK, VEC>, 2);
@@ -1325,23 +1319,13 @@ static cudaError_t tile_launch(void (*kernel)(P...), std::atomic<bool> (&set)[64
 static int col_blocks_of(int64_t cols) { return (int)((cols + TILE_COLS - 1) / TILE_COLS); }
 
 template <class R, bool VEC>
-static cudaError_t norm_tile(const NormArgs &a, int64_t block0, int64_t blocks, cudaStream_t s) {
-    static std::atomic<bool> set[64];
-    const int cb = col_blocks_of(a.held.cols);
-    return tile_launch(rms_tile_kernel<R, VEC>, set, tile_smem<R>(false), blocks * cb, THREADS, s, a, block0, cb);
-}
-template <class R>
 static cudaError_t norm_tiles(const NormArgs &a, cudaStream_t s) {
-    const int64_t rows = a.held.rows, cols = a.held.cols, step = rows_at_once(cols, R::SIZE), all = 4 * mx4_atoms(rows);
-    const bool pieces = a.vec && cols % 8 == 0;
-    for (int64_t r = 0; r < rows; r += step) {
-        const int64_t end = rows - r > step ? r + step : rows, block0 = r / TILE_ROWS, blocks = (end == rows ? all : end / TILE_ROWS) - block0;
-        const SumArgs sums = {a.x, a.residual, nullptr, a.ldx, a.ldr, rows, cols, r, 0, true, a.eps, a.mean, nullptr, a.rstd};
-        cudaError_t e = pieces ? sums_launch<R, false, true>(sums, end, s) : sums_launch<R, false, false>(sums, end, s);
-        if (e == cudaSuccess) e = pieces ? norm_tile<R, true>(a, block0, blocks, s) : norm_tile<R, false>(a, block0, blocks, s);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    static std::atomic<bool> set[64];
+    const int64_t rows = a.held.rows, cols = a.held.cols;
+    const int cb = col_blocks_of(cols);
+    const SumArgs sums = {a.x, a.residual, nullptr, a.ldx, a.ldr, rows, cols, 0, true, a.eps, a.mean, nullptr, a.rstd};
+    const cudaError_t e = sums_launch<R, false, VEC>(sums, s);
+    return e != cudaSuccess ? e : tile_launch(rms_tile_kernel<R, VEC>, set, tile_smem<R>(false), 4 * mx4_atoms(rows) * cb, THREADS, s, a, cb);
 }
 
 // Parts of dw, of a dx that is held and of one that is not: numbers of the sizes
@@ -1377,24 +1361,14 @@ static cudaError_t back_whole(BackArgs &a, cudaStream_t s) {
 }
 
 template <class R, bool VEC>
-static cudaError_t back_tile(const BackArgs &a, int64_t block0, int64_t block1, bool add, cudaStream_t s) {
-    static std::atomic<bool> set[64];
-    const int cb = col_blocks_of(a.held.cols);
-    return tile_launch(rms_back_kernel<R, VEC>, set, tile_smem<R>(true), a.parts * cb, THREADS, s, a, block0, block1, cb, parts_pitch(a.held.cols), add);
-}
-template <class R>
 static cudaError_t back_tiles(const BackArgs &a, cudaStream_t s) {
-    const int64_t rows = a.held.rows, cols = a.held.cols, step = rows_at_once(cols, R::SIZE);
-    const int64_t all = a.held.c_codes ? 4 * mx4_atoms(rows) : a.held.r_codes ? 4 * mx4_row_tiles(rows) : (rows + TILE_ROWS - 1) / TILE_ROWS;
-    const bool pieces = a.vec && cols % 8 == 0;
-    for (int64_t r = 0; r < rows; r += step) {
-        const int64_t end = rows - r > step ? r + step : rows, block0 = r / TILE_ROWS, block1 = end == rows ? all : end / TILE_ROWS;
-        const SumArgs sums = {a.x, a.dy, a.w, a.ldx, a.lddy, rows, cols, r, a.w_kind, a.vec_w, 0.0f, a.mean, a.rstd, a.slopes};
-        cudaError_t e = pieces ? sums_launch<R, true, true>(sums, end, s) : sums_launch<R, true, false>(sums, end, s);
-        if (e == cudaSuccess) e = pieces ? back_tile<R, true>(a, block0, block1, r > 0, s) : back_tile<R, false>(a, block0, block1, r > 0, s);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    static std::atomic<bool> set[64];
+    const int64_t rows = a.held.rows, cols = a.held.cols;
+    const int64_t blocks = a.held.c_codes ? 4 * mx4_atoms(rows) : a.held.r_codes ? 4 * mx4_row_tiles(rows) : (rows + TILE_ROWS - 1) / TILE_ROWS;
+    const int cb = col_blocks_of(cols);
+    const SumArgs sums = {a.x, a.dy, a.w, a.ldx, a.lddy, rows, cols, a.w_kind, a.vec_w, 0.0f, a.mean, a.rstd, a.slopes};
+    const cudaError_t e = sums_launch<R, true, VEC>(sums, s);
+    return e != cudaSuccess ? e : tile_launch(rms_back_kernel<R, VEC>, set, tile_smem<R>(true), a.parts * cb, THREADS, s, a, blocks, cb);
 }
 
 template <class F>
@@ -1499,7 +1473,9 @@ zs_status zs_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t 
         const int64_t grid_rows = r_codes ? 128 * mx4_row_tiles(rows) : rows;
         return cuda_status(by_type(dtype, [&](auto t) { return rows_of<decltype(t)>(a, grid_rows, s); }), fn);
     }
-    return cuda_status(by_type(dtype, [&](auto t) { return norm_tiles<decltype(t)>(a, s); }), fn);
+    return cuda_status(by_type(dtype, [&](auto t) {
+        return a.vec && cols % 8 == 0 ? norm_tiles<decltype(t), true>(a, s) : norm_tiles<decltype(t), false>(a, s);
+    }), fn);
 }
 
 zs_status zs_rms_norm_scratch(int64_t rows, int64_t cols, int64_t *bytes) {
@@ -1548,8 +1524,9 @@ zs_status zs_rms_norm_backward(const void *dy, int64_t lddy, const void *x, int6
               static_cast<uint8_t *>(c_scales), rows, cols};
     cudaError_t e = by_type(dtype, [&](auto t) {
         using R = decltype(t);
-        if (!whole) return back_tiles<R>(a, s);
-        return a.vec && cols % 8 == 0 ? back_whole<R, true>(a, s) : back_whole<R, false>(a, s);
+        const bool pieces = a.vec && cols % 8 == 0;
+        if (whole) return pieces ? back_whole<R, true>(a, s) : back_whole<R, false>(a, s);
+        return pieces ? back_tiles<R, true>(a, s) : back_tiles<R, false>(a, s);
     });
     if (e == cudaSuccess && dw)
         e = launch_dependent(rms_weight_kernel, (unsigned)((cols + 31) / 32), 32 * WEIGHT_WARPS, 0, 1, s, a.dw_parts, (int)a.parts, cols, parts_pitch(cols), dw, dw_dtype);
