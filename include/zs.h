@@ -778,7 +778,8 @@ zs_status zs_norm_tensors(const zs_tensors *list, double *scratch, float max_nor
 /* Clipping in place, for an update that takes no coefficient: every gradient
  * of the list becomes rne(float(grad) * *d_clip_coef).  With ZS_SKIP_NONFINITE
  * in d_flags (NULL: never), or a coefficient of 1, nothing is written.  The
- * gradients have to be writable.  Errors: as zs_norm_tensors. */
+ * gradients have to be writable, and none may be in the list twice.  Errors: as
+ * zs_norm_tensors. */
 zs_status zs_clip_tensors(const zs_tensors *list, const float *d_clip_coef, const int32_t *d_flags,
                           void *stream);
 
@@ -842,9 +843,12 @@ zs_status zs_mx4_matmul(int64_t m, int64_t n, int64_t k, const void *a_codes, co
  * of that largest.  The 32 products of a group are added in the tensor cores, 16
  * at a time, to an fp32 accumulator (each time off by at most 2^-22 of the
  * magnitudes), times the group's scale in fp32 to the sum of the groups, whose
- * parts are added in an order that the sizes alone set: out is within
- * (ceil(k / 32) + 24) 2^-22 sum |x w| before its one rounding to out_dtype.
- * A NaN group is NaN, k = 0 gives zeros.  m at most ZS_MATVEC_MAX_TOKENS.  Errors: ZS_EINVAL, ZS_ECUDA. */
+ * parts are added in an order that the sizes and the GPU set: out is within
+ * (ceil(k / 32) + 24) 2^-22 sum |x w| before its one rounding to out_dtype.  A
+ * group's sum before its scale is an fp32 number as well: past 2^128 it is an
+ * infinity (|x| below 2^120 never gets there), and below 2^-126 it loses bits.
+ * A NaN group is NaN, k = 0 gives zeros.  out must not overlap x.  m at most
+ * ZS_MATVEC_MAX_TOKENS.  Errors: ZS_EINVAL, ZS_ECUDA. */
 #define ZS_MATVEC_MAX_TOKENS 1024
 zs_status zs_mx4_matvec(int64_t m, int64_t n, int64_t k, const void *x, int64_t ldx, int32_t dtype,
                         const void *w_codes, const void *w_scales, void *out, int64_t ldo,

@@ -9,9 +9,10 @@ fails loudly when libzs.so is missing: there is no fallback.
 Functions keep the C names: zs_build_partition, zs_plan_upload,
 zs_partition, zs_reduce_scatter, zs_grad_norm, zs_adam_step,
 zs_all_gather_coalesced, zs_shard_step, plus the plan queries; and, for
-training with little memory, zs_build_tensors / zs_adam_tensors and
-zs_mx4_quantize, zs_mx4_dequantize, zs_mx4_matmul, which take torch tensors
-and read sizes, strides and types from them.
+training with little memory, zs_build_tensors / zs_norm_tensors,
+zs_clip_tensors, zs_adam_tensors, zs_mx4_quantize, zs_mx4_dequantize,
+zs_mx4_matmul, zs_mx4_matvec, and zs_rms_norm, zs_rms_norm_backward, which
+take torch tensors and read sizes, strides and types from them.
 """
 from __future__ import annotations
 

@@ -4,7 +4,10 @@
 // norm = sqrt(sum of squares) / S over every gradient of the list, with the
 // coefficient and the flag that zs_adam_tensors takes.  One read of the
 // gradients: 2 or 4 bytes an element at two to four instructions, so bandwidth
-// bounds it.
+// bounds it.  202M bf16 gradients: 77 us with the caches flushed before, 5.3 TB/s
+// (0.78 of a copy's rate; instructions and loads share the issue slots).  100M
+// fp16 gradients clipped in place, norm included: 97 us, 6.2 TB/s of two reads
+// and a write.  A short list is two launches: 4.5 us in a graph.
 #include <atomic>
 
 #include "zs_launch.h"
