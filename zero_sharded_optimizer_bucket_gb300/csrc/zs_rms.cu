@@ -16,7 +16,9 @@
 // A result held along its columns needs 32 rows at a time, which no SM holds
 // whole.  One kernel makes the rows' sums, another takes tiles of 32 rows by 512
 // columns and reads the inputs again, from L2 as far as they lie there: 4096 x
-// 4096 bf16 in both forms takes 36 us, backward 51.  Taking long matrices by as
+// 4096 bf16 in both forms takes 36 us.  The backward pass, whose dx is always
+// written, reads its inputs once and makes the forms from dx (42 us; by tiles 51,
+// which rows of more than 8192 columns take).  Taking long matrices by as
 // many rows as fit L2 costs more in the kernels' ends than it gains (backward
 // pass of 16384 x 4096 bf16: 215 us by 64 MB, 186 by 128 MB, 161 whole), and the
 // reverse order of tiles changes nothing (within 1 %).  Clusters that hold 32 rows and
@@ -1009,7 +1011,7 @@ rms_back_kernel(BackArgs a, int64_t blocks, int col_blocks) {
     }
 }
 
-// The backward pass of a dx that is not held, in one reading: WPR warps take a
+// The backward pass in one reading, dx as it is: WPR warps take a
 // row, two blocks of 256 columns each, from its sum to its result.  VEC: the next
 // rows' x, dy and residual are on their way to shared memory, a lane's 8 to a
 // place of its own (32 bits: two fours, each beside the neighbours', since a
@@ -1336,9 +1338,9 @@ static cudaError_t norm_tiles(const NormArgs &a, cudaStream_t s) {
     return e != cudaSuccess ? e : tile_launch(rms_tile_kernel<R, VEC>, set, tile_smem<R>(false), 4 * mx4_atoms(rows) * cb, THREADS, s, a, cb);
 }
 
-// Parts of dw, of a dx that is held and of one that is not: numbers of the sizes
-// alone, so that a sum has the same bits every time.  256 of the former keep
-// scratch small and the GPU busy; the latter are two CTAs an SM.
+// Parts of dw, by tiles and by whole rows: numbers of the sizes alone, so that a
+// sum has the same bits every time, whatever forms are asked for.  256 of the
+// former keep scratch small and the GPU busy; the latter are two CTAs an SM.
 static int64_t back_parts(int64_t rows) {
     const int64_t blocks = (rows + TILE_ROWS - 1) / TILE_ROWS;
     return blocks < 256 ? blocks : 256;
@@ -1521,8 +1523,10 @@ zs_status zs_rms_norm_backward(const void *dy, int64_t lddy, const void *x, int6
     using namespace zsk;
     BackArgs a;
     a.dy = dy; a.x = x; a.w = weight; a.residual = residual; a.rstd = rstd; a.dx = dx;
-    // one reading where a row fits the registers, unless columns or rows of 4 bits want the tiles
-    const bool whole = !r_codes && !c_codes && cols <= WHOLE_MOST;
+    // one reading where a row fits the registers, and the forms from dx, which then
+    // lies in L2: 4096 x 4096 bf16 in both 42 us, by tiles 51; fp32 63 and 104; 4000 x
+    // 4003 bf16 65 and 88; 300 x 1000 bf16 8 and 14; 16384 x 1024 bf16 53 and 51
+    const bool whole = cols <= WHOLE_MOST;
     a.parts = whole ? 0 : back_parts(rows);     // 0: set with the launch
     a.dw_parts = dw ? scratch : nullptr;
     a.slopes = scratch + a.parts * parts_pitch(cols);
@@ -1538,6 +1542,8 @@ zs_status zs_rms_norm_backward(const void *dy, int64_t lddy, const void *x, int6
     });
     if (e == cudaSuccess && dw)
         e = launch_dependent(rms_weight_kernel, (unsigned)((cols + 31) / 32), 32 * WEIGHT_WARPS, 0, 1, s, a.dw_parts, (int)a.parts, cols, parts_pitch(cols), dw, dw_dtype);
+    if (e == cudaSuccess && whole && (r_codes || c_codes))
+        return zs_mx4_quantize(dx, rows, cols, lddx, dtype, r_codes, r_scales, c_codes, c_scales, stream);
     return cuda_status(e, fn);
 }
 
