@@ -17,7 +17,7 @@
 // whole.  One kernel makes the rows' sums, another takes tiles of 32 rows by 512
 // columns and reads the inputs again, from L2 as far as they lie there: 4096 x
 // 4096 bf16 in both forms takes 36 us.  The backward pass, whose dx is always
-// written, reads its inputs once and makes the forms from dx (42 us; by tiles 51,
+// written, reads its inputs once and makes the forms from dx (41 us; by tiles 51,
 // which rows of more than 8192 columns take).  Taking long matrices by as
 // many rows as fit L2 costs more in the kernels' ends than it gains (backward
 // pass of 16384 x 4096 bf16: 215 us by 64 MB, 186 by 128 MB, 161 whole), and the
@@ -276,6 +276,18 @@ __device__ __forceinline__ f2 both(float x) { return f2pack(x, x); }
 __device__ __forceinline__ void warp_pair(float &hi, float &lo) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
+        const float h2 = __shfl_xor_sync(0xFFFFFFFFu, hi, off), l2 = __shfl_xor_sync(0xFFFFFFFFu, lo, off);
+        add22(hi, lo, h2, l2);
+    }
+}
+// The same of the pairs of a row's WPR warps, by lanes of one of them: fewer
+// instructions than one pair after another in every lane (2048 x 8192 bf16
+// backward 31 us, not 35), but a longer way for a row that waits for nothing else
+// (4096 x 4096 bf16 forward along the rows 29 us, 27 one after another).
+template <int WPR>
+__device__ __forceinline__ void row_pair(float &hi, float &lo) {
+#pragma unroll
+    for (int off = 1; off < WPR; off <<= 1) {
         const float h2 = __shfl_xor_sync(0xFFFFFFFFu, hi, off), l2 = __shfl_xor_sync(0xFFFFFFFFu, lo, off);
         add22(hi, lo, h2, l2);
     }
@@ -1018,8 +1030,9 @@ rms_back_kernel(BackArgs a, int64_t blocks, int col_blocks) {
 // warp's copies then read whole sectors; 4096 x 4096: 49 us, not 76); other rows
 // go through registers.  A CTA takes WARPS / WPR
 // rows at a time and leaves its part of dw.  Bandwidth bounds many rows, the way
-// through a row's sum a few.  4096 x 4096 bf16: 30 us with rms_weight_kernel (the
-// two readings of rms_back_kernel: 39), fp32 49 (107), 1333 x 1490 fp16 10 (20).
+// through a row's sum a few.  4096 x 4096 bf16: 29 us with rms_weight_kernel (the
+// two readings of rms_back_kernel: 39), fp32 48 (107), 1333 x 1490 fp16 10 (20);
+// 37 instructions a value, issue slots 61 % busy.
 // Three CTAs an SM spill; a ring of four rows takes as long as one of three.
 __host__ __device__ constexpr int whole_cta_warps(int wpr) { return wpr > WARPS ? wpr : WARPS; }
 template <class R, bool VEC>
@@ -1171,15 +1184,11 @@ rms_back_rows_kernel(BackArgs a) {
         if (WPR > 1) {
             if (lane == 0) parts[at][warp] = make_float2(hi, lo);
             any = __syncthreads_or(wide);
-            const float2 *of = parts[at] + (warp - mine);
-            hi = of[0].x;
-            lo = of[0].y;
-            wide = !(fabsf(hi) <= 1e30f);
-#pragma unroll
-            for (int k = 1; k < WPR; ++k) {
-                wide |= !(fabsf(of[k].x) <= 1e30f);
-                add22(hi, lo, of[k].x, of[k].y);
-            }
+            const float2 p = parts[at][warp - mine + lane % WPR];
+            hi = p.x;
+            lo = p.y;
+            wide = __any_sync(0xFFFFFFFFu, !(fabsf(hi) <= 1e30f));
+            row_pair<WPR>(hi, lo);
         }
         float c = slope_of(hi, lo, a.mean, given);
         if (any) {
@@ -1524,8 +1533,8 @@ zs_status zs_rms_norm_backward(const void *dy, int64_t lddy, const void *x, int6
     BackArgs a;
     a.dy = dy; a.x = x; a.w = weight; a.residual = residual; a.rstd = rstd; a.dx = dx;
     // one reading where a row fits the registers, and the forms from dx, which then
-    // lies in L2: 4096 x 4096 bf16 in both 42 us, by tiles 51; fp32 63 and 104; 4000 x
-    // 4003 bf16 65 and 88; 300 x 1000 bf16 8 and 14; 16384 x 1024 bf16 53 and 51
+    // lies in L2: 4096 x 4096 bf16 in both 41 us, by tiles 51; fp32 62 and 104; 4000 x
+    // 4003 bf16 63 and 88; 300 x 1000 bf16 8 and 14; 16384 x 1024 bf16 52 and 51
     const bool whole = cols <= WHOLE_MOST;
     a.parts = whole ? 0 : back_parts(rows);     // 0: set with the launch
     a.dw_parts = dw ? scratch : nullptr;
