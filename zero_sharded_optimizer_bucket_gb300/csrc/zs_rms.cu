@@ -1032,7 +1032,8 @@ rms_back_kernel(BackArgs a, int64_t blocks, int col_blocks) {
 // rows at a time and leaves its part of dw.  Bandwidth bounds many rows, the way
 // through a row's sum a few.  4096 x 4096 bf16: 29 us with rms_weight_kernel (the
 // two readings of rms_back_kernel: 39), fp32 48 (107), 1333 x 1490 fp16 10 (20);
-// 37 instructions a value, issue slots 61 % busy.
+// 37 instructions a value and issue slots 61 % busy before the lanes shared the
+// joining of a row's sums.
 // Three CTAs an SM spill; a ring of four rows takes as long as one of three.
 __host__ __device__ constexpr int whole_cta_warps(int wpr) { return wpr > WARPS ? wpr : WARPS; }
 template <class R, bool VEC>
