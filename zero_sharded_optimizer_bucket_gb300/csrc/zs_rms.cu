@@ -70,10 +70,6 @@ struct RowF32 {
         for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(o[i]);
         return of(v);
     }
-    static __device__ __forceinline__ Elem element(const Raw &r, int i) {
-        const uint4 &q = i < 4 ? r.a : r.b;
-        return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
-    }
     // the largest magnitude of the four neighbouring lanes' values
     static __device__ __forceinline__ float top4(const Raw &r) {
         float v[8], top = 0.0f;
@@ -92,7 +88,6 @@ struct Row16 {
     typedef T Type;
     typedef uint4 Raw;
     static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
-    static __device__ __forceinline__ Raw of(const uint32_t v[8]) { return pack8(v); }
     static __device__ __forceinline__ void floats(const Raw &r, float o[8]) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -121,7 +116,6 @@ struct Row16 {
         }
         return make_uint4(r[0], r[1], r[2], r[3]);
     }
-    static __device__ __forceinline__ Elem element(const Raw &r, int i) { return (Elem)lane16(r, i); }
     static __device__ __forceinline__ float top4(const Raw &r) {
         uint32_t m = 0;
         max_two<T>(m, r.x);
