@@ -891,7 +891,7 @@ zs_status zs_rms_norm_scratch(int64_t rows, int64_t cols, int64_t *bytes);
  * with the mean made to 2^-40 of the mean of the magnitudes.  dx may be dy's or
  * residual's own memory with the same stride.  r_codes .. c_scales: dx held in
  * 4 bits, as the products of the layer below read it, as zs_mx4_quantize makes
- * of dx (and, up to 8192 columns, by it).  dw [cols] may be NULL.  scratch (16-byte aligned,
+ * of dx (and, up to 8192 columns, by it: with its bounded waits).  dw [cols] may be NULL.  scratch (16-byte aligned,
  * zs_rms_norm_scratch bytes) is overwritten: calls that overlap on the GPU need
  * one each.  No rows: dw is 0.  Errors: ZS_EINVAL, ZS_ECUDA. */
 zs_status zs_rms_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
