@@ -878,7 +878,9 @@ zs_status zs_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t 
                       float *rstd, void *r_codes, void *r_scales, void *c_codes, void *c_scales,
                       void *stream);
 
-/* Bytes of device memory that the backward pass needs as scratch. */
+/* Bytes of device memory that the backward pass needs as scratch.  They grow
+ * with rows and with cols: the scratch of the largest of several matrices, in
+ * both sizes, does for each of them. */
 zs_status zs_rms_norm_scratch(int64_t rows, int64_t cols, int64_t *bytes);
 
 /* Its backward pass.  x: what was normalised (sum, where there was a

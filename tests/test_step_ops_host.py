@@ -62,3 +62,13 @@ def test_matvec_refusals():
                 dict(dtype=3), dict(dtype=2, x=a + 2), dict(codes=None), dict(codes=a + 8), dict(scales=None), dict(scales=a + 1), dict(out=None),
                 dict(out=a + 2), dict(ldo=39), dict(out_dtype=-1)):
         call("zs_mx4_matvec", *dict(good, **bad).values())
+
+
+def test_scratch_of_a_larger_matrix_does_for_a_smaller_one():
+    rows = [1, 2, 7, 8, 9, 31, 33, 151, 152, 153, 303, 304, 305, 607, 608, 609, 2432, 8191, 8192, 8193, 1 << 20]
+    cols = [1, 511, 512, 513, 1024, 2047, 2048, 2049, 4095, 4096, 4097, 4608, 4609, 8191, 8192, 8193, 8705, 16384, 32768, 1 << 18]
+    need = [[zs.zs_rms_norm_scratch(r, c) for c in cols] for r in rows]
+    for i in range(len(rows)):
+        for j in range(len(cols)):
+            assert i == 0 or need[i - 1][j] <= need[i][j], (rows[i], cols[j])
+            assert j == 0 or need[i][j - 1] <= need[i][j], (rows[i], cols[j])

@@ -1358,6 +1358,20 @@ static int64_t whole_parts(int64_t rows, int64_t cols, int ctas) {
     return n < 152 * ctas ? n : 152 * ctas;
 }
 
+// Floats of parts that a matrix of these sizes or of smaller ones can leave, by
+// any type and alignment.  A wide matrix leaves fewer parts than a narrower one
+// that is read in one go, and may then need less: so the most that each of the
+// ways asks for up to this width, which grows with either size.
+static int64_t scratch_parts(int64_t rows, int64_t cols) {
+    int64_t most = 0;
+    for (const int64_t edge : {(int64_t)4096, WHOLE_MOST}) {       // up to here parts grow with the width
+        const int64_t c = cols < edge ? cols : edge, n = whole_parts(rows, c, 2) * parts_pitch(c);
+        if (n > most) most = n;
+    }
+    const int64_t n = back_parts(rows) * parts_pitch(cols);
+    return n > most ? n : most;
+}
+
 template <class R, int WPR, bool VEC>
 static cudaError_t whole_launch(BackArgs &a, cudaStream_t s) {
     static std::atomic<bool> set[64];
@@ -1497,9 +1511,7 @@ zs_status zs_rms_norm_scratch(int64_t rows, int64_t cols, int64_t *bytes) {
     if (!bytes) return zs_fail(ZS_EINVAL, "%s: NULL result", fn);
     if (rows < 0 || cols < 0 || rows >= MOST || cols >= MOST)
         return zs_fail(ZS_EINVAL, "%s: %lld x %lld out of range", fn, (long long)rows, (long long)cols);
-    int64_t parts = zsk::back_parts(rows);
-    if (cols <= zsk::WHOLE_MOST && zsk::whole_parts(rows, cols, 2) > parts) parts = zsk::whole_parts(rows, cols, 2);
-    *bytes = rows > 0 && cols > 0 ? 4 * (parts * zsk::parts_pitch(cols) + rows) : 0;
+    *bytes = rows > 0 && cols > 0 ? 4 * (zsk::scratch_parts(rows, cols) + rows) : 0;
     zs_clear_error();
     return ZS_OK;
 }
