@@ -1030,20 +1030,19 @@ rms_back_kernel(BackArgs a, int64_t blocks, int col_blocks) {
 // joining of a row's sums.
 // Three CTAs an SM spill; a ring of four rows takes as long as one of three.
 __host__ __device__ constexpr int whole_cta_warps(int wpr) { return wpr > WARPS ? wpr : WARPS; }
-template <class R, bool VEC>
-__host__ __device__ constexpr int whole_ctas(int wpr) { return wpr > WARPS ? 1 : VEC && R::SIZE == 2 ? 2 : 2; }      // an SM
+__host__ __device__ constexpr int whole_ctas(int wpr) { return wpr > WARPS ? 1 : 2; }             // an SM
 template <class R>
-__host__ __device__ constexpr int whole_depth(int wpr) { return R::SIZE == 4 ? 2 : 3; }           // rows of the ring
+__host__ __device__ constexpr int whole_depth() { return R::SIZE == 4 ? 2 : 3; }                  // rows of the ring
 template <class R>
 __host__ __device__ constexpr int whole_stage(int wpr) { return 3 * 2 * 8 * R::SIZE * 32 * whole_cta_warps(wpr); }
 // bytes of shared memory: the ring, and the warps' parts of dw in its place
 template <class R, bool VEC>
-constexpr int whole_smem(int wpr) { return VEC ? whole_depth<R>(wpr) * whole_stage<R>(wpr) : whole_cta_warps(wpr) * 2 * 256 * 4; }
+constexpr int whole_smem(int wpr) { return VEC ? whole_depth<R>() * whole_stage<R>(wpr) : whole_cta_warps(wpr) * 2 * 256 * 4; }
 
 template <class R, int WPR, bool VEC>
-__global__ void __launch_bounds__(32 * whole_cta_warps(WPR), whole_ctas<R, VEC>(WPR))
+__global__ void __launch_bounds__(32 * whole_cta_warps(WPR), whole_ctas(WPR))
 rms_back_rows_kernel(BackArgs a) {
-    constexpr int NB = 2, W = whole_cta_warps(WPR), ROWS = W / WPR, DEPTH = whole_depth<R>(WPR), STAGE = whole_stage<R>(WPR), PIECES = R::SIZE / 2;
+    constexpr int NB = 2, W = whole_cta_warps(WPR), ROWS = W / WPR, DEPTH = whole_depth<R>(), STAGE = whole_stage<R>(WPR), PIECES = R::SIZE / 2;
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ float2 parts[2][W];
     __shared__ double wides[W];
@@ -1256,6 +1255,9 @@ rms_back_rows_kernel(BackArgs a) {
 // dw from its parts: 32 columns a CTA, 32 warps' shares of the parts, then a
 // tree over the shares.
 constexpr int WEIGHT_WARPS = 32;
+constexpr int MOST_WHOLE_PARTS = 152, MOST_TILE_PARTS = 256;     // the former for each CTA of an SM, two at most
+constexpr int WEIGHT_LOADS = (2 * MOST_WHOLE_PARTS + WEIGHT_WARPS - 1) / WEIGHT_WARPS;
+static_assert(WEIGHT_LOADS * WEIGHT_WARPS >= MOST_TILE_PARTS, "parts of dw");
 __global__ void __launch_bounds__(32 * WEIGHT_WARPS)
 rms_weight_kernel(const float *parts, int n, int64_t cols, int64_t pitch, void *dw, int kind) {
     __shared__ float share[WEIGHT_WARPS][33];
@@ -1265,11 +1267,11 @@ rms_weight_kernel(const float *parts, int n, int64_t cols, int64_t pitch, void *
     pdl_trigger();
     float s = 0.0f;
     if (c0 + lane < cols) {
-        float v[10];                                 // all loads in flight; n is 304 at most
+        float v[WEIGHT_LOADS];                       // all in flight
 #pragma unroll
-        for (int j = 0; j < 10; ++j) v[j] = warp + j * WEIGHT_WARPS < n ? parts[(warp + j * WEIGHT_WARPS) * pitch + c0 + lane] : 0.0f;
+        for (int j = 0; j < WEIGHT_LOADS; ++j) v[j] = warp + j * WEIGHT_WARPS < n ? parts[(warp + j * WEIGHT_WARPS) * pitch + c0 + lane] : 0.0f;
 #pragma unroll
-        for (int j = 0; j < 10; ++j) s = __fadd_rn(s, v[j]);
+        for (int j = 0; j < WEIGHT_LOADS; ++j) s = __fadd_rn(s, v[j]);
     }
     share[warp][lane] = s;
     __syncthreads();
@@ -1344,18 +1346,19 @@ static cudaError_t norm_tiles(const NormArgs &a, cudaStream_t s) {
 
 // Parts of dw, by tiles and by whole rows: numbers of the sizes alone, so that a
 // sum has the same bits every time, whatever forms are asked for.  256 of the
-// former keep scratch small and the GPU busy; the latter are two CTAs an SM.
+// former keep scratch small and the GPU busy; the latter are a CTA each, one or two an SM.
 static int64_t back_parts(int64_t rows) {
     const int64_t blocks = (rows + TILE_ROWS - 1) / TILE_ROWS;
-    return blocks < 256 ? blocks : 256;
+    return blocks < MOST_TILE_PARTS ? blocks : MOST_TILE_PARTS;
 }
 
 // One reading of a row: as many warps as give each lane 16 columns.
 constexpr int64_t WHOLE_MOST = 8192;                 // columns
 static int whole_warps(int64_t cols) { return cols <= 512 ? 1 : cols <= 2048 ? 4 : cols <= 4096 ? 8 : 16; }
-static int64_t whole_parts(int64_t rows, int64_t cols, int ctas) {
+static int64_t whole_parts(int64_t rows, int64_t cols) {
     const int64_t per = cols <= 2048 ? WARPS / whole_warps(cols) : 1, n = (rows + per - 1) / per;
-    return n < 152 * ctas ? n : 152 * ctas;
+    const int64_t most = MOST_WHOLE_PARTS * whole_ctas(whole_warps(cols));
+    return n < most ? n : most;
 }
 
 // Floats of parts that a matrix of these sizes or of smaller ones can leave, by
@@ -1365,7 +1368,7 @@ static int64_t whole_parts(int64_t rows, int64_t cols, int ctas) {
 static int64_t scratch_parts(int64_t rows, int64_t cols) {
     int64_t most = 0;
     for (const int64_t edge : {(int64_t)4096, WHOLE_MOST}) {       // up to here parts grow with the width
-        const int64_t c = cols < edge ? cols : edge, n = whole_parts(rows, c, 2) * parts_pitch(c);
+        const int64_t c = cols < edge ? cols : edge, n = whole_parts(rows, c) * parts_pitch(c);
         if (n > most) most = n;
     }
     const int64_t n = back_parts(rows) * parts_pitch(cols);
@@ -1375,7 +1378,7 @@ static int64_t scratch_parts(int64_t rows, int64_t cols) {
 template <class R, int WPR, bool VEC>
 static cudaError_t whole_launch(BackArgs &a, cudaStream_t s) {
     static std::atomic<bool> set[64];
-    a.parts = whole_parts(a.held.rows, a.held.cols, whole_ctas<R, VEC>(WPR));
+    a.parts = whole_parts(a.held.rows, a.held.cols);
     return tile_launch(rms_back_rows_kernel<R, WPR, VEC>, set, whole_smem<R, VEC>(WPR), a.parts, 32 * whole_cta_warps(WPR), s, a);
 }
 template <class R, bool VEC>
