@@ -1,0 +1,81 @@
+"""The sums over a row behind zs_rms_norm and zs_rms_norm_backward, where one
+value leads a row, and the kernels of rows of more than 8192 columns.
+
+Tolerances, with U = 2^-24 and from include/zs.h:
+  rstd    the nearest float32 to the formula's value, in rows that lie more than
+          2^-38 of it from the middle of two (the reference's own error: 2^-50)
+  slope   of a column whose dy is 0, x 1 and rstd 1, dx is -c: 2^-36 of the mean
+          of the magnitudes, and half a step of c
+"""
+import numpy as np
+import pytest
+import torch
+
+import zero_sharded_optimizer_bucket_gb300 as zs
+from tests.test_gpu_rms_norm import HALF, U, back, call
+from tests.test_gpu_tensors import KINDS
+
+pytestmark = pytest.mark.gpu
+
+
+def led_rows(cols, rows, near, far, seed):
+    """Rows [rows, cols] of float32 whose first value leads and whose rstd (eps 0) lies between near and far, relative, from
+    the middle of two floats; and the nearest floats."""
+    rng = np.random.default_rng(seed)
+    found, want = [], []
+    places = [c for c in range(1, cols) if c % 256 < 8]
+    while len(found) < rows:
+        tail = np.float32(2.0 ** -rng.uniform(8.5, 9.5))
+        first = (1 + rng.random(1 << 18)).astype(np.float32)
+        s = first.astype(np.float64) ** 2 + len(places) * float(tail) ** 2
+        r = 1 / np.sqrt(s / cols)
+        f = r.astype(np.float32)
+        # the middle on r's side of f
+        other = np.nextafter(f, np.where(r > f, np.float32(np.inf), np.float32(0)))
+        off = np.abs((f.astype(np.float64) + other.astype(np.float64)) / 2 - r) / r
+        for i in np.nonzero((off >= near) & (off <= far))[0]:
+            row = np.zeros(cols, np.float32)
+            row[places], row[0] = tail, first[i]
+            found.append(row)
+            want.append(f[i])
+    return torch.from_numpy(np.stack(found[:rows])).cuda(), torch.tensor(np.array(want[:rows])).cuda()
+
+
+@pytest.mark.parametrize("cols", [250, 512, 1024, 2048, 4096, 4099, 8192, 8191, 12288, 16384, 16377, 20000, 70000])
+@pytest.mark.parametrize("held", [(), ("cols",)])
+def test_a_value_that_leads_its_row(cols, held):
+    x, want = led_rows(cols, 64, 2.0 ** -38, 2.0 ** -35, cols)
+    w = torch.ones(cols, device="cuda")
+    got = call(x, w, 0.0, held=held, kind="fp32")
+    assert torch.equal(got["rstd"], want), int((got["rstd"] != want).sum())
+
+
+@pytest.mark.parametrize("cols", [300, 512, 2048, 1490, 4096, 8192, 8191, 8200, 12288, 12289, 20000])
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("lead", [8, 14])
+def test_leading_values_in_different_columns(cols, kind, lead):
+    """Rows whose sum of g x is 0, of columns that come twice, once negated, and of a g and an x that lead, not together."""
+    rows = 40
+    g = torch.Generator(device="cuda").manual_seed(cols + lead)
+    half = (cols - 1) // 2
+    x, dy = (torch.randn(rows, half, device="cuda", generator=g).to(KINDS[kind]) for _ in range(2))
+    for at in range(0, half - 1, 70):
+        x[:, at], dy[:, at] = 2.0 ** lead * (1 + at % 3), x[:, at] * 2.0 ** -lead
+        dy[:, at + 1], x[:, at + 1] = 2.0 ** lead, dy[:, at + 1] * 2.0 ** -lead
+    turn = torch.randperm(half, device="cuda", generator=g)
+    probe = torch.zeros(rows, cols - 2 * half, dtype=KINDS[kind], device="cuda")
+    x, dy = torch.cat([x, x[:, turn], probe + 1], 1), torch.cat([dy, -dy[:, turn], probe], 1)
+    got = back(dy.contiguous(), x.contiguous(), torch.ones(cols, device="cuda"), torch.ones(rows, device="cuda"), None, kind, dw=False)
+    c = -got["dx"].t[:, -1].double()
+    size = (dy.double() * x.double()).abs().mean(1)
+    assert bool((c.abs() <= 2.0 ** -36 * size * (1 + HALF[kind])).all()), float((c.abs() / size).max())
+
+
+@pytest.mark.parametrize("cols", [512, 4096, 8192, 12288, 12289])
+def test_slope_of_ordinary_rows(cols):
+    dy, x = (torch.randn(33, cols, device="cuda", generator=torch.Generator(device="cuda").manual_seed(cols + i)) for i in range(2))
+    dy[:, -1], x[:, -1] = 0, 1
+    got = back(dy, x, torch.ones(cols, device="cuda"), torch.ones(33, device="cuda"), None, "fp32", dw=False)
+    p = dy.double() * x.double()
+    want = p.mean(1)
+    assert bool(((got["dx"].t[:, -1].double() + want).abs() <= U * want.abs() + 2.0 ** -36 * p.abs().mean(1)).all())

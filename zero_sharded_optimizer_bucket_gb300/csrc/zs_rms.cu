@@ -10,8 +10,9 @@
 //   dw = sum over rows of dy (x rstd)
 // Results go straight to 4 bits, whose borders lie densely: a unit in the last
 // place of rstd moves values across them.  So the sums over a row are made as
-// float32 pairs, good to about 2^-44, and rstd is the float32 nearest to the
-// formula's value but where that lies within 2^-40 of the middle of two.
+// float32 pairs, good to 2^-37 of the magnitudes' sum at worst, and rstd is the
+// float32 nearest to the formula's value but where that lies within 2^-38 of the
+// middle of two.
 //
 // A result held along its columns needs 32 rows at a time, which no SM holds
 // whole.  One kernel makes the rows' sums, another takes tiles of 32 rows by 512
@@ -208,22 +209,32 @@ __device__ __forceinline__ int part(int64_t cols, int64_t at) { return (int)max(
 
 // ------------------------------------------------------- sums of a row --
 
+// Blocks of 8 pairs that a lane adds to one accumulator: 4096 x 4096 bf16 whole
+// 25.1 us, backward 28.8; with one block 25.8 and 29.5.
+constexpr int RUN = 2;
+
 // A sum of products a b as hi + lo.  The accumulator begins at 3 * 2^m, 2^m
-// above the sum of the magnitudes, and so stays in [2^(m+1), 2^(m+2)): then
+// above the sum of the magnitudes, and so stays in [2^(m+1), 2^(m+2)); of
+// squares at 2^m, and stays in [2^m, 2^(m+1)).  Then
 //   s = a b + h;  d = h - s (exact);  e = a b + d (the rounding error of s)
-// four paired instructions for two products.  m: from the largest magnitudes,
-// at least -100 (products below 2^-126 are lost then).
+// four paired instructions for two products.  2^m is at most 16 times the
+// largest product (two blocks; from the factors' largest magnitudes, which may
+// belong to different columns, it could be anything above), and at least 2^-100.
+// Of two blocks: each e is at most 2^(m-23), rounded once itself, and 8 of them
+// are added in float32: off by 25 2^(m-47) a half, 16 2^(m-47) more where the
+// halves meet, together 2^-36.9 of the largest product; squares half of that.
+template <bool SQUARES>
 struct Dot {
     f2 h, l;
     float start;
-    // of at most 8 N pairs with |a| <= top_a, |b| <= top_b; false: too large
+    // of at most 8 N pairs with |a b| <= top, rounded; false: too large
     template <int N>
-    __device__ __forceinline__ bool begin(float top_a, float top_b) {
-        const int ea = (int)(__float_as_uint(top_a) >> 23) - 127, eb = (int)(__float_as_uint(top_b) >> 23) - 127;
+    __device__ __forceinline__ bool begin(float top) {
+        const int e = (int)(__float_as_uint(top) >> 23) - 127;
         constexpr int LOG = N <= 1 ? 2 : N <= 2 ? 3 : N <= 4 ? 4 : 5;      // of the products of one half
-        const int m = max(ea + eb + 2 + LOG, -100);
-        const bool ok = max(ea, eb) < 60;            // infinities and NaN have 128
-        start = __uint_as_float(ok ? (uint32_t)(m + 1 + 127) << 23 | 0x400000u : 0x7F800000u);
+        const int m = max(e + 1 + LOG, -100);
+        const bool ok = e < 115;                     // infinities and NaN have 128
+        start = __uint_as_float(!ok ? 0x7F800000u : SQUARES ? (uint32_t)(m + 127) << 23 : (uint32_t)(m + 1 + 127) << 23 | 0x400000u);
         h = f2pack(start, start);
         l = 0;
         return ok;
@@ -447,24 +458,27 @@ rms_rows_kernel(NormArgs a) {
     float h[KEEP][8];
     float hi = 0.0f, lo = 0.0f;
     auto square = [&](auto &v) {                     // of one or all blocks
-        constexpr int N = sizeof(v) / 32;
-        float top = 0.0f;
+        constexpr int ALL = sizeof(v) / 32, N = ALL < RUN ? ALL : RUN;
 #pragma unroll
-        for (int b = 0; b < N; ++b)
+        for (int b0 = 0; b0 < ALL; b0 += N) {
+            float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) max_abs3(top, v[b][i], v[b][i + 1]);
-        Dot d;
-        const bool ok = d.begin<N>(top, top);
+            for (int b = b0; b < b0 + N; ++b)
 #pragma unroll
-        for (int b = 0; b < N; ++b)
+                for (int i = 0; i < 8; i += 2) max_abs3(top, v[b][i], v[b][i + 1]);
+            Dot<true> d;
+            const bool ok = d.template begin<N>(__fmul_rn(top, top));
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const f2 p = f2pack(v[b][i], v[b][i + 1]);
-                d.add(p, p);
-            }
-        float dh, dl;
-        d.end(dh, dl);
-        add22(hi, lo, ok ? dh : __uint_as_float(0x7F800000u), dl);
+            for (int b = b0; b < b0 + N; ++b)
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const f2 p = f2pack(v[b][i], v[b][i + 1]);
+                    d.add(p, p);
+                }
+            float dh, dl;
+            d.end(dh, dl);
+            add22(hi, lo, ok ? dh : __uint_as_float(0x7F800000u), dl);
+        }
     };
     if constexpr (NB > 0) {
         Load<R, VEC> first[KEEP], second[KEEP];
@@ -605,32 +619,31 @@ rms_sums_kernel(SumArgs a) {
             ro[b] = next_o[b].take(turn);
         }
         if (c0 + 256 * WPR * BLOCKS < a.cols) fetch(c0 + 256 * WPR * BLOCKS);
-        f2 u[BLOCKS][4], v[BLOCKS][4];
-        float tu = 0.0f, tv = 0.0f;
 #pragma unroll
-        for (int b = 0; b < BLOCKS; ++b) {
-            const int64_t c = c0 + 256 * WPR * b;
-            inputs(rx[b], ro[b], c, there ? part(a.cols, c) : 0, u[b], v[b]);
+        for (int b0 = 0; b0 < BLOCKS; b0 += RUN) {
+            f2 u[RUN][4], v[RUN][4];
+            float top = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float p, q;
-                f2unpack(v[b][j], p, q);
-                max_abs3(tv, p, q);
-                if (BACK) {
-                    f2unpack(u[b][j], p, q);
-                    max_abs3(tu, p, q);
+            for (int b = 0; b < RUN; ++b) {
+                const int64_t c = c0 + 256 * WPR * (b0 + b);
+                inputs(rx[b0 + b], ro[b0 + b], c, there ? part(a.cols, c) : 0, u[b], v[b]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float p, q;
+                    f2unpack(BACK ? mul2(u[b][j], v[b][j]) : v[b][j], p, q);
+                    max_abs3(top, p, q);
                 }
             }
+            Dot<!BACK> d;
+            const bool ok = d.template begin<RUN>(BACK ? top : __fmul_rn(top, top));
+#pragma unroll
+            for (int b = 0; b < RUN; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d.add(u[b][j], v[b][j]);
+            float dh, dl;
+            d.end(dh, dl);
+            add22(hi, lo, ok ? dh : __uint_as_float(0x7F800000u), dl);
         }
-        Dot d;
-        const bool ok = d.begin<BLOCKS>(BACK ? tu : tv, tv);
-#pragma unroll
-        for (int b = 0; b < BLOCKS; ++b)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d.add(u[b][j], v[b][j]);
-        float dh, dl;
-        d.end(dh, dl);
-        add22(hi, lo, ok ? dh : __uint_as_float(0x7F800000u), dl);
     }
     warp_pair(hi, lo);
     if (WPR > 1) {
@@ -1148,29 +1161,36 @@ rms_back_rows_kernel(BackArgs a) {
             }
         };
         f2 g[NB][4], z[NB][4];
-        float tu = 0.0f, tv = 0.0f, hi, lo;
+        float hi = 0.0f, lo = 0.0f;
+        bool ok = true;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            inputs(b, g[b], z[b]);
+        for (int b0 = 0; b0 < NB; b0 += RUN) {
+            float top = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float p, q;
-                f2unpack(mul2(g[b][j], w[b][j]), p, q);
-                max_abs3(tu, p, q);
-                f2unpack(z[b][j], p, q);
-                max_abs3(tv, p, q);
+            for (int b = b0; b < b0 + RUN; ++b) {
+                inputs(b, g[b], z[b]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float p, q;
+                    f2unpack(mul2(mul2(g[b][j], w[b][j]), z[b][j]), p, q);
+                    max_abs3(top, p, q);
+                }
             }
-        }
-        {
-            Dot d;
-            const bool ok = d.begin<NB>(tu, tv);
+            Dot<false> d;
+            ok &= d.template begin<RUN>(top);
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+            for (int b = b0; b < b0 + RUN; ++b)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d.add(mul2(g[b][j], w[b][j]), z[b][j]);
-            d.end(hi, lo);
-            if (!ok) hi = __uint_as_float(0x7F800000u);
+            if (b0 == 0) {
+                d.end(hi, lo);
+            } else {
+                float dh, dl;
+                d.end(dh, dl);
+                add22(hi, lo, dh, dl);
+            }
         }
+        if (!ok) hi = __uint_as_float(0x7F800000u);
         warp_pair(hi, lo);
         // too large for float32's products (or not finite): the row in 64 bits
         bool wide = !(fabsf(hi) <= 1e30f);           // sixteen such sums are finite
