@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import zero_sharded_optimizer_bucket_gb300 as zs
-from tests.test_gpu_rms_norm import HALF, U, back, call
+from tests.test_gpu_rms_norm import HALF, U, back, back_data, call, check_backward
 from tests.test_gpu_tensors import KINDS
 
 pytestmark = pytest.mark.gpu
@@ -79,3 +79,14 @@ def test_slope_of_ordinary_rows(cols):
     p = dy.double() * x.double()
     want = p.mean(1)
     assert bool(((got["dx"].t[:, -1].double() + want).abs() <= U * want.abs() + 2.0 ** -36 * p.abs().mean(1)).all())
+
+
+@pytest.mark.parametrize("cols", [500, 4096, 8191, 8192, 9000, 12291])
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("e", [-60, -63, -66, -90])
+def test_slope_of_a_small_input(cols, kind, e):
+    """rstd past 2^64, whose square float32 does not have."""
+    dy, x, w, _, res = back_data(20, cols, kind, "fp32")
+    x = (x.float() * 2.0 ** e).to(KINDS[kind])
+    rstd = x.double().square().mean(1).rsqrt().float()
+    check_backward(dy, x, w, rstd, res, back(dy, x, w, rstd, res, kind), kind, "fp32")

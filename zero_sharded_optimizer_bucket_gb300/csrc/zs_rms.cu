@@ -230,8 +230,9 @@ struct Dot {
     // of at most 8 N pairs with |a b| <= top, rounded; false: too large
     template <int N>
     __device__ __forceinline__ bool begin(float top) {
+        static_assert(N <= RUN, "blocks");
         const int e = (int)(__float_as_uint(top) >> 23) - 127;
-        constexpr int LOG = N <= 1 ? 2 : N <= 2 ? 3 : N <= 4 ? 4 : 5;      // of the products of one half
+        constexpr int LOG = N == 1 ? 2 : 3;          // of the products of one half
         const int m = max(e + 1 + LOG, -100);
         const bool ok = e < 115;                     // infinities and NaN have 128
         start = __uint_as_float(!ok ? 0x7F800000u : SQUARES ? (uint32_t)(m + 127) << 23 : (uint32_t)(m + 1 + 127) << 23 | 0x400000u);
@@ -336,11 +337,12 @@ __device__ __forceinline__ float rstd_of(float hi, float lo, const Mean &mean, f
 __device__ __forceinline__ float rstd_of(double total, double cols, float eps) {
     return (float)__drcp_rn(__dsqrt_rn(__dadd_rn(__ddiv_rn(total, cols), (double)eps)));
 }
-// rstd^2 mean(g x)
+// rstd^2 mean(g x), by one rstd after the other: the square alone leaves float32
+// where x is below 2^-63
 __device__ __forceinline__ float slope_of(float hi, float lo, const Mean &mean, float rstd) {
     times(hi, lo, mean.hi, mean.lo);
-    const float a = __fmul_rn(rstd, rstd), ae = __fmaf_rn(rstd, rstd, -a);
-    times(hi, lo, a, ae);
+    times(hi, lo, rstd, 0.0f);
+    times(hi, lo, rstd, 0.0f);
     return hi;
 }
 
