@@ -866,9 +866,9 @@ zs_status zs_mx4_matvec(int64_t m, int64_t n, int64_t k, const void *x, int64_t 
  * r_codes, r_scales and c_codes, c_scales: y held in 4 bits along its rows and
  * its columns, bit for bit what zs_mx4_quantize makes of y (either pair may be
  * NULL; of the three results one at least is asked for).  rstd [rows] is what
- * the backward pass reads.  The sum of squares is made to 2^-37 + cols 2^-54 of
- * itself (squares below 2^-126 are lost), and rstd is the fp32 number nearest to
- * its formula's value unless that lies within half as much of the middle of two.
+ * the backward pass reads.  mean + eps is made to 2^-37 + cols 2^-54 of itself,
+ * and rstd is the fp32 number nearest to its formula's value unless that lies
+ * within half as much of the middle of two.
  * A row with an infinity or NaN gives what the formula gives.  eps >= 0: of a row
  * of zeros with eps 0 the result is NaN.  No rows or no columns: nothing is
  * written.  Errors: ZS_EINVAL, ZS_ECUDA. */
@@ -890,7 +890,8 @@ zs_status zs_rms_norm_scratch(int64_t rows, int64_t cols, int64_t *bytes);
  *   dx = rne((g - x c) * rstd + residual)   (of x and of the residual alike)
  *   dw = sum over the rows of dy * (x * rstd), added in fp32 in an order that
  *        the sizes and the alignment set, rounded once to dw_dtype
- * with the mean made to 2^-36 + cols 2^-54 of the mean of the magnitudes |g x|.
+ * with the mean made to 2^-36 + cols 2^-54 of the mean of the magnitudes |g x|
+ * (and to 2^-148, which counts where all of them are below 2^-110).
  * dx may be dy's or residual's own memory with the same stride.  r_codes ..
  * c_scales: dx held in 4 bits, as the products of the layer below read it, as
  * zs_mx4_quantize makes of dx (and, up to 8192 columns, by it: with its bounded

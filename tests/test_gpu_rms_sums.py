@@ -4,6 +4,7 @@ value leads a row, and the kernels of rows of more than 8192 columns.
 Tolerances, with U = 2^-24 and from include/zs.h:
   rstd    the nearest float32 to the formula's value, in rows that lie more than
           2^-38 of it from the middle of two (the reference's own error: 2^-50)
+  small   rstd of rows whose squares float32 does not have: as the other rows (check_forward)
   slope   of a column whose dy is 0, x 1 and rstd 1, dx is -c: 2^-36 of the mean
           of the magnitudes, and half a step of c
 """
@@ -12,7 +13,7 @@ import pytest
 import torch
 
 import zero_sharded_optimizer_bucket_gb300 as zs
-from tests.test_gpu_rms_norm import HALF, U, back, back_data, call, check_backward
+from tests.test_gpu_rms_norm import HALF, U, back, back_data, call, check_backward, check_forward, data
 from tests.test_gpu_tensors import KINDS
 
 pytestmark = pytest.mark.gpu
@@ -90,3 +91,21 @@ def test_slope_of_a_small_input(cols, kind, e):
     x = (x.float() * 2.0 ** e).to(KINDS[kind])
     rstd = x.double().square().mean(1).rsqrt().float()
     check_backward(dy, x, w, rstd, res, back(dy, x, w, rstd, res, kind), kind, "fp32")
+
+
+@pytest.mark.parametrize("cols", [250, 2048, 4099, 8192, 16384, 20000])
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("held", [(), ("cols",)])
+def test_rows_of_small_values(cols, kind, held):
+    """Without eps, or with a tiny one: squares down to far below float32's least number."""
+    x, g = data(40, cols, kind)
+    for i, e in enumerate([0, -40, -48, -52, -55, -58, -62, -63, -64, -66, -70, -74, -80, -100, -115]):
+        x[2 * i] = (x[2 * i].float() * 2.0 ** e).to(KINDS[kind])
+    x[33] = 0
+    x[33, cols // 2] = 2.0 ** -70
+    x[35] = 2.0 ** -126
+    for eps in (0.0, 2.0 ** -149, 2.0 ** -130, 2.0 ** -110, 1e-30):
+        got = call(x, torch.ones(cols, device="cuda"), eps, held=held, kind=kind)
+        check_forward(x, None, torch.ones(cols, device="cuda"), eps, got)
+    got = call(x, torch.ones(cols, device="cuda"), 3e38, held=held, kind=kind)
+    check_forward(x, None, torch.ones(cols, device="cuda"), 3e38, got)

@@ -35,7 +35,7 @@ namespace zsk {
 
 typedef unsigned long long f2;
 
-__device__ __forceinline__ bool finite_f32(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+constexpr float MOST_F32 = 3.402823466e38f;
 
 // ------------------------------------------------------ 8 values a lane --
 
@@ -323,7 +323,7 @@ __device__ __forceinline__ float rstd_of(float hi, float lo, const Mean &mean, f
     times(hi, lo, mean.hi, mean.lo);
     add22(hi, lo, eps, 0.0f);
     const int e = ((int)(__float_as_uint(hi) >> 23) - 127) >> 1;           // floor
-    if (!(hi >= 1.1754944e-38f) || hi > 3e38f) return __fdiv_rn(1.0f, __fsqrt_rn(hi));
+    if (!(hi >= 1.1754944e-38f) || hi > 3e38f) return (float)__drcp_rn(__dsqrt_rn((double)hi));
     const float s = __uint_as_float((uint32_t)(127 - e) << 23);
     hi = __fmul_rn(__fmul_rn(hi, s), s);
     lo = __fmul_rn(__fmul_rn(lo, s), s);
@@ -416,7 +416,7 @@ struct NormArgs {
     int64_t ldx, ldr, lds, ldo;
     int32_t w_kind;
     bool vec, vec_w;                 // every matrix has 16-byte aligned rows; so does the weight
-    float eps;
+    float eps, least;                // least: of least_sum
     Mean mean;
     NormHeld held;
 };
@@ -509,8 +509,9 @@ rms_rows_kernel(NormArgs a) {
         for (int k = 1; k < WPR; ++k) add22(hi, lo, parts[first + k].x, parts[first + k].y);
     }
     float rstd = rstd_of(hi, lo, a.mean, a.eps);
-    // too large for float32's squares (or not finite): in 64 bits
-    if (__syncthreads_or(!finite_f32(hi))) {
+    // too large or too small for float32's squares (or not finite): in 64 bits
+    const bool wide = !(hi >= a.least && hi <= MOST_F32);
+    if (__syncthreads_or(wide)) {
         double s = 0.0;
         for (int b = 0; b < blocks; ++b) {
             float v[8];
@@ -523,7 +524,7 @@ rms_rows_kernel(NormArgs a) {
         __syncthreads();
         s = 0.0;
         for (int k = 0; k < WPR; ++k) s = __dadd_rn(s, wides[warp - mine + k]);
-        if (!finite_f32(hi)) rstd = rstd_of(s, (double)cols, a.eps);
+        if (wide) rstd = rstd_of(s, (double)cols, a.eps);
     }
     if (there && mine == 0 && lane == 0) a.rstd[row] = rstd;
 #pragma unroll
@@ -560,7 +561,7 @@ struct SumArgs {
     int64_t ldx, ldo, rows, cols;
     int32_t w_kind;
     bool vec_w;
-    float eps;
+    float eps, least;
     Mean mean;
     const float *rstd;               // of the backward pass
     float *result;                   // [rows]
@@ -659,8 +660,9 @@ rms_sums_kernel(SumArgs a) {
     }
     const float given = BACK && there ? a.rstd[row] : 0.0f;
     float result = BACK ? slope_of(hi, lo, a.mean, given) : rstd_of(hi, lo, a.mean, a.eps);
-    // too large for float32's products (or not finite): in 64 bits
-    if (__syncthreads_or(!finite_f32(hi))) {
+    // too large for float32's products, squares too small (or not finite): in 64 bits
+    const bool wide = !((BACK ? fabsf(hi) : hi) >= a.least && (BACK ? fabsf(hi) : hi) <= MOST_F32);
+    if (__syncthreads_or(wide)) {
         double s = 0.0;
 #pragma unroll 1
         for (int64_t c = 256 * mine; c < a.cols; c += 256 * WPR) {
@@ -681,7 +683,7 @@ rms_sums_kernel(SumArgs a) {
         __syncthreads();
         s = 0.0;
         for (int k = 0; k < WPR; ++k) s = __dadd_rn(s, wides[warp - mine + k]);
-        if (!finite_f32(hi)) {
+        if (wide) {
             if (BACK) result = (float)__dmul_rn(__ddiv_rn(s, (double)a.cols), __dmul_rn((double)given, (double)given));
             else result = rstd_of(s, (double)a.cols, a.eps);
         }
@@ -1308,6 +1310,10 @@ rms_weight_kernel(const float *parts, int n, int64_t cols, int64_t pitch, void *
 
 // ------------------------------------------------------------- launches --
 
+// The sum of squares below which a row is summed in 64 bits: the errors that
+// float32's least number leaves (2^-149 a square) would count, unless eps hides them.
+static float least_sum(int64_t cols, float eps) { return eps < 0x1p-100f ? (float)cols * 0x1p-100f : 0.0f; }
+
 template <class R, int WPR, int NB>
 static cudaError_t rows_launch(const NormArgs &a, int64_t grid_rows, cudaStream_t s) {
     const int64_t per = WARPS / WPR, grid = (grid_rows + per - 1) / per;
@@ -1361,7 +1367,7 @@ static cudaError_t norm_tiles(const NormArgs &a, cudaStream_t s) {
     static std::atomic<bool> set[64];
     const int64_t rows = a.held.rows, cols = a.held.cols;
     const int cb = col_blocks_of(cols);
-    const SumArgs sums = {a.x, a.residual, nullptr, a.ldx, a.ldr, rows, cols, 0, true, a.eps, a.mean, nullptr, a.rstd};
+    const SumArgs sums = {a.x, a.residual, nullptr, a.ldx, a.ldr, rows, cols, 0, true, a.eps, a.least, a.mean, nullptr, a.rstd};
     const cudaError_t e = sums_launch<R, false, VEC>(sums, s);
     return e != cudaSuccess ? e : tile_launch(rms_tile_kernel<R, VEC>, set, tile_smem<R>(false), 4 * mx4_atoms(rows) * cb, THREADS, s, a, cb);
 }
@@ -1419,7 +1425,7 @@ static cudaError_t back_tiles(const BackArgs &a, cudaStream_t s) {
     const int64_t rows = a.held.rows, cols = a.held.cols;
     const int64_t blocks = a.held.c_codes ? 4 * mx4_atoms(rows) : a.held.r_codes ? 4 * mx4_row_tiles(rows) : (rows + TILE_ROWS - 1) / TILE_ROWS;
     const int cb = col_blocks_of(cols);
-    const SumArgs sums = {a.x, a.dy, a.w, a.ldx, a.lddy, rows, cols, a.w_kind, a.vec_w, 0.0f, a.mean, a.rstd, a.slopes};
+    const SumArgs sums = {a.x, a.dy, a.w, a.ldx, a.lddy, rows, cols, a.w_kind, a.vec_w, 0.0f, 0.0f, a.mean, a.rstd, a.slopes};
     const cudaError_t e = sums_launch<R, true, VEC>(sums, s);
     return e != cudaSuccess ? e : tile_launch(rms_back_kernel<R, VEC>, set, tile_smem<R>(true), a.parts * cb, THREADS, s, a, blocks, cb);
 }
@@ -1518,7 +1524,7 @@ zs_status zs_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t 
     NormArgs a;
     a.x = x; a.residual = residual; a.w = weight; a.sum = sum; a.out = out; a.rstd = rstd;
     a.ldx = ldx; a.ldr = ldr; a.lds = lds; a.ldo = ldo;
-    a.w_kind = weight_dtype; a.vec = vec; a.vec_w = vec_w; a.eps = eps; a.mean = mean_of(cols);
+    a.w_kind = weight_dtype; a.vec = vec; a.vec_w = vec_w; a.eps = eps; a.least = least_sum(cols, eps); a.mean = mean_of(cols);
     a.held = {static_cast<uint8_t *>(r_codes), static_cast<uint8_t *>(r_scales), static_cast<uint8_t *>(c_codes), static_cast<uint8_t *>(c_scales), rows, cols};
     const cudaStream_t s = (cudaStream_t)stream;
     if (!c_codes) {
