@@ -481,6 +481,20 @@ typedef struct {
 } zs_mx4_launch;
 zs_status zs_test_mx4_launch(int64_t m, int64_t n, int64_t k, zs_mx4_launch *out);
 
+/* How zs_mx4_matvec shares out a product of these sizes on the current device
+ * (for tests; it asks the device and launches nothing).  Errors: ZS_EINVAL,
+ * ZS_ECUDA. */
+typedef struct {
+    int32_t tokens;                /* of a CTA, at most                        */
+    int32_t warps_n, warps_k;      /* of a CTA, along the rows and along k     */
+    int32_t split;                 /* CTAs of a cluster, which share k         */
+    int32_t units;                 /* of 128 of k, of each CTA                 */
+    int32_t stage;                 /* of them, whose tokens are there at once  */
+    int32_t depth;                 /* units of a warp's ring                   */
+    int32_t shared_bytes;          /* dynamic shared memory                    */
+} zs_mx4_matvec_launch;
+zs_status zs_test_mx4_matvec_launch(int64_t m, int64_t n, int64_t k, int32_t dtype, zs_mx4_matvec_launch *out);
+
 /* A2 over the consecutive buckets [first_bucket, first_bucket + n_buckets)
  * in one launch, for buckets that become ready back to back ([ZeRO-3
  * chapter] §6.2: a full IPG bucket is reduced and scattered; when several

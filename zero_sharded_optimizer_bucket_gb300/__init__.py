@@ -142,6 +142,10 @@ class zs_mx4_launch(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("cluster", "split", "stages", "shared_bytes", "tmem_columns", "reserved")]
 
 
+class zs_mx4_matvec_launch(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("tokens", "warps_n", "warps_k", "split", "units", "stage", "depth", "shared_bytes")]
+
+
 _P = C.c_void_p
 _i32, _i64, _f32 = C.c_int32, C.c_int64, C.c_float
 
@@ -219,6 +223,7 @@ _sig("zs_test_late_copy", _i32, [_P, _P, _i64, _i64, _P])
 _sig("zs_test_root", _i32, [_P, _P])
 _sig("zs_test_give_up", _i32, [_i32])
 _sig("zs_test_mx4_launch", _i32, [_i64, _i64, _i64, C.POINTER(zs_mx4_launch)])
+_sig("zs_test_mx4_matvec_launch", _i32, [_i64, _i64, _i64, _i32, C.POINTER(zs_mx4_matvec_launch)])
 _sig("zs_mx4_matmul", _i32, [_i64, _i64, _i64, _P, _P, _P, _P, _P, _i64, _i32, _P])
 
 
@@ -1041,4 +1046,11 @@ def zs_test_mx4_launch(m: int, n: int, k: int) -> dict:
     """What a CTA of zs_mx4_matmul's launch asks of its SM (for tests)."""
     o = zs_mx4_launch()
     _check(_lib.zs_test_mx4_launch(int(m), int(n), int(k), C.byref(o)), "zs_test_mx4_launch")
+    return _to_dict(o)
+
+
+def zs_test_mx4_matvec_launch(m: int, n: int, k: int, dtype: int) -> dict:
+    """How zs_mx4_matvec shares out a product of these sizes on the current device (for tests)."""
+    o = zs_mx4_matvec_launch()
+    _check(_lib.zs_test_mx4_matvec_launch(int(m), int(n), int(k), int(dtype), C.byref(o)), "zs_test_mx4_matvec_launch")
     return _to_dict(o)

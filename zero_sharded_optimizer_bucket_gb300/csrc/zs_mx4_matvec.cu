@@ -21,6 +21,7 @@
 // warp, k and rows shared out by measured costs, 12 and 18.
 #include <atomic>
 #include <cooperative_groups.h>
+#include <type_traits>
 
 #include "zs_launch.h"
 #include "zs_mx4.cuh"
@@ -453,8 +454,14 @@ mx4_matvec_kernel(MatvecArgs a) {
     cluster.sync();                  // the others may still read this CTA's sums
 }
 
+struct MvLaunch {
+    int tokens, split, ty, shared_bytes;
+    int64_t grid;
+};
+
+// The fields of a that follow from its sizes, and the launch's.
 template <int KIND, int NB>
-static cudaError_t matvec_launch(MatvecArgs a, cudaStream_t s) {
+static cudaError_t matvec_plan(MatvecArgs &a, MvLaunch &l) {
     constexpr int PER = KIND == ZS_DTYPE_FP32 ? 2 : 1, TOKENS = 8 * NB / PER;
     constexpr int ROOM = 227 * 1024 - mv_ring_bytes(NB, MV_LEAST_DEPTH), THREADS = 32 * mv_warps(NB);      // of tokens
     static_assert(2 * mv_stage_bytes(mv_most_stage(NB), 8 * NB) <= ROOM, "shared memory");
@@ -464,19 +471,17 @@ static cudaError_t matvec_launch(MatvecArgs a, cudaStream_t s) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(THREADS);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
     if (!seats[dev][8].load(std::memory_order_acquire)) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.blockDim = dim3(THREADS);
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
         e = cudaFuncSetAttribute(mx4_matvec_kernel<KIND, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
         for (int sp = 1; sp <= 8 && e == cudaSuccess; ++sp) {
             int clusters = 0;
-            attr[0].val.clusterDim.x = (unsigned)sp;
+            attr.val.clusterDim.x = (unsigned)sp;
             cfg.gridDim = dim3((unsigned)sp);
             cfg.dynamicSmemBytes = 227 * 1024;
             cfg.numAttrs = 1;
@@ -522,27 +527,52 @@ static cudaError_t matvec_launch(MatvecArgs a, cudaStream_t s) {
     a.per_token = (uint32_t)(((uint64_t)1 << 32) / (16 * a.stage) + 1);
     a.per_row = (uint32_t)(((uint64_t)1 << 32) / (MV_ROWS / 4 * a.warps_n) + 1);
     a.per_warp = (uint32_t)(((uint64_t)1 << 32) / a.warps_k + 1);
-    const int64_t grid = (int64_t)((tiles + a.warps_n - 1) / a.warps_n) * split;
-    if (grid > 0x7FFFFFFF || ty > 65535) return cudaErrorInvalidValue;
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)ty);
     const int room = (once ? 1 : 2) * mv_stage_bytes(a.stage, a.columns);
     const int share = MV_ROWS * a.warps_n * (a.columns / PER) * 4;     // the CTA's sums, in the tokens' place
     const int left = 227 * 1024 - (room > share ? room : share);
     a.depth = left / mv_ring_bytes(NB, 1) < MV_MOST_DEPTH ? left / mv_ring_bytes(NB, 1) : MV_MOST_DEPTH;
-    cfg.dynamicSmemBytes = mv_ring_bytes(NB, a.depth) + (room > share ? room : share);
-    cfg.stream = s;
-    attr[0].val.clusterDim.x = (unsigned)split;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, mx4_matvec_kernel<KIND, NB>, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    l = {TOKENS, split, ty, mv_ring_bytes(NB, a.depth) + (room > share ? room : share), (int64_t)((tiles + a.warps_n - 1) / a.warps_n) * split};
+    return cudaSuccess;
 }
 
+template <int KIND, int NB>
+static cudaError_t matvec_launch(MatvecArgs a, cudaStream_t s) {
+    MvLaunch l;
+    const cudaError_t e = matvec_plan<KIND, NB>(a, l);
+    if (e != cudaSuccess) return e;
+    if (l.grid > 0x7FFFFFFF || l.ty > 65535) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)l.split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3((unsigned)l.grid, (unsigned)l.ty);
+    cfg.blockDim = dim3(32 * mv_warps(NB));
+    cfg.dynamicSmemBytes = l.shared_bytes;
+    cfg.stream = s;
+    const cudaError_t launched = cudaLaunchKernelEx(&cfg, mx4_matvec_kernel<KIND, NB>, a);
+    return launched != cudaSuccess ? launched : cudaGetLastError();
+}
+
+// f with the kernel's tiles of 8 columns for m tokens
+template <int KIND, class F>
+static cudaError_t by_columns(int64_t m, F f) {
+    const int64_t cols = m * (KIND == ZS_DTYPE_FP32 ? 2 : 1);
+    if (cols <= 8) return f(std::integral_constant<int, 1>());
+    if (cols <= 16) return f(std::integral_constant<int, 2>());
+    return f(std::integral_constant<int, 4>());
+}
 template <int KIND>
 static cudaError_t matvec_of(const MatvecArgs &a, cudaStream_t s) {
-    const int64_t cols = a.m * (KIND == ZS_DTYPE_FP32 ? 2 : 1);
-    if (cols <= 8) return matvec_launch<KIND, 1>(a, s);
-    if (cols <= 16) return matvec_launch<KIND, 2>(a, s);
-    return matvec_launch<KIND, 4>(a, s);
+    return by_columns<KIND>(a.m, [&](auto nb) { return matvec_launch<KIND, decltype(nb)::value>(a, s); });
+}
+template <int KIND>
+static cudaError_t matvec_plan_of(MatvecArgs &a, MvLaunch &l) {
+    return by_columns<KIND>(a.m, [&](auto nb) { return matvec_plan<KIND, decltype(nb)::value>(a, l); });
 }
 
 }  // namespace zsk
@@ -578,6 +608,22 @@ extern "C" zs_status zs_mx4_matvec(int64_t m, int64_t n, int64_t k, const void *
           : dtype == ZS_DTYPE_FP16 ? zsk::matvec_of<ZS_DTYPE_FP16>(a, s) : zsk::matvec_of<ZS_DTYPE_BF16>(a, s);
     }
     if (e != cudaSuccess) return zs_fail(ZS_ECUDA, "%s: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
+    zs_clear_error();
+    return ZS_OK;
+}
+
+extern "C" zs_status zs_test_mx4_matvec_launch(int64_t m, int64_t n, int64_t k, int32_t dtype, zs_mx4_matvec_launch *out) {
+    const char *fn = "zs_test_mx4_matvec_launch";
+    const int64_t most = (int64_t)1 << 31;
+    if (!out || m < 1 || m > ZS_MATVEC_MAX_TOKENS || n < 1 || n >= most || k < 1 || k >= most || dtype < ZS_DTYPE_BF16 || dtype > ZS_DTYPE_FP32)
+        return zs_fail(ZS_EINVAL, "%s: NULL result, or m, n, k or dtype out of range", fn);
+    zsk::MatvecArgs a = {};
+    zsk::MvLaunch l = {};
+    a.m = m; a.n = n; a.k = k;
+    const cudaError_t e = dtype == ZS_DTYPE_FP32 ? zsk::matvec_plan_of<ZS_DTYPE_FP32>(a, l)
+                        : dtype == ZS_DTYPE_FP16 ? zsk::matvec_plan_of<ZS_DTYPE_FP16>(a, l) : zsk::matvec_plan_of<ZS_DTYPE_BF16>(a, l);
+    if (e != cudaSuccess) return zs_fail(ZS_ECUDA, "%s: %s (%s)", fn, cudaGetErrorName(e), cudaGetErrorString(e));
+    *out = {l.tokens, a.warps_n, a.warps_k, l.split, a.units, a.stage, a.depth, l.shared_bytes};
     zs_clear_error();
     return ZS_OK;
 }
