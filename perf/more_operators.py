@@ -207,6 +207,8 @@ def prepare(case, seed):
         s["norm"], s["coef"] = torch.empty(1, device=dev), torch.empty(1, device=dev)
         s["flags"] = torch.empty(1, dtype=torch.int32, device=dev)
         s["scale"] = torch.full((1,), 1024.0, device=dev) if case["scaled"] else None
+        if own:             # made once, for gradients that stay where they are
+            s["list"] = _tensor_list(_zs(), s)
         return s
     if case["op"] == "matvec":
         m, n, k = case["m"], case["n"], case["k"]
@@ -230,7 +232,8 @@ def prepare(case, seed):
         s["residual"] = (torch.randn(r, c, device=dev, generator=gen) * 1e-3).to(kind)
     s["rstd"] = (x.double().square().mean(1) + EPS).rsqrt().float()
     s["dx"], s["dw"] = torch.empty(r, c, dtype=kind, device=dev), torch.empty(c, dtype=w.dtype, device=dev)
-    s["scratch"] = None
+    if own:
+        s["scratch"] = torch.empty(_zs().zs_rms_norm_scratch(r, c), dtype=torch.uint8, device=dev)
     return s
 
 
@@ -315,8 +318,6 @@ def run(s):
     if case["op"] == "norm":
         if own:
             zs = _zs()
-            if "list" not in s:
-                s["list"] = _tensor_list(zs, s)
             scaler = None if s["scale"] is None else zs.make_loss_scaler(s["scale"], scale_window=0)
             zs.zs_norm_tensors(s["list"], s["scratch"], s["max_norm"], s["norm"], s["coef"], s["flags"], scaler=scaler)
             if case["clip"]:
@@ -343,8 +344,6 @@ def run(s):
         if not own:
             return _back_plain(s)
         zs = _zs()
-        if s["scratch"] is None:
-            s["scratch"] = torch.empty(zs.zs_rms_norm_scratch(case["rows"], case["cols"]), dtype=torch.uint8, device="cuda")
         zs.zs_rms_norm_backward(s["dy"], s["x"], s["w"], s["rstd"], residual=s["residual"], dx=s["dx"], dw=s["dw"],
                                 scratch=s["scratch"], rows=s.get("rows"), cols=s.get("cols"))
         got = dict(dx=s["dx"], dw=s["dw"])
