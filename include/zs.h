@@ -897,9 +897,11 @@ zs_status zs_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t 
  * both sizes, does for each of them. */
 zs_status zs_rms_norm_scratch(int64_t rows, int64_t cols, int64_t *bytes);
 
-/* Its backward pass.  x: what was normalised (sum, where there was a
- * residual), rstd as it came back, dy the gradient of y, residual (or NULL)
- * the gradient that reaches the residual stream on its other way.  In fp32:
+/* Its backward pass.  x: what was normalised, rstd as it came back, dy the
+ * gradient of y, residual (or NULL) the gradient that reaches the residual stream
+ * on its other way.  Where there was a residual, x is sum: of 16 bits that is h
+ * rounded, while y and rstd were made from h before its rounding, so that dx and
+ * dw are the formula's at sum.  In fp32:
  *   g = dy * weight;  c = rstd^2 * mean over the row of g x
  *   dx = rne((g - x c) * rstd + residual)   (of x and of the residual alike)
  *   dw = sum over the rows of dy * (x * rstd), added in fp32 in an order that

@@ -151,13 +151,15 @@ struct VtPair {
 // odd elements go to two accumulators, advanced together by Blackwell's
 // paired float32 instructions.  Each accumulator starts at B, a power of two
 // above 32 * max^2 (max the largest |x| of the thread), so it stays in
-// [B, 2B) while it gains the squares (at most 20 per accumulator).  Then
+// [B, 2B) while it gains the squares (at most 32 per accumulator, which is all
+// that B leaves room for: 20 of a tile's window, 32 of a list's chunk).  Then
 // for a square x*x (exact in float32: at most 22 significant bits):
 //   s = x*x + h;  d = h - s (exact, Sterbenz);  e = x*x + d (the exact
 //   rounding error of s);  l = l + e;  h = s
 // and h - B is exact at the end: four float32 operations per value.
 template <class T, int NG>
 __device__ __forceinline__ VtPair vt_sumsq(const uint4 (&w)[NG], int n) {
+    static_assert(4 * NG <= 32, "squares of an accumulator");
     uint32_t m2 = 0;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {

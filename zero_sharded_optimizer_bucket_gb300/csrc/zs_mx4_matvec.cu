@@ -10,9 +10,12 @@
 //
 // 1 x 4096 x 14336 bf16 takes 12 us where the weight's bytes at a copy's rate are
 // 4.6: about 4.5 go before the first unit and behind the last one (launch, first
-// loads, sums of warps and cluster), the rest is the issue of loads, decoding and
-// products.  32 x 14336 x 4096 fp16 takes 18 us, of which the products alone are
-// 6.4 (mma m16n8k16: 2.07 cycles of an SM each); their rate bounds more tokens.
+// loads, sums of warps and cluster), and in between latency bounds the six units or
+// so that a warp has (issue slots 40 %, tensor pipe 16 %, DRAM 26 % busy).  32 x
+// 14336 x 4096 fp16 takes 18 us, of which the products alone are 6.4 (mma m16n8k16:
+// 2.07 cycles of an SM each; tensor pipe 36 % busy), the rest what a group's scale
+// and its tokens' way cost 12 warps an SM.  Every 32 tokens read and decode the
+// weight again: 128 x 14336 x 4096 bf16 takes 70 us.
 // (tcgen05's 16-bit kinds would take the decoded weight from shared or tensor
 // memory, written there and read again at four times its bytes, in tiles of 128
 // rows, of which these sizes have few.  Not built.)  Codes decoded by bit
@@ -494,9 +497,10 @@ static cudaError_t matvec_plan(MatvecArgs &a, MvLaunch &l) {
     a.columns = (int)(a.m < TOKENS ? a.m : TOKENS) * PER;
     auto fits = [&](int whole) { return whole <= 512 && mv_stage_bytes(whole, a.columns) <= ROOM; };
     // How warps and CTAs share rows and k, by the time that an SM takes, in ns as
-    // measured: a step (a unit of each warp) 54, 75 or 130 a warp, and 450 at
-    // least; a CTA's beginning and end 2000, with 280 for each 8 values of tokens
-    // a thread, an exchange 700.
+    // measured (in a graph, with warps and split set by hand, and by a kernel whose
+    // loop over the units was left out): a step (a unit of each warp) 54, 75 or 130
+    // a warp, and 450 at least; a CTA's beginning and end 2000, with 280 for each 8
+    // values of tokens a thread, an exchange 700.
     constexpr int STEP = NB == 1 ? 54 : NB == 2 ? 75 : 130, MOST_WARPS = mv_warps(NB);
     int64_t best = -1;
     int split = 1;

@@ -423,9 +423,11 @@ struct NormArgs {
 
 // WPR warps take a row, 8 values a lane and block of 256 columns; a lane keeps
 // its NB blocks (NB 0: more than registers hold, read again).  Bandwidth
-// bounds many rows (4096 x 4096 fp32 along the rows: 34 us, 31 at a copy's rate;
-// bf16 27, 16), the way through the sum's exchange a few (24 x 4096 bf16: 2.5 us
-// in a graph).
+// bounds many rows of 32 bits (4096 x 4096 along the rows: 34 us, 31 at a copy's
+// rate); of 16 bits the issue of instructions (28 us, 16: 43 a value, issue slots
+// 72 % busy, DRAM 42 %), and past 8192 columns the few rows that are in flight (2048
+// x 16384: 50 us, 40); the way through the sum's exchange a few rows (24 x 4096
+// bf16: 2.6 us in a graph).
 template <class R, int WPR, int NB, bool VEC>
 __global__ void __launch_bounds__(THREADS)
 rms_rows_kernel(NormArgs a) {
@@ -552,9 +554,10 @@ rms_rows_kernel(NormArgs a) {
 
 // rstd of every row (h: x + residual), or of the backward pass c, rstd^2 times
 // the mean of g x: WPR warps a row, two blocks of 256 columns of both inputs on
-// their way while two are summed.  Bandwidth and the issue of instructions bound
-// it alike: 4096 x 4096 bf16 takes 15 us from cold caches, backward 19 (10 at a
-// copy's rate), with DRAM 57 and 45 % and issue slots 53 and 64 % busy.  VEC: rows
+// their way while two are summed.  Neither bandwidth
+// nor the issue of instructions alone bounds it: 4096 x 4096 bf16 takes 15 us from
+// cold caches (10 at a copy's rate; DRAM 56 %, issue slots 44 % busy), 4096 x 12288
+// backward 44 (30; 58 and 64 %).  VEC: rows
 // are 16-byte aligned and whole pieces of 8.
 struct SumArgs {
     const void *x, *other, *w;       // other: the residual or NULL; dy
@@ -829,9 +832,8 @@ constexpr int tile_ctas(bool back) { return R::SIZE == 4 || !back ? 3 : 2; }    
 // in its own type in x's place, its form along the rows from registers (4 lanes
 // a group), and through shared memory the one along the columns.  4096 x 4096
 // bf16 from cold caches: 27 us, 30 instructions a value, issue slots 57 % busy and
-// warps waiting for their first inputs; backward 35 us, 48 %.  (Tiles of 256
-// columns by 4 warps: within 2 %.  The residual by plain loads and three CTAs an
-// SM: 4 % more in the backward pass.  Greatest magnitudes by one instruction instead of two: the same.)
+// warps waiting for their first inputs.  (Tiles of 256 columns by 4 warps: within
+// 2 %.  Greatest magnitudes by one instruction instead of two: the same.)
 template <class R, bool VEC>
 __global__ void __launch_bounds__(THREADS, tile_ctas<R>(false))
 rms_tile_kernel(NormArgs a, int col_blocks) {
@@ -926,7 +928,9 @@ struct BackArgs {
 __host__ __device__ constexpr int64_t parts_pitch(int64_t cols) { return (cols + TILE_COLS - 1) / TILE_COLS * TILE_COLS; }
 
 // The same of the backward pass, c being known: a CTA takes its 512 columns of
-// the row blocks b, b + parts, ... and adds up their part of dw.
+// the row blocks b, b + parts, ... and adds up their part of dw.  Bandwidth bounds
+// it: 4096 x 12288 bf16 takes 61 us from cold caches, 59 at a copy's rate.  (The
+// residual by plain loads and three CTAs an SM took 4 % more.)
 template <class R, bool VEC>
 __global__ void __launch_bounds__(THREADS, tile_ctas<R>(true))
 rms_back_kernel(BackArgs a, int64_t blocks, int col_blocks) {
@@ -1040,11 +1044,12 @@ rms_back_kernel(BackArgs a, int64_t blocks, int col_blocks) {
 // place of its own (32 bits: two fours, each beside the neighbours', since a
 // warp's copies then read whole sectors; 4096 x 4096: 49 us, not 76); other rows
 // go through registers.  A CTA takes WARPS / WPR
-// rows at a time and leaves its part of dw.  Bandwidth bounds many rows, the way
-// through a row's sum a few.  4096 x 4096 bf16: 29 us with rms_weight_kernel (the
-// two readings of rms_back_kernel: 39), fp32 48 (107), 1333 x 1490 fp16 10 (20);
-// 37 instructions a value and issue slots 61 % busy before the lanes shared the
-// joining of a row's sums.
+// rows at a time and leaves its part of dw.  4096 x 4096 bf16: 29 us with
+// rms_weight_kernel (20 at a copy's rate; the two readings of rms_back_kernel: 39),
+// fp32 48 (40; 107), 1333 x 1490 fp16 10 (20).  Bandwidth bounds rows of 32 bits; of
+// 16 bits nothing is full (34 instructions a value, issue slots 51 % and DRAM 49 %
+// busy): four warps a scheduler wait for one another's sums.  A few rows wait for
+// the way through their sum.
 // Three CTAs an SM spill; a ring of four rows takes as long as one of three.
 __host__ __device__ constexpr int whole_cta_warps(int wpr) { return wpr > WARPS ? wpr : WARPS; }
 __host__ __device__ constexpr int whole_ctas(int wpr) { return wpr > WARPS ? 1 : 2; }             // an SM
