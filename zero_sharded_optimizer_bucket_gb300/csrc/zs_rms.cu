@@ -1342,7 +1342,8 @@ static cudaError_t rows_of(const NormArgs &a, int64_t grid_rows, cudaStream_t s)
 
 template <class R, bool BACK, bool VEC>
 static cudaError_t sums_launch(const SumArgs &a, cudaStream_t s) {
-    // as many warps a row as give every SM 16 (with 32, 4096 x 4096 bf16 took 2 us more)
+    // as many warps a row as give every SM 16 (with 32, 4096 x 4096 bf16 took 2 us
+    // more); of the backward pass rows are wider than 8192 here, and their number decides
     const int64_t rows = a.rows;
     auto go = [&](auto kernel, int wpr) { return launch_dependent(kernel, (unsigned)((rows * wpr + WARPS - 1) / WARPS), THREADS, 0, 1, s, a); };
     if (rows >= 2432 || a.cols <= 1024) return go(rms_sums_kernel<R, 1, BACK, VEC>, 1);
