@@ -109,3 +109,19 @@ def test_rows_of_small_values(cols, kind, held):
         check_forward(x, None, torch.ones(cols, device="cuda"), eps, got)
     got = call(x, torch.ones(cols, device="cuda"), 3e38, held=held, kind=kind)
     check_forward(x, None, torch.ones(cols, device="cuda"), 3e38, got)
+
+
+@pytest.mark.parametrize("cols", [250, 4099, 16384])
+@pytest.mark.parametrize("held", [(), ("cols",)])
+def test_large_eps(cols, held):
+    """An eps near float32's largest number, beside means that count and ones that take the sum past it."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x = torch.rand(90, cols, device="cuda", generator=g) * 2.0 ** torch.linspace(50, 64, 90, device="cuda")[:, None]
+    for eps in (1e36, 2.9e38, 3e38):
+        got = call(x, torch.ones(cols, device="cuda"), eps, held=held, kind="fp32")
+        check_forward(x, None, torch.ones(cols, device="cuda"), eps, got)
+        want = 1 / torch.sqrt(x.double().square().mean(1) + float(np.float32(eps)))
+        near = want.float()
+        # half a step of want's binade, and 2^-38: further than that is not the nearest
+        half = torch.ldexp(torch.ones((), dtype=torch.float64, device="cuda"), torch.frexp(want).exponent - 25)
+        assert bool(((got["rstd"].double() - want).abs() <= half + 2.0 ** -38 * want).all()), int((got["rstd"] != near).sum())

@@ -323,7 +323,7 @@ __device__ __forceinline__ float rstd_of(float hi, float lo, const Mean &mean, f
     times(hi, lo, mean.hi, mean.lo);
     add22(hi, lo, eps, 0.0f);
     const int e = ((int)(__float_as_uint(hi) >> 23) - 127) >> 1;           // floor
-    if (!(hi >= 1.1754944e-38f) || hi > 3e38f) return (float)__drcp_rn(__dsqrt_rn((double)hi));
+    if (!(hi >= 1.1754944e-38f) || hi > 3e38f) return 0.0f;                 // summed in 64 bits instead
     const float s = __uint_as_float((uint32_t)(127 - e) << 23);
     hi = __fmul_rn(__fmul_rn(hi, s), s);
     lo = __fmul_rn(__fmul_rn(lo, s), s);
@@ -1317,7 +1317,10 @@ rms_weight_kernel(const float *parts, int n, int64_t cols, int64_t pitch, void *
 
 // The sum of squares below which a row is summed in 64 bits: the errors that
 // float32's least number leaves (2^-149 a square) would count, unless eps hides them.
-static float least_sum(int64_t cols, float eps) { return eps < 0x1p-100f ? (float)cols * 0x1p-100f : 0.0f; }
+// With an eps that may take the mean out of float32, every row.
+static float least_sum(int64_t cols, float eps) {
+    return eps < 0x1p-100f ? (float)cols * 0x1p-100f : eps > 0x1p120f ? MOST_F32 : 0.0f;
+}
 
 template <class R, int WPR, int NB>
 static cudaError_t rows_launch(const NormArgs &a, int64_t grid_rows, cudaStream_t s) {
