@@ -27,6 +27,7 @@
 // us: 57 of them fit the GPU, and the 128 blocks of rows need three turns of all
 // that lies between two barriers.
 #include <atomic>
+#include <limits>
 
 #include "zs_launch.h"
 #include "zs_mx4.cuh"
@@ -554,11 +555,10 @@ rms_rows_kernel(NormArgs a) {
 
 // rstd of every row (h: x + residual), or of the backward pass c, rstd^2 times
 // the mean of g x: WPR warps a row, two blocks of 256 columns of both inputs on
-// their way while two are summed.  Neither bandwidth
-// nor the issue of instructions alone bounds it: 4096 x 4096 bf16 takes 15 us from
-// cold caches (10 at a copy's rate; DRAM 56 %, issue slots 44 % busy), 4096 x 12288
-// backward 44 (30; 58 and 64 %).  VEC: rows
-// are 16-byte aligned and whole pieces of 8.
+// their way while two are summed.  Neither bandwidth nor the issue of instructions
+// alone bounds it: 4096 x 4096 bf16 takes 15 us from cold caches (10 at a copy's
+// rate; DRAM 56 %, issue slots 44 % busy), 4096 x 12288 backward 44 (30; 58 and 64
+// %).  VEC: rows are 16-byte aligned and whole pieces of 8.
 struct SumArgs {
     const void *x, *other, *w;       // other: the residual or NULL; dy
     int64_t ldx, ldo, rows, cols;
@@ -625,31 +625,28 @@ rms_sums_kernel(SumArgs a) {
             ro[b] = next_o[b].take(turn);
         }
         if (c0 + 256 * WPR * BLOCKS < a.cols) fetch(c0 + 256 * WPR * BLOCKS);
+        f2 u[BLOCKS][4], v[BLOCKS][4];
+        float top = 0.0f;
 #pragma unroll
-        for (int b0 = 0; b0 < BLOCKS; b0 += RUN) {
-            f2 u[RUN][4], v[RUN][4];
-            float top = 0.0f;
+        for (int b = 0; b < BLOCKS; ++b) {
+            const int64_t c = c0 + 256 * WPR * b;
+            inputs(rx[b], ro[b], c, there ? part(a.cols, c) : 0, u[b], v[b]);
 #pragma unroll
-            for (int b = 0; b < RUN; ++b) {
-                const int64_t c = c0 + 256 * WPR * (b0 + b);
-                inputs(rx[b0 + b], ro[b0 + b], c, there ? part(a.cols, c) : 0, u[b], v[b]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float p, q;
-                    f2unpack(BACK ? mul2(u[b][j], v[b][j]) : v[b][j], p, q);
-                    max_abs3(top, p, q);
-                }
+            for (int j = 0; j < 4; ++j) {
+                float p, q;
+                f2unpack(BACK ? mul2(u[b][j], v[b][j]) : v[b][j], p, q);
+                max_abs3(top, p, q);
             }
-            Dot<!BACK> d;
-            const bool ok = d.template begin<RUN>(BACK ? top : __fmul_rn(top, top));
-#pragma unroll
-            for (int b = 0; b < RUN; ++b)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) d.add(u[b][j], v[b][j]);
-            float dh, dl;
-            d.end(dh, dl);
-            add22(hi, lo, ok ? dh : __uint_as_float(0x7F800000u), dl);
         }
+        Dot<!BACK> d;
+        const bool ok = d.template begin<BLOCKS>(BACK ? top : __fmul_rn(top, top));
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d.add(u[b][j], v[b][j]);
+        float dh, dl;
+        d.end(dh, dl);
+        add22(hi, lo, ok ? dh : __uint_as_float(0x7F800000u), dl);
     }
     warp_pair(hi, lo);
     if (WPR > 1) {
@@ -1170,36 +1167,27 @@ rms_back_rows_kernel(BackArgs a) {
             }
         };
         f2 g[NB][4], z[NB][4];
-        float hi = 0.0f, lo = 0.0f;
-        bool ok = true;
+        float top = 0.0f, hi, lo;
 #pragma unroll
-        for (int b0 = 0; b0 < NB; b0 += RUN) {
-            float top = 0.0f;
+        for (int b = 0; b < NB; ++b) {
+            inputs(b, g[b], z[b]);
 #pragma unroll
-            for (int b = b0; b < b0 + RUN; ++b) {
-                inputs(b, g[b], z[b]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float p, q;
-                    f2unpack(mul2(mul2(g[b][j], w[b][j]), z[b][j]), p, q);
-                    max_abs3(top, p, q);
-                }
-            }
-            Dot<false> d;
-            ok &= d.template begin<RUN>(top);
-#pragma unroll
-            for (int b = b0; b < b0 + RUN; ++b)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) d.add(mul2(g[b][j], w[b][j]), z[b][j]);
-            if (b0 == 0) {
-                d.end(hi, lo);
-            } else {
-                float dh, dl;
-                d.end(dh, dl);
-                add22(hi, lo, dh, dl);
+            for (int j = 0; j < 4; ++j) {
+                float p, q;
+                f2unpack(mul2(mul2(g[b][j], w[b][j]), z[b][j]), p, q);
+                max_abs3(top, p, q);
             }
         }
-        if (!ok) hi = __uint_as_float(0x7F800000u);
+        {
+            Dot<false> d;
+            const bool ok = d.template begin<NB>(top);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d.add(mul2(g[b][j], w[b][j]), z[b][j]);
+            d.end(hi, lo);
+            if (!ok) hi = __uint_as_float(0x7F800000u);
+        }
         warp_pair(hi, lo);
         // too large for float32's products (or not finite): the row in 64 bits
         bool wide = !(fabsf(hi) <= 1e30f);           // sixteen such sums are finite
@@ -1319,7 +1307,7 @@ rms_weight_kernel(const float *parts, int n, int64_t cols, int64_t pitch, void *
 // float32's least number leaves (2^-149 a square) would count, unless eps hides them.
 // With an eps that may take the mean out of float32, every row.
 static float least_sum(int64_t cols, float eps) {
-    return eps < 0x1p-100f ? (float)cols * 0x1p-100f : eps > 0x1p120f ? MOST_F32 : 0.0f;
+    return eps < 0x1p-100f ? (float)cols * 0x1p-100f : eps > 0x1p120f ? std::numeric_limits<float>::infinity() : 0.0f;
 }
 
 template <class R, int WPR, int NB>
