@@ -792,8 +792,8 @@ zs_status zs_norm_tensors(const zs_tensors *list, double *scratch, float max_nor
 /* Clipping in place, for an update that takes no coefficient: every gradient
  * of the list becomes rne(float(grad) * *d_clip_coef).  With ZS_SKIP_NONFINITE
  * in d_flags (NULL: never), or a coefficient of 1, nothing is written.  The
- * gradients have to be writable, and none may be in the list twice.  Errors: as
- * zs_norm_tensors. */
+ * gradients have to be writable; a list in which two of them overlap (or one is
+ * there twice) is refused.  Errors: as zs_norm_tensors. */
 zs_status zs_clip_tensors(const zs_tensors *list, const float *d_clip_coef, const int32_t *d_flags,
                           void *stream);
 

@@ -72,3 +72,15 @@ def test_scratch_of_a_larger_matrix_does_for_a_smaller_one():
         for j in range(len(cols)):
             assert i == 0 or need[i - 1][j] <= need[i][j], (rows[i], cols[j])
             assert j == 0 or need[i][j - 1] <= need[i][j], (rows[i], cols[j])
+
+
+def test_clipping_of_gradients_that_overlap_is_refused():
+    """A gradient that is in the list twice would be multiplied once or twice, as its chunks happen to meet."""
+    for grads in ((A16, A16), (A16 + 2000, A16, A16 + 3998), (A16 + 1998, A16), (A16, A16 + 40000, A16 + 40016)):
+        lst = zs.zs_build_tensors([tensor(grad=g) for g in grads], state_bits=8)
+        refuses(zs.zs_clip_tensors, lst, A16)
+    for grads in ((A16,), (A16 + 2000, A16, A16 + 4000), (A16 + 2002, A16)):
+        lst = zs.zs_build_tensors([tensor(grad=g) for g in grads], state_bits=8)
+        refuses(zs.zs_clip_tensors, lst, A16, status=zs.ZS_ESTATE)       # as far as the upload
+    lst = zs.zs_build_tensors([tensor(), tensor(numel=0)], state_bits=8)
+    refuses(zs.zs_clip_tensors, lst, A16, status=zs.ZS_ESTATE)

@@ -12,9 +12,11 @@
 // scale for each, 2^(floor(log2 max) - 7): e4m3 is a floating format, so a
 // power of two costs no precision, makes scaling exact and leaves its largest
 // value in [128, 256), which no rounding takes past 448.
+#include <algorithm>
 #include <atomic>
 #include <cstring>
 #include <new>
+#include <utility>
 
 #include "zs_launch.h"
 #include "zs_tensors.cuh"
@@ -536,6 +538,12 @@ zs_status zs_build_tensors(const zs_tensors_config *cfg, int32_t n, const zs_ten
     L->n = n;
     try {
         L->chunks.reserve((size_t)chunks);
+        std::vector<std::pair<uintptr_t, uintptr_t>> grads;              // first byte, past the last
+        grads.reserve((size_t)n);
+        for (int32_t i = 0; i < n; ++i)
+            if (t[i].numel > 0) grads.emplace_back(addr(t[i].grad), addr(t[i].grad) + (uintptr_t)(t[i].numel * gsize));
+        std::sort(grads.begin(), grads.end());
+        for (size_t i = 1; i < grads.size(); ++i) L->grads_apart &= grads[i - 1].second <= grads[i].first;
     } catch (const std::bad_alloc &) {
         delete L;
         return zs_fail(ZS_ENOMEM, "%s: out of host memory", fn);

@@ -23,6 +23,7 @@ struct zs_tensors {
     zs_tensors_config cfg;
     int32_t n = 0;
     int64_t numel = 0, blocks = 0;
+    bool grads_apart = true;         // no element is in two gradients
     std::vector<ZsChunk> chunks;
     const ZsChunk *d_chunks = nullptr;   // caller memory given to zs_tensors_upload
 };

@@ -368,6 +368,7 @@ zs_status zs_clip_tensors(const zs_tensors *L, const float *d_clip_coef, const i
     if (!L) return zs_fail(ZS_EINVAL, "%s: NULL list", fn);
     if (!al(d_clip_coef, 4) || addr(d_flags) % 4)
         return zs_fail(ZS_EINVAL, "%s: d_clip_coef NULL or misaligned, or d_flags misaligned", fn);
+    if (!L->grads_apart) return zs_fail(ZS_EINVAL, "%s: gradients of the list overlap", fn);
     if (L->chunks.empty()) {
         zs_clear_error();
         return ZS_OK;
